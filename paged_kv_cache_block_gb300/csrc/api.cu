@@ -963,4 +963,264 @@ kv_status kv_paged_attention_prefill(const void *q, kv_dtype q_dtype, const int3
     return ok();
 }
 
+// ---------------------------------------------------------------- a serving step (pagedkv_step.h)
+
+// Whether any two of the given byte ranges overlap (null or empty ranges overlap nothing).
+struct ByteRange {
+    const void *p;
+    int64_t bytes;
+};
+static bool overlap(const ByteRange &x, const ByteRange &y) {
+    if (!x.p || !y.p || x.bytes <= 0 || y.bytes <= 0) return false;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    return a < b + static_cast<uintptr_t>(y.bytes) && b < a + static_cast<uintptr_t>(x.bytes);
+}
+
+kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_lens, const int32_t *held_blocks,
+                         const int32_t *parents, int32_t num_seqs, int32_t num_tokens, int32_t *block_table,
+                         int64_t bt_stride, int32_t max_blocks_per_seq, int32_t block_size, int32_t num_blocks,
+                         const int32_t *free_blocks, int32_t num_free, const int32_t *free_start,
+                         int32_t *query_start_loc, int32_t *seq_lens, int32_t *positions, int64_t *slot_mapping,
+                         uint64_t *tree_mask, int32_t *held_out, int32_t *free_next, int32_t *d_err, void *stream) {
+    if (num_seqs < 0 || num_tokens < 0 || max_blocks_per_seq < 0 || num_blocks < 0 || num_free < 0 ||
+        bt_stride < max_blocks_per_seq)
+        return fail(KV_ERR_INVALID_ARG, "invalid size argument");
+    if (block_size != 4 && block_size != 8 && block_size != 16 && block_size != 32)
+        return fail(KV_ERR_UNSUPPORTED, "block_size %d (supported: 4, 8, 16, 32)", block_size);
+    if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX)
+        return fail(KV_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size past 32 bits");
+    if (!query_start_loc || !free_next)
+        return fail(KV_ERR_INVALID_ARG, "null query_start_loc or free_next");
+    if (num_seqs > 0 && (!context_lens || !new_lens || !block_table || !seq_lens || !held_out))
+        return fail(KV_ERR_INVALID_ARG, "null pointer");
+    if (num_tokens > 0 && (!positions || !slot_mapping)) return fail(KV_ERR_INVALID_ARG, "null positions or slot_mapping");
+    if (num_free > 0 && !free_blocks) return fail(KV_ERR_INVALID_ARG, "null free_blocks");
+    if (num_tokens > 0 && (parents != nullptr) != (tree_mask != nullptr))
+        return fail(KV_ERR_INVALID_ARG, "parents and tree_mask are given together or not at all");
+    if (!aligned(context_lens, 4) || !aligned(new_lens, 4) || !aligned(held_blocks, 4) || !aligned(parents, 4) ||
+        !aligned(block_table, 4) || !aligned(free_blocks, 4) || !aligned(free_start, 4) ||
+        !aligned(query_start_loc, 4) || !aligned(seq_lens, 4) || !aligned(positions, 4) ||
+        !aligned(slot_mapping, 8) || !aligned(tree_mask, 8) || !aligned(held_out, 4) || !aligned(free_next, 4) ||
+        !aligned(d_err, 4))
+        return fail(KV_ERR_INVALID_ARG, "misaligned pointer");
+    // every CTA reads all lengths, so an output over an input would be read half rewritten
+    const int64_t B = num_seqs, T = num_tokens;
+    const ByteRange outs[] = {{query_start_loc, 4 * (B + 1)}, {seq_lens, 4 * B}, {held_out, 4 * B}, {free_next, 4},
+                              {positions, 4 * T}, {slot_mapping, 8 * T}, {tree_mask, 8 * T},
+                              {block_table, B > 0 ? 4 * ((B - 1) * bt_stride + max_blocks_per_seq) : 0}};
+    const ByteRange ins[] = {{context_lens, 4 * B}, {new_lens, 4 * B}, {held_blocks, 4 * B}, {parents, 4 * T},
+                             {free_blocks, 4 * static_cast<int64_t>(num_free)}, {free_start, 4}};
+    constexpr int kOuts = sizeof outs / sizeof outs[0], kIns = sizeof ins / sizeof ins[0];
+    for (int i = 0; i < kOuts; ++i) {
+        for (int j = 0; j < kIns; ++j)
+            if (overlap(outs[i], ins[j])) return fail(KV_ERR_INVALID_ARG, "an output overlaps an input");
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i], outs[j])) return fail(KV_ERR_INVALID_ARG, "two outputs overlap");
+    }
+    int dev;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = bind_device(s, &dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device of stream");
+    DeviceInfo info;
+    if ((e = device_info(dev, &info)) != cudaSuccess) return cuda_fail(e, "device attributes");
+    pkv::BatchArgs a;
+    a.context_lens = context_lens;
+    a.new_lens = new_lens;
+    a.held_blocks = held_blocks;
+    a.parents = parents;
+    a.num_seqs = num_seqs;
+    a.num_tokens = num_tokens;
+    a.block_table = block_table;
+    a.bt_stride = bt_stride;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.block_shift = block_size == 4 ? 2 : (block_size == 8 ? 3 : (block_size == 16 ? 4 : 5));
+    a.num_blocks = num_blocks;
+    a.free_blocks = free_blocks;
+    a.num_free = num_free;
+    a.free_start = free_start;
+    a.query_start_loc = query_start_loc;
+    a.seq_lens = seq_lens;
+    a.positions = positions;
+    a.slot_mapping = slot_mapping;
+    a.tree_mask = tree_mask;
+    a.held_out = held_out;
+    a.free_next = free_next;
+    a.d_err = d_err;
+    e = pkv::launch_build_batch(a, info.sm_count, s);
+    if (e != cudaSuccess) return cuda_fail(e, "build batch launch");
+    return ok();
+}
+
+kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_dtype dtype, int64_t q_stride,
+                          int64_t key_stride, int64_t value_stride, int32_t num_tokens, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, const void *q_weight, const void *k_weight,
+                          float eps, const int32_t *positions, const float *cos_sin, int32_t max_position,
+                          int32_t rotary_dim, int32_t interleaved, void *q_out, int64_t q_out_stride, void *k_out,
+                          int64_t k_out_stride, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                          kv_dtype cache_dtype, int32_t num_blocks, int32_t block_size, float k_scale,
+                          float v_scale, int32_t *d_err, void *stream) {
+    if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim < 8 || rotary_dim < 0 || max_position < 0)
+        return fail(KV_ERR_INVALID_ARG, "invalid size argument");
+    if (dtype != KV_F16 && dtype != KV_BF16) return fail(KV_ERR_UNSUPPORTED, "q, key and value must be fp16 or bf16");
+    if (head_dim % 8 || head_dim > 256)
+        return fail(KV_ERR_UNSUPPORTED, "head_dim %d (supported: multiples of 8 up to 256)", head_dim);
+    if (rotary_dim % 16 || rotary_dim > head_dim)
+        return fail(KV_ERR_UNSUPPORTED, "rotary_dim %d (supported: multiples of 16 up to head_dim)", rotary_dim);
+    if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(KV_ERR_INVALID_ARG, "eps must be finite and >= 0");
+    const bool write = slot_mapping != nullptr;
+    if (write ? (!value || !k_cache || !v_cache) && num_tokens > 0 : (k_cache || v_cache))
+        return fail(KV_ERR_INVALID_ARG, "value, slot_mapping and both caches are given together or not at all");
+    if (write && (num_blocks < 0 || block_size < 1)) return fail(KV_ERR_INVALID_ARG, "invalid cache size");
+    if (write && cache_dtype != dtype && cache_dtype != KV_FP8_E4M3)
+        return fail(KV_ERR_UNSUPPORTED, "cache dtype must equal the source dtype or be E4M3");
+    if (write && cache_dtype == KV_FP8_E4M3 &&
+        !(k_scale > 0.f && v_scale > 0.f && std::isfinite(k_scale) && std::isfinite(v_scale)))
+        return fail(KV_ERR_INVALID_ARG, "E4M3 scales must be finite and > 0");
+    if (num_tokens == 0) return ok();
+    if (!q || !key || !q_out || (!k_out && !write)) return fail(KV_ERR_INVALID_ARG, "null pointer");
+    if (rotary_dim > 0 && (!positions || !cos_sin)) return fail(KV_ERR_INVALID_ARG, "null positions or cos_sin");
+    const int64_t qrow = static_cast<int64_t>(num_q_heads) * head_dim, krow = static_cast<int64_t>(num_kv_heads) * head_dim;
+    if (q_stride < qrow || q_out_stride < qrow || key_stride < krow || (k_out && k_out_stride < krow) ||
+        (write && value_stride < krow) || q_stride % 8 || q_out_stride % 8 || key_stride % 8 ||
+        (k_out && k_out_stride % 8) || (write && value_stride % 8))
+        return fail(KV_ERR_INVALID_ARG, "token strides must be >= heads*head_dim and multiples of 8");
+    if ((q_out == q && q_out_stride != q_stride) || (k_out && k_out == key && k_out_stride != key_stride))
+        return fail(KV_ERR_INVALID_ARG, "an output over its input must have its stride");
+    if (!aligned(q, 16) || !aligned(key, 16) || (write && !aligned(value, 16)) || !aligned(q_out, 16) ||
+        !aligned(k_out, 16) || !aligned(q_weight, 16) || !aligned(k_weight, 16) || !aligned(cos_sin, 16) ||
+        !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 8) ||
+        !aligned(d_err, 4))
+        return fail(KV_ERR_INVALID_ARG, "q, key, value, outputs, weights, cos_sin and caches must be 16-byte aligned");
+    int dev;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = bind_device(s, &dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device of stream");
+    DeviceInfo info;
+    if ((e = device_info(dev, &info)) != cudaSuccess) return cuda_fail(e, "device attributes");
+    pkv::RopeArgs a;
+    a.q = q;
+    a.key = key;
+    a.value = value;
+    a.q_stride = q_stride;
+    a.key_stride = key_stride;
+    a.value_stride = value_stride;
+    a.num_tokens = num_tokens;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.head_dim = head_dim;
+    a.q_weight = q_weight;
+    a.k_weight = k_weight;
+    a.eps = eps;
+    a.positions = positions;
+    a.cos_sin = cos_sin;
+    a.max_position = max_position;
+    a.rotary_dim = rotary_dim;
+    a.interleaved = interleaved;
+    a.q_out = q_out;
+    a.k_out = k_out;
+    a.q_out_stride = q_out_stride;
+    a.k_out_stride = k_out_stride;
+    a.slot_mapping = slot_mapping;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.cache_fp8 = write && cache_dtype == KV_FP8_E4M3;
+    a.total_slots = write ? static_cast<int64_t>(num_blocks) * block_size : 0;
+    a.k_scale = k_scale;
+    a.v_scale = v_scale;
+    a.parts = 1;
+    a.d_err = d_err;
+    e = pkv::launch_qk_norm_rope(a, dtype, info.sm_count, s);
+    if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
+    return ok();
+}
+
+// Sizes that kv_paged_attention_tree and its workspace query check alike.
+static kv_status check_tree_sizes(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t num_workers) {
+    if (num_seqs < 0 || max_query_len < 0 || num_q_heads < 1 || num_kv_heads < 1 || num_workers < 0)
+        return fail(KV_ERR_INVALID_ARG, "invalid size argument");
+    if (num_q_heads % num_kv_heads)
+        return fail(KV_ERR_INVALID_ARG, "num_q_heads (%d) is not a multiple of num_kv_heads (%d)", num_q_heads,
+                    num_kv_heads);
+    if (num_q_heads / num_kv_heads > 128)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: num_q_heads / num_kv_heads must be at most 128");
+    if (head_dim != 64 && head_dim != 128)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: head_dim %d (supported: 64, 128)", head_dim);
+    if (max_query_len > KV_MAX_TREE)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: max_query_len %d (at most %d)", max_query_len, KV_MAX_TREE);
+    return KV_OK;
+}
+
+size_t kv_paged_attention_tree_workspace_size(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                                              int32_t num_kv_heads, int32_t head_dim, int32_t num_workers) {
+    if (check_tree_sizes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, num_workers) != KV_OK)
+        return SIZE_MAX;
+    ok();
+    return 0;
+}
+
+kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs,
+                                  int32_t num_tokens, int32_t max_query_len, int32_t num_q_heads,
+                                  const void *k_cache, const void *v_cache, kv_dtype cache_dtype,
+                                  int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+                                  const int32_t *block_table, int64_t bt_stride, int32_t max_blocks_per_seq,
+                                  const int32_t *seq_lens, int32_t max_seq_len, float scale, int32_t window,
+                                  const uint64_t *tree_mask, int32_t num_workers, void *workspace,
+                                  size_t workspace_bytes, void *out, float *lse_out, int32_t *d_err, void *stream) {
+    if (num_tokens < 0 || num_blocks < 1 || max_blocks_per_seq < 0 || bt_stride < max_blocks_per_seq ||
+        max_seq_len < 0 || window < 0)
+        return fail(KV_ERR_INVALID_ARG, "invalid size argument");
+    kv_status st = check_tree_sizes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, num_workers);
+    if (st != KV_OK) return st;
+    if (q_dtype != KV_F16 && q_dtype != KV_BF16)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: q must be fp16 or bf16");
+    if (cache_dtype != q_dtype)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: the cache dtype must equal the q dtype");
+    if (block_size != 8 && block_size != 16 && block_size != 32)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: block_size must be 8, 16 or 32");
+    if (window > 0 && window < KV_MAX_TREE)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: window must be 0 or at least %d", KV_MAX_TREE);
+    if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return ok();
+    if (!q || !query_start_loc || !k_cache || !v_cache || !block_table || !seq_lens || !tree_mask || !out)
+        return fail(KV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(out, 16))
+        return fail(KV_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned");
+    if (!aligned(query_start_loc, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(tree_mask, 8) ||
+        !aligned(lse_out, 4) || !aligned(d_err, 4))
+        return fail(KV_ERR_INVALID_ARG, "misaligned pointer");
+    int dev;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = bind_device(s, &dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device of stream");
+    (void)workspace;
+    (void)workspace_bytes;
+    pkv::TreeArgs a;
+    a.q = q;
+    a.query_start_loc = query_start_loc;
+    a.seq_lens = seq_lens;
+    a.block_table = block_table;
+    a.bt_stride = bt_stride;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.tree_mask = tree_mask;
+    a.num_seqs = num_seqs;
+    a.num_tokens = num_tokens;
+    a.max_query_len = max_query_len;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = num_kv_heads;
+    a.block_size = block_size;
+    a.num_blocks = num_blocks;
+    a.max_seq_len = max_seq_len;
+    a.window = window;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.k_cache = k_cache;
+    a.v_cache = v_cache;
+    a.out = out;
+    a.lse_out = lse_out;
+    a.d_err = d_err;
+    e = pkv::launch_tree_attention(a, head_dim, q_dtype, s);
+    if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
+    return ok();
+}
+
 }  // extern "C"

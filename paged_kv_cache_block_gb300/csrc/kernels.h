@@ -10,6 +10,7 @@
 #include "../../include/pagedkv_blocks.h"
 #include "../../include/pagedkv_int4.h"
 #include "../../include/pagedkv_selftest.h"
+#include "../../include/pagedkv_step.h"
 
 namespace pkv {
 
@@ -154,6 +155,66 @@ struct PrefillArgs {
 size_t prefill_smem_bytes();
 cudaError_t launch_prefill(const CUtensorMap &tmap_q, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                            const PrefillArgs &a, int q_dtype, cudaStream_t stream);
+
+// Metadata of a step from its requests' lengths (kv_build_batch).
+struct BatchArgs {
+    const int32_t *context_lens, *new_lens, *held_blocks, *parents;
+    int32_t num_seqs, num_tokens;
+    int32_t *block_table;
+    int64_t bt_stride;
+    int32_t max_blocks_per_seq, block_shift, num_blocks;  // block_shift: log2(block_size)
+    const int32_t *free_blocks;
+    int32_t num_free;
+    const int32_t *free_start;
+    int32_t *query_start_loc, *seq_lens, *positions;
+    int64_t *slot_mapping;
+    uint64_t *tree_mask;
+    int32_t *held_out, *free_next;
+    int32_t *d_err;
+};
+
+cudaError_t launch_build_batch(const BatchArgs &a, int sm_count, cudaStream_t stream);
+
+// Query/key norm, rotation and cache write (kv_qk_norm_rope); strides in elements.
+struct RopeArgs {
+    const void *q, *key, *value;
+    int64_t q_stride, key_stride, value_stride;
+    int32_t num_tokens, num_q_heads, num_kv_heads, head_dim;
+    const void *q_weight, *k_weight;
+    float eps;
+    const int32_t *positions;
+    const float *cos_sin;
+    int32_t max_position, rotary_dim, interleaved;
+    void *q_out, *k_out;
+    int64_t q_out_stride, k_out_stride;
+    const int64_t *slot_mapping;
+    void *k_cache, *v_cache;
+    int32_t cache_fp8;
+    int64_t total_slots;
+    float k_scale, v_scale;
+    int32_t parts;  // warps a token's heads are shared out to (set by the launch)
+    int32_t *d_err;
+};
+
+cudaError_t launch_qk_norm_rope(const RopeArgs &a, int dtype, int sm_count, cudaStream_t stream);
+
+// Attention of drafted trees (kv_paged_attention_tree).
+struct TreeArgs {
+    const void *q;
+    const int32_t *query_start_loc, *seq_lens, *block_table;
+    int64_t bt_stride;
+    int32_t max_blocks_per_seq;
+    const uint64_t *tree_mask;
+    int32_t num_seqs, num_tokens, max_query_len, num_q_heads, num_kv_heads;
+    int32_t block_size, num_blocks, max_seq_len, window;
+    float scale_log2;  // softmax scale * log2(e)
+    const void *k_cache, *v_cache;
+    void *out;
+    float *lse_out;
+    int32_t *d_err;
+};
+
+cudaError_t launch_tree_attention(const TreeArgs &a, int head_dim, int q_dtype, cudaStream_t stream);
 
 // kv_selftest_bounded_wait: one thread waits limit_us on an mbarrier nothing completes.
 cudaError_t launch_selftest_bounded_wait(int32_t limit_us, int32_t *d_err, int32_t *d_waited_us,

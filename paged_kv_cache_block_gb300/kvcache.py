@@ -18,12 +18,16 @@ Same names as the C ABI:
     paged_attention_decode_int4(...) kv_paged_attention_decode_int4
     decode_step_int4(...)            kv_decode_step_int4
     selftest_bounded_wait(...)       kv_selftest_bounded_wait         (include/pagedkv_selftest.h)
+    build_batch(...)                 kv_build_batch                   (include/pagedkv_step.h)
+    qk_norm_rope(...)                kv_qk_norm_rope
+    qk_norm_rope_and_cache(...)      kv_qk_norm_rope, with the write of K and V into the cache
+    paged_attention_tree(...)        kv_paged_attention_tree
 """
 from __future__ import annotations
 
 import ctypes
 import os
-from typing import Optional
+from typing import NamedTuple, Optional, Tuple
 
 import torch
 
@@ -32,6 +36,8 @@ from . import build as _build
 KV_F16, KV_BF16, KV_FP8_E4M3, KV_INT4 = 0, 1, 2, 3
 KV_DERR_BAD_BLOCK, KV_DERR_BAD_SLOT, KV_DERR_PAST_TABLE, KV_DERR_TIMEOUT, KV_DERR_BAD_LEN = 1, 2, 4, 8, 16
 KV_DERR_BAD_UPDATE = 32
+KV_DERR_BAD_POS, KV_DERR_NO_BLOCKS, KV_DERR_BAD_TREE = 64, 128, 256
+KV_MAX_TREE = 64
 KV_OK, KV_ERR_INVALID_ARG, KV_ERR_UNSUPPORTED, KV_ERR_CUDA, KV_ERR_WORKSPACE, KV_ERR_OUT_OF_BLOCKS = range(6)
 KV_MAX_ZERO_CACHES = 128
 SIZE_MAX = (1 << 64) - 1
@@ -115,6 +121,17 @@ def _load() -> ctypes.CDLL:
     lib.kv_decode_step_int4.restype = i32
     lib.kv_selftest_bounded_wait.argtypes = [i32, P, P, P]
     lib.kv_selftest_bounded_wait.restype = i32
+    lib.kv_build_batch.argtypes = [P, P, P, P, i32, i32, P, i64, i32, i32, i32, P, i32, P, P, P, P, P, P, P, P,
+                                   P, P]
+    lib.kv_build_batch.restype = i32
+    lib.kv_qk_norm_rope.argtypes = [P, P, P, i32, i64, i64, i64, i32, i32, i32, i32, P, P, f32, P, P, i32, i32,
+                                    i32, P, i64, P, i64, P, P, P, i32, i32, i32, f32, f32, P, P]
+    lib.kv_qk_norm_rope.restype = i32
+    lib.kv_paged_attention_tree.argtypes = [P, i32, P, i32, i32, i32, i32, P, P, i32, i32, i32, i32, i32, P, i64,
+                                            i32, P, i32, f32, i32, P, i32, P, sz, P, P, P, P]
+    lib.kv_paged_attention_tree.restype = i32
+    lib.kv_paged_attention_tree_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
+    lib.kv_paged_attention_tree_workspace_size.restype = sz
     lib.kv_status_string.argtypes = [i32]
     lib.kv_status_string.restype = ctypes.c_char_p
     lib.kv_last_error.argtypes = []
@@ -508,3 +525,234 @@ def apply_block_updates(updates: torch.Tensor, block_table: torch.Tensor, zero_i
         block_table.shape[0], block_table.shape[1] if max_blocks_per_row is None else max_blocks_per_row,
         _ptr(zero_ids) if n_zero else None, n_zero, ptrs, len(caches), block_bytes, num_blocks,
         _ptr(d_err), _stream(stream)))
+
+
+# ---------------------------------------------------------------- a serving step (pagedkv_step.h)
+
+def _want(cond: bool, what: str) -> None:
+    if not cond:
+        raise KVError(KV_ERR_INVALID_ARG, what)
+
+
+def _place(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
+    """The CUDA device that holds every given tensor."""
+    dev = first.device
+    _want(dev.type == "cuda" and all(t is None or t.device == dev for t in others),
+          "every tensor must be on one CUDA device")
+    return dev
+
+
+def _ints(t: Optional[torch.Tensor], n: Optional[int], what: str, dtype=torch.int32) -> None:
+    _want(t is None or (t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() == n)),
+          f"{what}: a contiguous {dtype} tensor" + ("" if n is None else f" of {n} values"))
+
+
+def _call(dev: torch.device, stream, fn, *args) -> None:
+    """fn(*args, stream) with the tensors' device current."""
+    _want(stream is None or stream.device == dev, "the stream must be of the tensors' device")
+    s = torch.cuda.current_stream(dev) if stream is None else stream
+    if dev.index == torch.cuda.current_device():
+        _check(fn(*args, s.cuda_stream))
+    else:
+        with torch.cuda.device(dev):
+            _check(fn(*args, s.cuda_stream))
+
+
+def _table_width(t: torch.Tensor, rows: int, max_blocks: Optional[int]) -> int:
+    _want(t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] == rows and
+          (t.stride(1) == 1 or t.shape[1] <= 1 or rows == 0), "block_table: int32 [B, W] with rows in one piece")
+    width = t.shape[1] if max_blocks is None else max_blocks
+    _want(0 <= width <= t.shape[1], "max_blocks_per_seq is past the table's rows")
+    return width
+
+
+def _table_stride(t: torch.Tensor) -> int:
+    # the stride of a single row means nothing; it only has to hold the row
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+
+
+class Batch(NamedTuple):
+    """The metadata of a step (kv_build_batch); tree_mask is None without parents."""
+    query_start_loc: torch.Tensor
+    seq_lens: torch.Tensor
+    positions: torch.Tensor
+    slot_mapping: torch.Tensor
+    held_blocks: torch.Tensor
+    free_next: torch.Tensor
+    tree_mask: Optional[torch.Tensor]
+
+
+def batch_buffers(num_seqs: int, num_tokens: int, trees: bool = False, device="cuda") -> Batch:
+    """Buffers for build_batch's ``out`` (a loop that chains steps keeps two and swaps them)."""
+    def new(n, dtype=torch.int32):
+        return torch.empty(n, dtype=dtype, device=device)
+    return Batch(new(num_seqs + 1), new(num_seqs), new(num_tokens), new(num_tokens, torch.int64), new(num_seqs),
+                 new(1), new(num_tokens, torch.int64) if trees else None)
+
+
+def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
+                free_blocks: torch.Tensor, num_tokens: int, block_size: int, num_blocks: int,
+                held_blocks: Optional[torch.Tensor] = None, parents: Optional[torch.Tensor] = None,
+                free_start: Optional[torch.Tensor] = None, out: Optional[Batch] = None,
+                d_err: Optional[torch.Tensor] = None, max_blocks_per_seq: Optional[int] = None,
+                stream=None) -> Batch:
+    """kv_build_batch: context_lens, new_lens and held_blocks int32 [B]; block_table int32 [B, W],
+    updated in place; free_blocks int32 [F]; parents int32 [num_tokens] for drafted trees;
+    free_start int32 [1].  The masks are int64 words (bit j = token j of the request's tree)."""
+    B = context_lens.shape[0]
+    dev = _place(context_lens, new_lens, block_table, free_blocks, held_blocks, parents, free_start, d_err)
+    for t, n, what in ((context_lens, B, "context_lens"), (new_lens, B, "new_lens"), (held_blocks, B, "held_blocks"),
+                       (parents, num_tokens, "parents"), (free_blocks, None, "free_blocks"),
+                       (free_start, 1, "free_start"), (d_err, None, "d_err")):
+        _ints(t, n, what)
+    width = _table_width(block_table, B, max_blocks_per_seq)
+    if out is None:
+        out = batch_buffers(B, num_tokens, parents is not None, dev)
+    else:
+        _place(context_lens, *out)
+        for t, n, what in ((out.query_start_loc, B + 1, "query_start_loc"), (out.seq_lens, B, "seq_lens"),
+                           (out.positions, num_tokens, "positions"), (out.held_blocks, B, "held_blocks"),
+                           (out.free_next, 1, "free_next")):
+            _ints(t, n, what)
+        _ints(out.slot_mapping, num_tokens, "slot_mapping", torch.int64)
+        _ints(out.tree_mask, num_tokens, "tree_mask", torch.int64)
+        _want((out.tree_mask is None) == (parents is None), "tree_mask is given exactly when parents are")
+    _call(dev, stream, lib.kv_build_batch, _ptr(context_lens), _ptr(new_lens), _ptr(held_blocks), _ptr(parents), B,
+          num_tokens, _ptr(block_table), _table_stride(block_table), width, block_size, num_blocks,
+          _ptr(free_blocks), free_blocks.numel(), _ptr(free_start), _ptr(out.query_start_loc), _ptr(out.seq_lens),
+          _ptr(out.positions), _ptr(out.slot_mapping), _ptr(out.tree_mask), _ptr(out.held_blocks),
+          _ptr(out.free_next), _ptr(d_err))
+    return out
+
+
+def _heads(t: torch.Tensor, T: int, D: int, dtype, what: str) -> None:
+    _want(t.dtype == dtype and t.dim() == 3 and t.shape[0] == T and t.shape[2] == D and
+          (t.numel() == 0 or (t.stride(2) == 1 and (t.stride(1) == D or t.shape[1] == 1))),
+          f"{what}: {dtype} [{T}, heads, {D}] with each token's heads in one piece")
+
+
+def _token_stride(t: torch.Tensor) -> int:
+    # the stride of a single token means nothing; it only has to hold the row
+    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] * t.shape[2] // 8) * 8
+
+
+def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
+               interleaved, k_scale, v_scale, q_out, k_out, d_err, stream):
+    _want(q.dim() == 3 and key.dim() == 3, "q and key: [T, heads, D]")
+    T, Hq, D = q.shape
+    Hkv, dt = key.shape[1], q.dtype
+    dev = _place(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, q_out, k_out,
+                 d_err)
+    _heads(q, T, D, dt, "q")
+    _heads(key, T, D, dt, "key")
+    _heads(q_out, T, D, dt, "q_out")
+    _want(q_out.shape[1] == Hq, "q_out has other heads than q")
+    if k_out is not None:
+        _heads(k_out, T, D, dt, "k_out")
+        _want(k_out.shape[1] == Hkv, "k_out has other heads than key")
+    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        _want(w is None or (w.dtype == dt and w.shape == (D,) and (w.is_contiguous() or D == 1)), f"{what}: {dt} [{D}]")
+    _ints(positions, T, "positions")
+    _ints(d_err, None, "d_err")
+    _want(cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()),
+          "cos_sin: contiguous float32 [max_position, rotary_dim]")
+    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
+    cache_dtype, NB, bs, vstride = 0, 0, 1, 0
+    if slot_mapping is not None:
+        _ints(slot_mapping, T, "slot_mapping", torch.int64)
+        _heads(value, T, D, dt, "value")
+        _want(value.shape[1] == Hkv, "value has other heads than key")
+        _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and tuple(k_cache.shape[2:]) == (Hkv, D) and
+              k_cache.dtype == v_cache.dtype and k_cache.is_contiguous() and v_cache.is_contiguous(),
+              f"caches: two contiguous [blocks, block_size, {Hkv}, {D}] of one type")
+        NB, bs = k_cache.shape[:2]
+        cache_dtype, vstride = dtype_code(k_cache.dtype), _token_stride(value)
+    _call(dev, stream, lib.kv_qk_norm_rope, _ptr(q), _ptr(key), _ptr(value), dtype_code(dt), _token_stride(q),
+          _token_stride(key), vstride, T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions),
+          _ptr(cos_sin), max_pos, rot, int(interleaved), _ptr(q_out), _token_stride(q_out), _ptr(k_out),
+          0 if k_out is None else _token_stride(k_out), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), cache_dtype,
+          NB, bs, float(k_scale), float(v_scale), _ptr(d_err))
+
+
+def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: Optional[torch.Tensor],
+                 cos_sin: Optional[torch.Tensor], q_weight: Optional[torch.Tensor] = None,
+                 k_weight: Optional[torch.Tensor] = None, eps: float = 1e-6, interleaved: bool = False,
+                 q_out: Optional[torch.Tensor] = None, k_out: Optional[torch.Tensor] = None,
+                 d_err: Optional[torch.Tensor] = None, stream=None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """kv_qk_norm_rope without the cache: q [T, Hq, D] and key [T, Hkv, D] (views of one
+    projection will do; token stride = stride(0)), positions int32 [T], cos_sin float32
+    [max_position, rotary_dim].  q_out and k_out may be q and key."""
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    if k_out is None:
+        k_out = torch.empty(key.shape, dtype=key.dtype, device=key.device)
+    _norm_rope(q, key, None, positions, cos_sin, None, None, None, q_weight, k_weight, eps, interleaved, 1.0, 1.0,
+               q_out, k_out, d_err, stream)
+    return q_out, k_out
+
+
+def qk_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                           positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                           slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                           q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                           eps: float = 1e-6, interleaved: bool = False, k_scale: float = 1.0,
+                           v_scale: float = 1.0, q_out: Optional[torch.Tensor] = None,
+                           k_out: Optional[torch.Tensor] = None, d_err: Optional[torch.Tensor] = None,
+                           stream=None) -> torch.Tensor:
+    """kv_qk_norm_rope with the write of the turned keys and of the values into their slots;
+    returns the queries (and fills k_out when it is given)."""
+    _want(slot_mapping is not None and value is not None and k_cache is not None and v_cache is not None,
+          "value, slot_mapping and both caches are needed")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps, interleaved,
+               k_scale, v_scale, q_out, k_out, d_err, stream)
+    return q_out
+
+
+def paged_attention_tree_workspace_size(num_seqs: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
+                                        head_dim: int, num_workers: int = 0) -> int:
+    n = lib.kv_paged_attention_tree_workspace_size(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim,
+                                                   num_workers)
+    if n == SIZE_MAX:
+        raise KVError(2, lib.kv_last_error().decode() or "invalid or unsupported sizes")
+    return int(n)
+
+
+def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                         seq_lens: torch.Tensor, query_start_loc: torch.Tensor, tree_mask: torch.Tensor,
+                         max_seq_len: int, max_query_len: int, scale: float, window: int = 0, num_workers: int = 0,
+                         workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                         lse_out: Optional[torch.Tensor] = None, d_err: Optional[torch.Tensor] = None,
+                         max_blocks_per_seq: Optional[int] = None, stream=None) -> torch.Tensor:
+    """kv_paged_attention_tree: q [T, Hq, D] (the drafted tokens of sequence b are rows
+    query_start_loc[b] .. query_start_loc[b+1]-1); caches [NB, bs, Hkv, D]; block_table int32 [B, W];
+    seq_lens int32 [B] (including the drafted tokens); tree_mask int64 [T]."""
+    _want(q.dim() == 3 and q.is_contiguous(), "q: contiguous [T, heads, D]")
+    T, Hq, D = q.shape
+    B = seq_lens.shape[0]
+    dev = _place(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, tree_mask, workspace, out, lse_out, d_err)
+    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[3] == D and
+          k_cache.dtype == v_cache.dtype and k_cache.is_contiguous() and v_cache.is_contiguous(),
+          f"caches: two contiguous [blocks, block_size, heads, {D}] of one type")
+    NB, bs, Hkv, _ = k_cache.shape
+    _ints(seq_lens, B, "seq_lens")
+    _ints(query_start_loc, B + 1, "query_start_loc")
+    _ints(tree_mask, T, "tree_mask", torch.int64)
+    _ints(d_err, None, "d_err")
+    width = _table_width(block_table, B, max_blocks_per_seq)
+    _want(out is None or (out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()), "out: like q")
+    _want(workspace is None or workspace.is_contiguous(), "workspace: contiguous")
+    _want(lse_out is None or (lse_out.dtype == torch.float32 and tuple(lse_out.shape) == (T, Hq) and
+                              lse_out.is_contiguous()), f"lse_out: contiguous float32 [{T}, {Hq}]")
+    if out is None:
+        out = torch.empty_like(q)
+    need = paged_attention_tree_workspace_size(B, max_query_len, Hq, Hkv, D, num_workers)
+    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
+        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _call(dev, stream, lib.kv_paged_attention_tree, _ptr(q), dtype_code(q.dtype), _ptr(query_start_loc), B, T,
+          max_query_len, Hq, _ptr(k_cache), _ptr(v_cache), dtype_code(k_cache.dtype), Hkv, D, bs, NB,
+          _ptr(block_table), _table_stride(block_table), width, _ptr(seq_lens), max_seq_len, float(scale),
+          window, _ptr(tree_mask), num_workers, _ptr(workspace), ws_bytes, _ptr(out), _ptr(lse_out), _ptr(d_err))
+    return out
