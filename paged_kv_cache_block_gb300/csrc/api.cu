@@ -1148,6 +1148,7 @@ static kv_status check_tree_sizes(int32_t num_seqs, int32_t max_query_len, int32
         return fail(KV_ERR_UNSUPPORTED, "tree attention: head_dim %d (supported: 64, 128)", head_dim);
     if (max_query_len > KV_MAX_TREE)
         return fail(KV_ERR_UNSUPPORTED, "tree attention: max_query_len %d (at most %d)", max_query_len, KV_MAX_TREE);
+    if (num_workers > 32767) return fail(KV_ERR_UNSUPPORTED, "tree attention: num_workers > 32767");
     return KV_OK;
 }
 
@@ -1155,8 +1156,15 @@ size_t kv_paged_attention_tree_workspace_size(int32_t num_seqs, int32_t max_quer
                                               int32_t num_kv_heads, int32_t head_dim, int32_t num_workers) {
     if (check_tree_sizes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, num_workers) != KV_OK)
         return SIZE_MAX;
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    DeviceInfo info;
+    if (e != cudaSuccess || (e = device_info(dev, &info)) != cudaSuccess) {
+        cuda_fail(e, "device attributes");
+        return SIZE_MAX;
+    }
     ok();
-    return 0;
+    return pkv::plan_tree(max_query_len, num_q_heads / num_kv_heads, head_dim, num_workers, info.sm_count).workspace_bytes;
 }
 
 kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs,
@@ -1193,8 +1201,22 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = bind_device(s, &dev);
     if (e != cudaSuccess) return cuda_fail(e, "device of stream");
-    (void)workspace;
-    (void)workspace_bytes;
+    DeviceInfo info;
+    if ((e = device_info(dev, &info)) != cudaSuccess) return cuda_fail(e, "device attributes");
+    const int32_t g = num_q_heads / num_kv_heads;
+    const pkv::TreePlan plan = pkv::plan_tree(max_query_len, g, head_dim, num_workers, info.sm_count);
+    if (static_cast<size_t>(info.smem_optin) < plan.smem_bytes)
+        return fail(KV_ERR_UNSUPPORTED, "tree attention: needs %zu bytes of shared memory per block, the device has %d",
+                    plan.smem_bytes, info.smem_optin);
+    if (!workspace || workspace_bytes < plan.workspace_bytes)
+        return fail(KV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.workspace_bytes,
+                    workspace ? workspace_bytes : 0);
+    if (!aligned(workspace, 256)) return fail(KV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    CUtensorMap tq, tk, tv;
+    st = encode_query_map(&tq, q, num_tokens, num_q_heads, head_dim, g, plan.tokens_per_tile);
+    if (st == KV_OK) st = encode_cache_map(&tk, k_cache, cache_dtype, num_blocks, block_size, num_kv_heads, head_dim, 1);
+    if (st == KV_OK) st = encode_cache_map(&tv, v_cache, cache_dtype, num_blocks, block_size, num_kv_heads, head_dim, 1);
+    if (st != KV_OK) return st;
     pkv::TreeArgs a;
     a.q = q;
     a.query_start_loc = query_start_loc;
@@ -1213,12 +1235,11 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     a.max_seq_len = max_seq_len;
     a.window = window;
     a.scale_log2 = scale * 1.4426950408889634f;
-    a.k_cache = k_cache;
     a.v_cache = v_cache;
     a.out = out;
     a.lse_out = lse_out;
     a.d_err = d_err;
-    e = pkv::launch_tree_attention(a, head_dim, q_dtype, s);
+    e = pkv::launch_tree_attention(tq, tk, tv, a, plan, workspace, head_dim, q_dtype, dev, s);
     if (e != cudaSuccess) return cuda_fail(e, "tree attention launch");
     return ok();
 }

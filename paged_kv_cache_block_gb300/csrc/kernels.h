@@ -208,13 +208,24 @@ struct TreeArgs {
     int32_t num_seqs, num_tokens, max_query_len, num_q_heads, num_kv_heads;
     int32_t block_size, num_blocks, max_seq_len, window;
     float scale_log2;  // softmax scale * log2(e)
-    const void *k_cache, *v_cache;
+    const void *v_cache;
     void *out;
     float *lse_out;
     int32_t *d_err;
 };
 
-cudaError_t launch_tree_attention(const TreeArgs &a, int head_dim, int q_dtype, cudaStream_t stream);
+// Launch geometry and workspace layout of the tree kernels.
+struct TreePlan {
+    int workers;          // CTAs, each with one share of the key tiles
+    int tokens_per_tile;  // drafted tokens of a 128-row tile
+    int rows_per_item;    // rows of a partial result (128: every tree fits one row tile, else 256)
+    size_t lse_off, o_off, workspace_bytes, smem_bytes;
+};
+TreePlan plan_tree(int max_query_len, int group, int head_dim, int num_workers, int sm_count);
+
+cudaError_t launch_tree_attention(const CUtensorMap &tmap_q, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                  const TreeArgs &a, const TreePlan &plan, void *workspace, int head_dim, int q_dtype,
+                                  int dev, cudaStream_t stream);
 
 // kv_selftest_bounded_wait: one thread waits limit_us on an mbarrier nothing completes.
 cudaError_t launch_selftest_bounded_wait(int32_t limit_us, int32_t *d_err, int32_t *d_waited_us,

@@ -1,92 +1,965 @@
-// Attention of drafted trees over the paged cache (speculative decoding: "vLLM의 KV cache 연결
-// 흐름", section "EngineCore가 하는 일", several tokens a request and step; attention through the
-// block table as in its section "Slot mapping은 왜 필요한가").
+// Attention of drafted trees over the paged cache, on the fifth-generation tensor cores
+// (speculative decoding: "vLLM의 KV cache 연결 흐름", section "EngineCore가 하는 일", several tokens
+// a request and step; attention through the block table as in its section "Slot mapping은 왜
+// 필요한가").
 //
 // Row i of a sequence attends the context keys (those inside its window) and the drafted keys of
-// its mask:  out = sum_j p_j V_j / sum_j p_j,  p_j = exp2(scale log2(e) q.K_j - m).
-// One warp per (row, query head); a lane holds D / 32 dims of q and of the output, keys one after
-// another with a running maximum and sum in float32.
+// its mask word:  out = sum_j p_j V_j / sum_j p_j,  p_j = exp2(scale log2(e) q.K_j - m).
+//
+// The n drafted tokens x g heads of a kv head's group are its query rows, in tiles of up to 128
+// rows (whole tokens: 128 / g tokens, row r = token r / g, head r % g).  An item is (sequence, kv
+// head, two row tiles); its keys go in tiles of 128.  Two chains x = 0, 1 of
+//   S_x = Q K_j^T   tcgen05.mma, M 128, N 128; fp32 in TMEM
+//   P_x = exp2(S_x * scale - m)   one thread a row; 16-bit weights back into TMEM over S_x
+//   O_x += P_x V_j  tcgen05.mma, A = P_x in TMEM, fp32 in TMEM across key tiles
+// run at once, so that one chain's softmax overlaps the other's products.  An item with two row
+// tiles gives each chain one of them and both read every key tile.  An item with one row tile
+// (few drafted tokens, the case that is bound by reading the cache) gives chain x every second
+// key tile, and the chains' results are joined at the end.
+//
+// The flat list of (item, key tile) is cut into equal shares, one a CTA (an item costs kItemCost
+// tiles more), so the batch's lengths do not matter; an item that lies in several shares leaves a
+// partial result from each, joined by a second, small kernel.
+//
+// Warps (384 threads): 0-3 softmax of chain 0, 4-7 of chain 1 (thread = TMEM lane = query row), 8
+// TMA producer (Q once an item, K and V tiles through a ring), 9 and 10 issue the chains' MMAs, 11
+// cleans V tiles that hold keys which not every row sees: a weight of 0 times a NaN or an
+// infinity would not be 0, so values that no row sees are zeroed in shared memory, and non-finite
+// values that some rows see are zeroed and added afterwards to the rows that do see them.
+// Weights are taken against the reference maximum in use; only when a row's maximum exceeds it by
+// more than 2^8 are its O and sums rescaled.  Every wait is bounded (2 s): on expiry
+// KV_DERR_TIMEOUT is set, what was issued is drained, TMEM is freed and the CTA returns.
+#include <atomic>
+#include <type_traits>
+
 #include "common.cuh"
 #include "kernels.h"
+#include "tcgen05.cuh"
 
 namespace pkv {
 namespace {
 
-template <typename T, int D>
-__global__ void __launch_bounds__(256) tree_attention_kernel(const TreeArgs a) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
-    const int64_t t = w / a.num_q_heads;
-    const int hq = static_cast<int>(w - t * a.num_q_heads);
-    if (t >= a.num_tokens) return;
-    // the sequence: the last b with query_start_loc[b] <= t
-    int lo = 0, hi = a.num_seqs;
-    while (lo < hi) {
-        const int mid = (lo + hi) >> 1;
-        if (a.query_start_loc[mid + 1] <= t) lo = mid + 1;
-        else hi = mid;
-    }
-    const int b = lo;
-    if (b >= a.num_seqs || t < a.query_start_loc[b]) return;
-    const int q0 = a.query_start_loc[b], n = a.query_start_loc[b + 1] - q0, L = a.seq_lens[b];
-    const int64_t row = t * a.num_q_heads + hq;
-    T *out = static_cast<T *>(a.out) + row * D + lane * E;
-    const bool ok = q0 >= 0 && n <= a.max_query_len && q0 + n <= a.num_tokens && L >= n && L <= a.max_seq_len &&
-                    (L + a.block_size - 1) / a.block_size <= a.max_blocks_per_seq;
-    float o[E], m = -INFINITY, l = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = 0.f;
-    if (!ok) {
-        if (lane == 0) report(a.d_err, KV_DERR_BAD_LEN);
-    } else {
-        const int h = hq / (a.num_q_heads / a.num_kv_heads), ctx = L - n;
-        const uint64_t mask = a.tree_mask[t] & (n >= 64 ? ~0ull : (1ull << n) - 1);
-        const int pos = ctx - 1 + __popcll(mask);
-        const int first = a.window > 0 ? max(0, pos - a.window + 1) : 0;
-        float q[E];
-        const T *qs = static_cast<const T *>(a.q) + row * D + lane * E;
-#pragma unroll
-        for (int e = 0; e < E; ++e) q[e] = to_float<T>(qs[e]);
-        for (int j = first; j < L; ++j) {
-            if (j >= ctx && !((mask >> (j - ctx)) & 1)) continue;
-            const int id = a.block_table[b * a.bt_stride + j / a.block_size];
-            const bool good = id >= 0 && id < a.num_blocks;
-            if (!good && lane == 0) report(a.d_err, KV_DERR_BAD_BLOCK);
-            const int64_t at = ((static_cast<int64_t>(good ? id : 0) * a.block_size + j % a.block_size) * a.num_kv_heads + h) * D + lane * E;
-            float s = 0.f;
-#pragma unroll
-            for (int e = 0; e < E; ++e) s += q[e] * (good ? to_float<T>(static_cast<const T *>(a.k_cache)[at + e]) : 0.f);
-#pragma unroll
-            for (int x = 16; x > 0; x >>= 1) s += __shfl_xor_sync(0xffffffffu, s, x);
-            s *= a.scale_log2;
-            const float mn = fmaxf(m, s), f = m == mn ? 1.f : fast_exp2(m - mn), p = fast_exp2(s - mn);
-            m = mn;
-            l = l * f + p;
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                o[e] = o[e] * f + p * (good ? to_float<T>(static_cast<const T *>(a.v_cache)[at + e]) : 0.f);
-        }
-    }
-    const float inv = l == 0.f ? 0.f : 1.f / l;
-#pragma unroll
-    for (int e = 0; e < E; ++e) out[e] = from_float<T>(o[e] * inv);
-    if (a.lse_out && lane == 0) a.lse_out[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
+constexpr int kBM = 128;           // query rows of a row tile = TMEM lanes
+constexpr int kBN = 128;           // keys of a key tile
+constexpr int kHalf = 128 * 128;   // 128 rows x 64 16-bit elements (one swizzle column)
+constexpr int kThreads = 384;
+constexpr uint32_t kTmemCols = 512;
+constexpr uint32_t kColO = 256;
+constexpr float kRescaleLog2 = 8.0f;
+constexpr int kItemCost = 2;       // an item's fixed cost in key tiles
+constexpr int kMinShare = 4;       // least cost of a share: more than kItemCost, so that it holds a tile
+
+constexpr int kFlags = 8;
+
+template <int D> struct Tile {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kBytes = kHalves * kHalf;      // a Q, K or V tile
+    static constexpr int kStages = D == 128 ? 5 : 10;   // ring entries (160 KB)
+    static constexpr int kOffKV = 2 * kBytes;           // after Q_0, Q_1
+    static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // chain 1's maximum and sums: 3 x 128 floats
+    static constexpr int kOffBar = kOffJoin + 3 * 128 * 4;
+    static constexpr int kNumBars = 14 + 2 * kStages;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
+    static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
+    static_assert(kSmem + 128 <= 227 * 1024, "shared memory, with the kernel's static part");
+    // pieces whose V tiles can be in the ring at once, one more that the cleaning warp has begun,
+    // and one without mixed tiles (only a share's last)
+    static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
+};
+
+// mbarrier indices (+ x: one per chain)
+enum { kBarQFull = 0, kBarQEmpty = 1, kBarS = 2, kBarP = 4, kBarPv = 6, kBarPd = 8, kBarJoin = 10,
+       kBarJoined = 11, kBarDrain = 12, kBarKv = 14 };  // then KvFull[stages], KvEmpty[stages]
+
+struct TreeParams {
+    TreeArgs a;
+    int group, tokens_per_tile;
+    int workers;       // shares at most
+    int rows_per_item; // 128 or 256: rows of a partial result
+    int32_t *ws_first; // [workers][4] first piece of each share: sequence, item of it, key tile, -
+    float *ws_lse;     // [2 * workers][rows_per_item] log2-sum-exp2 of the partial results
+    float *ws_o;       // [2 * workers][rows_per_item][D] partial results, normalised
+};
+
+// A sequence's part of the work list.
+struct Seq {
+    int q0, n, L, ctx, kv_lo;  // first row, rows, length, context, first key any row sees
+    int j0, tiles;             // key tiles j0 .. j0 + tiles - 1 (128 keys each)
+    int pairs;                 // items a kv head (two row tiles each)
+};
+
+// The sequence's lengths; false when it has no rows, or is rejected (*rejected).
+__device__ __forceinline__ bool load_seq(const TreeParams &p, int b, Seq &s, bool *rejected) {
+    const TreeArgs &a = p.a;
+    s.q0 = a.query_start_loc[b];
+    s.n = a.query_start_loc[b + 1] - s.q0;
+    s.L = a.seq_lens[b];
+    const int bs = a.block_size;
+    *rejected = s.n > 0 && !(s.n <= a.max_query_len && s.q0 >= 0 && s.q0 <= a.num_tokens - s.n && s.L >= s.n &&
+                             s.L <= a.max_seq_len && (s.L - 1) / bs < a.max_blocks_per_seq);
+    if (s.n <= 0 || *rejected) return false;
+    s.ctx = s.L - s.n;
+    s.kv_lo = a.window > 0 ? max(0, s.ctx - a.window) : 0;
+    s.j0 = s.kv_lo / kBN;
+    s.tiles = (s.L - 1) / kBN + 1 - s.j0;
+    const int row_tiles = (s.n + p.tokens_per_tile - 1) / p.tokens_per_tile;
+    s.pairs = (row_tiles + 1) >> 1;
+    return true;
 }
 
-template <typename T> cudaError_t launch_typed(const TreeArgs &a, int head_dim, cudaStream_t stream) {
-    const int64_t blocks = (static_cast<int64_t>(a.num_tokens) * a.num_q_heads + 7) / 8;
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    if (head_dim == 128) tree_attention_kernel<T, 128><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
-    else tree_attention_kernel<T, 64><<<static_cast<unsigned>(blocks), 256, 0, stream>>>(a);
+__device__ __forceinline__ int64_t seq_cost(const TreeParams &p, int b) {
+    Seq s;
+    bool rejected;
+    if (!load_seq(p, b, s, &rejected)) return 0;
+    return static_cast<int64_t>(s.tiles + kItemCost) * s.pairs * p.a.num_kv_heads;
+}
+
+// The pieces of a share, in order: (item, key tiles ja .. jb - 1).  Every warp walks the same ones.
+struct Walk {
+    int b, idx;       // sequence, item of it (kv head * pairs + pair)
+    int64_t at;       // cost where the item starts
+    int64_t x0, x1;   // the share
+    Seq s;
+    int ja, jb;       // key tiles of the piece (absolute)
+    int h, pr, nt;    // kv head, pair, row tiles of the item (1 or 2)
+
+    __device__ __forceinline__ void start(const TreeParams &p, int b_, int idx_, int64_t at_, int64_t x0_, int64_t x1_) {
+        b = b_, idx = idx_, at = at_, x0 = x0_, x1 = x1_;
+        bool rejected;
+        load_seq(p, b, s, &rejected);
+    }
+    __device__ __forceinline__ bool next(const TreeParams &p) {
+        while (at < x1) {
+            const int64_t first = at + kItemCost;
+            ja = static_cast<int>(max(int64_t(0), x0 - first));
+            jb = static_cast<int>(min(static_cast<int64_t>(s.tiles), x1 - first));
+            const bool some = ja < jb;
+            if (some) {
+                h = idx / s.pairs;
+                pr = idx - h * s.pairs;
+                nt = s.n > (2 * pr + 1) * p.tokens_per_tile ? 2 : 1;
+                ja += s.j0;
+                jb += s.j0;
+                whole = ja == s.j0 && jb == s.j0 + s.tiles;
+                piece_b = b;
+                cur = s;
+            }
+            at = first + s.tiles;
+            if (++idx == s.pairs * p.a.num_kv_heads) {
+                idx = 0;
+                bool rejected = false;
+                while (++b < p.a.num_seqs && !load_seq(p, b, s, &rejected)) {}
+                if (b >= p.a.num_seqs) x1 = at;  // the end of the list
+            }
+            if (some) return true;
+        }
+        return false;
+    }
+    bool whole;       // the piece is its whole item
+    int piece_b;      // the piece's sequence
+    Seq cur;          // and its lengths
+};
+
+// Whether key tile j holds a key that not every row of the sequence sees.
+__device__ __forceinline__ bool mixed_tile(const TreeParams &p, const Seq &s, int j) {
+    const int k0 = j * kBN;
+    return k0 + kBN > s.ctx || (p.a.window > 0 && k0 < s.ctx + s.n - p.a.window);
+}
+
+// The keys k0 .. k0 + 31 a row sees (bit i: key k0 + i): context keys from klo, drafted keys of
+// the mask word.
+__device__ __forceinline__ uint32_t seen32(int k0, int ctx, int klo, uint64_t mask) {
+    const int lo = max(klo - k0, 0), hi = min(ctx - k0, 32);
+    uint32_t v = 0;
+    if (lo < hi) v = (hi == 32 ? 0xffffffffu : (1u << hi) - 1) & ~((1u << lo) - 1);  // lo < 32
+    const int d = k0 - ctx;
+    if (d >= 0) v |= d < 64 ? static_cast<uint32_t>(mask >> d) : 0u;
+    else if (d > -32) v |= static_cast<uint32_t>(mask << -d);
+    return v;
+}
+
+template <typename T> struct NonFinite;  // exponent bits all ones
+template <> struct NonFinite<__half> { static constexpr uint32_t mask = 0x7C00u; };
+template <> struct NonFinite<__nv_bfloat16> { static constexpr uint32_t mask = 0x7F80u; };
+
+template <typename T> __device__ __forceinline__ bool non_finite16(uint32_t bits) {
+    return (bits & NonFinite<T>::mask) == NonFinite<T>::mask;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// Add the non-finite values of V that a row sees among the keys [k0, k1) to its written result
+// (out16 of type T, or a float row): they were zeroed for the products.  Rare, so plain.
+template <typename T, int D>
+__device__ __noinline__ void add_non_finite(const TreeArgs &a, int b, int h, int k0, int k1, int ctx, int klo,
+                                            uint64_t mask, T *out16, float *out32) {
+    for (int k = k0; k < k1; ++k) {
+        const bool sees = k < ctx ? k >= klo : (mask >> (k - ctx)) & 1;
+        const int id = a.block_table[b * a.bt_stride + k / a.block_size];
+        if (!sees || id < 0 || id >= a.num_blocks) continue;
+        const T *v = static_cast<const T *>(a.v_cache) +
+                     ((static_cast<int64_t>(id) * a.block_size + k % a.block_size) * a.num_kv_heads + h) * D;
+        for (int d = 0; d < D; ++d) {
+            const float f = to_float<T>(v[d]);
+            if (isfinite(f)) continue;
+            if (out32) out32[d] += f;
+            else out16[d] = from_float<T>(to_float<T>(out16[d]) + f);
+        }
+    }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TreeParams p) {
+    using TL = Tile<D>;
+    constexpr int kStages = TL::kStages, kTileBytes = TL::kBytes;
+    const TreeArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = p.group, TQ = p.tokens_per_tile, bs = a.block_size;
+    const int c = blockIdx.x;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + TL::kOffBar);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + TL::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + TL::kOffMisc + 4);
+    volatile int *odd_flag = reinterpret_cast<volatile int *>(smem + TL::kOffMisc + 8);  // [kFlags], per piece
+    int32_t *cleaned = reinterpret_cast<int32_t *>(smem + TL::kOffMisc + 8 + 4 * kFlags);  // [kStages]: entry + 1
+    float *join = reinterpret_cast<float *>(smem + TL::kOffJoin);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto bar_full = [&](int s) { return smem_u32(&bars[kBarKv + s]); };
+    auto bar_empty = [&](int s) { return smem_u32(&bars[kBarKv + kStages + s]); };
+
+    // ---- the share: costs of the sequences summed over the block, then the sequence, item and
+    // cost where it starts
+    __shared__ int64_t warp_sum[kThreads / 32];
+    __shared__ int64_t start_at;
+    __shared__ int start_b, start_idx;
+    const int per = (a.num_seqs + kThreads - 1) / kThreads;
+    const int b_lo = min(a.num_seqs, static_cast<int>(threadIdx.x) * per), b_hi = min(a.num_seqs, b_lo + per);
+    int64_t sum = 0;
+    for (int b = b_lo; b < b_hi; ++b) sum += seq_cost(p, b);
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    const int64_t most = max(int64_t(1), total / kMinShare);
+    const int shares = total == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(p.workers), most));
+    const int64_t x0 = c < shares ? total * c / shares : 0, x1 = c < shares ? total * (c + 1) / shares : 0;
+    if (c < shares && x0 >= before && x0 < before + sum) {  // one thread
+        int64_t at = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const int64_t cost = seq_cost(p, b);
+            if (x0 < at + cost) {
+                Seq s;
+                bool rejected;
+                load_seq(p, b, s, &rejected);
+                const int idx = static_cast<int>((x0 - at) / (s.tiles + kItemCost));
+                start_b = b;
+                start_idx = idx;
+                start_at = at + static_cast<int64_t>(idx) * (s.tiles + kItemCost);
+                break;
+            }
+            at += cost;
+        }
+    }
+    // rows of rejected sequences are 0 (lse -inf)
+    for (int b = c; b < a.num_seqs; b += gridDim.x) {
+        Seq s;
+        bool rejected;
+        load_seq(p, b, s, &rejected);
+        if (!rejected) continue;
+        if (threadIdx.x == 0) report(a.d_err, KV_DERR_BAD_LEN);
+        const int64_t r0 = max(s.q0, 0), r1 = min(static_cast<int64_t>(s.q0) + s.n, static_cast<int64_t>(a.num_tokens));
+        const int64_t rows = (r1 - r0) * a.num_q_heads;
+        for (int64_t i = threadIdx.x; i < rows * (D / 8); i += kThreads)
+            reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + r0 * a.num_q_heads * D)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse_out)
+            for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse_out[r0 * a.num_q_heads + i] = -INFINITY;
+    }
+    if (c >= shares) {
+        if (threadIdx.x == 0) p.ws_first[4 * c] = -1;
+        return;
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(bar(kBarQFull), 1);
+        mbar_init(bar(kBarQEmpty), 2);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar(kBarS + x), 1);
+            mbar_init(bar(kBarP + x), 128);
+            mbar_init(bar(kBarPv + x), 1);
+            mbar_init(bar(kBarPd + x), 1);
+            mbar_init(bar(kBarDrain + x), 1);
+        }
+        mbar_init(bar(kBarJoin), 128);
+        mbar_init(bar(kBarJoined), 128);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar_full(s), 1);
+            mbar_init(bar_empty(s), 3);  // released by both chains and the cleaning warp
+        }
+        *abort_flag = 0;
+        for (int i = 0; i < kFlags; ++i) odd_flag[i] = 0;
+        for (int i = 0; i < kStages; ++i) cleaned[i] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    Walk w;
+    w.start(p, start_b, start_idx, start_at, x0, x1);
+
+    if (warp == 8) {
+        // ============================================================ TMA producer
+        const int bpt = kBN / bs;  // blocks of a key tile
+        const uint32_t q_bytes = static_cast<uint32_t>(TL::kHalves) * TQ * g * 128;
+        if (lane == 0) {
+            prefetch_tensormap(&tmap_q);
+            prefetch_tensormap(&tmap_k);
+            prefetch_tensormap(&tmap_v);
+        }
+        int entry = 0;  // ring entries filled
+        int piece = 0;
+        bool stop = false;
+        while (!stop && w.next(p)) {
+            const Seq s = w.cur;
+            if (piece == 0 && lane == 0) {
+                p.ws_first[4 * c] = w.piece_b;
+                p.ws_first[4 * c + 1] = w.h * s.pairs + w.pr;
+                p.ws_first[4 * c + 2] = w.ja - s.j0;
+            }
+            // block ids of key tile j: lane l holds block j * bpt + l
+            const int nblk = (s.L - 1) / bs + 1, first_blk = s.kv_lo / bs;
+            auto block_id = [&](int j) {
+                const int lb = j * bpt + lane;
+                int id = a.num_blocks;  // one past the pool: the copy reads zeros
+                if (lane < bpt && lb >= first_blk && lb < nblk) {
+                    const int e = a.block_table[static_cast<int64_t>(w.piece_b) * a.bt_stride + lb];
+                    if (e >= 0 && e < a.num_blocks) id = e;
+                    else report(a.d_err, KV_DERR_BAD_BLOCK);
+                }
+                return id;
+            };
+            int next_id = block_id(w.ja);
+            bool ok = true;
+            if (lane == 0) {
+                // Q of the item, once the piece before has formed its last scores
+                if (piece > 0) ok = mbar_wait_sleep(bar(kBarQEmpty), (piece - 1) & 1);
+                if (ok) {
+                    mbar_arrive_expect_tx(bar(kBarQFull), w.nt * q_bytes);
+                    for (int x = 0; x < w.nt; ++x)
+                        for (int hf = 0; hf < TL::kHalves; ++hf)
+                            tma_load_3d(smem_u32(smem + x * kTileBytes + hf * kHalf), &tmap_q, bar(kBarQFull), 64 * hf,
+                                        w.h * g, s.q0 + (2 * w.pr + x) * TQ);
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
+                if (lane == 0) {
+                    report(a.d_err, KV_DERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            ++piece;
+            for (int j = w.ja; j < w.jb && !stop; ++j) {
+                const int my_id = next_id;
+                if (j + 1 < w.jb) next_id = block_id(j + 1);
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    const int slot = entry % kStages;
+                    int quit = 0;
+                    if (lane == 0) {
+                        if (entry >= kStages && !mbar_wait_sleep(bar_empty(slot), (entry / kStages - 1) & 1)) {
+                            quit = 1;
+                            report(a.d_err, KV_DERR_TIMEOUT);
+                            *abort_flag = 1;
+                        } else if (*abort_flag) {
+                            quit = 1;
+                        }
+                        if (!quit) mbar_arrive_expect_tx(bar_full(slot), kTileBytes);
+                    }
+                    if (__shfl_sync(0xffffffffu, quit, 0)) {
+                        stop = true;
+                        break;
+                    }
+                    const CUtensorMap *m = is_v ? &tmap_v : &tmap_k;
+                    uint8_t *dst = smem + TL::kOffKV + slot * kTileBytes;
+                    for (int jb = 0; jb < bpt; ++jb) {
+                        const int id = __shfl_sync(0xffffffffu, my_id, jb);
+                        if (lane == 0)
+                            for (int hf = 0; hf < TL::kHalves; ++hf)
+                                tma_load_4d(smem_u32(dst + hf * kHalf + jb * bs * 128), m, bar_full(slot), 64 * hf, 0,
+                                            w.h, id);
+                    }
+                    ++entry;
+                }
+            }
+        }
+        // never leave with copies in flight into this CTA's shared memory
+        if (lane == 0) {
+            if (piece > 0 && !mbar_wait_sleep(bar(kBarQFull), (piece - 1) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+            for (int i = max(0, entry - kStages); i < entry; ++i)
+                if (!mbar_wait_sleep(bar_full(i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+        }
+    } else if (warp == 9 || warp == 10) {
+        // ============================================================ MMA issue, one warp a chain
+        // The whole warp runs the schedule (warp-uniform); one lane issues.  Chain x, key tile by
+        // key tile: S_x once the product that read the columns it overwrites has completed; O_x
+        // once the softmax has written P_x and the V tile has landed (and been cleaned).  The other
+        // chain's tiles are released as soon as they have landed: everyone who waits for a ring
+        // entry passes all of them in order, so that no phase of its barrier can be mistaken.
+        const int x = warp - 9;
+        constexpr uint32_t ab = AbFormat<T>::value;
+        constexpr uint32_t idesc_s = mma_idesc(ab, false, kBM, kBN);
+        constexpr uint32_t idesc_pv = mma_idesc(ab, true, kBM, D);
+        const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, 1024);
+        const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), kHalf, 1024);
+        const uint32_t t_s = tmem + x * 128, t_o = tmem + kColO + x * 128;
+        const bool leader = lane == 0;
+        auto wait_warp = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity));
+        };
+        int base = 0;                  // key tiles of the pieces before
+        int npv = 0;                   // products O_x committed
+        bool dead = false;
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (!wait_warp(bar(kBarQFull), piece & 1)) {
+                dead = true;
+                break;
+            }
+            const uint64_t dq = smem_desc(smem_u32(smem + (w.nt == 2 ? x * kTileBytes : 0)), 16, 1024);
+            const int step = w.nt == 2 ? 1 : 2;
+            const int first = w.ja + (w.nt == 2 ? 0 : x);
+            if (first >= w.jb && leader) mbar_arrive(bar(kBarQEmpty));  // no tile for this chain
+            for (int j = w.ja; j < w.jb; ++j) {
+                const bool last = j + step >= w.jb;
+                const int ek = 2 * (base + j - w.ja), ev = ek + 1;
+                const int sk = ek % kStages, sv = ev % kStages;
+                if (w.nt == 1 && ((j - w.ja) & 1) != x) {
+                    bool landed = wait_warp(bar_full(sk), (ek / kStages) & 1);
+                    if (landed && leader) mbar_arrive(bar_empty(sk));
+                    landed = landed && wait_warp(bar_full(sv), (ev / kStages) & 1);
+                    if (landed && leader) mbar_arrive(bar_empty(sv));
+                    __syncwarp();
+                    if (!landed) {
+                        dead = true;
+                        break;
+                    }
+                    continue;
+                }
+                if ((npv > 0 && !wait_warp(bar(kBarPd + x), (npv - 1) & 1)) ||
+                    !wait_warp(bar_full(sk), (ek / kStages) & 1)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                {
+                    const uint64_t dk = dkv + static_cast<uint64_t>((sk * kTileBytes) >> 4);
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < D / 16; ++k) {
+                            const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                            mma_f16(t_s, dq + off, dk + off, idesc_s, k > 0);
+                        }
+                        mma_commit(bar(kBarS + x));
+                        mma_commit(bar_empty(sk));
+                        if (last) mma_commit(bar(kBarQEmpty));
+                    }
+                    __syncwarp();
+                }
+                const bool mixed = mixed_tile(p, s, j);
+                if (!wait_warp(bar_full(sv), (ev / kStages) & 1) ||
+                    (mixed && !__all_sync(0xffffffffu, wait_at_least_bounded(&cleaned[sv], ev + 1))) ||
+                    !wait_warp(bar(kBarP + x), npv & 1)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                {
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((sv * kTileBytes) >> 4);
+                    if (leader) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2048) >> 4), idesc_pv, j > first || k > 0);
+                        mma_commit(bar_empty(sv));
+                        mma_commit(bar(kBarPd + x));
+                        if (last) mma_commit(bar(kBarPv + x));
+                    }
+                    __syncwarp();
+                }
+                ++npv;
+            }
+            base += w.jb - w.ja;
+        }
+        if (dead && leader) {
+            report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        // every MMA this warp issued has completed before TMEM is freed
+        if (leader) mma_commit(bar(kBarDrain + x));
+        __syncwarp();
+        if (!wait_warp(bar(kBarDrain + x), 0) && leader) report(a.d_err, KV_DERR_TIMEOUT);
+    } else if (warp == 11) {
+        // ============================================================ cleaning of V tiles
+        int base = 0;
+        bool dead = false;
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (lane == 0) odd_flag[piece % kFlags] = 0;
+            __syncwarp();
+            for (int e = 0; e < 2 * (w.jb - w.ja); ++e) {
+                const int j = w.ja + (e >> 1);
+                const int ev = 2 * base + e, sv = ev % kStages;
+                if (!__all_sync(0xffffffffu, mbar_wait_sleep(bar_full(sv), (ev / kStages) & 1))) {
+                    dead = true;
+                    break;
+                }
+                if (!(e & 1) || !mixed_tile(p, s, j)) {
+                    if (lane == 0) mbar_arrive(bar_empty(sv));
+                    continue;
+                }
+                const uint32_t tile = smem_u32(smem + TL::kOffKV + sv * kTileBytes);
+                const int k0 = j * kBN;
+                bool odd = false;
+                // keys no row sees: [block start, kv_lo) and [L, block end); keys some rows may not
+                // see: [kv_lo, ctx + n - window) of the context, the drafted [ctx, L)
+                auto clean = [&](int lo, int hi, bool zero) {
+                    lo = max(lo, k0) - k0;
+                    hi = min(hi, k0 + kBN) - k0;
+                    for (int i = lo * 8 + lane; i < hi * 8; i += 32) {
+                        for (int hf = 0; hf < TL::kHalves; ++hf) {
+                            const uint32_t at = tile + hf * kHalf + i * 16;
+                            if (zero) {
+                                st_shared_v4(at, make_uint4(0, 0, 0, 0));
+                                continue;
+                            }
+                            uint4 v = ld_shared_v4(at);
+                            uint32_t u[4] = {v.x, v.y, v.z, v.w};
+                            bool bad = false;
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                if (non_finite16<T>(u[e])) u[e] &= 0xffff0000u, bad = true;
+                                if (non_finite16<T>(u[e] >> 16)) u[e] &= 0x0000ffffu, bad = true;
+                            }
+                            if (bad) {
+                                st_shared_v4(at, make_uint4(u[0], u[1], u[2], u[3]));
+                                odd = true;
+                            }
+                        }
+                    }
+                };
+                if (a.window > 0) {
+                    clean(s.kv_lo / bs * bs, s.kv_lo, true);
+                    clean(s.kv_lo, min(s.ctx, s.ctx + s.n - a.window), false);
+                }
+                clean(s.ctx, s.L, false);
+                clean(s.L, (s.L + bs - 1) / bs * bs, true);
+                if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[piece % kFlags] = 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    st_release_cta(&cleaned[sv], ev + 1);
+                    mbar_arrive(bar_empty(sv));
+                }
+                __syncwarp();
+            }
+            base += w.jb - w.ja;
+        }
+        if (dead && lane == 0) {
+            report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    } else {
+        // ============================================================ softmax and results
+        const int x = warp >> 2;                // chain
+        const int r = threadIdx.x & 127;        // query row in the tile = TMEM lane
+        const int tl = r / g, hh = r - tl * g;  // its token in the tile and head in the group
+        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t t_s = trow + x * 128, t_o = trow + kColO + x * 128;
+        const float c2 = a.scale_log2;
+        const float2 cc = make_float2(c2, c2);
+        bool dead = false;
+        // waits are decided for the whole warp: its lanes take the warp-collective TMEM
+        // loads and stores together
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_sleep(b, parity));
+        };
+        int ns = 0, npv = 0, njoin = 0;  // phases taken of S, Pv, Join
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const int t0 = (2 * w.pr + (w.nt == 2 ? x : 0)) * TQ;   // first token of the row tile
+            const int nq = min(TQ, s.n - t0);                       // its tokens (the tile exists)
+            const bool valid = tl < nq;
+            const int64_t token = s.q0 + t0 + (valid ? tl : 0);
+            uint64_t mask = 0;
+            if (valid) mask = a.tree_mask[token] & (s.n >= 64 ? ~0ull : (1ull << s.n) - 1);
+            const int pos = s.ctx - 1 + __popcll(mask);
+            const int klo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            const bool warp_valid = __any_sync(0xffffffffu, valid);
+            float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
+            float2 rsum = make_float2(0.f, 0.f);  // sum of the rounded weights (what the product uses)
+            float2 esum = make_float2(0.f, 0.f);  // sum of the weights (log-sum-exp)
+            const int step = w.nt == 2 ? 1 : 2;
+            const int first = w.ja + (w.nt == 2 ? 0 : x);
+            uint32_t wt[64];
+            // One pass over the tile's S: weights against the reference in use, the tile maximum
+            // tracked alongside, 32 columns at a time with the next load in flight.
+            auto weights = [&](auto masked_tag, int kbase, float nref, float &mraw, float2 &tr, float2 &te) {
+                constexpr bool masked = decltype(masked_tag)::value;
+                const float2 rr = make_float2(nref, nref);
+                uint32_t ra[32], rb[32];
+                auto chunk = [&](const uint32_t (&v)[32], int ch) {
+                    uint32_t seen = 0xffffffffu;
+                    if constexpr (masked) seen = valid ? seen32(kbase + ch * 32, s.ctx, klo, mask) : 0u;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
+                        const float2 e = fma2(make_float2(s0, s1), cc, rr);
+                        float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+                        if constexpr (masked) {
+                            const bool v0 = (seen >> (2 * k)) & 1, v1 = (seen >> (2 * k + 1)) & 1;
+                            e0 = v0 ? e0 : 0.f;
+                            e1 = v1 ? e1 : 0.f;
+                            mraw = fmaxf(mraw, fmaxf(v0 ? s0 : -INFINITY, v1 ? s1 : -INFINITY));
+                        } else {
+                            mraw = fmaxf(mraw, fmaxf(s0, s1));
+                        }
+                        wt[ch * 16 + k] = pack2<T>(e0, e1);
+                        te = add2(te, make_float2(e0, e1));
+                        tr = add2(tr, unpack2<T>(wt[ch * 16 + k]));
+                    }
+                };
+                mraw = -INFINITY;
+                tr = te = make_float2(0.f, 0.f);
+                tmem_ld32_async(t_s, ra);
+                tmem_wait_regs(ra);
+                tmem_ld32_async(t_s + 32, rb);
+                chunk(ra, 0);
+                tmem_wait_regs(rb);
+                tmem_ld32_async(t_s + 64, ra);
+                chunk(rb, 1);
+                tmem_wait_regs(ra);
+                tmem_ld32_async(t_s + 96, rb);
+                chunk(ra, 2);
+                tmem_wait_regs(rb);
+                chunk(rb, 3);
+            };
+            for (int j = first; j < w.jb; j += step) {
+                if (!wait_all(bar(kBarS + x), ns & 1)) {
+                    dead = true;
+                    break;
+                }
+                ++ns;
+                tc_fence_after();
+                if (warp_valid) {  // (a warp without rows leaves its lanes of P as they are)
+                    const int kbase = j * kBN;
+                    const bool masked = mixed_tile(p, s, j);
+                    float mraw;
+                    float2 tr, te;
+                    auto run_weights = [&](float nref, float &mx) {
+                        if (masked) weights(std::true_type{}, kbase, nref, mx, tr, te);
+                        else weights(std::false_type{}, kbase, nref, mx, tr, te);
+                    };
+                    run_weights(m_used == -INFINITY ? 0.f : -m_used, mraw);
+                    // scale >= 0, so the scaled maximum is the maximum of the scaled scores
+                    const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
+                    const bool moved = valid && mt > m_used + kRescaleLog2;  // also the first finite maximum
+                    if (__any_sync(0xffffffffu, moved)) {
+                        const bool rescale = moved && m_used != -INFINITY;  // O and the sums hold earlier tiles
+                        const float f = moved ? fast_exp2(m_used - mt) : 1.f;
+                        if (moved) {
+                            m_used = mt;
+                            rsum.x *= f, rsum.y *= f;
+                            esum.x *= f, esum.y *= f;
+                        }
+                        if (__any_sync(0xffffffffu, rescale)) {
+                            // the warp loads and stores O together; rows that keep their maximum scale by 1
+#pragma unroll 1
+                            for (int ch = 0; ch < D / 32; ++ch) {
+                                float o[32];
+                                tmem_ld32(t_o + ch * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= f;
+                                tmem_st32(t_o + ch * 32, o);
+                            }
+                            tmem_wait_st();
+                        }
+                        float m2;
+                        run_weights(m_used == -INFINITY ? 0.f : -m_used, m2);
+                    }
+                    rsum = add2(rsum, tr);
+                    esum = add2(esum, te);
+                    // P_x into TMEM: 128 keys of 16-bit weights = 64 columns over the S_x just read
+                    tmem_st32u(t_s, wt);
+                    tmem_st32u(t_s + 32, wt + 32);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(bar(kBarP + x));
+            }
+            if (dead) break;
+            if (first < w.jb && !wait_all(bar(kBarPv + x), npv++ & 1)) {  // the last product has landed
+                dead = true;
+                break;
+            }
+            tc_fence_after();
+            float m = m_used, lr = rsum.x + rsum.y, le = esum.x + esum.y;
+            float f0 = 1.f, f1 = 0.f;  // weights of O_0 (O_x with two row tiles) and O_1 in the result
+            bool use1 = false;
+            if (w.nt == 1) {
+                if (x == 1) {
+                    // hand the maximum and sums to chain 0's thread of the same row, which joins the two
+                    join[r] = m;
+                    join[128 + r] = lr;
+                    join[256 + r] = le;
+                    tc_fence_before();
+                    mbar_arrive(bar(kBarJoin));
+                    if (!wait_all(bar(kBarJoined), njoin++ & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    continue;
+                }
+                if (!wait_all(bar(kBarJoin), njoin++ & 1)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                const float m1 = join[r], lr1 = join[128 + r], le1 = join[256 + r];
+                const float mm = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.f : fast_exp2(m - mm);
+                f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
+                use1 = w.jb - w.ja > 1;
+                m = mm;
+                lr = lr * f0 + (f1 != 0.f ? lr1 * f1 : 0.f);
+                le = le * f0 + (f1 != 0.f ? le1 * f1 : 0.f);
+            }
+            const float inv = lr == 0.f ? 0.f : 1.f / lr;
+            f0 *= inv;
+            f1 *= inv;
+            const int64_t row = token * a.num_q_heads + w.h * g + hh;
+            T *out16 = static_cast<T *>(a.out) + row * D;
+            const int64_t part = static_cast<int64_t>(2 * c + (w.ja == s.j0 ? 1 : 0)) * p.rows_per_item +
+                                 (w.nt == 2 ? x * 128 : 0) + r;
+            float *out32 = p.ws_o + part * D;
+            if (warp_valid) {
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float o[32];
+                    tmem_ld32(t_o + ch * 32, o);
+                    tmem_wait_ld();
+                    // a row of weight 0 in a chain has nothing there, whatever O holds
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = f0 != 0.f ? o[k] * f0 : 0.f;
+                    if (use1) {
+                        float o1[32];
+                        tmem_ld32(trow + kColO + 128 + ch * 32, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] += f1 != 0.f ? o1[k] * f1 : 0.f;
+                    }
+                    if (valid) {
+                        if (w.whole) {
+                            uint4 *dst = reinterpret_cast<uint4 *>(out16 + ch * 32);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                dst[k] = make_uint4(pack2<T>(o[8 * k], o[8 * k + 1]), pack2<T>(o[8 * k + 2], o[8 * k + 3]),
+                                                    pack2<T>(o[8 * k + 4], o[8 * k + 5]), pack2<T>(o[8 * k + 6], o[8 * k + 7]));
+                        } else {
+                            float4 *dst = reinterpret_cast<float4 *>(out32 + ch * 32);
+#pragma unroll
+                            for (int k = 0; k < 8; ++k)
+                                dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                        }
+                    }
+                }
+            }
+            if (w.nt == 1) {
+                tc_fence_before();
+                mbar_arrive(bar(kBarJoined));  // O_1 has been read
+            }
+            if (valid) {
+                const float lse2 = le == 0.f ? -INFINITY : m + log2f(le);
+                if (!w.whole) p.ws_lse[part] = lse2;
+                else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
+                if (odd_flag[piece % kFlags]) {
+                    const int ka = w.ja * kBN, kb = min(w.jb * kBN, s.L);
+                    T *o16 = w.whole ? out16 : nullptr;
+                    float *o32 = w.whole ? nullptr : out32;
+                    if (a.window > 0)
+                        add_non_finite<T, D>(a, w.piece_b, w.h, max(ka, s.kv_lo), min(min(s.ctx, s.ctx + s.n - a.window), kb),
+                                             s.ctx, klo, mask, o16, o32);
+                    add_non_finite<T, D>(a, w.piece_b, w.h, max(ka, s.ctx), kb, s.ctx, klo, mask, o16, o32);
+                }
+            }
+        }
+        if (dead) {
+            if (lane == 0) report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// Join the partial results of the item that starts in share c and goes on into the next ones: one
+// warp a row.  out = sum_i w_i o_i / sum_i w_i, w_i = exp2(lse_i - max).
+template <typename T, int D>
+__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int E = D / 32;
+    const TreeArgs &a = p.a;
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int rr = blockIdx.y * 8 + (threadIdx.x >> 5);
+    // the next share's first piece: where it starts decides whether this share's last item goes on
+    const int b = p.ws_first[4 * (c + 1)], idx = p.ws_first[4 * (c + 1) + 1], k = p.ws_first[4 * (c + 1) + 2];
+    if (b < 0 || k == 0) return;
+    if (p.ws_first[4 * c] == b && p.ws_first[4 * c + 1] == idx && p.ws_first[4 * c + 2] > 0) return;  // it started before
+    Seq s;
+    bool rejected;
+    load_seq(p, b, s, &rejected);
+    const int h = idx / s.pairs, pr = idx - h * s.pairs;
+    const int x = rr >> 7, r = rr & 127, tl = r / p.group, TQ = p.tokens_per_tile;
+    const int t = (2 * pr + x) * TQ + tl;
+    if (tl >= TQ || t >= s.n) return;
+    // pieces: share c (its last: slot 2c + 1), then c + 1 .. (their first: slot 2c') while they
+    // start inside the item
+    int last = c + 1;
+    while (last + 1 < p.workers && p.ws_first[4 * (last + 1)] == b && p.ws_first[4 * (last + 1) + 1] == idx &&
+           p.ws_first[4 * (last + 1) + 2] > 0)
+        ++last;
+    auto part = [&](int e) {
+        return static_cast<int64_t>(e == c ? 2 * c + 1 : 2 * e) * p.rows_per_item + rr;
+    };
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int e = c + lane; e <= last; e += 32) {
+        const float l = p.ws_lse[part(e)];
+        nan |= l != l;
+        mx = fmaxf(mx, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    nan = __any_sync(0xffffffffu, nan);
+    float acc[E], wsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (mx != -INFINITY || nan) {
+        for (int base = c; base <= last; base += 32) {
+            const float l = base + lane <= last ? p.ws_lse[part(base + lane)] : -INFINITY;
+            const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
+            const int cnt = min(32, last - base + 1);
+            for (int u0 = 0; u0 < cnt; u0 += 4) {
+                float wu[4], v[4][E];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    wu[u] = u0 + u < cnt ? __shfl_sync(0xffffffffu, wl, (u0 + u) & 31) : 0.f;
+                    const float *src = p.ws_o + part(base + u0 + u) * D + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[u][e] = wu[u] != 0.f ? __ldcg(src + e) : 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    wsum += wu[u];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += wu[u] != 0.f ? wu[u] * v[u][e] : 0.f;
+                }
+            }
+        }
+    }
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    const int64_t row = static_cast<int64_t>(s.q0 + t) * a.num_q_heads + h * p.group + (r - tl * p.group);
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+    if (a.lse_out && lane == 0) a.lse_out[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                         int dev, cudaStream_t stream) {
+    static std::atomic<bool> attr_set[64];
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<T, D>,
+                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    tree_attention_kernel<T, D><<<p.workers, kThreads, Tile<D>::kSmem, stream>>>(tq, tk, tv, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.workers < 2) return e;
+    tree_merge_kernel<T, D><<<dim3(p.workers - 1, p.rows_per_item / 8), 256, 0, stream>>>(p);
     return cudaGetLastError();
 }
 
+size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
+
 }  // namespace
 
-cudaError_t launch_tree_attention(const TreeArgs &a, int head_dim, int q_dtype, cudaStream_t stream) {
-    if (q_dtype == KV_BF16) return launch_typed<__nv_bfloat16>(a, head_dim, stream);
-    return launch_typed<__half>(a, head_dim, stream);
+TreePlan plan_tree(int max_query_len, int group, int head_dim, int num_workers, int sm_count) {
+    TreePlan t;
+    t.workers = num_workers > 0 ? num_workers : sm_count;
+    t.tokens_per_tile = kBM / group;
+    t.rows_per_item = max_query_len > t.tokens_per_tile ? 2 * kBM : kBM;
+    const size_t parts = static_cast<size_t>(2) * t.workers * t.rows_per_item;
+    t.lse_off = align256(16 * static_cast<size_t>(t.workers));
+    t.o_off = t.lse_off + align256(4 * parts);
+    t.workspace_bytes = t.o_off + 4 * parts * head_dim;
+    t.smem_bytes = head_dim == 128 ? Tile<128>::kSmem : Tile<64>::kSmem;
+    return t;
+}
+
+cudaError_t launch_tree_attention(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                  const TreeArgs &a, const TreePlan &plan, void *workspace, int head_dim, int q_dtype,
+                                  int dev, cudaStream_t stream) {
+    TreeParams p;
+    p.a = a;
+    p.group = a.num_q_heads / a.num_kv_heads;
+    p.tokens_per_tile = plan.tokens_per_tile;
+    p.workers = plan.workers;
+    p.rows_per_item = plan.rows_per_item;
+    char *ws = static_cast<char *>(workspace);
+    p.ws_first = reinterpret_cast<int32_t *>(ws);
+    p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_off);
+    p.ws_o = reinterpret_cast<float *>(ws + plan.o_off);
+    if (q_dtype == KV_BF16)
+        return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(tq, tk, tv, p, dev, stream)
+                               : launch_typed<__nv_bfloat16, 64>(tq, tk, tv, p, dev, stream);
+    return head_dim == 128 ? launch_typed<__half, 128>(tq, tk, tv, p, dev, stream)
+                           : launch_typed<__half, 64>(tq, tk, tv, p, dev, stream);
 }
 
 }  // namespace pkv
