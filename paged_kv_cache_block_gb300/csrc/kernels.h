@@ -192,7 +192,7 @@ struct RopeArgs {
     int32_t cache_fp8;
     int64_t total_slots;
     float k_scale, v_scale;
-    int32_t parts;  // warps a token's heads are shared out to (set by the launch)
+    int32_t heads_a_warp, parts;  // heads of a token that one warp takes, warps a token (set by the launch)
     int32_t *d_err;
 };
 

@@ -27,7 +27,7 @@ from __future__ import annotations
 
 import ctypes
 import os
-from typing import NamedTuple, Optional, Tuple
+from typing import Optional, Tuple
 
 import torch
 
@@ -528,42 +528,50 @@ def apply_block_updates(updates: torch.Tensor, block_table: torch.Tensor, zero_i
 
 
 # ---------------------------------------------------------------- a serving step (pagedkv_step.h)
+#
+# These calls are short next to Python, so their checks are written out in plain expressions (a
+# helper call or a message built in advance costs more than the check).
 
-def _want(cond: bool, what: str) -> None:
-    if not cond:
-        raise KVError(KV_ERR_INVALID_ARG, what)
-
-
-def _place(first: torch.Tensor, *others: Optional[torch.Tensor]) -> torch.device:
-    """The CUDA device that holds every given tensor."""
-    dev = first.device
-    _want(dev.type == "cuda" and all(t is None or t.device == dev for t in others),
-          "every tensor must be on one CUDA device")
-    return dev
+_raw_stream = torch._C._cuda_getCurrentRawStream
+_i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
 
 
-def _ints(t: Optional[torch.Tensor], n: Optional[int], what: str, dtype=torch.int32) -> None:
-    _want(t is None or (t.dtype == dtype and t.is_contiguous() and (n is None or t.numel() == n)),
-          f"{what}: a contiguous {dtype} tensor" + ("" if n is None else f" of {n} values"))
+def _refuse(what: str) -> None:
+    raise KVError(KV_ERR_INVALID_ARG, what)
 
 
-def _call(dev: torch.device, stream, fn, *args) -> None:
+def _one_device(dev: int, *tensors: Optional[torch.Tensor]) -> None:
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            _refuse("every tensor must be on one CUDA device")
+
+
+def _call(dev: int, stream, fn, *args) -> None:
     """fn(*args, stream) with the tensors' device current."""
-    _want(stream is None or stream.device == dev, "the stream must be of the tensors' device")
-    s = torch.cuda.current_stream(dev) if stream is None else stream
-    if dev.index == torch.cuda.current_device():
-        _check(fn(*args, s.cuda_stream))
+    if stream is None:
+        raw = _raw_stream(dev)
+    else:
+        if stream.device.index != dev:
+            _refuse("the stream must be of the tensors' device")
+        raw = stream.cuda_stream
+    if dev == torch.cuda.current_device():
+        status = fn(*args, raw)
     else:
         with torch.cuda.device(dev):
-            _check(fn(*args, s.cuda_stream))
+            status = fn(*args, raw)
+    if status:
+        _check(status)
 
 
 def _table_width(t: torch.Tensor, rows: int, max_blocks: Optional[int]) -> int:
-    _want(t.dtype == torch.int32 and t.dim() == 2 and t.shape[0] == rows and
-          (t.stride(1) == 1 or t.shape[1] <= 1 or rows == 0), "block_table: int32 [B, W] with rows in one piece")
-    width = t.shape[1] if max_blocks is None else max_blocks
-    _want(0 <= width <= t.shape[1], "max_blocks_per_seq is past the table's rows")
-    return width
+    if t.dtype is not _i32 or t.dim() != 2 or t.shape[0] != rows or (rows and t.shape[1] > 1 and t.stride(1) != 1):
+        _refuse("block_table: int32 [B, W] with rows in one piece")
+    width = t.shape[1]
+    if max_blocks is None:
+        return width
+    if not 0 <= max_blocks <= width:
+        _refuse("max_blocks_per_seq is past the table's rows")
+    return max_blocks
 
 
 def _table_stride(t: torch.Tensor) -> int:
@@ -571,23 +579,30 @@ def _table_stride(t: torch.Tensor) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]
 
 
-class Batch(NamedTuple):
-    """The metadata of a step (kv_build_batch); tree_mask is None without parents."""
-    query_start_loc: torch.Tensor
-    seq_lens: torch.Tensor
-    positions: torch.Tensor
-    slot_mapping: torch.Tensor
-    held_blocks: torch.Tensor
-    free_next: torch.Tensor
-    tree_mask: Optional[torch.Tensor]
+class Batch:
+    """The metadata of a step, in buffers that kv_build_batch fills (made by batch_buffers or
+    build_batch; the tensors stay as they are made).  tree_mask is None without parents."""
+    FIELDS = ("query_start_loc", "seq_lens", "positions", "slot_mapping", "held_blocks", "free_next", "tree_mask")
+    __slots__ = FIELDS + ("_sizes", "_pointers")
+
+    def __init__(self, num_seqs: int, num_tokens: int, trees: bool, device):
+        def new(n, dtype=_i32):
+            return torch.empty(n, dtype=dtype, device=device)
+        self.query_start_loc, self.seq_lens = new(num_seqs + 1), new(num_seqs)
+        self.positions, self.slot_mapping = new(num_tokens), new(num_tokens, _i64)
+        self.held_blocks, self.free_next = new(num_seqs), new(1)
+        self.tree_mask = new(num_tokens, _i64) if trees else None
+        self._sizes = (num_seqs, num_tokens, trees, self.positions.get_device())
+        self._pointers = (_ptr(self.query_start_loc), _ptr(self.seq_lens), _ptr(self.positions),
+                          _ptr(self.slot_mapping), _ptr(self.tree_mask), _ptr(self.held_blocks), _ptr(self.free_next))
+
+    def _asdict(self) -> dict:
+        return {name: getattr(self, name) for name in self.FIELDS}
 
 
 def batch_buffers(num_seqs: int, num_tokens: int, trees: bool = False, device="cuda") -> Batch:
     """Buffers for build_batch's ``out`` (a loop that chains steps keeps two and swaps them)."""
-    def new(n, dtype=torch.int32):
-        return torch.empty(n, dtype=dtype, device=device)
-    return Batch(new(num_seqs + 1), new(num_seqs), new(num_tokens), new(num_tokens, torch.int64), new(num_seqs),
-                 new(1), new(num_tokens, torch.int64) if trees else None)
+    return Batch(num_seqs, num_tokens, bool(trees), device)
 
 
 def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table: torch.Tensor,
@@ -599,79 +614,96 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     """kv_build_batch: context_lens, new_lens and held_blocks int32 [B]; block_table int32 [B, W],
     updated in place; free_blocks int32 [F]; parents int32 [num_tokens] for drafted trees;
     free_start int32 [1].  The masks are int64 words (bit j = token j of the request's tree)."""
-    B = context_lens.shape[0]
-    dev = _place(context_lens, new_lens, block_table, free_blocks, held_blocks, parents, free_start, d_err)
-    for t, n, what in ((context_lens, B, "context_lens"), (new_lens, B, "new_lens"), (held_blocks, B, "held_blocks"),
-                       (parents, num_tokens, "parents"), (free_blocks, None, "free_blocks"),
-                       (free_start, 1, "free_start"), (d_err, None, "d_err")):
-        _ints(t, n, what)
+    dev = context_lens.get_device()
+    if dev < 0:
+        _refuse("every tensor must be on one CUDA device")
+    _one_device(dev, new_lens, block_table, free_blocks, held_blocks, parents, free_start, d_err)
+    B = context_lens.numel()
+    if context_lens.dtype is not _i32 or not context_lens.is_contiguous():
+        _refuse("context_lens: contiguous int32 [B]")
+    if new_lens.dtype is not _i32 or not new_lens.is_contiguous() or new_lens.numel() != B:
+        _refuse("new_lens: contiguous int32 [B]")
+    if free_blocks.dtype is not _i32 or not free_blocks.is_contiguous():
+        _refuse("free_blocks: contiguous int32")
+    if held_blocks is not None and (held_blocks.dtype is not _i32 or not held_blocks.is_contiguous() or
+                                    held_blocks.numel() != B):
+        _refuse("held_blocks: contiguous int32 [B]")
+    if parents is not None and (parents.dtype is not _i32 or not parents.is_contiguous() or
+                                parents.numel() != num_tokens):
+        _refuse("parents: contiguous int32 [num_tokens]")
+    if free_start is not None and (free_start.dtype is not _i32 or free_start.numel() != 1):
+        _refuse("free_start: int32 [1]")
+    if d_err is not None and (d_err.dtype is not _i32 or d_err.numel() < 1):
+        _refuse("d_err: int32 [1]")
     width = _table_width(block_table, B, max_blocks_per_seq)
     if out is None:
-        out = batch_buffers(B, num_tokens, parents is not None, dev)
-    else:
-        _place(context_lens, *out)
-        for t, n, what in ((out.query_start_loc, B + 1, "query_start_loc"), (out.seq_lens, B, "seq_lens"),
-                           (out.positions, num_tokens, "positions"), (out.held_blocks, B, "held_blocks"),
-                           (out.free_next, 1, "free_next")):
-            _ints(t, n, what)
-        _ints(out.slot_mapping, num_tokens, "slot_mapping", torch.int64)
-        _ints(out.tree_mask, num_tokens, "tree_mask", torch.int64)
-        _want((out.tree_mask is None) == (parents is None), "tree_mask is given exactly when parents are")
+        out = Batch(B, num_tokens, parents is not None, context_lens.device)
+    elif out._sizes != (B, num_tokens, parents is not None, dev):
+        _refuse("out: batch_buffers of these sizes, with trees exactly when parents are given, on this device")
+    qsl, lens, pos, slots, mask, held_out, free_next = out._pointers
     _call(dev, stream, lib.kv_build_batch, _ptr(context_lens), _ptr(new_lens), _ptr(held_blocks), _ptr(parents), B,
-          num_tokens, _ptr(block_table), _table_stride(block_table), width, block_size, num_blocks,
-          _ptr(free_blocks), free_blocks.numel(), _ptr(free_start), _ptr(out.query_start_loc), _ptr(out.seq_lens),
-          _ptr(out.positions), _ptr(out.slot_mapping), _ptr(out.tree_mask), _ptr(out.held_blocks),
-          _ptr(out.free_next), _ptr(d_err))
+          num_tokens, _ptr(block_table), _table_stride(block_table), width, block_size, num_blocks, _ptr(free_blocks),
+          free_blocks.numel(), _ptr(free_start), qsl, lens, pos, slots, mask, held_out, free_next, _ptr(d_err))
     return out
 
 
-def _heads(t: torch.Tensor, T: int, D: int, dtype, what: str) -> None:
-    _want(t.dtype == dtype and t.dim() == 3 and t.shape[0] == T and t.shape[2] == D and
-          (t.numel() == 0 or (t.stride(2) == 1 and (t.stride(1) == D or t.shape[1] == 1))),
-          f"{what}: {dtype} [{T}, heads, {D}] with each token's heads in one piece")
-
-
-def _token_stride(t: torch.Tensor) -> int:
-    # the stride of a single token means nothing; it only has to hold the row
-    return t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] * t.shape[2] // 8) * 8
+def _token_stride(t: torch.Tensor, shape, dtype, what: str) -> int:
+    """The token stride of a [T, heads, D] tensor whose heads lie in one piece (that of a single
+    token means nothing; it only has to hold the row)."""
+    T, H, D = shape
+    if t.dtype is not dtype or t.shape != shape:
+        _refuse(f"{what}: {dtype} [{T}, {H}, {D}]")
+    s0, s1, s2 = t.stride()
+    if T and (s2 != 1 or (s1 != D and H > 1)):
+        _refuse(f"{what}: each token's heads in one piece")
+    return s0 if T > 1 else -(-H * D // 8) * 8
 
 
 def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
                interleaved, k_scale, v_scale, q_out, k_out, d_err, stream):
-    _want(q.dim() == 3 and key.dim() == 3, "q and key: [T, heads, D]")
-    T, Hq, D = q.shape
-    Hkv, dt = key.shape[1], q.dtype
-    dev = _place(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, q_out, k_out,
-                 d_err)
-    _heads(q, T, D, dt, "q")
-    _heads(key, T, D, dt, "key")
-    _heads(q_out, T, D, dt, "q_out")
-    _want(q_out.shape[1] == Hq, "q_out has other heads than q")
-    if k_out is not None:
-        _heads(k_out, T, D, dt, "k_out")
-        _want(k_out.shape[1] == Hkv, "k_out has other heads than key")
-    for w, what in ((q_weight, "q_weight"), (k_weight, "k_weight")):
-        _want(w is None or (w.dtype == dt and w.shape == (D,) and (w.is_contiguous() or D == 1)), f"{what}: {dt} [{D}]")
-    _ints(positions, T, "positions")
-    _ints(d_err, None, "d_err")
-    _want(cos_sin is None or (cos_sin.dtype == torch.float32 and cos_sin.dim() == 2 and cos_sin.is_contiguous()),
-          "cos_sin: contiguous float32 [max_position, rotary_dim]")
-    max_pos, rot = (0, 0) if cos_sin is None else cos_sin.shape
-    cache_dtype, NB, bs, vstride = 0, 0, 1, 0
+    dev, dt = q.get_device(), q.dtype
+    if dev < 0 or q.dim() != 3 or key.dim() != 3:
+        _refuse("q and key: [T, heads, D], and every tensor must be on one CUDA device")
+    _one_device(dev, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, q_out, k_out,
+                d_err)
+    qshape, kshape = q.shape, key.shape
+    T, Hq, D = qshape
+    Hkv = kshape[1]
+    qs = _token_stride(q, qshape, dt, "q")
+    if kshape[0] != T or kshape[2] != D:
+        _refuse("q and key differ in tokens or head size")
+    ks = _token_stride(key, kshape, dt, "key")
+    qos = _token_stride(q_out, qshape, dt, "q_out")
+    kos = 0 if k_out is None else _token_stride(k_out, kshape, dt, "k_out")
+    if (q_weight is not None and (q_weight.dtype is not dt or q_weight.numel() != D or not q_weight.is_contiguous())) or \
+            (k_weight is not None and (k_weight.dtype is not dt or k_weight.numel() != D or not k_weight.is_contiguous())):
+        _refuse(f"weights: contiguous {dt} [{D}]")
+    if positions is not None and (positions.dtype is not _i32 or positions.numel() != T or not positions.is_contiguous()):
+        _refuse("positions: contiguous int32 [T]")
+    if d_err is not None and (d_err.dtype is not _i32 or d_err.numel() < 1):
+        _refuse("d_err: int32 [1]")
+    max_pos = rot = 0
+    if cos_sin is not None:
+        if cos_sin.dtype is not _f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            _refuse("cos_sin: contiguous float32 [max_position, rotary_dim]")
+        max_pos, rot = cos_sin.shape
+    code = dtype_code(dt)
+    cache_code, NB, bs, vs = code, 0, 1, 0
     if slot_mapping is not None:
-        _ints(slot_mapping, T, "slot_mapping", torch.int64)
-        _heads(value, T, D, dt, "value")
-        _want(value.shape[1] == Hkv, "value has other heads than key")
-        _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and tuple(k_cache.shape[2:]) == (Hkv, D) and
-              k_cache.dtype == v_cache.dtype and k_cache.is_contiguous() and v_cache.is_contiguous(),
-              f"caches: two contiguous [blocks, block_size, {Hkv}, {D}] of one type")
-        NB, bs = k_cache.shape[:2]
-        cache_dtype, vstride = dtype_code(k_cache.dtype), _token_stride(value)
-    _call(dev, stream, lib.kv_qk_norm_rope, _ptr(q), _ptr(key), _ptr(value), dtype_code(dt), _token_stride(q),
-          _token_stride(key), vstride, T, Hq, Hkv, D, _ptr(q_weight), _ptr(k_weight), float(eps), _ptr(positions),
-          _ptr(cos_sin), max_pos, rot, int(interleaved), _ptr(q_out), _token_stride(q_out), _ptr(k_out),
-          0 if k_out is None else _token_stride(k_out), _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), cache_dtype,
-          NB, bs, float(k_scale), float(v_scale), _ptr(d_err))
+        if slot_mapping.dtype is not _i64 or slot_mapping.numel() != T or not slot_mapping.is_contiguous():
+            _refuse("slot_mapping: contiguous int64 [T]")
+        vs = _token_stride(value, kshape, dt, "value")
+        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or \
+                not k_cache.is_contiguous() or not v_cache.is_contiguous():
+            _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type")
+        NB, bs, ch, cd = k_cache.shape
+        if ch != Hkv or cd != D:
+            _refuse("caches of other heads than key's")
+        cache_code = code if k_cache.dtype is dt else dtype_code(k_cache.dtype)
+    _call(dev, stream, lib.kv_qk_norm_rope, _ptr(q), _ptr(key), _ptr(value), code, qs, ks, vs, T, Hq, Hkv, D,
+          _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0,
+          _ptr(q_out), qos, _ptr(k_out), kos, _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), cache_code, NB, bs,
+          k_scale, v_scale, _ptr(d_err))
 
 
 def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: Optional[torch.Tensor],
@@ -701,8 +733,8 @@ def qk_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tens
                            stream=None) -> torch.Tensor:
     """kv_qk_norm_rope with the write of the turned keys and of the values into their slots;
     returns the queries (and fills k_out when it is given)."""
-    _want(slot_mapping is not None and value is not None and k_cache is not None and v_cache is not None,
-          "value, slot_mapping and both caches are needed")
+    if slot_mapping is None or value is None or k_cache is None or v_cache is None:
+        _refuse("value, slot_mapping and both caches are needed")
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps, interleaved,
@@ -715,7 +747,7 @@ def paged_attention_tree_workspace_size(num_seqs: int, max_query_len: int, num_q
     n = lib.kv_paged_attention_tree_workspace_size(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim,
                                                    num_workers)
     if n == SIZE_MAX:
-        raise KVError(2, lib.kv_last_error().decode() or "invalid or unsupported sizes")
+        raise KVError(KV_ERR_UNSUPPORTED, lib.kv_last_error().decode() or "invalid or unsupported sizes")
     return int(n)
 
 
@@ -727,32 +759,45 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
                          max_blocks_per_seq: Optional[int] = None, stream=None) -> torch.Tensor:
     """kv_paged_attention_tree: q [T, Hq, D] (the drafted tokens of sequence b are rows
     query_start_loc[b] .. query_start_loc[b+1]-1); caches [NB, bs, Hkv, D]; block_table int32 [B, W];
-    seq_lens int32 [B] (including the drafted tokens); tree_mask int64 [T]."""
-    _want(q.dim() == 3 and q.is_contiguous(), "q: contiguous [T, heads, D]")
+    seq_lens int32 [B] (including the drafted tokens); tree_mask int64 [T].  A workspace that is
+    given must hold paged_attention_tree_workspace_size(...) bytes."""
+    dev, dt = q.get_device(), q.dtype
+    if dev < 0 or q.dim() != 3 or not q.is_contiguous():
+        _refuse("q: contiguous [T, heads, D], and every tensor must be on one CUDA device")
+    _one_device(dev, k_cache, v_cache, block_table, seq_lens, query_start_loc, tree_mask, workspace, out, lse_out, d_err)
     T, Hq, D = q.shape
-    B = seq_lens.shape[0]
-    dev = _place(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, tree_mask, workspace, out, lse_out, d_err)
-    _want(k_cache.dim() == 4 and k_cache.shape == v_cache.shape and k_cache.shape[3] == D and
-          k_cache.dtype == v_cache.dtype and k_cache.is_contiguous() and v_cache.is_contiguous(),
-          f"caches: two contiguous [blocks, block_size, heads, {D}] of one type")
-    NB, bs, Hkv, _ = k_cache.shape
-    _ints(seq_lens, B, "seq_lens")
-    _ints(query_start_loc, B + 1, "query_start_loc")
-    _ints(tree_mask, T, "tree_mask", torch.int64)
-    _ints(d_err, None, "d_err")
+    B = seq_lens.numel()
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or \
+            not k_cache.is_contiguous() or not v_cache.is_contiguous():
+        _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type")
+    NB, bs, Hkv, cd = k_cache.shape
+    if cd != D:
+        _refuse("caches of another head size than q's")
+    if seq_lens.dtype is not _i32 or not seq_lens.is_contiguous():
+        _refuse("seq_lens: contiguous int32 [B]")
+    if query_start_loc.dtype is not _i32 or not query_start_loc.is_contiguous() or query_start_loc.numel() != B + 1:
+        _refuse("query_start_loc: contiguous int32 [B + 1]")
+    if tree_mask.dtype is not _i64 or not tree_mask.is_contiguous() or tree_mask.numel() != T:
+        _refuse("tree_mask: contiguous int64 [T]")
+    if d_err is not None and (d_err.dtype is not _i32 or d_err.numel() < 1):
+        _refuse("d_err: int32 [1]")
     width = _table_width(block_table, B, max_blocks_per_seq)
-    _want(out is None or (out.shape == q.shape and out.dtype == q.dtype and out.is_contiguous()), "out: like q")
-    _want(workspace is None or workspace.is_contiguous(), "workspace: contiguous")
-    _want(lse_out is None or (lse_out.dtype == torch.float32 and tuple(lse_out.shape) == (T, Hq) and
-                              lse_out.is_contiguous()), f"lse_out: contiguous float32 [{T}, {Hq}]")
     if out is None:
         out = torch.empty_like(q)
-    need = paged_attention_tree_workspace_size(B, max_query_len, Hq, Hkv, D, num_workers)
-    if need and (workspace is None or workspace.numel() * workspace.element_size() < need):
-        workspace = torch.empty(need, dtype=torch.uint8, device=dev)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _call(dev, stream, lib.kv_paged_attention_tree, _ptr(q), dtype_code(q.dtype), _ptr(query_start_loc), B, T,
-          max_query_len, Hq, _ptr(k_cache), _ptr(v_cache), dtype_code(k_cache.dtype), Hkv, D, bs, NB,
-          _ptr(block_table), _table_stride(block_table), width, _ptr(seq_lens), max_seq_len, float(scale),
-          window, _ptr(tree_mask), num_workers, _ptr(workspace), ws_bytes, _ptr(out), _ptr(lse_out), _ptr(d_err))
+    elif out.shape != q.shape or out.dtype is not dt or not out.is_contiguous():
+        _refuse("out: like q")
+    if lse_out is not None and (lse_out.dtype is not _f32 or lse_out.shape != (T, Hq) or not lse_out.is_contiguous()):
+        _refuse("lse_out: contiguous float32 [T, heads]")
+    if workspace is None:
+        with torch.cuda.device(dev):
+            need = paged_attention_tree_workspace_size(B, max_query_len, Hq, Hkv, D, num_workers)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous():
+        _refuse("workspace: contiguous")
+    code = dtype_code(dt)
+    _call(dev, stream, lib.kv_paged_attention_tree, _ptr(q), code, _ptr(query_start_loc), B, T, max_query_len, Hq,
+          _ptr(k_cache), _ptr(v_cache), code if k_cache.dtype is dt else dtype_code(k_cache.dtype), Hkv, D, bs, NB,
+          _ptr(block_table), _table_stride(block_table), width, _ptr(seq_lens), max_seq_len, scale, window,
+          _ptr(tree_mask), num_workers, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
+          _ptr(lse_out), _ptr(d_err))
     return out
