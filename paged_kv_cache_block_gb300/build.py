@@ -22,8 +22,9 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libpagedkv.so")
 SOURCES = ["api.cu", "slot_mapping.cu", "reshape_and_cache.cu", "paged_attention.cu", "noalloc.cu",
            "block_updates.cu", "block_manager.cpp", "prefill_attention.cu", "paged_decode_int4.cu",
-           "selftest.cu", "paged_attention_fp8.cu", "build_batch.cu", "qk_norm_rope.cu", "tree_attention.cu"]
-HEADERS = ["common.cuh", "tcgen05.cuh", "decode_common.cuh", "paged_decode_kernel.cuh", "kernels.h"]
+           "selftest.cu", "paged_attention_fp8.cu", "build_batch.cu", "qk_norm_rope.cu", "tree_attention.cu",
+           "tree_packed.cu"]
+HEADERS = ["common.cuh", "tcgen05.cuh", "tree_common.cuh", "decode_common.cuh", "paged_decode_kernel.cuh", "kernels.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]

@@ -298,6 +298,26 @@ kv_status encode_query_map(CUtensorMap *m, const void *base, int32_t num_tokens,
     return KV_OK;
 }
 
+// A 16-bit cache viewed as (dim, token of 8, head, group of 8 tokens, block); one box = one block's rows
+// for a group of heads, 64 dims, swizzled 128B, laid out as [group of 8 tokens][head][token][dim]: the
+// 8-row swizzle atoms of one head then lie a constant distance apart over any number of blocks.
+kv_status encode_heads_map(CUtensorMap *m, const void *base, int32_t num_blocks, int32_t block_size,
+                           int32_t num_kv_heads, int32_t head_dim, int32_t heads) {
+    auto fn = encode_fn();
+    if (!fn) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
+    const uint64_t head = 2ull * head_dim, token = head * num_kv_heads;
+    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(head_dim), 8, static_cast<cuuint64_t>(num_kv_heads),
+                                static_cast<cuuint64_t>(block_size / 8), static_cast<cuuint64_t>(num_blocks)};
+    const cuuint64_t strides[4] = {token, head, 8 * token, token * block_size};
+    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(block_size / 8), 1};
+    const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
+    CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void *>(base), dims, strides, box, estr,
+                    CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                    CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (r != CUDA_SUCCESS) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled (heads) failed (CUresult %d)", (int)r);
+    return KV_OK;
+}
+
 kv_status cuda_fail(cudaError_t e, const char *what) {
     return fail(KV_ERR_CUDA, "%s: %s", what, cudaGetErrorString(e));
 }
@@ -1127,7 +1147,7 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
     a.total_slots = write ? static_cast<int64_t>(num_blocks) * block_size : 0;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    a.heads_a_warp = a.parts = 0;
+    a.heads_a_warp = a.parts = a.q_parts = a.kv_parts = 0;
     a.d_err = d_err;
     e = pkv::launch_qk_norm_rope(a, dtype, info.sm_count, s);
     if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
@@ -1164,7 +1184,7 @@ size_t kv_paged_attention_tree_workspace_size(int32_t num_seqs, int32_t max_quer
         return SIZE_MAX;
     }
     ok();
-    return pkv::plan_tree(max_query_len, num_q_heads / num_kv_heads, head_dim, num_workers, info.sm_count).workspace_bytes;
+    return pkv::plan_tree(max_query_len, num_q_heads / num_kv_heads, num_kv_heads, head_dim, num_workers, info.sm_count).workspace_bytes;
 }
 
 kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs,
@@ -1204,7 +1224,7 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     DeviceInfo info;
     if ((e = device_info(dev, &info)) != cudaSuccess) return cuda_fail(e, "device attributes");
     const int32_t g = num_q_heads / num_kv_heads;
-    const pkv::TreePlan plan = pkv::plan_tree(max_query_len, g, head_dim, num_workers, info.sm_count);
+    const pkv::TreePlan plan = pkv::plan_tree(max_query_len, g, num_kv_heads, head_dim, num_workers, info.sm_count);
     if (static_cast<size_t>(info.smem_optin) < plan.smem_bytes)
         return fail(KV_ERR_UNSUPPORTED, "tree attention: needs %zu bytes of shared memory per block, the device has %d",
                     plan.smem_bytes, info.smem_optin);
@@ -1214,8 +1234,13 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     if (!aligned(workspace, 256)) return fail(KV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
     CUtensorMap tq, tk, tv;
     st = encode_query_map(&tq, q, num_tokens, num_q_heads, head_dim, g, plan.tokens_per_tile);
-    if (st == KV_OK) st = encode_cache_map(&tk, k_cache, cache_dtype, num_blocks, block_size, num_kv_heads, head_dim, 1);
-    if (st == KV_OK) st = encode_cache_map(&tv, v_cache, cache_dtype, num_blocks, block_size, num_kv_heads, head_dim, 1);
+    for (int i = 0; i < 2 && st == KV_OK; ++i) {
+        CUtensorMap *m = i ? &tv : &tk;
+        const void *cache = i ? v_cache : k_cache;
+        st = plan.heads_per_item > 1
+                 ? encode_heads_map(m, cache, num_blocks, block_size, num_kv_heads, head_dim, plan.heads_per_item)
+                 : encode_cache_map(m, cache, cache_dtype, num_blocks, block_size, num_kv_heads, head_dim, 1);
+    }
     if (st != KV_OK) return st;
     pkv::TreeArgs a;
     a.q = q;

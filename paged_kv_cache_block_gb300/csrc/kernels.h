@@ -192,7 +192,8 @@ struct RopeArgs {
     int32_t cache_fp8;
     int64_t total_slots;
     float k_scale, v_scale;
-    int32_t heads_a_warp, parts;  // heads of a token that one warp takes, warps a token (set by the launch)
+    // set by the launch: heads of a token that one warp takes; warps a token, for q, for key (and value)
+    int32_t heads_a_warp, parts, q_parts, kv_parts;
     int32_t *d_err;
 };
 
@@ -216,12 +217,14 @@ struct TreeArgs {
 
 // Launch geometry and workspace layout of the tree kernels.
 struct TreePlan {
+    int heads_per_item;   // kv heads side by side in an item's 128 rows (1, 2 or 4)
     int workers;          // CTAs, each with one share of the key tiles
-    int tokens_per_tile;  // drafted tokens of a 128-row tile
-    int rows_per_item;    // rows of a partial result (128: every tree fits one row tile, else 256)
+    int tokens_per_tile;  // drafted tokens of one kv head in a row tile
+    int key_shift;        // log2 of the keys of a key tile
+    int rows_per_item;    // rows of a partial result
     size_t lse_off, o_off, workspace_bytes, smem_bytes;
 };
-TreePlan plan_tree(int max_query_len, int group, int head_dim, int num_workers, int sm_count);
+TreePlan plan_tree(int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count);
 
 cudaError_t launch_tree_attention(const CUtensorMap &tmap_q, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                   const TreeArgs &a, const TreePlan &plan, void *workspace, int head_dim, int q_dtype,

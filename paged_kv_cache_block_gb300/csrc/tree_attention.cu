@@ -29,27 +29,15 @@
 // Weights are taken against the reference maximum in use; only when a row's maximum exceeds it by
 // more than 2^8 are its O and sums rescaled.  Every wait is bounded (2 s): on expiry
 // KV_DERR_TIMEOUT is set, what was issued is drained, TMEM is freed and the CTA returns.
-#include <atomic>
-#include <type_traits>
-
-#include "common.cuh"
-#include "kernels.h"
-#include "tcgen05.cuh"
+#include "tree_common.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kBM = 128;           // query rows of a row tile = TMEM lanes
+constexpr int kBM = kTreeRows;
 constexpr int kBN = 128;           // keys of a key tile
-constexpr int kHalf = 128 * 128;   // 128 rows x 64 16-bit elements (one swizzle column)
 constexpr int kThreads = 384;
-constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColO = 256;
-constexpr float kRescaleLog2 = 8.0f;
-constexpr int kItemCost = 2;       // an item's fixed cost in key tiles
-constexpr int kMinShare = 4;       // least cost of a share: more than kItemCost, so that it holds a tile
-
-constexpr int kFlags = 8;
 
 template <int D> struct Tile {
     static constexpr int kHalves = D / 64;
@@ -71,148 +59,9 @@ template <int D> struct Tile {
 enum { kBarQFull = 0, kBarQEmpty = 1, kBarS = 2, kBarP = 4, kBarPv = 6, kBarPd = 8, kBarJoin = 10,
        kBarJoined = 11, kBarDrain = 12, kBarKv = 14 };  // then KvFull[stages], KvEmpty[stages]
 
-struct TreeParams {
-    TreeArgs a;
-    int group, tokens_per_tile;
-    int workers;       // shares at most
-    int rows_per_item; // 128 or 256: rows of a partial result
-    int32_t *ws_first; // [workers][4] first piece of each share: sequence, item of it, key tile, -
-    float *ws_lse;     // [2 * workers][rows_per_item] log2-sum-exp2 of the partial results
-    float *ws_o;       // [2 * workers][rows_per_item][D] partial results, normalised
-};
-
-// A sequence's part of the work list.
-struct Seq {
-    int q0, n, L, ctx, kv_lo;  // first row, rows, length, context, first key any row sees
-    int j0, tiles;             // key tiles j0 .. j0 + tiles - 1 (128 keys each)
-    int pairs;                 // items a kv head (two row tiles each)
-};
-
-// The sequence's lengths; false when it has no rows, or is rejected (*rejected).
-__device__ __forceinline__ bool load_seq(const TreeParams &p, int b, Seq &s, bool *rejected) {
-    const TreeArgs &a = p.a;
-    s.q0 = a.query_start_loc[b];
-    s.n = a.query_start_loc[b + 1] - s.q0;
-    s.L = a.seq_lens[b];
-    const int bs = a.block_size;
-    *rejected = s.n > 0 && !(s.n <= a.max_query_len && s.q0 >= 0 && s.q0 <= a.num_tokens - s.n && s.L >= s.n &&
-                             s.L <= a.max_seq_len && (s.L - 1) / bs < a.max_blocks_per_seq);
-    if (s.n <= 0 || *rejected) return false;
-    s.ctx = s.L - s.n;
-    s.kv_lo = a.window > 0 ? max(0, s.ctx - a.window) : 0;
-    s.j0 = s.kv_lo / kBN;
-    s.tiles = (s.L - 1) / kBN + 1 - s.j0;
-    const int row_tiles = (s.n + p.tokens_per_tile - 1) / p.tokens_per_tile;
-    s.pairs = (row_tiles + 1) >> 1;
-    return true;
-}
-
-__device__ __forceinline__ int64_t seq_cost(const TreeParams &p, int b) {
-    Seq s;
-    bool rejected;
-    if (!load_seq(p, b, s, &rejected)) return 0;
-    return static_cast<int64_t>(s.tiles + kItemCost) * s.pairs * p.a.num_kv_heads;
-}
-
-// The pieces of a share, in order: (item, key tiles ja .. jb - 1).  Every warp walks the same ones.
-struct Walk {
-    int b, idx;       // sequence, item of it (kv head * pairs + pair)
-    int64_t at;       // cost where the item starts
-    int64_t x0, x1;   // the share
-    Seq s;
-    int ja, jb;       // key tiles of the piece (absolute)
-    int h, pr, nt;    // kv head, pair, row tiles of the item (1 or 2)
-
-    __device__ __forceinline__ void start(const TreeParams &p, int b_, int idx_, int64_t at_, int64_t x0_, int64_t x1_) {
-        b = b_, idx = idx_, at = at_, x0 = x0_, x1 = x1_;
-        bool rejected;
-        load_seq(p, b, s, &rejected);
-    }
-    __device__ __forceinline__ bool next(const TreeParams &p) {
-        while (at < x1) {
-            const int64_t first = at + kItemCost;
-            ja = static_cast<int>(max(int64_t(0), x0 - first));
-            jb = static_cast<int>(min(static_cast<int64_t>(s.tiles), x1 - first));
-            const bool some = ja < jb;
-            if (some) {
-                h = idx / s.pairs;
-                pr = idx - h * s.pairs;
-                nt = s.n > (2 * pr + 1) * p.tokens_per_tile ? 2 : 1;
-                ja += s.j0;
-                jb += s.j0;
-                whole = ja == s.j0 && jb == s.j0 + s.tiles;
-                piece_b = b;
-                cur = s;
-            }
-            at = first + s.tiles;
-            if (++idx == s.pairs * p.a.num_kv_heads) {
-                idx = 0;
-                bool rejected = false;
-                while (++b < p.a.num_seqs && !load_seq(p, b, s, &rejected)) {}
-                if (b >= p.a.num_seqs) x1 = at;  // the end of the list
-            }
-            if (some) return true;
-        }
-        return false;
-    }
-    bool whole;       // the piece is its whole item
-    int piece_b;      // the piece's sequence
-    Seq cur;          // and its lengths
-};
-
-// Whether key tile j holds a key that not every row of the sequence sees.
-__device__ __forceinline__ bool mixed_tile(const TreeParams &p, const Seq &s, int j) {
-    const int k0 = j * kBN;
-    return k0 + kBN > s.ctx || (p.a.window > 0 && k0 < s.ctx + s.n - p.a.window);
-}
-
-// The keys k0 .. k0 + 31 a row sees (bit i: key k0 + i): context keys from klo, drafted keys of
-// the mask word.
-__device__ __forceinline__ uint32_t seen32(int k0, int ctx, int klo, uint64_t mask) {
-    const int lo = max(klo - k0, 0), hi = min(ctx - k0, 32);
-    uint32_t v = 0;
-    if (lo < hi) v = (hi == 32 ? 0xffffffffu : (1u << hi) - 1) & ~((1u << lo) - 1);  // lo < 32
-    const int d = k0 - ctx;
-    if (d >= 0) v |= d < 64 ? static_cast<uint32_t>(mask >> d) : 0u;
-    else if (d > -32) v |= static_cast<uint32_t>(mask << -d);
-    return v;
-}
-
-template <typename T> struct NonFinite;  // exponent bits all ones
-template <> struct NonFinite<__half> { static constexpr uint32_t mask = 0x7C00u; };
-template <> struct NonFinite<__nv_bfloat16> { static constexpr uint32_t mask = 0x7F80u; };
-
-template <typename T> __device__ __forceinline__ bool non_finite16(uint32_t bits) {
-    return (bits & NonFinite<T>::mask) == NonFinite<T>::mask;
-}
-
-__device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
-    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
-}
-__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
-    uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
-    return v;
-}
-
-// Add the non-finite values of V that a row sees among the keys [k0, k1) to its written result
-// (out16 of type T, or a float row): they were zeroed for the products.  Rare, so plain.
-template <typename T, int D>
-__device__ __noinline__ void add_non_finite(const TreeArgs &a, int b, int h, int k0, int k1, int ctx, int klo,
-                                            uint64_t mask, T *out16, float *out32) {
-    for (int k = k0; k < k1; ++k) {
-        const bool sees = k < ctx ? k >= klo : (mask >> (k - ctx)) & 1;
-        const int id = a.block_table[b * a.bt_stride + k / a.block_size];
-        if (!sees || id < 0 || id >= a.num_blocks) continue;
-        const T *v = static_cast<const T *>(a.v_cache) +
-                     ((static_cast<int64_t>(id) * a.block_size + k % a.block_size) * a.num_kv_heads + h) * D;
-        for (int d = 0; d < D; ++d) {
-            const float f = to_float<T>(v[d]);
-            if (isfinite(f)) continue;
-            if (out32) out32[d] += f;
-            else out16[d] = from_float<T>(to_float<T>(out16[d]) + f);
-        }
-    }
+// Row tiles of pair pr: 2, or 1 when the tree ends in its first.
+__device__ __forceinline__ int row_tiles(const TreeParams &p, const Seq &s, int pr) {
+    return s.n > (2 * pr + 1) * p.tokens_per_tile ? 2 : 1;
 }
 
 template <typename T, int D>
@@ -238,64 +87,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     auto bar_full = [&](int s) { return smem_u32(&bars[kBarKv + s]); };
     auto bar_empty = [&](int s) { return smem_u32(&bars[kBarKv + kStages + s]); };
 
-    // ---- the share: costs of the sequences summed over the block, then the sequence, item and
-    // cost where it starts
-    __shared__ int64_t warp_sum[kThreads / 32];
-    __shared__ int64_t start_at;
-    __shared__ int start_b, start_idx;
-    const int per = (a.num_seqs + kThreads - 1) / kThreads;
-    const int b_lo = min(a.num_seqs, static_cast<int>(threadIdx.x) * per), b_hi = min(a.num_seqs, b_lo + per);
-    int64_t sum = 0;
-    for (int b = b_lo; b < b_hi; ++b) sum += seq_cost(p, b);
-    int64_t incl = sum;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
-    }
-    if (lane == 31) warp_sum[warp] = incl;
-    __syncthreads();
-    int64_t before = incl - sum, total = 0;
-#pragma unroll
-    for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
-    }
-    const int64_t most = max(int64_t(1), total / kMinShare);
-    const int shares = total == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(p.workers), most));
-    const int64_t x0 = c < shares ? total * c / shares : 0, x1 = c < shares ? total * (c + 1) / shares : 0;
-    if (c < shares && x0 >= before && x0 < before + sum) {  // one thread
-        int64_t at = before;
-        for (int b = b_lo; b < b_hi; ++b) {
-            const int64_t cost = seq_cost(p, b);
-            if (x0 < at + cost) {
-                Seq s;
-                bool rejected;
-                load_seq(p, b, s, &rejected);
-                const int idx = static_cast<int>((x0 - at) / (s.tiles + kItemCost));
-                start_b = b;
-                start_idx = idx;
-                start_at = at + static_cast<int64_t>(idx) * (s.tiles + kItemCost);
-                break;
-            }
-            at += cost;
-        }
-    }
-    // rows of rejected sequences are 0 (lse -inf)
-    for (int b = c; b < a.num_seqs; b += gridDim.x) {
-        Seq s;
-        bool rejected;
-        load_seq(p, b, s, &rejected);
-        if (!rejected) continue;
-        if (threadIdx.x == 0) report(a.d_err, KV_DERR_BAD_LEN);
-        const int64_t r0 = max(s.q0, 0), r1 = min(static_cast<int64_t>(s.q0) + s.n, static_cast<int64_t>(a.num_tokens));
-        const int64_t rows = (r1 - r0) * a.num_q_heads;
-        for (int64_t i = threadIdx.x; i < rows * (D / 8); i += kThreads)
-            reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + r0 * a.num_q_heads * D)[i] = make_uint4(0, 0, 0, 0);
-        if (a.lse_out)
-            for (int64_t i = threadIdx.x; i < rows; i += kThreads) a.lse_out[r0 * a.num_q_heads + i] = -INFINITY;
-    }
-    if (c >= shares) {
+    __shared__ ShareStart start;
+    int64_t x0, x1;
+    share_of_cta<kThreads>(p, c, x0, x1, start);
+    zero_rejected<T, D>(p);
+    if (x0 == x1) {
         if (threadIdx.x == 0) p.ws_first[4 * c] = -1;
         return;
     }
@@ -331,7 +127,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     Walk w;
-    w.start(p, start_b, start_idx, start_at, x0, x1);
+    w.start(p, start, x0, x1);
 
     if (warp == 8) {
         // ============================================================ TMA producer
@@ -347,9 +143,10 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         bool stop = false;
         while (!stop && w.next(p)) {
             const Seq s = w.cur;
+            const int h = w.item / s.pairs, pr = w.item - h * s.pairs, nt = row_tiles(p, s, pr);
             if (piece == 0 && lane == 0) {
-                p.ws_first[4 * c] = w.piece_b;
-                p.ws_first[4 * c + 1] = w.h * s.pairs + w.pr;
+                p.ws_first[4 * c] = w.seq;
+                p.ws_first[4 * c + 1] = w.item;
                 p.ws_first[4 * c + 2] = w.ja - s.j0;
             }
             // block ids of key tile j: lane l holds block j * bpt + l
@@ -358,7 +155,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 const int lb = j * bpt + lane;
                 int id = a.num_blocks;  // one past the pool: the copy reads zeros
                 if (lane < bpt && lb >= first_blk && lb < nblk) {
-                    const int e = a.block_table[static_cast<int64_t>(w.piece_b) * a.bt_stride + lb];
+                    const int e = a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + lb];
                     if (e >= 0 && e < a.num_blocks) id = e;
                     else report(a.d_err, KV_DERR_BAD_BLOCK);
                 }
@@ -370,11 +167,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 // Q of the item, once the piece before has formed its last scores
                 if (piece > 0) ok = mbar_wait_sleep(bar(kBarQEmpty), (piece - 1) & 1);
                 if (ok) {
-                    mbar_arrive_expect_tx(bar(kBarQFull), w.nt * q_bytes);
-                    for (int x = 0; x < w.nt; ++x)
+                    mbar_arrive_expect_tx(bar(kBarQFull), nt * q_bytes);
+                    for (int x = 0; x < nt; ++x)
                         for (int hf = 0; hf < TL::kHalves; ++hf)
                             tma_load_3d(smem_u32(smem + x * kTileBytes + hf * kHalf), &tmap_q, bar(kBarQFull), 64 * hf,
-                                        w.h * g, s.q0 + (2 * w.pr + x) * TQ);
+                                        h * g, s.q0 + (2 * pr + x) * TQ);
                 }
             }
             if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
@@ -412,7 +209,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                         if (lane == 0)
                             for (int hf = 0; hf < TL::kHalves; ++hf)
                                 tma_load_4d(smem_u32(dst + hf * kHalf + jb * bs * 128), m, bar_full(slot), 64 * hf, 0,
-                                            w.h, id);
+                                            h, id);
                     }
                     ++entry;
                 }
@@ -447,20 +244,21 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         bool dead = false;
         for (int piece = 0; !dead && w.next(p); ++piece) {
             const Seq s = w.cur;
+            const int nt = row_tiles(p, s, w.item % s.pairs);
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             if (!wait_warp(bar(kBarQFull), piece & 1)) {
                 dead = true;
                 break;
             }
-            const uint64_t dq = smem_desc(smem_u32(smem + (w.nt == 2 ? x * kTileBytes : 0)), 16, 1024);
-            const int step = w.nt == 2 ? 1 : 2;
-            const int first = w.ja + (w.nt == 2 ? 0 : x);
+            const uint64_t dq = smem_desc(smem_u32(smem + (nt == 2 ? x * kTileBytes : 0)), 16, 1024);
+            const int step = nt == 2 ? 1 : 2;
+            const int first = w.ja + (nt == 2 ? 0 : x);
             if (first >= w.jb && leader) mbar_arrive(bar(kBarQEmpty));  // no tile for this chain
             for (int j = w.ja; j < w.jb; ++j) {
                 const bool last = j + step >= w.jb;
                 const int ek = 2 * (base + j - w.ja), ev = ek + 1;
                 const int sk = ek % kStages, sv = ev % kStages;
-                if (w.nt == 1 && ((j - w.ja) & 1) != x) {
+                if (nt == 1 && ((j - w.ja) & 1) != x) {
                     bool landed = wait_warp(bar_full(sk), (ek / kStages) & 1);
                     if (landed && leader) mbar_arrive(bar_empty(sk));
                     landed = landed && wait_warp(bar_full(sv), (ev / kStages) & 1);
@@ -552,27 +350,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 auto clean = [&](int lo, int hi, bool zero) {
                     lo = max(lo, k0) - k0;
                     hi = min(hi, k0 + kBN) - k0;
-                    for (int i = lo * 8 + lane; i < hi * 8; i += 32) {
-                        for (int hf = 0; hf < TL::kHalves; ++hf) {
-                            const uint32_t at = tile + hf * kHalf + i * 16;
-                            if (zero) {
-                                st_shared_v4(at, make_uint4(0, 0, 0, 0));
-                                continue;
-                            }
-                            uint4 v = ld_shared_v4(at);
-                            uint32_t u[4] = {v.x, v.y, v.z, v.w};
-                            bool bad = false;
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                if (non_finite16<T>(u[e])) u[e] &= 0xffff0000u, bad = true;
-                                if (non_finite16<T>(u[e] >> 16)) u[e] &= 0x0000ffffu, bad = true;
-                            }
-                            if (bad) {
-                                st_shared_v4(at, make_uint4(u[0], u[1], u[2], u[3]));
-                                odd = true;
-                            }
-                        }
-                    }
+                    for (int i = lo * 8 + lane; i < hi * 8; i += 32)
+                        for (int hf = 0; hf < TL::kHalves; ++hf) clean_chunk<T>(tile + hf * kHalf + i * 16, zero, odd);
                 };
                 if (a.window > 0) {
                     clean(s.kv_lo / bs * bs, s.kv_lo, true);
@@ -614,7 +393,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         for (int piece = 0; !dead && w.next(p); ++piece) {
             const Seq s = w.cur;
             if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-            const int t0 = (2 * w.pr + (w.nt == 2 ? x : 0)) * TQ;   // first token of the row tile
+            const int h = w.item / s.pairs, pr = w.item - h * s.pairs, nt = row_tiles(p, s, pr);
+            const int t0 = (2 * pr + (nt == 2 ? x : 0)) * TQ;       // first token of the row tile
             const int nq = min(TQ, s.n - t0);                       // its tokens (the tile exists)
             const bool valid = tl < nq;
             const int64_t token = s.q0 + t0 + (valid ? tl : 0);
@@ -626,8 +406,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
             float2 rsum = make_float2(0.f, 0.f);  // sum of the rounded weights (what the product uses)
             float2 esum = make_float2(0.f, 0.f);  // sum of the weights (log-sum-exp)
-            const int step = w.nt == 2 ? 1 : 2;
-            const int first = w.ja + (w.nt == 2 ? 0 : x);
+            const int step = nt == 2 ? 1 : 2;
+            const int first = w.ja + (nt == 2 ? 0 : x);
             uint32_t wt[64];
             // One pass over the tile's S: weights against the reference in use, the tile maximum
             // tracked alongside, 32 columns at a time with the next load in flight.
@@ -734,7 +514,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             float m = m_used, lr = rsum.x + rsum.y, le = esum.x + esum.y;
             float f0 = 1.f, f1 = 0.f;  // weights of O_0 (O_x with two row tiles) and O_1 in the result
             bool use1 = false;
-            if (w.nt == 1) {
+            if (nt == 1) {
                 if (x == 1) {
                     // hand the maximum and sums to chain 0's thread of the same row, which joins the two
                     join[r] = m;
@@ -766,10 +546,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             const float inv = lr == 0.f ? 0.f : 1.f / lr;
             f0 *= inv;
             f1 *= inv;
-            const int64_t row = token * a.num_q_heads + w.h * g + hh;
+            const int64_t row = token * a.num_q_heads + h * g + hh;
             T *out16 = static_cast<T *>(a.out) + row * D;
-            const int64_t part = static_cast<int64_t>(2 * c + (w.ja == s.j0 ? 1 : 0)) * p.rows_per_item +
-                                 (w.nt == 2 ? x * 128 : 0) + r;
+            const int64_t part = part_row(p, c, w.ja == s.j0, (nt == 2 ? x * 128 : 0) + r);
             float *out32 = p.ws_o + part * D;
             if (warp_valid) {
 #pragma unroll 1
@@ -803,7 +582,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     }
                 }
             }
-            if (w.nt == 1) {
+            if (nt == 1) {
                 tc_fence_before();
                 mbar_arrive(bar(kBarJoined));  // O_1 has been read
             }
@@ -811,15 +590,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 const float lse2 = le == 0.f ? -INFINITY : m + log2f(le);
                 if (!w.whole) p.ws_lse[part] = lse2;
                 else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
-                if (odd_flag[piece % kFlags]) {
-                    const int ka = w.ja * kBN, kb = min(w.jb * kBN, s.L);
-                    T *o16 = w.whole ? out16 : nullptr;
-                    float *o32 = w.whole ? nullptr : out32;
-                    if (a.window > 0)
-                        add_non_finite<T, D>(a, w.piece_b, w.h, max(ka, s.kv_lo), min(min(s.ctx, s.ctx + s.n - a.window), kb),
-                                             s.ctx, klo, mask, o16, o32);
-                    add_non_finite<T, D>(a, w.piece_b, w.h, max(ka, s.ctx), kb, s.ctx, klo, mask, o16, o32);
-                }
+                if (odd_flag[piece % kFlags])
+                    add_odd_values<T, D>(p, w, h, klo, mask, w.whole ? out16 : nullptr, w.whole ? nullptr : out32);
             }
         }
         if (dead) {
@@ -835,110 +607,34 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-// Join the partial results of the item that starts in share c and goes on into the next ones: one
-// warp a row.  out = sum_i w_i o_i / sum_i w_i, w_i = exp2(lse_i - max).
-template <typename T, int D>
-__global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    constexpr int E = D / 32;
-    const TreeArgs &a = p.a;
-    const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const int rr = blockIdx.y * 8 + (threadIdx.x >> 5);
-    // the next share's first piece: where it starts decides whether this share's last item goes on
-    const int b = p.ws_first[4 * (c + 1)], idx = p.ws_first[4 * (c + 1) + 1], k = p.ws_first[4 * (c + 1) + 2];
-    if (b < 0 || k == 0) return;
-    if (p.ws_first[4 * c] == b && p.ws_first[4 * c + 1] == idx && p.ws_first[4 * c + 2] > 0) return;  // it started before
-    Seq s;
-    bool rejected;
-    load_seq(p, b, s, &rejected);
-    const int h = idx / s.pairs, pr = idx - h * s.pairs;
-    const int x = rr >> 7, r = rr & 127, tl = r / p.group, TQ = p.tokens_per_tile;
-    const int t = (2 * pr + x) * TQ + tl;
-    if (tl >= TQ || t >= s.n) return;
-    // pieces: share c (its last: slot 2c + 1), then c + 1 .. (their first: slot 2c') while they
-    // start inside the item
-    int last = c + 1;
-    while (last + 1 < p.workers && p.ws_first[4 * (last + 1)] == b && p.ws_first[4 * (last + 1) + 1] == idx &&
-           p.ws_first[4 * (last + 1) + 2] > 0)
-        ++last;
-    auto part = [&](int e) {
-        return static_cast<int64_t>(e == c ? 2 * c + 1 : 2 * e) * p.rows_per_item + rr;
-    };
-    float mx = -INFINITY;
-    bool nan = false;
-    for (int e = c + lane; e <= last; e += 32) {
-        const float l = p.ws_lse[part(e)];
-        nan |= l != l;
-        mx = fmaxf(mx, l);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    nan = __any_sync(0xffffffffu, nan);
-    float acc[E], wsum = 0.f;
-#pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (mx != -INFINITY || nan) {
-        for (int base = c; base <= last; base += 32) {
-            const float l = base + lane <= last ? p.ws_lse[part(base + lane)] : -INFINITY;
-            const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
-            const int cnt = min(32, last - base + 1);
-            for (int u0 = 0; u0 < cnt; u0 += 4) {
-                float wu[4], v[4][E];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    wu[u] = u0 + u < cnt ? __shfl_sync(0xffffffffu, wl, (u0 + u) & 31) : 0.f;
-                    const float *src = p.ws_o + part(base + u0 + u) * D + lane * E;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) v[u][e] = wu[u] != 0.f ? __ldcg(src + e) : 0.f;
-                }
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    wsum += wu[u];
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += wu[u] != 0.f ? wu[u] * v[u][e] : 0.f;
-                }
-            }
-        }
-    }
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    const int64_t row = static_cast<int64_t>(s.q0 + t) * a.num_q_heads + h * p.group + (r - tl * p.group);
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + row * D + lane * E);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
-    if (a.lse_out && lane == 0) a.lse_out[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
-}
-
 template <typename T, int D>
 cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
                          int dev, cudaStream_t stream) {
     static std::atomic<bool> attr_set[64];
-    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
-    if (!attr_set[dev].load(std::memory_order_acquire)) {
-        const cudaError_t e = cudaFuncSetAttribute(tree_attention_kernel<T, D>,
-                                                   cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<D>::kSmem);
-        if (e != cudaSuccess) return e;
-        attr_set[dev].store(true, std::memory_order_release);
-    }
-    tree_attention_kernel<T, D><<<p.workers, kThreads, Tile<D>::kSmem, stream>>>(tq, tk, tv, p);
-    cudaError_t e = cudaGetLastError();
-    if (e != cudaSuccess || p.workers < 2) return e;
-    tree_merge_kernel<T, D><<<dim3(p.workers - 1, p.rows_per_item / 8), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    return launch_tree_kernel<T, D>(tree_attention_kernel<T, D>, kThreads, Tile<D>::kSmem, attr_set, tq, tk, tv, p, dev,
+                                    stream);
 }
 
 size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-TreePlan plan_tree(int max_query_len, int group, int head_dim, int num_workers, int sm_count) {
+// Several kv heads side by side when their rows fit 32 or 64 lanes each: larger copies (a TMA box
+// of 2 KB, one head of 16 tokens, moves 13 B a clock and SM, one of 4 heads 32) and all lanes in
+// use.  Wider trees, and fewer kv heads than lanes for them, take the kernel of this file.
+TreePlan plan_tree(int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count) {
     TreePlan t;
+    const int rows = max_query_len * group;
+    t.heads_per_item = rows <= 32 && num_kv_heads >= 3 ? 4 : (rows <= 64 && num_kv_heads >= 2 ? 2 : 1);
     t.workers = num_workers > 0 ? num_workers : sm_count;
-    t.tokens_per_tile = kBM / group;
-    t.rows_per_item = max_query_len > t.tokens_per_tile ? 2 * kBM : kBM;
+    t.tokens_per_tile = kTreeRows / t.heads_per_item / group;
+    t.key_shift = t.heads_per_item == 4 ? 6 : 7;
+    t.rows_per_item = t.heads_per_item == 1 && max_query_len > t.tokens_per_tile ? 2 * kTreeRows : kTreeRows;
     const size_t parts = static_cast<size_t>(2) * t.workers * t.rows_per_item;
     t.lse_off = align256(16 * static_cast<size_t>(t.workers));
     t.o_off = t.lse_off + align256(4 * parts);
     t.workspace_bytes = t.o_off + 4 * parts * head_dim;
-    t.smem_bytes = head_dim == 128 ? Tile<128>::kSmem : Tile<64>::kSmem;
+    t.smem_bytes = t.heads_per_item > 1 ? tree_packed_smem(head_dim) : (head_dim == 128 ? Tile<128>::kSmem : Tile<64>::kSmem);
     return t;
 }
 
@@ -949,12 +645,15 @@ cudaError_t launch_tree_attention(const CUtensorMap &tq, const CUtensorMap &tk, 
     p.a = a;
     p.group = a.num_q_heads / a.num_kv_heads;
     p.tokens_per_tile = plan.tokens_per_tile;
+    p.heads_per_item = plan.heads_per_item;
+    p.key_shift = plan.key_shift;
     p.workers = plan.workers;
     p.rows_per_item = plan.rows_per_item;
     char *ws = static_cast<char *>(workspace);
     p.ws_first = reinterpret_cast<int32_t *>(ws);
     p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_off);
     p.ws_o = reinterpret_cast<float *>(ws + plan.o_off);
+    if (p.heads_per_item > 1) return launch_tree_packed(tq, tk, tv, p, head_dim, q_dtype, dev, stream);
     if (q_dtype == KV_BF16)
         return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(tq, tk, tv, p, dev, stream)
                                : launch_typed<__nv_bfloat16, 64>(tq, tk, tv, p, dev, stream);

@@ -1,0 +1,391 @@
+// Pieces shared by the tree attention kernels (tree_attention.cu, tree_packed.cu): the work list of
+// (item, key tile) and its equal shares, the masks of drafted trees, the handling of values that
+// not every row sees, and the merge of items that lie in several shares.
+#pragma once
+
+#include <atomic>
+#include <type_traits>
+
+#include "common.cuh"
+#include "kernels.h"
+#include "tcgen05.cuh"
+
+namespace pkv {
+
+constexpr int kTreeRows = 128;         // query rows of a row tile = TMEM lanes
+constexpr int kHalf = 128 * 128;       // 128 rows x 64 16-bit elements (one swizzle column)
+constexpr uint32_t kTmemCols = 512;
+constexpr float kRescaleLog2 = 8.0f;   // a row's reference maximum moves when exceeded by more
+constexpr int kItemCost = 2;           // an item's fixed cost in key tiles
+constexpr int kMinShare = 4;           // least cost of a share: more than kItemCost, so that it holds a tile
+constexpr int kFlags = 8;              // pieces whose odd-value flags are kept
+
+struct TreeParams {
+    TreeArgs a;
+    int group;            // query heads of a kv head
+    int tokens_per_tile;  // drafted tokens of a kv head's rows in a row tile
+    int heads_per_item;   // 1: items of two row tiles of a kv head; 2 or 4: kv heads side by side in one
+    int key_shift;        // log2 of the keys of a key tile
+    int workers;          // shares at most
+    int rows_per_item;    // rows of a partial result
+    int32_t *ws_first;    // [workers][4] first piece of each share: sequence, item of it, key tile, -
+    float *ws_lse;        // [2 * workers][rows_per_item] log2-sum-exp2 of the partial results
+    float *ws_o;          // [2 * workers][rows_per_item][D] partial results, normalised
+};
+
+// A sequence's part of the work list.
+struct Seq {
+    int q0, n, L, ctx, kv_lo;  // first row, rows, length, context, first key any row sees
+    int j0, tiles;             // key tiles j0 .. j0 + tiles - 1
+    int items, pairs;          // items; of one kv head when items are pairs of row tiles
+};
+
+// The sequence's lengths; false when it has no rows, or is rejected (*rejected).
+__device__ __forceinline__ bool load_seq(const TreeParams &p, int b, Seq &s, bool *rejected) {
+    const TreeArgs &a = p.a;
+    s.q0 = a.query_start_loc[b];
+    s.n = a.query_start_loc[b + 1] - s.q0;
+    s.L = a.seq_lens[b];
+    const int bs = a.block_size;
+    *rejected = s.n > 0 && !(s.n <= a.max_query_len && s.q0 >= 0 && s.q0 <= a.num_tokens - s.n && s.L >= s.n &&
+                             s.L <= a.max_seq_len && (s.L - 1) / bs < a.max_blocks_per_seq);
+    if (s.n <= 0 || *rejected) return false;
+    s.ctx = s.L - s.n;
+    s.kv_lo = a.window > 0 ? max(0, s.ctx - a.window) : 0;
+    s.j0 = s.kv_lo >> p.key_shift;
+    s.tiles = ((s.L - 1) >> p.key_shift) + 1 - s.j0;
+    if (p.heads_per_item == 1) {
+        const int row_tiles = (s.n + p.tokens_per_tile - 1) / p.tokens_per_tile;
+        s.pairs = (row_tiles + 1) >> 1;
+        s.items = s.pairs * a.num_kv_heads;
+    } else {
+        s.pairs = 1;
+        s.items = (a.num_kv_heads + p.heads_per_item - 1) / p.heads_per_item;
+    }
+    return true;
+}
+
+__device__ __forceinline__ int64_t seq_cost(const TreeParams &p, int b) {
+    Seq s;
+    bool rejected;
+    if (!load_seq(p, b, s, &rejected)) return 0;
+    return static_cast<int64_t>(s.tiles + kItemCost) * s.items;
+}
+
+// The share [x0, x1) of CTA c (x0 == x1: none), and where it starts: sequence, item and the cost
+// where that item starts.  Computed by the whole block; b, idx and at are set in shared memory and
+// valid after the next __syncthreads.
+struct ShareStart {
+    int64_t at;
+    int b, idx;
+};
+
+template <int kThreads>
+__device__ __forceinline__ void share_of_cta(const TreeParams &p, int c, int64_t &x0, int64_t &x1, ShareStart &start) {
+    __shared__ int64_t warp_sum[kThreads / 32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int num_seqs = p.a.num_seqs;
+    const int per = (num_seqs + kThreads - 1) / kThreads;
+    const int b_lo = min(num_seqs, static_cast<int>(threadIdx.x) * per), b_hi = min(num_seqs, b_lo + per);
+    int64_t sum = 0;
+    for (int b = b_lo; b < b_hi; ++b) sum += seq_cost(p, b);
+    int64_t incl = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += v;
+    }
+    if (lane == 31) warp_sum[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - sum, total = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) before += warp_sum[w];
+        total += warp_sum[w];
+    }
+    const int64_t most = max(int64_t(1), total / kMinShare);
+    const int shares = total == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(p.workers), most));
+    x0 = x1 = 0;
+    if (c >= shares) return;
+    x0 = total * c / shares;
+    x1 = total * (c + 1) / shares;
+    if (x0 >= before && x0 < before + sum) {  // one thread
+        int64_t at = before;
+        for (int b = b_lo; b < b_hi; ++b) {
+            const int64_t cost = seq_cost(p, b);
+            if (x0 < at + cost) {
+                Seq s;
+                bool rejected;
+                load_seq(p, b, s, &rejected);
+                start.b = b;
+                start.idx = static_cast<int>((x0 - at) / (s.tiles + kItemCost));
+                start.at = at + static_cast<int64_t>(start.idx) * (s.tiles + kItemCost);
+                break;
+            }
+            at += cost;
+        }
+    }
+}
+
+// Rows of rejected sequences are 0 (lse -inf): the CTAs take the sequences in turn.
+template <typename T, int D> __device__ __forceinline__ void zero_rejected(const TreeParams &p) {
+    const TreeArgs &a = p.a;
+    for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
+        Seq s;
+        bool rejected;
+        load_seq(p, b, s, &rejected);
+        if (!rejected) continue;
+        if (threadIdx.x == 0) report(a.d_err, KV_DERR_BAD_LEN);
+        const int64_t r0 = max(s.q0, 0), r1 = min(static_cast<int64_t>(s.q0) + s.n, static_cast<int64_t>(a.num_tokens));
+        const int64_t rows = (r1 - r0) * a.num_q_heads;
+        for (int64_t i = threadIdx.x; i < rows * (D / 8); i += blockDim.x)
+            reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + r0 * a.num_q_heads * D)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse_out)
+            for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) a.lse_out[r0 * a.num_q_heads + i] = -INFINITY;
+    }
+}
+
+// The pieces of a share, in order: (item, key tiles ja .. jb - 1).  Every warp walks the same ones.
+struct Walk {
+    int b, idx;       // sequence, item of it (the next piece's)
+    int64_t at;       // cost where the item starts
+    int64_t x0, x1;   // the share
+    Seq s;
+    // the piece
+    Seq cur;
+    int seq, item, ja, jb;  // sequence, item of it, key tiles (absolute)
+    bool whole;             // it is its whole item
+
+    __device__ __forceinline__ void start(const TreeParams &p, const ShareStart &st, int64_t x0_, int64_t x1_) {
+        b = st.b, idx = st.idx, at = st.at, x0 = x0_, x1 = x1_;
+        bool rejected;
+        load_seq(p, b, s, &rejected);
+    }
+    __device__ __forceinline__ bool next(const TreeParams &p) {
+        while (at < x1) {
+            const int64_t first = at + kItemCost;
+            ja = static_cast<int>(max(int64_t(0), x0 - first));
+            jb = static_cast<int>(min(static_cast<int64_t>(s.tiles), x1 - first));
+            const bool some = ja < jb;
+            if (some) {
+                ja += s.j0;
+                jb += s.j0;
+                whole = ja == s.j0 && jb == s.j0 + s.tiles;
+                seq = b;
+                item = idx;
+                cur = s;
+            }
+            at = first + s.tiles;
+            if (++idx == s.items) {
+                idx = 0;
+                bool rejected = false;
+                while (++b < p.a.num_seqs && !load_seq(p, b, s, &rejected)) {}
+                if (b >= p.a.num_seqs) x1 = at;  // the end of the list
+            }
+            if (some) return true;
+        }
+        return false;
+    }
+};
+
+// Where the partial result of the piece goes: a share leaves at most one that starts inside its
+// item (slot 2c) and one that starts it (2c + 1).
+__device__ __forceinline__ int64_t part_row(const TreeParams &p, int c, bool starts, int row) {
+    return static_cast<int64_t>(2 * c + (starts ? 1 : 0)) * p.rows_per_item + row;
+}
+
+// Whether key tile j holds a key that not every row of the sequence sees.
+__device__ __forceinline__ bool mixed_tile(const TreeParams &p, const Seq &s, int j) {
+    const int k0 = j << p.key_shift;
+    return k0 + (1 << p.key_shift) > s.ctx || (p.a.window > 0 && k0 < s.ctx + s.n - p.a.window);
+}
+
+// The keys k0 .. k0 + 31 a row sees (bit i: key k0 + i): context keys from klo, drafted keys of
+// the mask word.
+__device__ __forceinline__ uint32_t seen32(int k0, int ctx, int klo, uint64_t mask) {
+    const int lo = max(klo - k0, 0), hi = min(ctx - k0, 32);
+    uint32_t v = 0;
+    if (lo < hi) v = (hi == 32 ? 0xffffffffu : (1u << hi) - 1) & ~((1u << lo) - 1);  // lo < 32
+    const int d = k0 - ctx;
+    if (d >= 0) v |= d < 64 ? static_cast<uint32_t>(mask >> d) : 0u;
+    else if (d > -32) v |= static_cast<uint32_t>(mask << -d);
+    return v;
+}
+
+template <typename T> struct NonFinite;  // exponent bits all ones
+template <> struct NonFinite<__half> { static constexpr uint32_t mask = 0x7C00u; };
+template <> struct NonFinite<__nv_bfloat16> { static constexpr uint32_t mask = 0x7F80u; };
+
+template <typename T> __device__ __forceinline__ bool non_finite16(uint32_t bits) {
+    return (bits & NonFinite<T>::mask) == NonFinite<T>::mask;
+}
+
+__device__ __forceinline__ void st_shared_v4(uint32_t a, uint4 v) {
+    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(a), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+__device__ __forceinline__ uint4 ld_shared_v4(uint32_t a) {
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(a) : "memory");
+    return v;
+}
+
+// One 16-byte chunk of a V tile in shared memory: zeroed, or its non-finite values zeroed (*odd set).
+template <typename T> __device__ __forceinline__ void clean_chunk(uint32_t at, bool zero, bool &odd) {
+    if (zero) {
+        st_shared_v4(at, make_uint4(0, 0, 0, 0));
+        return;
+    }
+    const uint4 v = ld_shared_v4(at);
+    uint32_t u[4] = {v.x, v.y, v.z, v.w};
+    bool bad = false;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (non_finite16<T>(u[e])) u[e] &= 0xffff0000u, bad = true;
+        if (non_finite16<T>(u[e] >> 16)) u[e] &= 0x0000ffffu, bad = true;
+    }
+    if (bad) {
+        st_shared_v4(at, make_uint4(u[0], u[1], u[2], u[3]));
+        odd = true;
+    }
+}
+
+// Add the non-finite values of V that a row sees among the keys [k0, k1) to its written result
+// (out16 of type T, or a float row): they were zeroed for the products.  Rare, so plain.
+template <typename T, int D>
+static __device__ __noinline__ void add_non_finite(const TreeArgs &a, int b, int h, int k0, int k1, int ctx, int klo,
+                                            uint64_t mask, T *out16, float *out32) {
+    for (int k = k0; k < k1; ++k) {
+        const bool sees = k < ctx ? k >= klo : (mask >> (k - ctx)) & 1;
+        const int id = a.block_table[b * a.bt_stride + k / a.block_size];
+        if (!sees || id < 0 || id >= a.num_blocks) continue;
+        const T *v = static_cast<const T *>(a.v_cache) +
+                     ((static_cast<int64_t>(id) * a.block_size + k % a.block_size) * a.num_kv_heads + h) * D;
+        for (int d = 0; d < D; ++d) {
+            const float f = to_float<T>(v[d]);
+            if (isfinite(f)) continue;
+            if (out32) out32[d] += f;
+            else out16[d] = from_float<T>(to_float<T>(out16[d]) + f);
+        }
+    }
+}
+
+// Add the non-finite values that the row sees in the piece's mixed tiles.
+template <typename T, int D>
+__device__ __forceinline__ void add_odd_values(const TreeParams &p, const Walk &w, int h, int klo, uint64_t mask, T *out16,
+                                               float *out32) {
+    const TreeArgs &a = p.a;
+    const Seq &s = w.cur;
+    const int ka = w.ja << p.key_shift, kb = min(w.jb << p.key_shift, s.L);
+    if (a.window > 0)
+        add_non_finite<T, D>(a, w.seq, h, max(ka, s.kv_lo), min(min(s.ctx, s.ctx + s.n - a.window), kb), s.ctx, klo, mask,
+                             out16, out32);
+    add_non_finite<T, D>(a, w.seq, h, max(ka, s.ctx), kb, s.ctx, klo, mask, out16, out32);
+}
+
+// Join the partial results of the item that starts in share c and goes on into the next ones: one
+// warp a row.  out = sum_i w_i o_i / sum_i w_i, w_i = exp2(lse_i - max).
+template <typename T, int D>
+static __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int E = D / 32;
+    const TreeArgs &a = p.a;
+    const int c = blockIdx.x, lane = threadIdx.x & 31;
+    const int rr = blockIdx.y * 8 + (threadIdx.x >> 5);
+    // the next share's first piece: where it starts decides whether this share's last item goes on
+    const int b = p.ws_first[4 * (c + 1)], idx = p.ws_first[4 * (c + 1) + 1], k = p.ws_first[4 * (c + 1) + 2];
+    if (b < 0 || k == 0) return;
+    if (p.ws_first[4 * c] == b && p.ws_first[4 * c + 1] == idx && p.ws_first[4 * c + 2] > 0) return;  // it started before
+    Seq s;
+    bool rejected;
+    load_seq(p, b, s, &rejected);
+    // the row's kv head, token and head of the group
+    int h, t, hh;
+    const int TQ = p.tokens_per_tile;
+    if (p.heads_per_item == 1) {
+        h = idx / s.pairs;
+        const int r = rr & 127, tl = r / p.group;
+        t = (2 * (idx - h * s.pairs) + (rr >> 7)) * TQ + tl;
+        hh = r - tl * p.group;
+        if (tl >= TQ || t >= s.n) return;
+    } else {
+        const int lanes = kTreeRows / p.heads_per_item, r = rr % lanes;
+        h = idx * p.heads_per_item + rr / lanes;
+        t = r / p.group;
+        hh = r - t * p.group;
+        if (h >= a.num_kv_heads || t >= s.n) return;
+    }
+    // pieces: share c (its last: slot 2c + 1), then c + 1 .. (their first: slot 2c') while they
+    // start inside the item
+    int last = c + 1;
+    while (last + 1 < p.workers && p.ws_first[4 * (last + 1)] == b && p.ws_first[4 * (last + 1) + 1] == idx &&
+           p.ws_first[4 * (last + 1) + 2] > 0)
+        ++last;
+    auto part = [&](int e) { return part_row(p, e, e == c, rr); };
+    float mx = -INFINITY;
+    bool nan = false;
+    for (int e = c + lane; e <= last; e += 32) {
+        const float l = p.ws_lse[part(e)];
+        nan |= l != l;
+        mx = fmaxf(mx, l);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
+    nan = __any_sync(0xffffffffu, nan);
+    float acc[E], wsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < E; ++e) acc[e] = 0.f;
+    if (mx != -INFINITY || nan) {
+        for (int base = c; base <= last; base += 32) {
+            const float l = base + lane <= last ? p.ws_lse[part(base + lane)] : -INFINITY;
+            const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
+            const int cnt = min(32, last - base + 1);
+            for (int u0 = 0; u0 < cnt; u0 += 4) {
+                float wu[4], v[4][E];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    wu[u] = u0 + u < cnt ? __shfl_sync(0xffffffffu, wl, (u0 + u) & 31) : 0.f;
+                    const float *src = p.ws_o + part(base + u0 + u) * D + lane * E;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) v[u][e] = wu[u] != 0.f ? __ldcg(src + e) : 0.f;
+                }
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    wsum += wu[u];
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += wu[u] != 0.f ? wu[u] * v[u][e] : 0.f;
+                }
+            }
+        }
+    }
+    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+    const int64_t row = static_cast<int64_t>(s.q0 + t) * a.num_q_heads + h * p.group + hh;
+    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + row * D + lane * E);
+#pragma unroll
+    for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
+    if (a.lse_out && lane == 0) a.lse_out[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
+}
+
+// The attention kernel and, with more than one share, the merge.
+template <typename T, int D, typename Kernel>
+static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, std::atomic<bool> *attr_set,
+                                      const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                      const TreeParams &p, int dev, cudaStream_t stream) {
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e =
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    kernel<<<p.workers, threads, smem, stream>>>(tq, tk, tv, p);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess || p.workers < 2) return e;
+    tree_merge_kernel<T, D><<<dim3(p.workers - 1, p.rows_per_item / 8), 256, 0, stream>>>(p);
+    return cudaGetLastError();
+}
+
+// Items of several kv heads side by side (tree_packed.cu).
+cudaError_t launch_tree_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                               int head_dim, int q_dtype, int dev, cudaStream_t stream);
+size_t tree_packed_smem(int head_dim);
+
+}  // namespace pkv

@@ -1,0 +1,575 @@
+// Tree attention for small trees: several kv heads of a sequence side by side in one 128-row tile.
+//
+// When a kv head has at most 32 (64) query rows, four (two) heads share the 128 TMEM lanes: lanes
+// 32 h .. belong to head h of the item's group.  Reading the cache is the bound then, and one head
+// at a time cannot read it fast enough: a TMA box of 16 tokens of one head and 64 dims (2 KB) costs
+// about 130 clocks plus two a row, 13 bytes a clock and SM, where HBM gives 23; a box of two heads
+// moves 21, of four 32.  The tensor map splits tokens into groups of 8 so that a box lands as
+// [group of 8 tokens][head][token][64 dims]: the swizzle atoms of one head lie a constant distance
+// apart over all blocks of a key tile, which is what a matrix descriptor can say.
+//
+// Per key tile (64 keys of four heads, or 128 of two: 64 KB of K and of V at 128 dims) and head h:
+//   S_h = Q K_h^T    all 128 rows, of which the lanes of head h are read
+//   P_h = exp2(S_h * scale - m)    one thread a row; P_h has TMEM columns of its own
+//   O  += P_h V_h    for the lanes of head h alone (the other lanes are switched off), so the
+//                    heads' results share the columns of O
+// TMEM: S 256 columns, P 128, O 64 or 128.  S_h is free as soon as the softmax has read it, so the next
+// tile's scores are formed before O += P_h V_h when its keys are there, and after it when they are not.
+// For the work list, the masks, cleaned V tiles and bounded waits see tree_attention.cu.
+//
+// Warps (224 threads): 0-3 softmax (thread = TMEM lane = query row), 4 TMA producer, 5 issues the
+// MMAs, 6 cleans V tiles.
+#include "tree_common.cuh"
+
+namespace pkv {
+namespace {
+
+constexpr int kThreads = 224;
+constexpr uint32_t kColP = 256, kColO = 384;
+
+template <int D, int PH> struct Pack {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kKeys = PH == 4 ? 64 : 128;         // keys of a key tile
+    static constexpr int kLanes = kTreeRows / PH;            // lanes of a head
+    static constexpr int kQBytes = kHalves * kHalf;
+    static constexpr int kSide = kKeys * PH * 128;           // 64 dims of a key tile of all heads (32 KB)
+    static constexpr int kEntry = kHalves * kSide;
+    static constexpr int kStages = D == 128 ? 3 : 6;         // ring entries (192 KB)
+    static constexpr int kOffKV = kQBytes;
+    static constexpr int kOffBar = kOffKV + kStages * kEntry;
+    static constexpr int kNumBars = 3 + 3 * PH + 2 * kStages;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM address, abort flag, flags, cleaned
+    static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
+    static_assert(kSmem + 128 <= 227 * 1024, "shared memory, with the kernel's static part");
+    static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
+};
+
+template <typename T, int D, int PH>
+__global__ void __launch_bounds__(kThreads, 1)
+tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                   const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TreeParams p) {
+    using PK = Pack<D, PH>;
+    constexpr int kStages = PK::kStages, kKeys = PK::kKeys, kLanes = PK::kLanes;
+    constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarDrain = 2, kBarS = 3, kBarP = kBarS + PH, kBarPd = kBarP + PH,
+                  kBarFull = kBarPd + PH, kBarEmpty = kBarFull + kStages;
+    const TreeArgs &a = p.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = p.group, TQ = p.tokens_per_tile, bs = a.block_size;
+    const int c = blockIdx.x;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + PK::kOffBar);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + PK::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + PK::kOffMisc + 4);
+    volatile int *odd_flag = reinterpret_cast<volatile int *>(smem + PK::kOffMisc + 8);  // [kFlags], per piece
+    int32_t *cleaned = reinterpret_cast<int32_t *>(smem + PK::kOffMisc + 8 + 4 * kFlags);  // [kStages]: entry + 1
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+
+    __shared__ ShareStart start;
+    int64_t x0, x1;
+    share_of_cta<kThreads>(p, c, x0, x1, start);
+    zero_rejected<T, D>(p);
+    if (x0 == x1) {
+        if (threadIdx.x == 0) p.ws_first[4 * c] = -1;
+        return;
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(bar(kBarQFull), 1);
+        mbar_init(bar(kBarQEmpty), 1);
+        mbar_init(bar(kBarDrain), 1);
+        for (int h = 0; h < PH; ++h) {
+            mbar_init(bar(kBarS + h), 1);
+            mbar_init(bar(kBarP + h), kLanes);
+            mbar_init(bar(kBarPd + h), 1);
+        }
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar(kBarFull + s), 1);
+            mbar_init(bar(kBarEmpty + s), 2);  // released by the MMA warp and the cleaning warp
+        }
+        *abort_flag = 0;
+        for (int i = 0; i < kFlags; ++i) odd_flag[i] = 0;
+        for (int i = 0; i < kStages; ++i) cleaned[i] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 5) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    Walk w;
+    w.start(p, start, x0, x1);
+
+    if (warp == 4) {
+        // ============================================================ TMA producer
+        const int bpt = kKeys / bs;  // blocks of a key tile
+        const uint32_t q_bytes = static_cast<uint32_t>(PH * PK::kHalves) * TQ * g * 128;
+        if (lane == 0) {
+            prefetch_tensormap(&tmap_q);
+            prefetch_tensormap(&tmap_k);
+            prefetch_tensormap(&tmap_v);
+        }
+        int entry = 0;  // ring entries filled
+        int piece = 0;
+        bool stop = false;
+        while (!stop && w.next(p)) {
+            const Seq s = w.cur;
+            const int h0 = w.item * PH;
+            if (piece == 0 && lane == 0) {
+                p.ws_first[4 * c] = w.seq;
+                p.ws_first[4 * c + 1] = w.item;
+                p.ws_first[4 * c + 2] = w.ja - s.j0;
+            }
+            // block ids of key tile j: lane l holds block j * bpt + l
+            const int nblk = (s.L - 1) / bs + 1, first_blk = s.kv_lo / bs;
+            auto block_id = [&](int j) {
+                const int lb = j * bpt + lane;
+                int id = a.num_blocks;  // one past the pool: the copy reads zeros
+                if (lane < bpt && lb >= first_blk && lb < nblk) {
+                    const int e = a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + lb];
+                    if (e >= 0 && e < a.num_blocks) id = e;
+                    else report(a.d_err, KV_DERR_BAD_BLOCK);
+                }
+                return id;
+            };
+            int next_id = block_id(w.ja);
+            bool ok = true;
+            if (lane == 0) {
+                // Q of the item (heads past the last read zeros), once the piece before has formed
+                // its last scores
+                if (piece > 0) ok = mbar_wait_sleep(bar(kBarQEmpty), (piece - 1) & 1);
+                if (ok) {
+                    mbar_arrive_expect_tx(bar(kBarQFull), q_bytes);
+                    for (int h = 0; h < PH; ++h)
+                        for (int hf = 0; hf < PK::kHalves; ++hf)
+                            tma_load_3d(smem_u32(smem + hf * kHalf + h * kLanes * 128), &tmap_q, bar(kBarQFull), 64 * hf,
+                                        (h0 + h) * g, s.q0);
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
+                if (lane == 0) {
+                    report(a.d_err, KV_DERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            ++piece;
+            for (int j = w.ja; j < w.jb && !stop; ++j) {
+                const int my_id = next_id;
+                if (j + 1 < w.jb) next_id = block_id(j + 1);
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    const int slot = entry % kStages;
+                    int quit = 0;
+                    if (lane == 0) {
+                        if (entry >= kStages && !mbar_wait_sleep(bar(kBarEmpty + slot), (entry / kStages - 1) & 1)) {
+                            quit = 1;
+                            report(a.d_err, KV_DERR_TIMEOUT);
+                            *abort_flag = 1;
+                        } else if (*abort_flag) {
+                            quit = 1;
+                        }
+                        if (!quit) mbar_arrive_expect_tx(bar(kBarFull + slot), PK::kEntry);
+                    }
+                    if (__shfl_sync(0xffffffffu, quit, 0)) {
+                        stop = true;
+                        break;
+                    }
+                    const CUtensorMap *m = is_v ? &tmap_v : &tmap_k;
+                    uint8_t *dst = smem + PK::kOffKV + slot * PK::kEntry;
+                    for (int jb = 0; jb < bpt; ++jb) {
+                        const int id = __shfl_sync(0xffffffffu, my_id, jb);
+                        if (lane == 0)
+                            for (int hf = 0; hf < PK::kHalves; ++hf)
+                                tma_load_5d(smem_u32(dst + hf * PK::kSide + jb * bs * PH * 128), m, bar(kBarFull + slot),
+                                            64 * hf, 0, h0, 0, id);
+                    }
+                    ++entry;
+                }
+            }
+        }
+        // never leave with copies in flight into this CTA's shared memory
+        if (lane == 0) {
+            if (piece > 0 && !mbar_wait_sleep(bar(kBarQFull), (piece - 1) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+            for (int i = max(0, entry - kStages); i < entry; ++i)
+                if (!mbar_wait_sleep(bar(kBarFull + i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+        }
+    } else if (warp == 5) {
+        // ============================================================ MMA issue
+        // The whole warp runs the schedule (warp-uniform); one lane issues.
+        constexpr uint32_t ab = AbFormat<T>::value;
+        constexpr uint32_t idesc_s = mma_idesc(ab, false, kTreeRows, kKeys);
+        constexpr uint32_t idesc_pv = mma_idesc(ab, true, kTreeRows, D);
+        const uint64_t dq = smem_desc(smem_u32(smem), 16, 1024);
+        // one head's atoms (8 keys x 64 dims, 1 KB) are PH KB apart
+        const uint64_t dk0 = smem_desc(smem_u32(smem + PK::kOffKV), 16, PH * 1024);
+        const uint64_t dv0 = smem_desc(smem_u32(smem + PK::kOffKV), PK::kSide, PH * 1024);
+        const bool leader = lane == 0;
+        auto wait_warp = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity));
+        };
+        // scores of head h against the keys in ring entry e
+        auto scores = [&](int h, int e) {
+            const int sk = e % kStages;
+            const uint64_t dk = dk0 + static_cast<uint64_t>((sk * PK::kEntry + h * 1024) >> 4);
+            if (leader) {
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_f16(tmem + h * kKeys, dq + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
+                            dk + (((k >> 2) * PK::kSide + (k & 3) * 32) >> 4), idesc_s, k > 0);
+                mma_commit(bar(kBarS + h));
+                if (h == PH - 1) mma_commit(bar(kBarEmpty + sk));
+            }
+            __syncwarp();
+        };
+        int done = 0;  // key tiles of the pieces before
+        bool dead = false;
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (!wait_warp(bar(kBarQFull), piece & 1) ||
+                !wait_warp(bar(kBarFull + 2 * done % kStages), (2 * done / kStages) & 1)) {
+                dead = true;
+                break;
+            }
+            tc_fence_after();
+            const int n = w.jb - w.ja;
+            for (int h = 0; h < PH; ++h) scores(h, 2 * done);
+            for (int t = 0; t < n; ++t, ++done) {
+                const int ev = 2 * done + 1, sv = ev % kStages, ek = ev + 1, sk = ek % kStages;
+                const bool more = t + 1 < n;
+                if (!more && leader) mma_commit(bar(kBarQEmpty));  // the piece's last scores have been issued
+                if (!wait_warp(bar(kBarFull + sv), (ev / kStages) & 1) ||
+                    (mixed_tile(p, s, w.ja + t) && !__all_sync(0xffffffffu, wait_at_least_bounded(&cleaned[sv], ev + 1)))) {
+                    dead = true;
+                    break;
+                }
+                bool keys = false;  // the next tile's keys are there
+                int ahead = 0;      // heads whose next scores have been issued
+                for (int h = 0; h < PH; ++h) {
+                    if (!wait_warp(bar(kBarP + h), done & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    if (more && !keys) keys = __all_sync(0xffffffffu, mbar_test(bar(kBarFull + sk), (ek / kStages) & 1));
+                    if (keys) {
+                        tc_fence_after();
+                        while (ahead <= h) scores(ahead++, ek);
+                    }
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((sv * PK::kEntry + h * 1024) >> 4);
+                    if (leader) {
+                        uint32_t off[4];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) off[i] = i * 32 / kLanes == h ? 0u : 0xffffffffu;
+#pragma unroll
+                        for (int k = 0; k < kKeys / 16; ++k)
+                            mma_f16_ts_rows(tmem + kColO, tmem + kColP + h * (kKeys / 2) + k * 8,
+                                            dv + ((k * PH * 2048) >> 4), idesc_pv, t > 0 || k > 0, off);
+                        mma_commit(bar(kBarPd + h));
+                        if (h == PH - 1) mma_commit(bar(kBarEmpty + sv));
+                    }
+                    __syncwarp();
+                }
+                if (dead) break;
+                if (more && ahead < PH) {
+                    if (!keys && !wait_warp(bar(kBarFull + sk), (ek / kStages) & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    while (ahead < PH) scores(ahead++, ek);
+                }
+            }
+        }
+        if (dead && leader) {
+            report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+        // every MMA this warp issued has completed before TMEM is freed
+        if (leader) mma_commit(bar(kBarDrain));
+        __syncwarp();
+        if (!wait_warp(bar(kBarDrain), 0) && leader) report(a.d_err, KV_DERR_TIMEOUT);
+    } else if (warp == 6) {
+        // ============================================================ cleaning of V tiles
+        int done = 0;
+        bool dead = false;
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (lane == 0) odd_flag[piece % kFlags] = 0;
+            __syncwarp();
+            for (int e = 0; e < 2 * (w.jb - w.ja); ++e) {
+                const int j = w.ja + (e >> 1);
+                const int ev = 2 * done + e, sv = ev % kStages;
+                if (!__all_sync(0xffffffffu, mbar_wait_sleep(bar(kBarFull + sv), (ev / kStages) & 1))) {
+                    dead = true;
+                    break;
+                }
+                if (!(e & 1) || !mixed_tile(p, s, j)) {
+                    if (lane == 0) mbar_arrive(bar(kBarEmpty + sv));
+                    continue;
+                }
+                const uint32_t tile = smem_u32(smem + PK::kOffKV + sv * PK::kEntry);
+                const int k0 = j * kKeys;
+                bool odd = false;
+                // keys no row sees: [block start, kv_lo) and [L, block end); keys some rows may not
+                // see: [kv_lo, ctx + n - window) of the context, the drafted [ctx, L)
+                auto clean = [&](int lo, int hi, bool zero) {
+                    lo = max(lo, k0) - k0;
+                    hi = min(hi, k0 + kKeys) - k0;
+                    // 16-byte chunks: 8 of a key's 64 dims, of every head and side
+                    for (int i = lo * 8 + lane; i < hi * 8; i += 32) {
+                        const int key = i >> 3;
+                        const uint32_t at0 = tile + (key >> 3) * PH * 1024 + (key & 7) * 128 + (i & 7) * 16;
+                        for (int u = 0; u < PH * PK::kHalves; ++u)
+                            clean_chunk<T>(at0 + (u % PH) * 1024 + (u / PH) * PK::kSide, zero, odd);
+                    }
+                };
+                if (a.window > 0) {
+                    clean(s.kv_lo / bs * bs, s.kv_lo, true);
+                    clean(s.kv_lo, min(s.ctx, s.ctx + s.n - a.window), false);
+                }
+                clean(s.ctx, s.L, false);
+                clean(s.L, (s.L + bs - 1) / bs * bs, true);
+                if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[piece % kFlags] = 1;
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    st_release_cta(&cleaned[sv], ev + 1);
+                    mbar_arrive(bar(kBarEmpty + sv));
+                }
+                __syncwarp();
+            }
+            done += w.jb - w.ja;
+        }
+        if (dead && lane == 0) {
+            report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    } else {
+        // ============================================================ softmax and results
+        const int r = threadIdx.x;                       // query row = TMEM lane
+        const int hi = r / kLanes, rr = r % kLanes;      // head of the item (one a warp), row of it
+        const int tl = rr / g, hh = rr - tl * g;         // token, head of the group
+        const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
+        const uint32_t t_s = trow + hi * kKeys, t_p = trow + kColP + hi * (kKeys / 2), t_o = trow + kColO;
+        const float c2 = a.scale_log2;
+        const float2 cc = make_float2(c2, c2);
+        bool dead = false;
+        // waits are decided for the whole warp: its lanes take the warp-collective TMEM
+        // loads and stores together
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_sleep(b, parity));
+        };
+        int done = 0, pd = 0;  // key tiles taken; of those, products O known to have completed
+        auto settled = [&] {   // O and P_h are free: the products of all tiles taken have completed
+            while (pd < done)
+                if (!wait_all(bar(kBarPd + hi), pd++ & 1)) return false;
+            tc_fence_after();
+            return true;
+        };
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const int h = w.item * PH + hi;
+            const bool valid = tl < s.n && h < a.num_kv_heads;
+            const int64_t token = s.q0 + (valid ? tl : 0);
+            uint64_t mask = 0;
+            if (valid) mask = a.tree_mask[token] & (s.n >= 64 ? ~0ull : (1ull << s.n) - 1);
+            const int pos = s.ctx - 1 + __popcll(mask);
+            const int klo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
+            const bool warp_valid = __any_sync(0xffffffffu, valid);
+            float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
+            float2 rsum = make_float2(0.f, 0.f);  // sum of the rounded weights (what the product uses)
+            float2 esum = make_float2(0.f, 0.f);  // sum of the weights (log-sum-exp)
+            uint32_t wt[kKeys / 2];
+            // One pass over the tile's S: weights against the reference in use, the tile maximum
+            // tracked alongside, 32 columns at a time with the next load in flight.
+            auto weights = [&](auto masked_tag, int kbase, float nref, float &mraw, float2 &tr, float2 &te) {
+                constexpr bool masked = decltype(masked_tag)::value;
+                const float2 ref2 = make_float2(nref, nref);
+                uint32_t buf[2][32];
+                mraw = -INFINITY;
+                tr = te = make_float2(0.f, 0.f);
+                tmem_ld32_async(t_s, buf[0]);
+#pragma unroll
+                for (int ch = 0; ch < kKeys / 32; ++ch) {
+                    uint32_t(&v)[32] = buf[ch & 1];
+                    tmem_wait_regs(v);
+                    if (ch + 1 < kKeys / 32) tmem_ld32_async(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
+                    uint32_t seen = 0xffffffffu;
+                    if constexpr (masked) seen = valid ? seen32(kbase + ch * 32, s.ctx, klo, mask) : 0u;
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) {
+                        const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
+                        const float2 e = fma2(make_float2(s0, s1), cc, ref2);
+                        float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
+                        if constexpr (masked) {
+                            const bool v0 = (seen >> (2 * k)) & 1, v1 = (seen >> (2 * k + 1)) & 1;
+                            e0 = v0 ? e0 : 0.f;
+                            e1 = v1 ? e1 : 0.f;
+                            mraw = fmaxf(mraw, fmaxf(v0 ? s0 : -INFINITY, v1 ? s1 : -INFINITY));
+                        } else {
+                            mraw = fmaxf(mraw, fmaxf(s0, s1));
+                        }
+                        wt[ch * 16 + k] = pack2<T>(e0, e1);
+                        te = add2(te, make_float2(e0, e1));
+                        tr = add2(tr, unpack2<T>(wt[ch * 16 + k]));
+                    }
+                }
+            };
+            for (int j = w.ja; j < w.jb; ++j) {
+                if (!wait_all(bar(kBarS + hi), done & 1)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                if (warp_valid) {
+                    const int kbase = j * kKeys;
+                    const bool masked = mixed_tile(p, s, j);
+                    float mraw;
+                    float2 tr, te;
+                    auto run_weights = [&](float nref, float &mx) {
+                        if (masked) weights(std::true_type{}, kbase, nref, mx, tr, te);
+                        else weights(std::false_type{}, kbase, nref, mx, tr, te);
+                    };
+                    run_weights(m_used == -INFINITY ? 0.f : -m_used, mraw);
+                    // scale >= 0, so the scaled maximum is the maximum of the scaled scores
+                    const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
+                    const bool moved = valid && mt > m_used + kRescaleLog2;  // also the first finite maximum
+                    const bool any_moved = __any_sync(0xffffffffu, moved);
+                    if (!settled()) {
+                        dead = true;
+                        break;
+                    }
+                    if (any_moved) {
+                        const bool rescale = moved && m_used != -INFINITY;  // O and the sums hold earlier tiles
+                        const float f = moved ? fast_exp2(m_used - mt) : 1.f;
+                        if (moved) {
+                            m_used = mt;
+                            rsum.x *= f, rsum.y *= f;
+                            esum.x *= f, esum.y *= f;
+                        }
+                        if (__any_sync(0xffffffffu, rescale)) {
+                            // the warp loads and stores its lanes of O together; rows that keep their
+                            // maximum scale by 1
+#pragma unroll 1
+                            for (int ch = 0; ch < D / 32; ++ch) {
+                                float o[32];
+                                tmem_ld32(t_o + ch * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= f;
+                                tmem_st32(t_o + ch * 32, o);
+                            }
+                            tmem_wait_st();
+                        }
+                        float m2;
+                        run_weights(m_used == -INFINITY ? 0.f : -m_used, m2);
+                    }
+                    rsum = add2(rsum, tr);
+                    esum = add2(esum, te);
+                    tmem_st32u(t_p, wt);
+                    if constexpr (kKeys == 128) tmem_st32u(t_p + 32, wt + 32);
+                    tmem_wait_st();
+                } else if (!settled()) {  // a warp without rows passes every phase all the same
+                    dead = true;
+                    break;
+                }
+                tc_fence_before();
+                mbar_arrive(bar(kBarP + hi));
+                ++done;
+            }
+            if (dead) break;
+            if (!settled()) {
+                dead = true;
+                break;
+            }
+            if (!warp_valid) continue;
+            const float lr = rsum.x + rsum.y, le = esum.x + esum.y;
+            const float inv = lr == 0.f ? 0.f : 1.f / lr;
+            const int64_t row = token * a.num_q_heads + h * g + hh;
+            T *out16 = static_cast<T *>(a.out) + row * D;
+            const int64_t part = part_row(p, c, w.ja == s.j0, r);
+            float *out32 = p.ws_o + part * D;
+#pragma unroll 1
+            for (int ch = 0; ch < D / 32; ++ch) {
+                float o[32];
+                tmem_ld32(t_o + ch * 32, o);
+                tmem_wait_ld();
+                if (!valid) continue;
+                // a row that saw nothing is 0
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] = inv != 0.f ? o[k] * inv : 0.f;
+                if (w.whole) {
+                    uint4 *dst = reinterpret_cast<uint4 *>(out16 + ch * 32);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        dst[k] = make_uint4(pack2<T>(o[8 * k], o[8 * k + 1]), pack2<T>(o[8 * k + 2], o[8 * k + 3]),
+                                            pack2<T>(o[8 * k + 4], o[8 * k + 5]), pack2<T>(o[8 * k + 6], o[8 * k + 7]));
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(out32 + ch * 32);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                }
+            }
+            if (valid) {
+                const float lse2 = le == 0.f ? -INFINITY : m_used + log2f(le);
+                if (!w.whole) p.ws_lse[part] = lse2;
+                else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
+                if (odd_flag[piece % kFlags])
+                    add_odd_values<T, D>(p, w, h, klo, mask, w.whole ? out16 : nullptr, w.whole ? nullptr : out32);
+            }
+        }
+        if (dead) {
+            if (lane == 0) report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 5)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+template <typename T, int D, int PH>
+cudaError_t launch_heads(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                         int dev, cudaStream_t stream) {
+    static std::atomic<bool> attr_set[64];
+    return launch_tree_kernel<T, D>(tree_packed_kernel<T, D, PH>, kThreads, Pack<D, PH>::kSmem, attr_set, tq, tk, tv, p,
+                                    dev, stream);
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                         int dev, cudaStream_t stream) {
+    return p.heads_per_item == 4 ? launch_heads<T, D, 4>(tq, tk, tv, p, dev, stream)
+                                 : launch_heads<T, D, 2>(tq, tk, tv, p, dev, stream);
+}
+
+}  // namespace
+
+size_t tree_packed_smem(int head_dim) {
+    const size_t a = head_dim == 128 ? Pack<128, 4>::kSmem : Pack<64, 4>::kSmem;
+    const size_t b = head_dim == 128 ? Pack<128, 2>::kSmem : Pack<64, 2>::kSmem;
+    return a > b ? a : b;
+}
+
+cudaError_t launch_tree_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
+                               int head_dim, int q_dtype, int dev, cudaStream_t stream) {
+    if (q_dtype == KV_BF16)
+        return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(tq, tk, tv, p, dev, stream)
+                               : launch_typed<__nv_bfloat16, 64>(tq, tk, tv, p, dev, stream);
+    return head_dim == 128 ? launch_typed<__half, 128>(tq, tk, tv, p, dev, stream)
+                           : launch_typed<__half, 64>(tq, tk, tv, p, dev, stream);
+}
+
+}  // namespace pkv
