@@ -17,17 +17,19 @@
 // tile's scores are formed before O += P_h V_h when its keys are there, and after it when they are not.
 // For the work list, the masks, cleaned V tiles and bounded waits see tree_attention.cu.
 //
-// Warps (224 threads): 0-3 softmax (thread = TMEM lane = query row), 4 TMA producer, 5 issues the
-// MMAs, 6 cleans V tiles.
+// Warps: 0-3 softmax (thread = TMEM lane = query row), 4 TMA producer, 5 cleans V tiles, 6 .. issue the
+// MMAs, one warp (and of it one lane) a head: a commit takes the issuing thread some 120 clocks and a
+// wait about as much, so that one warp for all heads was the bound (6,400 clocks a key tile of 4 heads
+// and 64 dims, of which 2,050 on the tensor cores).
 #include "tree_common.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr int kThreads = 224;
 constexpr uint32_t kColP = 256, kColO = 384;
 
 template <int D, int PH> struct Pack {
+    static constexpr int kThreads = (6 + PH) * 32;
     static constexpr int kHalves = D / 64;
     static constexpr int kKeys = PH == 4 ? 64 : 128;         // keys of a key tile
     static constexpr int kLanes = kTreeRows / PH;            // lanes of a head
@@ -37,7 +39,7 @@ template <int D, int PH> struct Pack {
     static constexpr int kStages = D == 128 ? 3 : 6;         // ring entries (192 KB)
     static constexpr int kOffKV = kQBytes;
     static constexpr int kOffBar = kOffKV + kStages * kEntry;
-    static constexpr int kNumBars = 3 + 3 * PH + 2 * kStages;
+    static constexpr int kNumBars = 2 + 4 * PH + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM address, abort flag, flags, cleaned
     static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
     static_assert(kSmem + 128 <= 227 * 1024, "shared memory, with the kernel's static part");
@@ -45,13 +47,13 @@ template <int D, int PH> struct Pack {
 };
 
 template <typename T, int D, int PH>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__((6 + PH) * 32, 1)
 tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TreeParams p) {
     using PK = Pack<D, PH>;
     constexpr int kStages = PK::kStages, kKeys = PK::kKeys, kLanes = PK::kLanes;
-    constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarDrain = 2, kBarS = 3, kBarP = kBarS + PH, kBarPd = kBarP + PH,
-                  kBarFull = kBarPd + PH, kBarEmpty = kBarFull + kStages;
+    constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarS = 2, kBarP = kBarS + PH, kBarPd = kBarP + PH,
+                  kBarDrain = kBarPd + PH, kBarFull = kBarDrain + PH, kBarEmpty = kBarFull + kStages;
     const TreeArgs &a = p.a;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int g = p.group, TQ = p.tokens_per_tile, bs = a.block_size;
@@ -68,7 +70,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 
     __shared__ ShareStart start;
     int64_t x0, x1;
-    share_of_cta<kThreads>(p, c, x0, x1, start);
+    share_of_cta<PK::kThreads>(p, c, x0, x1, start);
     zero_rejected<T, D>(p);
     if (x0 == x1) {
         if (threadIdx.x == 0) p.ws_first[4 * c] = -1;
@@ -76,16 +78,16 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     }
     if (threadIdx.x == 0) {
         mbar_init(bar(kBarQFull), 1);
-        mbar_init(bar(kBarQEmpty), 1);
-        mbar_init(bar(kBarDrain), 1);
+        mbar_init(bar(kBarQEmpty), PH);
         for (int h = 0; h < PH; ++h) {
             mbar_init(bar(kBarS + h), 1);
             mbar_init(bar(kBarP + h), kLanes);
             mbar_init(bar(kBarPd + h), 1);
+            mbar_init(bar(kBarDrain + h), 1);
         }
         for (int s = 0; s < kStages; ++s) {
             mbar_init(bar(kBarFull + s), 1);
-            mbar_init(bar(kBarEmpty + s), 2);  // released by the MMA warp and the cleaning warp
+            mbar_init(bar(kBarEmpty + s), PH + 1);  // released by the MMA warps and the cleaning warp
         }
         *abort_flag = 0;
         for (int i = 0; i < kFlags; ++i) odd_flag[i] = 0;
@@ -198,103 +200,85 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int i = max(0, entry - kStages); i < entry; ++i)
                 if (!mbar_wait_sleep(bar(kBarFull + i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
         }
-    } else if (warp == 5) {
-        // ============================================================ MMA issue
-        // The whole warp runs the schedule (warp-uniform); one lane issues.
+    } else if (warp >= 6) {
+        // ============================================================ MMA issue, one lane a head
+        const int h = warp - 6;
         constexpr uint32_t ab = AbFormat<T>::value;
         constexpr uint32_t idesc_s = mma_idesc(ab, false, kTreeRows, kKeys);
         constexpr uint32_t idesc_pv = mma_idesc(ab, true, kTreeRows, D);
-        const uint64_t dq = smem_desc(smem_u32(smem), 16, 1024);
-        // one head's atoms (8 keys x 64 dims, 1 KB) are PH KB apart
-        const uint64_t dk0 = smem_desc(smem_u32(smem + PK::kOffKV), 16, PH * 1024);
-        const uint64_t dv0 = smem_desc(smem_u32(smem + PK::kOffKV), PK::kSide, PH * 1024);
-        const bool leader = lane == 0;
-        auto wait_warp = [&](uint32_t b, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity));
-        };
-        // scores of head h against the keys in ring entry e
-        auto scores = [&](int h, int e) {
-            const int sk = e % kStages;
-            const uint64_t dk = dk0 + static_cast<uint64_t>((sk * PK::kEntry + h * 1024) >> 4);
-            if (leader) {
+        if (lane == 0) {
+            const uint64_t dq = smem_desc(smem_u32(smem), 16, 1024);
+            // one head's atoms (8 keys x 64 dims, 1 KB) are PH KB apart
+            const uint32_t kv = smem_u32(smem + PK::kOffKV) + h * 1024;
+            const uint64_t dk0 = smem_desc(kv, 16, PH * 1024);
+            const uint64_t dv0 = smem_desc(kv, PK::kSide, PH * 1024);
+            const uint32_t t_s = tmem + h * kKeys, t_p = tmem + kColP + h * (kKeys / 2), t_o = tmem + kColO;
+            uint32_t off[4];  // the other heads' lanes
+#pragma unroll
+            for (int i = 0; i < 4; ++i) off[i] = i * 32 / kLanes == h ? 0u : 0xffffffffu;
+            // scores against the keys in ring entry e
+            auto scores = [&](int e) {
+                const int sk = e % kStages;
+                const uint64_t dk = dk0 + static_cast<uint64_t>((sk * PK::kEntry) >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
-                    mma_f16(tmem + h * kKeys, dq + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
+                    mma_f16(t_s, dq + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
                             dk + (((k >> 2) * PK::kSide + (k & 3) * 32) >> 4), idesc_s, k > 0);
                 mma_commit(bar(kBarS + h));
-                if (h == PH - 1) mma_commit(bar(kBarEmpty + sk));
-            }
-            __syncwarp();
-        };
-        int done = 0;  // key tiles of the pieces before
-        bool dead = false;
-        for (int piece = 0; !dead && w.next(p); ++piece) {
-            const Seq s = w.cur;
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-            if (!wait_warp(bar(kBarQFull), piece & 1) ||
-                !wait_warp(bar(kBarFull + 2 * done % kStages), (2 * done / kStages) & 1)) {
-                dead = true;
-                break;
-            }
-            tc_fence_after();
-            const int n = w.jb - w.ja;
-            for (int h = 0; h < PH; ++h) scores(h, 2 * done);
-            for (int t = 0; t < n; ++t, ++done) {
-                const int ev = 2 * done + 1, sv = ev % kStages, ek = ev + 1, sk = ek % kStages;
-                const bool more = t + 1 < n;
-                if (!more && leader) mma_commit(bar(kBarQEmpty));  // the piece's last scores have been issued
-                if (!wait_warp(bar(kBarFull + sv), (ev / kStages) & 1) ||
-                    (mixed_tile(p, s, w.ja + t) && !__all_sync(0xffffffffu, wait_at_least_bounded(&cleaned[sv], ev + 1)))) {
+                mma_commit(bar(kBarEmpty + sk));
+            };
+            auto full = [&](int e) { return mbar_wait_bounded(bar(kBarFull + e % kStages), (e / kStages) & 1); };
+            int done = 0;  // key tiles of the pieces before
+            bool dead = false;
+            for (int piece = 0; !dead && w.next(p); ++piece) {
+                const Seq s = w.cur;
+                if (*abort_flag != 0) break;
+                if (!mbar_wait_bounded(bar(kBarQFull), piece & 1) || !full(2 * done)) {
                     dead = true;
                     break;
                 }
-                bool keys = false;  // the next tile's keys are there
-                int ahead = 0;      // heads whose next scores have been issued
-                for (int h = 0; h < PH; ++h) {
-                    if (!wait_warp(bar(kBarP + h), done & 1)) {
+                tc_fence_after();
+                const int n = w.jb - w.ja;
+                scores(2 * done);
+                for (int t = 0; t < n; ++t, ++done) {
+                    const int ev = 2 * done + 1, sv = ev % kStages, ek = ev + 1;
+                    const bool more = t + 1 < n;
+                    if (!more) mma_commit(bar(kBarQEmpty));  // the piece's last scores have been issued
+                    if (!full(ev) ||
+                        (mixed_tile(p, s, w.ja + t) && !wait_at_least_bounded(&cleaned[sv], ev + 1)) ||
+                        !mbar_wait_bounded(bar(kBarP + h), done & 1)) {
                         dead = true;
                         break;
                     }
+                    const bool keys = more && mbar_test(bar(kBarFull + ek % kStages), (ek / kStages) & 1);
                     tc_fence_after();
-                    if (more && !keys) keys = __all_sync(0xffffffffu, mbar_test(bar(kBarFull + sk), (ek / kStages) & 1));
-                    if (keys) {
+                    if (keys) scores(ek);
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((sv * PK::kEntry) >> 4);
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_f16_ts_rows(t_o, t_p + k * 8, dv + ((k * PH * 2048) >> 4), idesc_pv, t > 0 || k > 0, off);
+                    mma_commit(bar(kBarPd + h));
+                    mma_commit(bar(kBarEmpty + sv));
+                    if (more && !keys) {
+                        if (!full(ek)) {
+                            dead = true;
+                            break;
+                        }
                         tc_fence_after();
-                        while (ahead <= h) scores(ahead++, ek);
+                        scores(ek);
                     }
-                    const uint64_t dv = dv0 + static_cast<uint64_t>((sv * PK::kEntry + h * 1024) >> 4);
-                    if (leader) {
-                        uint32_t off[4];
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) off[i] = i * 32 / kLanes == h ? 0u : 0xffffffffu;
-#pragma unroll
-                        for (int k = 0; k < kKeys / 16; ++k)
-                            mma_f16_ts_rows(tmem + kColO, tmem + kColP + h * (kKeys / 2) + k * 8,
-                                            dv + ((k * PH * 2048) >> 4), idesc_pv, t > 0 || k > 0, off);
-                        mma_commit(bar(kBarPd + h));
-                        if (h == PH - 1) mma_commit(bar(kBarEmpty + sv));
-                    }
-                    __syncwarp();
-                }
-                if (dead) break;
-                if (more && ahead < PH) {
-                    if (!keys && !wait_warp(bar(kBarFull + sk), (ek / kStages) & 1)) {
-                        dead = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    while (ahead < PH) scores(ahead++, ek);
                 }
             }
+            if (dead) {
+                report(a.d_err, KV_DERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every MMA this lane issued has completed before TMEM is freed
+            mma_commit(bar(kBarDrain + h));
+            if (!mbar_wait_bounded(bar(kBarDrain + h), 0)) report(a.d_err, KV_DERR_TIMEOUT);
         }
-        if (dead && leader) {
-            report(a.d_err, KV_DERR_TIMEOUT);
-            *abort_flag = 1;
-        }
-        // every MMA this warp issued has completed before TMEM is freed
-        if (leader) mma_commit(bar(kBarDrain));
         __syncwarp();
-        if (!wait_warp(bar(kBarDrain), 0) && leader) report(a.d_err, KV_DERR_TIMEOUT);
-    } else if (warp == 6) {
+    } else if (warp == 5) {
         // ============================================================ cleaning of V tiles
         int done = 0;
         bool dead = false;
@@ -544,7 +528,7 @@ template <typename T, int D, int PH>
 cudaError_t launch_heads(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
                          int dev, cudaStream_t stream) {
     static std::atomic<bool> attr_set[64];
-    return launch_tree_kernel<T, D>(tree_packed_kernel<T, D, PH>, kThreads, Pack<D, PH>::kSmem, attr_set, tq, tk, tv, p,
+    return launch_tree_kernel<T, D>(tree_packed_kernel<T, D, PH>, Pack<D, PH>::kThreads, Pack<D, PH>::kSmem, attr_set, tq, tk, tv, p,
                                     dev, stream);
 }
 
