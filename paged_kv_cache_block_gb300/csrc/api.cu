@@ -3,6 +3,7 @@
 // stream.  Nothing here allocates device memory or synchronises.
 #include <cudaTypedefs.h>
 
+#include <cfloat>
 #include <cmath>
 #include <cstdarg>
 #include <cstdio>
@@ -1259,7 +1260,8 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     a.num_blocks = num_blocks;
     a.max_seq_len = max_seq_len;
     a.window = window;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    // a scale of 0 (all weights alike) as the least normal number: the kernels mask with -inf * scale
+    a.scale_log2 = std::fmax(scale * 1.4426950408889634f, FLT_MIN);
     a.v_cache = v_cache;
     a.out = out;
     a.lse_out = lse_out;

@@ -92,7 +92,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     share_of_cta<kThreads>(p, c, x0, x1, start);
     zero_rejected<T, D>(p);
     if (x0 == x1) {
-        if (threadIdx.x == 0) p.ws_first[4 * c] = -1;
+        if (threadIdx.x == 0) p.ws_first[2 * c] = make_int4(-1, 0, 0, 0);
         return;
     }
     if (threadIdx.x == 0) {
@@ -144,11 +144,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         while (!stop && w.next(p)) {
             const Seq s = w.cur;
             const int h = w.item / s.pairs, pr = w.item - h * s.pairs, nt = row_tiles(p, s, pr);
-            if (piece == 0 && lane == 0) {
-                p.ws_first[4 * c] = w.seq;
-                p.ws_first[4 * c + 1] = w.item;
-                p.ws_first[4 * c + 2] = w.ja - s.j0;
-            }
+            if (piece == 0 && lane == 0) w.record(p, c);
             // block ids of key tile j: lane l holds block j * bpt + l
             const int nblk = (s.L - 1) / bs + 1, first_blk = s.kv_lo / bs;
             auto block_id = [&](int j) {
@@ -222,106 +218,91 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 if (!mbar_wait_sleep(bar_full(i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
         }
     } else if (warp == 9 || warp == 10) {
-        // ============================================================ MMA issue, one warp a chain
-        // The whole warp runs the schedule (warp-uniform); one lane issues.  Chain x, key tile by
-        // key tile: S_x once the product that read the columns it overwrites has completed; O_x
-        // once the softmax has written P_x and the V tile has landed (and been cleaned).  The other
-        // chain's tiles are released as soon as they have landed: everyone who waits for a ring
-        // entry passes all of them in order, so that no phase of its barrier can be mistaken.
+        // ============================================================ MMA issue, one lane a chain
+        // Chain x, key tile by key tile: S_x once the product that read the columns it overwrites has
+        // completed; O_x once the softmax has written P_x and the V tile has landed (and been
+        // cleaned).  The other chain's tiles are released as soon as they have landed: everyone who
+        // waits for a ring entry passes all of them in order, so that no phase of its barrier can be
+        // mistaken.
         const int x = warp - 9;
         constexpr uint32_t ab = AbFormat<T>::value;
         constexpr uint32_t idesc_s = mma_idesc(ab, false, kBM, kBN);
         constexpr uint32_t idesc_pv = mma_idesc(ab, true, kBM, D);
-        const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, 1024);
-        const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), kHalf, 1024);
-        const uint32_t t_s = tmem + x * 128, t_o = tmem + kColO + x * 128;
-        const bool leader = lane == 0;
-        auto wait_warp = [&](uint32_t b, uint32_t parity) {
-            return __all_sync(0xffffffffu, mbar_wait_bounded(b, parity));
-        };
-        int base = 0;                  // key tiles of the pieces before
-        int npv = 0;                   // products O_x committed
-        bool dead = false;
-        for (int piece = 0; !dead && w.next(p); ++piece) {
-            const Seq s = w.cur;
-            const int nt = row_tiles(p, s, w.item % s.pairs);
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-            if (!wait_warp(bar(kBarQFull), piece & 1)) {
-                dead = true;
-                break;
-            }
-            const uint64_t dq = smem_desc(smem_u32(smem + (nt == 2 ? x * kTileBytes : 0)), 16, 1024);
-            const int step = nt == 2 ? 1 : 2;
-            const int first = w.ja + (nt == 2 ? 0 : x);
-            if (first >= w.jb && leader) mbar_arrive(bar(kBarQEmpty));  // no tile for this chain
-            for (int j = w.ja; j < w.jb; ++j) {
-                const bool last = j + step >= w.jb;
-                const int ek = 2 * (base + j - w.ja), ev = ek + 1;
-                const int sk = ek % kStages, sv = ev % kStages;
-                if (nt == 1 && ((j - w.ja) & 1) != x) {
-                    bool landed = wait_warp(bar_full(sk), (ek / kStages) & 1);
-                    if (landed && leader) mbar_arrive(bar_empty(sk));
-                    landed = landed && wait_warp(bar_full(sv), (ev / kStages) & 1);
-                    if (landed && leader) mbar_arrive(bar_empty(sv));
-                    __syncwarp();
-                    if (!landed) {
+        if (lane == 0) {
+            const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, 1024);
+            const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), kHalf, 1024);
+            const uint32_t t_s = tmem + x * 128, t_o = tmem + kColO + x * 128;
+            auto full = [&](int e) { return mbar_wait_bounded(bar_full(e % kStages), (e / kStages) & 1); };
+            int base = 0;  // key tiles of the pieces before
+            int npv = 0;   // products O_x committed
+            bool dead = false;
+            for (int piece = 0; !dead && w.next(p); ++piece) {
+                const Seq s = w.cur;
+                const int nt = row_tiles(p, s, w.item % s.pairs);
+                if (*abort_flag != 0) break;
+                if (!mbar_wait_bounded(bar(kBarQFull), piece & 1)) {
+                    dead = true;
+                    break;
+                }
+                const uint64_t dq = smem_desc(smem_u32(smem + (nt == 2 ? x * kTileBytes : 0)), 16, 1024);
+                const int step = nt == 2 ? 1 : 2;
+                const int first = w.ja + (nt == 2 ? 0 : x);
+                if (first >= w.jb) mbar_arrive(bar(kBarQEmpty));  // no tile for this chain
+                for (int j = w.ja; j < w.jb; ++j) {
+                    const bool last = j + step >= w.jb;
+                    const int ek = 2 * (base + j - w.ja), ev = ek + 1;
+                    const int sk = ek % kStages, sv = ev % kStages;
+                    if (nt == 1 && ((j - w.ja) & 1) != x) {
+                        bool landed = full(ek);
+                        if (landed) mbar_arrive(bar_empty(sk));
+                        landed = landed && full(ev);
+                        if (landed) mbar_arrive(bar_empty(sv));
+                        if (!landed) {
+                            dead = true;
+                            break;
+                        }
+                        continue;
+                    }
+                    if ((npv > 0 && !mbar_wait_bounded(bar(kBarPd + x), (npv - 1) & 1)) || !full(ek)) {
                         dead = true;
                         break;
                     }
-                    continue;
-                }
-                if ((npv > 0 && !wait_warp(bar(kBarPd + x), (npv - 1) & 1)) ||
-                    !wait_warp(bar_full(sk), (ek / kStages) & 1)) {
-                    dead = true;
-                    break;
-                }
-                tc_fence_after();
-                {
+                    tc_fence_after();
                     const uint64_t dk = dkv + static_cast<uint64_t>((sk * kTileBytes) >> 4);
-                    if (leader) {
 #pragma unroll
-                        for (int k = 0; k < D / 16; ++k) {
-                            const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                            mma_f16(t_s, dq + off, dk + off, idesc_s, k > 0);
-                        }
-                        mma_commit(bar(kBarS + x));
-                        mma_commit(bar_empty(sk));
-                        if (last) mma_commit(bar(kBarQEmpty));
+                    for (int k = 0; k < D / 16; ++k) {
+                        const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
+                        mma_f16(t_s, dq + off, dk + off, idesc_s, k > 0);
                     }
-                    __syncwarp();
-                }
-                const bool mixed = mixed_tile(p, s, j);
-                if (!wait_warp(bar_full(sv), (ev / kStages) & 1) ||
-                    (mixed && !__all_sync(0xffffffffu, wait_at_least_bounded(&cleaned[sv], ev + 1))) ||
-                    !wait_warp(bar(kBarP + x), npv & 1)) {
-                    dead = true;
-                    break;
-                }
-                tc_fence_after();
-                {
+                    mma_commit(bar(kBarS + x));
+                    mma_commit(bar_empty(sk));
+                    if (last) mma_commit(bar(kBarQEmpty));
+                    if (!full(ev) || (mixed_tile(p, s, j) && !wait_at_least_bounded(&cleaned[sv], ev + 1)) ||
+                        !mbar_wait_bounded(bar(kBarP + x), npv & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
                     const uint64_t dv = dv0 + static_cast<uint64_t>((sv * kTileBytes) >> 4);
-                    if (leader) {
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2048) >> 4), idesc_pv, j > first || k > 0);
-                        mma_commit(bar_empty(sv));
-                        mma_commit(bar(kBarPd + x));
-                        if (last) mma_commit(bar(kBarPv + x));
-                    }
-                    __syncwarp();
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2048) >> 4), idesc_pv, j > first || k > 0);
+                    mma_commit(bar(kBarPd + x));
+                    mma_commit(bar_empty(sv));
+                    if (last) mma_commit(bar(kBarPv + x));
+                    ++npv;
                 }
-                ++npv;
+                base += w.jb - w.ja;
             }
-            base += w.jb - w.ja;
+            if (dead) {
+                report(a.d_err, KV_DERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every MMA this lane issued has completed before TMEM is freed
+            mma_commit(bar(kBarDrain + x));
+            if (!mbar_wait_bounded(bar(kBarDrain + x), 0)) report(a.d_err, KV_DERR_TIMEOUT);
         }
-        if (dead && leader) {
-            report(a.d_err, KV_DERR_TIMEOUT);
-            *abort_flag = 1;
-        }
-        // every MMA this warp issued has completed before TMEM is freed
-        if (leader) mma_commit(bar(kBarDrain + x));
         __syncwarp();
-        if (!wait_warp(bar(kBarDrain + x), 0) && leader) report(a.d_err, KV_DERR_TIMEOUT);
     } else if (warp == 11) {
         // ============================================================ cleaning of V tiles
         int base = 0;
@@ -409,48 +390,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             const int step = nt == 2 ? 1 : 2;
             const int first = w.ja + (nt == 2 ? 0 : x);
             uint32_t wt[64];
-            // One pass over the tile's S: weights against the reference in use, the tile maximum
-            // tracked alongside, 32 columns at a time with the next load in flight.
-            auto weights = [&](auto masked_tag, int kbase, float nref, float &mraw, float2 &tr, float2 &te) {
-                constexpr bool masked = decltype(masked_tag)::value;
-                const float2 rr = make_float2(nref, nref);
-                uint32_t ra[32], rb[32];
-                auto chunk = [&](const uint32_t (&v)[32], int ch) {
-                    uint32_t seen = 0xffffffffu;
-                    if constexpr (masked) seen = valid ? seen32(kbase + ch * 32, s.ctx, klo, mask) : 0u;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
-                        const float2 e = fma2(make_float2(s0, s1), cc, rr);
-                        float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-                        if constexpr (masked) {
-                            const bool v0 = (seen >> (2 * k)) & 1, v1 = (seen >> (2 * k + 1)) & 1;
-                            e0 = v0 ? e0 : 0.f;
-                            e1 = v1 ? e1 : 0.f;
-                            mraw = fmaxf(mraw, fmaxf(v0 ? s0 : -INFINITY, v1 ? s1 : -INFINITY));
-                        } else {
-                            mraw = fmaxf(mraw, fmaxf(s0, s1));
-                        }
-                        wt[ch * 16 + k] = pack2<T>(e0, e1);
-                        te = add2(te, make_float2(e0, e1));
-                        tr = add2(tr, unpack2<T>(wt[ch * 16 + k]));
-                    }
-                };
-                mraw = -INFINITY;
-                tr = te = make_float2(0.f, 0.f);
-                tmem_ld32_async(t_s, ra);
-                tmem_wait_regs(ra);
-                tmem_ld32_async(t_s + 32, rb);
-                chunk(ra, 0);
-                tmem_wait_regs(rb);
-                tmem_ld32_async(t_s + 64, ra);
-                chunk(rb, 1);
-                tmem_wait_regs(ra);
-                tmem_ld32_async(t_s + 96, rb);
-                chunk(ra, 2);
-                tmem_wait_regs(rb);
-                chunk(rb, 3);
-            };
             for (int j = first; j < w.jb; j += step) {
                 if (!wait_all(bar(kBarS + x), ns & 1)) {
                     dead = true;
@@ -459,19 +398,46 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 ++ns;
                 tc_fence_after();
                 if (warp_valid) {  // (a warp without rows leaves its lanes of P as they are)
-                    const int kbase = j * kBN;
                     const bool masked = mixed_tile(p, s, j);
-                    float mraw;
                     float2 tr, te;
-                    auto run_weights = [&](float nref, float &mx) {
-                        if (masked) weights(std::true_type{}, kbase, nref, mx, tr, te);
-                        else weights(std::false_type{}, kbase, nref, mx, tr, te);
-                    };
-                    run_weights(m_used == -INFINITY ? 0.f : -m_used, mraw);
-                    // scale >= 0, so the scaled maximum is the maximum of the scaled scores
-                    const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
-                    const bool moved = valid && mt > m_used + kRescaleLog2;  // also the first finite maximum
-                    if (__any_sync(0xffffffffu, moved)) {
+                    // One pass over the tile's S: weights against the reference in use, the tile maximum
+                    // tracked alongside, 32 columns at a time with the next load in flight.  A second one
+                    // when the reference has to move.  (One copy of the code: a CTA's first tile pays for
+                    // fetching it.)
+#pragma unroll 1
+                    for (bool again = false;; again = true) {
+                        const float nref = m_used == -INFINITY ? 0.f : -m_used;
+                        const float2 ref2 = make_float2(nref, nref);
+                        float mraw = -INFINITY;
+                        tr = te = make_float2(0.f, 0.f);
+                        uint32_t buf[2][32];
+                        tmem_ld32_async(t_s, buf[0]);
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t(&v)[32] = buf[ch & 1];
+                            tmem_wait_regs(v);
+                            if (ch < 3) tmem_ld32_async(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
+                            if (masked) {  // (scale > 0: an unseen score of -inf gets weight 0)
+                                const uint32_t seen = valid ? seen32(j * kBN + ch * 32, s.ctx, klo, mask) : 0u;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1 ? v[k] : 0xff800000u;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
+                                const float2 e = fma2(make_float2(s0, s1), cc, ref2);
+                                const float2 x2 = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                                mraw = fmaxf(mraw, fmaxf(s0, s1));
+                                wt[ch * 16 + k] = pack2<T>(x2.x, x2.y);
+                                te = add2(te, x2);
+                                tr = add2(tr, unpack2<T>(wt[ch * 16 + k]));
+                            }
+                        }
+                        if (again) break;
+                        // scale > 0, so the scaled maximum is the maximum of the scaled scores
+                        const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
+                        const bool moved = valid && mt > m_used + kRescaleLog2;  // also the first finite maximum
+                        if (!__any_sync(0xffffffffu, moved)) break;
                         const bool rescale = moved && m_used != -INFINITY;  // O and the sums hold earlier tiles
                         const float f = moved ? fast_exp2(m_used - mt) : 1.f;
                         if (moved) {
@@ -492,8 +458,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                             }
                             tmem_wait_st();
                         }
-                        float m2;
-                        run_weights(m_used == -INFINITY ? 0.f : -m_used, m2);
                     }
                     rsum = add2(rsum, tr);
                     esum = add2(esum, te);
@@ -631,7 +595,7 @@ TreePlan plan_tree(int max_query_len, int group, int num_kv_heads, int head_dim,
     t.key_shift = t.heads_per_item == 4 ? 6 : 7;
     t.rows_per_item = t.heads_per_item == 1 && max_query_len > t.tokens_per_tile ? 2 * kTreeRows : kTreeRows;
     const size_t parts = static_cast<size_t>(2) * t.workers * t.rows_per_item;
-    t.lse_off = align256(16 * static_cast<size_t>(t.workers));
+    t.lse_off = align256(2 * sizeof(int4) * static_cast<size_t>(t.workers));
     t.o_off = t.lse_off + align256(4 * parts);
     t.workspace_bytes = t.o_off + 4 * parts * head_dim;
     t.smem_bytes = t.heads_per_item > 1 ? tree_packed_smem(head_dim) : (head_dim == 128 ? Tile<128>::kSmem : Tile<64>::kSmem);
@@ -650,7 +614,7 @@ cudaError_t launch_tree_attention(const CUtensorMap &tq, const CUtensorMap &tk, 
     p.workers = plan.workers;
     p.rows_per_item = plan.rows_per_item;
     char *ws = static_cast<char *>(workspace);
-    p.ws_first = reinterpret_cast<int32_t *>(ws);
+    p.ws_first = reinterpret_cast<int4 *>(ws);
     p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_off);
     p.ws_o = reinterpret_cast<float *>(ws + plan.o_off);
     if (p.heads_per_item > 1) return launch_tree_packed(tq, tk, tv, p, head_dim, q_dtype, dev, stream);

@@ -17,7 +17,7 @@ constexpr int kHalf = 128 * 128;       // 128 rows x 64 16-bit elements (one swi
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;   // a row's reference maximum moves when exceeded by more
 constexpr int kItemCost = 2;           // an item's fixed cost in key tiles
-constexpr int kMinShare = 4;           // least cost of a share: more than kItemCost, so that it holds a tile
+constexpr int kMinShare = 3;           // least cost of a share: more than kItemCost, so that it holds a tile
 constexpr int kFlags = 8;              // pieces whose odd-value flags are kept
 
 struct TreeParams {
@@ -28,7 +28,8 @@ struct TreeParams {
     int key_shift;        // log2 of the keys of a key tile
     int workers;          // shares at most
     int rows_per_item;    // rows of a partial result
-    int32_t *ws_first;    // [workers][4] first piece of each share: sequence, item of it, key tile, -
+    int4 *ws_first;       // [2 * workers] first piece of each share: (sequence, item of it, key tile of it,
+                          // -), (first row, rows, -, -) of the sequence; sequence -1: no share
     float *ws_lse;        // [2 * workers][rows_per_item] log2-sum-exp2 of the partial results
     float *ws_o;          // [2 * workers][rows_per_item][D] partial results, normalised
 };
@@ -147,44 +148,45 @@ template <typename T, int D> __device__ __forceinline__ void zero_rejected(const
 
 // The pieces of a share, in order: (item, key tiles ja .. jb - 1).  Every warp walks the same ones.
 struct Walk {
-    int b, idx;       // sequence, item of it (the next piece's)
     int64_t at;       // cost where the item starts
     int64_t x0, x1;   // the share
-    Seq s;
-    // the piece
-    Seq cur;
-    int seq, item, ja, jb;  // sequence, item of it, key tiles (absolute)
-    bool whole;             // it is its whole item
+    Seq cur;          // the piece's sequence,
+    int seq, item;    // its number, the item of it
+    int ja, jb;       // and key tiles (absolute)
+    bool whole;       // the piece is its whole item
+    bool begun;
 
     __device__ __forceinline__ void start(const TreeParams &p, const ShareStart &st, int64_t x0_, int64_t x1_) {
-        b = st.b, idx = st.idx, at = st.at, x0 = x0_, x1 = x1_;
+        seq = st.b, item = st.idx, at = st.at, x0 = x0_, x1 = x1_;
+        begun = false;
         bool rejected;
-        load_seq(p, b, s, &rejected);
+        load_seq(p, seq, cur, &rejected);
     }
     __device__ __forceinline__ bool next(const TreeParams &p) {
-        while (at < x1) {
+        for (;;) {
+            if (begun) {  // on to the next item
+                at += kItemCost + cur.tiles;
+                if (at >= x1) return false;
+                if (++item == cur.items) {
+                    item = 0;
+                    bool rejected = false;
+                    do {
+                        if (++seq >= p.a.num_seqs) return false;
+                    } while (!load_seq(p, seq, cur, &rejected));
+                }
+            }
+            begun = true;
             const int64_t first = at + kItemCost;
-            ja = static_cast<int>(max(int64_t(0), x0 - first));
-            jb = static_cast<int>(min(static_cast<int64_t>(s.tiles), x1 - first));
-            const bool some = ja < jb;
-            if (some) {
-                ja += s.j0;
-                jb += s.j0;
-                whole = ja == s.j0 && jb == s.j0 + s.tiles;
-                seq = b;
-                item = idx;
-                cur = s;
-            }
-            at = first + s.tiles;
-            if (++idx == s.items) {
-                idx = 0;
-                bool rejected = false;
-                while (++b < p.a.num_seqs && !load_seq(p, b, s, &rejected)) {}
-                if (b >= p.a.num_seqs) x1 = at;  // the end of the list
-            }
-            if (some) return true;
+            ja = static_cast<int>(max(int64_t(0), x0 - first)) + cur.j0;
+            jb = static_cast<int>(min(static_cast<int64_t>(cur.tiles), x1 - first)) + cur.j0;
+            whole = ja == cur.j0 && jb == cur.j0 + cur.tiles;
+            if (ja < jb) return true;
         }
-        return false;
+    }
+    // The share's first piece, for the merge.
+    __device__ __forceinline__ void record(const TreeParams &p, int c) const {
+        p.ws_first[2 * c] = make_int4(seq, item, ja - cur.j0, 0);
+        p.ws_first[2 * c + 1] = make_int4(cur.q0, cur.n, cur.pairs, 0);
     }
 };
 
@@ -283,81 +285,97 @@ __device__ __forceinline__ void add_odd_values(const TreeParams &p, const Walk &
 }
 
 // Join the partial results of the item that starts in share c and goes on into the next ones: one
-// warp a row.  out = sum_i w_i o_i / sum_i w_i, w_i = exp2(lse_i - max).
+// warp a row.  out = sum_i w_i o_i / sum_i w_i, w_i = exp2(lse_i - max).  What it costs is dependent
+// round trips: the shares' records, then the lse and the first four partial rows at once.
 template <typename T, int D>
 static __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     constexpr int E = D / 32;
     const TreeArgs &a = p.a;
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int rr = blockIdx.y * 8 + (threadIdx.x >> 5);
-    // the next share's first piece: where it starts decides whether this share's last item goes on
-    const int b = p.ws_first[4 * (c + 1)], idx = p.ws_first[4 * (c + 1) + 1], k = p.ws_first[4 * (c + 1) + 2];
-    if (b < 0 || k == 0) return;
-    if (p.ws_first[4 * c] == b && p.ws_first[4 * c + 1] == idx && p.ws_first[4 * c + 2] > 0) return;  // it started before
-    Seq s;
-    bool rejected;
-    load_seq(p, b, s, &rejected);
+    // lane i: the first piece of share c + i (none past the last)
+    const int4 none = make_int4(-1, 0, 0, 0);
+    int4 rec = c + lane < p.workers ? p.ws_first[2 * (c + lane)] : none;
+    const int4 sq = p.ws_first[2 * (c + 1) + 1];
+    // share c + 1's decides whether c's last item goes on; c's own, whether that item started before
+    const int b = __shfl_sync(0xffffffffu, rec.x, 1), idx = __shfl_sync(0xffffffffu, rec.y, 1);
+    const bool same = rec.x == b && rec.y == idx && rec.z > 0;  // this share goes on with the item
+    uint32_t go = __ballot_sync(0xffffffffu, same);
+    if (b < 0 || !(go & 2) || (go & 1)) return;
     // the row's kv head, token and head of the group
     int h, t, hh;
     const int TQ = p.tokens_per_tile;
     if (p.heads_per_item == 1) {
-        h = idx / s.pairs;
+        h = idx / sq.z;
         const int r = rr & 127, tl = r / p.group;
-        t = (2 * (idx - h * s.pairs) + (rr >> 7)) * TQ + tl;
+        t = (2 * (idx - h * sq.z) + (rr >> 7)) * TQ + tl;
         hh = r - tl * p.group;
-        if (tl >= TQ || t >= s.n) return;
+        if (tl >= TQ || t >= sq.y) return;
     } else {
         const int lanes = kTreeRows / p.heads_per_item, r = rr % lanes;
         h = idx * p.heads_per_item + rr / lanes;
         t = r / p.group;
         hh = r - t * p.group;
-        if (h >= a.num_kv_heads || t >= s.n) return;
+        if (h >= a.num_kv_heads || t >= sq.y) return;
     }
-    // pieces: share c (its last: slot 2c + 1), then c + 1 .. (their first: slot 2c') while they
-    // start inside the item
-    int last = c + 1;
-    while (last + 1 < p.workers && p.ws_first[4 * (last + 1)] == b && p.ws_first[4 * (last + 1) + 1] == idx &&
-           p.ws_first[4 * (last + 1) + 2] > 0)
-        ++last;
+    // pieces: share c's (its last: slot 2c + 1), then those of the next shares (their first: 2c')
+    int last = c + __ffs(~(go | 1)) - 2;  // (ffs 0: all 32 go on)
+    if (~(go | 1) == 0) last = c + 31;
+    while (last >= c + 31) {
+        const int e = last + 1 + lane;
+        rec = e < p.workers ? p.ws_first[2 * e] : none;
+        go = __ballot_sync(0xffffffffu, rec.x == b && rec.y == idx && rec.z > 0);
+        if (go == 0xffffffffu) {
+            last += 32;
+            continue;
+        }
+        last += __ffs(~go) - 1;
+        break;
+    }
     auto part = [&](int e) { return part_row(p, e, e == c, rr); };
-    float mx = -INFINITY;
-    bool nan = false;
-    for (int e = c + lane; e <= last; e += 32) {
-        const float l = p.ws_lse[part(e)];
-        nan |= l != l;
-        mx = fmaxf(mx, l);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-    nan = __any_sync(0xffffffffu, nan);
-    float acc[E], wsum = 0.f;
+    float acc[E], wsum = 0.f, mx = -INFINITY;
 #pragma unroll
     for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    if (mx != -INFINITY || nan) {
-        for (int base = c; base <= last; base += 32) {
-            const float l = base + lane <= last ? p.ws_lse[part(base + lane)] : -INFINITY;
-            const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
-            const int cnt = min(32, last - base + 1);
-            for (int u0 = 0; u0 < cnt; u0 += 4) {
-                float wu[4], v[4][E];
+    for (int base = c; base <= last; base += 32) {
+        const int cnt = min(32, last - base + 1);
+        const float l = lane < cnt ? p.ws_lse[part(base + lane)] : -INFINITY;
+        float v[4][E];
+        auto load = [&](int u0) {
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    wu[u] = u0 + u < cnt ? __shfl_sync(0xffffffffu, wl, (u0 + u) & 31) : 0.f;
-                    const float *src = p.ws_o + part(base + u0 + u) * D + lane * E;
+            for (int u = 0; u < 4; ++u) {
+                const float *src = p.ws_o + part(base + u0 + u) * D + lane * E;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) v[u][e] = wu[u] != 0.f ? __ldcg(src + e) : 0.f;
-                }
+                for (int e = 0; e < E; ++e) v[u][e] = u0 + u < cnt ? __ldcg(src + e) : 0.f;
+            }
+        };
+        load(0);
+        float m = l;
 #pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    wsum += wu[u];
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const bool nan = __any_sync(0xffffffffu, l != l);
+        const float mn = fmaxf(mx, m);
+        if (mn == -INFINITY && !nan) continue;  // nothing seen so far
+        const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - mn);
+        mx = mn;
+        wsum *= f;
 #pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += wu[u] != 0.f ? wu[u] * v[u][e] : 0.f;
+        for (int e = 0; e < E; ++e) acc[e] *= f;
+        const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
+        for (int u0 = 0; u0 < cnt; u0 += 4) {
+            if (u0) load(u0);
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const float wu = __shfl_sync(0xffffffffu, wl, (u0 + u) & 31);
+                if (u0 + u < cnt && wu != 0.f) {  // a piece of weight 0 adds nothing, whatever it holds
+                    wsum += wu;
+#pragma unroll
+                    for (int e = 0; e < E; ++e) acc[e] += wu * v[u][e];
                 }
             }
         }
     }
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    const int64_t row = static_cast<int64_t>(s.q0 + t) * a.num_q_heads + h * p.group + hh;
+    const int64_t row = static_cast<int64_t>(sq.x + t) * a.num_q_heads + h * p.group + hh;
     uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + row * D + lane * E);
 #pragma unroll
     for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);

@@ -73,7 +73,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     share_of_cta<PK::kThreads>(p, c, x0, x1, start);
     zero_rejected<T, D>(p);
     if (x0 == x1) {
-        if (threadIdx.x == 0) p.ws_first[4 * c] = -1;
+        if (threadIdx.x == 0) p.ws_first[2 * c] = make_int4(-1, 0, 0, 0);
         return;
     }
     if (threadIdx.x == 0) {
@@ -122,11 +122,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         while (!stop && w.next(p)) {
             const Seq s = w.cur;
             const int h0 = w.item * PH;
-            if (piece == 0 && lane == 0) {
-                p.ws_first[4 * c] = w.seq;
-                p.ws_first[4 * c + 1] = w.item;
-                p.ws_first[4 * c + 2] = w.ja - s.j0;
-            }
+            if (piece == 0 && lane == 0) w.record(p, c);
             // block ids of key tile j: lane l holds block j * bpt + l
             const int nblk = (s.L - 1) / bs + 1, first_blk = s.kv_lo / bs;
             auto block_id = [&](int j) {
@@ -372,41 +368,6 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             float2 rsum = make_float2(0.f, 0.f);  // sum of the rounded weights (what the product uses)
             float2 esum = make_float2(0.f, 0.f);  // sum of the weights (log-sum-exp)
             uint32_t wt[kKeys / 2];
-            // One pass over the tile's S: weights against the reference in use, the tile maximum
-            // tracked alongside, 32 columns at a time with the next load in flight.
-            auto weights = [&](auto masked_tag, int kbase, float nref, float &mraw, float2 &tr, float2 &te) {
-                constexpr bool masked = decltype(masked_tag)::value;
-                const float2 ref2 = make_float2(nref, nref);
-                uint32_t buf[2][32];
-                mraw = -INFINITY;
-                tr = te = make_float2(0.f, 0.f);
-                tmem_ld32_async(t_s, buf[0]);
-#pragma unroll
-                for (int ch = 0; ch < kKeys / 32; ++ch) {
-                    uint32_t(&v)[32] = buf[ch & 1];
-                    tmem_wait_regs(v);
-                    if (ch + 1 < kKeys / 32) tmem_ld32_async(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
-                    uint32_t seen = 0xffffffffu;
-                    if constexpr (masked) seen = valid ? seen32(kbase + ch * 32, s.ctx, klo, mask) : 0u;
-#pragma unroll
-                    for (int k = 0; k < 16; ++k) {
-                        const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
-                        const float2 e = fma2(make_float2(s0, s1), cc, ref2);
-                        float e0 = fast_exp2(e.x), e1 = fast_exp2(e.y);
-                        if constexpr (masked) {
-                            const bool v0 = (seen >> (2 * k)) & 1, v1 = (seen >> (2 * k + 1)) & 1;
-                            e0 = v0 ? e0 : 0.f;
-                            e1 = v1 ? e1 : 0.f;
-                            mraw = fmaxf(mraw, fmaxf(v0 ? s0 : -INFINITY, v1 ? s1 : -INFINITY));
-                        } else {
-                            mraw = fmaxf(mraw, fmaxf(s0, s1));
-                        }
-                        wt[ch * 16 + k] = pack2<T>(e0, e1);
-                        te = add2(te, make_float2(e0, e1));
-                        tr = add2(tr, unpack2<T>(wt[ch * 16 + k]));
-                    }
-                }
-            };
             for (int j = w.ja; j < w.jb; ++j) {
                 if (!wait_all(bar(kBarS + hi), done & 1)) {
                     dead = true;
@@ -414,24 +375,51 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 }
                 tc_fence_after();
                 if (warp_valid) {
-                    const int kbase = j * kKeys;
                     const bool masked = mixed_tile(p, s, j);
-                    float mraw;
                     float2 tr, te;
-                    auto run_weights = [&](float nref, float &mx) {
-                        if (masked) weights(std::true_type{}, kbase, nref, mx, tr, te);
-                        else weights(std::false_type{}, kbase, nref, mx, tr, te);
-                    };
-                    run_weights(m_used == -INFINITY ? 0.f : -m_used, mraw);
-                    // scale >= 0, so the scaled maximum is the maximum of the scaled scores
-                    const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
-                    const bool moved = valid && mt > m_used + kRescaleLog2;  // also the first finite maximum
-                    const bool any_moved = __any_sync(0xffffffffu, moved);
-                    if (!settled()) {
-                        dead = true;
-                        break;
-                    }
-                    if (any_moved) {
+                    // One pass over the tile's S: weights against the reference in use, the tile maximum
+                    // tracked alongside, 32 columns at a time with the next load in flight.  A second one
+                    // when the reference has to move.  (One copy of the code: a CTA's first tile pays for
+                    // fetching it.)
+#pragma unroll 1
+                    for (bool again = false;; again = true) {
+                        const float nref = m_used == -INFINITY ? 0.f : -m_used;
+                        const float2 ref2 = make_float2(nref, nref);
+                        float mraw = -INFINITY;
+                        tr = te = make_float2(0.f, 0.f);
+                        uint32_t buf[2][32];
+                        tmem_ld32_async(t_s, buf[0]);
+#pragma unroll
+                        for (int ch = 0; ch < kKeys / 32; ++ch) {
+                            uint32_t(&v)[32] = buf[ch & 1];
+                            tmem_wait_regs(v);
+                            if (ch + 1 < kKeys / 32) tmem_ld32_async(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
+                            if (masked) {  // (scale > 0: an unseen score of -inf gets weight 0)
+                                const uint32_t seen = valid ? seen32(j * kKeys + ch * 32, s.ctx, klo, mask) : 0u;
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1 ? v[k] : 0xff800000u;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
+                                const float2 e = fma2(make_float2(s0, s1), cc, ref2);
+                                const float2 x = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                                mraw = fmaxf(mraw, fmaxf(s0, s1));
+                                wt[ch * 16 + k] = pack2<T>(x.x, x.y);
+                                te = add2(te, x);
+                                tr = add2(tr, unpack2<T>(wt[ch * 16 + k]));
+                            }
+                        }
+                        if (again) break;
+                        // scale > 0, so the scaled maximum is the maximum of the scaled scores
+                        const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
+                        const bool moved = valid && mt > m_used + kRescaleLog2;  // also the first finite maximum
+                        const bool any_moved = __any_sync(0xffffffffu, moved);
+                        if (!settled()) {
+                            dead = true;
+                            break;
+                        }
+                        if (!any_moved) break;
                         const bool rescale = moved && m_used != -INFINITY;  // O and the sums hold earlier tiles
                         const float f = moved ? fast_exp2(m_used - mt) : 1.f;
                         if (moved) {
@@ -453,9 +441,8 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             }
                             tmem_wait_st();
                         }
-                        float m2;
-                        run_weights(m_used == -INFINITY ? 0.f : -m_used, m2);
                     }
+                    if (dead) break;
                     rsum = add2(rsum, tr);
                     esum = add2(esum, te);
                     tmem_st32u(t_p, wt);
