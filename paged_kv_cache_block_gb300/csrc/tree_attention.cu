@@ -583,22 +583,26 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-// Several kv heads side by side when their rows fit 32 or 64 lanes each: larger copies (a TMA box
-// of 2 KB, one head of 16 tokens, moves 13 B a clock and SM, one of 4 heads 32) and all lanes in
-// use.  Wider trees, and fewer kv heads than lanes for them, take the kernel of this file.
+// Trees of up to 128 rows a kv head go by groups of heads (tree_packed.cu, which has the times of both),
+// four at a time where the rows fit 32 lanes; wider ones, and a single kv head, take the kernel of this
+// file.
 TreePlan plan_tree(int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count) {
     TreePlan t;
     const int rows = max_query_len * group;
-    t.heads_per_item = rows <= 32 && num_kv_heads >= 3 ? 4 : (rows <= 64 && num_kv_heads >= 2 ? 2 : 1);
+    t.heads_per_item = num_kv_heads == 1 || rows > kTreeRows ? 1 : (rows <= 32 && num_kv_heads >= 3 ? 4 : 2);
     t.workers = num_workers > 0 ? num_workers : sm_count;
-    t.tokens_per_tile = kTreeRows / t.heads_per_item / group;
-    t.key_shift = t.heads_per_item == 4 ? 6 : 7;
-    t.rows_per_item = t.heads_per_item == 1 && max_query_len > t.tokens_per_tile ? 2 * kTreeRows : kTreeRows;
+    if (t.heads_per_item > 1) {
+        plan_tree_packed(t, rows, group, head_dim);
+    } else {
+        t.tokens_per_tile = kTreeRows / group;
+        t.key_shift = 7;
+        t.rows_per_item = max_query_len > t.tokens_per_tile ? 2 * kTreeRows : kTreeRows;
+        t.smem_bytes = head_dim == 128 ? Tile<128>::kSmem : Tile<64>::kSmem;
+    }
     const size_t parts = static_cast<size_t>(2) * t.workers * t.rows_per_item;
     t.lse_off = align256(2 * sizeof(int4) * static_cast<size_t>(t.workers));
     t.o_off = t.lse_off + align256(4 * parts);
     t.workspace_bytes = t.o_off + 4 * parts * head_dim;
-    t.smem_bytes = t.heads_per_item > 1 ? tree_packed_smem(head_dim) : (head_dim == 128 ? Tile<128>::kSmem : Tile<64>::kSmem);
     return t;
 }
 

@@ -24,7 +24,7 @@ struct TreeParams {
     TreeArgs a;
     int group;            // query heads of a kv head
     int tokens_per_tile;  // drafted tokens of a kv head's rows in a row tile
-    int heads_per_item;   // 1: items of two row tiles of a kv head; 2 or 4: kv heads side by side in one
+    int heads_per_item;   // 1: items of two row tiles of a kv head; 2 or 4: of so many kv heads
     int key_shift;        // log2 of the keys of a key tile
     int workers;          // shares at most
     int rows_per_item;    // rows of a partial result
@@ -312,7 +312,7 @@ static __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_con
         hh = r - tl * p.group;
         if (tl >= TQ || t >= sq.y) return;
     } else {
-        const int lanes = kTreeRows / p.heads_per_item, r = rr % lanes;
+        const int lanes = p.rows_per_item / p.heads_per_item, r = rr % lanes;
         h = idx * p.heads_per_item + rr / lanes;
         t = r / p.group;
         hh = r - t * p.group;
@@ -401,9 +401,10 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
     return cudaGetLastError();
 }
 
-// Items of several kv heads side by side (tree_packed.cu).
+// Items of several kv heads (tree_packed.cu): the plan for `rows` query rows a head (heads_per_item
+// set), and the launch.
+void plan_tree_packed(TreePlan &t, int rows, int group, int head_dim);
 cudaError_t launch_tree_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
                                int head_dim, int q_dtype, int dev, cudaStream_t stream);
-size_t tree_packed_smem(int head_dim);
 
 }  // namespace pkv

@@ -1,57 +1,68 @@
-// Tree attention for small trees: several kv heads of a sequence side by side in one 128-row tile.
+// Tree attention, two or four kv heads of a sequence at a time.
 //
-// When a kv head has at most 32 (64) query rows, four (two) heads share the 128 TMEM lanes: lanes
-// 32 h .. belong to head h of the item's group.  Reading the cache is the bound then, and one head
-// at a time cannot read it fast enough: a TMA box of 16 tokens of one head and 64 dims (2 KB) costs
-// about 130 clocks plus two a row, 13 bytes a clock and SM, where HBM gives 23; a box of two heads
-// moves 21, of four 32.  The tensor map splits tokens into groups of 8 so that a box lands as
-// [group of 8 tokens][head][token][64 dims]: the swizzle atoms of one head lie a constant distance
-// apart over all blocks of a key tile, which is what a matrix descriptor can say.
+// Reading the cache bounds small trees, and one head at a time cannot read it fast enough: a TMA box
+// of 16 tokens of one head and 64 dims (2 KB) costs about 130 clocks plus two a row, 13 bytes a
+// clock and SM, where HBM gives 23; a box of two heads moves 21, of four 32.  The tensor map splits
+// tokens into groups of 8 so that a box lands as [group of 8 tokens][head][token][64 dims]: the
+// swizzle atoms of one head lie a constant distance apart over all blocks of a key tile, which is
+// what a matrix descriptor can say.
 //
-// Per key tile (64 keys of four heads, or 128 of two: 64 KB of K and of V at 128 dims) and head h:
+// Heads of at most 32 (64) query rows share the 128 TMEM lanes of one row tile, four (two) of them,
+// lanes 32 h .. those of head h.  Heads of up to 128 rows have a row tile each, two at a time.  (38
+// sequences of 8000 tokens and 32/8 heads of 128 dims: 201 us for 28 rows a head, 216 for 64, 250 for
+// 128, where one head at a time took 269, 308 and 363; at 256 rows two row tiles of one head take 405
+// and two heads a row tile 505, so that wider trees stay with tree_attention.cu.)
+//
+// Per key tile and head h (key tiles of 64 or 128 keys: 32 or 64 KB of K and of V):
 //   S_h = Q K_h^T    all 128 rows, of which the lanes of head h are read
 //   P_h = exp2(S_h * scale - m)    one thread a row; P_h has TMEM columns of its own
-//   O  += P_h V_h    for the lanes of head h alone (the other lanes are switched off), so the
-//                    heads' results share the columns of O
-// TMEM: S 256 columns, P 128, O 64 or 128.  S_h is free as soon as the softmax has read it, so the next
-// tile's scores are formed before O += P_h V_h when its keys are there, and after it when they are not.
+//   O  += P_h V_h    for the lanes of head h alone (the other lanes are switched off), so that
+//                    heads that share a row tile share the columns of O
+// S_h is free as soon as the softmax has read it, so the next tile's scores are formed before
+// O += P_h V_h when its keys are there, and after it when they are not.
 // For the work list, the masks, cleaned V tiles and bounded waits see tree_attention.cu.
 //
-// Warps: 0-3 softmax (thread = TMEM lane = query row), 4 TMA producer, 5 cleans V tiles, 6 .. issue the
-// MMAs, one warp (and of it one lane) a head: a commit takes the issuing thread some 120 clocks and a
-// wait about as much, so that one warp for all heads was the bound (6,400 clocks a key tile of 4 heads
-// and 64 dims, of which 2,050 on the tensor cores).
+// Warps: 0 .. softmax, four a row tile (thread = TMEM lane = query row), then a TMA producer, one that
+// cleans V tiles, and one a head (of it one lane) that issues the MMAs: a commit takes the issuing
+// thread some 120 clocks and a wait about as much, so that one warp for all heads was the bound (6,400
+// clocks a key tile of 4 heads and 64 dims, of which 2,050 on the tensor cores).
 #include "tree_common.cuh"
 
 namespace pkv {
 namespace {
 
-constexpr uint32_t kColP = 256, kColO = 384;
-
-template <int D, int PH> struct Pack {
-    static constexpr int kThreads = (6 + PH) * 32;
+// PH heads in MT row tiles.
+template <int D, int PH, int MT> struct Pack {
     static constexpr int kHalves = D / 64;
-    static constexpr int kKeys = PH == 4 ? 64 : 128;         // keys of a key tile
-    static constexpr int kLanes = kTreeRows / PH;            // lanes of a head
-    static constexpr int kQBytes = kHalves * kHalf;
-    static constexpr int kSide = kKeys * PH * 128;           // 64 dims of a key tile of all heads (32 KB)
+    static constexpr int kKeys = PH == 4 || (MT == 2 && D == 128) ? 64 : 128;  // keys of a key tile
+    static constexpr int kLanes = MT * kTreeRows / PH;       // lanes of a head
+    static constexpr int kColP = PH * kKeys;                 // TMEM: S, P, O
+    static constexpr int kColO = kColP + PH * kKeys / 2;
+    static_assert(kColO + MT * D <= static_cast<int>(kTmemCols), "TMEM columns");
+    static constexpr int kSoftmax = 4 * MT;                  // warps
+    static constexpr int kThreads = (kSoftmax + 2 + PH) * 32;
+    static constexpr int kQBytes = kHalves * kHalf;          // Q of a row tile
+    static constexpr int kSide = kKeys * PH * 128;           // 64 dims of a key tile of all heads
     static constexpr int kEntry = kHalves * kSide;
-    static constexpr int kStages = D == 128 ? 3 : 6;         // ring entries (192 KB)
-    static constexpr int kOffKV = kQBytes;
+    static constexpr int kOffKV = MT * kQBytes;
+    static constexpr int kFit = (224 * 1024 - kOffKV) / kEntry;  // ring entries, 160 or 192 KB
+    static constexpr int kStages = kFit > 6 ? 6 : kFit;
     static constexpr int kOffBar = kOffKV + kStages * kEntry;
     static constexpr int kNumBars = 2 + 4 * PH + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM address, abort flag, flags, cleaned
     static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
-    static_assert(kSmem + 128 <= 227 * 1024, "shared memory, with the kernel's static part");
+    static_assert(kSmem + 192 <= 227 * 1024, "shared memory, with the kernel's static part");
     static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
 };
 
-template <typename T, int D, int PH>
-__global__ void __launch_bounds__((6 + PH) * 32, 1)
+template <typename T, int D, int PH, int MT>
+__global__ void __launch_bounds__((4 * MT + 2 + PH) * 32, 1)
 tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                    const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ TreeParams p) {
-    using PK = Pack<D, PH>;
+    using PK = Pack<D, PH, MT>;
     constexpr int kStages = PK::kStages, kKeys = PK::kKeys, kLanes = PK::kLanes;
+    constexpr int kPerTile = PH / MT;  // heads of a row tile
+    constexpr int kProducer = PK::kSoftmax, kCleaner = kProducer + 1, kIssuer = kCleaner + 1;  // warps
     constexpr int kBarQFull = 0, kBarQEmpty = 1, kBarS = 2, kBarP = kBarS + PH, kBarPd = kBarP + PH,
                   kBarDrain = kBarPd + PH, kBarFull = kBarDrain + PH, kBarEmpty = kBarFull + kStages;
     const TreeArgs &a = p.a;
@@ -94,7 +105,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         for (int i = 0; i < kStages; ++i) cleaned[i] = 0;
         fence_barrier_init();
     }
-    if (warp == 5) {
+    if (warp == kCleaner) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
                      "r"(kTmemCols)
                      : "memory");
@@ -107,7 +118,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     Walk w;
     w.start(p, start, x0, x1);
 
-    if (warp == 4) {
+    if (warp == kProducer) {
         // ============================================================ TMA producer
         const int bpt = kKeys / bs;  // blocks of a key tile
         const uint32_t q_bytes = static_cast<uint32_t>(PH * PK::kHalves) * TQ * g * 128;
@@ -145,8 +156,8 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     mbar_arrive_expect_tx(bar(kBarQFull), q_bytes);
                     for (int h = 0; h < PH; ++h)
                         for (int hf = 0; hf < PK::kHalves; ++hf)
-                            tma_load_3d(smem_u32(smem + hf * kHalf + h * kLanes * 128), &tmap_q, bar(kBarQFull), 64 * hf,
-                                        (h0 + h) * g, s.q0);
+                            tma_load_3d(smem_u32(smem + h / kPerTile * PK::kQBytes + hf * kHalf + h % kPerTile * kLanes * 128),
+                                        &tmap_q, bar(kBarQFull), 64 * hf, (h0 + h) * g, s.q0);
                 }
             }
             if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
@@ -196,22 +207,23 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             for (int i = max(0, entry - kStages); i < entry; ++i)
                 if (!mbar_wait_sleep(bar(kBarFull + i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
         }
-    } else if (warp >= 6) {
+    } else if (warp >= kIssuer) {
         // ============================================================ MMA issue, one lane a head
-        const int h = warp - 6;
+        const int h = warp - kIssuer;
         constexpr uint32_t ab = AbFormat<T>::value;
         constexpr uint32_t idesc_s = mma_idesc(ab, false, kTreeRows, kKeys);
         constexpr uint32_t idesc_pv = mma_idesc(ab, true, kTreeRows, D);
         if (lane == 0) {
-            const uint64_t dq = smem_desc(smem_u32(smem), 16, 1024);
+            const uint64_t dq = smem_desc(smem_u32(smem + h / kPerTile * PK::kQBytes), 16, 1024);
             // one head's atoms (8 keys x 64 dims, 1 KB) are PH KB apart
             const uint32_t kv = smem_u32(smem + PK::kOffKV) + h * 1024;
             const uint64_t dk0 = smem_desc(kv, 16, PH * 1024);
             const uint64_t dv0 = smem_desc(kv, PK::kSide, PH * 1024);
-            const uint32_t t_s = tmem + h * kKeys, t_p = tmem + kColP + h * (kKeys / 2), t_o = tmem + kColO;
+            const uint32_t t_s = tmem + h * kKeys, t_p = tmem + PK::kColP + h * (kKeys / 2);
+            const uint32_t t_o = tmem + PK::kColO + h / kPerTile * D;
             uint32_t off[4];  // the other heads' lanes
 #pragma unroll
-            for (int i = 0; i < 4; ++i) off[i] = i * 32 / kLanes == h ? 0u : 0xffffffffu;
+            for (int i = 0; i < 4; ++i) off[i] = i * 32 / kLanes == h % kPerTile ? 0u : 0xffffffffu;
             // scores against the keys in ring entry e
             auto scores = [&](int e) {
                 const int sk = e % kStages;
@@ -251,8 +263,11 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     if (keys) scores(ek);
                     const uint64_t dv = dv0 + static_cast<uint64_t>((sv * PK::kEntry) >> 4);
 #pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_f16_ts_rows(t_o, t_p + k * 8, dv + ((k * PH * 2048) >> 4), idesc_pv, t > 0 || k > 0, off);
+                    for (int k = 0; k < kKeys / 16; ++k) {
+                        const uint64_t db = dv + ((k * PH * 2048) >> 4);
+                        if constexpr (kPerTile == 1) mma_f16_ts(t_o, t_p + k * 8, db, idesc_pv, t > 0 || k > 0);
+                        else mma_f16_ts_rows(t_o, t_p + k * 8, db, idesc_pv, t > 0 || k > 0, off);
+                    }
                     mma_commit(bar(kBarPd + h));
                     mma_commit(bar(kBarEmpty + sv));
                     if (more && !keys) {
@@ -274,7 +289,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             if (!mbar_wait_bounded(bar(kBarDrain + h), 0)) report(a.d_err, KV_DERR_TIMEOUT);
         }
         __syncwarp();
-    } else if (warp == 5) {
+    } else if (warp == kCleaner) {
         // ============================================================ cleaning of V tiles
         int done = 0;
         bool dead = false;
@@ -333,11 +348,12 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         }
     } else {
         // ============================================================ softmax and results
-        const int r = threadIdx.x;                       // query row = TMEM lane
+        const int r = threadIdx.x;                       // query row (128 a row tile) = TMEM lane
         const int hi = r / kLanes, rr = r % kLanes;      // head of the item (one a warp), row of it
         const int tl = rr / g, hh = rr - tl * g;         // token, head of the group
-        const uint32_t trow = tmem + (static_cast<uint32_t>(warp * 32) << 16);
-        const uint32_t t_s = trow + hi * kKeys, t_p = trow + kColP + hi * (kKeys / 2), t_o = trow + kColO;
+        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t t_s = trow + hi * kKeys, t_p = trow + PK::kColP + hi * (kKeys / 2);
+        const uint32_t t_o = trow + PK::kColO + hi / kPerTile * D;
         const float c2 = a.scale_log2;
         const float2 cc = make_float2(c2, c2);
         bool dead = false;
@@ -507,31 +523,44 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    if (warp == 5)
+    if (warp == kCleaner)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-template <typename T, int D, int PH>
+template <typename T, int D, int PH, int MT>
 cudaError_t launch_heads(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
                          int dev, cudaStream_t stream) {
     static std::atomic<bool> attr_set[64];
-    return launch_tree_kernel<T, D>(tree_packed_kernel<T, D, PH>, Pack<D, PH>::kThreads, Pack<D, PH>::kSmem, attr_set, tq, tk, tv, p,
-                                    dev, stream);
+    return launch_tree_kernel<T, D>(tree_packed_kernel<T, D, PH, MT>, Pack<D, PH, MT>::kThreads, Pack<D, PH, MT>::kSmem,
+                                    attr_set, tq, tk, tv, p, dev, stream);
 }
 
 template <typename T, int D>
 cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
                          int dev, cudaStream_t stream) {
-    return p.heads_per_item == 4 ? launch_heads<T, D, 4>(tq, tk, tv, p, dev, stream)
-                                 : launch_heads<T, D, 2>(tq, tk, tv, p, dev, stream);
+    if (p.heads_per_item == 4) return launch_heads<T, D, 4, 1>(tq, tk, tv, p, dev, stream);
+    return p.rows_per_item == kTreeRows ? launch_heads<T, D, 2, 1>(tq, tk, tv, p, dev, stream)
+                                        : launch_heads<T, D, 2, 2>(tq, tk, tv, p, dev, stream);
+}
+
+template <typename PK> void set_plan(TreePlan &t, int group) {
+    t.rows_per_item = PK::kSoftmax * 32;
+    t.tokens_per_tile = PK::kLanes / group;
+    t.key_shift = PK::kKeys == 64 ? 6 : 7;
+    t.smem_bytes = PK::kSmem;
+}
+
+template <int D> void plan_heads(TreePlan &t, int rows, int group) {
+    if (t.heads_per_item == 4) set_plan<Pack<D, 4, 1>>(t, group);
+    else if (rows <= 64) set_plan<Pack<D, 2, 1>>(t, group);
+    else set_plan<Pack<D, 2, 2>>(t, group);
 }
 
 }  // namespace
 
-size_t tree_packed_smem(int head_dim) {
-    const size_t a = head_dim == 128 ? Pack<128, 4>::kSmem : Pack<64, 4>::kSmem;
-    const size_t b = head_dim == 128 ? Pack<128, 2>::kSmem : Pack<64, 2>::kSmem;
-    return a > b ? a : b;
+void plan_tree_packed(TreePlan &t, int rows, int group, int head_dim) {
+    if (head_dim == 128) plan_heads<128>(t, rows, group);
+    else plan_heads<64>(t, rows, group);
 }
 
 cudaError_t launch_tree_packed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
