@@ -49,7 +49,7 @@ template <int D> struct Tile {
     static constexpr int kNumBars = 14 + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
     static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
-    static_assert(kSmem + 128 <= 227 * 1024, "shared memory, with the kernel's static part");
+    static_assert(kSmem + 256 <= 227 * 1024, "shared memory, with the kernel's static part");
     // pieces whose V tiles can be in the ring at once, one more that the cleaning warp has begun,
     // and one without mixed tiles (only a share's last)
     static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
@@ -87,13 +87,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     auto bar_full = [&](int s) { return smem_u32(&bars[kBarKv + s]); };
     auto bar_empty = [&](int s) { return smem_u32(&bars[kBarKv + kStages + s]); };
 
-    __shared__ ShareStart start;
-    int64_t x0, x1;
-    share_of_cta<kThreads>(p, c, x0, x1, start);
-    zero_rejected<T, D>(p);
-    if (x0 == x1) {
-        if (threadIdx.x == 0) p.ws_first[2 * c] = make_int4(-1, 0, 0, 0);
-        return;
+    asm volatile("griddepcontrol.launch_dependents;");
+    if (threadIdx.x == 32) {
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
     }
     if (threadIdx.x == 0) {
         mbar_init(bar(kBarQFull), 1);
@@ -122,22 +120,25 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
+    __shared__ ShareStart start;
+    int64_t x0, x1;
+    int item_cost;
+    share_of_cta<kThreads>(p, c, x0, x1, item_cost, start);
+    zero_rejected<T, D>(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     Walk w;
-    w.start(p, start, x0, x1);
+    w.start(start, x0, x1, item_cost);
 
-    if (warp == 8) {
+    if (x0 == x1) {
+        // no share: nothing but the record that says so
+        if (threadIdx.x == 0) p.ws_first[2 * c] = make_int4(-1, 0, 0, 0);
+    } else if (warp == 8) {
         // ============================================================ TMA producer
         const int bpt = kBN / bs;  // blocks of a key tile
         const uint32_t q_bytes = static_cast<uint32_t>(TL::kHalves) * TQ * g * 128;
-        if (lane == 0) {
-            prefetch_tensormap(&tmap_q);
-            prefetch_tensormap(&tmap_k);
-            prefetch_tensormap(&tmap_v);
-        }
         int entry = 0;  // ring entries filled
         int piece = 0;
         bool stop = false;
@@ -147,17 +148,13 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             if (piece == 0 && lane == 0) w.record(p, c);
             // block ids of key tile j: lane l holds block j * bpt + l
             const int nblk = (s.L - 1) / bs + 1, first_blk = s.kv_lo / bs;
-            auto block_id = [&](int j) {
+            auto entry_of = [&](int j) {  // (read before it is needed, checked when it is)
                 const int lb = j * bpt + lane;
-                int id = a.num_blocks;  // one past the pool: the copy reads zeros
-                if (lane < bpt && lb >= first_blk && lb < nblk) {
-                    const int e = a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + lb];
-                    if (e >= 0 && e < a.num_blocks) id = e;
-                    else report(a.d_err, KV_DERR_BAD_BLOCK);
-                }
-                return id;
+                return lane < bpt && lb >= first_blk && lb < nblk
+                           ? a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + lb]
+                           : a.num_blocks;  // one past the pool: the copy reads zeros
             };
-            int next_id = block_id(w.ja);
+            int next_id = entry_of(w.ja);
             bool ok = true;
             if (lane == 0) {
                 // Q of the item, once the piece before has formed its last scores
@@ -179,8 +176,13 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             }
             ++piece;
             for (int j = w.ja; j < w.jb && !stop; ++j) {
-                const int my_id = next_id;
-                if (j + 1 < w.jb) next_id = block_id(j + 1);
+                int my_id = next_id;
+                if (j + 1 < w.jb) next_id = entry_of(j + 1);
+                if (my_id < 0 || my_id > a.num_blocks || (my_id == a.num_blocks && j * bpt + lane < nblk && lane < bpt &&
+                                                          j * bpt + lane >= first_blk)) {
+                    report(a.d_err, KV_DERR_BAD_BLOCK);
+                    my_id = a.num_blocks;
+                }
                 for (int is_v = 0; is_v < 2; ++is_v) {
                     const int slot = entry % kStages;
                     int quit = 0;
@@ -512,8 +514,11 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             f1 *= inv;
             const int64_t row = token * a.num_q_heads + h * g + hh;
             T *out16 = static_cast<T *>(a.out) + row * D;
-            const int64_t part = part_row(p, c, w.ja == s.j0, (nt == 2 ? x * 128 : 0) + r);
-            float *out32 = p.ws_o + part * D;
+            const int prow = (nt == 2 ? x * 128 : 0) + r;
+            const int64_t slot = part_slot(c, w.ja == s.j0);
+            float4 *part = part_o<D>(p, slot, prow);
+            T *rows[4];
+            if (w.whole) quad_rows<T>(valid ? out16 : nullptr, rows);
             if (warp_valid) {
 #pragma unroll 1
                 for (int ch = 0; ch < D / 32; ++ch) {
@@ -530,19 +535,13 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
 #pragma unroll
                         for (int k = 0; k < 32; ++k) o[k] += f1 != 0.f ? o1[k] * f1 : 0.f;
                     }
-                    if (valid) {
-                        if (w.whole) {
-                            uint4 *dst = reinterpret_cast<uint4 *>(out16 + ch * 32);
+                    if (w.whole) {
+                        store_rows<T>(o, rows, ch * 32);
+                    } else if (valid) {
 #pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                dst[k] = make_uint4(pack2<T>(o[8 * k], o[8 * k + 1]), pack2<T>(o[8 * k + 2], o[8 * k + 3]),
-                                                    pack2<T>(o[8 * k + 4], o[8 * k + 5]), pack2<T>(o[8 * k + 6], o[8 * k + 7]));
-                        } else {
-                            float4 *dst = reinterpret_cast<float4 *>(out32 + ch * 32);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                dst[k] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            part[static_cast<int64_t>(ch * 8 + k) * p.rows_per_item] =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                 }
             }
@@ -552,10 +551,10 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
             }
             if (valid) {
                 const float lse2 = le == 0.f ? -INFINITY : m + log2f(le);
-                if (!w.whole) p.ws_lse[part] = lse2;
+                if (!w.whole) *part_lse(p, slot, prow) = lse2;
                 else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
                 if (odd_flag[piece % kFlags])
-                    add_odd_values<T, D>(p, w, h, klo, mask, w.whole ? out16 : nullptr, w.whole ? nullptr : out32);
+                    add_odd_values<T, D>(p, w, h, klo, mask, out16, w.whole ? nullptr : part);
             }
         }
         if (dead) {
@@ -620,7 +619,7 @@ cudaError_t launch_tree_attention(const CUtensorMap &tq, const CUtensorMap &tk, 
     char *ws = static_cast<char *>(workspace);
     p.ws_first = reinterpret_cast<int4 *>(ws);
     p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_off);
-    p.ws_o = reinterpret_cast<float *>(ws + plan.o_off);
+    p.ws_o = reinterpret_cast<float4 *>(ws + plan.o_off);
     if (p.heads_per_item > 1) return launch_tree_packed(tq, tk, tv, p, head_dim, q_dtype, dev, stream);
     if (q_dtype == KV_BF16)
         return head_dim == 128 ? launch_typed<__nv_bfloat16, 128>(tq, tk, tv, p, dev, stream)

@@ -16,8 +16,10 @@ constexpr int kTreeRows = 128;         // query rows of a row tile = TMEM lanes
 constexpr int kHalf = 128 * 128;       // 128 rows x 64 16-bit elements (one swizzle column)
 constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;   // a row's reference maximum moves when exceeded by more
-constexpr int kItemCost = 2;           // an item's fixed cost in key tiles
-constexpr int kMinShare = 3;           // least cost of a share: more than kItemCost, so that it holds a tile
+// An item's fixed cost in key tiles (its queries, masked tiles and results), once shares hold kBigShare
+// tiles or more.  Smaller ones count tiles alone, down to one: latency is what matters then.
+constexpr int kItemCost = 2;
+constexpr int kBigShare = 8;
 constexpr int kFlags = 8;              // pieces whose odd-value flags are kept
 
 struct TreeParams {
@@ -31,7 +33,8 @@ struct TreeParams {
     int4 *ws_first;       // [2 * workers] first piece of each share: (sequence, item of it, key tile of it,
                           // -), (first row, rows, -, -) of the sequence; sequence -1: no share
     float *ws_lse;        // [2 * workers][rows_per_item] log2-sum-exp2 of the partial results
-    float *ws_o;          // [2 * workers][rows_per_item][D] partial results, normalised
+    float4 *ws_o;         // [2 * workers][D / 4][rows_per_item] partial results, normalised, four dims each: a
+                          // warp's rows lie side by side
 };
 
 // A sequence's part of the work list.
@@ -66,65 +69,70 @@ __device__ __forceinline__ bool load_seq(const TreeParams &p, int b, Seq &s, boo
     return true;
 }
 
-__device__ __forceinline__ int64_t seq_cost(const TreeParams &p, int b) {
-    Seq s;
-    bool rejected;
-    if (!load_seq(p, b, s, &rejected)) return 0;
-    return static_cast<int64_t>(s.tiles + kItemCost) * s.items;
-}
-
-// The share [x0, x1) of CTA c (x0 == x1: none), and where it starts: sequence, item and the cost
-// where that item starts.  Computed by the whole block; b, idx and at are set in shared memory and
-// valid after the next __syncthreads.
+// Where the share of a CTA starts: sequence, item and the cost where that item starts.
 struct ShareStart {
+    Seq s;
     int64_t at;
     int b, idx;
 };
 
+// The share [x0, x1) of CTA c (x0 == x1: none) and an item's cost.  Computed by the whole block; `start`
+// is set in shared memory and valid after the next __syncthreads.
 template <int kThreads>
-__device__ __forceinline__ void share_of_cta(const TreeParams &p, int c, int64_t &x0, int64_t &x1, ShareStart &start) {
-    __shared__ int64_t warp_sum[kThreads / 32];
+__device__ __forceinline__ void share_of_cta(const TreeParams &p, int c, int64_t &x0, int64_t &x1, int &item_cost,
+                                             ShareStart &start) {
+    __shared__ int64_t warp_tiles[kThreads / 32];
+    __shared__ int64_t warp_items[kThreads / 32];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int num_seqs = p.a.num_seqs;
     const int per = (num_seqs + kThreads - 1) / kThreads;
     const int b_lo = min(num_seqs, static_cast<int>(threadIdx.x) * per), b_hi = min(num_seqs, b_lo + per);
-    int64_t sum = 0;
-    for (int b = b_lo; b < b_hi; ++b) sum += seq_cost(p, b);
-    int64_t incl = sum;
+    Seq s;
+    bool rejected;
+    int64_t tiles = 0, items = 0;  // of this thread's sequences
+    for (int b = b_lo; b < b_hi; ++b) {
+        if (!load_seq(p, b, s, &rejected)) continue;
+        tiles += static_cast<int64_t>(s.tiles) * s.items;
+        items += s.items;
+    }
+    int64_t it = tiles, ii = items;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-        const int64_t v = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += v;
+        const int64_t t = __shfl_up_sync(0xffffffffu, it, o), i = __shfl_up_sync(0xffffffffu, ii, o);
+        if (lane >= o) it += t, ii += i;
     }
-    if (lane == 31) warp_sum[warp] = incl;
+    if (lane == 31) warp_tiles[warp] = it, warp_items[warp] = ii;
     __syncthreads();
-    int64_t before = incl - sum, total = 0;
+    int64_t tiles_before = it - tiles, items_before = ii - items, all_tiles = 0, all_items = 0;
 #pragma unroll
     for (int w = 0; w < kThreads / 32; ++w) {
-        if (w < warp) before += warp_sum[w];
-        total += warp_sum[w];
+        if (w < warp) tiles_before += warp_tiles[w], items_before += warp_items[w];
+        all_tiles += warp_tiles[w];
+        all_items += warp_items[w];
     }
-    const int64_t most = max(int64_t(1), total / kMinShare);
-    const int shares = total == 0 ? 0 : static_cast<int>(min(static_cast<int64_t>(p.workers), most));
+    // a share of cost above item_cost holds a tile at least
+    const bool big = all_tiles >= static_cast<int64_t>(kBigShare) * p.workers;
+    item_cost = big ? kItemCost : 0;
+    const int64_t total = all_tiles + item_cost * all_items;
+    const int64_t shares = min(static_cast<int64_t>(p.workers), all_tiles);
     x0 = x1 = 0;
     if (c >= shares) return;
     x0 = total * c / shares;
     x1 = total * (c + 1) / shares;
-    if (x0 >= before && x0 < before + sum) {  // one thread
-        int64_t at = before;
-        for (int b = b_lo; b < b_hi; ++b) {
-            const int64_t cost = seq_cost(p, b);
-            if (x0 < at + cost) {
-                Seq s;
-                bool rejected;
-                load_seq(p, b, s, &rejected);
-                start.b = b;
-                start.idx = static_cast<int>((x0 - at) / (s.tiles + kItemCost));
-                start.at = at + static_cast<int64_t>(start.idx) * (s.tiles + kItemCost);
-                break;
-            }
-            at += cost;
+    const int64_t before = tiles_before + item_cost * items_before;
+    if (x0 < before || x0 >= before + tiles + item_cost * items) return;
+    int64_t at = before;  // one thread
+    for (int b = b_lo; b < b_hi; ++b) {
+        if (per > 1 && !load_seq(p, b, s, &rejected)) continue;
+        const int64_t cost = static_cast<int64_t>(s.tiles + item_cost) * s.items;
+        if (x0 < at + cost) {
+            start.b = b;
+            start.idx = static_cast<int>((x0 - at) / (s.tiles + item_cost));
+            start.at = at + static_cast<int64_t>(start.idx) * (s.tiles + item_cost);
+            start.s = s;
+            break;
         }
+        at += cost;
     }
 }
 
@@ -150,22 +158,22 @@ template <typename T, int D> __device__ __forceinline__ void zero_rejected(const
 struct Walk {
     int64_t at;       // cost where the item starts
     int64_t x0, x1;   // the share
+    int item_cost;
     Seq cur;          // the piece's sequence,
     int seq, item;    // its number, the item of it
     int ja, jb;       // and key tiles (absolute)
     bool whole;       // the piece is its whole item
     bool begun;
 
-    __device__ __forceinline__ void start(const TreeParams &p, const ShareStart &st, int64_t x0_, int64_t x1_) {
-        seq = st.b, item = st.idx, at = st.at, x0 = x0_, x1 = x1_;
+    __device__ __forceinline__ void start(const ShareStart &st, int64_t x0_, int64_t x1_, int item_cost_) {
+        seq = st.b, item = st.idx, at = st.at, x0 = x0_, x1 = x1_, item_cost = item_cost_;
+        cur = st.s;
         begun = false;
-        bool rejected;
-        load_seq(p, seq, cur, &rejected);
     }
     __device__ __forceinline__ bool next(const TreeParams &p) {
         for (;;) {
             if (begun) {  // on to the next item
-                at += kItemCost + cur.tiles;
+                at += item_cost + cur.tiles;
                 if (at >= x1) return false;
                 if (++item == cur.items) {
                     item = 0;
@@ -176,7 +184,7 @@ struct Walk {
                 }
             }
             begun = true;
-            const int64_t first = at + kItemCost;
+            const int64_t first = at + item_cost;
             ja = static_cast<int>(max(int64_t(0), x0 - first)) + cur.j0;
             jb = static_cast<int>(min(static_cast<int64_t>(cur.tiles), x1 - first)) + cur.j0;
             whole = ja == cur.j0 && jb == cur.j0 + cur.tiles;
@@ -190,10 +198,55 @@ struct Walk {
     }
 };
 
-// Where the partial result of the piece goes: a share leaves at most one that starts inside its
-// item (slot 2c) and one that starts it (2c + 1).
-__device__ __forceinline__ int64_t part_row(const TreeParams &p, int c, bool starts, int row) {
-    return static_cast<int64_t>(2 * c + (starts ? 1 : 0)) * p.rows_per_item + row;
+// Where the partial result of a piece goes: a share leaves at most one that starts inside its item
+// (slot 2c) and one that starts it (2c + 1).
+__device__ __forceinline__ int64_t part_slot(int c, bool starts) { return 2 * c + (starts ? 1 : 0); }
+__device__ __forceinline__ float *part_lse(const TreeParams &p, int64_t slot, int row) {
+    return p.ws_lse + slot * p.rows_per_item + row;
+}
+template <int D> __device__ __forceinline__ float4 *part_o(const TreeParams &p, int64_t slot, int row) {
+    return p.ws_o + slot * (D / 4) * p.rows_per_item + row;  // four dims on: rows_per_item further
+}
+
+// 32 dims of a row a lane (o) to 16-bit rows.  Quads of lanes exchange 16-byte units first, so that a
+// store covers 64 bytes of 8 rows instead of 16 bytes of 32.  dst[k]: dims of the row of the quad's
+// lane k, at this lane's unit, or null.
+template <typename T> __device__ __forceinline__ void store_rows(const float (&o)[32], T *const (&dst)[4], int dim) {
+    const int lane = threadIdx.x & 31;
+    uint32_t u[4][4];  // unit (8 dims), word
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) u[k][e] = pack2<T>(o[8 * k + 2 * e], o[8 * k + 2 * e + 1]);
+#pragma unroll
+    for (int bit = 1; bit <= 2; bit <<= 1) {
+        const bool hi = lane & bit;
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            if (k & bit) continue;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                // the lower lane gives its upper unit for the upper lane's lower one
+                const uint32_t give = hi ? u[k][e] : u[k | bit][e];
+                const uint32_t got = __shfl_xor_sync(0xffffffffu, give, bit);
+                if (hi) u[k][e] = got;
+                else u[k | bit][e] = got;
+            }
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+        if (dst[k]) *reinterpret_cast<uint4 *>(dst[k] + dim) = make_uint4(u[k][0], u[k][1], u[k][2], u[k][3]);
+}
+
+// The rows of this lane's quad, at this lane's unit of 8 dims, for store_rows (mine: null for no row).
+template <typename T> __device__ __forceinline__ void quad_rows(T *mine, T *(&dst)[4]) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+        const unsigned long long q = __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(mine), (lane & ~3) | k);
+        dst[k] = q ? reinterpret_cast<T *>(q) + 8 * (lane & 3) : nullptr;
+    }
 }
 
 // Whether key tile j holds a key that not every row of the sequence sees.
@@ -252,10 +305,10 @@ template <typename T> __device__ __forceinline__ void clean_chunk(uint32_t at, b
 }
 
 // Add the non-finite values of V that a row sees among the keys [k0, k1) to its written result
-// (out16 of type T, or a float row): they were zeroed for the products.  Rare, so plain.
+// (out16 of type T, or a partial result): they were zeroed for the products.  Rare, so plain.
 template <typename T, int D>
 static __device__ __noinline__ void add_non_finite(const TreeArgs &a, int b, int h, int k0, int k1, int ctx, int klo,
-                                            uint64_t mask, T *out16, float *out32) {
+                                            uint64_t mask, T *out16, float4 *part, int part_step) {
     for (int k = k0; k < k1; ++k) {
         const bool sees = k < ctx ? k >= klo : (mask >> (k - ctx)) & 1;
         const int id = a.block_table[b * a.bt_stride + k / a.block_size];
@@ -265,7 +318,7 @@ static __device__ __noinline__ void add_non_finite(const TreeArgs &a, int b, int
         for (int d = 0; d < D; ++d) {
             const float f = to_float<T>(v[d]);
             if (isfinite(f)) continue;
-            if (out32) out32[d] += f;
+            if (part) reinterpret_cast<float *>(part + static_cast<int64_t>(d / 4) * part_step)[d % 4] += f;
             else out16[d] = from_float<T>(to_float<T>(out16[d]) + f);
         }
     }
@@ -274,34 +327,52 @@ static __device__ __noinline__ void add_non_finite(const TreeArgs &a, int b, int
 // Add the non-finite values that the row sees in the piece's mixed tiles.
 template <typename T, int D>
 __device__ __forceinline__ void add_odd_values(const TreeParams &p, const Walk &w, int h, int klo, uint64_t mask, T *out16,
-                                               float *out32) {
+                                               float4 *part) {
     const TreeArgs &a = p.a;
     const Seq &s = w.cur;
     const int ka = w.ja << p.key_shift, kb = min(w.jb << p.key_shift, s.L);
     if (a.window > 0)
         add_non_finite<T, D>(a, w.seq, h, max(ka, s.kv_lo), min(min(s.ctx, s.ctx + s.n - a.window), kb), s.ctx, klo, mask,
-                             out16, out32);
-    add_non_finite<T, D>(a, w.seq, h, max(ka, s.ctx), kb, s.ctx, klo, mask, out16, out32);
+                             out16, part, p.rows_per_item);
+    add_non_finite<T, D>(a, w.seq, h, max(ka, s.ctx), kb, s.ctx, klo, mask, out16, part,
+                         p.rows_per_item);
 }
 
-// Join the partial results of the item that starts in share c and goes on into the next ones: one
-// warp a row.  out = sum_i w_i o_i / sum_i w_i, w_i = exp2(lse_i - max).  What it costs is dependent
-// round trips: the shares' records, then the lse and the first four partial rows at once.
+// Join the partial results of the item that starts in share c and goes on into the next ones.
+//   out = sum_i w_i o_i / sum_i w_i,  w_i = exp2(lse_i - max)
+// A thread takes 8 dims of a row, a warp 32 rows, so that the partial results are read in whole lines.
+// What it costs is dependent round trips: the shares' records, then kPieces pieces at a time.
 template <typename T, int D>
-static __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    constexpr int E = D / 32;
+static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeParams p) {
+    constexpr int kPieces = 4;
     const TreeArgs &a = p.a;
     const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const int rr = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);   // 8 dims of 32 rows
+    const int rr = unit / (D / 8) * 32 + lane, q = unit % (D / 8) * 2;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's results
     // lane i: the first piece of share c + i (none past the last)
     const int4 none = make_int4(-1, 0, 0, 0);
-    int4 rec = c + lane < p.workers ? p.ws_first[2 * (c + lane)] : none;
-    const int4 sq = p.ws_first[2 * (c + 1) + 1];
+    int4 rec = c + lane < p.workers ? __ldcg(&p.ws_first[2 * (c + lane)]) : none;
+    const int4 sq = __ldcg(&p.ws_first[2 * (c + 1) + 1]);
     // share c + 1's decides whether c's last item goes on; c's own, whether that item started before
     const int b = __shfl_sync(0xffffffffu, rec.x, 1), idx = __shfl_sync(0xffffffffu, rec.y, 1);
     const bool same = rec.x == b && rec.y == idx && rec.z > 0;  // this share goes on with the item
     uint32_t go = __ballot_sync(0xffffffffu, same);
     if (b < 0 || !(go & 2) || (go & 1)) return;
+    // pieces: share c's (its last: slot 2c + 1), then those of the next shares (their first: 2c')
+    int last = c + 31;
+    if (~(go | 1)) last = c + __ffs(~(go | 1)) - 2;
+    while (last >= c + 31) {
+        const int e = last + 1 + lane;
+        rec = e < p.workers ? __ldcg(&p.ws_first[2 * e]) : none;
+        go = __ballot_sync(0xffffffffu, rec.x == b && rec.y == idx && rec.z > 0);
+        if (go == 0xffffffffu) {
+            last += 32;
+            continue;
+        }
+        last += __ffs(~go) - 1;
+        break;
+    }
     // the row's kv head, token and head of the group
     int h, t, hh;
     const int TQ = p.tokens_per_tile;
@@ -318,68 +389,46 @@ static __global__ void __launch_bounds__(256) tree_merge_kernel(const __grid_con
         hh = r - t * p.group;
         if (h >= a.num_kv_heads || t >= sq.y) return;
     }
-    // pieces: share c's (its last: slot 2c + 1), then those of the next shares (their first: 2c')
-    int last = c + __ffs(~(go | 1)) - 2;  // (ffs 0: all 32 go on)
-    if (~(go | 1) == 0) last = c + 31;
-    while (last >= c + 31) {
-        const int e = last + 1 + lane;
-        rec = e < p.workers ? p.ws_first[2 * e] : none;
-        go = __ballot_sync(0xffffffffu, rec.x == b && rec.y == idx && rec.z > 0);
-        if (go == 0xffffffffu) {
-            last += 32;
-            continue;
+    float acc[8], wsum = 0.f, mx = -INFINITY;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    for (int e0 = c; e0 <= last; e0 += kPieces) {
+        float l[kPieces];
+        float4 v[kPieces][2];
+#pragma unroll
+        for (int u = 0; u < kPieces; ++u) {
+            const bool in = e0 + u <= last;
+            const int64_t slot = part_slot(e0 + u, e0 + u == c);
+            const float4 *src = part_o<D>(p, slot, rr) + static_cast<int64_t>(q) * p.rows_per_item;
+            l[u] = in ? __ldcg(part_lse(p, slot, rr)) : -INFINITY;
+            v[u][0] = in ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+            v[u][1] = in ? __ldcg(src + p.rows_per_item) : make_float4(0.f, 0.f, 0.f, 0.f);
         }
-        last += __ffs(~go) - 1;
-        break;
-    }
-    auto part = [&](int e) { return part_row(p, e, e == c, rr); };
-    float acc[E], wsum = 0.f, mx = -INFINITY;
+        float m = mx;
+        bool nan = false;
 #pragma unroll
-    for (int e = 0; e < E; ++e) acc[e] = 0.f;
-    for (int base = c; base <= last; base += 32) {
-        const int cnt = min(32, last - base + 1);
-        const float l = lane < cnt ? p.ws_lse[part(base + lane)] : -INFINITY;
-        float v[4][E];
-        auto load = [&](int u0) {
-#pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float *src = p.ws_o + part(base + u0 + u) * D + lane * E;
-#pragma unroll
-                for (int e = 0; e < E; ++e) v[u][e] = u0 + u < cnt ? __ldcg(src + e) : 0.f;
-            }
-        };
-        load(0);
-        float m = l;
-#pragma unroll
-        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const bool nan = __any_sync(0xffffffffu, l != l);
-        const float mn = fmaxf(mx, m);
-        if (mn == -INFINITY && !nan) continue;  // nothing seen so far
-        const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - mn);
-        mx = mn;
+        for (int u = 0; u < kPieces; ++u) m = fmaxf(m, l[u]), nan |= l[u] != l[u];
+        if (m == -INFINITY && !nan) continue;  // nothing seen so far
+        const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - m);
+        mx = m;
         wsum *= f;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] *= f;
-        const float wl = l == -INFINITY ? 0.f : fast_exp2(l - mx);
-        for (int u0 = 0; u0 < cnt; u0 += 4) {
-            if (u0) load(u0);
+        for (int e = 0; e < 8; ++e) acc[e] *= f;
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const float wu = __shfl_sync(0xffffffffu, wl, (u0 + u) & 31);
-                if (u0 + u < cnt && wu != 0.f) {  // a piece of weight 0 adds nothing, whatever it holds
-                    wsum += wu;
-#pragma unroll
-                    for (int e = 0; e < E; ++e) acc[e] += wu * v[u][e];
-                }
-            }
+        for (int u = 0; u < kPieces; ++u) {
+            const float w = l[u] == -INFINITY ? 0.f : fast_exp2(l[u] - mx);
+            if (w == 0.f) continue;  // it adds nothing, whatever it holds
+            wsum += w;
+            acc[0] += w * v[u][0].x, acc[1] += w * v[u][0].y, acc[2] += w * v[u][0].z, acc[3] += w * v[u][0].w;
+            acc[4] += w * v[u][1].x, acc[5] += w * v[u][1].y, acc[6] += w * v[u][1].z, acc[7] += w * v[u][1].w;
         }
     }
     const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
     const int64_t row = static_cast<int64_t>(sq.x + t) * a.num_q_heads + h * p.group + hh;
-    uint32_t *dst = reinterpret_cast<uint32_t *>(static_cast<T *>(a.out) + row * D + lane * E);
-#pragma unroll
-    for (int e = 0; e < E; e += 2) dst[e / 2] = pack2<T>(acc[e] * inv, acc[e + 1] * inv);
-    if (a.lse_out && lane == 0) a.lse_out[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
+    *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + 4 * q) =
+        make_uint4(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv),
+                   pack2<T>(acc[4] * inv, acc[5] * inv), pack2<T>(acc[6] * inv, acc[7] * inv));
+    if (a.lse_out && q == 0) a.lse_out[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
 }
 
 // The attention kernel and, with more than one share, the merge.
@@ -397,8 +446,18 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
     kernel<<<p.workers, threads, smem, stream>>>(tq, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.workers < 2) return e;
-    tree_merge_kernel<T, D><<<dim3(p.workers - 1, p.rows_per_item / 8), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    // the merge is launched while the attention kernel runs, and waits for its end (a CTA of it does not
+    // fit beside one of the attention kernel's, whose registers fill the SM)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.workers - 1, p.rows_per_item / 32 * (D / 8) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, p);
 }
 
 // Items of several kv heads (tree_packed.cu): the plan for `rows` query rows a head (heads_per_item
