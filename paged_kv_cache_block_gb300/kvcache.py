@@ -533,34 +533,23 @@ def apply_block_updates(updates: torch.Tensor, block_table: torch.Tensor, zero_i
 # helper call or a message built in advance costs more than the check).
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
+_current_device = torch._C._cuda_getDevice
 _i32, _i64, _f32 = torch.int32, torch.int64, torch.float32
+_code_of = {torch.float16: KV_F16, torch.bfloat16: KV_BF16, torch.uint8: KV_FP8_E4M3,
+            torch.float8_e4m3fn: KV_FP8_E4M3}
 
 
 def _refuse(what: str) -> None:
     raise KVError(KV_ERR_INVALID_ARG, what)
 
 
-def _one_device(dev: int, *tensors: Optional[torch.Tensor]) -> None:
-    for t in tensors:
-        if t is not None and t.get_device() != dev:
-            _refuse("every tensor must be on one CUDA device")
+_DEVICES = "every tensor must be on one CUDA device"
 
 
-def _call(dev: int, stream, fn, *args) -> None:
-    """fn(*args, stream) with the tensors' device current."""
-    if stream is None:
-        raw = _raw_stream(dev)
-    else:
-        if stream.device.index != dev:
-            _refuse("the stream must be of the tensors' device")
-        raw = stream.cuda_stream
-    if dev == torch.cuda.current_device():
-        status = fn(*args, raw)
-    else:
-        with torch.cuda.device(dev):
-            status = fn(*args, raw)
-    if status:
-        _check(status)
+def _stream_of(stream, dev: int) -> int:
+    if stream.device.index != dev:
+        _refuse("the stream must be of the tensors' device")
+    return stream.cuda_stream
 
 
 def _table_width(t: torch.Tensor, rows: int, max_blocks: Optional[int]) -> int:
@@ -574,9 +563,10 @@ def _table_width(t: torch.Tensor, rows: int, max_blocks: Optional[int]) -> int:
     return max_blocks
 
 
-def _table_stride(t: torch.Tensor) -> int:
-    # the stride of a single row means nothing; it only has to hold the row
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1]
+def _error_word(d_err: torch.Tensor, dev: int) -> int:
+    if d_err.dtype is not _i32 or d_err.numel() < 1 or d_err.get_device() != dev:
+        _refuse("d_err: int32 [1] on the same device")
+    return d_err.data_ptr()
 
 
 class Batch:
@@ -615,9 +605,12 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     updated in place; free_blocks int32 [F]; parents int32 [num_tokens] for drafted trees;
     free_start int32 [1].  The masks are int64 words (bit j = token j of the request's tree)."""
     dev = context_lens.get_device()
-    if dev < 0:
-        _refuse("every tensor must be on one CUDA device")
-    _one_device(dev, new_lens, block_table, free_blocks, held_blocks, parents, free_start, d_err)
+    if dev < 0 or new_lens.get_device() != dev or block_table.get_device() != dev or free_blocks.get_device() != dev:
+        _refuse(_DEVICES)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return build_batch(context_lens, new_lens, block_table, free_blocks, num_tokens, block_size, num_blocks,
+                               held_blocks, parents, free_start, out, d_err, max_blocks_per_seq, stream)
     B = context_lens.numel()
     if context_lens.dtype is not _i32 or not context_lens.is_contiguous():
         _refuse("context_lens: contiguous int32 [B]")
@@ -625,37 +618,49 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
         _refuse("new_lens: contiguous int32 [B]")
     if free_blocks.dtype is not _i32 or not free_blocks.is_contiguous():
         _refuse("free_blocks: contiguous int32")
-    if held_blocks is not None and (held_blocks.dtype is not _i32 or not held_blocks.is_contiguous() or
-                                    held_blocks.numel() != B):
-        _refuse("held_blocks: contiguous int32 [B]")
-    if parents is not None and (parents.dtype is not _i32 or not parents.is_contiguous() or
-                                parents.numel() != num_tokens):
-        _refuse("parents: contiguous int32 [num_tokens]")
-    if free_start is not None and (free_start.dtype is not _i32 or free_start.numel() != 1):
-        _refuse("free_start: int32 [1]")
-    if d_err is not None and (d_err.dtype is not _i32 or d_err.numel() < 1):
-        _refuse("d_err: int32 [1]")
+    held = par = start = err = None
+    if held_blocks is not None:
+        if held_blocks.dtype is not _i32 or not held_blocks.is_contiguous() or held_blocks.numel() != B or \
+                held_blocks.get_device() != dev:
+            _refuse("held_blocks: contiguous int32 [B] on the same device")
+        held = held_blocks.data_ptr()
+    if parents is not None:
+        if parents.dtype is not _i32 or not parents.is_contiguous() or parents.numel() != num_tokens or \
+                parents.get_device() != dev:
+            _refuse("parents: contiguous int32 [num_tokens] on the same device")
+        par = parents.data_ptr()
+    if free_start is not None:
+        if free_start.dtype is not _i32 or free_start.numel() != 1 or free_start.get_device() != dev:
+            _refuse("free_start: int32 [1] on the same device")
+        start = free_start.data_ptr()
+    if d_err is not None:
+        err = _error_word(d_err, dev)
     width = _table_width(block_table, B, max_blocks_per_seq)
     if out is None:
         out = Batch(B, num_tokens, parents is not None, context_lens.device)
     elif out._sizes != (B, num_tokens, parents is not None, dev):
         _refuse("out: batch_buffers of these sizes, with trees exactly when parents are given, on this device")
     qsl, lens, pos, slots, mask, held_out, free_next = out._pointers
-    _call(dev, stream, lib.kv_build_batch, _ptr(context_lens), _ptr(new_lens), _ptr(held_blocks), _ptr(parents), B,
-          num_tokens, _ptr(block_table), _table_stride(block_table), width, block_size, num_blocks, _ptr(free_blocks),
-          free_blocks.numel(), _ptr(free_start), qsl, lens, pos, slots, mask, held_out, free_next, _ptr(d_err))
+    status = lib.kv_build_batch(
+        context_lens.data_ptr(), new_lens.data_ptr(), held, par, B, num_tokens, block_table.data_ptr(),
+        block_table.stride(0) if B > 1 else width, width, block_size, num_blocks, free_blocks.data_ptr(),
+        free_blocks.numel(), start, qsl, lens, pos, slots, mask, held_out, free_next, err,
+        _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+    if status:
+        _check(status)
     return out
 
 
-def _token_stride(t: torch.Tensor, shape, dtype, what: str) -> int:
+def _token_stride(t: torch.Tensor, shape, dtype, dev: int, what: str) -> int:
     """The token stride of a [T, heads, D] tensor whose heads lie in one piece (that of a single
     token means nothing; it only has to hold the row)."""
+    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
+        _refuse(f"{what}: {dtype} {list(shape)} on the same device")
     T, H, D = shape
-    if t.dtype is not dtype or t.shape != shape:
-        _refuse(f"{what}: {dtype} [{T}, {H}, {D}]")
     s0, s1, s2 = t.stride()
-    if T and (s2 != 1 or (s1 != D and H > 1)):
-        _refuse(f"{what}: each token's heads in one piece")
+    if s2 != 1 or s1 != D:
+        if T and (s2 != 1 or H > 1):
+            _refuse(f"{what}: each token's heads in one piece")
     return s0 if T > 1 else -(-H * D // 8) * 8
 
 
@@ -663,47 +668,69 @@ def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache
                interleaved, k_scale, v_scale, q_out, k_out, d_err, stream):
     dev, dt = q.get_device(), q.dtype
     if dev < 0 or q.dim() != 3 or key.dim() != 3:
-        _refuse("q and key: [T, heads, D], and every tensor must be on one CUDA device")
-    _one_device(dev, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, q_out, k_out,
-                d_err)
+        _refuse("q and key: [T, heads, D]; " + _DEVICES)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
+                              interleaved, k_scale, v_scale, q_out, k_out, d_err, stream)
     qshape, kshape = q.shape, key.shape
     T, Hq, D = qshape
-    Hkv = kshape[1]
-    qs = _token_stride(q, qshape, dt, "q")
     if kshape[0] != T or kshape[2] != D:
         _refuse("q and key differ in tokens or head size")
-    ks = _token_stride(key, kshape, dt, "key")
-    qos = _token_stride(q_out, qshape, dt, "q_out")
-    kos = 0 if k_out is None else _token_stride(k_out, kshape, dt, "k_out")
-    if (q_weight is not None and (q_weight.dtype is not dt or q_weight.numel() != D or not q_weight.is_contiguous())) or \
-            (k_weight is not None and (k_weight.dtype is not dt or k_weight.numel() != D or not k_weight.is_contiguous())):
-        _refuse(f"weights: contiguous {dt} [{D}]")
-    if positions is not None and (positions.dtype is not _i32 or positions.numel() != T or not positions.is_contiguous()):
-        _refuse("positions: contiguous int32 [T]")
-    if d_err is not None and (d_err.dtype is not _i32 or d_err.numel() < 1):
-        _refuse("d_err: int32 [1]")
-    max_pos = rot = 0
+    Hkv = kshape[1]
+    qs = _token_stride(q, qshape, dt, dev, "q")
+    ks = _token_stride(key, kshape, dt, dev, "key")
+    qos = _token_stride(q_out, qshape, dt, dev, "q_out")
+    pos = cs = wq = wk = kout = err = None
+    kos = max_pos = rot = 0
+    if k_out is not None:
+        kos, kout = _token_stride(k_out, kshape, dt, dev, "k_out"), k_out.data_ptr()
+    if q_weight is not None:
+        if q_weight.dtype is not dt or q_weight.numel() != D or not q_weight.is_contiguous() or q_weight.get_device() != dev:
+            _refuse(f"q_weight: contiguous {dt} [{D}] on the same device")
+        wq = q_weight.data_ptr()
+    if k_weight is not None:
+        if k_weight.dtype is not dt or k_weight.numel() != D or not k_weight.is_contiguous() or k_weight.get_device() != dev:
+            _refuse(f"k_weight: contiguous {dt} [{D}] on the same device")
+        wk = k_weight.data_ptr()
+    if positions is not None:
+        if positions.dtype is not _i32 or positions.numel() != T or not positions.is_contiguous() or \
+                positions.get_device() != dev:
+            _refuse("positions: contiguous int32 [T] on the same device")
+        pos = positions.data_ptr()
     if cos_sin is not None:
-        if cos_sin.dtype is not _f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            _refuse("cos_sin: contiguous float32 [max_position, rotary_dim]")
+        if cos_sin.dtype is not _f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
+            _refuse("cos_sin: contiguous float32 [max_position, rotary_dim] on the same device")
         max_pos, rot = cos_sin.shape
-    code = dtype_code(dt)
+        cs = cos_sin.data_ptr()
+    if d_err is not None:
+        err = _error_word(d_err, dev)
+    code = _code_of.get(dt, -1)
+    vp = slots = kc = vc = None
     cache_code, NB, bs, vs = code, 0, 1, 0
     if slot_mapping is not None:
-        if slot_mapping.dtype is not _i64 or slot_mapping.numel() != T or not slot_mapping.is_contiguous():
-            _refuse("slot_mapping: contiguous int64 [T]")
-        vs = _token_stride(value, kshape, dt, "value")
-        if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or \
-                not k_cache.is_contiguous() or not v_cache.is_contiguous():
-            _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type")
-        NB, bs, ch, cd = k_cache.shape
-        if ch != Hkv or cd != D:
-            _refuse("caches of other heads than key's")
-        cache_code = code if k_cache.dtype is dt else dtype_code(k_cache.dtype)
-    _call(dev, stream, lib.kv_qk_norm_rope, _ptr(q), _ptr(key), _ptr(value), code, qs, ks, vs, T, Hq, Hkv, D,
-          _ptr(q_weight), _ptr(k_weight), eps, _ptr(positions), _ptr(cos_sin), max_pos, rot, 1 if interleaved else 0,
-          _ptr(q_out), qos, _ptr(k_out), kos, _ptr(slot_mapping), _ptr(k_cache), _ptr(v_cache), cache_code, NB, bs,
-          k_scale, v_scale, _ptr(d_err))
+        if slot_mapping.dtype is not _i64 or slot_mapping.numel() != T or not slot_mapping.is_contiguous() or \
+                slot_mapping.get_device() != dev:
+            _refuse("slot_mapping: contiguous int64 [T] on the same device")
+        vs = _token_stride(value, kshape, dt, dev, "value")
+        cshape, cdt = k_cache.shape, k_cache.dtype
+        if len(cshape) != 4 or cshape[2] != Hkv or cshape[3] != D or v_cache.shape != cshape or \
+                v_cache.dtype is not cdt or not k_cache.is_contiguous() or not v_cache.is_contiguous() or \
+                k_cache.get_device() != dev or v_cache.get_device() != dev:
+            _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type, heads and D those of key, "
+                    "on the same device")
+        NB, bs = cshape[0], cshape[1]
+        if cdt is not dt:
+            cache_code = _code_of.get(cdt, -1)
+        vp, slots, kc, vc = value.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
+        if not slots:  # no tokens: nothing to write (and no slots to say so)
+            vp = kc = vc = None
+    status = lib.kv_qk_norm_rope(
+        q.data_ptr(), key.data_ptr(), vp, code, qs, ks, vs, T, Hq, Hkv, D, wq, wk, eps, pos, cs, max_pos, rot,
+        1 if interleaved else 0, q_out.data_ptr(), qos, kout, kos, slots, kc, vc, cache_code, NB, bs, k_scale, v_scale,
+        err, _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+    if status:
+        _check(status)
 
 
 def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: Optional[torch.Tensor],
@@ -763,41 +790,54 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     given must hold paged_attention_tree_workspace_size(...) bytes."""
     dev, dt = q.get_device(), q.dtype
     if dev < 0 or q.dim() != 3 or not q.is_contiguous():
-        _refuse("q: contiguous [T, heads, D], and every tensor must be on one CUDA device")
-    _one_device(dev, k_cache, v_cache, block_table, seq_lens, query_start_loc, tree_mask, workspace, out, lse_out, d_err)
+        _refuse("q: contiguous [T, heads, D]; " + _DEVICES)
+    if dev != _current_device():
+        with torch.cuda.device(dev):
+            return paged_attention_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, tree_mask, max_seq_len,
+                                        max_query_len, scale, window, num_workers, workspace, out, lse_out, d_err,
+                                        max_blocks_per_seq, stream)
     T, Hq, D = q.shape
     B = seq_lens.numel()
-    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or k_cache.dtype is not v_cache.dtype or \
-            not k_cache.is_contiguous() or not v_cache.is_contiguous():
-        _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type")
-    NB, bs, Hkv, cd = k_cache.shape
-    if cd != D:
-        _refuse("caches of another head size than q's")
-    if seq_lens.dtype is not _i32 or not seq_lens.is_contiguous():
-        _refuse("seq_lens: contiguous int32 [B]")
-    if query_start_loc.dtype is not _i32 or not query_start_loc.is_contiguous() or query_start_loc.numel() != B + 1:
-        _refuse("query_start_loc: contiguous int32 [B + 1]")
-    if tree_mask.dtype is not _i64 or not tree_mask.is_contiguous() or tree_mask.numel() != T:
-        _refuse("tree_mask: contiguous int64 [T]")
-    if d_err is not None and (d_err.dtype is not _i32 or d_err.numel() < 1):
-        _refuse("d_err: int32 [1]")
+    cshape, cdt = k_cache.shape, k_cache.dtype
+    if len(cshape) != 4 or cshape[3] != D or v_cache.shape != cshape or v_cache.dtype is not cdt or \
+            not k_cache.is_contiguous() or not v_cache.is_contiguous() or k_cache.get_device() != dev or \
+            v_cache.get_device() != dev:
+        _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type, D that of q, on the same device")
+    NB, bs, Hkv, _ = cshape
+    if seq_lens.dtype is not _i32 or not seq_lens.is_contiguous() or seq_lens.get_device() != dev:
+        _refuse("seq_lens: contiguous int32 [B] on the same device")
+    if query_start_loc.dtype is not _i32 or not query_start_loc.is_contiguous() or query_start_loc.numel() != B + 1 or \
+            query_start_loc.get_device() != dev:
+        _refuse("query_start_loc: contiguous int32 [B + 1] on the same device")
+    if tree_mask.dtype is not _i64 or not tree_mask.is_contiguous() or tree_mask.numel() != T or \
+            tree_mask.get_device() != dev:
+        _refuse("tree_mask: contiguous int64 [T] on the same device")
+    if block_table.get_device() != dev:
+        _refuse(_DEVICES)
     width = _table_width(block_table, B, max_blocks_per_seq)
+    err = lse = None
+    if d_err is not None:
+        err = _error_word(d_err, dev)
     if out is None:
         out = torch.empty_like(q)
-    elif out.shape != q.shape or out.dtype is not dt or not out.is_contiguous():
+    elif out.shape != q.shape or out.dtype is not dt or not out.is_contiguous() or out.get_device() != dev:
         _refuse("out: like q")
-    if lse_out is not None and (lse_out.dtype is not _f32 or lse_out.shape != (T, Hq) or not lse_out.is_contiguous()):
-        _refuse("lse_out: contiguous float32 [T, heads]")
+    if lse_out is not None:
+        if lse_out.dtype is not _f32 or lse_out.shape != (T, Hq) or not lse_out.is_contiguous() or \
+                lse_out.get_device() != dev:
+            _refuse("lse_out: contiguous float32 [T, heads] on the same device")
+        lse = lse_out.data_ptr()
     if workspace is None:
-        with torch.cuda.device(dev):
-            need = paged_attention_tree_workspace_size(B, max_query_len, Hq, Hkv, D, num_workers)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    elif not workspace.is_contiguous():
-        _refuse("workspace: contiguous")
-    code = dtype_code(dt)
-    _call(dev, stream, lib.kv_paged_attention_tree, _ptr(q), code, _ptr(query_start_loc), B, T, max_query_len, Hq,
-          _ptr(k_cache), _ptr(v_cache), code if k_cache.dtype is dt else dtype_code(k_cache.dtype), Hkv, D, bs, NB,
-          _ptr(block_table), _table_stride(block_table), width, _ptr(seq_lens), max_seq_len, scale, window,
-          _ptr(tree_mask), num_workers, _ptr(workspace), workspace.numel() * workspace.element_size(), _ptr(out),
-          _ptr(lse_out), _ptr(d_err))
+        workspace = torch.empty(paged_attention_tree_workspace_size(B, max_query_len, Hq, Hkv, D, num_workers),
+                                dtype=torch.uint8, device=q.device)
+    elif not workspace.is_contiguous() or workspace.get_device() != dev:
+        _refuse("workspace: contiguous, on the same device")
+    status = lib.kv_paged_attention_tree(
+        q.data_ptr(), _code_of.get(dt, -1), query_start_loc.data_ptr(), B, T, max_query_len, Hq, k_cache.data_ptr(),
+        v_cache.data_ptr(), _code_of.get(cdt, -1), Hkv, D, bs, NB, block_table.data_ptr(),
+        block_table.stride(0) if B > 1 else width, width, seq_lens.data_ptr(), max_seq_len, scale, window,
+        tree_mask.data_ptr(), num_workers, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+        out.data_ptr(), lse, err, _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+    if status:
+        _check(status)
     return out
