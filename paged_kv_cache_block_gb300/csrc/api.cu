@@ -1067,6 +1067,8 @@ kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_lens, c
     a.held_out = held_out;
     a.free_next = free_next;
     a.d_err = d_err;
+    a.aligned = aligned(positions, 16) && aligned(slot_mapping, 16);
+    a.fours = false;
     e = pkv::launch_build_batch(a, info.sm_count, s);
     if (e != cudaSuccess) return cuda_fail(e, "build batch launch");
     return ok();

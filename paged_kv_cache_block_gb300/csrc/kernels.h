@@ -171,6 +171,8 @@ struct BatchArgs {
     uint64_t *tree_mask;
     int32_t *held_out, *free_next;
     int32_t *d_err;
+    bool aligned;  // positions and slot_mapping on 16-byte boundaries: four tokens a store
+    bool fours;    // four tokens a thread (set by the launch)
 };
 
 cudaError_t launch_build_batch(const BatchArgs &a, int sm_count, cudaStream_t stream);
