@@ -1150,7 +1150,7 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
     a.total_slots = write ? static_cast<int64_t>(num_blocks) * block_size : 0;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
-    a.heads_a_warp = a.parts = a.q_parts = a.kv_parts = 0;
+    a.heads_a_warp = a.q_parts = a.kv_parts = 0;
     a.d_err = d_err;
     e = pkv::launch_qk_norm_rope(a, dtype, info.sm_count, s);
     if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");

@@ -194,8 +194,8 @@ struct RopeArgs {
     int32_t cache_fp8;
     int64_t total_slots;
     float k_scale, v_scale;
-    // set by the launch: heads of a token that one warp takes; warps a token, for q, for key (and value)
-    int32_t heads_a_warp, parts, q_parts, kv_parts;
+    // set by the launch: heads of a token that one warp takes; warps a token for q, and for key (and value)
+    int32_t heads_a_warp, q_parts, kv_parts;
     int32_t *d_err;
 };
 

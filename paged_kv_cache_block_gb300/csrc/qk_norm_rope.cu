@@ -25,10 +25,10 @@ namespace {
 
 constexpr int kThreads = 256;
 // Loads in flight a lane, batches of them a warp at most, blocks an SM.  16384 tokens of 64 + 16 heads
-// took 131 us so; 137, 136 and 144 us with 2, 3 and 8 loads, 143 and 134 us with 1 and 4 batches, 141
-// and 183 us with 3 and 5 blocks (80 registers: fewer warps; 48: spills).
+// take 111 us so (6.1 TB/s); 121, 115 us with 2 and 4 batches, 119 with 5 loads, 128 us with 3 blocks
+// (80 registers: fewer warps), 132 with 5 (48: spills; and 2 loads, 4 batches).
 constexpr int kBatch = 4;
-constexpr int kRounds = 2;
+constexpr int kRounds = 8;
 constexpr int kBlocksAnSm = 4;
 
 __device__ __forceinline__ float2 mul2(float2 a, float2 b) {
@@ -76,9 +76,8 @@ template <typename T, int LP, bool kAdjacent, int kD>
 __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int HPW = 32 / LP;
     const int lane = threadIdx.x & 31;
-    const int64_t w = (static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x) >> 5;
-    const int64_t t = w / a.parts;
-    int part = static_cast<int>(w - t * a.parts);
+    const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
+    int part = blockIdx.y;
     if (t >= a.num_tokens) return;
     const bool reports = part == 0 && lane == 0;
     const int32_t pos = a.positions ? a.positions[t] : 0;
@@ -269,10 +268,9 @@ cudaError_t launch_lanes(RopeArgs a, int sm_count, cudaStream_t stream) {
     a.heads_a_warp = n * HPW;
     a.q_parts = parts(a.num_q_heads);
     a.kv_parts = parts(a.num_kv_heads);
-    a.parts = all();
-    const int64_t blocks = (static_cast<int64_t>(a.num_tokens) * a.parts + kThreads / 32 - 1) / (kThreads / 32);
-    if (blocks > 0x7fffffff) return cudaErrorInvalidConfiguration;
-    const unsigned grid = static_cast<unsigned>(blocks);
+    if (all() > 65535) return cudaErrorInvalidConfiguration;
+    // a warp a token, the parts of its heads along y
+    const dim3 grid((static_cast<unsigned>(a.num_tokens) + kThreads / 32 - 1) / (kThreads / 32), all());
     if (a.interleaved) qk_norm_rope_kernel<T, LP, true, kD><<<grid, kThreads, 0, stream>>>(a);
     else qk_norm_rope_kernel<T, LP, false, kD><<<grid, kThreads, 0, stream>>>(a);
     return cudaGetLastError();

@@ -443,6 +443,17 @@ TREE_CASES = [
     ([2000, 128, 4096], [16, 16, 40], 32, 8, 128, 32, torch.bfloat16, 1024),
     ([4000], [3], 8, 8, 64, 16, torch.float16, 0),                            # one long sequence, split
     ([1], [2], 2, 2, 128, 16, torch.float16, 4096),
+    # groups of kv heads: 4 of up to 32 rows, 2 of up to 64 and 128, the last group not full
+    ([130, 63, 700], [8, 3, 6], 12, 3, 128, 16, torch.bfloat16, 0),
+    ([130, 64, 700], [32, 31, 1], 5, 5, 64, 8, torch.float16, 0),
+    ([900, 65, 0], [9, 16, 10], 28, 7, 128, 32, torch.float16, 200),
+    ([900, 127], [64, 33], 6, 6, 64, 16, torch.bfloat16, 0),
+    ([500, 128, 2], [12, 9, 11], 15, 3, 64, 16, torch.bfloat16, 0),           # 60 rows, the group of 5
+    ([1000, 257, 12], [32, 17, 31], 20, 5, 128, 16, torch.bfloat16, 0),       # 128 rows
+    ([1000, 257, 12], [18, 16, 14], 21, 3, 128, 8, torch.float16, 300),       # 126 rows
+    ([700, 40], [33, 64], 12, 6, 64, 32, torch.bfloat16, 0),                  # up to 128 rows of 64 dims
+    ([700, 40, 300], [1, 1, 1], 64, 8, 128, 16, torch.bfloat16, 0),           # single tokens
+    ([70] * 40, [2] * 40, 32, 8, 128, 16, torch.bfloat16, 64),
 ]
 
 
@@ -471,10 +482,14 @@ def test_tree_masks_of_any_kind(kc):
 @pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
 @pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
 @pytest.mark.parametrize("window", [0, 70])
-def test_tree_unseen_keys_have_no_part(kc, dt, poison, window):
+@pytest.mark.parametrize("drafts,Hq,Hkv", [([13, 64, 7, 30], 8, 2), ([8, 7, 2, 5], 12, 3), ([13, 16, 7, 11], 20, 5),
+                                           ([13, 32, 7, 30], 12, 3), ([9, 11, 2, 8], 16, 1)],
+                         ids=["pair", "four", "two", "two_wide", "one"])
+def test_tree_unseen_keys_have_no_part(kc, dt, poison, window, drafts, Hq, Hkv):
     """Poison in every slot no row sees: free blocks, the rest of the last block, keys before the
     window; and in drafted keys and window keys that only some rows see, whose other rows stay clean."""
-    contexts, drafts, Hq, Hkv, bs = [150, 0, 40, 263], [13, 64, 7, 30], 8, 2, 16
+    contexts, bs = [150, 0, 40, 263], 16
+    # (row 0 of each tree sees itself alone of it, so that no drafted key is seen by all)
     c = tree_case(21, contexts, drafts, Hq, Hkv, 128, bs, dt, window)
     clean = {k: c[k].clone() for k in ("k", "v")}
     seen_any = torch.zeros(c["k"].shape[0] * bs, dtype=torch.bool)
