@@ -49,7 +49,8 @@ template <int D> struct Tile {
     static constexpr int kNumBars = 14 + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
     static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
-    static_assert(kSmem + 256 <= 227 * 1024, "shared memory, with the kernel's static part");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(sizeof(ShareScratch) <= 3 * 128 * 4, "the scratch lies where the chains join later");
     // pieces whose V tiles can be in the ring at once, one more that the cleaning warp has begun,
     // and one without mixed tiles (only a share's last)
     static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
@@ -120,17 +121,17 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    __shared__ ShareStart start;
+    ShareScratch &scratch = *reinterpret_cast<ShareScratch *>(join);
     int64_t x0, x1;
     int item_cost;
-    share_of_cta<kThreads>(p, c, x0, x1, item_cost, start);
+    share_of_cta<kThreads>(p, c, x0, x1, item_cost, scratch);
     zero_rejected<T, D>(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     Walk w;
-    w.start(start, x0, x1, item_cost);
+    w.start(scratch.start, x0, x1, item_cost);
 
     if (x0 == x1) {
         // no share: nothing but the record that says so

@@ -76,13 +76,20 @@ struct ShareStart {
     int b, idx;
 };
 
-// The share [x0, x1) of CTA c (x0 == x1: none) and an item's cost.  Computed by the whole block; `start`
-// is set in shared memory and valid after the next __syncthreads.
+struct ShareScratch {
+    int64_t warp_tiles[16], warp_items[16];
+    ShareStart start;
+};
+
+// The share [x0, x1) of CTA c (x0 == x1: none) and an item's cost.  Computed by the whole block, with
+// scratch in shared memory; scratch.start is valid after the next __syncthreads.
 template <int kThreads>
 __device__ __forceinline__ void share_of_cta(const TreeParams &p, int c, int64_t &x0, int64_t &x1, int &item_cost,
-                                             ShareStart &start) {
-    __shared__ int64_t warp_tiles[kThreads / 32];
-    __shared__ int64_t warp_items[kThreads / 32];
+                                             ShareScratch &scratch) {
+    static_assert(kThreads <= 16 * 32, "a word a warp");
+    int64_t(&warp_tiles)[16] = scratch.warp_tiles;
+    int64_t(&warp_items)[16] = scratch.warp_items;
+    ShareStart &start = scratch.start;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int num_seqs = p.a.num_seqs;
     const int per = (num_seqs + kThreads - 1) / kThreads;

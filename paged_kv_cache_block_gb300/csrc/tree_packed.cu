@@ -34,7 +34,7 @@ namespace {
 // PH heads in MT row tiles.
 template <int D, int PH, int MT> struct Pack {
     static constexpr int kHalves = D / 64;
-    static constexpr int kKeys = PH == 4 || (MT == 2 && D == 128) ? 64 : 128;  // keys of a key tile
+    static constexpr int kKeys = PH == 4 || D == 128 ? 64 : 128;  // keys of a key tile
     static constexpr int kLanes = MT * kTreeRows / PH;       // lanes of a head
     static constexpr int kColP = PH * kKeys;                 // TMEM: S, P, O
     static constexpr int kColO = kColP + PH * kKeys / 2;
@@ -51,7 +51,7 @@ template <int D, int PH, int MT> struct Pack {
     static constexpr int kNumBars = 2 + 4 * PH + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;  // TMEM address, abort flag, flags, cleaned
     static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
-    static_assert(kSmem + 256 <= 227 * 1024, "shared memory, with the kernel's static part");
+    static_assert(kSmem + 512 <= 227 * 1024, "shared memory, with the kernel's static part");
     static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
 };
 
@@ -109,17 +109,17 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    __shared__ ShareStart start;
+    __shared__ ShareScratch scratch;
     int64_t x0, x1;
     int item_cost;
-    share_of_cta<PK::kThreads>(p, c, x0, x1, item_cost, start);
+    share_of_cta<PK::kThreads>(p, c, x0, x1, item_cost, scratch);
     zero_rejected<T, D>(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
     Walk w;
-    w.start(start, x0, x1, item_cost);
+    w.start(scratch.start, x0, x1, item_cost);
 
     if (x0 == x1) {
         // no share: nothing but the record that says so
