@@ -77,7 +77,8 @@ extern "C" {
  *   tree_mask        uint64 [num_tokens], given exactly when parents are
  *   free_next        device int32
  * Outputs may not overlap inputs or each other (KV_ERR_INVALID_ARG): a loop keeps two sets and
- * swaps them.  block_size 4, 8, 16 or 32.  Exact integer arithmetic; one launch.
+ * swaps them.  block_size 4, 8, 16 or 32.  Exact integer arithmetic; one launch, whose every CTA reads
+ * all lengths (made for batches of up to some thousand requests; larger ones work).
  */
 KV_API kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_lens,
                                 const int32_t *held_blocks, const int32_t *parents, int32_t num_seqs,
@@ -142,6 +143,9 @@ KV_API kv_status kv_qk_norm_rope(const void *q, const void *key, const void *val
  *   out = sum_j softmax_j(scale * q.K_j) V_j,   lse = log(sum_j exp(scale * q.K_j))
  * A key that a row does not see has no part in its result, whatever the cache holds there (NaN and
  * infinities included).
+ * Once a path of the tree is accepted, its K/V belong in slots c_b, c_b + 1, ...: kv_reshape_and_cache of
+ * the step's rows (k_out of kv_qk_norm_rope, whose positions c_b + depth are the final ones) with a
+ * slot mapping that is -1 for the rejected rows puts them there.
  *
  *   q            [num_tokens, num_q_heads, head_dim] fp16/bf16, equal to cache_dtype, 16-byte aligned
  *   query_start_loc int32 [num_seqs + 1], non-decreasing; max_query_len >= every n_b (host bound)
@@ -156,6 +160,9 @@ KV_API kv_status kv_qk_norm_rope(const void *q, const void *key, const void *val
  * its keys read as zeros.
  * Supported: head_dim 64 or 128, block_size 8, 16 or 32, num_q_heads / num_kv_heads up to 128,
  * window 0 or >= KV_MAX_TREE.  num_workers as for kv_paged_attention_decode.
+ * Two launches: the attention kernel and the merge of the trees that several workers shared.  Calls
+ * that may overlap on the GPU need workspaces of their own; captured calls replayed one after the
+ * other may share one.
  */
 KV_API kv_status kv_paged_attention_tree(
     const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs,

@@ -1,11 +1,24 @@
-// Helpers of the tcgen05 kernels (prefill_attention.cu, tree_attention.cu): shared-memory and
-// instruction descriptors, matrix products issued by one thread, TMEM loads and stores, and packed
-// float pairs.
+// Helpers of the tcgen05 kernels (prefill_attention.cu, tree_attention.cu, tree_packed.cu): shared-memory
+// and instruction descriptors, matrix products issued by one thread, TMEM loads and stores, and packed
+// float pairs (also for qk_norm_rope.cu).
 #pragma once
 
 #include "common.cuh"
 
 namespace pkv {
+
+// Whether the phase has completed, without waiting.
+__device__ __forceinline__ bool mbar_test(uint32_t bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return done != 0;
+}
 
 // Shared-memory matrix descriptor: start address, leading and stride byte offsets (16-byte
 // units), the fixed version bit 46, 128B swizzle (mode 2 in bits 61-63).

@@ -9,11 +9,13 @@
 //
 // Heads of at most 32 (64) query rows share the 128 TMEM lanes of one row tile, four (two) of them,
 // lanes 32 h .. those of head h.  Heads of up to 128 rows have a row tile each, two at a time.  (38
-// sequences of 8000 tokens and 32/8 heads of 128 dims: 201 us for 28 rows a head, 216 for 64, 250 for
-// 128, where one head at a time took 269, 308 and 363; at 256 rows two row tiles of one head take 405
+// sequences of 8000 tokens and 32/8 heads of 128 dims: 201 us for 28 rows a head, 219 for 64, 247 for
+// 128, where one head at a time took 269, 308 and 363; at 256 rows two row tiles of one head take 395
 // and two heads a row tile 505, so that wider trees stay with tree_attention.cu.)
 //
-// Per key tile and head h (key tiles of 64 or 128 keys: 32 or 64 KB of K and of V):
+// Per key tile and head h (64 keys, or 128 of two heads of 64 dims: 32 KB of K and of V, 64 KB for four
+// heads of 128 dims; with 128 keys of two heads of 128 dims the ring has three entries instead of six,
+// and the Mistral-shaped window layer took 235 us instead of 208):
 //   S_h = Q K_h^T    all 128 rows, of which the lanes of head h are read
 //   P_h = exp2(S_h * scale - m)    one thread a row; P_h has TMEM columns of its own
 //   O  += P_h V_h    for the lanes of head h alone (the other lanes are switched off), so that

@@ -176,6 +176,36 @@ def test_batch_strided_table_and_narrow_rows(kc):
     check_batch(kc, ctx, new, held, table, free, T, bs, NB, width=int(held.max()))
 
 
+def test_batch_long_prompts_over_several_chunks_of_requests(kc):
+    """More tokens than the grid has threads (four a thread) and more requests than a block has."""
+    _, err = check_batch(kc, *batch_case(17, 1100, 40, 400, 16, extra_held=1, pad=2))
+    assert err == 0
+    ctx, new, held, table, free, T, bs, NB, _ = batch_case(18, 700, 300, 600, 8, pad=0)
+    got, err = check_batch(kc, ctx, new, held, table, free[:len(free) // 2], T, bs, NB)
+    assert err == 128
+
+
+def test_batch_outputs_off_the_16_byte_boundary(kc):
+    """The C call takes positions on 4 and slots on 8 bytes; the neighbours stay as they are."""
+    ctx, new, held, table, free, T, bs, NB, _ = batch_case(19, 500, 40, 800, 16, pad=1)
+    want, _ = R.build_batch(ctx, new, held, table, free, T, bs, NB)
+    i32 = lambda a: dev(np.asarray(a, np.int32))  # noqa: E731
+    B, tab, b = len(ctx), i32(table), kc.batch_buffers(len(ctx), T)
+    ins = [i32(ctx), i32(new), i32(held), i32(free)]
+    pos = torch.full((T + 8,), 77, dtype=torch.int32, device="cuda")
+    slots = torch.full((T + 8,), 77, dtype=torch.int64, device="cuda")
+    status = kc.lib.kv_build_batch(
+        ins[0].data_ptr(), ins[1].data_ptr(), ins[2].data_ptr(), None, B, T, tab.data_ptr(), tab.shape[1], tab.shape[1], bs,
+        NB, ins[3].data_ptr(), len(free), None, b.query_start_loc.data_ptr(), b.seq_lens.data_ptr(), pos.data_ptr() + 12,
+        slots.data_ptr() + 24, None, b.held_blocks.data_ptr(), b.free_next.data_ptr(), None, None)
+    torch.cuda.synchronize()
+    assert status == 0
+    np.testing.assert_array_equal(pos[3:3 + T].cpu().numpy(), want["positions"])
+    np.testing.assert_array_equal(slots[3:3 + T].cpu().numpy(), want["slot_mapping"])
+    for t in (pos, slots):
+        assert (t[:3] == 77).all() and (t[3 + T:] == 77).all()
+
+
 def test_batch_slots_agree_with_slot_mapping(kc):
     ctx, new, held, table, free, T, bs, NB, _ = batch_case(15, 60, 400, 90, 16, pad=0)
     i32 = lambda a: dev(np.asarray(a, np.int32))  # noqa: E731
@@ -652,15 +682,16 @@ def test_tree_small_workspace_is_refused(kc):
 class Step:
     """One speculative step of one layer: metadata, norm with rotation and cache write, attention."""
 
-    def __init__(self, kc, seed=40, B=9, Hq=8, Hkv=2, D=128, bs=16, dt=torch.bfloat16, pad=3):
+    def __init__(self, kc, seed=40, B=9, Hq=8, Hkv=2, D=128, bs=16, dt=torch.bfloat16, pad=3, max_new=29):
         rng = np.random.default_rng(seed)
         self.kc, self.D, self.bs, self.dt = kc, D, bs, dt
-        self.ctx, self.new = rng.integers(0, 200, B), rng.integers(0, 30, B)
+        self.ctx, self.new = rng.integers(0, 200, B), rng.integers(0, max_new + 1, B)
+        self.new[0] = max_new
         self.held = -(-self.ctx // bs)
         need = -(-(self.ctx + self.new) // bs) - self.held
         self.NB = int(self.held.sum() + need.sum()) + 4
         ids = rng.permutation(self.NB).astype(np.int32)
-        self.table = np.full((B, 16), -1, np.int32)
+        self.table = np.full((B, 300 // bs + 1), -1, np.int32)
         at = 0
         for r in range(B):
             self.table[r, :self.held[r]] = ids[at:at + self.held[r]]
@@ -734,8 +765,11 @@ class Step:
         assert (self.out[n:] == 7).all()
 
 
-def test_step_together(kc):
-    s = Step(kc)
+@pytest.mark.parametrize("Hq,Hkv,D,bs,dt,max_new", [
+    (8, 2, 128, 16, torch.bfloat16, 29), (6, 3, 64, 8, torch.float16, 12), (4, 4, 128, 32, torch.bfloat16, 64),
+    (16, 1, 64, 16, torch.float16, 40), (64, 8, 128, 16, torch.bfloat16, 50)])
+def test_step_together(kc, Hq, Hkv, D, bs, dt, max_new):
+    s = Step(kc, Hq=Hq, Hkv=Hkv, D=D, bs=bs, dt=dt, max_new=max_new)
     s.run()
     s.check()
     s.reset()  # again on fresh buffers
@@ -822,3 +856,83 @@ def test_step_after_step(kc):
         ctx = ctx + accepted
         d_held, d_start = b.held_blocks, b.free_next
         held, table, start = want["held_blocks"], want["block_table"], int(want["free_next"][0])
+
+
+def test_step_accepted_path_then_the_next_step(kc):
+    """Drafted trees, acceptance of one path of each, its K/V moved to their final slots, and the next
+    step over the accepted context: the cache then holds each sequence as if it had been written token
+    by token, and the second step's attention is that of the definition over it."""
+    rng = np.random.default_rng(60)
+    B, Hq, Hkv, D, bs, NB, T, dt = 6, 8, 4, 128, 16, 200, 80, torch.bfloat16
+    ctx = rng.integers(1, 90, B)
+    held = -(-ctx // bs)
+    ids = rng.permutation(NB).astype(np.int32)
+    table = np.full((B, 16), -1, np.int32)
+    at = 0
+    for r in range(B):
+        table[r, :held[r]] = ids[at:at + held[r]]
+        at += held[r]
+    i32 = lambda a: dev(np.asarray(a, np.int32))  # noqa: E731
+    gen = torch.Generator().manual_seed(60)
+    kcache, vcache = (torch.randn(NB, bs, Hkv, D, generator=gen).to(dt).cuda() for _ in range(2))
+    cs = dev(rope_table(300, D))
+    w = torch.ones(D, dtype=dt, device="cuda")
+    d_table, d_free = i32(table), i32(ids[at:])
+    sets = [kc.batch_buffers(B, T, True), kc.batch_buffers(B, T, True)]
+    d_held, d_start = i32(held), None
+    tokens = [[(kcache.view(-1, Hkv, D)[s].clone(), vcache.view(-1, Hkv, D)[s].clone())
+               for s in (int(table[r, p // bs]) * bs + p % bs for p in range(ctx[r]))] for r in range(B)]
+    for step in range(3):
+        new = rng.integers(1, 13, B)
+        n = int(new.sum())
+        parents = np.full(T, -1)
+        trees = [R.random_parents(rng, int(k)) for k in new]
+        parents[:n] = np.concatenate(trees)
+        b = kc.build_batch(i32(ctx), i32(new), d_table, d_free, T, bs, NB, held_blocks=d_held, parents=i32(parents),
+                           free_start=d_start, out=sets[step % 2])
+        q, k, v = (torch.randn(T, h, D, generator=gen).to(dt).cuda() for h in (Hq, Hkv, Hkv))
+        k_out = torch.zeros_like(k)
+        q = kc.qk_norm_rope_and_cache(q, k, v, b.positions, cs, b.slot_mapping, kcache, vcache, w, w, k_out=k_out)
+        out = kc.paged_attention_tree(q, kcache, vcache, d_table, b.seq_lens, b.query_start_loc, b.tree_mask,
+                                      int((ctx + new).max()), int(new.max()), 0.09)
+        # every row against its own path, token by token
+        qsl = b.query_start_loc.cpu().numpy()
+        for r in range(B):
+            for i in range(new[r]):
+                path = [i]
+                while trees[r][path[-1]] >= 0:
+                    path.append(int(trees[r][path[-1]]))
+                rows = [qsl[r] + j for j in path]
+                K = torch.stack([t[0] for t in tokens[r]] + [k_out[j] for j in rows]).double().cpu().numpy()
+                V = torch.stack([t[1] for t in tokens[r]] + [v[j] for j in rows]).double().cpu().numpy()
+                Q = f64(q[qsl[r] + i])
+                for h in range(Hq):
+                    kk, vv = K[:, h * Hkv // Hq], V[:, h * Hkv // Hq]
+                    s = kk @ Q[h] * 0.09
+                    p = np.exp(s - s.max())
+                    o, size = p @ vv / p.sum(), p @ np.abs(vv) / p.sum()
+                    smax = (np.abs(kk) @ np.abs(Q[h]) * 0.09).max()
+                    tol, _ = R.tree_bounds(o, np.float64(0), size, np.float64(smax), D, dt)
+                    assert (np.abs(f64(out[qsl[r] + i, h]) - o) <= tol).all()
+        # accept the path to one token of each tree
+        tab = d_table.cpu().numpy()
+        move = np.full(T, -1, np.int64)
+        accepted = np.zeros(B, np.int64)
+        for r in range(B):
+            path = [int(rng.integers(0, new[r]))]
+            while trees[r][path[-1]] >= 0:
+                path.append(int(trees[r][path[-1]]))
+            for depth, j in enumerate(reversed(path)):
+                p = ctx[r] + depth
+                assert int(b.positions[qsl[r] + j]) == p
+                move[qsl[r] + j] = tab[r, p // bs].astype(np.int64) * bs + p % bs
+                tokens[r].append((k_out[qsl[r] + j].clone(), v[qsl[r] + j].clone()))
+            accepted[r] = len(path)
+        kc.reshape_and_cache(k_out, v, dev(move), kcache, vcache)
+        ctx = ctx + accepted
+        for r in range(B):
+            p = np.arange(ctx[r])
+            s = dev(tab[r, p // bs].astype(np.int64) * bs + p % bs)
+            assert torch.equal(kcache.view(-1, Hkv, D)[s], torch.stack([t[0] for t in tokens[r]]))
+            assert torch.equal(vcache.view(-1, Hkv, D)[s], torch.stack([t[1] for t in tokens[r]]))
+        d_held, d_start = b.held_blocks, b.free_next
