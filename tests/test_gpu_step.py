@@ -426,12 +426,13 @@ def tree_case(seed, contexts, drafts, Hq, Hkv, D, bs, dt, window=0, pad=0, masks
                 window=window, scale=D ** -0.5, dt=dt, D=D)
 
 
-def run_tree(kc, c, workers=0, stream=None, fill=7.0):
+def run_tree(kc, c, workers=0, stream=None, fill=7.0, max_query_len=None):
     out = torch.full_like(c["q"], fill)
     lse = torch.full(c["q"].shape[:2], fill, dtype=torch.float32, device="cuda")
     err = torch.zeros(1, dtype=torch.int32, device="cuda")
     kc.paged_attention_tree(c["q"], c["k"], c["v"], dev(c["table"]), dev(c["L"]), dev(c["qsl"]), dev(c["masks"]),
-                            max(1, int(c["L"].max(initial=1))), max(list(c["drafts"]) + [1]), c["scale"], c["window"],
+                            max(1, int(c["L"].max(initial=1))),
+                            max(list(c["drafts"]) + [1]) if max_query_len is None else max_query_len, c["scale"], c["window"],
                             num_workers=workers, out=out, lse_out=lse, d_err=err, stream=stream)
     torch.cuda.synchronize()
     return out, lse, int(err)
@@ -493,6 +494,52 @@ def test_tree(kc, case):
     ref = reference_tree(c)
     for workers in (0, 1, 7):
         out, lse, err = run_tree(kc, c, workers)
+        assert err == 0
+        check_tree(c, out, lse, ref)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D", [(8, 2, 128), (6, 1, 64), (12, 6, 64)])
+def test_tree_more_workers_than_sms_and_loose_bounds(kc, Hq, Hkv, D):
+    """Shares of more CTAs than the GPU holds at once, and a max_query_len above every tree (which
+    chooses the kernel): the same rows."""
+    c = tree_case(31, [3000, 70, 1, 900], [3, 1, 20, 9], Hq, Hkv, D, 16, torch.bfloat16)
+    ref = reference_tree(c)
+    for workers, most in ((400, None), (1000, 64), (0, 64), (0, 40), (3, 21)):
+        out, lse, err = run_tree(kc, c, workers, max_query_len=most)
+        assert err == 0
+        check_tree(c, out, lse, ref)
+
+
+def test_step_in_a_cache_past_32_bit_offsets(kc):
+    """Caches of more than 2^31 elements: slots and blocks at their end, written and read."""
+    NB, bs, Hkv, Hq, D, dt = 140_000, 16, 8, 32, 128, torch.bfloat16
+    kbig, vbig = (torch.empty(NB, bs, Hkv, D, dtype=dt, device="cuda") for _ in range(2))
+    contexts, drafts = [300, 17], [9, 30]
+    c = tree_case(32, contexts, drafts, Hq, Hkv, D, bs, dt)
+    small = c["k"].shape[0]
+    first = NB - small  # the small pool's blocks, at the end of the big one
+    kbig[first:], vbig[first:] = c["k"], c["v"]
+    # the drafted keys and values come through the norm, rotation and cache write
+    gen = torch.Generator().manual_seed(32)
+    T = int(c["qsl"][-1])
+    q, k, v = (torch.randn(T, h, D, generator=gen).to(dt).cuda() for h in (Hq, Hkv, Hkv))
+    table, slots, pos = c["table"].copy(), [], []
+    for b, (ctx, n) in enumerate(zip(contexts, drafts)):
+        at = np.arange(ctx, ctx + n)
+        slots += (table[b, at // bs].astype(np.int64) * bs + at % bs).tolist()
+        pos += at.tolist()
+    cs = dev(rope_table(400, D))
+    k_out = torch.empty_like(k)
+    big_slots = dev(np.array(slots) + first * bs)
+    assert int(big_slots.max()) * Hkv * D > 2 ** 31
+    c["q"] = kc.qk_norm_rope_and_cache(q, k, v, dev(np.array(pos, np.int32)), cs, big_slots, kbig, vbig, k_out=k_out)
+    for cache, rows in ((c["k"], k_out), (c["v"], v)):
+        cache.view(-1, Hkv, D)[dev(np.array(slots))] = rows
+    assert torch.equal(kbig[first:], c["k"]) and torch.equal(vbig[first:], c["v"])
+    ref = reference_tree(c)
+    big = dict(c, k=kbig, v=vbig, table=np.where(table >= 0, table + first, -1).astype(np.int32))
+    for most in (None, 64):
+        out, lse, err = run_tree(kc, big, max_query_len=most)
         assert err == 0
         check_tree(c, out, lse, ref)
 
