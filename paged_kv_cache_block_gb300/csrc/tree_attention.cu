@@ -88,6 +88,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     auto bar_full = [&](int s) { return smem_u32(&bars[kBarKv + s]); };
     auto bar_empty = [&](int s) { return smem_u32(&bars[kBarKv + kStages + s]); };
 
+    asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 32) {
         prefetch_tensormap(&tmap_q);
         prefetch_tensormap(&tmap_k);

@@ -356,6 +356,7 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);   // 8 dims of 32 rows
     const int rr = unit / (D / 8) * 32 + lane, q = unit % (D / 8) * 2;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's results
     // lane i: the first piece of share c + i (none past the last)
     const int4 none = make_int4(-1, 0, 0, 0);
     int4 rec = c + lane < p.workers ? __ldcg(&p.ws_first[2 * (c + lane)]) : none;
@@ -452,8 +453,18 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
     kernel<<<p.workers, threads, smem, stream>>>(tq, tk, tv, p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess || p.workers < 2) return e;
-    tree_merge_kernel<T, D><<<dim3(p.workers - 1, p.rows_per_item / 32 * (D / 8) / 8), 256, 0, stream>>>(p);
-    return cudaGetLastError();
+    // the merge is launched while the attention kernel runs, and waits for its end (a CTA of it does not
+    // fit beside one of the attention kernel's, whose registers fill the SM)
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(p.workers - 1, p.rows_per_item / 32 * (D / 8) / 8);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute at[1];
+    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = at;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, p);
 }
 
 // Items of several kv heads (tree_packed.cu): the plan for `rows` query rows a head (heads_per_item

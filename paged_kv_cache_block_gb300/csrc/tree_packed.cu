@@ -81,6 +81,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     int32_t *cleaned = reinterpret_cast<int32_t *>(smem + PK::kOffMisc + 8 + 4 * kFlags);  // [kStages]: entry + 1
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
+    asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 32) {
         prefetch_tensormap(&tmap_q);
         prefetch_tensormap(&tmap_k);
