@@ -78,7 +78,7 @@ extern "C" {
  *   free_next        device int32
  * Outputs may not overlap inputs or each other (KV_ERR_INVALID_ARG): a loop keeps two sets and
  * swaps them.  block_size 4, 8, 16 or 32.  Exact integer arithmetic; one launch, whose every CTA reads
- * all lengths (made for batches of up to some thousand requests; larger ones work).
+ * all lengths (made for batches of up to some thousand requests; num_seqs up to 2^24).
  */
 KV_API kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_lens,
                                 const int32_t *held_blocks, const int32_t *parents, int32_t num_seqs,
@@ -110,11 +110,13 @@ KV_API kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_
  *   q, key, value    fp16/bf16 [num_tokens, heads, head_dim], token stride in elements (>= heads *
  *                    head_dim, a multiple of 8), 16-byte aligned: views of one projection will do
  *   q_out, k_out     like q and key; each may be its input (same stride), else overlap nothing
+ *                    (KV_ERR_INVALID_ARG; rows of one stride may lie between each other)
  *   q_weight, k_weight  of the same dtype, [head_dim], 16-byte aligned
  *   cos_sin          float32 [max_position, rotary_dim], 16-byte aligned (NULL when rotary_dim 0)
  *   value, caches    as for kv_reshape_and_cache; all NULL when slot_mapping is
  * Supported: head_dim a multiple of 8 up to 256; rotary_dim a multiple of 16 up to head_dim (0: no
- * rotation; positions may then be NULL, else they still mark padding).  One launch.
+ * rotation; positions may then be NULL, else they still mark padding); up to 65535 heads of a kind.  One
+ * launch.
  */
 KV_API kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_dtype dtype,
                                  int64_t q_stride, int64_t key_stride, int64_t value_stride,
@@ -154,9 +156,10 @@ KV_API kv_status kv_qk_norm_rope(const void *q, const void *key, const void *val
  *                wholly outside every row's window are never read)
  *   workspace    at least kv_paged_attention_tree_workspace_size(...) bytes, 256-byte aligned
  *   out          [num_tokens, num_q_heads, head_dim]; lse_out float32 [num_tokens, num_q_heads] or
- *                NULL.  Rows of no sequence are not written.
- * A sequence whose length is rejected (n_b > max_query_len, L_b < n_b, > max_seq_len or past the
- * table) sets KV_DERR_BAD_LEN and its rows are 0 (lse -inf).  A bad block id sets KV_DERR_BAD_BLOCK;
+ *                NULL.  Rows of no sequence are not written.  Neither they nor the workspace may overlap
+ *                an input or each other (KV_ERR_INVALID_ARG)
+ * A sequence whose length is rejected (n_b > max_query_len, L_b < n_b, > max_seq_len, > 2^31 - 257 or past
+ * the table) sets KV_DERR_BAD_LEN and its rows are 0 (lse -inf).  A bad block id sets KV_DERR_BAD_BLOCK;
  * its keys read as zeros.
  * Supported: head_dim 64 or 128, block_size 8, 16 or 32, num_q_heads / num_kv_heads up to 128,
  * window 0 or >= KV_MAX_TREE.  num_workers as for kv_paged_attention_decode.

@@ -3,6 +3,7 @@
 // stream.  Nothing here allocates device memory or synchronises.
 #include <cudaTypedefs.h>
 
+#include <algorithm>
 #include <cfloat>
 #include <cmath>
 #include <cstdarg>
@@ -997,6 +998,23 @@ static bool overlap(const ByteRange &x, const ByteRange &y) {
     return a < b + static_cast<uintptr_t>(y.bytes) && b < a + static_cast<uintptr_t>(x.bytes);
 }
 
+// Rows of `bytes` at p, p + stride, ... (bytes <= stride).  Two sets of one stride may lie between each other
+// (views of one projection); sets of different strides count as overlapping when their ranges do.
+struct RowSet {
+    const void *p;
+    int64_t stride, bytes, rows;
+    ByteRange range() const { return {p, (rows - 1) * stride + bytes}; }
+};
+static bool rows_overlap(const RowSet &x, const RowSet &y) {
+    if (!overlap(x.range(), y.range())) return false;
+    if (x.stride != y.stride) return true;
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x.p), b = reinterpret_cast<uintptr_t>(y.p);
+    // the later set's first row lies this far behind the start of a row of the earlier set
+    const RowSet &first = a < b ? x : y, &second = a < b ? y : x;
+    const int64_t behind = static_cast<int64_t>((a < b ? b - a : a - b) % static_cast<uintptr_t>(x.stride));
+    return behind < first.bytes || (behind + second.bytes > x.stride && x.rows > 1 && y.rows > 1);
+}
+
 kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_lens, const int32_t *held_blocks,
                          const int32_t *parents, int32_t num_seqs, int32_t num_tokens, int32_t *block_table,
                          int64_t bt_stride, int32_t max_blocks_per_seq, int32_t block_size, int32_t num_blocks,
@@ -1010,6 +1028,7 @@ kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_lens, c
         return fail(KV_ERR_UNSUPPORTED, "block_size %d (supported: 4, 8, 16, 32)", block_size);
     if (static_cast<int64_t>(max_blocks_per_seq) * block_size > INT32_MAX)
         return fail(KV_ERR_UNSUPPORTED, "max_blocks_per_seq * block_size past 32 bits");
+    if (num_seqs > 1 << 24) return fail(KV_ERR_UNSUPPORTED, "num_seqs %d (at most 2^24)", num_seqs);
     if (!query_start_loc || !free_next)
         return fail(KV_ERR_INVALID_ARG, "null query_start_loc or free_next");
     if (num_seqs > 0 && (!context_lens || !new_lens || !block_table || !seq_lens || !held_out))
@@ -1085,6 +1104,7 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
     if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim < 8 || rotary_dim < 0 || max_position < 0)
         return fail(KV_ERR_INVALID_ARG, "invalid size argument");
     if (dtype != KV_F16 && dtype != KV_BF16) return fail(KV_ERR_UNSUPPORTED, "q, key and value must be fp16 or bf16");
+    if (num_q_heads > 65535 || num_kv_heads > 65535) return fail(KV_ERR_UNSUPPORTED, "more than 65535 heads");
     if (head_dim % 8 || head_dim > 256)
         return fail(KV_ERR_UNSUPPORTED, "head_dim %d (supported: multiples of 8 up to 256)", head_dim);
     if (rotary_dim % 16 || rotary_dim > head_dim)
@@ -1114,6 +1134,25 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
         !aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(positions, 4) || !aligned(slot_mapping, 8) ||
         !aligned(d_err, 4))
         return fail(KV_ERR_INVALID_ARG, "q, key, value, outputs, weights, cos_sin and caches must be 16-byte aligned");
+    // a token's heads are read and written by different warps: an output may only be its own input
+    const int64_t T = num_tokens, cache_bytes = write ? static_cast<int64_t>(num_blocks) * block_size * krow *
+                                                            (cache_dtype == KV_FP8_E4M3 ? 1 : 2) : 0;
+    const RowSet in_rows[] = {{q, 2 * q_stride, 2 * qrow, T}, {key, 2 * key_stride, 2 * krow, T},
+                              {write ? value : nullptr, 2 * value_stride, 2 * krow, T}};
+    const RowSet out_rows[] = {{q_out, 2 * q_out_stride, 2 * qrow, T}, {k_out, 2 * k_out_stride, 2 * krow, T}};
+    const ByteRange in_ranges[] = {{q_weight, 2 * head_dim}, {k_weight, 2 * head_dim}, {positions, 4 * T},
+                                   {rotary_dim ? cos_sin : nullptr, 4ll * max_position * rotary_dim},
+                                   {slot_mapping, 8 * T}};
+    const ByteRange caches[] = {{k_cache, cache_bytes}, {v_cache, cache_bytes}};
+    bool clash = rows_overlap(out_rows[0], out_rows[1]) || overlap(caches[0], caches[1]);
+    for (int o = 0; o < 2; ++o) {
+        for (int i = 0; i < 3; ++i)
+            clash |= (o != i || out_rows[o].p != in_rows[i].p) && rows_overlap(out_rows[o], in_rows[i]);
+        for (const ByteRange &r : in_ranges) clash |= overlap(out_rows[o].range(), r) || overlap(caches[o], r);
+        for (const RowSet &r : in_rows) clash |= overlap(caches[o], r.range());
+        for (const RowSet &r : out_rows) clash |= overlap(caches[o], r.range());
+    }
+    if (clash) return fail(KV_ERR_INVALID_ARG, "an output overlaps an input other than its own, or another output");
     int dev;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = bind_device(s, &dev);
@@ -1211,7 +1250,8 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
         return fail(KV_ERR_UNSUPPORTED, "tree attention: block_size must be 8, 16 or 32");
     if (window > 0 && window < KV_MAX_TREE)
         return fail(KV_ERR_UNSUPPORTED, "tree attention: window must be 0 or at least %d", KV_MAX_TREE);
-    if (!(scale >= 0.f) || !std::isfinite(scale)) return fail(KV_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    if (!(scale >= 0.f) || !std::isfinite(scale * 1.4426950408889634f))
+        return fail(KV_ERR_INVALID_ARG, "scale must be finite and >= 0");
     if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return ok();
     if (!q || !query_start_loc || !k_cache || !v_cache || !block_table || !seq_lens || !tree_mask || !out)
         return fail(KV_ERR_INVALID_ARG, "null pointer");
@@ -1220,6 +1260,18 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     if (!aligned(query_start_loc, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(tree_mask, 8) ||
         !aligned(lse_out, 4) || !aligned(d_err, 4))
         return fail(KV_ERR_INVALID_ARG, "misaligned pointer");
+    // items are finished while others still read
+    const int64_t B = num_seqs, T = num_tokens, rows = T * num_q_heads;
+    const int64_t cache_bytes = 2ll * num_blocks * block_size * num_kv_heads * head_dim;
+    const ByteRange outs[] = {{out, 2 * rows * head_dim}, {lse_out, 4 * rows},
+                              {workspace, static_cast<int64_t>(std::min<size_t>(workspace_bytes, INT64_MAX))}};
+    const ByteRange ins[] = {{q, 2 * rows * head_dim}, {query_start_loc, 4 * (B + 1)}, {seq_lens, 4 * B}, {tree_mask, 8 * T},
+                             {block_table, 4 * ((B - 1) * bt_stride + max_blocks_per_seq)}, {k_cache, cache_bytes},
+                             {v_cache, cache_bytes}};
+    bool clash = overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2]);
+    for (const ByteRange &o : outs)
+        for (const ByteRange &i : ins) clash |= overlap(o, i);
+    if (clash) return fail(KV_ERR_INVALID_ARG, "an output or the workspace overlaps an input or another output");
     int dev;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     cudaError_t e = bind_device(s, &dev);
@@ -1260,7 +1312,7 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     a.num_kv_heads = num_kv_heads;
     a.block_size = block_size;
     a.num_blocks = num_blocks;
-    a.max_seq_len = max_seq_len;
+    a.max_seq_len = std::min(max_seq_len, INT32_MAX - 256);  // the keys of a whole tile count in 32 bits
     a.window = window;
     // a scale of 0 (all weights alike) as the least normal number: the kernels mask with -inf * scale
     a.scale_log2 = std::fmax(scale * 1.4426950408889634f, FLT_MIN);

@@ -268,8 +268,8 @@ cudaError_t launch_lanes(RopeArgs a, int sm_count, cudaStream_t stream) {
     a.heads_a_warp = n * HPW;
     a.q_parts = parts(a.num_q_heads);
     a.kv_parts = parts(a.num_kv_heads);
-    if (all() > 65535) return cudaErrorInvalidConfiguration;
-    // a warp a token, the parts of its heads along y
+    // a warp a token, the parts of its heads along y (fewer than 65536: n is halved only below 32 warps an
+    // SM, and 65535 heads of each kind make at most 6144 parts at first)
     const dim3 grid((static_cast<unsigned>(a.num_tokens) + kThreads / 32 - 1) / (kThreads / 32), all());
     if (a.interleaved) qk_norm_rope_kernel<T, LP, true, kD><<<grid, kThreads, 0, stream>>>(a);
     else qk_norm_rope_kernel<T, LP, false, kD><<<grid, kThreads, 0, stream>>>(a);

@@ -546,10 +546,12 @@ def _refuse(what: str) -> None:
 _DEVICES = "every tensor must be on one CUDA device"
 
 
-def _stream_of(stream, dev: int) -> int:
+def _on(stream, dev: int):
+    """The context of a call on a given stream: what the call allocates is then of that stream's memory,
+    so that freeing it hands it to no other stream while the call still runs."""
     if stream.device.index != dev:
         _refuse("the stream must be of the tensors' device")
-    return stream.cuda_stream
+    return torch.cuda.stream(stream)
 
 
 def _table_width(t: torch.Tensor, rows: int, max_blocks: Optional[int]) -> int:
@@ -570,24 +572,46 @@ def _error_word(d_err: torch.Tensor, dev: int) -> int:
 
 
 class Batch:
-    """The metadata of a step, in buffers that kv_build_batch fills (made by batch_buffers or
-    build_batch; the tensors stay as they are made).  tree_mask is None without parents."""
+    """The metadata of a step, as kv_build_batch fills it (made by batch_buffers or build_batch): views
+    of one allocation.  tree_mask is None without parents."""
     FIELDS = ("query_start_loc", "seq_lens", "positions", "slot_mapping", "held_blocks", "free_next", "tree_mask")
-    __slots__ = FIELDS + ("_sizes", "_pointers")
+    __slots__ = ("_base", "_starts", "_views", "_sizes", "_at", "_pointers")
 
     def __init__(self, num_seqs: int, num_tokens: int, trees: bool, device):
-        def new(n, dtype=_i32):
-            return torch.empty(n, dtype=dtype, device=device)
-        self.query_start_loc, self.seq_lens = new(num_seqs + 1), new(num_seqs)
-        self.positions, self.slot_mapping = new(num_tokens), new(num_tokens, _i64)
-        self.held_blocks, self.free_next = new(num_seqs), new(1)
-        self.tree_mask = new(num_tokens, _i64) if trees else None
-        self._sizes = (num_seqs, num_tokens, trees, self.positions.get_device())
-        self._pointers = (_ptr(self.query_start_loc), _ptr(self.seq_lens), _ptr(self.positions),
-                          _ptr(self.slot_mapping), _ptr(self.tree_mask), _ptr(self.held_blocks), _ptr(self.free_next))
+        if num_tokens < 0:
+            _refuse("num_tokens must not be negative")
+        words = (num_seqs + 1, num_seqs, num_tokens, 2 * num_tokens, num_seqs, 1, 2 * num_tokens if trees else 0)
+        starts, end = [], 0  # of each field, in int32 words, on 16-byte boundaries
+        for n in words:
+            starts.append(end)
+            end += (n + 3) & ~3
+        self._base = base = torch.empty(end, dtype=_i32, device=device)
+        views = [base[at:at + n] for at, n in zip(starts, words)]
+        views[3] = views[3].view(_i64)
+        views[6] = views[6].view(_i64) if trees else None
+        self._views = tuple(views)
+        self._sizes = (num_seqs, num_tokens, trees, base.get_device())
+        self._starts = tuple(starts if trees else starts[:6] + [None])
+        self._at = None  # of which base _pointers are
+
+    query_start_loc = property(lambda self: self._views[0])
+    seq_lens = property(lambda self: self._views[1])
+    positions = property(lambda self: self._views[2])
+    slot_mapping = property(lambda self: self._views[3])
+    held_blocks = property(lambda self: self._views[4])
+    free_next = property(lambda self: self._views[5])
+    tree_mask = property(lambda self: self._views[6])
 
     def _asdict(self) -> dict:
-        return {name: getattr(self, name) for name in self.FIELDS}
+        return dict(zip(self.FIELDS, self._views))
+
+    def _place(self, base: int) -> tuple:
+        """The fields' addresses for kv_build_batch, once the allocation is at `base`."""
+        if not base:
+            _refuse("out: its memory has been released")
+        self._at = base
+        self._pointers = tuple(None if at is None else base + 4 * at for at in self._starts)
+        return self._pointers
 
 
 def batch_buffers(num_seqs: int, num_tokens: int, trees: bool = False, device="cuda") -> Batch:
@@ -607,10 +631,10 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     dev = context_lens.get_device()
     if dev < 0 or new_lens.get_device() != dev or block_table.get_device() != dev or free_blocks.get_device() != dev:
         _refuse(_DEVICES)
-    if dev != _current_device():
-        with torch.cuda.device(dev):
+    if stream is not None or dev != _current_device():
+        with torch.cuda.device(dev) if stream is None else _on(stream, dev):
             return build_batch(context_lens, new_lens, block_table, free_blocks, num_tokens, block_size, num_blocks,
-                               held_blocks, parents, free_start, out, d_err, max_blocks_per_seq, stream)
+                               held_blocks, parents, free_start, out, d_err, max_blocks_per_seq)
     B = context_lens.numel()
     if context_lens.dtype is not _i32 or not context_lens.is_contiguous():
         _refuse("context_lens: contiguous int32 [B]")
@@ -640,12 +664,13 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
         out = Batch(B, num_tokens, parents is not None, context_lens.device)
     elif out._sizes != (B, num_tokens, parents is not None, dev):
         _refuse("out: batch_buffers of these sizes, with trees exactly when parents are given, on this device")
-    qsl, lens, pos, slots, mask, held_out, free_next = out._pointers
+    at = out._base.data_ptr()
+    qsl, lens, pos, slots, held_out, free_next, mask = out._pointers if at == out._at else out._place(at)
     status = lib.kv_build_batch(
         context_lens.data_ptr(), new_lens.data_ptr(), held, par, B, num_tokens, block_table.data_ptr(),
         block_table.stride(0) if B > 1 else width, width, block_size, num_blocks, free_blocks.data_ptr(),
         free_blocks.numel(), start, qsl, lens, pos, slots, mask, held_out, free_next, err,
-        _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+        _raw_stream(dev))
     if status:
         _check(status)
     return out
@@ -665,14 +690,14 @@ def _token_stride(t: torch.Tensor, shape, dtype, dev: int, what: str) -> int:
 
 
 def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
-               interleaved, k_scale, v_scale, q_out, k_out, d_err, stream):
+               interleaved, k_scale, v_scale, q_out, k_out, d_err):
     dev, dt = q.get_device(), q.dtype
     if dev < 0 or q.dim() != 3 or key.dim() != 3:
         _refuse("q and key: [T, heads, D]; " + _DEVICES)
     if dev != _current_device():
         with torch.cuda.device(dev):
             return _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
-                              interleaved, k_scale, v_scale, q_out, k_out, d_err, stream)
+                              interleaved, k_scale, v_scale, q_out, k_out, d_err)
     qshape, kshape = q.shape, key.shape
     T, Hq, D = qshape
     if kshape[0] != T or kshape[2] != D:
@@ -728,7 +753,7 @@ def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache
     status = lib.kv_qk_norm_rope(
         q.data_ptr(), key.data_ptr(), vp, code, qs, ks, vs, T, Hq, Hkv, D, wq, wk, eps, pos, cs, max_pos, rot,
         1 if interleaved else 0, q_out.data_ptr(), qos, kout, kos, slots, kc, vc, cache_code, NB, bs, k_scale, v_scale,
-        err, _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+        err, _raw_stream(dev))
     if status:
         _check(status)
 
@@ -741,12 +766,15 @@ def qk_norm_rope(q: torch.Tensor, key: torch.Tensor, positions: Optional[torch.T
     """kv_qk_norm_rope without the cache: q [T, Hq, D] and key [T, Hkv, D] (views of one
     projection will do; token stride = stride(0)), positions int32 [T], cos_sin float32
     [max_position, rotary_dim].  q_out and k_out may be q and key."""
+    if stream is not None:
+        with _on(stream, q.get_device()):
+            return qk_norm_rope(q, key, positions, cos_sin, q_weight, k_weight, eps, interleaved, q_out, k_out, d_err)
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     if k_out is None:
         k_out = torch.empty(key.shape, dtype=key.dtype, device=key.device)
     _norm_rope(q, key, None, positions, cos_sin, None, None, None, q_weight, k_weight, eps, interleaved, 1.0, 1.0,
-               q_out, k_out, d_err, stream)
+               q_out, k_out, d_err)
     return q_out, k_out
 
 
@@ -760,12 +788,16 @@ def qk_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tens
                            stream=None) -> torch.Tensor:
     """kv_qk_norm_rope with the write of the turned keys and of the values into their slots;
     returns the queries (and fills k_out when it is given)."""
+    if stream is not None:
+        with _on(stream, q.get_device()):
+            return qk_norm_rope_and_cache(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight,
+                                          k_weight, eps, interleaved, k_scale, v_scale, q_out, k_out, d_err)
     if slot_mapping is None or value is None or k_cache is None or v_cache is None:
         _refuse("value, slot_mapping and both caches are needed")
     if q_out is None:
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps, interleaved,
-               k_scale, v_scale, q_out, k_out, d_err, stream)
+               k_scale, v_scale, q_out, k_out, d_err)
     return q_out
 
 
@@ -791,11 +823,11 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     dev, dt = q.get_device(), q.dtype
     if dev < 0 or q.dim() != 3 or not q.is_contiguous():
         _refuse("q: contiguous [T, heads, D]; " + _DEVICES)
-    if dev != _current_device():
-        with torch.cuda.device(dev):
+    if stream is not None or dev != _current_device():
+        with torch.cuda.device(dev) if stream is None else _on(stream, dev):
             return paged_attention_tree(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, tree_mask, max_seq_len,
                                         max_query_len, scale, window, num_workers, workspace, out, lse_out, d_err,
-                                        max_blocks_per_seq, stream)
+                                        max_blocks_per_seq)
     T, Hq, D = q.shape
     B = seq_lens.numel()
     cshape, cdt = k_cache.shape, k_cache.dtype
@@ -837,7 +869,7 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         v_cache.data_ptr(), _code_of.get(cdt, -1), Hkv, D, bs, NB, block_table.data_ptr(),
         block_table.stride(0) if B > 1 else width, width, seq_lens.data_ptr(), max_seq_len, scale, window,
         tree_mask.data_ptr(), num_workers, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-        out.data_ptr(), lse, err, _raw_stream(dev) if stream is None else _stream_of(stream, dev))
+        out.data_ptr(), lse, err, _raw_stream(dev))
     if status:
         _check(status)
     return out

@@ -713,9 +713,10 @@ def test_tree_small_workspace_is_refused(kc):
     need = kc.paged_attention_tree_workspace_size(1, 20, 8, 2, 128)
     if need == 0:
         pytest.skip("no workspace needed")
-    args = (c["q"].data_ptr(), 1, dev(c["qsl"]).data_ptr(), 1, 20, 20, 8, c["k"].data_ptr(), c["v"].data_ptr(), 1, 2, 128,
-            16, c["k"].shape[0], dev(c["table"]).data_ptr(), c["table"].shape[1], c["table"].shape[1],
-            dev(c["L"]).data_ptr(), 320, 0.1, 0, dev(c["masks"]).data_ptr(), 0)
+    qsl, table, lens, masks = (dev(c[x]) for x in ("qsl", "table", "L", "masks"))
+    args = (c["q"].data_ptr(), 1, qsl.data_ptr(), 1, 20, 20, 8, c["k"].data_ptr(), c["v"].data_ptr(), 1, 2, 128, 16,
+            c["k"].shape[0], table.data_ptr(), table.shape[1], table.shape[1], lens.data_ptr(), 320, 0.1, 0,
+            masks.data_ptr(), 0)
     ws = torch.empty(need + 256, dtype=torch.uint8, device="cuda")
     out = torch.empty_like(c["q"])
     f = kc.lib.kv_paged_attention_tree
@@ -868,6 +869,43 @@ def test_steps_on_two_streams_at_once(kc):
     torch.cuda.synchronize()
     a.out[int(a.new.sum()):] = 7.0
     a.check()
+
+
+def test_memory_of_a_call_on_another_stream(kc, monkeypatch):
+    """The workspace that a call on a given stream makes for itself is that stream's: what the current
+    stream allocates next, while the call may still run, lies elsewhere."""
+    s = Step(kc, 46)
+    s.run()
+    torch.cuda.synchronize()
+    seen = []
+    real = kc.lib.kv_paged_attention_tree
+
+    def call(*args):
+        seen.append((args[23], args[24], args[25]))  # workspace, its bytes, out
+        return real(*args)
+    monkeypatch.setattr(kc.lib, "kv_paged_attention_tree", call)
+    b, st = s.batch, torch.cuda.Stream()
+    args = (s.q_out, s.kcache, s.vcache, s.d["table"], b.seq_lens, b.query_start_loc, b.tree_mask, s.max_len, s.max_new,
+            s.D ** -0.5)
+    s.out.fill_(7.0)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        kc.paged_attention_tree(*args, out=s.out, d_err=s.err, stream=st)
+        at, size, _ = seen[-1]
+        other = [torch.full((size,), 255, dtype=torch.uint8, device="cuda") for _ in range(2)]
+        assert all(x.data_ptr() + size <= at or at + size <= x.data_ptr() for x in other)
+        del other
+    s.check()
+    out = kc.paged_attention_tree(*args, stream=st)
+    st.synchronize()
+    n = int(s.new.sum())
+    assert torch.equal(out[:n], s.out[:n]) and seen[-1][2] == out.data_ptr()
+    with torch.cuda.stream(st):
+        assert torch.cuda.current_stream() == st
+        q1 = kc.qk_norm_rope(s.q, s.k, b.positions, s.cs, s.wq, s.wk)[0]
+    q2 = kc.qk_norm_rope(s.q, s.k, b.positions, s.cs, s.wq, s.wk, stream=st)[0]
+    torch.cuda.synchronize()
+    assert torch.equal(q1[:n], q2[:n])
 
 
 def test_step_after_step(kc):

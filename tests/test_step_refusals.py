@@ -54,7 +54,7 @@ def call(kc, fn, base, **changes):
     (dict(free_start=11 * P), INVALID),                                          # the list's start in place
     (dict(query_start_loc=7 * P - 16), INVALID),                                 # two outputs: five words, then lens
     (dict(slot_mapping=8 * P), INVALID), (dict(free_next=4 * P + 4 * 31), INVALID),
-    (dict(free_next=5 * P), INVALID),
+    (dict(free_next=5 * P), INVALID), (dict(num_seqs=(1 << 24) + 1), UNSUPPORTED),
 ])
 def test_build_batch_refuses(kc, changes, status):
     assert call(kc, "kv_build_batch", BATCH, **changes) == status
@@ -79,6 +79,16 @@ def test_build_batch_refuses(kc, changes, status):
     (dict(q_out=P, q_out_stride=1024), INVALID),                                 # in place, another stride
     (dict(cache_dtype=2, k_scale=0.0), INVALID), (dict(cache_dtype=2, v_scale=float("nan")), INVALID),
     (dict(block_size=0), INVALID), (dict(num_blocks=-1), INVALID),
+    (dict(q_heads=65536, q_stride=1 << 23, q_out_stride=1 << 23), UNSUPPORTED), (dict(kv_heads=1 << 20), UNSUPPORTED),
+    # outputs over something: 4 tokens, 4 query heads and one key head of 256 bytes
+    (dict(q_out=2 * P), INVALID), (dict(k_out=3 * P), INVALID), (dict(q_out=P + 1024), INVALID),
+    (dict(q_out=P - 16), INVALID), (dict(k_out=8 * P + 16), INVALID), (dict(k_out=2 * P + 16), INVALID),
+    (dict(q_out=P, q_stride=512, key=P + 512, key_stride=512), INVALID),
+    (dict(k_out=P + 1008, key=P + 1024, q_stride=640, key_stride=640, k_out_stride=640), INVALID),
+    (dict(q_out=4 * P - 3840), INVALID), (dict(k_out=5 * P), INVALID), (dict(k_out=6 * P - 256), INVALID),
+    (dict(q_out=7 * P), INVALID), (dict(k_out=10 * P + 16), INVALID),
+    (dict(k_cache=12 * P), INVALID), (dict(k_cache=12 * P - 32752), INVALID), (dict(v_cache=3 * P - 16), INVALID),
+    (dict(v_cache=8 * P), INVALID), (dict(k_cache=7 * P), INVALID), (dict(k_cache=10 * P), INVALID),
 ])
 def test_qk_norm_rope_refuses(kc, changes, status):
     assert call(kc, "kv_qk_norm_rope", ROPE, **changes) == status
@@ -99,10 +109,52 @@ def test_qk_norm_rope_refuses(kc, changes, status):
     (dict(block_table=None), INVALID), (dict(seq_lens=None), INVALID), (dict(out=None), INVALID),
     (dict(k_cache=None), INVALID), (dict(q=P + 8), INVALID), (dict(out=8 * P + 4), INVALID),
     (dict(tree_mask=7 * P + 4), INVALID), (dict(seq_lens=6 * P + 2), INVALID), (dict(lse_out=9 * P + 2), INVALID),
+    (dict(scale=3e38), INVALID),
+    (dict(out=P), INVALID), (dict(out=P + 8176), INVALID), (dict(out=7 * P), INVALID), (dict(out=3 * P), INVALID),
+    (dict(lse_out=8 * P + 8188), INVALID), (dict(lse_out=6 * P), INVALID), (dict(lse_out=5 * P + 60), INVALID),
+    (dict(workspace=8 * P, workspace_bytes=1 << 16), INVALID), (dict(workspace=P, workspace_bytes=1 << 16), INVALID),
+    (dict(workspace=2 * P - 256, workspace_bytes=1 << 16), INVALID), (dict(workspace=4 * P, workspace_bytes=1 << 62), INVALID),
 ])
 def test_tree_attention_refuses(kc, changes, status):
     assert call(kc, "kv_paged_attention_tree", TREE, **changes) == status
     assert kc.lib.kv_last_error()
+
+
+def test_views_of_one_projection_are_not_an_overlap(kc):
+    """Rows of one stride may lie between each other: such calls pass every check up to the device's, which
+    needs a machine without one (the pointers are made up)."""
+    if torch.cuda.is_available():
+        pytest.skip("made-up pointers stay off a device")
+    qkv = dict(q=P, key=P + 1024, value=P + 1280, q_stride=768, key_stride=768, value_stride=768)
+    for out in (dict(), dict(q_out=P, q_out_stride=768), dict(k_out=P + 1024, k_out_stride=768),
+                dict(q_out=P, q_out_stride=768, k_out=P + 1024, k_out_stride=768),
+                dict(q_out=8 * P, k_out=8 * P + 1024, q_out_stride=640, k_out_stride=640)):
+        assert call(kc, "kv_qk_norm_rope", ROPE, **qkv, **out) == CUDA
+    assert call(kc, "kv_qk_norm_rope", ROPE, **qkv, q_out=P + 16, q_out_stride=768) == INVALID
+
+
+def test_batch_buffers_follow_their_memory(kc):
+    import copy
+    a = kc.batch_buffers(5, 21, True, device="cpu")
+    for b in (a, copy.deepcopy(a), copy.copy(a)):
+        got = b._place(b._base.data_ptr())
+        views = (b.query_start_loc, b.seq_lens, b.positions, b.slot_mapping, b.held_blocks, b.free_next, b.tree_mask)
+        assert got == tuple(v.data_ptr() for v in views)
+        assert [v.numel() for v in views] == [6, 5, 21, 21, 5, 1, 21]
+        assert [v.dtype for v in views] == [torch.int32] * 3 + [torch.int64] + [torch.int32] * 2 + [torch.int64]
+        assert all(v.data_ptr() % 16 == 0 for v in views)
+        ends = sorted((v.data_ptr(), v.data_ptr() + v.numel() * v.element_size()) for v in views)
+        assert all(x[1] <= y[0] for x, y in zip(ends, ends[1:])) and ends[-1][1] <= b._base.data_ptr() + 4 * b._base.numel()
+    assert copy.deepcopy(a).positions.data_ptr() != a.positions.data_ptr()
+    with pytest.raises(AttributeError):
+        a.positions = torch.empty(21, dtype=torch.int32)
+    plain = kc.batch_buffers(0, 0, device="cpu")
+    assert plain.tree_mask is None and plain._place(plain._base.data_ptr())[6] is None
+    with pytest.raises(kc.KVError):
+        kc.batch_buffers(2, -1, device="cpu")
+    a._base.untyped_storage().resize_(0)
+    with pytest.raises(kc.KVError, match="released"):
+        a._place(a._base.data_ptr())
 
 
 def test_nothing_to_do_needs_no_device(kc):
