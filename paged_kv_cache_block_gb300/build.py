@@ -24,7 +24,7 @@ SOURCES = ["api.cu", "slot_mapping.cu", "reshape_and_cache.cu", "paged_attention
            "block_updates.cu", "block_manager.cpp", "prefill_attention.cu", "paged_decode_int4.cu",
            "selftest.cu", "paged_attention_fp8.cu", "build_batch.cu", "qk_norm_rope.cu", "tree_attention.cu",
            "tree_packed.cu"]
-HEADERS = ["common.cuh", "tcgen05.cuh", "tree_common.cuh", "decode_common.cuh", "paged_decode_kernel.cuh", "kernels.h"]
+HEADERS = ["common.cuh", "dependent_launch.cuh", "tcgen05.cuh", "tree_common.cuh", "decode_common.cuh", "paged_decode_kernel.cuh", "kernels.h"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr", "-Xcompiler", "-fPIC",
          "-Xcompiler", "-fvisibility=hidden", "-I", os.path.join(ROOT, "include")]

@@ -12,6 +12,7 @@
 // of 557,000 tokens 9.7 and 7.8.  With trees a warp takes a request, whose at most 64 tokens find their
 // ancestors by pointer jumping between lanes (128 trees: 5.1 us, 6.8 when each token walked up by itself).
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "kernels.h"
 
 namespace pkv {
@@ -185,6 +186,7 @@ __global__ void __launch_bounds__(kThreads) build_batch_kernel(const BatchArgs a
     const int shift = a.block_shift;
     const int64_t stride = static_cast<int64_t>(gridDim.x) * kThreads;
     const int64_t gtid = static_cast<int64_t>(blockIdx.x) * kThreads + tid;
+    previous_kernel_done();
     const int32_t start = a.free_start ? *a.free_start : 0;
     // a start outside the list: nothing can be taken
     const int64_t avail = start >= 0 && start <= a.num_free ? a.num_free - start : 0;
@@ -281,8 +283,8 @@ cudaError_t launch_build_batch(const BatchArgs &args, int sm_count, cudaStream_t
     // a request a warp, or a token or four a thread
     const int64_t threads = a.parents ? 32 * static_cast<int64_t>(a.num_seqs) : (a.fours ? a.num_tokens / 4 + 1 : a.num_tokens);
     const int64_t want = (threads + kThreads - 1) / kThreads;
-    build_batch_kernel<<<static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most)), kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(build_batch_kernel, dim3(static_cast<unsigned>(want < 1 ? 1 : (want < most ? want : most))),
+                            dim3(kThreads), 0, stream, a);
 }
 
 }  // namespace pkv

@@ -17,6 +17,7 @@
 // at a time before the first is used, once there are tokens enough to fill the GPU; fewer heads a
 // warp below that (see launch_lanes).
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
 
@@ -78,6 +79,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(con
     const int lane = threadIdx.x & 31;
     const int64_t t = static_cast<int64_t>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5);
     int part = blockIdx.y;
+    previous_kernel_done();
     if (t >= a.num_tokens) return;
     const bool reports = part == 0 && lane == 0;
     const int32_t pos = a.positions ? a.positions[t] : 0;
@@ -271,9 +273,8 @@ cudaError_t launch_lanes(RopeArgs a, int sm_count, cudaStream_t stream) {
     // a warp a token, the parts of its heads along y (fewer than 65536: n is halved only below 32 warps an
     // SM, and 65535 heads of each kind make at most 6144 parts at first)
     const dim3 grid((static_cast<unsigned>(a.num_tokens) + kThreads / 32 - 1) / (kThreads / 32), all());
-    if (a.interleaved) qk_norm_rope_kernel<T, LP, true, kD><<<grid, kThreads, 0, stream>>>(a);
-    else qk_norm_rope_kernel<T, LP, false, kD><<<grid, kThreads, 0, stream>>>(a);
-    return cudaGetLastError();
+    return launch_dependent(a.interleaved ? qk_norm_rope_kernel<T, LP, true, kD> : qk_norm_rope_kernel<T, LP, false, kD>,
+                            grid, dim3(kThreads), 0, stream, a);
 }
 
 template <typename T> cudaError_t launch_typed(const RopeArgs &a, int sm_count, cudaStream_t stream) {

@@ -88,7 +88,6 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     auto bar_full = [&](int s) { return smem_u32(&bars[kBarKv + s]); };
     auto bar_empty = [&](int s) { return smem_u32(&bars[kBarKv + kStages + s]); };
 
-    asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 32) {
         prefetch_tensormap(&tmap_q);
         prefetch_tensormap(&tmap_k);
@@ -124,6 +123,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
     ShareScratch &scratch = *reinterpret_cast<ShareScratch *>(join);
     int64_t x0, x1;
     int item_cost;
+    previous_kernel_done();
+    let_next_kernel_launch();
     share_of_cta<kThreads>(p, c, x0, x1, item_cost, scratch);
     zero_rejected<T, D>(p);
     tc_fence_before();

@@ -7,6 +7,7 @@
 #include <type_traits>
 
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "kernels.h"
 #include "tcgen05.cuh"
 
@@ -356,7 +357,7 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);   // 8 dims of 32 rows
     const int rr = unit / (D / 8) * 32 + lane, q = unit % (D / 8) * 2;
-    asm volatile("griddepcontrol.wait;" ::: "memory");  // the attention kernel's results
+    previous_kernel_done();  // the attention kernel's results
     // lane i: the first piece of share c + i (none past the last)
     const int4 none = make_int4(-1, 0, 0, 0);
     int4 rec = c + lane < p.workers ? __ldcg(&p.ws_first[2 * (c + lane)]) : none;
@@ -450,21 +451,16 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    kernel<<<p.workers, threads, smem, stream>>>(tq, tk, tv, p);
-    cudaError_t e = cudaGetLastError();
+    // The attention kernel waits for the kernel before it once its barriers and TMEM are set up, and lets the
+    // merge launch then, which waits at once (a CTA of it does not fit beside one of the attention kernel's,
+    // whose registers fill the SM).  Calls in a stream take 18.0, 54.7, 206.5, 359 us so; 20.5, 57.4, 210, 365
+    // when only the merge is launched this way and 22.6, 60.6, 212, 365 when neither is (a sequence of 1117
+    // keys; 64 of OPT-125m; a window of 4096; 38 trees of 48 tokens).  Letting the next kernel launch at the merge's start:
+    // 17.7, 54.5, 207.7, 361.6.
+    const cudaError_t e = launch_dependent(kernel, dim3(p.workers), dim3(threads), smem, stream, tq, tk, tv, p);
     if (e != cudaSuccess || p.workers < 2) return e;
-    // the merge is launched while the attention kernel runs, and waits for its end (a CTA of it does not
-    // fit beside one of the attention kernel's, whose registers fill the SM)
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(p.workers - 1, p.rows_per_item / 32 * (D / 8) / 8);
-    cfg.blockDim = dim3(256);
-    cfg.stream = stream;
-    cudaLaunchAttribute at[1];
-    at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    at[0].val.programmaticStreamSerializationAllowed = 1;
-    cfg.attrs = at;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, tree_merge_kernel<T, D>, p);
+    return launch_dependent(tree_merge_kernel<T, D>, dim3(p.workers - 1, p.rows_per_item / 32 * (D / 8) / 8), dim3(256), 0,
+                            stream, p);
 }
 
 // Items of several kv heads (tree_packed.cu): the plan for `rows` query rows a head (heads_per_item

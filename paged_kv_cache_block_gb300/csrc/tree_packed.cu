@@ -81,7 +81,6 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     int32_t *cleaned = reinterpret_cast<int32_t *>(smem + PK::kOffMisc + 8 + 4 * kFlags);  // [kStages]: entry + 1
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
 
-    asm volatile("griddepcontrol.launch_dependents;");
     if (threadIdx.x == 32) {
         prefetch_tensormap(&tmap_q);
         prefetch_tensormap(&tmap_k);
@@ -114,6 +113,8 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
     __shared__ ShareScratch scratch;
     int64_t x0, x1;
     int item_cost;
+    previous_kernel_done();
+    let_next_kernel_launch();
     share_of_cta<PK::kThreads>(p, c, x0, x1, item_cost, scratch);
     zero_rejected<T, D>(p);
     tc_fence_before();
