@@ -554,15 +554,22 @@ def _on(stream, dev: int):
     return torch.cuda.stream(stream)
 
 
-def _table_width(t: torch.Tensor, rows: int, max_blocks: Optional[int]) -> int:
-    if t.dtype is not _i32 or t.dim() != 2 or t.shape[0] != rows or (rows and t.shape[1] > 1 and t.stride(1) != 1):
-        _refuse("block_table: int32 [B, W] with rows in one piece")
-    width = t.shape[1]
+def _table(t: torch.Tensor, rows: int, max_blocks: Optional[int]) -> Tuple[int, int]:
+    """Row stride and width of a block table [B, W]."""
+    shape = t.shape
+    if t.dtype is not _i32 or len(shape) != 2 or shape[0] != rows:
+        _refuse("block_table: int32 [B, W]")
+    width = shape[1]
+    stride, step = t.stride()
+    if step != 1 and rows and width > 1:
+        _refuse("block_table: rows in one piece")
+    if rows < 2:
+        stride = width
     if max_blocks is None:
-        return width
+        return stride, width
     if not 0 <= max_blocks <= width:
         _refuse("max_blocks_per_seq is past the table's rows")
-    return max_blocks
+    return stride, max_blocks
 
 
 def _error_word(d_err: torch.Tensor, dev: int) -> int:
@@ -659,7 +666,7 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
         start = free_start.data_ptr()
     if d_err is not None:
         err = _error_word(d_err, dev)
-    width = _table_width(block_table, B, max_blocks_per_seq)
+    bt_stride, width = _table(block_table, B, max_blocks_per_seq)
     if out is None:
         out = Batch(B, num_tokens, parents is not None, context_lens.device)
     elif out._sizes != (B, num_tokens, parents is not None, dev):
@@ -668,7 +675,7 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     qsl, lens, pos, slots, held_out, free_next, mask = out._pointers if at == out._at else out._place(at)
     status = lib.kv_build_batch(
         context_lens.data_ptr(), new_lens.data_ptr(), held, par, B, num_tokens, block_table.data_ptr(),
-        block_table.stride(0) if B > 1 else width, width, block_size, num_blocks, free_blocks.data_ptr(),
+        bt_stride, width, block_size, num_blocks, free_blocks.data_ptr(),
         free_blocks.numel(), start, qsl, lens, pos, slots, mask, held_out, free_next, err,
         _raw_stream(dev))
     if status:
@@ -676,40 +683,56 @@ def build_batch(context_lens: torch.Tensor, new_lens: torch.Tensor, block_table:
     return out
 
 
-def _token_stride(t: torch.Tensor, shape, dtype, dev: int, what: str) -> int:
-    """The token stride of a [T, heads, D] tensor whose heads lie in one piece (that of a single
-    token means nothing; it only has to hold the row)."""
-    if t.dtype is not dtype or t.shape != shape or t.get_device() != dev:
-        _refuse(f"{what}: {dtype} {list(shape)} on the same device")
-    T, H, D = shape
-    s0, s1, s2 = t.stride()
-    if s2 != 1 or s1 != D:
-        if T and (s2 != 1 or H > 1):
-            _refuse(f"{what}: each token's heads in one piece")
-    return s0 if T > 1 else -(-H * D // 8) * 8
+def _odd_rows(t: torch.Tensor, what: str) -> None:
+    """A [T, heads, D] tensor whose strides are not (any, D, 1): an error if they mean something."""
+    T, H, _ = t.shape
+    if T and (t.stride(2) != 1 or H > 1):
+        _refuse(f"{what}: each token's heads in one piece")
 
 
 def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
                interleaved, k_scale, v_scale, q_out, k_out, d_err):
     dev, dt = q.get_device(), q.dtype
-    if dev < 0 or q.dim() != 3 or key.dim() != 3:
+    qshape, kshape = q.shape, key.shape
+    if dev < 0 or len(qshape) != 3 or len(kshape) != 3:
         _refuse("q and key: [T, heads, D]; " + _DEVICES)
     if dev != _current_device():
         with torch.cuda.device(dev):
             return _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
                               interleaved, k_scale, v_scale, q_out, k_out, d_err)
-    qshape, kshape = q.shape, key.shape
     T, Hq, D = qshape
     if kshape[0] != T or kshape[2] != D:
         _refuse("q and key differ in tokens or head size")
     Hkv = kshape[1]
-    qs = _token_stride(q, qshape, dt, dev, "q")
-    ks = _token_stride(key, kshape, dt, dev, "key")
-    qos = _token_stride(q_out, qshape, dt, dev, "q_out")
+    # token strides (that of a single token means nothing; it only has to hold the row)
+    qs, s1, s2 = q.stride()
+    if s2 != 1 or s1 != D:
+        _odd_rows(q, "q")
+    ks, s1, s2 = key.stride()
+    if key.dtype is not dt or key.get_device() != dev:
+        _refuse(f"key: {dt} on the same device")
+    if s2 != 1 or s1 != D:
+        _odd_rows(key, "key")
+    if q_out.dtype is not dt or q_out.shape != qshape or q_out.get_device() != dev:
+        _refuse(f"q_out: {dt} {list(qshape)} on the same device")
+    qos, s1, s2 = q_out.stride()
+    if s2 != 1 or s1 != D:
+        _odd_rows(q_out, "q_out")
+    one_k = -(-Hkv * D // 8) * 8
+    if T < 2:
+        qs = qos = -(-Hq * D // 8) * 8
+        ks = one_k
     pos = cs = wq = wk = kout = err = None
     kos = max_pos = rot = 0
     if k_out is not None:
-        kos, kout = _token_stride(k_out, kshape, dt, dev, "k_out"), k_out.data_ptr()
+        if k_out.dtype is not dt or k_out.shape != kshape or k_out.get_device() != dev:
+            _refuse(f"k_out: {dt} {list(kshape)} on the same device")
+        kos, s1, s2 = k_out.stride()
+        if s2 != 1 or s1 != D:
+            _odd_rows(k_out, "k_out")
+        if T < 2:
+            kos = one_k
+        kout = k_out.data_ptr()
     if q_weight is not None:
         if q_weight.dtype is not dt or q_weight.numel() != D or not q_weight.is_contiguous() or q_weight.get_device() != dev:
             _refuse(f"q_weight: contiguous {dt} [{D}] on the same device")
@@ -724,9 +747,10 @@ def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache
             _refuse("positions: contiguous int32 [T] on the same device")
         pos = positions.data_ptr()
     if cos_sin is not None:
-        if cos_sin.dtype is not _f32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
+        cs_shape = cos_sin.shape
+        if cos_sin.dtype is not _f32 or len(cs_shape) != 2 or not cos_sin.is_contiguous() or cos_sin.get_device() != dev:
             _refuse("cos_sin: contiguous float32 [max_position, rotary_dim] on the same device")
-        max_pos, rot = cos_sin.shape
+        max_pos, rot = cs_shape
         cs = cos_sin.data_ptr()
     if d_err is not None:
         err = _error_word(d_err, dev)
@@ -737,7 +761,13 @@ def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache
         if slot_mapping.dtype is not _i64 or slot_mapping.numel() != T or not slot_mapping.is_contiguous() or \
                 slot_mapping.get_device() != dev:
             _refuse("slot_mapping: contiguous int64 [T] on the same device")
-        vs = _token_stride(value, kshape, dt, dev, "value")
+        if value.dtype is not dt or value.shape != kshape or value.get_device() != dev:
+            _refuse(f"value: {dt} {list(kshape)} on the same device")
+        vs, s1, s2 = value.stride()
+        if s2 != 1 or s1 != D:
+            _odd_rows(value, "value")
+        if T < 2:
+            vs = one_k
         cshape, cdt = k_cache.shape, k_cache.dtype
         if len(cshape) != 4 or cshape[2] != Hkv or cshape[3] != D or v_cache.shape != cshape or \
                 v_cache.dtype is not cdt or not k_cache.is_contiguous() or not v_cache.is_contiguous() or \
@@ -846,7 +876,7 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
         _refuse("tree_mask: contiguous int64 [T] on the same device")
     if block_table.get_device() != dev:
         _refuse(_DEVICES)
-    width = _table_width(block_table, B, max_blocks_per_seq)
+    bt_stride, width = _table(block_table, B, max_blocks_per_seq)
     err = lse = None
     if d_err is not None:
         err = _error_word(d_err, dev)
@@ -867,7 +897,7 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     status = lib.kv_paged_attention_tree(
         q.data_ptr(), _code_of.get(dt, -1), query_start_loc.data_ptr(), B, T, max_query_len, Hq, k_cache.data_ptr(),
         v_cache.data_ptr(), _code_of.get(cdt, -1), Hkv, D, bs, NB, block_table.data_ptr(),
-        block_table.stride(0) if B > 1 else width, width, seq_lens.data_ptr(), max_seq_len, scale, window,
+        bt_stride, width, seq_lens.data_ptr(), max_seq_len, scale, window,
         tree_mask.data_ptr(), num_workers, workspace.data_ptr(), workspace.numel() * workspace.element_size(),
         out.data_ptr(), lse, err, _raw_stream(dev))
     if status:
