@@ -300,18 +300,20 @@ kv_status encode_query_map(CUtensorMap *m, const void *base, int32_t num_tokens,
     return KV_OK;
 }
 
-// A 16-bit cache viewed as (dim, token of 8, head, group of 8 tokens, block); one box = one block's rows
-// for a group of heads, 64 dims, swizzled 128B, laid out as [group of 8 tokens][head][token][dim]: the
-// 8-row swizzle atoms of one head then lie a constant distance apart over any number of blocks.
+// A 16-bit cache viewed as (dim of 64, token of 8, 64 dims of a head, group of 8 tokens, block); one box =
+// one block's rows for a group of heads, swizzled 128B, laid out as [group of 8 tokens][head][64 dims of
+// it][token][dim]: the 8-row swizzle atoms of 64 dims of one head then lie a constant distance apart over
+// any number of blocks.
 kv_status encode_heads_map(CUtensorMap *m, const void *base, int32_t num_blocks, int32_t block_size,
                            int32_t num_kv_heads, int32_t head_dim, int32_t heads) {
     auto fn = encode_fn();
     if (!fn) return fail(KV_ERR_CUDA, "cuTensorMapEncodeTiled is not available from the driver");
-    const uint64_t head = 2ull * head_dim, token = head * num_kv_heads;
-    const cuuint64_t dims[5] = {static_cast<cuuint64_t>(head_dim), 8, static_cast<cuuint64_t>(num_kv_heads),
+    const uint32_t parts = head_dim / 64;
+    const uint64_t token = 2ull * head_dim * num_kv_heads;
+    const cuuint64_t dims[5] = {64, 8, static_cast<cuuint64_t>(num_kv_heads) * parts,
                                 static_cast<cuuint64_t>(block_size / 8), static_cast<cuuint64_t>(num_blocks)};
-    const cuuint64_t strides[4] = {token, head, 8 * token, token * block_size};
-    const cuuint32_t box[5] = {64, 8, static_cast<cuuint32_t>(heads), static_cast<cuuint32_t>(block_size / 8), 1};
+    const cuuint64_t strides[4] = {token, 128, 8 * token, token * block_size};
+    const cuuint32_t box[5] = {64, 8, heads * parts, static_cast<cuuint32_t>(block_size / 8), 1};
     const cuuint32_t estr[5] = {1, 1, 1, 1, 1};
     CUresult r = fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 5, const_cast<void *>(base), dims, strides, box, estr,
                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
@@ -1292,9 +1294,7 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     for (int i = 0; i < 2 && st == KV_OK; ++i) {
         CUtensorMap *m = i ? &tv : &tk;
         const void *cache = i ? v_cache : k_cache;
-        st = plan.heads_per_item > 1
-                 ? encode_heads_map(m, cache, num_blocks, block_size, num_kv_heads, head_dim, plan.heads_per_item)
-                 : encode_cache_map(m, cache, cache_dtype, num_blocks, block_size, num_kv_heads, head_dim, 1);
+        st = encode_heads_map(m, cache, num_blocks, block_size, num_kv_heads, head_dim, plan.heads_per_item);
     }
     if (st != KV_OK) return st;
     pkv::TreeArgs a;

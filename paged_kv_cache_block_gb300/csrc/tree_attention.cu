@@ -42,6 +42,7 @@ constexpr uint32_t kColO = 256;
 template <int D> struct Tile {
     static constexpr int kHalves = D / 64;
     static constexpr int kBytes = kHalves * kHalf;      // a Q, K or V tile
+    static constexpr int kGroup = kHalves * 1024;       // 8 keys of a K or V tile: [64 dims of D][key][dim]
     static constexpr int kStages = D == 128 ? 5 : 10;   // ring entries (160 KB)
     static constexpr int kOffKV = 2 * kBytes;           // after Q_0, Q_1
     static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // chain 1's maximum and sums: 3 x 128 floats
@@ -207,9 +208,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     for (int jb = 0; jb < bpt; ++jb) {
                         const int id = __shfl_sync(0xffffffffu, my_id, jb);
                         if (lane == 0)
-                            for (int hf = 0; hf < TL::kHalves; ++hf)
-                                tma_load_4d(smem_u32(dst + hf * kHalf + jb * bs * 128), m, bar_full(slot), 64 * hf, 0,
-                                            h, id);
+                            tma_load_5d(smem_u32(dst + jb * bs * TL::kHalves * 128), m, bar_full(slot), 0, 0,
+                                        h * TL::kHalves, 0, id);
                     }
                     ++entry;
                 }
@@ -233,8 +233,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         constexpr uint32_t idesc_s = mma_idesc(ab, false, kBM, kBN);
         constexpr uint32_t idesc_pv = mma_idesc(ab, true, kBM, D);
         if (lane == 0) {
-            const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, 1024);
-            const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), kHalf, 1024);
+            const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, TL::kGroup);
+            const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), 1024, TL::kGroup);
             const uint32_t t_s = tmem + x * 128, t_o = tmem + kColO + x * 128;
             auto full = [&](int e) { return mbar_wait_bounded(bar_full(e % kStages), (e / kStages) & 1); };
             int base = 0;  // key tiles of the pieces before
@@ -275,8 +275,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     const uint64_t dk = dkv + static_cast<uint64_t>((sk * kTileBytes) >> 4);
 #pragma unroll
                     for (int k = 0; k < D / 16; ++k) {
-                        const uint64_t off = ((k >> 2) * kHalf + (k & 3) * 32) >> 4;
-                        mma_f16(t_s, dq + off, dk + off, idesc_s, k > 0);
+                        const int in = (k & 3) * 32;
+                        mma_f16(t_s, dq + (((k >> 2) * kHalf + in) >> 4), dk + (((k >> 2) * 1024 + in) >> 4), idesc_s, k > 0);
                     }
                     mma_commit(bar(kBarS + x));
                     mma_commit(bar_empty(sk));
@@ -290,7 +290,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     const uint64_t dv = dv0 + static_cast<uint64_t>((sv * kTileBytes) >> 4);
 #pragma unroll
                     for (int k = 0; k < 8; ++k)
-                        mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2048) >> 4), idesc_pv, j > first || k > 0);
+                        mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2 * TL::kGroup) >> 4), idesc_pv, j > first || k > 0);
                     mma_commit(bar(kBarPd + x));
                     mma_commit(bar_empty(sv));
                     if (last) mma_commit(bar(kBarPv + x));
@@ -336,7 +336,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                     lo = max(lo, k0) - k0;
                     hi = min(hi, k0 + kBN) - k0;
                     for (int i = lo * 8 + lane; i < hi * 8; i += 32)
-                        for (int hf = 0; hf < TL::kHalves; ++hf) clean_chunk<T>(tile + hf * kHalf + i * 16, zero, odd);
+                        for (int hf = 0; hf < TL::kHalves; ++hf)
+                            clean_chunk<T>(tile + (i >> 6) * TL::kGroup + hf * 1024 + (i & 63) * 16, zero, odd);
                 };
                 if (a.window > 0) {
                     clean(s.kv_lo / bs * bs, s.kv_lo, true);

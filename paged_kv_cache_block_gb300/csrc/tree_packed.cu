@@ -44,8 +44,8 @@ template <int D, int PH, int MT> struct Pack {
     static constexpr int kSoftmax = 4 * MT;                  // warps
     static constexpr int kThreads = (kSoftmax + 2 + PH) * 32;
     static constexpr int kQBytes = kHalves * kHalf;          // Q of a row tile
-    static constexpr int kSide = kKeys * PH * 128;           // 64 dims of a key tile of all heads
-    static constexpr int kEntry = kHalves * kSide;
+    static constexpr int kGroup = PH * kHalves * 1024;       // 8 keys: [head][64 dims of D][key][dim]
+    static constexpr int kEntry = kKeys / 8 * kGroup;        // a key tile
     static constexpr int kOffKV = MT * kQBytes;
     static constexpr int kFit = (224 * 1024 - kOffKV) / kEntry;  // ring entries, 160 or 192 KB
     static constexpr int kStages = kFit > 6 ? 6 : kFit;
@@ -198,9 +198,8 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     for (int jb = 0; jb < bpt; ++jb) {
                         const int id = __shfl_sync(0xffffffffu, my_id, jb);
                         if (lane == 0)
-                            for (int hf = 0; hf < PK::kHalves; ++hf)
-                                tma_load_5d(smem_u32(dst + hf * PK::kSide + jb * bs * PH * 128), m, bar(kBarFull + slot),
-                                            64 * hf, 0, h0, 0, id);
+                            tma_load_5d(smem_u32(dst + bs / 8 * jb * PK::kGroup), m, bar(kBarFull + slot), 0, 0,
+                                        h0 * PK::kHalves, 0, id);
                     }
                     ++entry;
                 }
@@ -220,10 +219,10 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
         constexpr uint32_t idesc_pv = mma_idesc(ab, true, kTreeRows, D);
         if (lane == 0) {
             const uint64_t dq = smem_desc(smem_u32(smem + h / kPerTile * PK::kQBytes), 16, 1024);
-            // one head's atoms (8 keys x 64 dims, 1 KB) are PH KB apart
-            const uint32_t kv = smem_u32(smem + PK::kOffKV) + h * 1024;
-            const uint64_t dk0 = smem_desc(kv, 16, PH * 1024);
-            const uint64_t dv0 = smem_desc(kv, PK::kSide, PH * 1024);
+            // a head's swizzle atoms (8 keys x 64 dims, 1 KB): those of the next keys are kGroup bytes on
+            const uint32_t kv = smem_u32(smem + PK::kOffKV) + h * PK::kHalves * 1024;
+            const uint64_t dk0 = smem_desc(kv, 16, PK::kGroup);
+            const uint64_t dv0 = smem_desc(kv, 1024, PK::kGroup);
             const uint32_t t_s = tmem + h * kKeys, t_p = tmem + PK::kColP + h * (kKeys / 2);
             const uint32_t t_o = tmem + PK::kColO + h / kPerTile * D;
             uint32_t off[4];  // the other heads' lanes
@@ -236,7 +235,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
 #pragma unroll
                 for (int k = 0; k < D / 16; ++k)
                     mma_f16(t_s, dq + (((k >> 2) * kHalf + (k & 3) * 32) >> 4),
-                            dk + (((k >> 2) * PK::kSide + (k & 3) * 32) >> 4), idesc_s, k > 0);
+                            dk + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idesc_s, k > 0);
                 mma_commit(bar(kBarS + h));
                 mma_commit(bar(kBarEmpty + sk));
             };
@@ -269,7 +268,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     const uint64_t dv = dv0 + static_cast<uint64_t>((sv * PK::kEntry) >> 4);
 #pragma unroll
                     for (int k = 0; k < kKeys / 16; ++k) {
-                        const uint64_t db = dv + ((k * PH * 2048) >> 4);
+                        const uint64_t db = dv + ((k * 2 * PK::kGroup) >> 4);
                         if constexpr (kPerTile == 1) mma_f16_ts(t_o, t_p + k * 8, db, idesc_pv, t > 0 || k > 0);
                         else mma_f16_ts_rows(t_o, t_p + k * 8, db, idesc_pv, t > 0 || k > 0, off);
                     }
@@ -325,9 +324,8 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     // 16-byte chunks: 8 of a key's 64 dims, of every head and side
                     for (int i = lo * 8 + lane; i < hi * 8; i += 32) {
                         const int key = i >> 3;
-                        const uint32_t at0 = tile + (key >> 3) * PH * 1024 + (key & 7) * 128 + (i & 7) * 16;
-                        for (int u = 0; u < PH * PK::kHalves; ++u)
-                            clean_chunk<T>(at0 + (u % PH) * 1024 + (u / PH) * PK::kSide, zero, odd);
+                        const uint32_t at0 = tile + (key >> 3) * PK::kGroup + (key & 7) * 128 + (i & 7) * 16;
+                        for (int u = 0; u < PH * PK::kHalves; ++u) clean_chunk<T>(at0 + u * 1024, zero, odd);
                     }
                 };
                 if (a.window > 0) {
