@@ -177,7 +177,8 @@ KV_API kv_status kv_paged_attention_tree(
     size_t workspace_bytes, void *out, float *lse_out, int32_t *d_err, void *stream);
 
 /* Workspace bytes of kv_paged_attention_tree for these sizes (SIZE_MAX when they are invalid or
- * unsupported, with the reason in kv_last_error(), or no device can be queried). */
+ * unsupported, with the reason in kv_last_error(), or no device can be queried).  More sequences or a larger
+ * max_query_len never need less. */
 KV_API size_t kv_paged_attention_tree_workspace_size(int32_t num_seqs, int32_t max_query_len,
                                                      int32_t num_q_heads, int32_t num_kv_heads,
                                                      int32_t head_dim, int32_t num_workers);

@@ -1228,7 +1228,7 @@ size_t kv_paged_attention_tree_workspace_size(int32_t num_seqs, int32_t max_quer
         return SIZE_MAX;
     }
     ok();
-    return pkv::plan_tree(max_query_len, num_q_heads / num_kv_heads, num_kv_heads, head_dim, num_workers, info.sm_count).workspace_bytes;
+    return pkv::plan_tree(num_seqs, max_query_len, num_q_heads / num_kv_heads, num_kv_heads, head_dim, num_workers, info.sm_count).workspace_bytes;
 }
 
 kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs,
@@ -1281,7 +1281,7 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     DeviceInfo info;
     if ((e = device_info(dev, &info)) != cudaSuccess) return cuda_fail(e, "device attributes");
     const int32_t g = num_q_heads / num_kv_heads;
-    const pkv::TreePlan plan = pkv::plan_tree(max_query_len, g, num_kv_heads, head_dim, num_workers, info.sm_count);
+    const pkv::TreePlan plan = pkv::plan_tree(num_seqs, max_query_len, g, num_kv_heads, head_dim, num_workers, info.sm_count);
     if (static_cast<size_t>(info.smem_optin) < plan.smem_bytes)
         return fail(KV_ERR_UNSUPPORTED, "tree attention: needs %zu bytes of shared memory per block, the device has %d",
                     plan.smem_bytes, info.smem_optin);

@@ -226,7 +226,7 @@ struct TreePlan {
     int rows_per_item;    // rows of a partial result
     size_t lse_off, o_off, workspace_bytes, smem_bytes;
 };
-TreePlan plan_tree(int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count);
+TreePlan plan_tree(int num_seqs, int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count);
 
 cudaError_t launch_tree_attention(const CUtensorMap &tmap_q, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                   const TreeArgs &a, const TreePlan &plan, void *workspace, int head_dim, int q_dtype,

@@ -585,14 +585,17 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 
 }  // namespace
 
-// Trees of up to 128 rows a kv head go by groups of heads (tree_packed.cu, which has the times of both),
-// four at a time where the rows fit 32 lanes; wider ones, and a single kv head, take the kernel of this
-// file.
-TreePlan plan_tree(int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count) {
+// Trees of up to 128 rows a kv head go by groups of heads (tree_packed.cu, which has the times of both);
+// wider ones, and a single kv head, take the kernel of this file.
+TreePlan plan_tree(int num_seqs, int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count) {
     TreePlan t;
     const int rows = max_query_len * group;
-    t.heads_per_item = num_kv_heads == 1 || rows > kTreeRows ? 1 : (rows <= 32 && num_kv_heads >= 3 ? 4 : 2);
     t.workers = num_workers > 0 ? num_workers : sm_count;
+    t.heads_per_item = num_kv_heads == 1 || rows > kTreeRows ? 1 : 2;
+    if (head_dim == 64 && num_kv_heads >= 3) {
+        const int64_t items = static_cast<int64_t>(num_seqs) * ((num_kv_heads + 3) / 4);
+        if (rows <= 32 || (rows <= 64 && 4 * items >= t.workers)) t.heads_per_item = 4;
+    }
     if (t.heads_per_item > 1) {
         plan_tree_packed(t, rows, group, head_dim);
     } else {
@@ -619,6 +622,9 @@ cudaError_t launch_tree_attention(const CUtensorMap &tq, const CUtensorMap &tk, 
     p.key_shift = plan.key_shift;
     p.workers = plan.workers;
     p.rows_per_item = plan.rows_per_item;
+    const int row_tiles = (a.max_query_len + p.tokens_per_tile - 1) / p.tokens_per_tile;
+    p.items_per_seq = p.heads_per_item == 1 ? (row_tiles + 1) / 2 * a.num_kv_heads
+                                            : (a.num_kv_heads + p.heads_per_item - 1) / p.heads_per_item;
     char *ws = static_cast<char *>(workspace);
     p.ws_first = reinterpret_cast<int4 *>(ws);
     p.ws_lse = reinterpret_cast<float *>(ws + plan.lse_off);

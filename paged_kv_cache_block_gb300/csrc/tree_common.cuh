@@ -4,6 +4,7 @@
 #pragma once
 
 #include <atomic>
+#include <climits>
 #include <type_traits>
 
 #include "common.cuh"
@@ -21,6 +22,8 @@ constexpr float kRescaleLog2 = 8.0f;   // a row's reference maximum moves when e
 // tiles or more.  Smaller ones count tiles alone, down to one: latency is what matters then.
 constexpr int kItemCost = 2;
 constexpr int kBigShare = 8;
+// Workers an item from which a CTA's warps share out the pieces of an item (see the merge kernels).
+constexpr int kLongMerge = 32;
 constexpr int kFlags = 8;              // pieces whose odd-value flags are kept
 
 struct TreeParams {
@@ -31,6 +34,7 @@ struct TreeParams {
     int key_shift;        // log2 of the keys of a key tile
     int workers;          // shares at most
     int rows_per_item;    // rows of a partial result
+    int items_per_seq;    // at most
     int4 *ws_first;       // [2 * workers] first piece of each share: (sequence, item of it, key tile of it,
                           // -), (first row, rows, -, -) of the sequence; sequence -1: no share
     float *ws_lse;        // [2 * workers][rows_per_item] log2-sum-exp2 of the partial results
@@ -346,16 +350,96 @@ __device__ __forceinline__ void add_odd_values(const TreeParams &p, const Walk &
                          p.rows_per_item);
 }
 
-// Join the partial results of the item that starts in share c and goes on into the next ones.
+// Join the partial results of an item that lies in several shares:
 //   out = sum_i w_i o_i / sum_i w_i,  w_i = exp2(lse_i - max)
 // A thread takes 8 dims of a row, a warp 32 rows, so that the partial results are read in whole lines.
 // What it costs is dependent round trips: the shares' records, then kPieces pieces at a time.
+constexpr int kPieces = 4;
+
+struct Joined {
+    float acc[8], wsum, mx;
+    __device__ __forceinline__ Joined() : wsum(0.f), mx(-INFINITY) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] = 0.f;
+    }
+    // Further pieces: their lse (-inf: nothing seen, or no piece) and 8 dims.
+    template <int N> __device__ __forceinline__ void add(const float (&l)[N], const float4 (&v)[N][2]) {
+        float m = mx;
+        bool nan = false;
+#pragma unroll
+        for (int u = 0; u < N; ++u) m = fmaxf(m, l[u]), nan |= l[u] != l[u];
+        if (m == -INFINITY && !nan) return;  // nothing seen so far
+        const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - m);
+        mx = m;
+        wsum *= f;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) acc[e] *= f;
+#pragma unroll
+        for (int u = 0; u < N; ++u) {
+            const float w = l[u] == -INFINITY ? 0.f : fast_exp2(l[u] - mx);
+            if (w == 0.f) continue;  // it adds nothing, whatever it holds
+            wsum += w;
+            acc[0] += w * v[u][0].x, acc[1] += w * v[u][0].y, acc[2] += w * v[u][0].z, acc[3] += w * v[u][0].w;
+            acc[4] += w * v[u][1].x, acc[5] += w * v[u][1].y, acc[6] += w * v[u][1].z, acc[7] += w * v[u][1].w;
+        }
+    }
+    // Pieces e0, e0 + step, .. up to `last` of the item that starts in share c: row rr, the dims of float4s q, q + 1.
+    template <int D>
+    __device__ __forceinline__ void add_pieces(const TreeParams &p, int c, int e0, int step, int last, int rr, int q) {
+        for (; e0 <= last; e0 += kPieces * step) {
+            float l[kPieces];
+            float4 v[kPieces][2];
+#pragma unroll
+            for (int u = 0; u < kPieces; ++u) {
+                const int e = e0 + u * step;
+                const bool in = e <= last;
+                const int64_t slot = part_slot(e, e == c);
+                const float4 *src = part_o<D>(p, slot, rr) + static_cast<int64_t>(q) * p.rows_per_item;
+                l[u] = in ? __ldcg(part_lse(p, slot, rr)) : -INFINITY;
+                v[u][0] = in ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
+                v[u][1] = in ? __ldcg(src + p.rows_per_item) : make_float4(0.f, 0.f, 0.f, 0.f);
+            }
+            add(l, v);
+        }
+    }
+    // The joined result of that row of item idx of a sequence (sq: its second record), if the row exists.
+    template <typename T, int D>
+    __device__ __forceinline__ void store(const TreeParams &p, const int4 &sq, int idx, int rr, int q) const {
+        const int64_t row = row_of(p, sq, idx, rr);
+        if (row < 0) return;
+        const TreeArgs &a = p.a;
+        const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
+        *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + 4 * q) =
+            make_uint4(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv),
+                       pack2<T>(acc[4] * inv, acc[5] * inv), pack2<T>(acc[6] * inv, acc[7] * inv));
+        if (a.lse_out && q == 0) a.lse_out[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
+    }
+    // Row of the output of an item's row rr, or -1: its kv head, token and head of the group.
+    static __device__ __forceinline__ int64_t row_of(const TreeParams &p, const int4 &sq, int idx, int rr) {
+        int h, t, hh;
+        const int TQ = p.tokens_per_tile;
+        if (p.heads_per_item == 1) {
+            h = idx / sq.z;
+            const int r = rr & 127, tl = r / p.group;
+            t = (2 * (idx - h * sq.z) + (rr >> 7)) * TQ + tl;
+            hh = r - tl * p.group;
+            if (tl >= TQ || t >= sq.y) return -1;
+        } else {
+            const int lanes = p.rows_per_item / p.heads_per_item, r = rr % lanes;
+            h = idx * p.heads_per_item + rr / lanes;
+            t = r / p.group;
+            hh = r - t * p.group;
+            if (h >= p.a.num_kv_heads || t >= sq.y) return -1;
+        }
+        return static_cast<int64_t>(sq.x + t) * p.a.num_q_heads + h * p.group + hh;
+    }
+};
+
+// A CTA a share c (and 8 units of 8 dims of 32 rows): the item that starts in it and goes on into the next ones.
 template <typename T, int D>
 static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeParams p) {
-    constexpr int kPieces = 4;
-    const TreeArgs &a = p.a;
     const int c = blockIdx.x, lane = threadIdx.x & 31;
-    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);   // 8 dims of 32 rows
+    const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);
     const int rr = unit / (D / 8) * 32 + lane, q = unit % (D / 8) * 2;
     previous_kernel_done();  // the attention kernel's results
     // lane i: the first piece of share c + i (none past the last)
@@ -381,62 +465,54 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_
         last += __ffs(~go) - 1;
         break;
     }
-    // the row's kv head, token and head of the group
-    int h, t, hh;
-    const int TQ = p.tokens_per_tile;
-    if (p.heads_per_item == 1) {
-        h = idx / sq.z;
-        const int r = rr & 127, tl = r / p.group;
-        t = (2 * (idx - h * sq.z) + (rr >> 7)) * TQ + tl;
-        hh = r - tl * p.group;
-        if (tl >= TQ || t >= sq.y) return;
-    } else {
-        const int lanes = p.rows_per_item / p.heads_per_item, r = rr % lanes;
-        h = idx * p.heads_per_item + rr / lanes;
-        t = r / p.group;
-        hh = r - t * p.group;
-        if (h >= a.num_kv_heads || t >= sq.y) return;
+    if (Joined::row_of(p, sq, idx, rr) < 0) return;
+    Joined x;
+    x.add_pieces<D>(p, c, c, 1, last, rr, q);
+    x.store<T, D>(p, sq, idx, rr, q);
+}
+
+// The same when there are few items, of many pieces each: a CTA an item (and a unit), whose 8 warps share
+// out its pieces.  One sequence of 32/8 heads takes 15.5 us for 1117 tokens, 18.6 for 4000 and 40 for 30000, and
+// 17.7, 23.5 and 45 with the other merge; but with 16 items (8 sequences of 600) it is 25.4 against 20.3, as
+// every CTA reads all records and each unit is a CTA.
+template <typename T, int D>
+static __global__ void __launch_bounds__(256, 4) tree_merge_long_kernel(const __grid_constant__ TreeParams p) {
+    __shared__ float lse[8][32];
+    __shared__ float4 part[8][2][32];
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int b = blockIdx.x / p.items_per_seq, idx = blockIdx.x % p.items_per_seq;
+    const int rr = blockIdx.y / (D / 8) * 32 + lane, q = blockIdx.y % (D / 8) * 2;
+    previous_kernel_done();
+    // the shares that begin in the middle of the item: `first` and the next ones
+    int mine = INT_MAX, count = 0;
+    for (int e = lane; e < p.workers; e += 32) {
+        const int4 rec = __ldcg(&p.ws_first[2 * e]);
+        if (rec.x == b && rec.y == idx && rec.z > 0) mine = min(mine, e), ++count;
     }
-    float acc[8], wsum = 0.f, mx = -INFINITY;
+    const int first = __reduce_min_sync(0xffffffffu, mine);
+    count = __reduce_add_sync(0xffffffffu, count);
+    if (count == 0 || first == 0) return;  // the item is in one share (the first one starts its item)
+    const int4 sq = __ldcg(&p.ws_first[2 * first + 1]);
+    const int c = first - 1, last = c + count;
+    Joined x;  // (a row that does not exist is read as it is, and not stored)
+    x.add_pieces<D>(p, c, c + warp, 8, last, rr, q);
+    // each warp's result as one more piece
+    lse[warp][lane] = x.wsum == 0.f ? -INFINITY : x.mx + log2f(x.wsum);
+    const float inv = x.wsum == 0.f ? 0.f : 1.f / x.wsum;
+    part[warp][0][lane] = make_float4(x.acc[0] * inv, x.acc[1] * inv, x.acc[2] * inv, x.acc[3] * inv);
+    part[warp][1][lane] = make_float4(x.acc[4] * inv, x.acc[5] * inv, x.acc[6] * inv, x.acc[7] * inv);
+    __syncthreads();
+    if (warp) return;
+    Joined y;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) acc[e] = 0.f;
-    for (int e0 = c; e0 <= last; e0 += kPieces) {
+    for (int w0 = 0; w0 < 8; w0 += kPieces) {
         float l[kPieces];
         float4 v[kPieces][2];
 #pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
-            const bool in = e0 + u <= last;
-            const int64_t slot = part_slot(e0 + u, e0 + u == c);
-            const float4 *src = part_o<D>(p, slot, rr) + static_cast<int64_t>(q) * p.rows_per_item;
-            l[u] = in ? __ldcg(part_lse(p, slot, rr)) : -INFINITY;
-            v[u][0] = in ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
-            v[u][1] = in ? __ldcg(src + p.rows_per_item) : make_float4(0.f, 0.f, 0.f, 0.f);
-        }
-        float m = mx;
-        bool nan = false;
-#pragma unroll
-        for (int u = 0; u < kPieces; ++u) m = fmaxf(m, l[u]), nan |= l[u] != l[u];
-        if (m == -INFINITY && !nan) continue;  // nothing seen so far
-        const float f = mx == -INFINITY ? 0.f : fast_exp2(mx - m);
-        mx = m;
-        wsum *= f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) acc[e] *= f;
-#pragma unroll
-        for (int u = 0; u < kPieces; ++u) {
-            const float w = l[u] == -INFINITY ? 0.f : fast_exp2(l[u] - mx);
-            if (w == 0.f) continue;  // it adds nothing, whatever it holds
-            wsum += w;
-            acc[0] += w * v[u][0].x, acc[1] += w * v[u][0].y, acc[2] += w * v[u][0].z, acc[3] += w * v[u][0].w;
-            acc[4] += w * v[u][1].x, acc[5] += w * v[u][1].y, acc[6] += w * v[u][1].z, acc[7] += w * v[u][1].w;
-        }
+        for (int u = 0; u < kPieces; ++u) l[u] = lse[w0 + u][lane], v[u][0] = part[w0 + u][0][lane], v[u][1] = part[w0 + u][1][lane];
+        y.add(l, v);
     }
-    const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
-    const int64_t row = static_cast<int64_t>(sq.x + t) * a.num_q_heads + h * p.group + hh;
-    *reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + row * D + 4 * q) =
-        make_uint4(pack2<T>(acc[0] * inv, acc[1] * inv), pack2<T>(acc[2] * inv, acc[3] * inv),
-                   pack2<T>(acc[4] * inv, acc[5] * inv), pack2<T>(acc[6] * inv, acc[7] * inv));
-    if (a.lse_out && q == 0) a.lse_out[row] = wsum == 0.f ? -INFINITY : (mx + log2f(wsum)) * 0.69314718055994531f;
+    y.store<T, D>(p, sq, idx, rr, q);
 }
 
 // The attention kernel and, with more than one share, the merge.
@@ -459,8 +535,11 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
     // 17.7, 54.5, 207.7, 361.6.
     const cudaError_t e = launch_dependent(kernel, dim3(p.workers), dim3(threads), smem, stream, tq, tk, tv, p);
     if (e != cudaSuccess || p.workers < 2) return e;
-    return launch_dependent(tree_merge_kernel<T, D>, dim3(p.workers - 1, p.rows_per_item / 32 * (D / 8) / 8), dim3(256), 0,
-                            stream, p);
+    const int units = p.rows_per_item / 32 * (D / 8);
+    const int64_t items = static_cast<int64_t>(p.items_per_seq) * p.a.num_seqs;
+    if (items * kLongMerge <= p.workers)
+        return launch_dependent(tree_merge_long_kernel<T, D>, dim3(static_cast<unsigned>(items), units), dim3(256), 0, stream, p);
+    return launch_dependent(tree_merge_kernel<T, D>, dim3(p.workers - 1, units / 8), dim3(256), 0, stream, p);
 }
 
 // Items of several kv heads (tree_packed.cu): the plan for `rows` query rows a head (heads_per_item

@@ -1,21 +1,26 @@
 // Tree attention, two or four kv heads of a sequence at a time.
 //
-// Reading the cache bounds small trees, and one head at a time cannot read it fast enough: a TMA box
-// of 16 tokens of one head and 64 dims (2 KB) costs about 130 clocks plus two a row, 13 bytes a
-// clock and SM, where HBM gives 23; a box of two heads moves 21, of four 32.  The tensor map splits
-// tokens into groups of 8 so that a box lands as [group of 8 tokens][head][token][64 dims]: the
-// swizzle atoms of one head lie a constant distance apart over all blocks of a key tile, which is
-// what a matrix descriptor can say.
+// Reading the cache bounds small trees, and one head at a time cannot read it fast enough: a TMA box of 2 KB
+// (16 tokens of 64 dims of one head) costs about 130 clocks plus two a row, 13 bytes a clock and SM, where
+// HBM gives 23; a box of 4 KB moves 21, one of 8 KB 32.  So a box takes all dims of a block of several
+// heads.  The tensor map splits tokens into groups of 8 and heads into parts of 64 dims, and a box lands as
+// [group of 8 tokens][head][part][token][64 dims]: the swizzle atoms of one part of one head lie a constant
+// distance apart over all blocks of a key tile, which is what a matrix descriptor can say.  (A box a part:
+// the Mistral-shaped window layer 206 us instead of 200.)
 //
-// Heads of at most 32 (64) query rows share the 128 TMEM lanes of one row tile, four (two) of them,
-// lanes 32 h .. those of head h.  Heads of up to 128 rows have a row tile each, two at a time.  (38
-// sequences of 8000 tokens and 32/8 heads of 128 dims: 201 us for 28 rows a head, 219 for 64, 247 for
-// 128, where one head at a time took 269, 308 and 363; at 256 rows two row tiles of one head take 395
-// and two heads a row tile 505, so that wider trees stay with tree_attention.cu.)
+// Two heads of up to 64 rows share the 128 TMEM lanes of a row tile, those of up to 128 rows have one each.
+// Heads of 64 dims go by four, in one row tile (up to 32 rows) or two (up to 64, when the batch gives the
+// workers enough items).  38 sequences of 8000 tokens, us, and (152 of 1000):
+//   32/8 heads of 128 dims, 28 rows: two heads 201 (122), four 201 (112), one 252 (193); but 38 of 500 and
+//     2000 tokens take 26 and 62 with two, 30 and 69 with four
+//   64 rows: two 203 (126), one 254 (196);  128 rows: two 233 (164), one 256 (261)
+//   256 rows: two row tiles of one head 375, two heads a row tile 505: tree_attention.cu
+//   12/12 heads of 64 dims, 24 rows: four 160 (92), two 203 (116), one 363 (220)
+//   64 rows: four 174 (114), two 216 (135); one sequence of 1117 tokens 18.5 and 15.5
 //
-// Per key tile and head h (64 keys, or 128 of two heads of 64 dims: 32 KB of K and of V, 64 KB for four
-// heads of 128 dims; with 128 keys of two heads of 128 dims the ring has three entries instead of six,
-// and the Mistral-shaped window layer took 235 us instead of 208):
+// Per key tile and head h (64 keys, or 128 of two heads of 64 dims: 32 KB of K and of V; with 128 keys
+// of two heads of 128 dims the ring has three entries instead of six, and the window layer took 235 us
+// instead of 208; with 64 of two heads of 64 dims 64 rows took 255 instead of 216):
 //   S_h = Q K_h^T    all 128 rows, of which the lanes of head h are read
 //   P_h = exp2(S_h * scale - m)    one thread a row; P_h has TMEM columns of its own
 //   O  += P_h V_h    for the lanes of head h alone (the other lanes are switched off), so that
@@ -538,7 +543,10 @@ cudaError_t launch_heads(const CUtensorMap &tq, const CUtensorMap &tk, const CUt
 template <typename T, int D>
 cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv, const TreeParams &p,
                          int dev, cudaStream_t stream) {
-    if (p.heads_per_item == 4) return launch_heads<T, D, 4, 1>(tq, tk, tv, p, dev, stream);
+    if constexpr (D == 64)
+        if (p.heads_per_item == 4)
+            return p.rows_per_item == kTreeRows ? launch_heads<T, D, 4, 1>(tq, tk, tv, p, dev, stream)
+                                                : launch_heads<T, D, 4, 2>(tq, tk, tv, p, dev, stream);
     return p.rows_per_item == kTreeRows ? launch_heads<T, D, 2, 1>(tq, tk, tv, p, dev, stream)
                                         : launch_heads<T, D, 2, 2>(tq, tk, tv, p, dev, stream);
 }
@@ -551,8 +559,9 @@ template <typename PK> void set_plan(TreePlan &t, int group) {
 }
 
 template <int D> void plan_heads(TreePlan &t, int rows, int group) {
-    if (t.heads_per_item == 4) set_plan<Pack<D, 4, 1>>(t, group);
-    else if (rows <= 64) set_plan<Pack<D, 2, 1>>(t, group);
+    if constexpr (D == 64)
+        if (t.heads_per_item == 4) return rows <= 32 ? set_plan<Pack<D, 4, 1>>(t, group) : set_plan<Pack<D, 4, 2>>(t, group);
+    if (rows <= 64) set_plan<Pack<D, 2, 1>>(t, group);
     else set_plan<Pack<D, 2, 2>>(t, group);
 }
 

@@ -556,18 +556,12 @@ def test_tree_masks_of_any_kind(kc):
         assert (out[row] == 0).all() and torch.isneginf(lse[row]).all()
 
 
-@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
-@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
-@pytest.mark.parametrize("window", [0, 70])
-@pytest.mark.parametrize("drafts,Hq,Hkv", [([13, 64, 7, 30], 8, 2), ([8, 7, 2, 5], 12, 3), ([13, 16, 7, 11], 20, 5),
-                                           ([13, 32, 7, 30], 12, 3), ([9, 11, 2, 8], 16, 1)],
-                         ids=["pair", "four", "two", "two_wide", "one"])
-def test_tree_unseen_keys_have_no_part(kc, dt, poison, window, drafts, Hq, Hkv):
+def check_unseen_keys(kc, dt, poison, window, drafts, Hq, Hkv, D=128, workers=0):
     """Poison in every slot no row sees: free blocks, the rest of the last block, keys before the
     window; and in drafted keys and window keys that only some rows see, whose other rows stay clean."""
     contexts, bs = [150, 0, 40, 263], 16
     # (row 0 of each tree sees itself alone of it, so that no drafted key is seen by all)
-    c = tree_case(21, contexts, drafts, Hq, Hkv, 128, bs, dt, window)
+    c = tree_case(21, contexts, drafts, Hq, Hkv, D, bs, dt, window)
     clean = {k: c[k].clone() for k in ("k", "v")}
     seen_any = torch.zeros(c["k"].shape[0] * bs, dtype=torch.bool)
     touched = np.zeros(len(c["q"]), bool)
@@ -584,8 +578,8 @@ def test_tree_unseen_keys_have_no_part(kc, dt, poison, window, drafts, Hq, Hkv):
             partly.append(int(slots[j]))
             touched[t0:t0 + n] |= seen[:, j]
     for name in ("k", "v"):
-        c[name].view(-1, Hkv, 128)[~seen_any] = poison
-    out, lse, err = run_tree(kc, c)
+        c[name].view(-1, Hkv, D)[~seen_any] = poison
+    out, lse, err = run_tree(kc, c, workers)
     assert err == 0
     poisoned = dict(c)
     c_ref = {**c, **clean}
@@ -594,18 +588,56 @@ def test_tree_unseen_keys_have_no_part(kc, dt, poison, window, drafts, Hq, Hkv):
     # poison in values that some rows see: the other rows are untouched, bit for bit
     for name in ("v", "k"):
         p = {**poisoned, name: poisoned[name].clone()}
-        p[name].view(-1, Hkv, 128)[partly, :, 3] = poison
-        out2, lse2, err = run_tree(kc, p)
+        p[name].view(-1, Hkv, D)[partly, :, 3] = poison
+        out2, lse2, err = run_tree(kc, p, workers)
         rest = torch.from_numpy(~touched)
         assert touched.any() and (~touched).any() and torch.equal(out2[rest], out[rest]) and torch.equal(lse2[rest], lse[rest])
         if name == "v":  # and the rows that see it get it, in that dim alone
             hit = out2[torch.from_numpy(touched)]
             same = out[torch.from_numpy(touched)]
-            dims = [d for d in range(128) if d != 3]
+            dims = [d for d in range(D) if d != 3]
             assert torch.equal(hit[..., dims], same[..., dims]) and not torch.isfinite(hit[..., 3]).any()
             assert torch.equal(lse2, lse)
             if poison == poison:
                 assert (hit[..., 3] == poison).all()
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float16])
+@pytest.mark.parametrize("poison", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("drafts,Hq,Hkv", [([13, 64, 7, 30], 8, 2), ([8, 7, 2, 5], 12, 3), ([13, 16, 7, 11], 20, 5),
+                                           ([13, 32, 7, 30], 12, 3), ([9, 11, 2, 8], 16, 1)],
+                         ids=["pair", "four", "two", "two_wide", "one"])
+def test_tree_unseen_keys_have_no_part(kc, dt, poison, window, drafts, Hq, Hkv):
+    check_unseen_keys(kc, dt, poison, window, drafts, Hq, Hkv)
+
+
+@pytest.mark.parametrize("poison", [float("nan"), float("inf")])
+@pytest.mark.parametrize("window", [0, 70])
+@pytest.mark.parametrize("drafts,Hq,Hkv,workers", [([8, 7, 2, 5], 12, 3, 0), ([13, 16, 7, 11], 20, 5, 5),
+                                                   ([8, 7, 2, 16], 28, 7, 0), ([13, 64, 7, 30], 2, 2, 0)],
+                         ids=["four", "four_in_two_tiles", "seven", "two"])
+def test_tree_unseen_keys_of_64_dims_have_no_part(kc, poison, window, drafts, Hq, Hkv, workers):
+    check_unseen_keys(kc, torch.bfloat16, poison, window, drafts, Hq, Hkv, 64, workers)
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,n,bs,window", [
+    (8, 2, 128, 7, 16, 0), (32, 8, 128, 64, 16, 0), (32, 8, 128, 7, 8, 0), (12, 12, 64, 24, 16, 0), (6, 1, 64, 40, 16, 0),
+    (4, 1, 128, 64, 32, 0), (12, 3, 64, 11, 16, 5000), (7, 7, 64, 50, 16, 0)])
+def test_tree_one_sequence_over_every_worker(kc, Hq, Hkv, D, n, bs, window):
+    """One sequence in many shares: few items of many pieces, which the warps of a CTA join together."""
+    c = tree_case(35, [9000], [n], Hq, Hkv, D, bs, torch.bfloat16, window, pad=2)
+    c["masks"][n // 2] = 0  # a row of the context alone
+    ref = reference_tree(c)
+    for workers in (0, 33, 700):
+        out, lse, err = run_tree(kc, c, workers)
+        assert err == 0
+        check_tree(c, out, lse, ref)
+        assert (out[n:] == 7).all() and (lse[n:] == 7).all()
+    small = tree_case(36, [130], [n], Hq, Hkv, D, bs, torch.bfloat16, masks=[0] * (n - 1) + [1])  # few pieces of many
+    out, lse, err = run_tree(kc, small)
+    assert err == 0
+    check_tree(small, out, lse)
 
 
 def test_tree_seen_context_nan_reaches_every_row(kc):
@@ -706,6 +738,15 @@ def test_tree_many_short_sequences(kc):
     out, lse, err = run_tree(kc, c)
     assert err == 0
     check_tree(c, out, lse)
+
+
+def test_tree_workspace_grows_with_the_batch(kc):
+    """A workspace made for the largest batch serves the smaller ones."""
+    for Hq, Hkv, D in ((12, 12, 64), (32, 8, 64), (6, 3, 64), (4, 1, 64), (2, 2, 64), (32, 8, 128), (64, 8, 128), (8, 1, 128)):
+        for workers in (0, 5, 600):
+            sizes = np.array([[kc.paged_attention_tree_workspace_size(B, n, Hq, Hkv, D, workers) for n in range(1, 65)]
+                              for B in (1, 2, 9, 13, 40, 500)])
+            assert (np.diff(sizes, axis=0) >= 0).all() and (np.diff(sizes, axis=1) >= 0).all()
 
 
 def test_tree_small_workspace_is_refused(kc):
