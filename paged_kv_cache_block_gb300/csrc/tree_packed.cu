@@ -389,8 +389,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             const int klo = a.window > 0 ? max(0, pos - a.window + 1) : 0;
             const bool warp_valid = __any_sync(0xffffffffu, valid);
             float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
-            float2 rsum = make_float2(0.f, 0.f);  // sum of the rounded weights (what the product uses)
-            float2 esum = make_float2(0.f, 0.f);  // sum of the weights (log-sum-exp)
+            float2 sum = make_float2(0.f, 0.f);  // sum of the weights
             uint32_t wt[kKeys / 2];
             for (int j = w.ja; j < w.jb; ++j) {
                 if (!wait_all(bar(kBarS + hi), done & 1)) {
@@ -400,7 +399,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 tc_fence_after();
                 if (warp_valid) {
                     const bool masked = mixed_tile(p, s, j);
-                    float2 tr, te;
+                    float2 part_sum;
                     // One pass over the tile's S: weights against the reference in use, the tile maximum
                     // tracked alongside, 32 columns at a time with the next load in flight.  A second one
                     // when the reference has to move.  (One copy of the code: a CTA's first tile pays for
@@ -410,7 +409,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         const float nref = m_used == -INFINITY ? 0.f : -m_used;
                         const float2 ref2 = make_float2(nref, nref);
                         float mraw = -INFINITY;
-                        tr = te = make_float2(0.f, 0.f);
+                        part_sum = make_float2(0.f, 0.f);
                         uint32_t buf[2][32];
                         tmem_ld32_async(t_s, buf[0]);
 #pragma unroll
@@ -430,8 +429,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                                 const float2 x = make_float2(fast_exp2(e.x), fast_exp2(e.y));
                                 mraw = fmaxf(mraw, fmaxf(s0, s1));
                                 wt[ch * 16 + k] = pack2<T>(x.x, x.y);
-                                te = add2(te, x);
-                                tr = add2(tr, unpack2<T>(wt[ch * 16 + k]));
+                                part_sum = add2(part_sum, x);
                             }
                         }
                         if (again) break;
@@ -448,8 +446,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         const float f = moved ? fast_exp2(m_used - mt) : 1.f;
                         if (moved) {
                             m_used = mt;
-                            rsum.x *= f, rsum.y *= f;
-                            esum.x *= f, esum.y *= f;
+                            sum.x *= f, sum.y *= f;
                         }
                         if (__any_sync(0xffffffffu, rescale)) {
                             // the warp loads and stores its lanes of O together; rows that keep their
@@ -467,8 +464,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                         }
                     }
                     if (dead) break;
-                    rsum = add2(rsum, tr);
-                    esum = add2(esum, te);
+                    sum = add2(sum, part_sum);
                     tmem_st32u(t_p, wt);
                     if constexpr (kKeys == 128) tmem_st32u(t_p + 32, wt + 32);
                     tmem_wait_st();
@@ -486,8 +482,8 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 break;
             }
             if (!warp_valid) continue;
-            const float lr = rsum.x + rsum.y, le = esum.x + esum.y;
-            const float inv = lr == 0.f ? 0.f : 1.f / lr;
+            const float l = sum.x + sum.y;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             const int64_t row = token * a.num_q_heads + h * g + hh;
             T *out16 = static_cast<T *>(a.out) + row * D;
             const int64_t slot = part_slot(c, w.ja == s.j0);
@@ -511,8 +507,9 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                 }
             }
+            __syncwarp();  // (a row is written by the lanes of its quad)
             if (valid) {
-                const float lse2 = le == 0.f ? -INFINITY : m_used + log2f(le);
+                const float lse2 = l == 0.f ? -INFINITY : m_used + log2f(l);
                 if (!w.whole) *part_lse(p, slot, r) = lse2;
                 else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
                 if (odd_flag[piece % kFlags])
