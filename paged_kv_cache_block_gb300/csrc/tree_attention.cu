@@ -29,7 +29,7 @@
 // Weights are taken against the reference maximum in use; only when a row's maximum exceeds it by
 // more than 2^8 are its O and sum rescaled.  The sum is of the weights before their rounding to 16 bits
 // (half a step of each, for the second product): with a second sum, of the rounded ones, as normaliser a
-// batch of 38 trees of 256 rows took 373 us instead of 353.  Every wait is bounded (2 s): on expiry
+// batch of 38 trees of 256 rows took 373 us instead of 348.  Every wait is bounded (2 s): on expiry
 // KV_DERR_TIMEOUT is set, what was issued is drained, TMEM is freed and the CTA returns.
 #include "tree_common.cuh"
 

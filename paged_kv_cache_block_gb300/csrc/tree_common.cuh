@@ -472,8 +472,8 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_
 }
 
 // The same when there are few items, of many pieces each: a CTA an item (and a unit), whose 8 warps share
-// out its pieces.  One sequence of 32/8 heads takes 15.5 us for 1117 tokens, 18.6 for 4000 and 40 for 30000, and
-// 17.7, 23.5 and 45 with the other merge; but with 16 items (8 sequences of 600) it is 25.4 against 20.3, as
+// out its pieces.  One sequence of 32/8 heads takes 15.5 us for 1117 tokens, 17.9 for 4000 and 39 for 30000, and
+// 17.0, 22.6 and 46 with the other merge; but with 16 items (8 sequences of 600) it was 25.4 against 20.3, as
 // every CTA reads all records and each unit is a CTA.
 template <typename T, int D>
 static __global__ void __launch_bounds__(256, 4) tree_merge_long_kernel(const __grid_constant__ TreeParams p) {
@@ -529,10 +529,9 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
     }
     // The attention kernel waits for the kernel before it once its barriers and TMEM are set up, and lets the
     // merge launch then, which waits at once (a CTA of it does not fit beside one of the attention kernel's,
-    // whose registers fill the SM).  Calls in a stream take 18.0, 54.7, 206.5, 359 us so; 20.5, 57.4, 210, 365
-    // when only the merge is launched this way and 22.6, 60.6, 212, 365 when neither is (a sequence of 1117
-    // keys; 64 of OPT-125m; a window of 4096; 38 trees of 48 tokens).  Letting the next kernel launch at the merge's start:
-    // 17.7, 54.5, 207.7, 361.6.
+    // whose registers fill the SM).  In a stream of calls that takes 2.5 to 5 us less than launching the
+    // merge alone this way, and that 2 us less than plain launches.  Letting the next kernel launch at the
+    // merge's start: 0.3 us less for one sequence, 1.2 and 2.5 us more for the largest batches.
     const cudaError_t e = launch_dependent(kernel, dim3(p.workers), dim3(threads), smem, stream, tq, tk, tv, p);
     if (e != cudaSuccess || p.workers < 2) return e;
     const int units = p.rows_per_item / 32 * (D / 8);

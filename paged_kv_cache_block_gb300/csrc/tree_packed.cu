@@ -5,18 +5,21 @@
 // HBM gives 23; a box of 4 KB moves 21, one of 8 KB 32.  So a box takes all dims of a block of several
 // heads.  The tensor map splits tokens into groups of 8 and heads into parts of 64 dims, and a box lands as
 // [group of 8 tokens][head][part][token][64 dims]: the swizzle atoms of one part of one head lie a constant
-// distance apart over all blocks of a key tile, which is what a matrix descriptor can say.  (A box a part:
-// the Mistral-shaped window layer 206 us instead of 200.)
+// distance apart over all blocks of a key tile, which is what a matrix descriptor can say.  (A box a part
+// took 3 % longer on the Mistral-shaped window layer, 8 % on 38 sequences of 8000 tokens and 64 rows.)
 //
 // Two heads of up to 64 rows share the 128 TMEM lanes of a row tile, those of up to 128 rows have one each.
 // Heads of 64 dims go by four, in one row tile (up to 32 rows) or two (up to 64, when the batch gives the
-// workers enough items).  38 sequences of 8000 tokens, us, and (152 of 1000):
-//   32/8 heads of 128 dims, 28 rows: two heads 201 (122), four 201 (112), one 252 (193); but 38 of 500 and
-//     2000 tokens take 26 and 62 with two, 30 and 69 with four
-//   64 rows: two 203 (126), one 254 (196);  128 rows: two 233 (164), one 256 (261)
-//   256 rows: two row tiles of one head 375, two heads a row tile 505: tree_attention.cu
-//   12/12 heads of 64 dims, 24 rows: four 160 (92), two 203 (116), one 363 (220)
-//   64 rows: four 174 (114), two 216 (135); one sequence of 1117 tokens 18.5 and 15.5
+// workers items enough).  us for 38 sequences of 8000 tokens, and for 152 of 1000:
+//   32/8 heads of 128 dims, 28 rows    two heads 201, 119   one 242, 176
+//                           64 rows    two 202, 122         one 243, 177
+//                           128 rows   two 233, 159         one 245, 221
+//   12/12 heads of 64 dims, 24 rows    four 159, 91         two 189, 108   one 343, 205
+//                           64 rows    four 168, 107        two 195, 121   (one sequence of 1117: 18.5, two 15.4)
+// Four heads of 128 dims and up to 32 rows (16 KB a box) took as long as two on long contexts, 112 us instead of
+// 122 on the 152 of 1000, and 69 instead of 62 on 38 of 2000, 30 instead of 26 on 38 of 500: they go by two.
+// Above 128 rows two row tiles of one head are faster than two heads (405 against 505 us at 256 rows):
+// tree_attention.cu.
 //
 // Per key tile and head h (64 keys, or 128 of two heads of 64 dims: 32 KB of K and of V; with 128 keys
 // of two heads of 128 dims the ring has three entries instead of six, and the window layer took 235 us
