@@ -401,7 +401,21 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 }
                 tc_fence_after();
                 if (warp_valid) {
-                    const bool masked = mixed_tile(p, s, j);
+                    if (mixed_tile(p, s, j)) {
+                        // (scale > 0: an unseen score of -inf gets weight 0; apart from the pass below, whose
+                        // code the warps fetch anew each time)
+#pragma unroll 1
+                        for (int ch = 0; ch < kKeys / 32; ++ch) {
+                            uint32_t v[32];
+                            tmem_ld32_async(t_s + 32 * ch, v);
+                            tmem_wait_regs(v);
+                            const uint32_t seen = valid ? seen32(j * kKeys + ch * 32, s.ctx, klo, mask) : 0u;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1 ? v[k] : 0xff800000u;
+                            tmem_st32u(t_s + 32 * ch, v);
+                        }
+                        tmem_wait_st();
+                    }
                     float2 part_sum;
                     // One pass over the tile's S: weights against the reference in use, the tile maximum
                     // tracked alongside, 32 columns at a time with the next load in flight.  A second one
@@ -420,11 +434,6 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                             uint32_t(&v)[32] = buf[ch & 1];
                             tmem_wait_regs(v);
                             if (ch + 1 < kKeys / 32) tmem_ld32_async(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
-                            if (masked) {  // (scale > 0: an unseen score of -inf gets weight 0)
-                                const uint32_t seen = valid ? seen32(j * kKeys + ch * 32, s.ctx, klo, mask) : 0u;
-#pragma unroll
-                                for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1 ? v[k] : 0xff800000u;
-                            }
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
                                 const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
