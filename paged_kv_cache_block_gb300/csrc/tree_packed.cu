@@ -11,15 +11,15 @@
 // Two heads of up to 64 rows share the 128 TMEM lanes of a row tile, those of up to 128 rows have one each.
 // Heads of 64 dims go by four, in one row tile (up to 32 rows) or two (up to 64, when the batch gives the
 // workers items enough).  us for 38 sequences of 8000 tokens, and for 152 of 1000:
-//   32/8 heads of 128 dims, 28 rows    two heads 201, 119   one 242, 176
-//                           64 rows    two 202, 122         one 243, 177
-//                           128 rows   two 233, 159         one 245, 221
-//   12/12 heads of 64 dims, 24 rows    four 159, 91         two 189, 108   one 343, 205
-//                           64 rows    four 168, 107        two 195, 121   (one sequence of 1117: 18.5, two 15.4)
+//   32/8 heads of 128 dims, 28 rows    two heads 200, 117   one 239, 168
+//                           64 rows    two 201, 121         one 239, 169
+//                           128 rows   two 225, 151         one 240, 202
+//   12/12 heads of 64 dims, 24 rows    four 159, 90         two 182, 104   one 346, 201
+//                           64 rows    four 167, 105        two 186, 118   (one sequence of 1117: 18.5, two 15.0)
 // Four heads of 128 dims and up to 32 rows (16 KB a box) took as long as two on long contexts, 112 us instead of
 // 122 on the 152 of 1000, and 69 instead of 62 on 38 of 2000, 30 instead of 26 on 38 of 500: they go by two.
-// Above 128 rows two row tiles of one head are faster than two heads (405 against 505 us at 256 rows):
-// tree_attention.cu.
+// Above 128 rows two row tiles of one head are faster than two heads (405 against 505 us at 256 rows when both
+// were tried, 317 now): tree_attention.cu.
 //
 // Per key tile and head h (64 keys, or 128 of two heads of 64 dims: 32 KB of K and of V; with 128 keys
 // of two heads of 128 dims the ring has three entries instead of six, and the window layer took 235 us
@@ -402,8 +402,8 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 tc_fence_after();
                 if (warp_valid) {
                     if (mixed_tile(p, s, j)) {
-                        // (scale > 0: an unseen score of -inf gets weight 0; apart from the pass below, whose
-                        // code the warps fetch anew each time)
+                        // (scale > 0: an unseen score of -inf gets weight 0.  Apart from the pass below, whose
+                        // unrolled code the warps fetch anew each time: 128 rows 225 us instead of 233.)
 #pragma unroll 1
                         for (int ch = 0; ch < kKeys / 32; ++ch) {
                             uint32_t v[32];
