@@ -528,10 +528,11 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
         attr_set[dev].store(true, std::memory_order_release);
     }
     // The attention kernel waits for the kernel before it once its barriers and TMEM are set up, and lets the
-    // merge launch then, which waits at once (a CTA of it does not fit beside one of the attention kernel's,
-    // whose registers fill the SM).  In a stream of calls that takes 2.5 to 5 us less than launching the
-    // merge alone this way, and that 2 us less than plain launches.  Letting the next kernel launch at the
-    // merge's start: 0.3 us less for one sequence, 1.2 and 2.5 us more for the largest batches.
+    // merge launch then, whose CTAs wait at once (those that fit beside the attention kernel's; it is launched
+    // when all of these are on an SM or done, so that it keeps none of them out).  In a stream of calls that
+    // takes 2.5 to 5 us less than launching the merge alone this way, and that 2 us less than plain launches.
+    // Letting the next kernel launch at the merge's start: 0.3 us less for one sequence, 1.2 and 2.5 us more
+    // for the largest batches.
     const cudaError_t e = launch_dependent(kernel, dim3(p.workers), dim3(threads), smem, stream, tq, tk, tv, p);
     if (e != cudaSuccess || p.workers < 2) return e;
     const int units = p.rows_per_item / 32 * (D / 8);

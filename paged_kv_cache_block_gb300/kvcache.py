@@ -531,6 +531,7 @@ def apply_block_updates(updates: torch.Tensor, block_table: torch.Tensor, zero_i
 #
 # These calls are short next to Python, so their checks are written out in plain expressions (a
 # helper call or a message built in advance costs more than the check).
+# With stream=, what a call makes (outputs left to it, the workspace) is memory of that stream.
 
 _raw_stream = torch._C._cuda_getCurrentRawStream
 _current_device = torch._C._cuda_getDevice
