@@ -219,7 +219,7 @@ struct TreeArgs {
 
 // Launch geometry and workspace layout of the tree kernels.
 struct TreePlan {
-    int heads_per_item;   // kv heads side by side in an item's 128 rows (1, 2 or 4)
+    int heads_per_item;   // kv heads side by side in an item (1, 2 or 4)
     int workers;          // CTAs, each with one share of the key tiles
     int tokens_per_tile;  // drafted tokens of one kv head in a row tile
     int key_shift;        // log2 of the keys of a key tile

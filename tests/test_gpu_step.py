@@ -812,6 +812,12 @@ class Step:
         self.d["table"] = dev(self.table)
         self.kcache, self.vcache = self.kc0.clone(), self.vc0.clone()
 
+    def reset_in_place(self):
+        """The state before a step again, in the tensors that a graph has captured."""
+        self.d["table"].copy_(dev(self.table))
+        self.kcache.copy_(self.kc0)
+        self.vcache.copy_(self.vc0)
+
     def run(self, stream=None):
         kc, d = self.kc, self.d
         if stream is None:
@@ -888,6 +894,39 @@ def test_step_captured_and_replayed(kc):
         g.replay()
     a.check()
     b.check()
+
+
+def test_steps_captured_behind_every_kind_of_work(kc):
+    """The calls in one capture after a fill, a copy, a join of two streams, and on a forked stream."""
+    a, b = Step(kc, 47), Step(kc, 48, B=20, bs=8)
+    for s in (a, b):
+        s.run()
+    torch.cuda.synchronize()
+    x = torch.zeros(1 << 20, device="cuda")
+    y, host = torch.empty_like(x), torch.empty(1 << 20, pin_memory=True)
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        x.zero_()
+        y.copy_(x)
+        a.run()
+        side.wait_stream(main)
+        with torch.cuda.stream(side):
+            b.run()          # first on a forked stream
+            b.run()
+        y.add_(1)
+        main.wait_stream(side)
+        a.run(stream=main)   # first after the join
+        host.copy_(y, non_blocking=True)
+        a.run()
+    for _ in range(3):
+        for s in (a, b):
+            s.reset_in_place()
+            s.out.fill_(7.0)
+        graph.replay()
+        a.check()
+        b.check()
+        assert (host == 1).all()
 
 
 def test_steps_on_two_streams_at_once(kc):
