@@ -162,8 +162,8 @@ def tree_bounds(out, lse, size, smax, D, dtype):
     """Bounds of the kernel's error.  The scores are float32 sums of D exact products, each addition
     off by at most 2^-23 of the sum of magnitudes; exp2, the sums and the merge of pieces add about
     2^-20 to a weight's relative error.  The weights are rounded to the 16-bit type for the second
-    product and the normaliser sums the rounded weights: twice half a step of the weighted mean of
-    |v|.  The result is rounded once."""
+    product: half a step of the weighted mean of |v|, and as much again when the normaliser sums the
+    rounded weights (the kernels' sums the weights before it).  The result is rounded once."""
     u = HALF[dtype]
     e32 = (D * 2.0 ** -23 * smax + 2.0 ** -20)
     acc = (2 * e32[..., None] + 2 * u) * size
