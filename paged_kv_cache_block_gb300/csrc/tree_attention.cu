@@ -52,8 +52,7 @@ template <int D> struct Tile {
     static constexpr int kNumBars = 14 + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
     static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
-    static_assert(kSmem <= 227 * 1024, "shared memory");
-    static_assert(sizeof(ShareScratch) <= 2 * 128 * 4, "the scratch lies where the chains join later");
+    static_assert(kSmem + 512 <= 227 * 1024, "shared memory, with the kernel's static part");
     // pieces whose V tiles can be in the ring at once, one more that the cleaning warp has begun,
     // and one without mixed tiles (only a share's last)
     static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
@@ -123,7 +122,8 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
-    ShareScratch &scratch = *reinterpret_cast<ShareScratch *>(join);
+    // (memory of its own: chain 1 may write `join` while other warps still read the share's start)
+    __shared__ ShareScratch scratch;
     int64_t x0, x1;
     int item_cost;
     previous_kernel_done();
