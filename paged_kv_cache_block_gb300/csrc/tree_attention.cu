@@ -516,7 +516,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
                 use1 = w.jb - w.ja > 1;
                 m = mm;
-                l = l * f0 + (f1 != 0.f ? l1 * f1 : 0.f);
+                // (no guard: a chain whose scores are all NaN has no maximum, hence weight 0, and a sum of NaN,
+                // which has to come through; an empty one has a sum of 0)
+                l = l * f0 + l1 * f1;
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;
             f0 *= inv;
