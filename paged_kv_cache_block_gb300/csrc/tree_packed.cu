@@ -423,7 +423,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                     // fetching it.)
 #pragma unroll 1
                     for (bool again = false;; again = true) {
-                        const float nref = m_used == -INFINITY ? 0.f : -m_used;
+                        const float nref = m_used == -INFINITY ? 0.f : kWeightLog2<T> - m_used;
                         const float2 ref2 = make_float2(nref, nref);
                         float mraw = -INFINITY;
                         part_sum = make_float2(0.f, 0.f);
@@ -521,7 +521,7 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
             }
             __syncwarp();  // (a row is written by the lanes of its quad)
             if (valid) {
-                const float lse2 = l == 0.f ? -INFINITY : m_used + log2f(l);
+                const float lse2 = l == 0.f ? -INFINITY : m_used + (log2f(l) - kWeightLog2<T>);
                 if (!w.whole) *part_lse(p, slot, r) = lse2;
                 else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
                 if (odd_flag[piece % kFlags])
