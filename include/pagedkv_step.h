@@ -140,8 +140,9 @@ KV_API kv_status kv_qk_norm_rope(const void *q, const void *key, const void *val
  *   j < c_b   when window = 0 or j > p_i - window,  p_i = c_b - 1 + (number of its mask bits < n_b)
  *   j >= c_b  when bit j - c_b of tree_mask[row] is set
  * (p_i is the row's position when its mask is itself and its ancestors).  Any mask is taken: a
- * row need not see itself, and a row that sees no key gives out 0, lse -inf.  With GQA, scale and
- * softmax as in kv_paged_attention_decode:
+ * row need not see itself, and a row that sees no key gives out 0, lse -inf.  With GQA and softmax
+ * as in kv_paged_attention_decode, and a scale that is finite and not negative (a negative one,
+ * which that call takes, is KV_ERR_INVALID_ARG; 0 weighs all keys of a row alike):
  *   out = sum_j softmax_j(scale * q.K_j) V_j,   lse = log(sum_j exp(scale * q.K_j))
  * A key that a row does not see has no part in its result, whatever the cache holds there (NaN and
  * infinities included).
