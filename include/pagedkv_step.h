@@ -151,7 +151,9 @@ KV_API kv_status kv_qk_norm_rope(const void *q, const void *key, const void *val
  * slot mapping that is -1 for the rejected rows puts them there.
  *
  *   q            [num_tokens, num_q_heads, head_dim] fp16/bf16, equal to cache_dtype, 16-byte aligned
- *   query_start_loc int32 [num_seqs + 1], non-decreasing; max_query_len >= every n_b (host bound)
+ *   query_start_loc int32 [num_seqs + 1], non-decreasing; max_query_len >= every n_b (host bound; 0
+ *                says that no sequence has rows: as with no sequences or tokens at all, nothing is
+ *                launched, read, checked against the lengths or written)
  *   tree_mask    uint64 [num_tokens] (kv_build_batch writes it; bits from n_b on are ignored)
  *   block_table, seq_lens, max_seq_len, caches: as for kv_paged_attention_decode (entries of blocks
  *                wholly outside every row's window are never read)

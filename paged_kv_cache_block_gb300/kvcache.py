@@ -850,7 +850,8 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     """kv_paged_attention_tree: q [T, Hq, D] (the drafted tokens of sequence b are rows
     query_start_loc[b] .. query_start_loc[b+1]-1); caches [NB, bs, Hkv, D]; block_table int32 [B, W];
     seq_lens int32 [B] (including the drafted tokens); tree_mask int64 [T].  A workspace that is
-    given must hold paged_attention_tree_workspace_size(...) bytes."""
+    given must hold paged_attention_tree_workspace_size(...) bytes.  A max_query_len of 0 declares an
+    empty batch, of which nothing is looked at or written."""
     dev, dt = q.get_device(), q.dtype
     if dev < 0 or q.dim() != 3 or not q.is_contiguous():
         _refuse("q: contiguous [T, heads, D]; " + _DEVICES)

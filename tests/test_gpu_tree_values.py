@@ -205,3 +205,14 @@ def test_tree_within_the_tight_bound(kc, case, dt):
         out, lse, err = run_tree(kc, c, workers)
         assert err == 0 and np.array_equal(np.isfinite(ref[1]), torch.isfinite(lse).cpu().numpy())
         check_tight(c, out, torch.where(torch.isfinite(lse), lse, 0), (ref[0], finite, *ref[2:]))
+
+
+def test_a_bound_of_no_rows_declares_an_empty_batch(kc):
+    """max_query_len 0: rows, lse and the error word stay as they were, although sequences have rows; a
+    bound of 1 already rejects the longer ones."""
+    c = tree_case(76, [20, 5], [3, 1], 8, 2, 128, 16, torch.bfloat16)
+    out, lse, err = run_tree(kc, c, max_query_len=0)
+    assert err == 0 and (out == 7).all() and (lse == 7).all()
+    out, lse, err = run_tree(kc, c, max_query_len=1)
+    assert err == 16 and (out[:3] == 0).all() and torch.isneginf(lse[:3]).all()
+    check_tree(c, out, lse, rows=np.array([3]))
