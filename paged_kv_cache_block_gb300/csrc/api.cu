@@ -1298,7 +1298,6 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     }
     if (st != KV_OK) return st;
     pkv::TreeArgs a;
-    a.q = q;
     a.query_start_loc = query_start_loc;
     a.seq_lens = seq_lens;
     a.block_table = block_table;

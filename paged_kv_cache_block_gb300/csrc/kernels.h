@@ -203,7 +203,6 @@ cudaError_t launch_qk_norm_rope(const RopeArgs &a, int dtype, int sm_count, cuda
 
 // Attention of drafted trees (kv_paged_attention_tree).
 struct TreeArgs {
-    const void *q;
     const int32_t *query_start_loc, *seq_lens, *block_table;
     int64_t bt_stride;
     int32_t max_blocks_per_seq;
