@@ -2,6 +2,8 @@
 // CTAs set themselves up, while that kernel still runs.  Such a kernel calls previous_kernel_done() in
 // every thread before it reads or writes anything that an earlier kernel may have written or read; it
 // returns when all of that kernel has completed.  After anything but a kernel it is a plain launch.
+// Nor does it load through the read-only path (__ldg, ld.global.nc), which takes the data for unchanged from
+// the kernel's launch on, when the kernel before may still be writing it.
 #pragma once
 
 #include <cuda_runtime.h>

@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(con
     Eight wt;
     wt.p[0] = wt.p[1] = wt.q[0] = wt.q[1] = make_float2(1.f, 1.f);
     if (norm && has)
-        wt = widen<T>(__ldg(reinterpret_cast<const uint2 *>(weight + d0)), __ldg(reinterpret_cast<const uint2 *>(weight + d1)));
+        wt = widen<T>(*reinterpret_cast<const uint2 *>(weight + d0), *reinterpret_cast<const uint2 *>(weight + d1));
     float2 pc[2], ps[2], qc[2], qs[2];  // p -> p wp cos, p wp sin; q -> q wq cos, -q wq sin
     if (kAdjacent) {
         // pair e is elements 2e and 2e + 1: regroup the eight as evens (p) and odds (q)
@@ -174,8 +174,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(con
     }
     if (turns) {
         const float *row = a.cos_sin + static_cast<int64_t>(pos) * a.rotary_dim + 4 * c;
-        const float4 cs = __ldg(reinterpret_cast<const float4 *>(row));
-        const float4 sn = __ldg(reinterpret_cast<const float4 *>(row + half));
+        const float4 cs = *reinterpret_cast<const float4 *>(row);
+        const float4 sn = *reinterpret_cast<const float4 *>(row + half);
         const float2 c2[2] = {make_float2(cs.x, cs.y), make_float2(cs.z, cs.w)};
         const float2 s2[2] = {make_float2(sn.x, sn.y), make_float2(sn.z, sn.w)};
 #pragma unroll
