@@ -48,11 +48,13 @@ template <int D> struct Tile {
     static constexpr int kStages = D == 128 ? 4 : 8;    // ring entries (128 KB)
     static constexpr int kOffKV = 2 * kBytes;           // after Q_0, Q_1
     static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // chain 1's maxima and sums: 2 x 128 floats
-    static constexpr int kOffBar = kOffJoin + 2 * 128 * 4;
+    static constexpr int kOffScratch = kOffJoin + 2 * 128 * 4;   // of the schedule
+    static constexpr int kOffBar = kOffScratch + sizeof(ShareScratch);
     static constexpr int kNumBars = 14 + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
     static constexpr int kSmem = kOffMisc + 8 + 4 * kFlags + 4 * kStages + 1024;  // + alignment
-    static_assert(kSmem + 512 <= 227 * 1024, "shared memory, with the kernel's static part");
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    static_assert(sizeof(ShareScratch) % 8 == 0, "the barriers behind it");
     // pieces whose V tiles can be in the ring at once, one more that the cleaning warp has begun,
     // and one without mixed tiles (only a share's last)
     static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
@@ -123,7 +125,7 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
     }
     // (memory of its own: chain 1 may write `join` while other warps still read the share's start)
-    __shared__ ShareScratch scratch;
+    ShareScratch &scratch = *reinterpret_cast<ShareScratch *>(smem + TL::kOffScratch);
     int64_t x0, x1;
     int item_cost;
     previous_kernel_done();
