@@ -27,9 +27,14 @@
 // infinity would not be 0, so values that no row sees are zeroed in shared memory, and non-finite
 // values that some rows see are zeroed and added afterwards to the rows that do see them.
 // Weights are taken against the reference maximum in use; only when a row's maximum exceeds it by
-// more than 2^8 are its O and sum rescaled.  The sum is of the weights before their rounding to 16 bits
-// (half a step of each, for the second product): with a second sum, of the rounded ones, as normaliser a
-// batch of 38 trees of 256 rows took 7 % longer.  Every wait is bounded (2 s): on expiry
+// more than 2^8 are its O and sum rescaled.
+// The matrix instructions take 16-bit operands, so the weights are rounded (half a step of each) for the
+// second product; float32 weights would be two such products.  On normal scores that makes the output's
+// error 1.35 to 1.4 times that of rounding the result alone (bf16 2.3e-3 of its rms, fp16 2.9e-4).  The sum is of
+// the weights before that rounding: with a second sum, of the rounded ones, as normaliser a batch of 38
+// trees of 256 rows took 7 % longer, with the same error on normal scores; only where most weights of a
+// row are equal, so that one rounding is common to them all, would it cancel (1.0 times instead of 1.35).
+// Every wait is bounded (2 s): on expiry
 // KV_DERR_TIMEOUT is set, what was issued is drained, TMEM is freed and the CTA returns.
 #include "tree_common.cuh"
 
@@ -597,7 +602,12 @@ size_t align256(size_t x) { return (x + 255) & ~static_cast<size_t>(255); }
 }  // namespace
 
 // Trees of up to 128 rows a kv head go by groups of heads (tree_packed.cu, which has the times of both);
-// wider ones, and a single kv head, take the kernel of this file.
+// wider ones, and a single kv head, take the kernel of this file.  A single head, us here and as the first of
+// two packed ones (whose boxes carry it alone, the other half zeros), 38 sequences of 8000 tokens and 304:
+//   16/1 heads of 128 dims, 64 rows      47, 243   packed 53, 320   (blocks of 8: 59, 341 against 67, 435)
+//   5/1 heads of 64 dims, 60 rows        43, 238   packed 42, 231   (blocks of 8: 58, 346 against 56, 335)
+//                         125 rows       44, 238   packed 45, 235
+// (64 dims are within 5 % either way, so that one rule serves both).
 TreePlan plan_tree(int num_seqs, int max_query_len, int group, int num_kv_heads, int head_dim, int num_workers, int sm_count) {
     TreePlan t;
     const int rows = max_query_len * group;

@@ -20,7 +20,7 @@ constexpr uint32_t kTmemCols = 512;
 constexpr float kRescaleLog2 = 8.0f;   // a row's reference maximum moves when exceeded by more
 // log2 of a factor on all weights, sums and O (it leaves with the normaliser, and the lse takes it off).  fp16
 // weights below 2^-14 lose digits and those below 2^-25 vanish, which the sum of many such keys shows: 9000
-// keys of 2^-20.5 each were 2 % off, of 2^-25.5 lost.  With the largest weight, 2^kRescaleLog2, at 2^15 under
+// keys of 2^-20.5 each were 3 % off, of 2^-25.5 lost.  With the largest weight, 2^kRescaleLog2, at 2^15 under
 // fp16's 65504, a key is off by at most 2^-32 of its row's largest weight.  bf16 has float's exponents.
 template <typename T> constexpr float kWeightLog2 = 0.f;
 template <> constexpr float kWeightLog2<__half> = 7.f;
