@@ -71,6 +71,17 @@ KV_API kv_status kv_bm_create(int32_t num_blocks, int32_t block_size, int32_t nu
                               int32_t max_blocks_per_row, int32_t window, int32_t zero_fill,
                               kv_block_manager **out);
 
+/*
+ * kv_bm_create_sinks - kv_bm_create for layers whose windows keep sinks (pagedkv_sinks.h): the window's
+ * release spares the blocks of a row's first num_sinks tokens (the first ceil(num_sinks / block_size)
+ * entries), so that after a step of n tokens a row holds at most that many more live blocks.  Those
+ * blocks also stay shareable: kv_bm_share_prefix takes up to that many from a row whose window has moved
+ * on.  num_sinks 0 is kv_bm_create; without a window nothing is released and it means nothing.
+ */
+KV_API kv_status kv_bm_create_sinks(int32_t num_blocks, int32_t block_size, int32_t num_rows,
+                                    int32_t max_blocks_per_row, int32_t window, int32_t num_sinks,
+                                    int32_t zero_fill, kv_block_manager **out);
+
 /* Frees the manager (NULL is ignored). */
 KV_API void kv_bm_destroy(kv_block_manager *bm);
 

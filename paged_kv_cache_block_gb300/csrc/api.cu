@@ -1324,4 +1324,163 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
     return ok();
 }
 
+// ---------------------------------------------------------------- windows with sinks (pagedkv_sinks.h)
+
+static int log2_of(int32_t power_of_two) {
+    int shift = 0;
+    while ((1 << shift) < power_of_two) ++shift;
+    return shift;
+}
+
+// A paged cache of any type, as the calls with sinks take it.
+struct SinkCache {
+    const void *k, *v;
+    kv_dtype dtype;
+    int32_t num_kv_heads, head_dim, block_size, num_blocks;
+    float k_scale, v_scale;            // E4M3
+    const float *k_scales, *v_scales;  // INT4
+    int32_t group_size;
+    int64_t bytes() const {
+        const int64_t elements = static_cast<int64_t>(num_blocks) * block_size * num_kv_heads * head_dim;
+        return dtype == KV_INT4 ? elements / 2 : (dtype == KV_FP8_E4M3 ? elements : 2 * elements);
+    }
+    int64_t scale_bytes() const { return dtype == KV_INT4 ? 4ll * num_kv_heads * (head_dim / group_size) : 0; }
+};
+
+static kv_status check_sink_cache(const SinkCache &c, kv_dtype q_dtype) {
+    if (q_dtype != KV_F16 && q_dtype != KV_BF16) return fail(KV_ERR_UNSUPPORTED, "q dtype must be fp16 or bf16");
+    if (c.dtype == KV_INT4) return check_int4_layout(c.head_dim, c.group_size, c.k_scales, c.v_scales);
+    if (c.dtype != q_dtype && c.dtype != KV_FP8_E4M3)
+        return fail(KV_ERR_UNSUPPORTED, "a 16-bit cache must have the q dtype");
+    if (c.dtype == KV_FP8_E4M3 &&
+        !(c.k_scale > 0.f && c.v_scale > 0.f && std::isfinite(c.k_scale) && std::isfinite(c.v_scale)))
+        return fail(KV_ERR_INVALID_ARG, "E4M3 scales must be finite and > 0");
+    return KV_OK;
+}
+
+static kv_status decode_sinks(const void *q, kv_dtype q_dtype, int32_t num_seqs, int32_t q_len, int32_t num_q_heads,
+                              const SinkCache &c, const int32_t *block_table, int64_t bt_stride,
+                              int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, float scale,
+                              int32_t window, int32_t num_sinks, int32_t num_workers, void *workspace,
+                              size_t workspace_bytes, void *out, float *lse_out, int32_t *d_err, void *stream) {
+    if (num_seqs < 0 || q_len < 1 || num_q_heads < 1 || c.num_kv_heads < 1 || max_seq_len < 1 || window < 0 ||
+        num_sinks < 0 || num_workers < 0 || c.num_blocks < 1 || max_blocks_per_seq < 1 || bt_stride < max_blocks_per_seq)
+        return fail(KV_ERR_INVALID_ARG, "invalid size argument");
+    kv_status st = check_sink_cache(c, q_dtype);
+    if (st != KV_OK) return st;
+    const bool int4 = c.dtype == KV_INT4, fp8 = c.dtype == KV_FP8_E4M3;
+    const float scale_log2 = scale * (fp8 ? c.k_scale : 1.0f) * 1.4426950408889634f * (int4 ? 16777216.f : 1.0f);
+    if (!std::isfinite(scale_log2)) return fail(KV_ERR_INVALID_ARG, "scale must be finite");
+    if (num_seqs == 0) return ok();
+    if (!q || !c.k || !c.v || !block_table || !seq_lens || !out) return fail(KV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(c.k, 16) || !aligned(c.v, 16))
+        return fail(KV_ERR_INVALID_ARG, "q, out and caches must be 16-byte aligned");
+    if (!aligned(lse_out, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(d_err, 4))
+        return fail(KV_ERR_INVALID_ARG, "misaligned pointer");
+    // workers finish sequences while others still read theirs
+    const int64_t B = num_seqs, rows = B * q_len * num_q_heads;
+    const ByteRange outs[] = {{out, 2 * rows * c.head_dim}, {lse_out, 4 * rows},
+                              {workspace, static_cast<int64_t>(std::min<size_t>(workspace_bytes, INT64_MAX))}};
+    const ByteRange ins[] = {{q, 2 * rows * c.head_dim}, {seq_lens, 4 * B},
+                             {block_table, 4 * ((B - 1) * bt_stride + max_blocks_per_seq)}, {c.k, c.bytes()},
+                             {c.v, c.bytes()}, {c.k_scales, c.scale_bytes()}, {c.v_scales, c.scale_bytes()}};
+    bool clash = overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2]);
+    for (const ByteRange &o : outs)
+        for (const ByteRange &i : ins) clash |= overlap(o, i);
+    if (clash) return fail(KV_ERR_INVALID_ARG, "an output or the workspace overlaps an input or another output");
+    int dev;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = bind_device(s, &dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device of stream");
+    DeviceInfo info;
+    if ((e = device_info(dev, &info)) != cudaSuccess) return cuda_fail(e, "device attributes");
+    pkv::DecodePlan plan{};
+    st = int4 ? plan_decode_int4(num_seqs, q_len, num_q_heads, c.num_kv_heads, c.head_dim, c.block_size, max_seq_len,
+                                 window, num_workers, info, &plan)
+              : plan_decode(num_seqs, q_len, num_q_heads, c.num_kv_heads, c.head_dim, c.block_size, max_seq_len,
+                            window, num_workers, c.dtype, info, &plan);
+    if (st != KV_OK) return st;
+    if (!workspace || workspace_bytes < plan.workspace_bytes)
+        return fail(KV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.workspace_bytes,
+                    workspace ? workspace_bytes : 0);
+    if (!aligned(workspace, 256)) return fail(KV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    pkv::DecodeArgs a;
+    std::memset(&a, 0, sizeof a);
+    char *ws = static_cast<char *>(workspace);
+    a.ws_prefix = reinterpret_cast<int32_t *>(ws + plan.ws_prefix_off);
+    a.ws_pieces = int4 ? nullptr : reinterpret_cast<int32_t *>(ws + plan.ws_pieces_off);
+    a.ws_lse = reinterpret_cast<float *>(ws + plan.ws_lse_off);
+    a.ws_o = reinterpret_cast<float *>(ws + plan.ws_o_off);
+    CUtensorMap tk, tv;
+    const int32_t heads = int4 ? 1 : plan.heads_per_cta;  // INT4: every warp loads its own head's rows
+    for (int i = 0; i < 2 && st == KV_OK; ++i)
+        st = encode_cache_map(i ? &tv : &tk, i ? c.v : c.k, c.dtype, c.num_blocks, c.block_size, c.num_kv_heads,
+                              c.head_dim, heads);
+    if (st != KV_OK) return st;
+    a.q = q;
+    a.out = out;
+    a.lse_out = lse_out;
+    a.block_table = block_table;
+    a.bt_stride = bt_stride;
+    a.max_blocks_per_seq = max_blocks_per_seq;
+    a.seq_lens = seq_lens;
+    a.max_seq_len = std::min(max_seq_len, INT32_MAX - 64);  // a last block's tokens count in 32 bits
+    a.d_err = d_err;
+    a.num_seqs = num_seqs;
+    a.q_len = q_len;
+    a.num_q_heads = num_q_heads;
+    a.num_kv_heads = c.num_kv_heads;
+    a.head_dim = c.head_dim;
+    a.block_size = c.block_size;
+    a.num_blocks = c.num_blocks;
+    a.window = window;
+    a.num_sinks = window > 0 ? std::min(num_sinks, a.max_seq_len) : 0;
+    a.scale_log2 = scale_log2;  // INT4: the MMAs see codes in units of 2^-24
+    a.v_scale = fp8 ? c.v_scale : 1.0f;
+    a.v_cache = c.v;
+    if (int4) {
+        a.k_gscales = c.k_scales;
+        a.v_gscales = c.v_scales;
+        a.group_shift = log2_of(c.group_size);
+        a.lse_offset_scale = 8.f * scale;
+        e = pkv::launch_paged_decode_sinks_int4(tk, tv, a, plan, q_dtype, s);
+    } else {
+        e = pkv::launch_paged_decode_sinks(tk, tv, a, plan, q_dtype, c.dtype, s);
+    }
+    if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
+    return ok();
+}
+
+kv_status kv_paged_attention_decode_sinks(const void *q, kv_dtype q_dtype, int32_t num_seqs, int32_t q_len,
+                                          int32_t num_q_heads, const void *k_cache, const void *v_cache,
+                                          kv_dtype cache_dtype, int32_t num_kv_heads, int32_t head_dim,
+                                          int32_t block_size, int32_t num_blocks, const int32_t *block_table,
+                                          int64_t bt_stride, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+                                          int32_t max_seq_len, float scale, int32_t window, int32_t num_sinks,
+                                          float k_scale, float v_scale, int32_t num_workers, void *workspace,
+                                          size_t workspace_bytes, void *out, float *lse_out, int32_t *d_err,
+                                          void *stream) {
+    if (cache_dtype == KV_INT4)
+        return fail(KV_ERR_UNSUPPORTED, "INT4 caches are read by kv_paged_attention_decode_sinks_int4");
+    const SinkCache c{k_cache, v_cache, cache_dtype, num_kv_heads, head_dim, block_size, num_blocks,
+                      k_scale, v_scale, nullptr, nullptr, 0};
+    return decode_sinks(q, q_dtype, num_seqs, q_len, num_q_heads, c, block_table, bt_stride, max_blocks_per_seq, seq_lens,
+                        max_seq_len, scale, window, num_sinks, num_workers, workspace, workspace_bytes, out, lse_out,
+                        d_err, stream);
+}
+
+kv_status kv_paged_attention_decode_sinks_int4(
+    const void *q, kv_dtype q_dtype, int32_t num_seqs, int32_t q_len, int32_t num_q_heads, const void *k_cache,
+    const void *v_cache, int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks,
+    const int32_t *block_table, int64_t bt_stride, int32_t max_blocks_per_seq, const int32_t *seq_lens,
+    int32_t max_seq_len, float scale, int32_t window, int32_t num_sinks, const float *k_scales, const float *v_scales,
+    int32_t group_size, int32_t num_workers, void *workspace, size_t workspace_bytes, void *out, float *lse_out,
+    int32_t *d_err, void *stream) {
+    const SinkCache c{k_cache, v_cache, KV_INT4, num_kv_heads, head_dim, block_size, num_blocks,
+                      1.f, 1.f, k_scales, v_scales, group_size};
+    return decode_sinks(q, q_dtype, num_seqs, q_len, num_q_heads, c, block_table, bt_stride, max_blocks_per_seq, seq_lens,
+                        max_seq_len, scale, window, num_sinks, num_workers, workspace, workspace_bytes, out, lse_out,
+                        d_err, stream);
+}
+
 }  // extern "C"

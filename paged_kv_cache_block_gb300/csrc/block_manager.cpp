@@ -12,8 +12,9 @@
 //   - the free pool is a ring of num_blocks ids (first in, first out);
 //   - the table is mirrored in one flat int32 array [num_rows * max_blocks_per_row] that holds
 //     the last value staged for each entry, so a row's blocks are a contiguous slice;
-//   - released blocks are always a prefix of a row (a window only moves forward), so a row is
-//     (tokens, logical block count, first live index);
+//   - released blocks are always one run of a row (a window only moves forward, and the blocks of
+//     the first num_sinks tokens stay), so a row is (tokens, logical block count, first live index
+//     behind the run), and the run starts at sink_blocks;
 //   - staged writes are a dirty flag per table entry plus the list of dirty entries, sorted by
 //     flat index (= (row, column) order) at flush; new blocks are a flag per block plus a list.
 // Every operation is O(blocks it touches); nothing scans the pool or the table.
@@ -26,6 +27,7 @@
 
 struct kv_block_manager {
     int32_t num_blocks, block_size, num_rows, max_blocks, window;
+    int32_t sink_blocks;  // blocks at the start of a row that its window never releases
     bool zero_fill;
     std::vector<int32_t> ring;  // free pool, ring buffer: ring[(head + i) % num_blocks]
     int64_t head = 0;
@@ -38,7 +40,7 @@ struct kv_block_manager {
     std::vector<int64_t> dirty_list;
     std::vector<int64_t> tokens;     // per row
     std::vector<int32_t> nblk;       // per row: logical blocks
-    std::vector<int32_t> first_live;  // per row: entries below it were released by the window
+    std::vector<int32_t> first_live;  // per row: entries from sink_blocks up to it were released by the window
 
     int32_t take() {
         const int32_t b = ring[head];
@@ -77,13 +79,13 @@ struct kv_block_manager {
         if (window <= 0) return;
         const int64_t first_query = tokens[row];
         int32_t *e = row_entries(row);
-        int32_t j = first_live[row];
+        int32_t j = std::max(first_live[row], sink_blocks);
         while (j < nblk[row] && static_cast<int64_t>(j + 1) * block_size - 1 <= first_query - window) {
             drop(e[j]);
             stage(row, j, -1);
             ++j;
         }
-        first_live[row] = j;
+        if (j > sink_blocks) first_live[row] = j;  // (else nothing of the row has been released)
     }
 
     int32_t pending_zero() const {
@@ -114,13 +116,19 @@ extern "C" {
 kv_status kv_bm_create(int32_t num_blocks, int32_t block_size, int32_t num_rows,
                        int32_t max_blocks_per_row, int32_t window, int32_t zero_fill,
                        kv_block_manager **out) {
+    return kv_bm_create_sinks(num_blocks, block_size, num_rows, max_blocks_per_row, window, 0, zero_fill, out);
+}
+
+kv_status kv_bm_create_sinks(int32_t num_blocks, int32_t block_size, int32_t num_rows,
+                             int32_t max_blocks_per_row, int32_t window, int32_t num_sinks,
+                             int32_t zero_fill, kv_block_manager **out) {
     if (!out) return pkv::record_error(KV_ERR_INVALID_ARG, "kv_bm_create: null out");
     *out = nullptr;
-    if (num_blocks <= 0 || block_size <= 0 || num_rows <= 0 || max_blocks_per_row <= 0 || window < 0)
+    if (num_blocks <= 0 || block_size <= 0 || num_rows <= 0 || max_blocks_per_row <= 0 || window < 0 || num_sinks < 0)
         return pkv::record_error(KV_ERR_INVALID_ARG,
-                                 "kv_bm_create: sizes must be positive (window >= 0): blocks %d, "
-                                 "block_size %d, rows %d, max_blocks_per_row %d, window %d",
-                                 num_blocks, block_size, num_rows, max_blocks_per_row, window);
+                                 "kv_bm_create: sizes must be positive (window, sinks >= 0): blocks %d, "
+                                 "block_size %d, rows %d, max_blocks_per_row %d, window %d, sinks %d",
+                                 num_blocks, block_size, num_rows, max_blocks_per_row, window, num_sinks);
     kv_block_manager *bm = new (std::nothrow) kv_block_manager();
     if (!bm) return pkv::record_error(KV_ERR_INVALID_ARG, "kv_bm_create: out of host memory");
     try {
@@ -129,6 +137,7 @@ kv_status kv_bm_create(int32_t num_blocks, int32_t block_size, int32_t num_rows,
         bm->num_rows = num_rows;
         bm->max_blocks = max_blocks_per_row;
         bm->window = window;
+        bm->sink_blocks = static_cast<int32_t>((static_cast<int64_t>(num_sinks) + block_size - 1) / block_size);
         bm->zero_fill = zero_fill != 0;
         bm->ring.resize(num_blocks);
         for (int32_t b = 0; b < num_blocks; ++b) bm->ring[b] = b;
@@ -198,6 +207,8 @@ kv_status kv_bm_free(kv_block_manager *bm, int32_t row) {
     if (st == KV_OK) st = check_row(bm, row, "kv_bm_free");
     if (st != KV_OK) return st;
     const int32_t *e = bm->row_entries(row);
+    if (bm->first_live[row] > 0)  // the sinks' blocks, before the released run
+        for (int32_t j = 0; j < bm->sink_blocks; ++j) bm->drop(e[j]);
     for (int32_t j = bm->first_live[row]; j < bm->nblk[row]; ++j) bm->drop(e[j]);
     bm->nblk[row] = 0;
     bm->first_live[row] = 0;
@@ -219,9 +230,9 @@ kv_status kv_bm_share_prefix(kv_block_manager *bm, int32_t dst_row, int32_t src_
         bm->tokens[src_row] < static_cast<int64_t>(num_blocks) * bm->block_size)
         return pkv::record_error(KV_ERR_INVALID_ARG,
                                  "kv_bm_share_prefix: row %d has no %d full blocks", src_row, num_blocks);
-    if (num_blocks > 0 && bm->first_live[src_row] > 0)
+    if (num_blocks > bm->sink_blocks && bm->first_live[src_row] > 0)
         return pkv::record_error(KV_ERR_INVALID_ARG,
-                                 "kv_bm_share_prefix: row %d released its first blocks", src_row);
+                                 "kv_bm_share_prefix: row %d released blocks of that prefix", src_row);
     const int32_t *s = bm->row_entries(src_row);
     for (int32_t j = 0; j < num_blocks; ++j) {
         const int32_t b = s[j];

@@ -95,13 +95,33 @@ __device__ __forceinline__ int checked_len(const DecodeArgs &a, int b) {
     return ok ? L : -1;
 }
 
+// The keys that a sequence of length L attends, as the axis the stages are cut from.  Without sinks
+// the axis is the positions themselves and starts at the window's first block.  With sinks it is the
+// sequence without the blocks that no row sees, those between the last sink's block and the window's
+// first: block c of the axis is block c of the sequence below sink_blocks, and block c + hidden from
+// there on, and all lengths and positions behind the gap are smaller by hidden * block_size.  The
+// kernel runs on that axis as on an ordinary sequence that starts at block 0, so a window's keys and
+// its sinks share stages and no stage is spent on the gap.
+struct SinkAxis {
+    int hidden;  // blocks left out
+    int len;     // length on the axis
+};
+__device__ __forceinline__ int sink_blocks(const DecodeArgs &a, int bs_shift) {
+    return (a.num_sinks + a.block_size - 1) >> bs_shift;
+}
+__device__ __forceinline__ SinkAxis sink_axis(const DecodeArgs &a, int L, int bs_shift) {
+    const int first = a.window > 0 ? max(0, L - a.q_len - a.window + 1) >> bs_shift : 0;
+    const int hidden = max(0, first - sink_blocks(a, bs_shift));
+    return SinkAxis{hidden, L - (hidden << bs_shift)};
+}
+
 // Per-CTA schedule, computed by every thread of the block (it contains __syncthreads):
 //   Ls[b]  the length of sequence b, or -1 when it is rejected (KV_DERR_BAD_LEN, reported once);
 //          without kLens there is no table: lengths are read from seq_lens (checked_len);
 //   (returns whether some length was rejected)
 //   P[i]   the number of stages of items 0 .. i-1 (an item is (head group, sequence), group-major;
 //          a stage is BPS consecutive cache blocks of the attended range), P[0] = 0.
-template <bool kLens = true>
+template <bool kLens = true, bool kSinks = false>
 __device__ __forceinline__ bool build_schedule(const DecodeArgs &a, int NI, int BPS, int32_t *Ls,
                                                int32_t *P, int32_t *warp_sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -126,9 +146,13 @@ __device__ __forceinline__ bool build_schedule(const DecodeArgs &a, int NI, int 
             if constexpr (kLens) L = Ls[seq];
             else L = checked_len(a, seq);
             if (L < 0) return 0;
-            const int lo_key = a.window > 0 ? max(0, L - q_len - a.window + 1) : 0;
-            const int nb = ((L + bs - 1) >> bs_shift) - (lo_key >> bs_shift);
-            return (nb + BPS - 1) >> bps_shift;
+            if constexpr (kSinks) {
+                return (((sink_axis(a, L, bs_shift).len + bs - 1) >> bs_shift) + BPS - 1) >> bps_shift;
+            } else {
+                const int lo_key = a.window > 0 ? max(0, L - q_len - a.window + 1) : 0;
+                const int nb = ((L + bs - 1) >> bs_shift) - (lo_key >> bs_shift);
+                return (nb + BPS - 1) >> bps_shift;
+            }
         };
         int sum = 0;
         const int seq_lo = lo % B;
@@ -163,9 +187,13 @@ __device__ __forceinline__ bool build_schedule(const DecodeArgs &a, int NI, int 
     return any_rejected;  // (an item without stages is one of a rejected length)
 }
 
+// Whether a piece of weight w counts in a merge: one of weight 0 (no key seen) adds nothing.  kNan:
+// a piece whose weight is NaN (a score that its row sees was NaN) counts, so that the NaN stays.
+template <bool kNan> __device__ __forceinline__ bool counts(float w) { return kNan ? w != 0.f : w > 0.f; }
+
 // One warp per (item, row): combine the pieces of a sequence that several CTAs shared, and
 // write zeros (lse -inf) for sequences whose length was rejected.  P is the stage prefix.
-template <typename QT, int D>
+template <typename QT, int D, bool kNan = false>
 __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t *P, int num_ctas,
                                           int64_t w, int lane) {
     const DecodeArgs &a = kp.a;
@@ -220,7 +248,8 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
         mx = lv;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        const float wl = has && mx != -INFINITY ? expf(lv - mx) : 0.f;
+        const float wl = kNan ? (has && lv != -INFINITY ? expf(lv - (mx == -INFINITY ? 0.f : mx)) : 0.f)
+                              : (has && mx != -INFINITY ? expf(lv - mx) : 0.f);
         wsum = wl;
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
@@ -228,21 +257,22 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
         for (int u = 0; u < kFewPieces; ++u) {
             const float wu = __shfl_sync(0xffffffffu, wl, u);
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] += wu > 0.f ? wu * v[u][e] : 0.f;
+            for (int e = 0; e < kPer; ++e) acc[e] += counts<kNan>(wu) ? wu * v[u][e] : 0.f;
         }
     } else {
         for (int c = c_lo + lane; c <= c_hi; c += 32)
             if (!empty_share(c)) mx = fmaxf(mx, __ldcg(a.ws_lse + static_cast<int64_t>(item + c) * kp.rows_per_item + rr));
 #pragma unroll
         for (int o = 16; o > 0; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-        if (mx != -INFINITY) {
+        const float ref = kNan && mx == -INFINITY ? 0.f : mx;
+        if (kNan || mx != -INFINITY) {
             // pieces 32 at a time: lane i weighs piece base + i; the partial rows are then loaded
             // four pieces at a time, every load issued before the sums use them
             for (int base = c_lo; base <= c_hi; base += 32) {
                 const int c = base + lane;
                 float wl = 0.f;
                 if (c <= c_hi && !empty_share(c))
-                    wl = expf(__ldcg(a.ws_lse + static_cast<int64_t>(item + c) * kp.rows_per_item + rr) - mx);
+                    wl = expf(__ldcg(a.ws_lse + static_cast<int64_t>(item + c) * kp.rows_per_item + rr) - ref);
                 float wsb = wl;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) wsb += __shfl_xor_sync(0xffffffffu, wsb, o);
@@ -253,7 +283,7 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         w[u] = __shfl_sync(0xffffffffu, wl, (u0 + u) & 31);
-                        const bool ok = u0 + u < nb && w[u] > 0.f;  // a piece of weight 0 adds nothing
+                        const bool ok = u0 + u < nb && counts<kNan>(w[u]);  // a piece of weight 0 adds nothing
                         const float *src =
                             a.ws_o + (static_cast<int64_t>(item + base + u0 + u) * kp.rows_per_item + rr) * D + lane * kPer;
 #pragma unroll
@@ -267,27 +297,27 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
             }
         }
     }
-    const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+    const float inv = counts<kNan>(wsum) ? 1.f / wsum : 0.f;
 #pragma unroll
     for (int e = 0; e < kPer; e += 2)
         *reinterpret_cast<uint32_t *>(orow + e) = pack2<QT>(acc[e] * inv, acc[e + 1] * inv);
-    if (a.lse_out && lane == 0) a.lse_out[rowid] = wsum > 0.f ? mx + logf(wsum) : -INFINITY;
+    if (a.lse_out && lane == 0) a.lse_out[rowid] = counts<kNan>(wsum) ? mx + logf(wsum) : -INFINITY;
 }
 
-template <typename QT, int D>
+template <typename QT, int D, bool kNan>
 __global__ void lse_merge_kernel(const __grid_constant__ KernelParams kp, int num_ctas) {
     const int64_t rows = static_cast<int64_t>(kp.num_items) * kp.rows_per_item;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     if (w >= rows) return;
-    merge_row<QT, D>(kp, kp.a.ws_prefix, num_ctas, w, threadIdx.x & 31);
+    merge_row<QT, D, kNan>(kp, kp.a.ws_prefix, num_ctas, w, threadIdx.x & 31);
 }
 
-template <typename QT, int D>
+template <typename QT, int D, bool kNan = false>
 static cudaError_t row_merge(const KernelParams &kp, int num_workers, cudaStream_t stream) {
     const int64_t rows = static_cast<int64_t>(kp.num_items) * kp.rows_per_item;
     const int threads = 256;
     const int64_t blocks = (rows * 32 + threads - 1) / threads;
-    lse_merge_kernel<QT, D><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
+    lse_merge_kernel<QT, D, kNan><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
     return cudaGetLastError();
 }
 
@@ -296,5 +326,7 @@ static cudaError_t row_merge(const KernelParams &kp, int num_workers, cudaStream
 // (The 16-bit and E4M3 decode kernels write their partial results as fragment tiles and have
 // their own tile merge, in paged_decode_kernel.cuh.)
 cudaError_t launch_lse_merge(const KernelParams &kp, int num_workers, int q_dtype, cudaStream_t stream);
+// The same for the INT4 kernel with sinks, whose pieces may hold NaN (paged_sinks.cu).
+cudaError_t launch_lse_merge_nan(const KernelParams &kp, int num_workers, int q_dtype, cudaStream_t stream);
 
 }  // namespace pkv

@@ -10,6 +10,7 @@
 #include "../../include/pagedkv_blocks.h"
 #include "../../include/pagedkv_int4.h"
 #include "../../include/pagedkv_selftest.h"
+#include "../../include/pagedkv_sinks.h"
 #include "../../include/pagedkv_step.h"
 
 namespace pkv {
@@ -114,11 +115,19 @@ struct DecodeArgs {
     const float *k_gscales, *v_gscales;  // [num_kv_heads, head_dim >> group_shift]
     int32_t group_shift;                 // log2(group_size)
     float lse_offset_scale;              // 8 * softmax scale
+    // kernels with sinks only
+    const void *v_cache;  // 16-bit and E4M3 caches
+    int32_t num_sinks;    // a windowed row sees the keys below it too (0 without a window)
 };
 
 cudaError_t launch_paged_decode(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                 const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
                                 int cache_dtype, cudaStream_t stream);
+
+// The same with a window and sinks (paged_sinks.cu).
+cudaError_t launch_paged_decode_sinks(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                      const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
+                                      int cache_dtype, cudaStream_t stream);
 
 // Decode attention over INT4 caches (paged_decode_int4.cu): warps with private TMA rings,
 // int4_decode_warps(rows_per_warp) per CTA, then the merge kernel.
@@ -126,6 +135,9 @@ int int4_decode_warps(int rows_per_warp);
 cudaError_t launch_paged_decode_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                      const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
                                      cudaStream_t stream);
+cudaError_t launch_paged_decode_sinks_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                           const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
+                                           cudaStream_t stream);
 // The INT4 one-launch step: each worker writes (as INT4 codes) the new-token rows it reads.
 cudaError_t launch_decode_step_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                     const DecodeArgs &a, const StepArgs &f, const DecodePlan &plan,

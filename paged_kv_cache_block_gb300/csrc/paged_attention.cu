@@ -26,26 +26,6 @@ static cudaError_t launch_any(const CUtensorMap &tmap_k, const CUtensorMap &tmap
                : launch_rows<__nv_bfloat16, __nv_bfloat16, 128, kFused>(tmap_k, tmap_v, kp, plan, stream);
 }
 
-static KernelParams make_params(const DecodeArgs &a, const DecodePlan &plan) {
-    KernelParams kp;
-    kp.a = a;
-    kp.f = StepArgs{};
-    kp.heads_per_cta = plan.heads_per_cta;
-    kp.warps_per_head = plan.warps_per_head;
-    kp.blocks_per_stage = plan.blocks_per_stage;
-    kp.num_stages = plan.num_stages;
-    kp.box_bytes = plan.box_bytes;
-    kp.box_stride = plan.box_stride;
-    kp.num_items = plan.num_items;
-    kp.rows_per_item = plan.rows_per_item;
-    kp.sets_per_cta = 1;
-    kp.num_workers = plan.num_ctas;
-    kp.tile_ws = plan.tile_ws;
-    kp.item_cost = plan.item_cost;
-    kp.lens_smem = plan.lens_smem;
-    return kp;
-}
-
 cudaError_t launch_paged_decode(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                 const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
                                 int cache_dtype, cudaStream_t stream) {

@@ -72,7 +72,11 @@ __device__ __forceinline__ void write_int4_chunk(const DecodeArgs &a, const Step
 
 // kBS: the block size when it is fixed at compile time (8, 16 or 32: stages of 32 keys whose
 // geometry is then constant), 0 when it is read from the arguments (4, and 16-row tiles)
-template <typename QT, int RN, bool kFused, int kBS>
+// kSinks: a windowed row also sees the first num_sinks keys, on the shortened key axis (SinkAxis,
+// decode_common.cuh).  fp16 weights are then formed 2^14 higher than they are, as in
+// paged_decode_kernel.cuh, and a row whose scores hold NaN comes out NaN.  Codes decode to finite
+// values, so no value of a key that a row does not see can reach it.
+template <typename QT, int RN, bool kFused, int kBS, bool kSinks>
 __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
     paged_decode_int4_kernel(const __grid_constant__ CUtensorMap tmap_k,
                              const __grid_constant__ CUtensorMap tmap_v,
@@ -98,6 +102,9 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
     const int R = g * a.q_len;
     const int q_len = a.q_len;
     const int gshift = a.group_shift;
+    static_assert(!(kSinks && kFused), "the one-launch step has no form with sinks");
+    const int bs_shift = __ffs(bs) - 1;  // kSinks
+    constexpr float kShift = kSinks ? 14.f : 0.f;
 
     // ---------------------------------------------------------------- shared memory
     // [kWarps][NS] stages of (K boxes, V boxes), [kWarps][NS] full barriers, [kWarps][NS] stage
@@ -123,7 +130,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
         for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&full_bar[i]), 1);
         fence_barrier_init();
     }
-    (void)build_schedule(a, NI, BPS, Ls, P, warp_sums);
+    (void)build_schedule<true, kSinks>(a, NI, BPS, Ls, P, warp_sums);
     if (blockIdx.x == 0)  // the merge kernel reads the same prefix
         for (int i = threadIdx.x; i <= NI; i += blockDim.x) a.ws_prefix[i] = P[i];
 
@@ -228,6 +235,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
     const uint32_t stage_tx = 2u * BPS * kp.box_bytes;
     int ps = s0, p_slot = 0, p_item = item0 - 1, p_end = s0;  // p_end: first stage past p_item
     int p_row = 0, p_head = 0, p_nblk = 0, p_lb = 0;          // table row, kv head, blocks, next block
+    int p_hidden = 0;  // kSinks: blocks left out of the axis
     int cache_base = 0, my_id = a.num_blocks;
     bool my_ok = false;
     auto refresh_ids = [&](int base) {
@@ -236,7 +244,8 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
         my_ok = false;
         my_id = a.num_blocks;  // one past the pool: a copy from there reads zeros
         if (lb < p_nblk) {
-            const int e = a.block_table[static_cast<int64_t>(p_row) * a.bt_stride + lb];
+            const int behind = kSinks && lb >= sink_blocks(a, bs_shift) ? p_hidden : 0;
+            const int e = a.block_table[static_cast<int64_t>(p_row) * a.bt_stride + lb + behind];
             if (e >= 0 && e < a.num_blocks) {
                 my_id = e;
                 my_ok = true;
@@ -255,8 +264,15 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
             const int L = Ls[seq];
             p_row = seq;
             p_head = grp * HG + h_loc;
-            p_nblk = (L + bs - 1) / bs;
-            p_lb = (a.window > 0 ? max(0, L - q_len - a.window + 1) : 0) / bs + (ps - P[p_item]) * BPS;
+            if constexpr (kSinks) {
+                const SinkAxis ax = sink_axis(a, L, bs_shift);
+                p_hidden = ax.hidden;
+                p_nblk = (ax.len + bs - 1) >> bs_shift;
+                p_lb = (ps - P[p_item]) * BPS;
+            } else {
+                p_nblk = (L + bs - 1) / bs;
+                p_lb = (a.window > 0 ? max(0, L - q_len - a.window + 1) : 0) / bs + (ps - P[p_item]) * BPS;
+            }
             refresh_ids(p_lb);
         } else if (p_lb + BPS > cache_base + 32) {
             refresh_ids(p_lb);
@@ -382,7 +398,8 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                         const int tok = cr[j].c0 + l4 + (e >> 1) * 8;
                         const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
                         const int ph = pos_hi[nt][e & 1];
-                        const bool okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
+                        const bool okk =
+                            blk_ok && tok <= ph && (W <= 0 || tok > ph - W || (kSinks && tok < a.num_sinks));
                         v = okk ? v : -INFINITY;
                     }
                     sa[j][nt][e] = v;
@@ -400,10 +417,11 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                 const float ref = m_new == -INFINITY ? 0.f : m_new;
                 alpha[nt][e] = fast_exp2(m_run[nt][e] - ref);
                 m_run[nt][e] = m_new;
+                const float base = kSinks ? ref - kShift : ref;
 #pragma unroll
                 for (int j = 0; j < NCH; ++j) {
-                    sa[j][nt][e] = fast_exp2(sa[j][nt][e] - ref);
-                    sa[j][nt][e + 2] = fast_exp2(sa[j][nt][e + 2] - ref);
+                    sa[j][nt][e] = fast_exp2(sa[j][nt][e] - base);
+                    sa[j][nt][e + 2] = fast_exp2(sa[j][nt][e + 2] - base);
                 }
             }
         }
@@ -484,8 +502,9 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
             grp = item / B;
             L = Ls[seq];
             n_item = item_end - item_begin;
+            if constexpr (kSinks) L = sink_axis(a, L, bs_shift).len;  // positions on the axis from here on
             const int key_lo = a.window > 0 ? max(0, L - q_len - a.window + 1) : 0;
-            b0 = key_lo / bs;
+            b0 = kSinks ? 0 : key_lo / bs;
             lo_last = a.window > 0 ? max(0, L - a.window) : 0;
             hi_first = L - q_len;
             const int hkv = grp * HG + h_loc;
@@ -560,9 +579,10 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
             }
         }
         const bool pair = two || n_chunks == 2;
-        bool need_mask = (cr[0].c0 < lo_last) || (cr[0].c0 + 15 > hi_first) || (cr[0].mask != full_mask);
+        auto below = [&](const Int4Chunk &c) { return c.c0 < lo_last && !(kSinks && c.c0 + 15 < a.num_sinks); };
+        bool need_mask = below(cr[0]) || (cr[0].c0 + 15 > hi_first) || (cr[0].mask != full_mask);
         if (pair)
-            need_mask = need_mask || (cr[1].c0 < lo_last) || (cr[1].c0 + 15 > hi_first) ||
+            need_mask = need_mask || below(cr[1]) || (cr[1].c0 + 15 > hi_first) ||
                         (cr[1].mask != full_mask);
         if (pair) {
             if (need_mask) unit(cr, std::integral_constant<int, 2>{}, std::true_type{});
@@ -603,10 +623,12 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                     l += __shfl_xor_sync(0xffffffffu, l, 16);
                     const int r = rt * RN + nt * 8 + 2 * c4 + e;
                     if (r >= R) continue;
-                    const float inv = l > 0.f ? 1.f / l : 0.f;
-                    const float lse = l > 0.f ? (m_run[nt][e] + log2f(l)) * 0.69314718055994531f -
-                                                    a.lse_offset_scale * q_sum[nt][e]
-                                              : -INFINITY;
+                    const bool some = kSinks ? l != 0.f : l > 0.f;  // kSinks: NaN stays NaN
+                    const float inv = some ? 1.f / l : 0.f;
+                    const float m = kSinks ? m_run[nt][e] - kShift : m_run[nt][e];
+                    const float lse = some ? (m + log2f(l)) * 0.69314718055994531f -
+                                                 a.lse_offset_scale * q_sum[nt][e]
+                                           : -INFINITY;
                     const int64_t tokq = static_cast<int64_t>(seq) * q_len + r / g;
                     const int64_t rowid = tokq * a.num_q_heads + hkv * g + r % g;
                     const int64_t wrow = static_cast<int64_t>(item + vc) * kp.rows_per_item + h_loc * R + r;
@@ -618,7 +640,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                             const int d = (mt >> 1) * 32 + 4 * l4 + 2 * (mt & 1) + hf;
                             const float unit_scale = hf ? 1048576.f : 16777216.f;  // 2^20, 2^24
                             const float v =
-                                l > 0.f ? vsc[d >> gshift] * fmaf(o[mt][nt][2 * hf + e] * unit_scale, inv, -8.f) : 0.f;
+                                some ? vsc[d >> gshift] * fmaf(o[mt][nt][2 * hf + e] * unit_scale, inv, -8.f) : 0.f;
                             if (whole) static_cast<QT *>(a.out)[rowid * kD + d] = from_float<QT>(v);
                             else a.ws_o[wrow * kD + d] = v;
                         }
@@ -649,10 +671,10 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
     }
 }
 
-template <typename QT, int RN, bool kFused, int kBS>
+template <typename QT, int RN, bool kFused, int kBS, bool kSinks>
 cudaError_t launch_int4_typed(const CUtensorMap &tk, const CUtensorMap &tv, const KernelParams &kp,
                               const DecodePlan &plan, int q_dtype, cudaStream_t stream) {
-    auto kern = paged_decode_int4_kernel<QT, RN, kFused, kBS>;
+    auto kern = paged_decode_int4_kernel<QT, RN, kFused, kBS, kSinks>;
     constexpr int kMaxDevices = 64;
     static std::once_flag once[kMaxDevices];
     static cudaError_t attr_status[kMaxDevices];
@@ -674,7 +696,8 @@ cudaError_t launch_int4_typed(const CUtensorMap &tk, const CUtensorMap &tv, cons
     kern<<<plan.num_ctas, Int4Launch<RN>::kThreads, plan.smem_bytes, stream>>>(tk, tv, kp);
     e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    return launch_lse_merge(kp, kp.num_workers, q_dtype, stream);
+    return kSinks ? launch_lse_merge_nan(kp, kp.num_workers, q_dtype, stream)
+                  : launch_lse_merge(kp, kp.num_workers, q_dtype, stream);
 }
 
 }  // namespace
@@ -683,7 +706,7 @@ int int4_decode_warps(int rows_per_warp) {
     return rows_per_warp == 8 ? Int4Launch<8>::kWarps : Int4Launch<16>::kWarps;
 }
 
-template <bool kFused>
+template <bool kFused, bool kSinks = false>
 static cudaError_t launch_int4_any(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const DecodeArgs &a,
                                    const StepArgs &f, const DecodePlan &plan, int q_dtype, cudaStream_t stream) {
     if (a.num_seqs == 0) return cudaSuccess;
@@ -704,31 +727,34 @@ static cudaError_t launch_int4_any(const CUtensorMap &tmap_k, const CUtensorMap 
     kp.item_cost = 0;
     kp.lens_smem = 1;
     const bool f16 = q_dtype == KV_F16;
+    auto launch = [&](auto rows, auto block) {
+        constexpr int RN = decltype(rows)::value, kBS = decltype(block)::value;
+        return f16 ? launch_int4_typed<__half, RN, kFused, kBS, kSinks>(tmap_k, tmap_v, kp, plan, q_dtype, stream)
+                   : launch_int4_typed<__nv_bfloat16, RN, kFused, kBS, kSinks>(tmap_k, tmap_v, kp, plan, q_dtype, stream);
+    };
+    using std::integral_constant;
     if (plan.rows_per_warp == 8) {
         // 8-row tiles: the block size as a compile-time constant where stages hold 32 keys
         switch (a.block_size) {
-            case 8:
-                return f16 ? launch_int4_typed<__half, 8, kFused, 8>(tmap_k, tmap_v, kp, plan, q_dtype, stream)
-                           : launch_int4_typed<__nv_bfloat16, 8, kFused, 8>(tmap_k, tmap_v, kp, plan, q_dtype, stream);
-            case 16:
-                return f16 ? launch_int4_typed<__half, 8, kFused, 16>(tmap_k, tmap_v, kp, plan, q_dtype, stream)
-                           : launch_int4_typed<__nv_bfloat16, 8, kFused, 16>(tmap_k, tmap_v, kp, plan, q_dtype, stream);
-            case 32:
-                return f16 ? launch_int4_typed<__half, 8, kFused, 32>(tmap_k, tmap_v, kp, plan, q_dtype, stream)
-                           : launch_int4_typed<__nv_bfloat16, 8, kFused, 32>(tmap_k, tmap_v, kp, plan, q_dtype, stream);
-            default:
-                return f16 ? launch_int4_typed<__half, 8, kFused, 0>(tmap_k, tmap_v, kp, plan, q_dtype, stream)
-                           : launch_int4_typed<__nv_bfloat16, 8, kFused, 0>(tmap_k, tmap_v, kp, plan, q_dtype, stream);
+            case 8: return launch(integral_constant<int, 8>{}, integral_constant<int, 8>{});
+            case 16: return launch(integral_constant<int, 8>{}, integral_constant<int, 16>{});
+            case 32: return launch(integral_constant<int, 8>{}, integral_constant<int, 32>{});
+            default: return launch(integral_constant<int, 8>{}, integral_constant<int, 0>{});
         }
     }
-    return f16 ? launch_int4_typed<__half, 16, kFused, 0>(tmap_k, tmap_v, kp, plan, q_dtype, stream)
-               : launch_int4_typed<__nv_bfloat16, 16, kFused, 0>(tmap_k, tmap_v, kp, plan, q_dtype, stream);
+    return launch(integral_constant<int, 16>{}, integral_constant<int, 0>{});
 }
 
 cudaError_t launch_paged_decode_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                      const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
                                      cudaStream_t stream) {
     return launch_int4_any<false>(tmap_k, tmap_v, a, StepArgs{}, plan, q_dtype, stream);
+}
+
+cudaError_t launch_paged_decode_sinks_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                           const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
+                                           cudaStream_t stream) {
+    return launch_int4_any<false, true>(tmap_k, tmap_v, a, StepArgs{}, plan, q_dtype, stream);
 }
 
 cudaError_t launch_decode_step_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,

@@ -36,6 +36,9 @@
 //     them, and the head-dim order this produces is folded into the q fragments (for K) and
 //     into the output index (for V); k_scale folds into the score scale, v_scale into the output.
 //   * INT4 caches have their own kernel (paged_decode_int4.cu) on the same schedule and merge.
+//   * With sinks (kSinks, paged_sinks.cu) a windowed row also sees the sequence's first num_sinks
+//     keys.  The blocks between the sinks and the window are left out of the key axis (SinkAxis,
+//     decode_common.cuh), which is all the schedule, the ring and the masks have to know.
 #pragma once
 
 #include <mutex>
@@ -263,7 +266,18 @@ struct ChunkRef {
     uint32_t mask;          // valid blocks of that stage
 };
 
-template <typename QT, typename CT, int D, int RN, bool kFused, int kBS, bool kLens>
+// Non-finite halves of a packed 16-bit pair, as a mask of 0xffff each.
+template <typename T> __device__ __forceinline__ uint32_t nonfinite2(uint32_t v) {
+    constexpr uint32_t kExp = std::is_same<T, __half>::value ? 0x7c007c00u : 0x7f807f80u;
+    return __vcmpeq2(v & kExp, kExp);
+}
+
+// The weights of fp16 products are formed 2^14 higher than they are (kernels with sinks): a sink
+// often holds nearly all of a row's weight, and next to a weight of 1 an fp16 weight below 2^-14
+// would lose digits (below 2^-25 vanish) that the sum of some thousand such keys still needs.
+template <typename MT> constexpr float kWeightShift = std::is_same<MT, __half>::value ? 14.f : 0.f;
+
+template <typename QT, typename CT, int D, int RN, bool kFused, int kBS, bool kLens, bool kSinks>
 __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
     paged_decode_kernel(const __grid_constant__ CUtensorMap tmap_k,
                         const __grid_constant__ CUtensorMap tmap_v,
@@ -288,6 +302,8 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
     const int g = a.num_q_heads / a.num_kv_heads;
     const int R = g * a.q_len;
     const int q_len = a.q_len;
+    static_assert(!(kSinks && kFused), "the one-launch step has no form with sinks");
+    const int bs_shift = __ffs(bs) - 1;  // kSinks
 
     // ---------------------------------------------------------------- shared memory
     extern __shared__ uint8_t smem_raw[];
@@ -323,7 +339,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
     // seq_lens where they are needed, so that large batches keep the ring's stages)
     // (kLens: the plan kept the length table in shared memory)
     int32_t *Ls = kLens ? P + NI + 1 : nullptr;
-    const bool any_empty = build_schedule<kLens>(a, NI, BPS, Ls, P, warp_sums);
+    const bool any_empty = build_schedule<kLens, kSinks>(a, NI, BPS, Ls, P, warp_sums);
     // an item with stages has an accepted length
     auto len_of = [&](int seq) {
         if constexpr (kLens) return Ls[seq];
@@ -386,8 +402,16 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 }
                 L = len_cur;
             }
-            const int nblk = (L + bs - 1) / bs;
-            const int lb0 = (a.window > 0 ? max(0, L - q_len - a.window + 1) : 0) / bs + k * BPS;
+            int nblk, lb0, hidden = 0;
+            if constexpr (kSinks) {
+                const SinkAxis ax = sink_axis(a, L, bs_shift);
+                hidden = ax.hidden;
+                nblk = (ax.len + bs - 1) >> bs_shift;
+                lb0 = k * BPS;
+            } else {
+                nblk = (L + bs - 1) / bs;
+                lb0 = (a.window > 0 ? max(0, L - q_len - a.window + 1) : 0) / bs + k * BPS;
+            }
             // fused step: a new item's query offsets load beside its block ids (below), then its
             // positions
             const bool new_item = kFused && guard_item != item;
@@ -407,7 +431,8 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 my_ok = false;
                 my_id = a.num_blocks;  // one past the pool: a copy from there reads zeros
                 if (lb < nblk) {
-                    const int e = a.block_table[static_cast<int64_t>(seq) * a.bt_stride + lb];
+                    const int behind = kSinks && lb >= sink_blocks(a, bs_shift) ? hidden : 0;
+                    const int e = a.block_table[static_cast<int64_t>(seq) * a.bt_stride + lb + behind];
                     if (e >= 0 && e < a.num_blocks) {
                         my_id = e;
                         my_ok = true;
@@ -440,7 +465,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 int nx = item + 1;
                 while (P[nx + 1] == P[nx]) ++nx;
                 const int nseq = nx % B, nL = len_of(nseq);
-                const int nb0 = (a.window > 0 ? max(0, nL - q_len - a.window + 1) : 0) / bs;
+                const int nb0 = kSinks ? 0 : (a.window > 0 ? max(0, nL - q_len - a.window + 1) : 0) / bs;
                 prefetch_l2(a.block_table + static_cast<int64_t>(nseq) * a.bt_stride + nb0);
             }
             const int slot = pslot;
@@ -576,6 +601,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
     int seq = 0, grp = 0, L = 0, b0 = 0, key_lo = 0, lo_last = 0, hi_first = 0, n_item = 0;
     int slot = 0;
     uint32_t phase = 0;
+    uint32_t nonfinite = 0;  // kSinks: this lane has set aside a non-finite value of a partly seen key
     const int s0 = static_cast<int>(s_begin), s1 = static_cast<int>(s_end);
 
     // NCH 16-key chunks processed together; kMasked: some chunk holds keys a row must not see, or
@@ -646,7 +672,8 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                         const int tok = cr[j].c0 + l4 + (e >> 1) * 8;
                         const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
                         const int ph = pos_hi[nt][e & 1];
-                        const bool okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
+                        const bool okk =
+                            blk_ok && tok <= ph && (W <= 0 || tok > ph - W || (kSinks && tok < a.num_sinks));
                         v = okk ? v : -INFINITY;
                     }
                     sa[j][nt][e] = v;
@@ -664,10 +691,11 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 const float ref = m_new == -INFINITY ? 0.f : m_new;
                 alpha[nt][e] = fast_exp2(m_run[nt][e] - ref);
                 m_run[nt][e] = m_new;
+                const float base = kSinks ? ref - kWeightShift<MT> : ref;
 #pragma unroll
                 for (int j = 0; j < NCH; ++j) {
-                    sa[j][nt][e] = fast_exp2(sa[j][nt][e] - ref);
-                    sa[j][nt][e + 2] = fast_exp2(sa[j][nt][e + 2] - ref);
+                    sa[j][nt][e] = fast_exp2(sa[j][nt][e] - base);
+                    sa[j][nt][e + 2] = fast_exp2(sa[j][nt][e + 2] - base);
                 }
             }
         }
@@ -680,10 +708,15 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
             for (int j = 0; j < NCH; ++j) {
                 const uint32_t lo = pack2<MT>(sa[j][nt][0], sa[j][nt][1]);
                 const uint32_t hi = pack2<MT>(sa[j][nt][2], sa[j][nt][3]);
-                // the normaliser sums the rounded weights the MMA uses
-                const float2 ul = unpack2<MT>(lo), uh = unpack2<MT>(hi);
-                add0 += ul.x + uh.x;
-                add1 += ul.y + uh.y;
+                if constexpr (kSinks) {  // the weights themselves: the log-sum-exp keeps its digits
+                    add0 += sa[j][nt][0] + sa[j][nt][2];
+                    add1 += sa[j][nt][1] + sa[j][nt][3];
+                } else {
+                    // the normaliser sums the rounded weights the MMA uses
+                    const float2 ul = unpack2<MT>(lo), uh = unpack2<MT>(hi);
+                    add0 += ul.x + uh.x;
+                    add1 += ul.y + uh.y;
+                }
                 pb[j][nt][0] = movmatrix_t(lo);
                 pb[j][nt][1] = movmatrix_t(hi);
             }
@@ -714,11 +747,34 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 for (int e = 0; e < 4; ++e) {
                     const int tok = cr[j].c0 + 2 * c4 + (e >> 1) * 8 + (e & 1);
                     const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
-                    keep[e] = (blk_ok && tok >= key_lo && tok < L) ? 0xffffu : 0u;
+                    keep[e] = (blk_ok && (tok >= key_lo || (kSinks && tok < a.num_sinks)) && tok < L) ? 0xffffu : 0u;
                 }
                 keep_lo = keep[0] | (keep[1] << 16);
                 keep_hi = keep[2] | (keep[3] << 16);
             }
+            // kSinks: a non-finite value of a key that only some rows see (a weight of 0 times it would be
+            // NaN in the other rows) becomes zero too, and is added at the end of the piece to the rows
+            // that see it.  some_lo, some_hi: such keys.
+            uint32_t some_lo = 0, some_hi = 0;
+            if constexpr (kMasked && kSinks) {
+                uint32_t some[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int tok = cr[j].c0 + 2 * c4 + (e >> 1) * 8 + (e & 1);
+                    some[e] = tok > hi_first || (tok < lo_last && tok >= a.num_sinks) ? 0xffffu : 0u;
+                }
+                some_lo = some[0] | (some[1] << 16);
+                some_hi = some[2] | (some[3] << 16);
+            }
+            auto set_aside = [&](uint32_t (&f)[4]) {
+                if (q_len == 1) return;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t bad = nonfinite2<MT>(f[i]) & (i < 2 ? some_lo : some_hi);
+                    f[i] &= ~bad;
+                    nonfinite |= bad;
+                }
+            };
             if constexpr (kFp8) {
 #pragma unroll
                 for (int mt2 = 0; mt2 < kMT; mt2 += 2) {
@@ -735,6 +791,10 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                     if constexpr (kMasked) {
                         af0[0] &= keep_lo; af0[1] &= keep_lo; af0[2] &= keep_hi; af0[3] &= keep_hi;
                         af1[0] &= keep_lo; af1[1] &= keep_lo; af1[2] &= keep_hi; af1[3] &= keep_hi;
+                    }
+                    if constexpr (kMasked && kSinks) {
+                        set_aside(af0);
+                        set_aside(af1);
                     }
 #pragma unroll
                     for (int nt = 0; nt < kNR; ++nt) {
@@ -755,6 +815,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                         af[2] &= keep_hi;
                         af[3] &= keep_hi;
                     }
+                    if constexpr (kMasked && kSinks) set_aside(af);
 #pragma unroll
                     for (int nt = 0; nt < kNR; ++nt) MmaOp<MT>::run(o[mt][nt], af, pb[j][nt][0], pb[j][nt][1]);
                 }
@@ -772,8 +833,10 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
             grp = item / B;
             L = len_of(seq);
             n_item = P[item + 1] - P[item];
+            if constexpr (kSinks) L = sink_axis(a, L, bs_shift).len;  // positions on the axis from here on
+            nonfinite = 0;
             key_lo = a.window > 0 ? max(0, L - q_len - a.window + 1) : 0;
-            b0 = key_lo / bs;
+            b0 = kSinks ? 0 : key_lo / bs;
             lo_last = a.window > 0 ? max(0, L - a.window) : 0;
             hi_first = L - q_len;
             const int hkv = grp * HG + h_loc;
@@ -851,7 +914,8 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
         }
         const bool pair = two || n_chunks == 2;
         auto chunk_masked = [&](const ChunkRef &c) {
-            return (c.c0 < lo_last) || (c.c0 + 15 > hi_first) || (c.mask != full_mask);
+            return (c.c0 < lo_last && !(kSinks && c.c0 + 15 < a.num_sinks)) || (c.c0 + 15 > hi_first) ||
+                   (c.mask != full_mask);
         };
         if constexpr (kNR == 1) {
             const bool need_mask = chunk_masked(cr[0]) || (pair && chunk_masked(cr[1]));
@@ -890,6 +954,51 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
             const bool whole = seg_k0 == 0 && k_last == n_item - 1;
             const int hkv = grp * HG + h_loc;
             const TileRows tr{static_cast<int64_t>(seq) * q_len, hkv * g, g, R, a.num_q_heads};
+            if constexpr (kSinks) {
+                if (__any_sync(0xffffffffu, nonfinite != 0)) {
+                    // the values set aside, added to the rows that see their keys: as the weight is above
+                    // 0, the value itself will do.  The keys are the q_len - 1 at each edge of what the
+                    // window and the rows' own tokens leave in full view.
+                    const int hidden = sink_axis(a, len_of(seq), bs_shift).hidden;
+                    const int from = seg_k0 * ST, to = min(L, (k_last + 1) * ST);
+                    const int edge = max(key_lo, a.num_sinks), view = max(edge, lo_last);
+                    for (int t = edge; t < L; ++t) {
+                        if (t >= view && t <= hi_first) {  // seen by every row
+                            t = hi_first;
+                            continue;
+                        }
+                        if (t < from || t >= to) continue;
+                        const int lb = t >> bs_shift;
+                        const int id = a.block_table[static_cast<int64_t>(seq) * a.bt_stride + lb +
+                                                     (lb >= sink_blocks(a, bs_shift) ? hidden : 0)];
+                        if (id < 0 || id >= a.num_blocks) continue;
+                        const int64_t at =
+                            ((static_cast<int64_t>(id) * bs + (t & (bs - 1))) * a.num_kv_heads + hkv) * D;
+#pragma unroll
+                        for (int mt = 0; mt < kMT; ++mt)
+#pragma unroll
+                            for (int hf = 0; hf < 2; ++hf) {
+                                float v;
+                                if constexpr (kFp8) {
+                                    const __nv_fp8_storage_t c =
+                                        static_cast<const uint8_t *>(a.v_cache)[at + mt * 16 + 2 * l4 + hf];
+                                    v = __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
+                                } else {
+                                    v = to_float<QT>(static_cast<const QT *>(a.v_cache)[at + mt * 16 + l4 + 8 * hf]);
+                                }
+                                if (isfinite(v)) continue;
+#pragma unroll
+                                for (int nt = 0; nt < kNR; ++nt)
+#pragma unroll
+                                    for (int e = 0; e < 2; ++e) {
+                                        const int ph = pos_hi[nt][e];
+                                        if (t <= ph && (W <= 0 || t > ph - W || t < a.num_sinks))
+                                            o[mt][nt][2 * hf + e] += v;
+                                    }
+                            }
+                    }
+                }
+            }
             float inv[kNR][2];
 #pragma unroll
             for (int nt = 0; nt < kNR; ++nt) {
@@ -899,10 +1008,12 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                     l += __shfl_xor_sync(0xffffffffu, l, 4);
                     l += __shfl_xor_sync(0xffffffffu, l, 8);
                     l += __shfl_xor_sync(0xffffffffu, l, 16);
-                    inv[nt][e] = l > 0.f ? a.v_scale / l : 0.f;
+                    const bool some = kSinks ? l != 0.f : l > 0.f;  // kSinks: NaN stays NaN
+                    inv[nt][e] = some ? a.v_scale / l : 0.f;
                     const int r = rt * RN + nt * 8 + 2 * c4 + e;
                     if (l4 == 0 && r < R) {
-                        const float lse = l > 0.f ? (m_run[nt][e] + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        const float m = kSinks ? m_run[nt][e] - kWeightShift<MT> : m_run[nt][e];
+                        const float lse = some ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
                         if (whole) {
                             if (a.lse_out) a.lse_out[tr.row(r)] = lse;
                         } else {
@@ -953,7 +1064,7 @@ struct TileMerge {
     static constexpr int kRuns = D / 16 / kMW;
 };
 
-template <typename QT, bool kFp8, int D, int RN>
+template <typename QT, bool kFp8, int D, int RN, bool kNan>
 __global__ void __launch_bounds__(128) tile_merge_kernel(const __grid_constant__ KernelParams kp, int num_ctas) {
     constexpr int kNR = RN / 8, kMW = TileMerge<QT, kFp8, D, RN>::kMW, kRuns = TileMerge<QT, kFp8, D, RN>::kRuns;
     constexpr int kMT = D / 16, kG = RN == 8 ? 8 : 4;  // pieces a group
@@ -1040,24 +1151,29 @@ __global__ void __launch_bounds__(128) tile_merge_kernel(const __grid_constant__
 #pragma unroll
                 for (int nt = 0; nt < kNR; ++nt) {
                     float w0 = wl[u][nt][0], w1 = wl[u][nt][1];
-                    w0 = (w0 != -INFINITY && mx[nt][0] != -INFINITY) ? expf(w0 - mx[nt][0]) : 0.f;
-                    w1 = (w1 != -INFINITY && mx[nt][1] != -INFINITY) ? expf(w1 - mx[nt][1]) : 0.f;
+                    if constexpr (kNan) {  // (a maximum of -inf: every piece so far without keys, or NaN)
+                        w0 = w0 != -INFINITY ? expf(w0 - (mx[nt][0] == -INFINITY ? 0.f : mx[nt][0])) : 0.f;
+                        w1 = w1 != -INFINITY ? expf(w1 - (mx[nt][1] == -INFINITY ? 0.f : mx[nt][1])) : 0.f;
+                    } else {
+                        w0 = (w0 != -INFINITY && mx[nt][0] != -INFINITY) ? expf(w0 - mx[nt][0]) : 0.f;
+                        w1 = (w1 != -INFINITY && mx[nt][1] != -INFINITY) ? expf(w1 - mx[nt][1]) : 0.f;
+                    }
                     wsum[nt][0] += w0;
                     wsum[nt][1] += w1;
                     // pieces of weight 0 (empty rows) may hold anything: selected away, never multiplied
 #pragma unroll
                     for (int m = 0; m < kMW; ++m) {
-                        acc[m][nt][0] += w0 > 0.f ? w0 * v[u][nt][m].x : 0.f;
-                        acc[m][nt][1] += w1 > 0.f ? w1 * v[u][nt][m].y : 0.f;
-                        acc[m][nt][2] += w0 > 0.f ? w0 * v[u][nt][m].z : 0.f;
-                        acc[m][nt][3] += w1 > 0.f ? w1 * v[u][nt][m].w : 0.f;
+                        acc[m][nt][0] += counts<kNan>(w0) ? w0 * v[u][nt][m].x : 0.f;
+                        acc[m][nt][1] += counts<kNan>(w1) ? w1 * v[u][nt][m].y : 0.f;
+                        acc[m][nt][2] += counts<kNan>(w0) ? w0 * v[u][nt][m].z : 0.f;
+                        acc[m][nt][3] += counts<kNan>(w1) ? w1 * v[u][nt][m].w : 0.f;
                     }
                 }
         }
 #pragma unroll
         for (int nt = 0; nt < kNR; ++nt)
 #pragma unroll
-            for (int e = 0; e < 2; ++e) inv[nt][e] = wsum[nt][e] > 0.f ? 1.f / wsum[nt][e] : 0.f;
+            for (int e = 0; e < 2; ++e) inv[nt][e] = counts<kNan>(wsum[nt][e]) ? 1.f / wsum[nt][e] : 0.f;
     }
     store_out_tile<QT, kFp8, D, RN, kMW>(acc, inv, rt * RN, tr, static_cast<QT *>(a.out), lane, run * kMW);
     if (run == 0 && a.lse_out && (lane >> 2) == 0) {
@@ -1066,25 +1182,26 @@ __global__ void __launch_bounds__(128) tile_merge_kernel(const __grid_constant__
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int r = rt * RN + nt * 8 + 2 * c4 + e;
-                if (r < R) a.lse_out[tr.row(r)] = wsum[nt][e] > 0.f ? mx[nt][e] + logf(wsum[nt][e]) : -INFINITY;
+                if (r < R)
+                    a.lse_out[tr.row(r)] = counts<kNan>(wsum[nt][e]) ? mx[nt][e] + logf(wsum[nt][e]) : -INFINITY;
             }
     }
 }
 
-template <typename QT, bool kFp8, int D, int RN>
+template <typename QT, bool kFp8, int D, int RN, bool kNan>
 static cudaError_t tile_merge(const KernelParams &kp, int num_workers, cudaStream_t stream) {
     const int64_t warps = static_cast<int64_t>(kp.num_items) * kp.heads_per_cta * kp.warps_per_head *
                           TileMerge<QT, kFp8, D, RN>::kRuns;
     const int threads = 128;
     const int64_t blocks = (warps * 32 + threads - 1) / threads;
-    tile_merge_kernel<QT, kFp8, D, RN><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
+    tile_merge_kernel<QT, kFp8, D, RN, kNan><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
     return cudaGetLastError();
 }
 
-template <typename QT, typename CT, int D, int RN, bool kFused, int kBS, bool kLens>
+template <typename QT, typename CT, int D, int RN, bool kFused, int kBS, bool kLens, bool kSinks>
 static cudaError_t launch_typed(const CUtensorMap &tk, const CUtensorMap &tv, const KernelParams &kp,
                                 const DecodePlan &plan, cudaStream_t stream) {
-    auto kern = paged_decode_kernel<QT, CT, D, RN, kFused, kBS, kLens>;
+    auto kern = paged_decode_kernel<QT, CT, D, RN, kFused, kBS, kLens, kSinks>;
     // raise the kernel's dynamic shared-memory limit to the device maximum once per device
     constexpr int kMaxDevices = 64;
     static std::once_flag once[kMaxDevices];
@@ -1108,26 +1225,47 @@ static cudaError_t launch_typed(const CUtensorMap &tk, const CUtensorMap &tv, co
         kern<<<plan.num_ctas, plan.threads, plan.smem_bytes, stream>>>(tk, tv, kp);
         e = cudaGetLastError();
         if (e != cudaSuccess) return e;
-        return kp.tile_ws ? tile_merge<QT, CacheTraits<CT>::kFp8, D, RN>(kp, plan.num_ctas, stream)
-                          : row_merge<QT, D>(kp, plan.num_ctas, stream);
+        return kp.tile_ws ? tile_merge<QT, CacheTraits<CT>::kFp8, D, RN, kSinks>(kp, plan.num_ctas, stream)
+                          : row_merge<QT, D, kSinks>(kp, plan.num_ctas, stream);
     }
 }
 
-template <typename QT, typename CT, int D, bool kFused>
+template <typename QT, typename CT, int D, bool kFused, bool kSinks = false>
 static cudaError_t launch_rows(const CUtensorMap &tk, const CUtensorMap &tv, const KernelParams &kp,
                                const DecodePlan &plan, cudaStream_t stream) {
     // the FP8 cache with 16-token blocks (one block per stage) runs a kernel with that block size
     // built in; measured 6% faster on a 32-sequence Llama-70B-shaped batch (16-bit caches gain ~1%)
     if (!plan.lens_smem)  // a batch whose length table would cost the ring a stage
-        return plan.rows_per_warp == 8 ? launch_typed<QT, CT, D, 8, kFused, 0, false>(tk, tv, kp, plan, stream)
-                                       : launch_typed<QT, CT, D, 16, kFused, 0, false>(tk, tv, kp, plan, stream);
+        return plan.rows_per_warp == 8 ? launch_typed<QT, CT, D, 8, kFused, 0, false, kSinks>(tk, tv, kp, plan, stream)
+                                       : launch_typed<QT, CT, D, 16, kFused, 0, false, kSinks>(tk, tv, kp, plan, stream);
     if constexpr (CacheTraits<CT>::kFp8) {
         if (kp.a.block_size == 16 && kp.blocks_per_stage == 1)
-            return plan.rows_per_warp == 8 ? launch_typed<QT, CT, D, 8, kFused, 16, true>(tk, tv, kp, plan, stream)
-                                           : launch_typed<QT, CT, D, 16, kFused, 16, true>(tk, tv, kp, plan, stream);
+            return plan.rows_per_warp == 8 ? launch_typed<QT, CT, D, 8, kFused, 16, true, kSinks>(tk, tv, kp, plan, stream)
+                                           : launch_typed<QT, CT, D, 16, kFused, 16, true, kSinks>(tk, tv, kp, plan, stream);
     }
-    return plan.rows_per_warp == 8 ? launch_typed<QT, CT, D, 8, kFused, 0, true>(tk, tv, kp, plan, stream)
-                                   : launch_typed<QT, CT, D, 16, kFused, 0, true>(tk, tv, kp, plan, stream);
+    return plan.rows_per_warp == 8 ? launch_typed<QT, CT, D, 8, kFused, 0, true, kSinks>(tk, tv, kp, plan, stream)
+                                   : launch_typed<QT, CT, D, 16, kFused, 0, true, kSinks>(tk, tv, kp, plan, stream);
+}
+
+// The launch parameters of a plan, without the fused step's.
+inline KernelParams make_params(const DecodeArgs &a, const DecodePlan &plan) {
+    KernelParams kp;
+    kp.a = a;
+    kp.f = StepArgs{};
+    kp.heads_per_cta = plan.heads_per_cta;
+    kp.warps_per_head = plan.warps_per_head;
+    kp.blocks_per_stage = plan.blocks_per_stage;
+    kp.num_stages = plan.num_stages;
+    kp.box_bytes = plan.box_bytes;
+    kp.box_stride = plan.box_stride;
+    kp.num_items = plan.num_items;
+    kp.rows_per_item = plan.rows_per_item;
+    kp.sets_per_cta = 1;
+    kp.num_workers = plan.num_ctas;
+    kp.tile_ws = plan.tile_ws;
+    kp.item_cost = plan.item_cost;
+    kp.lens_smem = plan.lens_smem;
+    return kp;
 }
 
 // E4M3 caches (paged_attention_fp8.cu): launch_rows over (f16 or bf16 queries, head dim 128)

@@ -22,6 +22,8 @@ Same names as the C ABI:
     qk_norm_rope(...)                kv_qk_norm_rope
     qk_norm_rope_and_cache(...)      kv_qk_norm_rope, with the write of K and V into the cache
     paged_attention_tree(...)        kv_paged_attention_tree
+    paged_attention_decode_sinks(...)       kv_paged_attention_decode_sinks       (include/pagedkv_sinks.h)
+    paged_attention_decode_sinks_int4(...)  kv_paged_attention_decode_sinks_int4
 """
 from __future__ import annotations
 
@@ -84,6 +86,8 @@ def _load() -> ctypes.CDLL:
     pi32 = ctypes.POINTER(i32)
     lib.kv_bm_create.argtypes = [i32, i32, i32, i32, i32, i32, ctypes.POINTER(P)]
     lib.kv_bm_create.restype = i32
+    lib.kv_bm_create_sinks.argtypes = [i32, i32, i32, i32, i32, i32, i32, ctypes.POINTER(P)]
+    lib.kv_bm_create_sinks.restype = i32
     lib.kv_bm_destroy.argtypes = [P]
     lib.kv_bm_destroy.restype = None
     lib.kv_bm_allocate.argtypes = [P, i32, i32]
@@ -132,6 +136,12 @@ def _load() -> ctypes.CDLL:
     lib.kv_paged_attention_tree.restype = i32
     lib.kv_paged_attention_tree_workspace_size.argtypes = [i32, i32, i32, i32, i32, i32]
     lib.kv_paged_attention_tree_workspace_size.restype = sz
+    lib.kv_paged_attention_decode_sinks.argtypes = [P, i32, i32, i32, i32, P, P, i32, i32, i32, i32, i32, P, i64, i32,
+                                                    P, i32, f32, i32, i32, f32, f32, i32, P, sz, P, P, P, P]
+    lib.kv_paged_attention_decode_sinks.restype = i32
+    lib.kv_paged_attention_decode_sinks_int4.argtypes = [P, i32, i32, i32, i32, P, P, i32, i32, i32, i32, P, i64, i32,
+                                                         P, i32, f32, i32, i32, P, P, i32, i32, P, sz, P, P, P, P]
+    lib.kv_paged_attention_decode_sinks_int4.restype = i32
     lib.kv_status_string.argtypes = [i32]
     lib.kv_status_string.restype = ctypes.c_char_p
     lib.kv_last_error.argtypes = []
@@ -431,13 +441,14 @@ class BlockManager:
     outcome (kv_last_error() says why); the constructor, row and flush raise KVError."""
 
     def __init__(self, num_blocks: int, block_size: int, num_rows: int, max_blocks_per_row: int,
-                 window: int = 0, zero_fill: bool = True):
+                 window: int = 0, zero_fill: bool = True, num_sinks: int = 0):
         h = ctypes.c_void_p()
-        _check(lib.kv_bm_create(num_blocks, block_size, num_rows, max_blocks_per_row, window,
-                                int(bool(zero_fill)), ctypes.byref(h)))
+        _check(lib.kv_bm_create_sinks(num_blocks, block_size, num_rows, max_blocks_per_row, window, num_sinks,
+                                      int(bool(zero_fill)), ctypes.byref(h)))
         self._h = h
         self.num_blocks, self.block_size = num_blocks, block_size
         self.num_rows, self.max_blocks_per_row, self.window = num_rows, max_blocks_per_row, window
+        self.num_sinks = num_sinks
 
     def __del__(self):
         h = getattr(self, "_h", None)
@@ -905,3 +916,120 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     if status:
         _check(status)
     return out
+
+
+
+# ---------------------------------------------------------------- windows with sinks (pagedkv_sinks.h)
+
+def _cache_code(k_cache, v_cache, D, dev, k_scales, v_scales):
+    """The type code of two caches and the group size of INT4 ones: uint8 [NB, bs, Hkv, D / 2] with float32
+    scales [Hkv, D / group_size] (scales given), else [NB, bs, Hkv, D]."""
+    cshape, cdt = k_cache.shape, k_cache.dtype
+    int4 = k_scales is not None
+    if len(cshape) != 4 or cshape[3] * (2 if int4 else 1) != D or v_cache.shape != cshape or v_cache.dtype is not cdt or \
+            not k_cache.is_contiguous() or not v_cache.is_contiguous() or k_cache.get_device() != dev or \
+            v_cache.get_device() != dev:
+        _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type (INT4: D / 2 bytes), D that of q, on "
+                "the same device")
+    if not int4:
+        return _code_of.get(cdt, -1), 0
+    if cdt is not torch.uint8:
+        _refuse("INT4 caches: uint8")
+    for t in (k_scales, v_scales):
+        if t.dtype is not _f32 or t.dim() != 2 or t.shape[0] != cshape[2] or t.shape[1] < 1 or D % t.shape[1] or \
+                not t.is_contiguous() or t.get_device() != dev or t.shape != k_scales.shape:
+            _refuse("k_scales and v_scales: contiguous float32 [heads, D / group_size] on the same device")
+    return KV_INT4, D // k_scales.shape[1]
+
+
+def _outputs(q, out, lse_out, d_err, dev):
+    """out (made when it is None), and the addresses of lse_out and d_err."""
+    if out is None:
+        out = torch.empty_like(q)
+    elif out.shape != q.shape or out.dtype is not q.dtype or not out.is_contiguous() or out.get_device() != dev:
+        _refuse("out: like q")
+    lse = err = None
+    if lse_out is not None:
+        if lse_out.dtype is not _f32 or lse_out.shape != q.shape[:2] or not lse_out.is_contiguous() or \
+                lse_out.get_device() != dev:
+            _refuse("lse_out: contiguous float32 [T, heads] on the same device")
+        lse = lse_out.data_ptr()
+    if d_err is not None:
+        err = _error_word(d_err, dev)
+    return out, lse, err
+
+
+def _scratch(workspace, size, dev, like):
+    """The workspace of size() bytes: the given one, or a new one."""
+    if workspace is None:
+        return torch.empty(size(), dtype=torch.uint8, device=like.device)
+    if not workspace.is_contiguous() or workspace.get_device() != dev:
+        _refuse("workspace: contiguous, on the same device")
+    return workspace
+
+
+def _decode_sinks(q, k_cache, v_cache, block_table, seq_lens, max_seq_len, q_len, scale, window, num_sinks, k_scale,
+                  v_scale, k_scales, v_scales, num_workers, workspace, out, lse_out, d_err, max_blocks_per_seq, stream):
+    dev, dt = q.get_device(), q.dtype
+    if dev < 0 or q.dim() != 3 or not q.is_contiguous():
+        _refuse("q: contiguous [B * q_len, heads, D]; " + _DEVICES)
+    if stream is not None or dev != _current_device():
+        with torch.cuda.device(dev) if stream is None else _on(stream, dev):
+            return _decode_sinks(q, k_cache, v_cache, block_table, seq_lens, max_seq_len, q_len, scale, window, num_sinks,
+                                 k_scale, v_scale, k_scales, v_scales, num_workers, workspace, out, lse_out, d_err,
+                                 max_blocks_per_seq, None)
+    TQ, Hq, D = q.shape
+    B = seq_lens.numel()
+    code, group = _cache_code(k_cache, v_cache, D, dev, k_scales, v_scales)
+    NB, bs, Hkv = k_cache.shape[:3]
+    if seq_lens.dtype is not _i32 or not seq_lens.is_contiguous() or seq_lens.get_device() != dev or TQ != B * q_len:
+        _refuse("seq_lens: contiguous int32 [B] on the same device, with B * q_len rows of q")
+    if block_table.get_device() != dev:
+        _refuse(_DEVICES)
+    bt_stride, width = _table(block_table, B, max_blocks_per_seq)
+    out, lse, err = _outputs(q, out, lse_out, d_err, dev)
+    workspace = _scratch(workspace, lambda: paged_attention_workspace_size(
+        B, q_len, Hq, Hkv, D, bs, code, max_seq_len, window, num_workers), dev, q)
+    head = (q.data_ptr(), _code_of.get(dt, -1), B, q_len, Hq, k_cache.data_ptr(), v_cache.data_ptr())
+    tail = (num_workers, workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(), lse, err,
+            _raw_stream(dev))
+    if k_scales is not None:
+        status = lib.kv_paged_attention_decode_sinks_int4(
+            *head, Hkv, D, bs, NB, block_table.data_ptr(), bt_stride, width, seq_lens.data_ptr(), max_seq_len, scale, window,
+            num_sinks, k_scales.data_ptr(), v_scales.data_ptr(), group, *tail)
+    else:
+        status = lib.kv_paged_attention_decode_sinks(
+            *head, code, Hkv, D, bs, NB, block_table.data_ptr(), bt_stride, width, seq_lens.data_ptr(), max_seq_len, scale,
+            window, num_sinks, k_scale, v_scale, *tail)
+    if status:
+        _check(status)
+    return out
+
+
+def paged_attention_decode_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor, block_table: torch.Tensor,
+                                 seq_lens: torch.Tensor, max_seq_len: int, q_len: int, scale: float, window: int,
+                                 num_sinks: int, k_scale: float = 1.0, v_scale: float = 1.0, num_workers: int = 0,
+                                 workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                 lse_out: Optional[torch.Tensor] = None, d_err: Optional[torch.Tensor] = None,
+                                 max_blocks_per_seq: Optional[int] = None, stream=None) -> torch.Tensor:
+    """kv_paged_attention_decode_sinks: paged_attention_decode where a windowed row also sees the first
+    num_sinks keys.  q [B * q_len, Hq, D]; caches [NB, bs, Hkv, D] (of q's type, or E4M3 with k_scale and
+    v_scale); block_table int32 [B, W]; seq_lens int32 [B].  A workspace that is given must hold
+    paged_attention_workspace_size(...) bytes."""
+    return _decode_sinks(q, k_cache, v_cache, block_table, seq_lens, max_seq_len, q_len, scale, window, num_sinks, k_scale,
+                         v_scale, None, None, num_workers, workspace, out, lse_out, d_err, max_blocks_per_seq, stream)
+
+
+def paged_attention_decode_sinks_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                      block_table: torch.Tensor, seq_lens: torch.Tensor, max_seq_len: int, q_len: int,
+                                      scale: float, k_scales: torch.Tensor, v_scales: torch.Tensor, window: int,
+                                      num_sinks: int, num_workers: int = 0, workspace: Optional[torch.Tensor] = None,
+                                      out: Optional[torch.Tensor] = None, lse_out: Optional[torch.Tensor] = None,
+                                      d_err: Optional[torch.Tensor] = None, max_blocks_per_seq: Optional[int] = None,
+                                      stream=None) -> torch.Tensor:
+    """kv_paged_attention_decode_sinks_int4: the same over INT4 caches, uint8 [NB, bs, Hkv, D / 2], with
+    float32 scales [Hkv, D / group_size]."""
+    if k_scales is None or v_scales is None:
+        _refuse("k_scales and v_scales are needed")
+    return _decode_sinks(q, k_cache, v_cache, block_table, seq_lens, max_seq_len, q_len, scale, window, num_sinks, 1.0, 1.0,
+                         k_scales, v_scales, num_workers, workspace, out, lse_out, d_err, max_blocks_per_seq, stream)
