@@ -5,6 +5,7 @@
  *   kv_build_batch             request lengths -> block tables, slots, positions, tree masks
  *   kv_qk_norm_rope            RMS norm of each query and key head, rotary embedding, and the
  *                              write of K and V into the paged cache, in one pass
+ *   kv_qk_norm_rope_int4       the same into an INT4 cache
  *   kv_paged_attention_tree    attention of a tree of drafted tokens over the paged cache
  *
  * One speculative step of one layer calls them in this order; kv_build_batch runs once a step and
@@ -129,6 +130,27 @@ KV_API kv_status kv_qk_norm_rope(const void *q, const void *key, const void *val
                                  void *v_cache, kv_dtype cache_dtype, int32_t num_blocks,
                                  int32_t block_size, float k_scale, float v_scale, int32_t *d_err,
                                  void *stream);
+
+/*
+ * kv_qk_norm_rope_int4 - kv_qk_norm_rope into the INT4 caches of pagedkv_int4.h: norm, rotation, and the
+ * write of K and V as INT4 codes.  The code of a key is its float32 value (not the 16-bit rounding that
+ * k_out, which may be NULL, gets) divided by the scale of its (head, dim group), rounded and clamped as
+ * kv_reshape_and_cache_int4 does; values take exactly the codes of that call.
+ *   slot_mapping, value and both caches are needed (num_tokens > 0); caches as for that call
+ *   k_scales, v_scales  float32 [num_kv_heads, head_dim / group_size]
+ * Supported: head_dim 128 and the group sizes of pagedkv_int4.h; the rest as above.  One launch.
+ */
+KV_API kv_status kv_qk_norm_rope_int4(const void *q, const void *key, const void *value, kv_dtype dtype,
+                                      int64_t q_stride, int64_t key_stride, int64_t value_stride,
+                                      int32_t num_tokens, int32_t num_q_heads, int32_t num_kv_heads,
+                                      int32_t head_dim, const void *q_weight, const void *k_weight,
+                                      float eps, const int32_t *positions, const float *cos_sin,
+                                      int32_t max_position, int32_t rotary_dim, int32_t interleaved,
+                                      void *q_out, int64_t q_out_stride, void *k_out,
+                                      int64_t k_out_stride, const int64_t *slot_mapping, void *k_cache,
+                                      void *v_cache, int32_t num_blocks, int32_t block_size,
+                                      const float *k_scales, const float *v_scales, int32_t group_size,
+                                      int32_t *d_err, void *stream);
 
 /*
  * kv_paged_attention_tree - attention of drafted trees over the paged cache (speculative decoding:

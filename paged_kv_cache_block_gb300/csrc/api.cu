@@ -562,6 +562,12 @@ kv_status kv_selftest_bounded_wait(int32_t limit_us, int32_t *d_err, int32_t *d_
 
 // ---------------------------------------------------------------- INT4 caches (pagedkv_int4.h)
 
+static int log2_of(int32_t power_of_two) {
+    int shift = 0;
+    while ((1 << shift) < power_of_two) ++shift;
+    return shift;
+}
+
 static kv_status check_int4_layout(int32_t head_dim, int32_t group_size, const float *k_scales,
                                    const float *v_scales) {
     if (head_dim != 128) return fail(KV_ERR_UNSUPPORTED, "INT4 caches need head_dim 128");
@@ -1095,14 +1101,20 @@ kv_status kv_build_batch(const int32_t *context_lens, const int32_t *new_lens, c
     return ok();
 }
 
-kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_dtype dtype, int64_t q_stride,
-                          int64_t key_stride, int64_t value_stride, int32_t num_tokens, int32_t num_q_heads,
-                          int32_t num_kv_heads, int32_t head_dim, const void *q_weight, const void *k_weight,
-                          float eps, const int32_t *positions, const float *cos_sin, int32_t max_position,
-                          int32_t rotary_dim, int32_t interleaved, void *q_out, int64_t q_out_stride, void *k_out,
-                          int64_t k_out_stride, const int64_t *slot_mapping, void *k_cache, void *v_cache,
-                          kv_dtype cache_dtype, int32_t num_blocks, int32_t block_size, float k_scale,
-                          float v_scale, int32_t *d_err, void *stream) {
+// The group scales of an INT4 cache (given exactly for such a cache).
+struct GroupScales {
+    const float *k, *v;
+    int32_t group_size;
+};
+
+static kv_status qk_norm_rope(const void *q, const void *key, const void *value, kv_dtype dtype, int64_t q_stride,
+                              int64_t key_stride, int64_t value_stride, int32_t num_tokens, int32_t num_q_heads,
+                              int32_t num_kv_heads, int32_t head_dim, const void *q_weight, const void *k_weight,
+                              float eps, const int32_t *positions, const float *cos_sin, int32_t max_position,
+                              int32_t rotary_dim, int32_t interleaved, void *q_out, int64_t q_out_stride, void *k_out,
+                              int64_t k_out_stride, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                              kv_dtype cache_dtype, int32_t num_blocks, int32_t block_size, float k_scale,
+                              float v_scale, const GroupScales *int4, int32_t *d_err, void *stream) {
     if (num_tokens < 0 || num_q_heads < 1 || num_kv_heads < 1 || head_dim < 8 || rotary_dim < 0 || max_position < 0)
         return fail(KV_ERR_INVALID_ARG, "invalid size argument");
     if (dtype != KV_F16 && dtype != KV_BF16) return fail(KV_ERR_UNSUPPORTED, "q, key and value must be fp16 or bf16");
@@ -1116,7 +1128,11 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
     if (write ? (!value || !k_cache || !v_cache) && num_tokens > 0 : (k_cache || v_cache))
         return fail(KV_ERR_INVALID_ARG, "value, slot_mapping and both caches are given together or not at all");
     if (write && (num_blocks < 0 || block_size < 1)) return fail(KV_ERR_INVALID_ARG, "invalid cache size");
-    if (write && cache_dtype != dtype && cache_dtype != KV_FP8_E4M3)
+    if (int4) {
+        const kv_status st = check_int4_layout(head_dim, int4->group_size, int4->k, int4->v);
+        if (st != KV_OK) return st;
+    }
+    if (write && !int4 && cache_dtype != dtype && cache_dtype != KV_FP8_E4M3)
         return fail(KV_ERR_UNSUPPORTED, "cache dtype must equal the source dtype or be E4M3");
     if (write && cache_dtype == KV_FP8_E4M3 &&
         !(k_scale > 0.f && v_scale > 0.f && std::isfinite(k_scale) && std::isfinite(v_scale)))
@@ -1137,14 +1153,16 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
         !aligned(d_err, 4))
         return fail(KV_ERR_INVALID_ARG, "q, key, value, outputs, weights, cos_sin and caches must be 16-byte aligned");
     // a token's heads are read and written by different warps: an output may only be its own input
-    const int64_t T = num_tokens, cache_bytes = write ? static_cast<int64_t>(num_blocks) * block_size * krow *
-                                                            (cache_dtype == KV_FP8_E4M3 ? 1 : 2) : 0;
+    const int64_t T = num_tokens, elements = write ? static_cast<int64_t>(num_blocks) * block_size * krow : 0;
+    const int64_t cache_bytes = int4 ? elements / 2 : elements * (cache_dtype == KV_FP8_E4M3 ? 1 : 2);
+    const int64_t scale_bytes = int4 ? 4ll * num_kv_heads * (head_dim / int4->group_size) : 0;
     const RowSet in_rows[] = {{q, 2 * q_stride, 2 * qrow, T}, {key, 2 * key_stride, 2 * krow, T},
                               {write ? value : nullptr, 2 * value_stride, 2 * krow, T}};
     const RowSet out_rows[] = {{q_out, 2 * q_out_stride, 2 * qrow, T}, {k_out, 2 * k_out_stride, 2 * krow, T}};
     const ByteRange in_ranges[] = {{q_weight, 2 * head_dim}, {k_weight, 2 * head_dim}, {positions, 4 * T},
                                    {rotary_dim ? cos_sin : nullptr, 4ll * max_position * rotary_dim},
-                                   {slot_mapping, 8 * T}};
+                                   {slot_mapping, 8 * T}, {int4 ? int4->k : nullptr, scale_bytes},
+                                   {int4 ? int4->v : nullptr, scale_bytes}};
     const ByteRange caches[] = {{k_cache, cache_bytes}, {v_cache, cache_bytes}};
     bool clash = rows_overlap(out_rows[0], out_rows[1]) || overlap(caches[0], caches[1]);
     for (int o = 0; o < 2; ++o) {
@@ -1187,7 +1205,11 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
     a.slot_mapping = slot_mapping;
     a.k_cache = k_cache;
     a.v_cache = v_cache;
-    a.cache_fp8 = write && cache_dtype == KV_FP8_E4M3;
+    a.cache_fp8 = write && !int4 && cache_dtype == KV_FP8_E4M3;
+    a.cache_int4 = int4 != nullptr;
+    a.k_gscales = int4 ? int4->k : nullptr;
+    a.v_gscales = int4 ? int4->v : nullptr;
+    a.group_shift = int4 ? log2_of(int4->group_size) : 0;
     a.total_slots = write ? static_cast<int64_t>(num_blocks) * block_size : 0;
     a.k_scale = k_scale;
     a.v_scale = v_scale;
@@ -1196,6 +1218,36 @@ kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_
     e = pkv::launch_qk_norm_rope(a, dtype, info.sm_count, s);
     if (e != cudaSuccess) return cuda_fail(e, "norm and rotation launch");
     return ok();
+}
+
+kv_status kv_qk_norm_rope(const void *q, const void *key, const void *value, kv_dtype dtype, int64_t q_stride,
+                          int64_t key_stride, int64_t value_stride, int32_t num_tokens, int32_t num_q_heads,
+                          int32_t num_kv_heads, int32_t head_dim, const void *q_weight, const void *k_weight,
+                          float eps, const int32_t *positions, const float *cos_sin, int32_t max_position,
+                          int32_t rotary_dim, int32_t interleaved, void *q_out, int64_t q_out_stride, void *k_out,
+                          int64_t k_out_stride, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                          kv_dtype cache_dtype, int32_t num_blocks, int32_t block_size, float k_scale,
+                          float v_scale, int32_t *d_err, void *stream) {
+    return qk_norm_rope(q, key, value, dtype, q_stride, key_stride, value_stride, num_tokens, num_q_heads, num_kv_heads,
+                        head_dim, q_weight, k_weight, eps, positions, cos_sin, max_position, rotary_dim, interleaved, q_out,
+                        q_out_stride, k_out, k_out_stride, slot_mapping, k_cache, v_cache, cache_dtype, num_blocks,
+                        block_size, k_scale, v_scale, nullptr, d_err, stream);
+}
+
+kv_status kv_qk_norm_rope_int4(const void *q, const void *key, const void *value, kv_dtype dtype, int64_t q_stride,
+                               int64_t key_stride, int64_t value_stride, int32_t num_tokens, int32_t num_q_heads,
+                               int32_t num_kv_heads, int32_t head_dim, const void *q_weight, const void *k_weight,
+                               float eps, const int32_t *positions, const float *cos_sin, int32_t max_position,
+                               int32_t rotary_dim, int32_t interleaved, void *q_out, int64_t q_out_stride, void *k_out,
+                               int64_t k_out_stride, const int64_t *slot_mapping, void *k_cache, void *v_cache,
+                               int32_t num_blocks, int32_t block_size, const float *k_scales, const float *v_scales,
+                               int32_t group_size, int32_t *d_err, void *stream) {
+    if (num_tokens > 0 && !slot_mapping) return fail(KV_ERR_INVALID_ARG, "null slot_mapping");
+    const GroupScales scales{k_scales, v_scales, group_size};
+    return qk_norm_rope(q, key, value, dtype, q_stride, key_stride, value_stride, num_tokens, num_q_heads, num_kv_heads,
+                        head_dim, q_weight, k_weight, eps, positions, cos_sin, max_position, rotary_dim, interleaved, q_out,
+                        q_out_stride, k_out, k_out_stride, slot_mapping, k_cache, v_cache, KV_INT4, num_blocks, block_size,
+                        1.f, 1.f, &scales, d_err, stream);
 }
 
 // Sizes that kv_paged_attention_tree and its workspace query check alike.
@@ -1325,12 +1377,6 @@ kv_status kv_paged_attention_tree(const void *q, kv_dtype q_dtype, const int32_t
 }
 
 // ---------------------------------------------------------------- windows with sinks (pagedkv_sinks.h)
-
-static int log2_of(int32_t power_of_two) {
-    int shift = 0;
-    while ((1 << shift) < power_of_two) ++shift;
-    return shift;
-}
 
 // A paged cache of any type, as the calls with sinks take it.
 struct SinkCache {

@@ -203,9 +203,11 @@ struct RopeArgs {
     int64_t q_out_stride, k_out_stride;
     const int64_t *slot_mapping;
     void *k_cache, *v_cache;
-    int32_t cache_fp8;
+    int32_t cache_fp8, cache_int4;
     int64_t total_slots;
     float k_scale, v_scale;
+    const float *k_gscales, *v_gscales;  // INT4 caches: [num_kv_heads, head_dim >> group_shift]
+    int32_t group_shift;
     // set by the launch: heads of a token that one warp takes; warps a token for q, and for key (and value)
     int32_t heads_a_warp, q_parts, kv_parts;
     int32_t *d_err;

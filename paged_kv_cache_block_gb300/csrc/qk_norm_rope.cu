@@ -12,6 +12,9 @@
 //   u = r (p wp cos - q wq sin),  v = r (q wq cos + p wp sin),  r = 1 / sqrt(mean + eps)
 // in packed pairs of floats.
 //
+// INT4 caches (kInt4) take a key's four codes of a piece, its float32 values divided by the scale of
+// their group, as 16 bits; a piece never crosses a group, whose size is at least 8.
+//
 // About 2 bytes move per element each way: the bound is HBM, once the instructions per element are
 // few (packed arithmetic, pointers advanced by a constant).  A warp takes several heads, loaded four
 // at a time before the first is used, once there are tokens enough to fill the GPU; fewer heads a
@@ -63,6 +66,12 @@ __device__ __forceinline__ uint32_t quantise4(const float2 (&x)[2], float scale)
     return lo | (hi << 16);
 }
 
+// Four float32 values -> four INT4 codes (the rounding of kv_reshape_and_cache_int4).
+__device__ __forceinline__ uint16_t quantise4_int4(const float2 (&x)[2], float scale) {
+    return static_cast<uint16_t>(int4_code(x[0].x, scale) | (int4_code(x[0].y, scale) << 4) |
+                                 (int4_code(x[1].x, scale) << 8) | (int4_code(x[1].y, scale) << 12));
+}
+
 __device__ __forceinline__ uint2 ld_piece(const void *p) {
     uint2 v;
     asm volatile("ld.global.L1::no_allocate.v2.b32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p) : "memory");
@@ -73,7 +82,7 @@ __device__ __forceinline__ uint2 ld_piece(const void *p) {
 // at run time (64 and 128, the sizes the attention calls take, get their addresses as constants).
 // An output may be its input: a piece is read and then written by one lane, and no other lane
 // touches it.
-template <typename T, int LP, bool kAdjacent, int kD>
+template <typename T, int LP, bool kAdjacent, int kD, bool kInt4>
 __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(const RopeArgs a) {
     constexpr int HPW = 32 / LP;
     const int lane = threadIdx.x & 31;
@@ -130,7 +139,23 @@ __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(con
     const int64_t at = (slot * a.num_kv_heads + mine) * D;  // in the caches, once slot >= 0
     if (kind == 2) {
         if (slot < 0) return;
-        if (a.cache_fp8) {
+        if constexpr (kInt4) {
+            uint8_t *dst = static_cast<uint8_t *>(a.v_cache) + (at >> 1);
+            const float *sc = a.v_gscales + static_cast<int64_t>(mine) * (D >> a.group_shift);
+            const int s0 = d0 >> a.group_shift, s1 = d1 >> a.group_shift, next = step >> a.group_shift;
+            for (int i0 = 0; i0 < rounds; i0 += kBatch) {
+                if (i0) load(i0);
+#pragma unroll
+                for (int i = 0; i < kBatch; ++i) {
+                    if (i0 + i >= n) continue;
+                    const Eight x = widen<T>(raw[i][0], raw[i][1]);
+                    *reinterpret_cast<uint16_t *>(dst + ((i * step + d0) >> 1)) = quantise4_int4(x.p, sc[i * next + s0]);
+                    *reinterpret_cast<uint16_t *>(dst + ((i * step + d1) >> 1)) = quantise4_int4(x.q, sc[i * next + s1]);
+                }
+                dst += kBatch * step / 2;
+                sc += kBatch * next;
+            }
+        } else if (a.cache_fp8) {
             uint8_t *dst = static_cast<uint8_t *>(a.v_cache) + at;
             for (int i0 = 0; i0 < rounds; i0 += kBatch) {
                 if (i0) load(i0);
@@ -194,7 +219,8 @@ __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(con
     if (dst) dst += static_cast<int64_t>(mine) * D;
     const bool to_cache = kind == 1 && slot >= 0;
     const int esize = a.cache_fp8 ? 1 : 2;
-    uint8_t *cdst = to_cache ? static_cast<uint8_t *>(a.k_cache) + at * esize : nullptr;
+    uint8_t *cdst = to_cache ? static_cast<uint8_t *>(a.k_cache) + (kInt4 ? at >> 1 : at * esize) : nullptr;
+    const float *sc = kInt4 ? a.k_gscales + static_cast<int64_t>(mine) * (D >> a.group_shift) : nullptr;
     const float inv_d = 1.f / static_cast<float>(D);
     for (int i0 = 0; i0 < rounds; i0 += kBatch) {
         if (i0) load(i0);
@@ -243,7 +269,11 @@ __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(con
                     *reinterpret_cast<uint2 *>(dst + i * step + d1) = r1;
                 }
                 if (to_cache) {
-                    if (a.cache_fp8) {
+                    if constexpr (kInt4) {
+                        const float c0 = sc[(i * step + d0) >> a.group_shift], c1 = sc[(i * step + d1) >> a.group_shift];
+                        *reinterpret_cast<uint16_t *>(cdst + ((i * step + d0) >> 1)) = quantise4_int4(u, c0);
+                        *reinterpret_cast<uint16_t *>(cdst + ((i * step + d1) >> 1)) = quantise4_int4(v, c1);
+                    } else if (a.cache_fp8) {
                         *reinterpret_cast<uint32_t *>(cdst + i * step + d0) = quantise4(u, a.k_scale);
                         *reinterpret_cast<uint32_t *>(cdst + i * step + d1) = quantise4(v, a.k_scale);
                     } else {
@@ -254,11 +284,15 @@ __global__ void __launch_bounds__(kThreads, kBlocksAnSm) qk_norm_rope_kernel(con
             }
         }
         if (dst) dst += kBatch * step;
-        if (to_cache) cdst += kBatch * step * esize;
+        if constexpr (kInt4) {
+            if (to_cache) cdst += kBatch * step / 2, sc += (kBatch * step) >> a.group_shift;
+        } else {
+            if (to_cache) cdst += kBatch * step * esize;
+        }
     }
 }
 
-template <typename T, int LP, int kD>
+template <typename T, int LP, int kD, bool kInt4 = false>
 cudaError_t launch_lanes(RopeArgs a, int sm_count, cudaStream_t stream) {
     constexpr int HPW = 32 / LP;
     // heads a warp: as many as leave each SM 32 warps (what a lane reads ahead, times 32 warps, covers
@@ -273,12 +307,14 @@ cudaError_t launch_lanes(RopeArgs a, int sm_count, cudaStream_t stream) {
     // a warp a token, the parts of its heads along y (fewer than 65536: n is halved only below 32 warps an
     // SM, and 65535 heads of each kind make at most 6144 parts at first)
     const dim3 grid((static_cast<unsigned>(a.num_tokens) + kThreads / 32 - 1) / (kThreads / 32), all());
-    return launch_dependent(a.interleaved ? qk_norm_rope_kernel<T, LP, true, kD> : qk_norm_rope_kernel<T, LP, false, kD>,
+    return launch_dependent(a.interleaved ? qk_norm_rope_kernel<T, LP, true, kD, kInt4>
+                                          : qk_norm_rope_kernel<T, LP, false, kD, kInt4>,
                             grid, dim3(kThreads), 0, stream, a);
 }
 
 template <typename T> cudaError_t launch_typed(const RopeArgs &a, int sm_count, cudaStream_t stream) {
     const int chunks = a.head_dim / 8;
+    if (a.cache_int4) return launch_lanes<T, 16, 128, true>(a, sm_count, stream);  // (head_dim 128)
     if (a.head_dim == 128) return launch_lanes<T, 16, 128>(a, sm_count, stream);
     if (a.head_dim == 64) return launch_lanes<T, 8, 64>(a, sm_count, stream);
     if (chunks <= 2) return launch_lanes<T, 2, 0>(a, sm_count, stream);

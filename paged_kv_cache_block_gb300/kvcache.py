@@ -21,6 +21,7 @@ Same names as the C ABI:
     build_batch(...)                 kv_build_batch                   (include/pagedkv_step.h)
     qk_norm_rope(...)                kv_qk_norm_rope
     qk_norm_rope_and_cache(...)      kv_qk_norm_rope, with the write of K and V into the cache
+    qk_norm_rope_and_cache_int4(...) kv_qk_norm_rope_int4
     paged_attention_tree(...)        kv_paged_attention_tree
     paged_attention_decode_sinks(...)       kv_paged_attention_decode_sinks       (include/pagedkv_sinks.h)
     paged_attention_decode_sinks_int4(...)  kv_paged_attention_decode_sinks_int4
@@ -131,6 +132,9 @@ def _load() -> ctypes.CDLL:
     lib.kv_qk_norm_rope.argtypes = [P, P, P, i32, i64, i64, i64, i32, i32, i32, i32, P, P, f32, P, P, i32, i32,
                                     i32, P, i64, P, i64, P, P, P, i32, i32, i32, f32, f32, P, P]
     lib.kv_qk_norm_rope.restype = i32
+    lib.kv_qk_norm_rope_int4.argtypes = [P, P, P, i32, i64, i64, i64, i32, i32, i32, i32, P, P, f32, P, P, i32, i32,
+                                         i32, P, i64, P, i64, P, P, P, i32, i32, P, P, i32, P, P]
+    lib.kv_qk_norm_rope_int4.restype = i32
     lib.kv_paged_attention_tree.argtypes = [P, i32, P, i32, i32, i32, i32, P, P, i32, i32, i32, i32, i32, P, i64,
                                             i32, P, i32, f32, i32, P, i32, P, sz, P, P, P, P]
     lib.kv_paged_attention_tree.restype = i32
@@ -703,7 +707,7 @@ def _odd_rows(t: torch.Tensor, what: str) -> None:
 
 
 def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
-               interleaved, k_scale, v_scale, q_out, k_out, d_err):
+               interleaved, k_scale, v_scale, q_out, k_out, d_err, scales=None):
     dev, dt = q.get_device(), q.dtype
     qshape, kshape = q.shape, key.shape
     if dev < 0 or len(qshape) != 3 or len(kshape) != 3:
@@ -711,7 +715,7 @@ def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache
     if dev != _current_device():
         with torch.cuda.device(dev):
             return _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps,
-                              interleaved, k_scale, v_scale, q_out, k_out, d_err)
+                              interleaved, k_scale, v_scale, q_out, k_out, d_err, scales)
     T, Hq, D = qshape
     if kshape[0] != T or kshape[2] != D:
         _refuse("q and key differ in tokens or head size")
@@ -781,7 +785,7 @@ def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache
         if T < 2:
             vs = one_k
         cshape, cdt = k_cache.shape, k_cache.dtype
-        if len(cshape) != 4 or cshape[2] != Hkv or cshape[3] != D or v_cache.shape != cshape or \
+        if len(cshape) != 4 or cshape[2] != Hkv or cshape[3] != (D if scales is None else D // 2) or v_cache.shape != cshape or \
                 v_cache.dtype is not cdt or not k_cache.is_contiguous() or not v_cache.is_contiguous() or \
                 k_cache.get_device() != dev or v_cache.get_device() != dev:
             _refuse("caches: two contiguous [blocks, block_size, heads, D] of one type, heads and D those of key, "
@@ -792,6 +796,15 @@ def _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache
         vp, slots, kc, vc = value.data_ptr(), slot_mapping.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr()
         if not slots:  # no tokens: nothing to write (and no slots to say so)
             vp = kc = vc = None
+    if scales is not None:
+        _, group = _cache_code(k_cache, v_cache, D, dev, *scales)
+        status = lib.kv_qk_norm_rope_int4(
+            q.data_ptr(), key.data_ptr(), vp, code, qs, ks, vs, T, Hq, Hkv, D, wq, wk, eps, pos, cs, max_pos, rot,
+            1 if interleaved else 0, q_out.data_ptr(), qos, kout, kos, slots, kc, vc, NB, bs, scales[0].data_ptr(),
+            scales[1].data_ptr(), group, err, _raw_stream(dev))
+        if status:
+            _check(status)
+        return
     status = lib.kv_qk_norm_rope(
         q.data_ptr(), key.data_ptr(), vp, code, qs, ks, vs, T, Hq, Hkv, D, wq, wk, eps, pos, cs, max_pos, rot,
         1 if interleaved else 0, q_out.data_ptr(), qos, kout, kos, slots, kc, vc, cache_code, NB, bs, k_scale, v_scale,
@@ -840,6 +853,29 @@ def qk_norm_rope_and_cache(q: torch.Tensor, key: torch.Tensor, value: torch.Tens
         q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
     _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps, interleaved,
                k_scale, v_scale, q_out, k_out, d_err)
+    return q_out
+
+
+def qk_norm_rope_and_cache_int4(q: torch.Tensor, key: torch.Tensor, value: torch.Tensor,
+                                positions: Optional[torch.Tensor], cos_sin: Optional[torch.Tensor],
+                                slot_mapping: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                k_scales: torch.Tensor, v_scales: torch.Tensor,
+                                q_weight: Optional[torch.Tensor] = None, k_weight: Optional[torch.Tensor] = None,
+                                eps: float = 1e-6, interleaved: bool = False, q_out: Optional[torch.Tensor] = None,
+                                k_out: Optional[torch.Tensor] = None, d_err: Optional[torch.Tensor] = None,
+                                stream=None) -> torch.Tensor:
+    """kv_qk_norm_rope_int4: qk_norm_rope_and_cache into INT4 caches, uint8 [NB, bs, Hkv, D / 2], with float32
+    scales [Hkv, D / group_size]."""
+    if stream is not None:
+        with _on(stream, q.get_device()):
+            return qk_norm_rope_and_cache_int4(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, k_scales,
+                                               v_scales, q_weight, k_weight, eps, interleaved, q_out, k_out, d_err)
+    if slot_mapping is None or value is None or k_cache is None or v_cache is None or k_scales is None or v_scales is None:
+        _refuse("value, slot_mapping, both caches and their scales are needed")
+    if q_out is None:
+        q_out = torch.empty(q.shape, dtype=q.dtype, device=q.device)
+    _norm_rope(q, key, value, positions, cos_sin, slot_mapping, k_cache, v_cache, q_weight, k_weight, eps, interleaved, 1.0, 1.0,
+               q_out, k_out, d_err, (k_scales, v_scales))
     return q_out
 
 
