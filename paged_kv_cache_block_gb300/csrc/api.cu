@@ -1529,4 +1529,164 @@ kv_status kv_paged_attention_decode_sinks_int4(
                         d_err, stream);
 }
 
+// Sizes that the prefill calls with sinks and their workspace query check alike.
+static kv_status check_prefill_sinks_sizes(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                                           int32_t num_kv_heads, int32_t head_dim, kv_dtype cache_dtype,
+                                           int32_t max_seq_len, int32_t window, int32_t num_sinks, int32_t num_workers) {
+    if (num_seqs < 0 || max_query_len < 0 || num_q_heads < 1 || num_kv_heads < 1 || max_seq_len < 0 || window < 0 ||
+        num_sinks < 0 || num_workers < 0)
+        return fail(KV_ERR_INVALID_ARG, "invalid size argument");
+    if (num_q_heads % num_kv_heads)
+        return fail(KV_ERR_INVALID_ARG, "num_q_heads (%d) is not a multiple of num_kv_heads (%d)", num_q_heads,
+                    num_kv_heads);
+    if (num_q_heads / num_kv_heads > 128)
+        return fail(KV_ERR_UNSUPPORTED, "prefill: num_q_heads / num_kv_heads must be at most 128");
+    const bool wide = cache_dtype == KV_FP8_E4M3 || cache_dtype == KV_INT4;
+    if (head_dim != 128 && (head_dim != 64 || wide))
+        return fail(KV_ERR_UNSUPPORTED, "prefill: head_dim %d (supported: 64, 128; E4M3 and INT4 caches: 128)", head_dim);
+    if (num_workers > 32767) return fail(KV_ERR_UNSUPPORTED, "prefill: num_workers > 32767");
+    return KV_OK;
+}
+
+size_t kv_paged_attention_prefill_sinks_workspace_size(int32_t num_seqs, int32_t max_query_len, int32_t num_q_heads,
+                                                       int32_t num_kv_heads, int32_t head_dim, kv_dtype cache_dtype,
+                                                       int32_t max_seq_len, int32_t window, int32_t num_sinks,
+                                                       int32_t num_workers) {
+    if (check_prefill_sinks_sizes(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim, cache_dtype, max_seq_len,
+                                  window, num_sinks, num_workers) != KV_OK)
+        return SIZE_MAX;
+    int dev;
+    cudaError_t e = cudaGetDevice(&dev);
+    DeviceInfo info;
+    if (e != cudaSuccess || (e = device_info(dev, &info)) != cudaSuccess) {
+        cuda_fail(e, "device attributes");
+        return SIZE_MAX;
+    }
+    ok();
+    return pkv::plan_prefill_sinks(max_query_len, num_q_heads / num_kv_heads, head_dim, num_workers, info.sm_count)
+        .workspace_bytes;
+}
+
+static kv_status prefill_sinks(const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs,
+                               int32_t num_tokens, int32_t max_query_len, int32_t num_q_heads, const SinkCache &c,
+                               const int32_t *block_table, int64_t bt_stride, int32_t max_blocks_per_seq,
+                               const int32_t *seq_lens, int32_t max_seq_len, float scale, int32_t window,
+                               int32_t num_sinks, int32_t num_workers, void *workspace, size_t workspace_bytes, void *out,
+                               float *lse_out, int32_t *d_err, void *stream) {
+    if (num_tokens < 0 || c.num_blocks < 1 || max_blocks_per_seq < 0 || bt_stride < max_blocks_per_seq)
+        return fail(KV_ERR_INVALID_ARG, "invalid size argument");
+    kv_status st = check_prefill_sinks_sizes(num_seqs, max_query_len, num_q_heads, c.num_kv_heads, c.head_dim, c.dtype,
+                                             max_seq_len, window, num_sinks, num_workers);
+    if (st == KV_OK) st = check_sink_cache(c, q_dtype);
+    if (st != KV_OK) return st;
+    if (c.block_size != 8 && c.block_size != 16 && c.block_size != 32)
+        return fail(KV_ERR_UNSUPPORTED, "prefill: block_size must be 8, 16 or 32");
+    const bool int4 = c.dtype == KV_INT4, fp8 = c.dtype == KV_FP8_E4M3;
+    const float scale_log2 = scale * (fp8 ? c.k_scale : 1.0f) * 1.4426950408889634f;
+    if (!(scale >= 0.f) || !std::isfinite(scale_log2)) return fail(KV_ERR_INVALID_ARG, "scale must be finite and >= 0");
+    if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return ok();
+    if (!q || !query_start_loc || !c.k || !c.v || !block_table || !seq_lens || !out)
+        return fail(KV_ERR_INVALID_ARG, "null pointer");
+    if (!aligned(q, 16) || !aligned(c.k, 16) || !aligned(c.v, 16) || !aligned(out, 16))
+        return fail(KV_ERR_INVALID_ARG, "q, caches and out must be 16-byte aligned");
+    if (!aligned(query_start_loc, 4) || !aligned(block_table, 4) || !aligned(seq_lens, 4) || !aligned(lse_out, 4) ||
+        !aligned(d_err, 4))
+        return fail(KV_ERR_INVALID_ARG, "misaligned pointer");
+    // items are finished while others still read
+    const int64_t B = num_seqs, rows = static_cast<int64_t>(num_tokens) * num_q_heads;
+    const ByteRange outs[] = {{out, 2 * rows * c.head_dim}, {lse_out, 4 * rows},
+                              {workspace, static_cast<int64_t>(std::min<size_t>(workspace_bytes, INT64_MAX))}};
+    const ByteRange ins[] = {{q, 2 * rows * c.head_dim}, {query_start_loc, 4 * (B + 1)}, {seq_lens, 4 * B},
+                             {block_table, 4 * ((B - 1) * bt_stride + max_blocks_per_seq)}, {c.k, c.bytes()},
+                             {c.v, c.bytes()}, {c.k_scales, c.scale_bytes()}, {c.v_scales, c.scale_bytes()}};
+    bool clash = overlap(outs[0], outs[1]) || overlap(outs[0], outs[2]) || overlap(outs[1], outs[2]);
+    for (const ByteRange &o : outs)
+        for (const ByteRange &i : ins) clash |= overlap(o, i);
+    if (clash) return fail(KV_ERR_INVALID_ARG, "an output or the workspace overlaps an input or another output");
+    int dev;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    cudaError_t e = bind_device(s, &dev);
+    if (e != cudaSuccess) return cuda_fail(e, "device of stream");
+    DeviceInfo info;
+    if ((e = device_info(dev, &info)) != cudaSuccess) return cuda_fail(e, "device attributes");
+    const int32_t g = num_q_heads / c.num_kv_heads;
+    const pkv::TreePlan plan = pkv::plan_prefill_sinks(max_query_len, g, c.head_dim, num_workers, info.sm_count);
+    if (static_cast<size_t>(info.smem_optin) < plan.smem_bytes)
+        return fail(KV_ERR_UNSUPPORTED, "prefill: needs %zu bytes of shared memory per block, the device has %d",
+                    plan.smem_bytes, info.smem_optin);
+    if (!workspace || workspace_bytes < plan.workspace_bytes)
+        return fail(KV_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", plan.workspace_bytes,
+                    workspace ? workspace_bytes : 0);
+    if (!aligned(workspace, 256)) return fail(KV_ERR_INVALID_ARG, "workspace must be 256-byte aligned");
+    CUtensorMap tq{}, tk{}, tv{};
+    if (!int4 && !fp8) {
+        st = encode_query_map(&tq, q, num_tokens, num_q_heads, c.head_dim, g, plan.tokens_per_tile);
+        for (int i = 0; i < 2 && st == KV_OK; ++i)
+            st = encode_heads_map(i ? &tv : &tk, i ? c.v : c.k, c.num_blocks, c.block_size, c.num_kv_heads, c.head_dim, 1);
+        if (st != KV_OK) return st;
+    }
+    pkv::SinkPrefillArgs a;
+    a.t.query_start_loc = query_start_loc;
+    a.t.seq_lens = seq_lens;
+    a.t.block_table = block_table;
+    a.t.bt_stride = bt_stride;
+    a.t.max_blocks_per_seq = max_blocks_per_seq;
+    a.t.tree_mask = nullptr;
+    a.t.num_seqs = num_seqs;
+    a.t.num_tokens = num_tokens;
+    a.t.max_query_len = max_query_len;
+    a.t.num_q_heads = num_q_heads;
+    a.t.num_kv_heads = c.num_kv_heads;
+    a.t.block_size = c.block_size;
+    a.t.num_blocks = c.num_blocks;
+    a.t.max_seq_len = std::min(max_seq_len, INT32_MAX - 256);  // the keys of a whole tile count in 32 bits
+    a.t.window = window;
+    // a scale of 0 (all weights alike) as the least normal number: the kernels mask with -inf * scale
+    a.t.scale_log2 = std::fmax(scale_log2, FLT_MIN);
+    a.t.v_cache = c.v;
+    a.t.out = out;
+    a.t.lse_out = lse_out;
+    a.t.d_err = d_err;
+    a.num_sinks = window > 0 ? std::min(num_sinks, a.t.max_seq_len) : 0;
+    a.q = q;
+    a.k_cache = c.k;
+    a.v_scale = c.v_scale;
+    a.k_gscales = c.k_scales;
+    a.v_gscales = c.v_scales;
+    a.group_shift = int4 ? log2_of(c.group_size) : 0;
+    e = pkv::launch_prefill_sinks(tq, tk, tv, a, plan, workspace, c.head_dim, q_dtype, c.dtype, dev, s);
+    if (e != cudaSuccess) return cuda_fail(e, "prefill launch");
+    return ok();
+}
+
+kv_status kv_paged_attention_prefill_sinks(
+    const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+    int32_t max_query_len, int32_t num_q_heads, const void *k_cache, const void *v_cache, kv_dtype cache_dtype,
+    int32_t num_kv_heads, int32_t head_dim, int32_t block_size, int32_t num_blocks, const int32_t *block_table,
+    int64_t bt_stride, int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, float scale,
+    int32_t window, int32_t num_sinks, float k_scale, float v_scale, int32_t num_workers, void *workspace,
+    size_t workspace_bytes, void *out, float *lse_out, int32_t *d_err, void *stream) {
+    if (cache_dtype == KV_INT4)
+        return fail(KV_ERR_UNSUPPORTED, "INT4 caches are read by kv_paged_attention_prefill_sinks_int4");
+    const SinkCache c{k_cache, v_cache, cache_dtype, num_kv_heads, head_dim, block_size, num_blocks,
+                      k_scale, v_scale, nullptr, nullptr, 0};
+    return prefill_sinks(q, q_dtype, query_start_loc, num_seqs, num_tokens, max_query_len, num_q_heads, c, block_table,
+                         bt_stride, max_blocks_per_seq, seq_lens, max_seq_len, scale, window, num_sinks, num_workers,
+                         workspace, workspace_bytes, out, lse_out, d_err, stream);
+}
+
+kv_status kv_paged_attention_prefill_sinks_int4(
+    const void *q, kv_dtype q_dtype, const int32_t *query_start_loc, int32_t num_seqs, int32_t num_tokens,
+    int32_t max_query_len, int32_t num_q_heads, const void *k_cache, const void *v_cache, int32_t num_kv_heads,
+    int32_t head_dim, int32_t block_size, int32_t num_blocks, const int32_t *block_table, int64_t bt_stride,
+    int32_t max_blocks_per_seq, const int32_t *seq_lens, int32_t max_seq_len, float scale, int32_t window,
+    int32_t num_sinks, const float *k_scales, const float *v_scales, int32_t group_size, int32_t num_workers,
+    void *workspace, size_t workspace_bytes, void *out, float *lse_out, int32_t *d_err, void *stream) {
+    const SinkCache c{k_cache, v_cache, KV_INT4, num_kv_heads, head_dim, block_size, num_blocks,
+                      1.f, 1.f, k_scales, v_scales, group_size};
+    return prefill_sinks(q, q_dtype, query_start_loc, num_seqs, num_tokens, max_query_len, num_q_heads, c, block_table,
+                         bt_stride, max_blocks_per_seq, seq_lens, max_seq_len, scale, window, num_sinks, num_workers,
+                         workspace, workspace_bytes, out, lse_out, d_err, stream);
+}
+
 }  // extern "C"

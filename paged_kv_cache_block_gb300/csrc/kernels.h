@@ -245,6 +245,21 @@ cudaError_t launch_tree_attention(const CUtensorMap &tmap_q, const CUtensorMap &
                                   const TreeArgs &a, const TreePlan &plan, void *workspace, int head_dim, int q_dtype,
                                   int dev, cudaStream_t stream);
 
+// Prefill attention with a window and sinks (kv_paged_attention_prefill_sinks, _int4): the tree's arguments
+// (no masks), and
+struct SinkPrefillArgs {
+    TreeArgs t;
+    int32_t num_sinks;  // 0 without a window
+    const void *q, *k_cache;
+    float v_scale;                       // E4M3
+    const float *k_gscales, *v_gscales;  // INT4
+    int32_t group_shift;
+};
+TreePlan plan_prefill_sinks(int max_query_len, int group, int head_dim, int num_workers, int sm_count);
+cudaError_t launch_prefill_sinks(const CUtensorMap &tmap_q, const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
+                                 const SinkPrefillArgs &a, const TreePlan &plan, void *workspace, int head_dim,
+                                 int q_dtype, int cache_dtype, int dev, cudaStream_t stream);
+
 // kv_selftest_bounded_wait: one thread waits limit_us on an mbarrier nothing completes.
 cudaError_t launch_selftest_bounded_wait(int32_t limit_us, int32_t *d_err, int32_t *d_waited_us,
                                          cudaStream_t stream);

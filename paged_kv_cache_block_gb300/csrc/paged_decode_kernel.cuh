@@ -61,16 +61,6 @@ template <> struct CacheTraits<Fp8E4M3> {
     static constexpr bool kFp8 = true;
 };
 
-// Four E4M3 bytes -> two packed fp16 pairs (bytes 0,1 -> lo; bytes 2,3 -> hi), exact.
-__device__ __forceinline__ void e4m3x4_to_h2x2(uint32_t four, uint32_t &lo, uint32_t &hi) {
-    asm("{\n\t.reg .b16 l, h;\n\t"
-        "mov.b32 {l, h}, %2;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %0, l;\n\t"
-        "cvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
-        : "=r"(lo), "=r"(hi)
-        : "r"(four));
-}
-
 // One 16-byte chunk c of token t's K and V rows (row = chunks 16-byte chunks) into its slot:
 // a bit copy, or E4M3 quantisation with the per-tensor scales.
 template <typename QT, typename CT>

@@ -1,0 +1,1085 @@
+// Prefill attention with a sliding window and sinks, over 16-bit, E4M3 and INT4 caches, on the
+// fifth-generation tensor cores (chunked prefill: "vLLM의 KV cache 연결 흐름", section "EngineCore가
+// 하는 일"; windows: "vLLM Worker侧GPU KV Cache初始化流程深度解析", section "混合注意力机制", and its
+// section "KV Cache技术背景" for the 8- and 4-bit caches; the pages have no sinks).
+//
+// The row at position p sees key j <= p when window = 0, j > p - window or j < num_sinks:
+//   out = sum_j p_j V_j / sum_j p_j,  p_j = exp2(scale log2(e) q.K_j - m)
+// Row tiles are up to 128 rows of a kv head (128 / g tokens x the g heads of its group).  An item is
+// (sequence, kv head, two row tiles).  Its keys form an axis of their own, the sequence without the
+// blocks that none of its rows sees (those between the last sink's block and the first row's window):
+// block c of the axis is block c of the sequence below sink_blocks, and block c + hidden from there on.
+// The cache being paged, a tile of 128 keys is any 128 / block_size blocks, so sinks and window share
+// tiles and the axis starts at a block, not at a multiple of 128.
+//
+// Two chains x = 0, 1 of
+//   S_x = Q K_j^T   tcgen05.mma, M 128, N 128; fp32 in TMEM
+//   P_x = exp2(S_x * scale - m)   one thread a row; 16-bit weights back into TMEM over S_x
+//   O_x += P_x V_j  tcgen05.mma, A = P_x in TMEM, fp32 in TMEM across key tiles
+// run at once: one row tile each, or, for an item of one row tile, every second key tile each, joined at
+// the end.  The flat list of (item, key tile) is cut into equal shares, one a CTA, so that neither the
+// batch's lengths nor the triangle of whole prompts matter; items that lie in several shares leave
+// partial results, joined by the merge of the tree attention (tree_common.cuh), whose parameters and
+// records this kernel shares.
+//
+// 16-bit caches: a warp copies K and V tiles by TMA, a block and all dims of a head a box, and another
+// cleans V tiles that hold keys which not every row sees (a weight of 0 times a NaN or an infinity would not be
+// 0): what no row sees is zeroed, and a non-finite value that some rows see is zeroed and added to those
+// rows' results afterwards.  E4M3 and INT4 caches (kWide): both warps load codes and write them as fp16
+// tiles instead, where the products take them from: INT4 codes as the integers they are, two a lop3 and
+// one packed add, their dims in the order (0, 4, 1, 5, 2, 6, 3, 7) of each eight that this leaves them in.  The
+// queries follow that order; each row is multiplied by its head's K scales and by the power of two that
+// puts its largest product at 2^7 .. 2^8, so that any scale keeps its digits in fp16, and the power comes
+// off in the row's softmax scale.  V scales multiply the result.
+// Weights are taken against the reference maximum in use; only when a row's maximum exceeds it by
+// more than 2^8 are its O and sum rescaled.  The sum is of the weights before their rounding.
+// Every wait is bounded (2 s): on expiry KV_DERR_TIMEOUT is set, what was issued is drained, TMEM is freed
+// and the CTA returns.
+#pragma once
+
+#include <cfloat>
+
+#include "tree_common.cuh"
+
+namespace pkv {
+
+enum { kCache16 = 0, kCacheE4M3 = 1, kCacheInt4 = 2 };
+
+struct SinkPrefillParams {
+    TreeParams t;          // sizes, outputs and the workspace, for the merge too
+    int num_sinks;         // 0 without a window
+    int sink_blocks;
+    int bs_shift;          // log2(block_size)
+    const void *k_cache;   // E4M3 and INT4
+    float v_scale;         // E4M3
+    const float *k_gscales, *v_gscales;  // INT4: [num_kv_heads, D >> group_shift]
+    int group_shift;
+    const void *q;         // E4M3 and INT4: [num_tokens, num_q_heads, D]
+};
+
+namespace sinks {
+
+constexpr int kBM = kTreeRows;
+constexpr int kBN = 128;           // keys of a key tile
+constexpr int kThreads = 384;
+constexpr uint32_t kColO = 256;
+
+template <int D> struct Tile {
+    static constexpr int kHalves = D / 64;
+    static constexpr int kBytes = kHalves * kHalf;      // a Q, K or V tile
+    static constexpr int kGroup = kHalves * 1024;       // 8 keys of a K or V tile: [64 dims of D][key][dim]
+    static constexpr int kStages = D == 128 ? 4 : 8;    // ring entries (128 KB)
+    static constexpr int kOffKV = 2 * kBytes;           // after Q_0, Q_1
+    static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // chain 1's maxima and sums: 2 x 128 floats
+    static constexpr int kOffScratch = kOffJoin + 2 * 128 * 4;   // of the schedule
+    static constexpr int kScratchBytes = 512;
+    static constexpr int kOffBar = kOffScratch + kScratchBytes;
+    static constexpr int kNumBars = 14 + 2 * kStages;
+    static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
+    static constexpr int kSmem = kOffMisc + 8 + 8 * kFlags + 4 * kStages + 1024;  // + alignment
+    static_assert(kSmem <= 227 * 1024, "shared memory");
+    // pieces whose V tiles can be in the ring at once, one more that the cleaning warp has begun,
+    // and one without mixed tiles (only a share's last)
+    static_assert(kFlags >= (kStages + 1) / 2 + 2, "a flag per piece in flight");
+};
+
+// mbarrier indices (+ x: one per chain)
+enum { kBarQFull = 0, kBarQEmpty = 1, kBarS = 2, kBarP = 4, kBarPv = 6, kBarPd = 8, kBarJoin = 10,
+       kBarJoined = 11, kBarDrain = 12, kBarKv = 14 };  // then KvFull[stages], KvEmpty[stages]
+
+// A sequence's part of the work list.  Costs are counted in keys: pair i of a kv head costs
+//   c_i = min(keys up to its last token, cap) + item_cost
+// where cap is what a window and the sinks leave; it is never above the keys of the pair's axis, so that
+// c_i - item_cost <= 128 * (its key tiles).
+struct Seq {
+    int q0, n, L, ctx;  // first row, rows, length, context
+    int pairs;          // of row tiles
+};
+
+struct Costs {
+    int step;           // tokens of a pair
+    int64_t extra;      // of a window: window - 1 + keys of the sinks' blocks (no window: far above any length)
+    int64_t item;
+    __device__ __forceinline__ Costs(const SinkPrefillParams &p, int64_t item_cost)
+        : step(2 * p.t.tokens_per_tile),
+          extra(p.t.a.window > 0 ? static_cast<int64_t>(p.t.a.window) - 1 + (p.sink_blocks << p.bs_shift) : int64_t(1) << 40),
+          item(item_cost) {}
+    __device__ __forceinline__ int64_t of(const Seq &s, int i) const {
+        const int last = min(s.n, (i + 1) * step);
+        return min(static_cast<int64_t>(s.ctx) + last, extra + (last - i * step)) + item;
+    }
+    // Of pairs 0 .. k - 1: whole pairs i < m lie below the window's bound ctx + (i + 1) step <= extra + step.
+    __device__ __forceinline__ int64_t before(const Seq &s, int k) const {
+        const int64_t whole = min(k, s.pairs - 1);
+        const int64_t m = min(whole, extra < s.ctx ? int64_t(0) : (extra - s.ctx) / step + 1);
+        int64_t sum = m * s.ctx + step * (m * (m + 1) / 2) + (whole - m) * (extra + step) + whole * item;
+        if (k == s.pairs) sum += of(s, s.pairs - 1);
+        return sum;
+    }
+};
+
+// The sequence's lengths; false when it has no rows, or is rejected (*rejected).
+__device__ __forceinline__ bool load_seq(const SinkPrefillParams &p, int b, Seq &s, bool *rejected) {
+    const TreeArgs &a = p.t.a;
+    s.q0 = a.query_start_loc[b];
+    s.n = a.query_start_loc[b + 1] - s.q0;
+    s.L = a.seq_lens[b];
+    *rejected = s.n > 0 && !(s.n <= a.max_query_len && s.q0 >= 0 && s.q0 <= a.num_tokens - s.n && s.L >= s.n &&
+                             s.L <= a.max_seq_len && ((s.L - 1) >> p.bs_shift) < a.max_blocks_per_seq);
+    if (s.n <= 0 || *rejected) return false;
+    s.ctx = s.L - s.n;
+    s.pairs = (s.n - 1) / (2 * p.t.tokens_per_tile) + 1;
+    return true;
+}
+
+// Where the share of a CTA starts: sequence, item and the cost where that item starts.
+struct ShareStart {
+    Seq s;
+    int64_t at;
+    int b, idx;
+};
+struct ShareScratch {
+    int64_t warp_keys[16], warp_items[16];
+    ShareStart start;
+};
+static_assert(sizeof(ShareScratch) <= 512, "Tile::kScratchBytes");
+
+// The share [x0, x1) of CTA c (x0 == x1: none) and an item's cost.  Computed by the whole block, with
+// scratch in shared memory; scratch.start is valid after the next __syncthreads.
+__device__ __forceinline__ void share_of_cta(const SinkPrefillParams &p, int c, int64_t &x0, int64_t &x1,
+                                             int64_t &item_cost, ShareScratch &scratch) {
+    static_assert(kThreads <= 16 * 32, "a word a warp");
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int num_seqs = p.t.a.num_seqs, heads = p.t.a.num_kv_heads;
+    const int per = (num_seqs + kThreads - 1) / kThreads;
+    const int b_lo = min(num_seqs, static_cast<int>(threadIdx.x) * per), b_hi = min(num_seqs, b_lo + per);
+    const Costs free(p, 0);
+    Seq s;
+    bool rejected;
+    int64_t keys = 0, items = 0;  // of this thread's sequences
+    for (int b = b_lo; b < b_hi; ++b) {
+        if (!load_seq(p, b, s, &rejected)) continue;
+        keys += free.before(s, s.pairs) * heads;
+        items += static_cast<int64_t>(s.pairs) * heads;
+    }
+    int64_t ik = keys, ii = items;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t t = __shfl_up_sync(0xffffffffu, ik, o), i = __shfl_up_sync(0xffffffffu, ii, o);
+        if (lane >= o) ik += t, ii += i;
+    }
+    if (lane == 31) scratch.warp_keys[warp] = ik, scratch.warp_items[warp] = ii;
+    __syncthreads();
+    int64_t keys_before = ik - keys, items_before = ii - items, all_keys = 0, all_items = 0;
+#pragma unroll
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) keys_before += scratch.warp_keys[w], items_before += scratch.warp_items[w];
+        all_keys += scratch.warp_keys[w];
+        all_items += scratch.warp_items[w];
+    }
+    // A share is at least as long as any tile (128 keys of an axis and an item's cost), so that each holds
+    // a tile's end, hence a tile: no share between two of an item is empty.
+    const bool big = all_keys >= static_cast<int64_t>(kBigShare) * kBN * p.t.workers;
+    item_cost = big ? kItemCost * kBN : 0;
+    const int64_t total = all_keys + item_cost * all_items;
+    const int64_t most = total / (kBN + item_cost);
+    const int64_t shares = min(static_cast<int64_t>(p.t.workers), most > 0 ? most : (total > 0 ? 1 : 0));
+    x0 = x1 = 0;
+    if (c >= shares) return;
+    x0 = total * c / shares;
+    x1 = total * (c + 1) / shares;
+    const int64_t before = keys_before + item_cost * items_before;
+    if (x0 < before || x0 >= before + keys + item_cost * items) return;
+    const Costs costs(p, item_cost);
+    int64_t at = before;  // one thread
+    for (int b = b_lo; b < b_hi; ++b) {
+        if (!load_seq(p, b, s, &rejected)) continue;
+        const int64_t head = costs.before(s, s.pairs);
+        if (x0 < at + head * heads) {
+            const int64_t h = (x0 - at) / head;
+            at += h * head;
+            int lo = 0, hi = s.pairs - 1;  // the last pair that starts at or before x0
+            while (lo < hi) {
+                const int mid = (lo + hi + 1) >> 1;
+                if (at + costs.before(s, mid) <= x0) lo = mid;
+                else hi = mid - 1;
+            }
+            scratch.start.b = b;
+            scratch.start.idx = static_cast<int>(h) * s.pairs + lo;
+            scratch.start.at = at + costs.before(s, lo);
+            scratch.start.s = s;
+            break;
+        }
+        at += head * heads;
+    }
+}
+
+// Rows of rejected sequences are 0 (lse -inf): the CTAs take the sequences in turn.
+template <typename T, int D> __device__ __forceinline__ void zero_rejected(const SinkPrefillParams &p) {
+    const TreeArgs &a = p.t.a;
+    for (int b = blockIdx.x; b < a.num_seqs; b += gridDim.x) {
+        Seq s;
+        bool rejected;
+        load_seq(p, b, s, &rejected);
+        if (!rejected) continue;
+        if (threadIdx.x == 0) report(a.d_err, KV_DERR_BAD_LEN);
+        const int64_t r0 = max(s.q0, 0), r1 = min(static_cast<int64_t>(s.q0) + s.n, static_cast<int64_t>(a.num_tokens));
+        const int64_t rows = (r1 - r0) * a.num_q_heads;
+        for (int64_t i = threadIdx.x; i < rows * (D / 8); i += blockDim.x)
+            reinterpret_cast<uint4 *>(static_cast<T *>(a.out) + r0 * a.num_q_heads * D)[i] = make_uint4(0, 0, 0, 0);
+        if (a.lse_out)
+            for (int64_t i = threadIdx.x; i < rows; i += blockDim.x) a.lse_out[r0 * a.num_q_heads + i] = -INFINITY;
+    }
+}
+
+// The pieces of a share, in order: (item, key tiles ja .. jb - 1 of its axis).  Every warp walks the same ones.
+struct Walk {
+    int64_t at, cost;  // cost where the item starts, and of the item
+    int64_t x0, x1;    // the share
+    int64_t item_cost;
+    Seq cur;           // the piece's sequence,
+    int seq, item;     // its number, the item of it:
+    int h, nt, t0;     // kv head, row tiles, first token
+    int pf, pl;        // positions of the item's first and last token, on its axis
+    int hidden;        // blocks the axis leaves out
+    int tiles;         // of the axis
+    int ja, jb;
+    bool whole;        // the piece is its whole item
+    bool begun;
+
+    __device__ __forceinline__ void start(const ShareStart &st, int64_t x0_, int64_t x1_, int64_t item_cost_) {
+        seq = st.b, item = st.idx, at = st.at, x0 = x0_, x1 = x1_, item_cost = item_cost_;
+        cur = st.s;
+        begun = false;
+    }
+    // The tile that a cost lies in, of a cost within the item (its end: tiles): a tile belongs to the share
+    // that its end lies in.
+    __device__ __forceinline__ int tile_at(int64_t x) const { return static_cast<int>((x - at) * tiles / cost); }
+    __device__ __forceinline__ bool next(const SinkPrefillParams &p) {
+        const Costs costs(p, item_cost);
+        const TreeArgs &a = p.t.a;
+        for (;;) {
+            if (begun) {  // on to the next item
+                at += cost;
+                if (at >= x1) return false;
+                if (++item == cur.pairs * a.num_kv_heads) {
+                    item = 0;
+                    bool rejected = false;
+                    do {
+                        if (++seq >= a.num_seqs) return false;
+                    } while (!load_seq(p, seq, cur, &rejected));
+                }
+            }
+            begun = true;
+            h = item / cur.pairs;
+            const int pr = item - h * cur.pairs;
+            cost = costs.of(cur, pr);
+            t0 = pr * costs.step;
+            const int count = min(cur.n - t0, costs.step);
+            nt = count > p.t.tokens_per_tile ? 2 : 1;
+            pf = cur.ctx + t0;
+            hidden = a.window > 0 ? max(0, (max(0, pf - a.window + 1) >> p.bs_shift) - p.sink_blocks) : 0;
+            pf -= hidden << p.bs_shift;
+            pl = pf + count - 1;
+            tiles = pl / kBN + 1;
+            ja = tile_at(max(x0, at));
+            jb = tile_at(min(x1, at + cost));
+            whole = ja == 0 && jb == tiles;
+            if (ja < jb) return true;
+        }
+    }
+    // The share's first piece, for the merge.
+    __device__ __forceinline__ void record(const SinkPrefillParams &p, int c) const {
+        p.t.ws_first[2 * c] = make_int4(seq, item, ja, 0);
+        p.t.ws_first[2 * c + 1] = make_int4(cur.q0, cur.n, cur.pairs, 0);
+    }
+    // First key (on the axis) of the window of the row at axis position pos.
+    static __device__ __forceinline__ int window_from(const SinkPrefillParams &p, int pos) {
+        return p.t.a.window > 0 ? max(0, pos - p.t.a.window + 1) : 0;
+    }
+    // Whether key tile j holds a key that not all rows at axis positions first .. last see.
+    static __device__ __forceinline__ bool mixed(const SinkPrefillParams &p, int j, int first, int last) {
+        const int k1 = j * kBN + kBN - 1;
+        return k1 > first || (j * kBN < window_from(p, last) && k1 >= p.num_sinks);
+    }
+    __device__ __forceinline__ bool mixed(const SinkPrefillParams &p, int j) const { return mixed(p, j, pf, pl); }
+    // Block of the sequence that holds block c of the axis.
+    __device__ __forceinline__ int block(const SinkPrefillParams &p, int c) const { return c < p.sink_blocks ? c : c + hidden; }
+};
+
+// The keys k0 .. k0 + 31 (bit i: key k0 + i) that the row at position pos sees, with a window from klo.
+__device__ __forceinline__ uint32_t seen32(int k0, int pos, int klo, int num_sinks) {
+    const int hi = pos + 1 - k0, lo = klo - k0, s = num_sinks - k0;
+    const uint32_t upto = hi >= 32 ? ~0u : (hi > 0 ? (1u << hi) - 1 : 0u);
+    const uint32_t from = lo <= 0 ? ~0u : (lo < 32 ? ~((1u << lo) - 1) : 0u);
+    const uint32_t sink = s >= 32 ? ~0u : (s > 0 ? (1u << s) - 1 : 0u);
+    return upto & (from | sink);
+}
+
+template <typename QT, int kCache> using OperandOf = typename std::conditional<kCache == kCache16, QT, __half>::type;
+
+// The value at byte or element `at` of a 16-bit or E4M3 cache.
+template <typename QT, int kCache> __device__ __forceinline__ float cache_value(const void *cache, int64_t at) {
+    if constexpr (kCache == kCacheE4M3)
+        return __half2float(__half(__nv_cvt_fp8_to_halfraw(static_cast<const __nv_fp8_storage_t *>(cache)[at], __NV_E4M3)));
+    else
+        return to_float<QT>(static_cast<const QT *>(cache)[at]);
+}
+
+// Add the non-finite values of V that a row sees among the axis's keys [k0, k1) to its written result (out of
+// type QT, or a partial result): they were zeroed for the products.  Rare, so plain.
+template <typename QT, int D, int kCache>
+static __device__ __noinline__ void add_non_finite(const SinkPrefillParams &p, const Walk &w, int k0, int k1, int pos, int klo,
+                                                   QT *out, float4 *part) {
+    const TreeArgs &a = p.t.a;
+    for (int k = k0; k < k1; ++k) {
+        if (k > pos || (k < klo && k >= p.num_sinks)) continue;
+        const int id = a.block_table[w.seq * a.bt_stride + w.block(p, k >> p.bs_shift)];
+        if (id < 0 || id >= a.num_blocks) continue;
+        const int64_t at = ((static_cast<int64_t>(id) * a.block_size + (k & (a.block_size - 1))) * a.num_kv_heads + w.h) * D;
+        for (int d = 0; d < D; ++d) {
+            const float f = cache_value<QT, kCache>(a.v_cache, at + d);
+            if (isfinite(f)) continue;
+            if (part) reinterpret_cast<float *>(part + static_cast<int64_t>(d / 4) * p.t.rows_per_item)[d % 4] += f;
+            else out[d] = from_float<QT>(to_float<QT>(out[d]) + f);
+        }
+    }
+}
+
+// Eight INT4 codes (a 32-bit word) -> their values in fp16, as pairs (0, 4), (1, 5), (2, 6), (3, 7): with u =
+// code ^ 8, the fp16 of bits 0x6400 | u is 1024 + u, that of 0x6400 | u << 4 is 1024 + 16 u, both exact.
+__device__ __forceinline__ uint4 int4x8_values(uint32_t w) {
+    const __half2 off = __half2half2(__ushort_as_half(0xE408));       // -(1024 + 8)
+    const __half2 sixteenth = __half2half2(__ushort_as_half(0x2C00)), off16 = __half2half2(__ushort_as_half(0xD480));  // -72
+    auto as_h2 = [](uint32_t v) { return *reinterpret_cast<__half2 *>(&v); };
+    auto as_u = [](__half2 v) { return *reinterpret_cast<uint32_t *>(&v); };
+    const uint32_t w8 = w >> 8;
+    uint4 r;
+    r.x = as_u(__hadd2(as_h2(and_xor(w, 0x000f000fu, 0x64086408u)), off));
+    r.y = as_u(__hfma2(as_h2(and_xor(w, 0x00f000f0u, 0x64806480u)), sixteenth, off16));
+    r.z = as_u(__hadd2(as_h2(and_xor(w8, 0x000f000fu, 0x64086408u)), off));
+    r.w = as_u(__hfma2(as_h2(and_xor(w8, 0x00f000f0u, 0x64806480u)), sixteenth, off16));
+    return r;
+}
+// Where dim d of each eight stands among such pairs, and the other way round.
+__host__ __device__ constexpr int int4_place(int d) { return d < 4 ? 2 * d : 2 * (d - 4) + 1; }
+
+__device__ __forceinline__ void fence_proxy_async_shared() {
+    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+}
+
+template <typename QT, int D, int kCache>
+__global__ void __launch_bounds__(kThreads, 1)
+prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
+                     const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ SinkPrefillParams p) {
+    using TL = Tile<D>;
+    using MT = OperandOf<QT, kCache>;
+    constexpr bool kWide = kCache != kCache16;
+    constexpr int kStages = TL::kStages, kTileBytes = TL::kBytes;
+    const TreeArgs &a = p.t.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int g = p.t.group, TQ = p.t.tokens_per_tile, bs = a.block_size;
+    const int c = blockIdx.x;
+
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+    uint64_t *bars = reinterpret_cast<uint64_t *>(smem + TL::kOffBar);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + TL::kOffMisc);
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + TL::kOffMisc + 4);
+    // per piece, and per widening warp
+    volatile int *odd_flag = reinterpret_cast<volatile int *>(smem + TL::kOffMisc + 8);  // [2][kFlags]
+    int32_t *cleaned = reinterpret_cast<int32_t *>(smem + TL::kOffMisc + 8 + 8 * kFlags);  // [kStages]: entry + 1
+    float *join = reinterpret_cast<float *>(smem + TL::kOffJoin);
+    auto bar = [&](int i) { return smem_u32(&bars[i]); };
+    auto bar_full = [&](int s) { return smem_u32(&bars[kBarKv + s]); };
+    auto bar_empty = [&](int s) { return smem_u32(&bars[kBarKv + kStages + s]); };
+
+    if (!kWide && threadIdx.x == 32) {
+        prefetch_tensormap(&tmap_q);
+        prefetch_tensormap(&tmap_k);
+        prefetch_tensormap(&tmap_v);
+    }
+    if (threadIdx.x == 0) {
+        mbar_init(bar(kBarQFull), kWide ? 256 : 1);
+        mbar_init(bar(kBarQEmpty), 2);
+        for (int x = 0; x < 2; ++x) {
+            mbar_init(bar(kBarS + x), 1);
+            mbar_init(bar(kBarP + x), 128);
+            mbar_init(bar(kBarPv + x), 1);
+            mbar_init(bar(kBarPd + x), 1);
+            mbar_init(bar(kBarDrain + x), 1);
+        }
+        mbar_init(bar(kBarJoin), 128);
+        mbar_init(bar(kBarJoined), 128);
+        for (int s = 0; s < kStages; ++s) {
+            mbar_init(bar_full(s), kWide ? 2 : 1);
+            mbar_init(bar_empty(s), kWide ? 2 : 3);  // released by both chains, and the cleaning warp
+        }
+        *abort_flag = 0;
+        for (int i = 0; i < 2 * kFlags; ++i) odd_flag[i] = 0;
+        for (int i = 0; i < kStages; ++i) cleaned[i] = 0;
+        fence_barrier_init();
+    }
+    if (warp == 9) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(tmem_holder)),
+                     "r"(kTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
+    }
+    ShareScratch &scratch = *reinterpret_cast<ShareScratch *>(smem + TL::kOffScratch);
+    int64_t x0, x1, item_cost;
+    previous_kernel_done();
+    let_next_kernel_launch();
+    share_of_cta(p, c, x0, x1, item_cost, scratch);
+    zero_rejected<QT, D>(p);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_holder;
+    Walk w;
+    w.start(scratch.start, x0, x1, item_cost);
+
+    if (x0 == x1) {
+        // no share: nothing but the record that says so
+        if (threadIdx.x == 0) p.t.ws_first[2 * c] = make_int4(-1, 0, 0, 0);
+    } else if (!kWide && warp == 8) {
+        // ============================================================ TMA producer
+        const int bpt = kBN / bs;  // blocks of a key tile
+        const uint32_t q_bytes = static_cast<uint32_t>(TL::kHalves) * TQ * g * 128;
+        int entry = 0;  // ring entries filled
+        int piece = 0;
+        bool stop = false;
+        while (!stop && w.next(p)) {
+            const Seq s = w.cur;
+            if (piece == 0 && lane == 0) w.record(p, c);
+            // block ids of key tile j: lane l holds block j * bpt + l of the axis
+            const int nblk = (w.pl >> p.bs_shift) + 1;
+            auto entry_of = [&](int j) {  // (read before it is needed, checked when it is)
+                const int lb = j * bpt + lane;
+                return lane < bpt && lb < nblk ? a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + w.block(p, lb)]
+                                               : a.num_blocks;  // one past the pool: the copy reads zeros
+            };
+            int next_id = entry_of(w.ja);
+            bool ok = true;
+            if (lane == 0) {
+                // Q of the item, once the piece before has formed its last scores
+                if (piece > 0) ok = mbar_wait_sleep(bar(kBarQEmpty), (piece - 1) & 1);
+                if (ok) {
+                    mbar_arrive_expect_tx(bar(kBarQFull), w.nt * q_bytes);
+                    for (int x = 0; x < w.nt; ++x)
+                        for (int hf = 0; hf < TL::kHalves; ++hf)
+                            tma_load_3d(smem_u32(smem + x * kTileBytes + hf * kHalf), &tmap_q, bar(kBarQFull), 64 * hf,
+                                        w.h * g, s.q0 + w.t0 + x * TQ);
+                }
+            }
+            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
+                if (lane == 0) {
+                    report(a.d_err, KV_DERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                break;
+            }
+            ++piece;
+            for (int j = w.ja; j < w.jb && !stop; ++j) {
+                int my_id = next_id;
+                if (j + 1 < w.jb) next_id = entry_of(j + 1);
+                if (my_id < 0 || my_id > a.num_blocks || (my_id == a.num_blocks && lane < bpt && j * bpt + lane < nblk)) {
+                    report(a.d_err, KV_DERR_BAD_BLOCK);
+                    my_id = a.num_blocks;
+                }
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    const int slot = entry % kStages;
+                    int quit = 0;
+                    if (lane == 0) {
+                        if (entry >= kStages && !mbar_wait_sleep(bar_empty(slot), (entry / kStages - 1) & 1)) {
+                            quit = 1;
+                            report(a.d_err, KV_DERR_TIMEOUT);
+                            *abort_flag = 1;
+                        } else if (*abort_flag) {
+                            quit = 1;
+                        }
+                        if (!quit) mbar_arrive_expect_tx(bar_full(slot), kTileBytes);
+                    }
+                    if (__shfl_sync(0xffffffffu, quit, 0)) {
+                        stop = true;
+                        break;
+                    }
+                    const CUtensorMap *m = is_v ? &tmap_v : &tmap_k;
+                    uint8_t *dst = smem + TL::kOffKV + slot * kTileBytes;
+                    for (int jb = 0; jb < bpt; ++jb) {
+                        const int id = __shfl_sync(0xffffffffu, my_id, jb);
+                        if (lane == 0)
+                            tma_load_5d(smem_u32(dst + jb * bs * TL::kHalves * 128), m, bar_full(slot), 0, 0,
+                                        w.h * TL::kHalves, 0, id);
+                    }
+                    ++entry;
+                }
+            }
+        }
+        // never leave with copies in flight into this CTA's shared memory
+        if (lane == 0) {
+            if (piece > 0 && !mbar_wait_sleep(bar(kBarQFull), (piece - 1) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+            for (int i = max(0, entry - kStages); i < entry; ++i)
+                if (!mbar_wait_sleep(bar_full(i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+        }
+    } else if (warp == 9 || warp == 10) {
+        // ============================================================ MMA issue, one lane a chain
+        // Chain x, key tile by key tile: S_x once the product that read the columns it overwrites has
+        // completed; O_x once the softmax has written P_x and the V tile has landed (and been
+        // cleaned).  The other chain's tiles are released as soon as they have landed: everyone who
+        // waits for a ring entry passes all of them in order, so that no phase of its barrier can be
+        // mistaken.
+        const int x = warp - 9;
+        constexpr uint32_t ab = AbFormat<MT>::value;
+        constexpr uint32_t idesc_s = mma_idesc(ab, false, kBM, kBN);
+        constexpr uint32_t idesc_pv = mma_idesc(ab, true, kBM, D);
+        if (lane == 0) {
+            const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, TL::kGroup);
+            const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), 1024, TL::kGroup);
+            const uint32_t t_s = tmem + x * 128, t_o = tmem + kColO + x * 128;
+            auto full = [&](int e) { return mbar_wait_bounded(bar_full(e % kStages), (e / kStages) & 1); };
+            int base = 0;  // key tiles of the pieces before
+            int npv = 0;   // products O_x committed
+            bool dead = false;
+            for (int piece = 0; !dead && w.next(p); ++piece) {
+                if (*abort_flag != 0) break;
+                if (!mbar_wait_bounded(bar(kBarQFull), piece & 1)) {
+                    dead = true;
+                    break;
+                }
+                const int nt = w.nt;
+                const uint64_t dq = smem_desc(smem_u32(smem + (nt == 2 ? x * kTileBytes : 0)), 16, 1024);
+                const int step = nt == 2 ? 1 : 2;
+                const int first = w.ja + (nt == 2 ? 0 : x);
+                if (first >= w.jb) mbar_arrive(bar(kBarQEmpty));  // no tile for this chain
+                for (int j = w.ja; j < w.jb; ++j) {
+                    const bool last = j + step >= w.jb;
+                    const int ek = 2 * (base + j - w.ja), ev = ek + 1;
+                    const int sk = ek % kStages, sv = ev % kStages;
+                    if (nt == 1 && ((j - w.ja) & 1) != x) {
+                        bool landed = full(ek);
+                        if (landed) mbar_arrive(bar_empty(sk));
+                        landed = landed && full(ev);
+                        if (landed) mbar_arrive(bar_empty(sv));
+                        if (!landed) {
+                            dead = true;
+                            break;
+                        }
+                        continue;
+                    }
+                    if ((npv > 0 && !mbar_wait_bounded(bar(kBarPd + x), (npv - 1) & 1)) || !full(ek)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t dk = dkv + static_cast<uint64_t>((sk * kTileBytes) >> 4);
+#pragma unroll
+                    for (int k = 0; k < D / 16; ++k) {
+                        const int in = (k & 3) * 32;
+                        mma_f16(t_s, dq + (((k >> 2) * kHalf + in) >> 4), dk + (((k >> 2) * 1024 + in) >> 4), idesc_s, k > 0);
+                    }
+                    mma_commit(bar(kBarS + x));
+                    mma_commit(bar_empty(sk));
+                    if (last) mma_commit(bar(kBarQEmpty));
+                    if (!full(ev) || (!kWide && w.mixed(p, j) && !wait_at_least_bounded(&cleaned[sv], ev + 1)) ||
+                        !mbar_wait_bounded(bar(kBarP + x), npv & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint64_t dv = dv0 + static_cast<uint64_t>((sv * kTileBytes) >> 4);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k)
+                        mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2 * TL::kGroup) >> 4), idesc_pv, j > first || k > 0);
+                    mma_commit(bar(kBarPd + x));
+                    mma_commit(bar_empty(sv));
+                    if (last) mma_commit(bar(kBarPv + x));
+                    ++npv;
+                }
+                base += w.jb - w.ja;
+            }
+            if (dead) {
+                report(a.d_err, KV_DERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+            // every MMA this lane issued has completed before TMEM is freed
+            mma_commit(bar(kBarDrain + x));
+            if (!mbar_wait_bounded(bar(kBarDrain + x), 0)) report(a.d_err, KV_DERR_TIMEOUT);
+        }
+        __syncwarp();
+    } else if (!kWide && warp == 11) {
+        // ============================================================ cleaning of V tiles
+        int base = 0;
+        bool dead = false;
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            if (lane == 0) odd_flag[piece % kFlags] = 0;
+            __syncwarp();
+            for (int e = 0; e < 2 * (w.jb - w.ja); ++e) {
+                const int j = w.ja + (e >> 1);
+                const int ev = 2 * base + e, sv = ev % kStages;
+                if (!__all_sync(0xffffffffu, mbar_wait_sleep(bar_full(sv), (ev / kStages) & 1))) {
+                    dead = true;
+                    break;
+                }
+                if (!(e & 1) || !w.mixed(p, j)) {
+                    if (lane == 0) mbar_arrive(bar_empty(sv));
+                    continue;
+                }
+                const uint32_t tile = smem_u32(smem + TL::kOffKV + sv * kTileBytes);
+                const int k0 = j * kBN;
+                bool odd = false;
+                auto clean = [&](int lo, int hi, bool zero) {
+                    lo = max(lo, k0) - k0;
+                    hi = min(hi, k0 + kBN) - k0;
+                    for (int i = lo * 8 + lane; i < hi * 8; i += 32)
+                        for (int hf = 0; hf < TL::kHalves; ++hf)
+                            clean_chunk<MT>(tile + (i >> 6) * TL::kGroup + hf * 1024 + (i & 63) * 16, zero, odd);
+                };
+                // keys no row sees: between the sinks and the first row's window, and behind the last row;
+                // keys some rows do not see: up to the last row's window, and the item's own behind its first
+                const int from = max(w.window_from(p, w.pf), p.num_sinks), to = w.window_from(p, w.pl);
+                if (a.window > 0) {
+                    clean(p.num_sinks, w.window_from(p, w.pf), true);
+                    clean(from, min(to, w.pf + 1), false);
+                }
+                clean(w.pf + 1, w.pl + 1, false);
+                clean(w.pl + 1, ((w.pl >> p.bs_shift) + 1) << p.bs_shift, true);
+                if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[piece % kFlags] = 1;
+                fence_proxy_async_shared();
+                __syncwarp();
+                if (lane == 0) {
+                    st_release_cta(&cleaned[sv], ev + 1);
+                    mbar_arrive(bar_empty(sv));
+                }
+                __syncwarp();
+            }
+            base += w.jb - w.ja;
+        }
+        if (dead && lane == 0) {
+            report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    } else if (kWide && (warp == 8 || warp == 11)) {
+        // ============================================================ codes to fp16 tiles
+        // Each of the two warps takes every second group of 8 keys; lane l holds 16 bytes of key l & 7 (E4M3:
+        // 16 of each half of it).  As soon as a group has been written, its place takes the load of the next
+        // ring entry's, whose block ids were read a tile before.
+        if constexpr (kWide) {
+            constexpr int kRow = kCache == kCacheInt4 ? D / 2 : D;  // bytes of a key of a head
+            constexpr int kParts = kRow / 64;                       // 64-byte parts of it
+            constexpr int kGroups = kBN / 16;                       // of a tile, for a warp
+            const int wi = warp == 8 ? 0 : 1;
+            const int bpt = kBN / bs;
+            const int row = lane & 7, quarter = lane >> 3;
+            uint4 held[kGroups][kParts];
+            int entry = 0;
+            bool dead = false;
+            const int64_t token = static_cast<int64_t>(a.num_kv_heads) * kRow;
+            auto load_ids = [&](int j) {  // lane l: block l of key tile j (-1: zeros)
+                const int lb = j * bpt + lane;
+                if (lane >= bpt || lb > w.pl >> p.bs_shift) return -1;
+                const int e = a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + w.block(p, lb)];
+                if (e >= 0 && e < a.num_blocks) return e;
+                if (wi == 0) report(a.d_err, KV_DERR_BAD_BLOCK);
+                return -1;
+            };
+            auto load = [&](int i, bool is_v, int ids) {  // group i of a K or V tile
+                const int k = (2 * i + wi) * 8;  // its first key, in the tile
+                const int id = __shfl_sync(0xffffffffu, ids, k >> p.bs_shift);
+                const uint8_t *src = static_cast<const uint8_t *>(is_v ? a.v_cache : p.k_cache) + w.h * kRow + quarter * 16 +
+                                     (static_cast<int64_t>(id) * bs + (k & (bs - 1)) + row) * token;
+#pragma unroll
+                for (int u = 0; u < kParts; ++u)
+                    held[i][u] = id >= 0 ? *reinterpret_cast<const uint4 *>(src + 64 * u) : make_uint4(0, 0, 0, 0);
+            };
+            for (int piece = 0; !dead && w.next(p); ++piece) {
+                if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                if (piece == 0 && wi == 0 && lane == 0) w.record(p, c);
+                if (lane == 0) odd_flag[wi * kFlags + piece % kFlags] = 0;
+                __syncwarp();
+                int ids = load_ids(w.ja), next_ids = -1;
+#pragma unroll
+                for (int i = 0; i < kGroups; ++i) load(i, false, ids);
+                for (int e = 0; e < 2 * (w.jb - w.ja); ++e, ++entry) {
+                    const int j = w.ja + (e >> 1);
+                    const bool is_v = e & 1, more = e + 1 < 2 * (w.jb - w.ja);
+                    if (is_v) ids = next_ids;  // of the entry that is loaded now
+                    else if (j + 1 < w.jb) next_ids = load_ids(j + 1);
+                    const int slot = entry % kStages;
+                    if (entry >= kStages &&
+                        !__all_sync(0xffffffffu, mbar_wait_sleep(bar_empty(slot), (entry / kStages - 1) & 1))) {
+                        dead = true;
+                        break;
+                    }
+                    if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                    uint8_t *tile = smem + TL::kOffKV + slot * kTileBytes + row * 128;
+                    const bool mixed = kCache == kCacheE4M3 && is_v && w.mixed(p, j);
+                    bool odd = false;
+#pragma unroll
+                    for (int i = 0; i < kGroups; ++i) {
+                        const int grp = 2 * i + wi;
+                        uint8_t *dst = tile + grp * TL::kGroup;
+                        if constexpr (kCache == kCacheInt4) {
+                            const uint32_t words[4] = {held[i][0].x, held[i][0].y, held[i][0].z, held[i][0].w};
+                            // 32 dims: four chunks of one half of the head
+#pragma unroll
+                            for (int u = 0; u < 4; ++u)
+                                *reinterpret_cast<uint4 *>(dst + (quarter >> 1) * 1024 +
+                                                           ((((quarter & 1) * 4 + u) ^ row) << 4)) = int4x8_values(words[u]);
+                        } else {
+                            const int k = j * kBN + grp * 8 + row;
+                            const bool none = mixed && (k > w.pl || (k >= p.num_sinks && k < w.window_from(p, w.pf)));
+                            const bool some = mixed && (k > w.pf || (k >= p.num_sinks && k < w.window_from(p, w.pl)));
+#pragma unroll
+                            for (int u = 0; u < kParts; ++u) {
+                                uint32_t words[4] = {held[i][u].x, held[i][u].y, held[i][u].z, held[i][u].w};
+                                if (mixed) {
+#pragma unroll
+                                    for (int q4 = 0; q4 < 4; ++q4) {
+                                        // bytes that are NaN (there are no infinities)
+                                        const uint32_t nan = some ? __vcmpeq4(words[q4] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+                                        odd |= nan != 0 && !none;
+                                        words[q4] &= none ? 0u : ~nan;
+                                    }
+                                }
+                                // 16 dims: two chunks of half u of the head
+                                uint32_t v[8];
+#pragma unroll
+                                for (int q4 = 0; q4 < 4; ++q4) e4m3x4_to_h2x2(words[q4], v[2 * q4], v[2 * q4 + 1]);
+                                *reinterpret_cast<uint4 *>(dst + u * 1024 + (((quarter * 2) ^ row) << 4)) =
+                                    make_uint4(v[0], v[1], v[2], v[3]);
+                                *reinterpret_cast<uint4 *>(dst + u * 1024 + (((quarter * 2 + 1) ^ row) << 4)) =
+                                    make_uint4(v[4], v[5], v[6], v[7]);
+                            }
+                        }
+                        if (more) load(i, !is_v, ids);
+                    }
+                    if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[wi * kFlags + piece % kFlags] = 1;
+                    fence_proxy_async_shared();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar_full(slot));
+                }
+            }
+            if (dead && lane == 0) {
+                report(a.d_err, KV_DERR_TIMEOUT);
+                *abort_flag = 1;
+            }
+        }
+    } else {
+        // ============================================================ softmax and results
+        const int x = warp >> 2;                // chain
+        const int r = threadIdx.x & 127;        // query row in the tile = TMEM lane
+        const int tl = r / g, hh = r - tl * g;  // its token in the tile and head in the group
+        const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
+        const uint32_t t_s = trow + x * 128, t_o = trow + kColO + x * 128;
+        bool dead = false;
+        // waits are decided for the whole warp: its lanes take the warp-collective TMEM
+        // loads and stores together
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
+            return __all_sync(0xffffffffu, mbar_wait_sleep(b, parity));
+        };
+        int ns = 0, npv = 0, njoin = 0;  // phases taken of S, Pv, Join
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+            const int nt = w.nt;
+            const int tok0 = w.t0 + (nt == 2 ? x : 0) * TQ;         // first token of the row tile
+            const int nq = min(TQ, s.n - tok0);                     // its tokens (the tile exists)
+            const bool valid = tl < nq;
+            const int64_t token = s.q0 + tok0 + (valid ? tl : 0);
+            const int64_t row = token * a.num_q_heads + w.h * g + hh;
+            const int first_pos = w.pf + (nt == 2 ? x : 0) * TQ, last_pos = first_pos + nq - 1;  // of the tile, on the axis
+            const int pos = first_pos + (valid ? tl : 0);
+            const int klo = w.window_from(p, pos);
+            const bool warp_valid = __any_sync(0xffffffffu, valid);
+            float c2 = a.scale_log2;
+            if constexpr (kWide) {
+                // the row's queries, times the K scales and a power of two, into the tile (once, where both chains
+                // share it)
+                uint4 raw[D / 8];
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) + row * D);
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) raw[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
+                const float *ks = kCache == kCacheInt4 ? p.k_gscales + w.h * (D >> p.group_shift) : nullptr;
+                auto scale_of = [&](int i) { return kCache == kCacheInt4 ? ks[(8 * i) >> p.group_shift] : 1.f; };
+                float most = 0.f;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) {
+                    const float f = scale_of(i);
+                    const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 v = unpack2<QT>(u[e]);
+                        most = fmaxf(most, fmaxf(fabsf(v.x * f), fabsf(v.y * f)));
+                    }
+                }
+                // 2^up with 2^7 <= most * 2^up < 2^8, as far as floats go
+                const int exponent = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // (-127: 0 or subnormal)
+                const int up = most > 0.f && exponent < 128 ? min(max(7 - exponent, -100), 100) : 0;
+                const float factor = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
+                // (a scale that underflows, or of 0, as the least normal number: an unseen score of -inf times it
+                // has to stay -inf)
+                c2 = fmaxf(c2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), FLT_MIN);
+                if (piece > 0 && !wait_all(bar(kBarQEmpty), (piece - 1) & 1)) {  // the piece before has formed its last scores
+                    dead = true;
+                    break;
+                }
+                if (nt == 2 || x == 0) {
+                    uint8_t *dst = smem + (nt == 2 ? x * kTileBytes : 0) + r * 128;
+#pragma unroll
+                    for (int i = 0; i < D / 8; ++i) {
+                        const float f = scale_of(i);
+                        const uint32_t u[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
+                        float v[8];
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float2 v2 = unpack2<QT>(u[e]);
+                            v[2 * e] = v2.x * f * factor, v[2 * e + 1] = v2.y * f * factor;
+                        }
+                        const uint4 h8 = kCache == kCacheInt4
+                                             ? make_uint4(pack2<MT>(v[0], v[4]), pack2<MT>(v[1], v[5]), pack2<MT>(v[2], v[6]),
+                                                          pack2<MT>(v[3], v[7]))
+                                             : make_uint4(pack2<MT>(v[0], v[1]), pack2<MT>(v[2], v[3]), pack2<MT>(v[4], v[5]),
+                                                          pack2<MT>(v[6], v[7]));
+                        *reinterpret_cast<uint4 *>(dst + (i >> 3) * kHalf + (((i & 7) ^ (r & 7)) << 4)) = h8;
+                    }
+                    fence_proxy_async_shared();
+                }
+                mbar_arrive(bar(kBarQFull));
+            }
+            const float2 cc = make_float2(c2, c2);
+            float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
+            float2 sum = make_float2(0.f, 0.f);  // sum of the weights
+            const int step = nt == 2 ? 1 : 2;
+            const int first = w.ja + (nt == 2 ? 0 : x);
+            uint32_t wt[64];
+            for (int j = first; j < w.jb; j += step) {
+                if (!wait_all(bar(kBarS + x), ns & 1)) {
+                    dead = true;
+                    break;
+                }
+                ++ns;
+                tc_fence_after();
+                if (warp_valid) {  // (a warp without rows leaves its lanes of P as they are)
+                    if (w.mixed(p, j, first_pos, last_pos)) {
+                        // (scale > 0: an unseen score of -inf gets weight 0.  Apart from the pass below, whose
+                        // unrolled code the warps would fetch anew each time.)
+#pragma unroll 1
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t v[32];
+                            tmem_ld32_async(t_s + 32 * ch, v);
+                            tmem_wait_regs(v);
+                            const uint32_t seen = valid ? seen32(j * kBN + ch * 32, pos, klo, p.num_sinks) : 0u;
+#pragma unroll
+                            for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1 ? v[k] : 0xff800000u;
+                            tmem_st32u(t_s + 32 * ch, v);
+                        }
+                        tmem_wait_st();
+                    }
+                    float2 part_sum;
+                    // One pass over the tile's S: weights against the reference in use, the tile maximum
+                    // tracked alongside, 32 columns at a time with the next load in flight.  A second one
+                    // when the reference has to move.
+#pragma unroll 1
+                    for (bool again = false;; again = true) {
+                        const float nref = m_used == -INFINITY ? 0.f : kWeightLog2<MT> - m_used;
+                        const float2 ref2 = make_float2(nref, nref);
+                        float mraw = -INFINITY;
+                        part_sum = make_float2(0.f, 0.f);
+                        uint32_t buf[2][32];
+                        tmem_ld32_async(t_s, buf[0]);
+#pragma unroll
+                        for (int ch = 0; ch < 4; ++ch) {
+                            uint32_t(&v)[32] = buf[ch & 1];
+                            tmem_wait_regs(v);
+                            if (ch < 3) tmem_ld32_async(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) {
+                                const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
+                                const float2 e = fma2(make_float2(s0, s1), cc, ref2);
+                                const float2 x2 = make_float2(fast_exp2(e.x), fast_exp2(e.y));
+                                mraw = fmaxf(mraw, fmaxf(s0, s1));
+                                wt[ch * 16 + k] = pack2<MT>(x2.x, x2.y);
+                                part_sum = add2(part_sum, x2);
+                            }
+                        }
+                        if (again) break;
+                        // scale > 0, so the scaled maximum is the maximum of the scaled scores
+                        const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
+                        const bool moved = valid && mt > m_used + kRescaleLog2;  // also the first finite maximum
+                        if (!__any_sync(0xffffffffu, moved)) break;
+                        const bool rescale = moved && m_used != -INFINITY;  // O and the sums hold earlier tiles
+                        const float f = moved ? fast_exp2(m_used - mt) : 1.f;
+                        if (moved) {
+                            m_used = mt;
+                            sum.x *= f, sum.y *= f;
+                        }
+                        if (__any_sync(0xffffffffu, rescale)) {
+                            // the warp loads and stores O together; rows that keep their maximum scale by 1
+#pragma unroll 1
+                            for (int ch = 0; ch < D / 32; ++ch) {
+                                float o[32];
+                                tmem_ld32(t_o + ch * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= f;
+                                tmem_st32(t_o + ch * 32, o);
+                            }
+                            tmem_wait_st();
+                        }
+                    }
+                    sum = add2(sum, part_sum);
+                    // P_x into TMEM: 128 keys of 16-bit weights = 64 columns over the S_x just read
+                    tmem_st32u(t_s, wt);
+                    tmem_st32u(t_s + 32, wt + 32);
+                    tmem_wait_st();
+                }
+                tc_fence_before();
+                mbar_arrive(bar(kBarP + x));
+            }
+            if (dead) break;
+            if (first < w.jb && !wait_all(bar(kBarPv + x), npv++ & 1)) {  // the last product has landed
+                dead = true;
+                break;
+            }
+            tc_fence_after();
+            float m = m_used, l = sum.x + sum.y;
+            float f0 = 1.f, f1 = 0.f;  // weights of O_0 (O_x with two row tiles) and O_1 in the result
+            bool use1 = false;
+            if (nt == 1) {
+                if (x == 1) {
+                    // hand the maximum and sum to chain 0's thread of the same row, which joins the two
+                    join[r] = m;
+                    join[128 + r] = l;
+                    tc_fence_before();
+                    mbar_arrive(bar(kBarJoin));
+                    if (!wait_all(bar(kBarJoined), njoin++ & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    continue;
+                }
+                if (!wait_all(bar(kBarJoin), njoin++ & 1)) {
+                    dead = true;
+                    break;
+                }
+                tc_fence_after();
+                const float m1 = join[r], l1 = join[128 + r];
+                const float mm = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.f : fast_exp2(m - mm);
+                f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
+                use1 = w.jb - w.ja > 1;
+                m = mm;
+                // (no guard: a chain whose scores are all NaN has no maximum, hence weight 0, and a sum of NaN,
+                // which has to come through; an empty one has a sum of 0)
+                l = l * f0 + l1 * f1;
+            }
+            const float inv = l == 0.f ? 0.f : (kCache == kCacheE4M3 ? p.v_scale : 1.f) / l;
+            f0 *= inv;
+            f1 *= inv;
+            QT *out16 = static_cast<QT *>(a.out) + row * D;
+            const int prow = (nt == 2 ? x * 128 : 0) + r;
+            const int64_t slot = part_slot(c, w.ja == 0);
+            float4 *part = part_o<D>(p.t, slot, prow);
+            QT *rows[4];
+            if (w.whole) quad_rows<QT>(valid ? out16 : nullptr, rows);
+            if (warp_valid) {
+#pragma unroll 1
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float o[32];
+                    tmem_ld32(t_o + ch * 32, o);
+                    tmem_wait_ld();
+                    // a row of weight 0 in a chain has nothing there, whatever O holds
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = f0 != 0.f ? o[k] * f0 : 0.f;
+                    if (use1) {
+                        float o1[32];
+                        tmem_ld32(trow + kColO + 128 + ch * 32, o1);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) o[k] += f1 != 0.f ? o1[k] * f1 : 0.f;
+                    }
+                    if constexpr (kCache == kCacheInt4) {
+                        // times the V scales, the dims of each eight back in order
+                        const float *vs = p.v_gscales + w.h * (D >> p.group_shift);
+#pragma unroll
+                        for (int k8 = 0; k8 < 4; ++k8) {
+                            const float f = vs[(ch * 32 + 8 * k8) >> p.group_shift];
+                            float t[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) t[e] = o[8 * k8 + int4_place(e)] * f;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[8 * k8 + e] = t[e];
+                        }
+                    }
+                    if (w.whole) {
+                        store_rows<QT>(o, rows, ch * 32);
+                    } else if (valid) {
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            part[static_cast<int64_t>(ch * 8 + k) * p.t.rows_per_item] =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+                    }
+                }
+            }
+            if (nt == 1) {
+                tc_fence_before();
+                mbar_arrive(bar(kBarJoined));  // O_1 has been read
+            }
+            __syncwarp();  // (a row is written by the lanes of its quad)
+            if (valid) {
+                const float lse2 = l == 0.f ? -INFINITY : m + (log2f(l) - kWeightLog2<MT>);
+                if (!w.whole) *part_lse(p.t, slot, prow) = lse2;
+                else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
+                if constexpr (kCache != kCacheInt4) {
+                    if (odd_flag[piece % kFlags] | odd_flag[kFlags + piece % kFlags]) {
+                        const int ka = w.ja * kBN, kb = min(w.jb * kBN, w.pl + 1);
+                        const int edge = max(w.window_from(p, w.pf), p.num_sinks);
+                        float4 *mine = w.whole ? nullptr : part;
+                        if (a.window > 0)
+                            add_non_finite<QT, D, kCache>(p, w, max(ka, edge), min(min(w.window_from(p, w.pl), w.pf + 1), kb), pos,
+                                                          klo, out16, mine);
+                        add_non_finite<QT, D, kCache>(p, w, max(ka, w.pf + 1), kb, pos, klo, out16, mine);
+                    }
+                }
+            }
+        }
+        if (dead) {
+            if (lane == 0) report(a.d_err, KV_DERR_TIMEOUT);
+            *abort_flag = 1;
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 9)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
+}
+
+// The attention kernel and, with more than one share, the merge (launched as in tree_common.cuh).
+template <typename QT, int D, int kCache>
+static cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, const CUtensorMap &tv,
+                                const SinkPrefillParams &p, int dev, cudaStream_t stream) {
+    static std::atomic<bool> attr_set[64];
+    auto kernel = prefill_sinks_kernel<QT, D, kCache>;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    if (!attr_set[dev].load(std::memory_order_acquire)) {
+        const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, Tile<D>::kSmem);
+        if (e != cudaSuccess) return e;
+        attr_set[dev].store(true, std::memory_order_release);
+    }
+    const cudaError_t e = launch_dependent(kernel, dim3(p.t.workers), dim3(kThreads), Tile<D>::kSmem, stream, tq, tk, tv, p);
+    if (e != cudaSuccess || p.t.workers < 2) return e;
+    return launch_tree_merge<QT, D>(p.t, stream);
+}
+
+}  // namespace sinks
+
+// The launches over E4M3 and INT4 caches (prefill_sinks_wide.cu).
+cudaError_t launch_prefill_sinks_wide(const CUtensorMap &tmap, const SinkPrefillParams &p, int cache_dtype, int q_dtype,
+                                      int dev, cudaStream_t stream);
+
+}  // namespace pkv

@@ -521,6 +521,15 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_long_kernel(const __
     y.store<T, D>(p, sq, idx, rr, q);
 }
 
+// The merge, with more than one share.
+template <typename T, int D> static cudaError_t launch_tree_merge(const TreeParams &p, cudaStream_t stream) {
+    const int units = p.rows_per_item / 32 * (D / 8);
+    const int64_t items = static_cast<int64_t>(p.items_per_seq) * p.a.num_seqs;
+    if (items * kLongMerge <= p.workers)
+        return launch_dependent(tree_merge_long_kernel<T, D>, dim3(static_cast<unsigned>(items), units), dim3(256), 0, stream, p);
+    return launch_dependent(tree_merge_kernel<T, D>, dim3(p.workers - 1, units / 8), dim3(256), 0, stream, p);
+}
+
 // The attention kernel and, with more than one share, the merge.
 template <typename T, int D, typename Kernel>
 static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, std::atomic<bool> *attr_set,
@@ -541,11 +550,7 @@ static cudaError_t launch_tree_kernel(Kernel kernel, int threads, size_t smem, s
     // for the largest batches.
     const cudaError_t e = launch_dependent(kernel, dim3(p.workers), dim3(threads), smem, stream, tq, tk, tv, p);
     if (e != cudaSuccess || p.workers < 2) return e;
-    const int units = p.rows_per_item / 32 * (D / 8);
-    const int64_t items = static_cast<int64_t>(p.items_per_seq) * p.a.num_seqs;
-    if (items * kLongMerge <= p.workers)
-        return launch_dependent(tree_merge_long_kernel<T, D>, dim3(static_cast<unsigned>(items), units), dim3(256), 0, stream, p);
-    return launch_dependent(tree_merge_kernel<T, D>, dim3(p.workers - 1, units / 8), dim3(256), 0, stream, p);
+    return launch_tree_merge<T, D>(p, stream);
 }
 
 // Items of several kv heads (tree_packed.cu): the plan for `rows` query rows a head (heads_per_item

@@ -25,6 +25,8 @@ Same names as the C ABI:
     paged_attention_tree(...)        kv_paged_attention_tree
     paged_attention_decode_sinks(...)       kv_paged_attention_decode_sinks       (include/pagedkv_sinks.h)
     paged_attention_decode_sinks_int4(...)  kv_paged_attention_decode_sinks_int4
+    paged_attention_prefill_sinks(...)      kv_paged_attention_prefill_sinks
+    paged_attention_prefill_sinks_int4(...) kv_paged_attention_prefill_sinks_int4
 """
 from __future__ import annotations
 
@@ -146,6 +148,14 @@ def _load() -> ctypes.CDLL:
     lib.kv_paged_attention_decode_sinks_int4.argtypes = [P, i32, i32, i32, i32, P, P, i32, i32, i32, i32, P, i64, i32,
                                                          P, i32, f32, i32, i32, P, P, i32, i32, P, sz, P, P, P, P]
     lib.kv_paged_attention_decode_sinks_int4.restype = i32
+    lib.kv_paged_attention_prefill_sinks.argtypes = [P, i32, P, i32, i32, i32, i32, P, P, i32, i32, i32, i32, i32, P, i64,
+                                                     i32, P, i32, f32, i32, i32, f32, f32, i32, P, sz, P, P, P, P]
+    lib.kv_paged_attention_prefill_sinks.restype = i32
+    lib.kv_paged_attention_prefill_sinks_int4.argtypes = [P, i32, P, i32, i32, i32, i32, P, P, i32, i32, i32, i32, P, i64,
+                                                          i32, P, i32, f32, i32, i32, P, P, i32, i32, P, sz, P, P, P, P]
+    lib.kv_paged_attention_prefill_sinks_int4.restype = i32
+    lib.kv_paged_attention_prefill_sinks_workspace_size.argtypes = [i32] * 10
+    lib.kv_paged_attention_prefill_sinks_workspace_size.restype = sz
     lib.kv_status_string.argtypes = [i32]
     lib.kv_status_string.restype = ctypes.c_char_p
     lib.kv_last_error.argtypes = []
@@ -1069,3 +1079,88 @@ def paged_attention_decode_sinks_int4(q: torch.Tensor, k_cache: torch.Tensor, v_
         _refuse("k_scales and v_scales are needed")
     return _decode_sinks(q, k_cache, v_cache, block_table, seq_lens, max_seq_len, q_len, scale, window, num_sinks, 1.0, 1.0,
                          k_scales, v_scales, num_workers, workspace, out, lse_out, d_err, max_blocks_per_seq, stream)
+
+
+def paged_attention_prefill_sinks_workspace_size(num_seqs: int, max_query_len: int, num_q_heads: int, num_kv_heads: int,
+                                                 head_dim: int, cache_dtype: int, max_seq_len: int, window: int = 0,
+                                                 num_sinks: int = 0, num_workers: int = 0) -> int:
+    n = lib.kv_paged_attention_prefill_sinks_workspace_size(num_seqs, max_query_len, num_q_heads, num_kv_heads, head_dim,
+                                                            cache_dtype, max_seq_len, window, num_sinks, num_workers)
+    if n == SIZE_MAX:
+        raise KVError(KV_ERR_UNSUPPORTED, lib.kv_last_error().decode() or "invalid or unsupported sizes")
+    return int(n)
+
+
+def _prefill_sinks(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, max_seq_len, max_query_len, scale, window,
+                   num_sinks, k_scale, v_scale, k_scales, v_scales, num_workers, workspace, out, lse_out, d_err,
+                   max_blocks_per_seq, stream):
+    dev, dt = q.get_device(), q.dtype
+    if dev < 0 or q.dim() != 3 or not q.is_contiguous():
+        _refuse("q: contiguous [T, heads, D]; " + _DEVICES)
+    if stream is not None or dev != _current_device():
+        with torch.cuda.device(dev) if stream is None else _on(stream, dev):
+            return _prefill_sinks(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, max_seq_len, max_query_len,
+                                  scale, window, num_sinks, k_scale, v_scale, k_scales, v_scales, num_workers, workspace, out,
+                                  lse_out, d_err, max_blocks_per_seq, None)
+    T, Hq, D = q.shape
+    B = seq_lens.numel()
+    code, group = _cache_code(k_cache, v_cache, D, dev, k_scales, v_scales)
+    NB, bs, Hkv = k_cache.shape[:3]
+    if seq_lens.dtype is not _i32 or not seq_lens.is_contiguous() or seq_lens.get_device() != dev:
+        _refuse("seq_lens: contiguous int32 [B] on the same device")
+    if query_start_loc.dtype is not _i32 or not query_start_loc.is_contiguous() or query_start_loc.numel() != B + 1 or \
+            query_start_loc.get_device() != dev:
+        _refuse("query_start_loc: contiguous int32 [B + 1] on the same device")
+    if block_table.get_device() != dev:
+        _refuse(_DEVICES)
+    bt_stride, width = _table(block_table, B, max_blocks_per_seq)
+    out, lse, err = _outputs(q, out, lse_out, d_err, dev)
+    workspace = _scratch(workspace, lambda: paged_attention_prefill_sinks_workspace_size(
+        B, max_query_len, Hq, Hkv, D, code, max_seq_len, window, num_sinks, num_workers), dev, q)
+    head = (q.data_ptr(), _code_of.get(dt, -1), query_start_loc.data_ptr(), B, T, max_query_len, Hq, k_cache.data_ptr(),
+            v_cache.data_ptr())
+    tail = (num_workers, workspace.data_ptr(), workspace.numel() * workspace.element_size(), out.data_ptr(), lse, err,
+            _raw_stream(dev))
+    if k_scales is not None:
+        status = lib.kv_paged_attention_prefill_sinks_int4(
+            *head, Hkv, D, bs, NB, block_table.data_ptr(), bt_stride, width, seq_lens.data_ptr(), max_seq_len, scale, window,
+            num_sinks, k_scales.data_ptr(), v_scales.data_ptr(), group, *tail)
+    else:
+        status = lib.kv_paged_attention_prefill_sinks(
+            *head, code, Hkv, D, bs, NB, block_table.data_ptr(), bt_stride, width, seq_lens.data_ptr(), max_seq_len, scale,
+            window, num_sinks, k_scale, v_scale, *tail)
+    if status:
+        _check(status)
+    return out
+
+
+def paged_attention_prefill_sinks(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                  block_table: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                                  max_seq_len: int, max_query_len: int, scale: float, window: int = 0, num_sinks: int = 0,
+                                  k_scale: float = 1.0, v_scale: float = 1.0, num_workers: int = 0,
+                                  workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                  lse_out: Optional[torch.Tensor] = None, d_err: Optional[torch.Tensor] = None,
+                                  max_blocks_per_seq: Optional[int] = None, stream=None) -> torch.Tensor:
+    """kv_paged_attention_prefill_sinks: q [T, Hq, D] (rows of sequence b are query_start_loc[b] ..
+    query_start_loc[b+1]-1, its last positions); caches [NB, bs, Hkv, D], of q's type, or E4M3 with k_scale and
+    v_scale; block_table int32 [B, W]; seq_lens int32 [B] (including the new rows).  A workspace that is given
+    must hold paged_attention_prefill_sinks_workspace_size(...) bytes."""
+    return _prefill_sinks(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, max_seq_len, max_query_len, scale,
+                          window, num_sinks, k_scale, v_scale, None, None, num_workers, workspace, out, lse_out, d_err,
+                          max_blocks_per_seq, stream)
+
+
+def paged_attention_prefill_sinks_int4(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.Tensor,
+                                       block_table: torch.Tensor, seq_lens: torch.Tensor, query_start_loc: torch.Tensor,
+                                       max_seq_len: int, max_query_len: int, scale: float, k_scales: torch.Tensor,
+                                       v_scales: torch.Tensor, window: int = 0, num_sinks: int = 0, num_workers: int = 0,
+                                       workspace: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                                       lse_out: Optional[torch.Tensor] = None, d_err: Optional[torch.Tensor] = None,
+                                       max_blocks_per_seq: Optional[int] = None, stream=None) -> torch.Tensor:
+    """kv_paged_attention_prefill_sinks_int4: the same over INT4 caches, uint8 [NB, bs, Hkv, D / 2], with float32
+    scales [Hkv, D / group_size]; window 0 is full attention."""
+    if k_scales is None or v_scales is None:
+        _refuse("k_scales and v_scales are needed")
+    return _prefill_sinks(q, k_cache, v_cache, block_table, seq_lens, query_start_loc, max_seq_len, max_query_len, scale,
+                          window, num_sinks, 1.0, 1.0, k_scales, v_scales, num_workers, workspace, out, lse_out, d_err,
+                          max_blocks_per_seq, stream)

@@ -175,6 +175,6 @@ def check(got, want, tol, what):
     assert np.array_equal(got[inf], want[inf]), f"{what}: infinities of another sign"
     fine = np.isfinite(want)
     tol = np.broadcast_to(tol, want.shape)
-    over = np.abs(got - want)[fine] / tol[fine]
+    over = np.abs(got[fine] - want[fine]) / tol[fine]
     assert over.size == 0 or over.max() <= 1, f"{what}: {over.max():.3g} times its bound"
     return float(over.max(initial=0.0))
