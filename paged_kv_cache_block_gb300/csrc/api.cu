@@ -1582,6 +1582,8 @@ static kv_status prefill_sinks(const void *q, kv_dtype q_dtype, const int32_t *q
     if (c.block_size != 8 && c.block_size != 16 && c.block_size != 32)
         return fail(KV_ERR_UNSUPPORTED, "prefill: block_size must be 8, 16 or 32");
     const bool int4 = c.dtype == KV_INT4, fp8 = c.dtype == KV_FP8_E4M3;
+    if ((int4 || fp8) && static_cast<int64_t>(c.block_size) * c.num_kv_heads * c.head_dim > UINT32_MAX)
+        return fail(KV_ERR_UNSUPPORTED, "prefill: a block of the cache of more than 2^32 elements");
     const float scale_log2 = scale * (fp8 ? c.k_scale : 1.0f) * 1.4426950408889634f;
     if (!(scale >= 0.f) || !std::isfinite(scale_log2)) return fail(KV_ERR_INVALID_ARG, "scale must be finite and >= 0");
     if (num_seqs == 0 || num_tokens == 0 || max_query_len == 0) return ok();

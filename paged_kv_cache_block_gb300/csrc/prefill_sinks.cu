@@ -15,7 +15,7 @@ TreePlan plan_prefill_sinks(int max_query_len, int group, int head_dim, int num_
     t.tokens_per_tile = kTreeRows / group;
     t.key_shift = 7;
     t.rows_per_item = max_query_len > t.tokens_per_tile ? 2 * kTreeRows : kTreeRows;
-    t.smem_bytes = head_dim == 128 ? sinks::Tile<128>::kSmem : sinks::Tile<64>::kSmem;
+    t.smem_bytes = head_dim == 128 ? sinks::Tile<128>::smem(true) : sinks::Tile<64>::smem(false);  // (at most)
     const size_t parts = static_cast<size_t>(2) * t.workers * t.rows_per_item;
     t.lse_off = align256(2 * sizeof(int4) * static_cast<size_t>(t.workers));
     t.o_off = t.lse_off + align256(4 * parts);
