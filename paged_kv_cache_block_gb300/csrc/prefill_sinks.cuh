@@ -74,11 +74,11 @@ template <int D> struct Tile {
     static constexpr int kGroup = kHalves * 1024;       // 8 keys of a K or V tile: [64 dims of D][key][dim]
     static constexpr int kStages = D == 128 ? 4 : 8;    // ring entries (128 KB)
     static constexpr int kOffKV = 2 * kBytes;           // after Q_0, Q_1
-    static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // what the halves of a row exchange: 4 x 256 floats
-    static constexpr int kOffScratch = kOffJoin + 4 * 256 * 4;   // of the schedule
+    static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // chain 1's maxima and sums: 2 x 128 floats
+    static constexpr int kOffScratch = kOffJoin + 2 * 128 * 4;   // of the schedule
     static constexpr int kScratchBytes = 512;
     static constexpr int kOffBar = kOffScratch + kScratchBytes;
-    static constexpr int kNumBars = 12 + 2 * kStages;
+    static constexpr int kNumBars = 14 + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
     static constexpr int kOffUnits = (kOffMisc + 8 + 8 * kFlags + 4 * kStages + 15) / 16 * 16;  // kWide: codes
     static constexpr int smem(bool wide) { return kOffUnits + (wide ? kUnits * kUnitBytes : 0) + 1024; }  // + alignment
@@ -88,8 +88,8 @@ template <int D> struct Tile {
 };
 
 // mbarrier indices (+ x: one per chain)
-enum { kBarQFull = 0, kBarQEmpty = 1, kBarS = 2, kBarP = 4, kBarPv = 6, kBarPd = 8, kBarDrain = 10,
-       kBarKv = 12 };  // then KvFull[stages], KvEmpty[stages]
+enum { kBarQFull = 0, kBarQEmpty = 1, kBarS = 2, kBarP = 4, kBarPv = 6, kBarPd = 8, kBarJoin = 10,
+       kBarJoined = 11, kBarDrain = 12, kBarKv = 14 };  // then KvFull[stages], KvEmpty[stages]
 
 // A sequence's part of the work list.  Costs are counted in keys: pair i of a kv head costs
 //   c_i = min(keys up to its last token, cap) + item_cost
@@ -331,11 +331,11 @@ template <typename QT, int kCache> __device__ __forceinline__ float cache_value(
         return to_float<QT>(static_cast<const QT *>(cache)[at]);
 }
 
-// Add the non-finite values of V that a row sees among the axis's keys [k0, k1) to dims [d0, d1) of its written
-// result (out of type QT, or a partial result): they were zeroed for the products.  Rare, so plain.
+// Add the non-finite values of V that a row sees among the axis's keys [k0, k1) to its written result (out of
+// type QT, or a partial result): they were zeroed for the products.  Rare, so plain.
 template <typename QT, int D, int kCache>
 static __device__ __noinline__ void add_non_finite(const SinkPrefillParams &p, int seq, int h, int hidden, int k0, int k1,
-                                                   int pos, int klo, int d0, int d1, QT *out, float4 *part) {
+                                                   int pos, int klo, QT *out, float4 *part) {
     const TreeArgs &a = p.t.a;
     for (int k = k0; k < k1; ++k) {
         if (k > pos || (k < klo && k >= p.num_sinks)) continue;
@@ -343,7 +343,7 @@ static __device__ __noinline__ void add_non_finite(const SinkPrefillParams &p, i
         const int id = a.block_table[seq * a.bt_stride + (c < p.sink_blocks ? c : c + hidden)];
         if (id < 0 || id >= a.num_blocks) continue;
         const int64_t at = ((static_cast<int64_t>(id) * a.block_size + (k & (a.block_size - 1))) * a.num_kv_heads + h) * D;
-        for (int d = d0; d < d1; ++d) {
+        for (int d = 0; d < D; ++d) {
             const float f = cache_value<QT, kCache>(a.v_cache, at + d);
             if (isfinite(f)) continue;
             if (part) reinterpret_cast<float *>(part + static_cast<int64_t>(d / 4) * p.t.rows_per_item)[d % 4] += f;
@@ -369,25 +369,6 @@ __device__ __forceinline__ uint4 int4x8_values(uint32_t w) {
 }
 // Where dim d of each eight stands among such pairs, and the other way round.
 __host__ __device__ constexpr int int4_place(int d) { return d < 4 ? 2 * d : 2 * (d - 4) + 1; }
-
-// A barrier of two warps (64 threads), and one that tells whether any of them brought a true value.
-__device__ __forceinline__ void pair_sync(int id) {
-    __syncwarp();
-    asm volatile("bar.sync %0, 64;" ::"r"(id) : "memory");
-}
-__device__ __forceinline__ bool pair_any(int id, bool v) {
-    uint32_t any;
-    __syncwarp();
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t"
-        "setp.ne.u32 q, %2, 0;\n\t"
-        "bar.red.or.pred p, %1, 64, q;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(any)
-        : "r"(id), "r"(static_cast<uint32_t>(v))
-        : "memory");
-    return any != 0;
-}
 
 // 16 bytes from global to shared memory, asynchronously (zeros when !there); in groups, of which all but the
 // latest N are waited for.
@@ -444,11 +425,13 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
         mbar_init(bar(kBarQEmpty), 2);
         for (int x = 0; x < 2; ++x) {
             mbar_init(bar(kBarS + x), 1);
-            mbar_init(bar(kBarP + x), 256);
+            mbar_init(bar(kBarP + x), 128);
             mbar_init(bar(kBarPv + x), 1);
             mbar_init(bar(kBarPd + x), 1);
             mbar_init(bar(kBarDrain + x), 1);
         }
+        mbar_init(bar(kBarJoin), 128);
+        mbar_init(bar(kBarJoined), 128);
         for (int s = 0; s < kStages; ++s) {
             mbar_init(bar_full(s), kWide ? 2 : 1);
             mbar_init(bar_empty(s), kWide ? 2 : 3);  // released by both chains, and the cleaning warp
@@ -843,50 +826,39 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
         }
     } else {
         // ============================================================ softmax and results
-        // All eight warps take the two chains' tiles in turn, so that one chain's softmax overlaps the
-        // other's products: a row of S is shared by two threads, of warps w and w + 4, half of the keys (and
-        // of the result's dims) each.  Both keep the row's reference maximum; they have to talk only when
-        // one of them finds it exceeded.  The two warps' decisions to give up are taken together.
-        const int half = warp >> 2;
+        const int x = warp >> 2;                // chain
         const int r = threadIdx.x & 127;        // query row in the tile = TMEM lane
         const int tl = r / g, hh = r - tl * g;  // its token in the tile and head in the group
         const uint32_t trow = tmem + (static_cast<uint32_t>((warp & 3) * 32) << 16);
-        const int pair = 1 + (warp & 3);        // their barrier
-        float *mine = join + half * 128 + r, *other = join + (half ^ 1) * 128 + r;  // + 256 i: kind of exchange
-        auto wait_all = [&](uint32_t b, uint32_t parity) {  // (decided for the whole warp)
+        const uint32_t t_s = trow + x * 128, t_o = trow + kColO + x * 128;
+        bool dead = false;
+        // waits are decided for the whole warp: its lanes take the warp-collective TMEM
+        // loads and stores together
+        auto wait_all = [&](uint32_t b, uint32_t parity) {
             return __all_sync(0xffffffffu, mbar_wait_sleep(b, parity));
         };
-        struct Chain {
-            float m;        // the reference maximum of O and the sums, in log2 units
-            float c2;       // log2 e * scale of the row
-            float2 sum;     // of this half's weights
-            int ns;         // phases of S taken
-        };
-        Chain cur, alt;     // of the chain of this unit, and of the other one
-        cur.ns = alt.ns = 0;
-        cur.c2 = alt.c2 = a.scale_log2;
-        int npv0 = 0, npv1 = 0;  // phases of Pv taken
-        bool bad = false;
-        for (int piece = 0; w.next(p); ++piece) {
-            if (pair_any(pair, bad || *abort_flag != 0)) {
-                bad = true;
-                break;
-            }
+        int ns = 0, npv = 0, njoin = 0;  // phases taken of S, Pv, Join
+        for (int piece = 0; !dead && w.next(p); ++piece) {
+            const Seq s = w.cur;
+            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
             const int nt = w.nt;
-            const int n0 = w.cur.n - w.t0;  // tokens from the item's first on
-            auto offset = [&](int x) { return nt == 2 && x ? TQ : 0; };                      // first token of chain x's rows
-            auto tokens = [&](int x) { return min(TQ, n0 - offset(x)); };
-            const int64_t row0 = (static_cast<int64_t>(w.cur.q0) + w.t0 + tl) * a.num_q_heads + w.h * g + hh;  // of chain 0
-            const int64_t row1 = row0 + static_cast<int64_t>(offset(1)) * a.num_q_heads;
+            const int tok0 = w.t0 + (nt == 2 ? x : 0) * TQ;         // first token of the row tile
+            const int nq = min(TQ, s.n - tok0);                     // its tokens (the tile exists)
+            const bool valid = tl < nq;
+            const int64_t token = s.q0 + tok0 + (valid ? tl : 0);
+            const int64_t row = token * a.num_q_heads + w.h * g + hh;
+            const int first_pos = w.pf + (nt == 2 ? x : 0) * TQ, last_pos = first_pos + nq - 1;  // of the tile, on the axis
+            const int pos = first_pos + (valid ? tl : 0);
+            const int klo = w.window_from(p, pos);
+            const bool warp_valid = __any_sync(0xffffffffu, valid);
+            float c2 = a.scale_log2;
             if constexpr (kWide) {
-                // the row's queries, times the K scales and a power of two, into the tile: each half writes one row
-                // tile
-                const bool writes = nt == 2 || half == 0;
-                const bool there = writes && tl < tokens(half);
+                // the row's queries, times the K scales and a power of two, into the tile (once, where both chains
+                // share it)
                 uint4 raw[D / 8];
-                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) + (half ? row1 : row0) * D);
+                const uint4 *src = reinterpret_cast<const uint4 *>(static_cast<const QT *>(p.q) + row * D);
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) raw[i] = there ? src[i] : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < D / 8; ++i) raw[i] = valid ? src[i] : make_uint4(0, 0, 0, 0);
                 const float *ks = kCache == kCacheInt4 ? p.k_gscales + w.h * (D >> p.group_shift) : nullptr;
                 auto scale_of = [&](int i) { return kCache == kCacheInt4 ? ks[(8 * i) >> p.group_shift] : 1.f; };
                 float most = 0.f;
@@ -906,10 +878,13 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                 const float factor = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
                 // (a scale that underflows, or of 0, as the least normal number: an unseen score of -inf times it
                 // has to stay -inf)
-                const float c2 = fmaxf(a.scale_log2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), FLT_MIN);
-                if (piece > 0 && !wait_all(bar(kBarQEmpty), (piece - 1) & 1)) bad = true;  // the last scores before
-                if (writes) {
-                    uint8_t *dst = smem + half * kTileBytes + r * 128;
+                c2 = fmaxf(c2 * __uint_as_float(static_cast<uint32_t>(127 - up) << 23), FLT_MIN);
+                if (piece > 0 && !wait_all(bar(kBarQEmpty), (piece - 1) & 1)) {  // the piece before has formed its last scores
+                    dead = true;
+                    break;
+                }
+                if (nt == 2 || x == 0) {
+                    uint8_t *dst = smem + (nt == 2 ? x * kTileBytes : 0) + r * 128;
 #pragma unroll
                     for (int i = 0; i < D / 8; ++i) {
                         const float f = scale_of(i);
@@ -930,65 +905,55 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                     fence_proxy_async_shared();
                 }
                 mbar_arrive(bar(kBarQFull));
-                mine[256] = c2;
-                pair_sync(pair);
-                cur.c2 = half == 0 ? c2 : other[256];
-                alt.c2 = nt == 1 ? cur.c2 : (half == 0 ? other[256] : c2);
             }
-            cur.m = alt.m = -INFINITY;
-            cur.sum = alt.sum = make_float2(0.f, 0.f);
-            // a unit is a key tile of a chain, of both in turn
-            const int units = nt == 2 ? 2 * (w.jb - w.ja) : w.jb - w.ja;
-            bool quit = false;
-            for (int u = 0; u < units; ++u) {
-                const int x = u & 1, j = w.ja + (nt == 2 ? u >> 1 : u);
-                const int nq = tokens(x);
-                const bool valid = tl < nq;
-                const bool warp_valid = __any_sync(0xffffffffu, valid);
-                const uint32_t t_s = trow + x * 128, t_mine = t_s + half * 64;
-                const bool ok = wait_all(bar(kBarS + x), cur.ns & 1);
-                ++cur.ns;
+            const float2 cc = make_float2(c2, c2);
+            float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
+            float2 sum = make_float2(0.f, 0.f);  // sum of the weights
+            const int step = nt == 2 ? 1 : 2;
+            const int first = w.ja + (nt == 2 ? 0 : x);
+            uint32_t wt[64];
+            for (int j = first; j < w.jb; j += step) {
+                if (!wait_all(bar(kBarS + x), ns & 1)) {
+                    dead = true;
+                    break;
+                }
+                ++ns;
                 tc_fence_after();
-                const float c2 = cur.c2;
-                const float2 cc = make_float2(c2, c2);
-                if (ok && warp_valid) {  // (a warp without rows leaves its lanes of P as they are)
-                    const int first_pos = w.pf + offset(x);
-                    if (w.mixed(p, j, first_pos, first_pos + nq - 1)) {
-                        // (scale > 0: an unseen score of -inf gets weight 0)
-                        const int pos = first_pos + tl, klo = w.window_from(p, pos);
+                if (warp_valid) {  // (a warp without rows leaves its lanes of P as they are)
+                    if (w.mixed(p, j, first_pos, last_pos)) {
+                        // (scale > 0: an unseen score of -inf gets weight 0.  Apart from the pass below, whose
+                        // unrolled code the warps would fetch anew each time.)
 #pragma unroll 1
-                        for (int ch = 0; ch < 2; ++ch) {
-                            const uint32_t seen = valid ? seen32(j * kBN + half * 64 + ch * 32, pos, klo, p.num_sinks) : 0u;
+                        for (int ch = 0; ch < 4; ++ch) {
+                            const uint32_t seen = valid ? seen32(j * kBN + ch * 32, pos, klo, p.num_sinks) : 0u;
                             if (__all_sync(0xffffffffu, seen == ~0u)) continue;
                             uint32_t v[32];
-                            tmem_ld32_async(t_mine + 32 * ch, v);
+                            tmem_ld32_async(t_s + 32 * ch, v);
                             tmem_wait_regs(v);
 #pragma unroll
                             for (int k = 0; k < 32; ++k) v[k] = (seen >> k) & 1 ? v[k] : 0xff800000u;
-                            tmem_st32u(t_mine + 32 * ch, v);
+                            tmem_st32u(t_s + 32 * ch, v);
                         }
                         tmem_wait_st();
                     }
-                }
-                uint32_t wt[32];
-                float2 part_sum = make_float2(0.f, 0.f);
-                // One pass over this half of the tile's S: weights against the reference in use (0 at first), the
-                // half's maximum tracked alongside.  A second one when the reference has to move.
+                    float2 part_sum;
+                    // One pass over the tile's S: weights against the reference in use (0 at first), the tile
+                    // maximum tracked alongside, 32 columns at a time with the next load in flight.  A second one
+                    // when the reference has to move.
 #pragma unroll 1
-                for (bool again = false;; again = true) {
-                    const float ref = cur.m == -INFINITY ? 0.f : cur.m;
-                    float mraw = -INFINITY;
-                    if (ok && warp_valid) {
-                        const float nref = kWeightLog2<MT> - ref;
+                    for (bool again = false;; again = true) {
+                        const bool none = m_used == -INFINITY;  // no key seen so far
+                        const float nref = kWeightLog2<MT> - (none ? 0.f : m_used);
                         const float2 ref2 = make_float2(nref, nref);
+                        float mraw = -INFINITY;
                         part_sum = make_float2(0.f, 0.f);
                         uint32_t buf[2][32];
-                        tmem_ld32_async(t_mine, buf[0]);
+                        tmem_ld32_async(t_s, buf[0]);
 #pragma unroll
-                        for (int ch = 0; ch < 2; ++ch) {
+                        for (int ch = 0; ch < 4; ++ch) {
                             uint32_t(&v)[32] = buf[ch & 1];
                             tmem_wait_regs(v);
-                            if (ch < 1) tmem_ld32_async(t_mine + 32, buf[1]);
+                            if (ch < 3) tmem_ld32_async(t_s + 32 * (ch + 1), buf[(ch + 1) & 1]);
 #pragma unroll
                             for (int k = 0; k < 16; ++k) {
                                 const float s0 = __uint_as_float(v[2 * k]), s1 = __uint_as_float(v[2 * k + 1]);
@@ -999,175 +964,153 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                                 part_sum = add2(part_sum, x2);
                             }
                         }
-                    }
-                    if (again) {
-                        pair_sync(pair);  // both halves have read S, which P overwrites
-                        break;
-                    }
-                    // scale > 0, so the scaled maximum is the maximum of the scaled scores
-                    const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
-                    const bool first = cur.m == -INFINITY;  // no reference yet: 0, unless the maximum lies too far off
-                    const bool out_of = valid && (mt > ref + kAbove<MT> || (first && mt < -kBelow<MT>));
-                    // (behind this barrier both halves have read S, which P overwrites)
-                    if (!pair_any(pair, !ok || out_of)) {
-                        if (first) cur.m = 0.f;
-                        break;
-                    }
-                    if (pair_any(pair, !ok)) {
-                        quit = true;
-                        break;
-                    }
-                    *mine = mt;
-                    pair_sync(pair);
-                    const float both = fmaxf(mt, *other);
-                    float to = cur.m;
-                    if (valid) {
-                        if (first) to = both > kAbove<MT> || both < -kBelow<MT> ? both : 0.f;  // (-inf: nothing seen yet)
-                        else if (both > cur.m + kAbove<MT>) to = both;
-                    }
-                    const bool moved = !first && to != cur.m;  // O and the sums hold earlier tiles
-                    const float f = moved ? fast_exp2(cur.m - to) : 1.f;
-                    cur.sum.x *= f, cur.sum.y *= f;
-                    cur.m = to;
-                    if (__any_sync(0xffffffffu, moved)) {
-                        // the warp loads and stores its dims of O together; rows that keep their maximum scale by 1
-#pragma unroll 1
-                        for (int ch = 0; ch < D / 64; ++ch) {
-                            const uint32_t t_o = trow + kColO + x * 128 + half * (D / 2) + ch * 32;
-                            float o[32];
-                            tmem_ld32(t_o, o);
-                            tmem_wait_ld();
-#pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] *= f;
-                            tmem_st32(t_o, o);
+                        if (again) break;
+                        // scale > 0, so the scaled maximum is the maximum of the scaled scores
+                        const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
+                        bool moved = valid && mt > (none ? 0.f : m_used) + kAbove<MT>;
+                        if (none && mt != -INFINITY && !moved) {
+                            if (mt >= -kBelow<MT>) m_used = 0.f;
+                            else moved = valid;
                         }
-                        tmem_wait_st();
+                        if (!__any_sync(0xffffffffu, moved)) break;
+                        const bool rescale = moved && !none;  // O and the sums hold earlier tiles
+                        const float f = rescale ? fast_exp2(m_used - mt) : 1.f;
+                        if (moved) {
+                            m_used = mt;
+                            sum.x *= f, sum.y *= f;
+                        }
+                        if (__any_sync(0xffffffffu, rescale)) {
+                            // the warp loads and stores O together; rows that keep their maximum scale by 1
+#pragma unroll 1
+                            for (int ch = 0; ch < D / 32; ++ch) {
+                                float o[32];
+                                tmem_ld32(t_o + ch * 32, o);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int k = 0; k < 32; ++k) o[k] *= f;
+                                tmem_st32(t_o + ch * 32, o);
+                            }
+                            tmem_wait_st();
+                        }
                     }
-                    if (!pair_any(pair, (to == -INFINITY ? 0.f : to) != ref)) break;
-                }
-                if (quit) break;
-                cur.sum = add2(cur.sum, part_sum);
-                if (warp_valid) {
-                    // P_x into TMEM: 128 keys of 16-bit weights = 64 columns over the S_x just read, half of them here
-                    tmem_st32u(t_s + half * 32, wt);
+                    sum = add2(sum, part_sum);
+                    // P_x into TMEM: 128 keys of 16-bit weights = 64 columns over the S_x just read
+                    tmem_st32u(t_s, wt);
+                    tmem_st32u(t_s + 32, wt + 32);
                     tmem_wait_st();
                 }
                 tc_fence_before();
                 mbar_arrive(bar(kBarP + x));
-                const Chain t = cur;
-                cur = alt;
-                alt = t;
             }
-            if (quit) {
-                bad = true;
+            if (dead) break;
+            if (first < w.jb && !wait_all(bar(kBarPv + x), npv++ & 1)) {  // the last product has landed
+                dead = true;
                 break;
             }
-            // chain 0 and chain 1 again
-            if (units & 1) {
-                const Chain t = cur;
-                cur = alt;
-                alt = t;
-            }
-            // the sums of both halves
-            float l0 = cur.sum.x + cur.sum.y, l1 = alt.sum.x + alt.sum.y;
-            mine[512] = l0, mine[768] = l1;
-            pair_sync(pair);
-            l0 += other[512], l1 += other[768];
-            const bool two = nt == 2 || units > 1;  // chain 1 has had tiles
-            float m = cur.m, l = l0, f0 = 1.f, f1 = 0.f;  // f: weights of O_0 and O_1 in the result
+            tc_fence_after();
+            float m = m_used, l = sum.x + sum.y;
+            float f0 = 1.f, f1 = 0.f;  // weights of O_0 (O_x with two row tiles) and O_1 in the result
+            bool use1 = false;
             if (nt == 1) {
-                // chain 0's and chain 1's part of the keys.  (No guard: a chain whose scores are all NaN has a sum of
-                // NaN, which has to come through; one without keys has a sum of 0.)
-                const float mm = fmaxf(cur.m, alt.m);
-                f0 = cur.m == -INFINITY ? 0.f : fast_exp2(cur.m - mm);
-                f1 = alt.m == -INFINITY ? 0.f : fast_exp2(alt.m - mm);
-                m = mm;
-                l = l0 * f0 + l1 * f1;
-            }
-            const float top = kCache == kCacheE4M3 ? p.v_scale : 1.f;
-            const int64_t slot = part_slot(c, w.ja == 0);
-#pragma unroll 1
-            for (int x = 0; x < nt; ++x) {
-                if (x == 1) m = alt.m, l = l1;
-                // the last products have landed (a failed wait ends the CTA at the next piece, or below)
-                if (x == 0 && !wait_all(bar(kBarPv), npv0++ & 1)) bad = true;
-                if (x == nt - 1 && two && !wait_all(bar(kBarPv + 1), npv1++ & 1)) bad = true;
+                if (x == 1) {
+                    // hand the maximum and sum to chain 0's thread of the same row, which joins the two
+                    join[r] = m;
+                    join[128 + r] = l;
+                    tc_fence_before();
+                    mbar_arrive(bar(kBarJoin));
+                    if (!wait_all(bar(kBarJoined), njoin++ & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    tc_fence_after();
+                    continue;
+                }
+                if (!wait_all(bar(kBarJoin), njoin++ & 1)) {
+                    dead = true;
+                    break;
+                }
                 tc_fence_after();
-                const bool valid = tl < tokens(x) && !bad;
-                const float inv = l == 0.f ? 0.f : top / l;
-                const float a0 = f0 * inv, a1 = f1 * inv;
-                const int64_t row = x ? row1 : row0;
-                QT *out16 = static_cast<QT *>(a.out) + row * D;
-                const int prow = x * 128 + r;
-                float4 *part = part_o<D>(p.t, slot, prow);
-                QT *rows[4];
-                if (w.whole) quad_rows<QT>(valid ? out16 : nullptr, rows);
-                if (__any_sync(0xffffffffu, valid)) {
-                    const uint32_t t_o = trow + kColO + x * 128;
+                const float m1 = join[r], l1 = join[128 + r];
+                const float mm = fmaxf(m, m1);
+                f0 = m == -INFINITY ? 0.f : fast_exp2(m - mm);
+                f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
+                use1 = w.jb - w.ja > 1;
+                m = mm;
+                // (no guard: a chain whose scores are all NaN has no maximum, hence weight 0, and a sum of NaN,
+                // which has to come through; an empty one has a sum of 0)
+                l = l * f0 + l1 * f1;
+            }
+            const float inv = l == 0.f ? 0.f : (kCache == kCacheE4M3 ? p.v_scale : 1.f) / l;
+            f0 *= inv;
+            f1 *= inv;
+            QT *out16 = static_cast<QT *>(a.out) + row * D;
+            const int prow = (nt == 2 ? x * 128 : 0) + r;
+            const int64_t slot = part_slot(c, w.ja == 0);
+            float4 *part = part_o<D>(p.t, slot, prow);
+            QT *rows[4];
+            if (w.whole) quad_rows<QT>(valid ? out16 : nullptr, rows);
+            if (warp_valid) {
 #pragma unroll 1
-                    for (int ch = half * (D / 64); ch < (half + 1) * (D / 64); ++ch) {
-                        float o[32];
-                        tmem_ld32(t_o + ch * 32, o);
+                for (int ch = 0; ch < D / 32; ++ch) {
+                    float o[32];
+                    tmem_ld32(t_o + ch * 32, o);
+                    tmem_wait_ld();
+                    // a row of weight 0 in a chain has nothing there, whatever O holds
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) o[k] = f0 != 0.f ? o[k] * f0 : 0.f;
+                    if (use1) {
+                        float o1[32];
+                        tmem_ld32(trow + kColO + 128 + ch * 32, o1);
                         tmem_wait_ld();
-                        // a row of weight 0 in a chain has nothing there, whatever O holds
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] = a0 != 0.f ? o[k] * a0 : 0.f;
-                        if (nt == 1 && two) {
-                            float o1[32];
-                            tmem_ld32(t_o + 128 + ch * 32, o1);
-                            tmem_wait_ld();
+                        for (int k = 0; k < 32; ++k) o[k] += f1 != 0.f ? o1[k] * f1 : 0.f;
+                    }
+                    if constexpr (kCache == kCacheInt4) {
+                        // times the V scales, the dims of each eight back in order
+                        const float *vs = p.v_gscales + w.h * (D >> p.group_shift);
 #pragma unroll
-                            for (int k = 0; k < 32; ++k) o[k] += a1 != 0.f ? o1[k] * a1 : 0.f;
+                        for (int k8 = 0; k8 < 4; ++k8) {
+                            const float f = vs[(ch * 32 + 8 * k8) >> p.group_shift];
+                            float t[8];
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) t[e] = o[8 * k8 + int4_place(e)] * f;
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) o[8 * k8 + e] = t[e];
                         }
-                        if constexpr (kCache == kCacheInt4) {
-                            // times the V scales, the dims of each eight back in order
-                            const float *vs = p.v_gscales + w.h * (D >> p.group_shift);
+                    }
+                    if (w.whole) {
+                        store_rows<QT>(o, rows, ch * 32);
+                    } else if (valid) {
 #pragma unroll
-                            for (int k8 = 0; k8 < 4; ++k8) {
-                                const float f = vs[(ch * 32 + 8 * k8) >> p.group_shift];
-                                float t[8];
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) t[e] = o[8 * k8 + int4_place(e)] * f;
-#pragma unroll
-                                for (int e = 0; e < 8; ++e) o[8 * k8 + e] = t[e];
-                            }
-                        }
-                        if (w.whole) {
-                            store_rows<QT>(o, rows, ch * 32);
-                        } else if (valid) {
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                part[static_cast<int64_t>(ch * 8 + k) * p.t.rows_per_item] =
-                                    make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            part[static_cast<int64_t>(ch * 8 + k) * p.t.rows_per_item] =
+                                make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
                     }
                 }
-                __syncwarp();  // (a row is written by the lanes of its quad)
-                if (valid) {
-                    const float lse2 = l == 0.f ? -INFINITY : m + (log2f(l) - kWeightLog2<MT>);
-                    if (half == 0) {
-                        if (!w.whole) *part_lse(p.t, slot, prow) = lse2;
-                        else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
-                    }
-                    if constexpr (kCache != kCacheInt4) {
-                        if (odd_flag[piece % kFlags] | odd_flag[kFlags + piece % kFlags]) {
-                            const int pos = w.pf + offset(x) + tl, klo = w.window_from(p, pos);
-                            const int ka = w.ja * kBN, kb = min(w.jb * kBN, w.pl + 1);
-                            const int edge = max(w.window_from(p, w.pf), p.num_sinks);
-                            const int d0 = half * (D / 2), d1 = d0 + D / 2;
-                            float4 *mine_part = w.whole ? nullptr : part;
-                            if (a.window > 0)
-                                add_non_finite<QT, D, kCache>(p, w.seq, w.h, w.hidden, max(ka, edge),
-                                                              min(min(w.window_from(p, w.pl), w.pf + 1), kb), pos, klo, d0, d1,
-                                                              out16, mine_part);
-                            add_non_finite<QT, D, kCache>(p, w.seq, w.h, w.hidden, max(ka, w.pf + 1), kb, pos, klo, d0, d1, out16,
-                                                          mine_part);
-                        }
+            }
+            if (nt == 1) {
+                tc_fence_before();
+                mbar_arrive(bar(kBarJoined));  // O_1 has been read
+            }
+            __syncwarp();  // (a row is written by the lanes of its quad)
+            if (valid) {
+                const float lse2 = l == 0.f ? -INFINITY : m + (log2f(l) - kWeightLog2<MT>);
+                if (!w.whole) *part_lse(p.t, slot, prow) = lse2;
+                else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
+                if constexpr (kCache != kCacheInt4) {
+                    if (odd_flag[piece % kFlags] | odd_flag[kFlags + piece % kFlags]) {
+                        const int ka = w.ja * kBN, kb = min(w.jb * kBN, w.pl + 1);
+                        const int edge = max(w.window_from(p, w.pf), p.num_sinks);
+                        float4 *mine = w.whole ? nullptr : part;
+                        if (a.window > 0)
+                            add_non_finite<QT, D, kCache>(p, w.seq, w.h, w.hidden, max(ka, edge),
+                                                          min(min(w.window_from(p, w.pl), w.pf + 1), kb), pos, klo, out16, mine);
+                        add_non_finite<QT, D, kCache>(p, w.seq, w.h, w.hidden, max(ka, w.pf + 1), kb, pos, klo, out16, mine);
                     }
                 }
             }
         }
-        if (bad) {
+        if (dead) {
             if (lane == 0) report(a.d_err, KV_DERR_TIMEOUT);
             *abort_flag = 1;
         }
