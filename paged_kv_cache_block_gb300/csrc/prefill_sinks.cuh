@@ -61,12 +61,13 @@ namespace sinks {
 
 constexpr int kBM = kTreeRows;
 constexpr int kBN = 128;           // keys of a key tile
-constexpr int kThreads = 384;
+template <int kCache> constexpr int kThreads = kCache == kCache16 ? 384 : 512;
 constexpr uint32_t kColO = 256;
 
 // E4M3 and INT4 codes come to shared memory in units of 8 KB (an INT4 tile, half an E4M3 one), so many at a time.
 constexpr int kUnitBytes = 8192;
 constexpr int kUnits = 3;
+constexpr int kWideners = 6;       // warps that write them as fp16 tiles
 
 template <int D> struct Tile {
     static constexpr int kHalves = D / 64;
@@ -80,7 +81,7 @@ template <int D> struct Tile {
     static constexpr int kOffBar = kOffScratch + kScratchBytes;
     static constexpr int kNumBars = 14 + 2 * kStages;
     static constexpr int kOffMisc = kOffBar + kNumBars * 8;      // TMEM address, abort flag, flags, cleaned
-    static constexpr int kOffUnits = (kOffMisc + 8 + 8 * kFlags + 4 * kStages + 15) / 16 * 16;  // kWide: codes
+    static constexpr int kOffUnits = (kOffMisc + 8 + 4 * kWideners * kFlags + 4 * kStages + 15) / 16 * 16;  // kWide: codes
     static constexpr int smem(bool wide) { return kOffUnits + (wide ? kUnits * kUnitBytes : 0) + 1024; }  // + alignment
     // pieces whose V tiles can be in the ring at once, one more that the cleaning warp has begun,
     // and one without mixed tiles (only a share's last)
@@ -150,6 +151,7 @@ static_assert(sizeof(ShareScratch) <= 512, "Tile::kScratchBytes");
 
 // The share [x0, x1) of CTA c (x0 == x1: none) and an item's cost.  Computed by the whole block, with
 // scratch in shared memory; scratch.start is valid after the next __syncthreads.
+template <int kThreads>
 __device__ __forceinline__ void share_of_cta(const SinkPrefillParams &p, int c, int64_t &x0, int64_t &x1,
                                              int64_t &item_cost, ShareScratch &scratch) {
     static_assert(kThreads <= 16 * 32, "a word a warp");
@@ -390,7 +392,7 @@ __device__ __forceinline__ void fence_proxy_async_shared() {
 }
 
 template <typename QT, int D, int kCache>
-__global__ void __launch_bounds__(kThreads, 1)
+__global__ void __launch_bounds__(kThreads<kCache>, 1)
 prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_constant__ CUtensorMap tmap_k,
                      const __grid_constant__ CUtensorMap tmap_v, const __grid_constant__ SinkPrefillParams p) {
     using TL = Tile<D>;
@@ -408,8 +410,8 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + TL::kOffMisc);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + TL::kOffMisc + 4);
     // per piece, and per widening warp
-    volatile int *odd_flag = reinterpret_cast<volatile int *>(smem + TL::kOffMisc + 8);  // [2][kFlags]
-    int32_t *cleaned = reinterpret_cast<int32_t *>(smem + TL::kOffMisc + 8 + 8 * kFlags);  // [kStages]: entry + 1
+    volatile int *odd_flag = reinterpret_cast<volatile int *>(smem + TL::kOffMisc + 8);  // [kWideners][kFlags]
+    int32_t *cleaned = reinterpret_cast<int32_t *>(smem + TL::kOffMisc + 8 + 4 * kWideners * kFlags);  // [kStages]: entry + 1
     float *join = reinterpret_cast<float *>(smem + TL::kOffJoin);
     auto bar = [&](int i) { return smem_u32(&bars[i]); };
     auto bar_full = [&](int s) { return smem_u32(&bars[kBarKv + s]); };
@@ -433,11 +435,11 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
         mbar_init(bar(kBarJoin), 128);
         mbar_init(bar(kBarJoined), 128);
         for (int s = 0; s < kStages; ++s) {
-            mbar_init(bar_full(s), kWide ? 2 : 1);
+            mbar_init(bar_full(s), kWide ? kWideners : 1);
             mbar_init(bar_empty(s), kWide ? 2 : 3);  // released by both chains, and the cleaning warp
         }
         *abort_flag = 0;
-        for (int i = 0; i < 2 * kFlags; ++i) odd_flag[i] = 0;
+        for (int i = 0; i < kWideners * kFlags; ++i) odd_flag[i] = 0;
         for (int i = 0; i < kStages; ++i) cleaned[i] = 0;
         fence_barrier_init();
     }
@@ -451,381 +453,393 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
     int64_t x0, x1, item_cost;
     previous_kernel_done();
     let_next_kernel_launch();
-    share_of_cta(p, c, x0, x1, item_cost, scratch);
+    share_of_cta<kThreads<kCache>>(p, c, x0, x1, item_cost, scratch);
     zero_rejected<QT, D>(p);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tmem_holder;
-    Walk w;
-    w.start(scratch.start, x0, x1, item_cost);
 
     if (x0 == x1) {
         // no share: nothing but the record that says so
         if (threadIdx.x == 0) p.t.ws_first[2 * c] = make_int4(-1, 0, 0, 0);
-    } else if (!kWide && warp == 8) {
-        // ============================================================ TMA producer
-        const int bpt = kBN / bs;  // blocks of a key tile
-        const uint32_t q_bytes = static_cast<uint32_t>(TL::kHalves) * TQ * g * 128;
-        int entry = 0;  // ring entries filled
-        int piece = 0;
-        bool stop = false;
-        while (!stop && w.next(p)) {
-            const Seq s = w.cur;
-            if (piece == 0 && lane == 0) w.record(p, c);
-            // block ids of key tile j: lane l holds block j * bpt + l of the axis
-            const int nblk = (w.pl >> p.bs_shift) + 1;
-            auto entry_of = [&](int j) {  // (read before it is needed, checked when it is)
-                const int lb = j * bpt + lane;
-                return lane < bpt && lb < nblk ? a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + w.block(p, lb)]
-                                               : a.num_blocks;  // one past the pool: the copy reads zeros
-            };
-            int next_id = entry_of(w.ja);
-            bool ok = true;
-            if (lane == 0) {
-                // Q of the item, once the piece before has formed its last scores
-                if (piece > 0) ok = mbar_wait_sleep(bar(kBarQEmpty), (piece - 1) & 1);
-                if (ok) {
-                    mbar_arrive_expect_tx(bar(kBarQFull), w.nt * q_bytes);
-                    for (int x = 0; x < w.nt; ++x)
-                        for (int hf = 0; hf < TL::kHalves; ++hf)
-                            tma_load_3d(smem_u32(smem + x * kTileBytes + hf * kHalf), &tmap_q, bar(kBarQFull), 64 * hf,
-                                        w.h * g, s.q0 + w.t0 + x * TQ);
-                }
-            }
-            if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
+    } else if (warp >= 8) {
+        // (kWide: 512 threads start with 128 registers each, of which the softmax's two warpgroups take 168 and
+        // the others keep 88)
+        if constexpr (kWide) asm volatile("setmaxnreg.dec.sync.aligned.u32 88;");
+        Walk w;
+        w.start(scratch.start, x0, x1, item_cost);
+        if (!kWide && warp == 8) {
+            // ============================================================ TMA producer
+            const int bpt = kBN / bs;  // blocks of a key tile
+            const uint32_t q_bytes = static_cast<uint32_t>(TL::kHalves) * TQ * g * 128;
+            int entry = 0;  // ring entries filled
+            int piece = 0;
+            bool stop = false;
+            while (!stop && w.next(p)) {
+                const Seq s = w.cur;
+                if (piece == 0 && lane == 0) w.record(p, c);
+                // block ids of key tile j: lane l holds block j * bpt + l of the axis
+                const int nblk = (w.pl >> p.bs_shift) + 1;
+                auto entry_of = [&](int j) {  // (read before it is needed, checked when it is)
+                    const int lb = j * bpt + lane;
+                    return lane < bpt && lb < nblk ? a.block_table[static_cast<int64_t>(w.seq) * a.bt_stride + w.block(p, lb)]
+                                                   : a.num_blocks;  // one past the pool: the copy reads zeros
+                };
+                int next_id = entry_of(w.ja);
+                bool ok = true;
                 if (lane == 0) {
-                    report(a.d_err, KV_DERR_TIMEOUT);
-                    *abort_flag = 1;
+                    // Q of the item, once the piece before has formed its last scores
+                    if (piece > 0) ok = mbar_wait_sleep(bar(kBarQEmpty), (piece - 1) & 1);
+                    if (ok) {
+                        mbar_arrive_expect_tx(bar(kBarQFull), w.nt * q_bytes);
+                        for (int x = 0; x < w.nt; ++x)
+                            for (int hf = 0; hf < TL::kHalves; ++hf)
+                                tma_load_3d(smem_u32(smem + x * kTileBytes + hf * kHalf), &tmap_q, bar(kBarQFull), 64 * hf,
+                                            w.h * g, s.q0 + w.t0 + x * TQ);
+                    }
                 }
-                break;
-            }
-            ++piece;
-            for (int j = w.ja; j < w.jb && !stop; ++j) {
-                int my_id = next_id;
-                if (j + 1 < w.jb) next_id = entry_of(j + 1);
-                if (my_id < 0 || my_id > a.num_blocks || (my_id == a.num_blocks && lane < bpt && j * bpt + lane < nblk)) {
-                    report(a.d_err, KV_DERR_BAD_BLOCK);
-                    my_id = a.num_blocks;
-                }
-                for (int is_v = 0; is_v < 2; ++is_v) {
-                    const int slot = entry % kStages;
-                    int quit = 0;
+                if (!__shfl_sync(0xffffffffu, ok ? 1 : 0, 0)) {
                     if (lane == 0) {
-                        if (entry >= kStages && !mbar_wait_sleep(bar_empty(slot), (entry / kStages - 1) & 1)) {
-                            quit = 1;
-                            report(a.d_err, KV_DERR_TIMEOUT);
-                            *abort_flag = 1;
-                        } else if (*abort_flag) {
-                            quit = 1;
-                        }
-                        if (!quit) mbar_arrive_expect_tx(bar_full(slot), kTileBytes);
+                        report(a.d_err, KV_DERR_TIMEOUT);
+                        *abort_flag = 1;
                     }
-                    if (__shfl_sync(0xffffffffu, quit, 0)) {
-                        stop = true;
-                        break;
-                    }
-                    const CUtensorMap *m = is_v ? &tmap_v : &tmap_k;
-                    uint8_t *dst = smem + TL::kOffKV + slot * kTileBytes;
-                    for (int jb = 0; jb < bpt; ++jb) {
-                        const int id = __shfl_sync(0xffffffffu, my_id, jb);
-                        if (lane == 0)
-                            tma_load_5d(smem_u32(dst + jb * bs * TL::kHalves * 128), m, bar_full(slot), 0, 0,
-                                        w.h * TL::kHalves, 0, id);
-                    }
-                    ++entry;
-                }
-            }
-        }
-        // never leave with copies in flight into this CTA's shared memory
-        if (lane == 0) {
-            if (piece > 0 && !mbar_wait_sleep(bar(kBarQFull), (piece - 1) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
-            for (int i = max(0, entry - kStages); i < entry; ++i)
-                if (!mbar_wait_sleep(bar_full(i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
-        }
-    } else if (warp == 9 || warp == 10) {
-        // ============================================================ MMA issue, one lane a chain
-        // Chain x, key tile by key tile: S_x once the product that read the columns it overwrites has
-        // completed; O_x once the softmax has written P_x and the V tile has landed (and been
-        // cleaned).  The other chain's tiles are released as soon as they have landed: everyone who
-        // waits for a ring entry passes all of them in order, so that no phase of its barrier can be
-        // mistaken.
-        const int x = warp - 9;
-        constexpr uint32_t ab = AbFormat<MT>::value;
-        constexpr uint32_t idesc_s = mma_idesc(ab, false, kBM, kBN);
-        constexpr uint32_t idesc_pv = mma_idesc(ab, true, kBM, D);
-        if (lane == 0) {
-            const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, TL::kGroup);
-            const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), 1024, TL::kGroup);
-            const uint32_t t_s = tmem + x * 128, t_o = tmem + kColO + x * 128;
-            auto full = [&](int e) { return mbar_wait_bounded(bar_full(e % kStages), (e / kStages) & 1); };
-            int base = 0;  // key tiles of the pieces before
-            int npv = 0;   // products O_x committed
-            bool dead = false;
-            for (int piece = 0; !dead && w.next(p); ++piece) {
-                if (*abort_flag != 0) break;
-                if (!mbar_wait_bounded(bar(kBarQFull), piece & 1)) {
-                    dead = true;
                     break;
                 }
-                const int nt = w.nt;
-                const uint64_t dq = smem_desc(smem_u32(smem + (nt == 2 ? x * kTileBytes : 0)), 16, 1024);
-                const int step = nt == 2 ? 1 : 2;
-                const int first = w.ja + (nt == 2 ? 0 : x);
-                if (first >= w.jb) mbar_arrive(bar(kBarQEmpty));  // no tile for this chain
-                for (int j = w.ja; j < w.jb; ++j) {
-                    const bool last = j + step >= w.jb;
-                    const int ek = 2 * (base + j - w.ja), ev = ek + 1;
-                    const int sk = ek % kStages, sv = ev % kStages;
-                    if (nt == 1 && ((j - w.ja) & 1) != x) {
-                        bool landed = full(ek);
-                        if (landed) mbar_arrive(bar_empty(sk));
-                        landed = landed && full(ev);
-                        if (landed) mbar_arrive(bar_empty(sv));
-                        if (!landed) {
+                ++piece;
+                for (int j = w.ja; j < w.jb && !stop; ++j) {
+                    int my_id = next_id;
+                    if (j + 1 < w.jb) next_id = entry_of(j + 1);
+                    if (my_id < 0 || my_id > a.num_blocks || (my_id == a.num_blocks && lane < bpt && j * bpt + lane < nblk)) {
+                        report(a.d_err, KV_DERR_BAD_BLOCK);
+                        my_id = a.num_blocks;
+                    }
+                    for (int is_v = 0; is_v < 2; ++is_v) {
+                        const int slot = entry % kStages;
+                        int quit = 0;
+                        if (lane == 0) {
+                            if (entry >= kStages && !mbar_wait_sleep(bar_empty(slot), (entry / kStages - 1) & 1)) {
+                                quit = 1;
+                                report(a.d_err, KV_DERR_TIMEOUT);
+                                *abort_flag = 1;
+                            } else if (*abort_flag) {
+                                quit = 1;
+                            }
+                            if (!quit) mbar_arrive_expect_tx(bar_full(slot), kTileBytes);
+                        }
+                        if (__shfl_sync(0xffffffffu, quit, 0)) {
+                            stop = true;
+                            break;
+                        }
+                        const CUtensorMap *m = is_v ? &tmap_v : &tmap_k;
+                        uint8_t *dst = smem + TL::kOffKV + slot * kTileBytes;
+                        for (int jb = 0; jb < bpt; ++jb) {
+                            const int id = __shfl_sync(0xffffffffu, my_id, jb);
+                            if (lane == 0)
+                                tma_load_5d(smem_u32(dst + jb * bs * TL::kHalves * 128), m, bar_full(slot), 0, 0,
+                                            w.h * TL::kHalves, 0, id);
+                        }
+                        ++entry;
+                    }
+                }
+            }
+            // never leave with copies in flight into this CTA's shared memory
+            if (lane == 0) {
+                if (piece > 0 && !mbar_wait_sleep(bar(kBarQFull), (piece - 1) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+                for (int i = max(0, entry - kStages); i < entry; ++i)
+                    if (!mbar_wait_sleep(bar_full(i % kStages), (i / kStages) & 1)) report(a.d_err, KV_DERR_TIMEOUT);
+            }
+        } else if (warp == 9 || warp == 10) {
+            // ============================================================ MMA issue, one lane a chain
+            // Chain x, key tile by key tile: S_x once the product that read the columns it overwrites has
+            // completed; O_x once the softmax has written P_x and the V tile has landed (and been
+            // cleaned).  The other chain's tiles are released as soon as they have landed: everyone who
+            // waits for a ring entry passes all of them in order, so that no phase of its barrier can be
+            // mistaken.
+            const int x = warp - 9;
+            constexpr uint32_t ab = AbFormat<MT>::value;
+            constexpr uint32_t idesc_s = mma_idesc(ab, false, kBM, kBN);
+            constexpr uint32_t idesc_pv = mma_idesc(ab, true, kBM, D);
+            if (lane == 0) {
+                const uint64_t dkv = smem_desc(smem_u32(smem + TL::kOffKV), 16, TL::kGroup);
+                const uint64_t dv0 = smem_desc(smem_u32(smem + TL::kOffKV), 1024, TL::kGroup);
+                const uint32_t t_s = tmem + x * 128, t_o = tmem + kColO + x * 128;
+                auto full = [&](int e) { return mbar_wait_bounded(bar_full(e % kStages), (e / kStages) & 1); };
+                int base = 0;  // key tiles of the pieces before
+                int npv = 0;   // products O_x committed
+                bool dead = false;
+                for (int piece = 0; !dead && w.next(p); ++piece) {
+                    if (*abort_flag != 0) break;
+                    if (!mbar_wait_bounded(bar(kBarQFull), piece & 1)) {
+                        dead = true;
+                        break;
+                    }
+                    const int nt = w.nt;
+                    const uint64_t dq = smem_desc(smem_u32(smem + (nt == 2 ? x * kTileBytes : 0)), 16, 1024);
+                    const int step = nt == 2 ? 1 : 2;
+                    const int first = w.ja + (nt == 2 ? 0 : x);
+                    if (first >= w.jb) mbar_arrive(bar(kBarQEmpty));  // no tile for this chain
+                    for (int j = w.ja; j < w.jb; ++j) {
+                        const bool last = j + step >= w.jb;
+                        const int ek = 2 * (base + j - w.ja), ev = ek + 1;
+                        const int sk = ek % kStages, sv = ev % kStages;
+                        if (nt == 1 && ((j - w.ja) & 1) != x) {
+                            bool landed = full(ek);
+                            if (landed) mbar_arrive(bar_empty(sk));
+                            landed = landed && full(ev);
+                            if (landed) mbar_arrive(bar_empty(sv));
+                            if (!landed) {
+                                dead = true;
+                                break;
+                            }
+                            continue;
+                        }
+                        if ((npv > 0 && !mbar_wait_bounded(bar(kBarPd + x), (npv - 1) & 1)) || !full(ek)) {
                             dead = true;
                             break;
                         }
-                        continue;
-                    }
-                    if ((npv > 0 && !mbar_wait_bounded(bar(kBarPd + x), (npv - 1) & 1)) || !full(ek)) {
-                        dead = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t dk = dkv + static_cast<uint64_t>((sk * kTileBytes) >> 4);
+                        tc_fence_after();
+                        const uint64_t dk = dkv + static_cast<uint64_t>((sk * kTileBytes) >> 4);
 #pragma unroll
-                    for (int k = 0; k < D / 16; ++k) {
-                        const int in = (k & 3) * 32;
-                        mma_f16(t_s, dq + (((k >> 2) * kHalf + in) >> 4), dk + (((k >> 2) * 1024 + in) >> 4), idesc_s, k > 0);
-                    }
-                    mma_commit(bar(kBarS + x));
-                    mma_commit(bar_empty(sk));
-                    if (last) mma_commit(bar(kBarQEmpty));
-                    if (!full(ev) || (!kWide && w.mixed(p, j) && !wait_at_least_bounded(&cleaned[sv], ev + 1)) ||
-                        !mbar_wait_bounded(bar(kBarP + x), npv & 1)) {
-                        dead = true;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint64_t dv = dv0 + static_cast<uint64_t>((sv * kTileBytes) >> 4);
-#pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2 * TL::kGroup) >> 4), idesc_pv, j > first || k > 0);
-                    mma_commit(bar(kBarPd + x));
-                    mma_commit(bar_empty(sv));
-                    if (last) mma_commit(bar(kBarPv + x));
-                    ++npv;
-                }
-                base += w.jb - w.ja;
-            }
-            if (dead) {
-                report(a.d_err, KV_DERR_TIMEOUT);
-                *abort_flag = 1;
-            }
-            // every MMA this lane issued has completed before TMEM is freed
-            mma_commit(bar(kBarDrain + x));
-            if (!mbar_wait_bounded(bar(kBarDrain + x), 0)) report(a.d_err, KV_DERR_TIMEOUT);
-        }
-        __syncwarp();
-    } else if (!kWide && warp == 11) {
-        // ============================================================ cleaning of V tiles
-        int base = 0;
-        bool dead = false;
-        for (int piece = 0; !dead && w.next(p); ++piece) {
-            if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-            if (lane == 0) odd_flag[piece % kFlags] = 0;
-            __syncwarp();
-            for (int e = 0; e < 2 * (w.jb - w.ja); ++e) {
-                const int j = w.ja + (e >> 1);
-                const int ev = 2 * base + e, sv = ev % kStages;
-                if (!__all_sync(0xffffffffu, mbar_wait_sleep(bar_full(sv), (ev / kStages) & 1))) {
-                    dead = true;
-                    break;
-                }
-                if (!(e & 1) || !w.mixed(p, j)) {
-                    if (lane == 0) mbar_arrive(bar_empty(sv));
-                    continue;
-                }
-                const uint32_t tile = smem_u32(smem + TL::kOffKV + sv * kTileBytes);
-                const int k0 = j * kBN;
-                bool odd = false;
-                auto clean = [&](int lo, int hi, bool zero) {
-                    lo = max(lo, k0) - k0;
-                    hi = min(hi, k0 + kBN) - k0;
-                    for (int i = lo * 8 + lane; i < hi * 8; i += 32)
-                        for (int hf = 0; hf < TL::kHalves; ++hf)
-                            clean_chunk<MT>(tile + (i >> 6) * TL::kGroup + hf * 1024 + (i & 63) * 16, zero, odd);
-                };
-                // keys no row sees: between the sinks and the first row's window, and behind the last row;
-                // keys some rows do not see: up to the last row's window, and the item's own behind its first
-                const int from = max(w.window_from(p, w.pf), p.num_sinks), to = w.window_from(p, w.pl);
-                if (a.window > 0) {
-                    clean(p.num_sinks, w.window_from(p, w.pf), true);
-                    clean(from, min(to, w.pf + 1), false);
-                }
-                clean(w.pf + 1, w.pl + 1, false);
-                clean(w.pl + 1, ((w.pl >> p.bs_shift) + 1) << p.bs_shift, true);
-                if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[piece % kFlags] = 1;
-                fence_proxy_async_shared();
-                __syncwarp();
-                if (lane == 0) {
-                    st_release_cta(&cleaned[sv], ev + 1);
-                    mbar_arrive(bar_empty(sv));
-                }
-                __syncwarp();
-            }
-            base += w.jb - w.ja;
-        }
-        if (dead && lane == 0) {
-            report(a.d_err, KV_DERR_TIMEOUT);
-            *abort_flag = 1;
-        }
-    } else if (kWide && (warp == 8 || warp == 11)) {
-        // ============================================================ codes to fp16 tiles
-        // Each of the two warps takes every second group of 8 keys; lane l holds 16 bytes of key l & 7 (E4M3:
-        // 16 of each half of it).  A lane fetches what it will convert itself, two units ahead.
-        if constexpr (kWide) {
-            constexpr int kRow = kCache == kCacheInt4 ? D / 2 : D;  // bytes of a key of a head
-            constexpr int kParts = kRow / 64;                       // 64-byte parts of it = units of a tile
-            constexpr int kGroups = kBN / 16 / kParts;              // of a unit, for a warp
-            const int wi = warp == 8 ? 0 : 1;
-            const int bpt = kBN / bs;
-            const int row = lane & 7, quarter = lane >> 3;
-            const uint32_t token = static_cast<uint32_t>(a.num_kv_heads) * kRow;  // bytes of a slot,
-            const uint32_t block = token << p.bs_shift;                           // and of a block (below 2^32)
-            uint8_t *codes = smem + TL::kOffUnits + wi * (kUnitBytes / 2) + lane * 16;
-            // ---- the fetching side: its own walk over the units
-            Walk f = w;
-            int fj = 0, fpart = 0, fslot = 0;  // key tile, unit of its K (below kParts) and V, place
-            int ids = -1, next_ids = -1;       // lane l: block l of tiles fj and fj + 1 (-1: zeros)
-            bool more = f.next(p);
-            int64_t at = 0;                    // this lane's bytes of a block's first key
-            auto load_ids = [&](int j) {
-                const int lb = j * bpt + lane;
-                if (lane >= bpt || lb > f.pl >> p.bs_shift) return -1;
-                const int e = a.block_table[static_cast<int64_t>(f.seq) * a.bt_stride + f.block(p, lb)];
-                if (e >= 0 && e < a.num_blocks) return e;
-                if (wi == 0) report(a.d_err, KV_DERR_BAD_BLOCK);
-                return -1;
-            };
-            auto begin = [&]() {  // a piece
-                fj = f.ja, fpart = 0;
-                ids = load_ids(fj);
-                at = f.h * kRow + quarter * 16 + static_cast<int64_t>(row) * token;
-            };
-            auto fetch = [&]() {
-                if (more) {
-                    if (fpart == 0 && fj + 1 < f.jb) next_ids = load_ids(fj + 1);
-                    const bool is_v = fpart >= kParts;
-                    const int base = is_v ? fpart - kParts : fpart;
-                    const uint8_t *mine = static_cast<const uint8_t *>(is_v ? a.v_cache : p.k_cache) + at;
-                    const uint32_t dst = smem_u32(codes + fslot * kUnitBytes);
-#pragma unroll
-                    for (int i = 0; i < kGroups; ++i) {
-                        const int k = (2 * (base * kGroups + i) + wi) * 8;  // first key of the group, in the tile
-                        const int id = __shfl_sync(0xffffffffu, ids, k >> p.bs_shift);
-                        const uint8_t *src = mine + (k & (bs - 1)) * token + static_cast<uint64_t>(static_cast<uint32_t>(max(id, 0))) * block;
-#pragma unroll
-                        for (int u = 0; u < kParts; ++u) copy16_async(dst + (i * kParts + u) * 512, src + 64 * u, id >= 0);
-                    }
-                    if (++fpart == 2 * kParts) {
-                        fpart = 0;
-                        ids = next_ids;
-                        if (++fj == f.jb) {
-                            more = f.next(p);
-                            if (more) begin();
+                        for (int k = 0; k < D / 16; ++k) {
+                            const int in = (k & 3) * 32;
+                            mma_f16(t_s, dq + (((k >> 2) * kHalf + in) >> 4), dk + (((k >> 2) * 1024 + in) >> 4), idesc_s, k > 0);
                         }
-                    }
-                }
-                copies_commit();
-                if (++fslot == kUnits) fslot = 0;
-            };
-            if (more) begin();
+                        mma_commit(bar(kBarS + x));
+                        mma_commit(bar_empty(sk));
+                        if (last) mma_commit(bar(kBarQEmpty));
+                        if (!full(ev) || (!kWide && w.mixed(p, j) && !wait_at_least_bounded(&cleaned[sv], ev + 1)) ||
+                            !mbar_wait_bounded(bar(kBarP + x), npv & 1)) {
+                            dead = true;
+                            break;
+                        }
+                        tc_fence_after();
+                        const uint64_t dv = dv0 + static_cast<uint64_t>((sv * kTileBytes) >> 4);
 #pragma unroll
-            for (int i = 0; i < kUnits - 1; ++i) fetch();
-            // ---- the converting side
-            int entry = 0, cslot = 0;
+                        for (int k = 0; k < 8; ++k)
+                            mma_f16_ts(t_o, t_s + k * 8, dv + ((k * 2 * TL::kGroup) >> 4), idesc_pv, j > first || k > 0);
+                        mma_commit(bar(kBarPd + x));
+                        mma_commit(bar_empty(sv));
+                        if (last) mma_commit(bar(kBarPv + x));
+                        ++npv;
+                    }
+                    base += w.jb - w.ja;
+                }
+                if (dead) {
+                    report(a.d_err, KV_DERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+                // every MMA this lane issued has completed before TMEM is freed
+                mma_commit(bar(kBarDrain + x));
+                if (!mbar_wait_bounded(bar(kBarDrain + x), 0)) report(a.d_err, KV_DERR_TIMEOUT);
+            }
+            __syncwarp();
+        } else if (!kWide && warp == 11) {
+            // ============================================================ cleaning of V tiles
+            int base = 0;
             bool dead = false;
             for (int piece = 0; !dead && w.next(p); ++piece) {
                 if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-                if (piece == 0 && wi == 0 && lane == 0) w.record(p, c);
-                if (lane == 0) odd_flag[wi * kFlags + piece % kFlags] = 0;
+                if (lane == 0) odd_flag[piece % kFlags] = 0;
                 __syncwarp();
-                for (int e = 0; e < 2 * (w.jb - w.ja); ++e, ++entry) {
+                for (int e = 0; e < 2 * (w.jb - w.ja); ++e) {
                     const int j = w.ja + (e >> 1);
-                    const bool is_v = e & 1;
-                    const int slot = entry % kStages;
-                    if (entry >= kStages &&
-                        !__all_sync(0xffffffffu, mbar_wait_sleep(bar_empty(slot), (entry / kStages - 1) & 1))) {
+                    const int ev = 2 * base + e, sv = ev % kStages;
+                    if (!__all_sync(0xffffffffu, mbar_wait_sleep(bar_full(sv), (ev / kStages) & 1))) {
                         dead = true;
                         break;
                     }
-                    if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
-                    uint8_t *tile = smem + TL::kOffKV + slot * kTileBytes + row * 128;
-                    const bool mixed = kCache == kCacheE4M3 && is_v && w.mixed(p, j);
-                    bool odd = false;
-#pragma unroll 1
-                    for (int part = 0; part < kParts; ++part) {
-                        fetch();  // (into the place of the unit before this one)
-                        copies_wait<kUnits - 1>();
-                        const uint8_t *unit = codes + cslot * kUnitBytes;
-                        if (++cslot == kUnits) cslot = 0;
-#pragma unroll
-                        for (int i = 0; i < kGroups; ++i) {
-                            const int grp = 2 * (part * kGroups + i) + wi;
-                            uint8_t *dst = tile + grp * TL::kGroup;
-                            if constexpr (kCache == kCacheInt4) {
-                                const uint4 held = *reinterpret_cast<const uint4 *>(unit + i * 512);
-                                const uint32_t words[4] = {held.x, held.y, held.z, held.w};
-                                // 32 dims: four chunks of one half of the head
-#pragma unroll
-                                for (int u = 0; u < 4; ++u)
-                                    *reinterpret_cast<uint4 *>(dst + (quarter >> 1) * 1024 +
-                                                               ((((quarter & 1) * 4 + u) ^ row) << 4)) = int4x8_values(words[u]);
-                            } else {
-                                const int k = j * kBN + grp * 8 + row;
-                                const bool none = mixed && (k > w.pl || (k >= p.num_sinks && k < w.window_from(p, w.pf)));
-                                const bool some = mixed && (k > w.pf || (k >= p.num_sinks && k < w.window_from(p, w.pl)));
-#pragma unroll
-                                for (int u = 0; u < kParts; ++u) {
-                                    const uint4 held = *reinterpret_cast<const uint4 *>(unit + (i * kParts + u) * 512);
-                                    uint32_t words[4] = {held.x, held.y, held.z, held.w};
-                                    if (mixed) {
-#pragma unroll
-                                        for (int q4 = 0; q4 < 4; ++q4) {
-                                            // bytes that are NaN (there are no infinities)
-                                            const uint32_t nan = some ? __vcmpeq4(words[q4] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
-                                            odd |= nan != 0 && !none;
-                                            words[q4] &= none ? 0u : ~nan;
-                                        }
-                                    }
-                                    // 16 dims: two chunks of half u of the head
-                                    uint32_t v[8];
-#pragma unroll
-                                    for (int q4 = 0; q4 < 4; ++q4) e4m3x4_to_h2x2(words[q4], v[2 * q4], v[2 * q4 + 1]);
-                                    *reinterpret_cast<uint4 *>(dst + u * 1024 + (((quarter * 2) ^ row) << 4)) =
-                                        make_uint4(v[0], v[1], v[2], v[3]);
-                                    *reinterpret_cast<uint4 *>(dst + u * 1024 + (((quarter * 2 + 1) ^ row) << 4)) =
-                                        make_uint4(v[4], v[5], v[6], v[7]);
-                                }
-                            }
-                        }
+                    if (!(e & 1) || !w.mixed(p, j)) {
+                        if (lane == 0) mbar_arrive(bar_empty(sv));
+                        continue;
                     }
-                    if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[wi * kFlags + piece % kFlags] = 1;
+                    const uint32_t tile = smem_u32(smem + TL::kOffKV + sv * kTileBytes);
+                    const int k0 = j * kBN;
+                    bool odd = false;
+                    auto clean = [&](int lo, int hi, bool zero) {
+                        lo = max(lo, k0) - k0;
+                        hi = min(hi, k0 + kBN) - k0;
+                        for (int i = lo * 8 + lane; i < hi * 8; i += 32)
+                            for (int hf = 0; hf < TL::kHalves; ++hf)
+                                clean_chunk<MT>(tile + (i >> 6) * TL::kGroup + hf * 1024 + (i & 63) * 16, zero, odd);
+                    };
+                    // keys no row sees: between the sinks and the first row's window, and behind the last row;
+                    // keys some rows do not see: up to the last row's window, and the item's own behind its first
+                    const int from = max(w.window_from(p, w.pf), p.num_sinks), to = w.window_from(p, w.pl);
+                    if (a.window > 0) {
+                        clean(p.num_sinks, w.window_from(p, w.pf), true);
+                        clean(from, min(to, w.pf + 1), false);
+                    }
+                    clean(w.pf + 1, w.pl + 1, false);
+                    clean(w.pl + 1, ((w.pl >> p.bs_shift) + 1) << p.bs_shift, true);
+                    if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[piece % kFlags] = 1;
                     fence_proxy_async_shared();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(bar_full(slot));
+                    if (lane == 0) {
+                        st_release_cta(&cleaned[sv], ev + 1);
+                        mbar_arrive(bar_empty(sv));
+                    }
+                    __syncwarp();
                 }
+                base += w.jb - w.ja;
             }
-            copies_wait<0>();  // never leave with copies in flight into this CTA's shared memory
             if (dead && lane == 0) {
                 report(a.d_err, KV_DERR_TIMEOUT);
                 *abort_flag = 1;
             }
+        } else if (kWide && warp >= 8) {
+            // ============================================================ codes to fp16 tiles
+            // Each of the six warps takes every sixth group of 8 keys; lane l holds 16 bytes of key l & 7 (E4M3:
+            // 16 of each half of it).  A lane fetches what it will convert itself, two units ahead.
+            if constexpr (kWide) {
+                constexpr int kRow = kCache == kCacheInt4 ? D / 2 : D;  // bytes of a key of a head
+                constexpr int kParts = kRow / 64;                       // 64-byte parts of it = units of a tile
+                constexpr int kAll = kBN / 8 / kParts;                  // groups of a unit,
+                constexpr int kGroups = (kAll + kWideners - 1) / kWideners;  // of a warp at most
+                const int wi = warp == 8 ? 0 : warp - 10;
+                const int bpt = kBN / bs;
+                const int row = lane & 7, quarter = lane >> 3;
+                const uint32_t token = static_cast<uint32_t>(a.num_kv_heads) * kRow;  // bytes of a slot,
+                const uint32_t block = token << p.bs_shift;                           // and of a block (below 2^32)
+                uint8_t *codes = smem + TL::kOffUnits + lane * 16;
+                // ---- the fetching side: its own walk over the units
+                Walk f = w;
+                int fj = 0, fpart = 0, fslot = 0;  // key tile, unit of its K (below kParts) and V, place
+                int ids = -1, next_ids = -1;       // lane l: block l of tiles fj and fj + 1 (-1: zeros)
+                bool more = f.next(p);
+                int64_t at = 0;                    // this lane's bytes of a block's first key
+                auto load_ids = [&](int j) {
+                    const int lb = j * bpt + lane;
+                    if (lane >= bpt || lb > f.pl >> p.bs_shift) return -1;
+                    const int e = a.block_table[static_cast<int64_t>(f.seq) * a.bt_stride + f.block(p, lb)];
+                    if (e >= 0 && e < a.num_blocks) return e;
+                    if (wi == 0) report(a.d_err, KV_DERR_BAD_BLOCK);
+                    return -1;
+                };
+                auto begin = [&]() {  // a piece
+                    fj = f.ja, fpart = 0;
+                    ids = load_ids(fj);
+                    at = f.h * kRow + quarter * 16 + static_cast<int64_t>(row) * token;
+                };
+                auto fetch = [&]() {
+                    if (more) {
+                        if (fpart == 0 && fj + 1 < f.jb) next_ids = load_ids(fj + 1);
+                        const bool is_v = fpart >= kParts;
+                        const int base = is_v ? fpart - kParts : fpart;
+                        const uint8_t *mine = static_cast<const uint8_t *>(is_v ? a.v_cache : p.k_cache) + at;
+                        const uint32_t dst = smem_u32(codes + fslot * kUnitBytes);
+#pragma unroll
+                        for (int i = 0; i < kGroups; ++i) {
+                            const int grp = i * kWideners + wi;          // of the unit
+                            if (grp >= kAll) break;
+                            const int k = (base * kAll + grp) * 8;  // its first key, in the tile
+                            const int id = __shfl_sync(0xffffffffu, ids, k >> p.bs_shift);
+                            const uint8_t *src = mine + (k & (bs - 1)) * token + static_cast<uint64_t>(static_cast<uint32_t>(max(id, 0))) * block;
+#pragma unroll
+                            for (int u = 0; u < kParts; ++u) copy16_async(dst + (grp * kParts + u) * 512, src + 64 * u, id >= 0);
+                        }
+                        if (++fpart == 2 * kParts) {
+                            fpart = 0;
+                            ids = next_ids;
+                            if (++fj == f.jb) {
+                                more = f.next(p);
+                                if (more) begin();
+                            }
+                        }
+                    }
+                    copies_commit();
+                    if (++fslot == kUnits) fslot = 0;
+                };
+                if (more) begin();
+#pragma unroll
+                for (int i = 0; i < kUnits - 1; ++i) fetch();
+                // ---- the converting side
+                int entry = 0, cslot = 0;
+                bool dead = false;
+                for (int piece = 0; !dead && w.next(p); ++piece) {
+                    if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                    if (piece == 0 && wi == 0 && lane == 0) w.record(p, c);
+                    if (lane == 0) odd_flag[wi * kFlags + piece % kFlags] = 0;
+                    __syncwarp();
+                    for (int e = 0; e < 2 * (w.jb - w.ja); ++e, ++entry) {
+                        const int j = w.ja + (e >> 1);
+                        const bool is_v = e & 1;
+                        const int slot = entry % kStages;
+                        if (entry >= kStages &&
+                            !__all_sync(0xffffffffu, mbar_wait_sleep(bar_empty(slot), (entry / kStages - 1) & 1))) {
+                            dead = true;
+                            break;
+                        }
+                        if (__any_sync(0xffffffffu, *abort_flag != 0)) break;
+                        uint8_t *tile = smem + TL::kOffKV + slot * kTileBytes + row * 128;
+                        const bool mixed = kCache == kCacheE4M3 && is_v && w.mixed(p, j);
+                        bool odd = false;
+#pragma unroll 1
+                        for (int part = 0; part < kParts; ++part) {
+                            fetch();  // (into the place of the unit before this one)
+                            copies_wait<kUnits - 1>();
+                            const uint8_t *unit = codes + cslot * kUnitBytes;
+                            if (++cslot == kUnits) cslot = 0;
+#pragma unroll
+                            for (int i = 0; i < kGroups; ++i) {
+                                const int in = i * kWideners + wi, grp = part * kAll + in;  // in the unit, in the tile
+                                if (in >= kAll) break;
+                                uint8_t *dst = tile + grp * TL::kGroup;
+                                if constexpr (kCache == kCacheInt4) {
+                                    const uint4 held = *reinterpret_cast<const uint4 *>(unit + in * 512);
+                                    const uint32_t words[4] = {held.x, held.y, held.z, held.w};
+                                    // 32 dims: four chunks of one half of the head
+#pragma unroll
+                                    for (int u = 0; u < 4; ++u)
+                                        *reinterpret_cast<uint4 *>(dst + (quarter >> 1) * 1024 +
+                                                                   ((((quarter & 1) * 4 + u) ^ row) << 4)) = int4x8_values(words[u]);
+                                } else {
+                                    const int k = j * kBN + grp * 8 + row;
+                                    const bool none = mixed && (k > w.pl || (k >= p.num_sinks && k < w.window_from(p, w.pf)));
+                                    const bool some = mixed && (k > w.pf || (k >= p.num_sinks && k < w.window_from(p, w.pl)));
+#pragma unroll
+                                    for (int u = 0; u < kParts; ++u) {
+                                        const uint4 held = *reinterpret_cast<const uint4 *>(unit + (in * kParts + u) * 512);
+                                        uint32_t words[4] = {held.x, held.y, held.z, held.w};
+                                        if (mixed) {
+#pragma unroll
+                                            for (int q4 = 0; q4 < 4; ++q4) {
+                                                // bytes that are NaN (there are no infinities)
+                                                const uint32_t nan = some ? __vcmpeq4(words[q4] & 0x7f7f7f7fu, 0x7f7f7f7fu) : 0u;
+                                                odd |= nan != 0 && !none;
+                                                words[q4] &= none ? 0u : ~nan;
+                                            }
+                                        }
+                                        // 16 dims: two chunks of half u of the head
+                                        uint32_t v[8];
+#pragma unroll
+                                        for (int q4 = 0; q4 < 4; ++q4) e4m3x4_to_h2x2(words[q4], v[2 * q4], v[2 * q4 + 1]);
+                                        *reinterpret_cast<uint4 *>(dst + u * 1024 + (((quarter * 2) ^ row) << 4)) =
+                                            make_uint4(v[0], v[1], v[2], v[3]);
+                                        *reinterpret_cast<uint4 *>(dst + u * 1024 + (((quarter * 2 + 1) ^ row) << 4)) =
+                                            make_uint4(v[4], v[5], v[6], v[7]);
+                                    }
+                                }
+                            }
+                        }
+                        if (__any_sync(0xffffffffu, odd) && lane == 0) odd_flag[wi * kFlags + piece % kFlags] = 1;
+                        fence_proxy_async_shared();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar_full(slot));
+                    }
+                }
+                copies_wait<0>();  // never leave with copies in flight into this CTA's shared memory
+                if (dead && lane == 0) {
+                    report(a.d_err, KV_DERR_TIMEOUT);
+                    *abort_flag = 1;
+                }
+            }
         }
     } else {
         // ============================================================ softmax and results
+        if constexpr (kWide) asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        Walk w;
+        w.start(scratch.start, x0, x1, item_cost);
         const int x = warp >> 2;                // chain
         const int r = threadIdx.x & 127;        // query row in the tile = TMEM lane
         const int tl = r / g, hh = r - tl * g;  // its token in the tile and head in the group
@@ -1098,7 +1112,10 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                 if (!w.whole) *part_lse(p.t, slot, prow) = lse2;
                 else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
                 if constexpr (kCache != kCacheInt4) {
-                    if (odd_flag[piece % kFlags] | odd_flag[kFlags + piece % kFlags]) {
+                    int odd = 0;
+#pragma unroll
+                    for (int i = 0; i < (kWide ? kWideners : 1); ++i) odd |= odd_flag[i * kFlags + piece % kFlags];
+                    if (odd) {
                         const int ka = w.ja * kBN, kb = min(w.jb * kBN, w.pl + 1);
                         const int edge = max(w.window_from(p, w.pf), p.num_sinks);
                         float4 *mine = w.whole ? nullptr : part;
@@ -1137,7 +1154,7 @@ static cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, co
         if (e != cudaSuccess) return e;
         attr_set[dev].store(true, std::memory_order_release);
     }
-    const cudaError_t e = launch_dependent(kernel, dim3(p.t.workers), dim3(kThreads), kSmem, stream, tq, tk, tv, p);
+    const cudaError_t e = launch_dependent(kernel, dim3(p.t.workers), dim3(kThreads<kCache>), kSmem, stream, tq, tk, tv, p);
     if (e != cudaSuccess || p.t.workers < 2) return e;
     return launch_tree_merge<QT, D>(p.t, stream);
 }
