@@ -6,6 +6,7 @@
 #pragma once
 
 #include "common.cuh"
+#include "dependent_launch.cuh"
 #include "kernels.h"
 
 namespace pkv {
@@ -304,8 +305,93 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
     if (a.lse_out && lane == 0) a.lse_out[rowid] = counts<kNan>(wsum) ? mx + logf(wsum) : -INFINITY;
 }
 
+// Items at most, as a share of the workers, for the merges below that take a CTA where the others take a warp:
+// with few items each is in many pieces, and a warp's round trips through L2, one for every 4 or 8 pieces, add
+// up.  (One sequence of 4104 keys over 64 workers, the
+// whole call: 31 us with the merge by warps, 14 by CTAs and as a programmatic dependent.)
+constexpr int kLongMergeShare = 16;
+
+// The merge of one row's pieces by a CTA of 8 warps: each takes every eighth piece, then their sums are joined.
+// (Kernels with sinks: NaN stays.)
+template <typename QT, int D>
+__global__ void __launch_bounds__(256) lse_merge_long_kernel(const __grid_constant__ KernelParams kp, int num_ctas) {
+    constexpr int kPer = D / 32, kG = 4, kWarps = 8;
+    __shared__ float part[kWarps][32 * kPer], part_m[kWarps], part_sum[kWarps];
+    const DecodeArgs &a = kp.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int item = static_cast<int>(blockIdx.x / kp.rows_per_item), rr = static_cast<int>(blockIdx.x % kp.rows_per_item);
+    const int B = a.num_seqs, g = a.num_q_heads / a.num_kv_heads, R = g * a.q_len;
+    const int seq = item % B, grp = item / B, h_loc = rr / R, r = rr % R;
+    const int64_t rowid = (static_cast<int64_t>(seq) * a.q_len + r / g) * a.num_q_heads + (grp * kp.heads_per_cta + h_loc) * g + r % g;
+    QT *orow = static_cast<QT *>(a.out) + rowid * D + lane * kPer;
+    previous_kernel_done();  // the attention kernel's results
+    const int32_t *P = a.ws_prefix;
+    const long long p0 = P[item], p1 = P[item + 1], S = P[kp.num_items];
+    float acc[kPer], mx = -INFINITY, wsum = 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) acc[e] = 0.f;
+    if (p1 > p0) {
+        num_ctas = active_shares(S, num_ctas);
+        const bool owners = a.ws_pieces != nullptr;
+        const int c_lo = owners ? a.ws_pieces[2 * item] : owner_cta(p0, S, num_ctas);
+        const int c_hi = owners ? a.ws_pieces[2 * item + 1] : owner_cta(p1 - 1, S, num_ctas);
+        if (c_lo == c_hi) return;  // one worker covered it and wrote the output (every warp of the CTA alike)
+        for (int base = c_lo + warp; base <= c_hi; base += kG * kWarps) {
+            float l[kG], v[kG][kPer];
+#pragma unroll
+            for (int u = 0; u < kG; ++u) {
+                const int c = base + u * kWarps;
+                const int64_t row = static_cast<int64_t>(item + c) * kp.rows_per_item + rr;
+                l[u] = c <= c_hi ? __ldcg(a.ws_lse + row) : -INFINITY;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) v[u][e] = c <= c_hi ? __ldcg(a.ws_o + row * D + lane * kPer + e) : 0.f;
+            }
+            float m = mx;
+#pragma unroll
+            for (int u = 0; u < kG; ++u) m = fmaxf(m, l[u]);
+            const float ref = m == -INFINITY ? 0.f : m, f = mx == -INFINITY ? 1.f : expf(mx - ref);
+            mx = m;
+            wsum *= f;  // (all zero, or NaN, while there is no maximum)
+#pragma unroll
+            for (int e = 0; e < kPer; ++e) acc[e] *= f;
+#pragma unroll
+            for (int u = 0; u < kG; ++u) {
+                const float w = l[u] == -INFINITY ? 0.f : expf(l[u] - ref);
+                if (!counts<true>(w)) continue;
+                wsum += w;
+#pragma unroll
+                for (int e = 0; e < kPer; ++e) acc[e] += w * v[u][e];
+            }
+        }
+    }
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) part[warp][e * 32 + lane] = acc[e];
+    if (lane == 0) part_m[warp] = mx, part_sum[warp] = wsum;
+    __syncthreads();
+    if (warp) return;
+    float top = -INFINITY, total = 0.f, out[kPer];
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) top = fmaxf(top, part_m[i]);
+#pragma unroll
+    for (int e = 0; e < kPer; ++e) out[e] = 0.f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) {
+        const float f = part_m[i] == -INFINITY ? 1.f : expf(part_m[i] - top);
+        if (part_sum[i] == 0.f) continue;
+        total += part_sum[i] * f;
+#pragma unroll
+        for (int e = 0; e < kPer; ++e) out[e] += part[i][e * 32 + lane] * f;
+    }
+    const float inv = counts<true>(total) ? 1.f / total : 0.f;
+#pragma unroll
+    for (int e = 0; e < kPer; e += 2) *reinterpret_cast<uint32_t *>(orow + e) = pack2<QT>(out[e] * inv, out[e + 1] * inv);
+    if (a.lse_out && lane == 0)
+        a.lse_out[rowid] = counts<true>(total) ? (top == -INFINITY ? 0.f : top) + logf(total) : -INFINITY;
+}
+
 template <typename QT, int D, bool kNan>
 __global__ void lse_merge_kernel(const __grid_constant__ KernelParams kp, int num_ctas) {
+    if constexpr (kNan) previous_kernel_done();
     const int64_t rows = static_cast<int64_t>(kp.num_items) * kp.rows_per_item;
     const int64_t w = (static_cast<int64_t>(blockIdx.x) * blockDim.x + threadIdx.x) >> 5;
     if (w >= rows) return;
@@ -317,8 +403,16 @@ static cudaError_t row_merge(const KernelParams &kp, int num_workers, cudaStream
     const int64_t rows = static_cast<int64_t>(kp.num_items) * kp.rows_per_item;
     const int threads = 256;
     const int64_t blocks = (rows * 32 + threads - 1) / threads;
-    lse_merge_kernel<QT, D, kNan><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
-    return cudaGetLastError();
+    if constexpr (kNan) {  // kernels with sinks: as a programmatic dependent of theirs
+        if (static_cast<int64_t>(kp.num_items) * kLongMergeShare <= num_workers)
+            return launch_dependent(lse_merge_long_kernel<QT, D>, dim3(static_cast<unsigned>(rows)), dim3(256), 0, stream, kp,
+                                    num_workers);
+        return launch_dependent(lse_merge_kernel<QT, D, true>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0, stream, kp,
+                                num_workers);
+    } else {
+        lse_merge_kernel<QT, D, false><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
+        return cudaGetLastError();
+    }
 }
 
 // The row merge for a finished INT4 decode launch (defined in paged_attention.cu): one warp per

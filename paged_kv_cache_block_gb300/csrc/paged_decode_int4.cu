@@ -130,6 +130,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
         for (int i = 0; i < NS; ++i) mbar_init(smem_u32(&full_bar[i]), 1);
         fence_barrier_init();
     }
+    if constexpr (kSinks) previous_kernel_done();  // launched as a programmatic dependent
     (void)build_schedule<true, kSinks>(a, NI, BPS, Ls, P, warp_sums);
     if (blockIdx.x == 0)  // the merge kernel reads the same prefix
         for (int i = threadIdx.x; i <= NI; i += blockDim.x) a.ws_prefix[i] = P[i];
@@ -693,8 +694,12 @@ cudaError_t launch_int4_typed(const CUtensorMap &tk, const CUtensorMap &tv, cons
         attr_status[dev] = r;
     });
     if (attr_status[dev] != cudaSuccess) return attr_status[dev];
-    kern<<<plan.num_ctas, Int4Launch<RN>::kThreads, plan.smem_bytes, stream>>>(tk, tv, kp);
-    e = cudaGetLastError();
+    if constexpr (kSinks) {
+        e = launch_dependent(kern, dim3(plan.num_ctas), dim3(Int4Launch<RN>::kThreads), plan.smem_bytes, stream, tk, tv, kp);
+    } else {
+        kern<<<plan.num_ctas, Int4Launch<RN>::kThreads, plan.smem_bytes, stream>>>(tk, tv, kp);
+        e = cudaGetLastError();
+    }
     if (e != cudaSuccess) return e;
     return kSinks ? launch_lse_merge_nan(kp, kp.num_workers, q_dtype, stream)
                   : launch_lse_merge(kp, kp.num_workers, q_dtype, stream);

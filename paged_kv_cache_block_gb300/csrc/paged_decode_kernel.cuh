@@ -328,6 +328,9 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
     // the length table, when the plan kept it in shared memory (else lengths are read from
     // seq_lens where they are needed, so that large batches keep the ring's stages)
     // (kLens: the plan kept the length table in shared memory)
+    // kSinks: launched as a programmatic dependent, as its merge is.  (The merge is not let in early: its CTAs
+    // beside this kernel's cost more than they saved, 16.1 us a call for one sequence instead of 14.1.)
+    if constexpr (kSinks) previous_kernel_done();
     int32_t *Ls = kLens ? P + NI + 1 : nullptr;
     const bool any_empty = build_schedule<kLens, kSinks>(a, NI, BPS, Ls, P, warp_sums);
     // an item with stages has an accepted length
@@ -1056,6 +1059,7 @@ struct TileMerge {
 
 template <typename QT, bool kFp8, int D, int RN, bool kNan>
 __global__ void __launch_bounds__(128) tile_merge_kernel(const __grid_constant__ KernelParams kp, int num_ctas) {
+    if constexpr (kNan) previous_kernel_done();
     constexpr int kNR = RN / 8, kMW = TileMerge<QT, kFp8, D, RN>::kMW, kRuns = TileMerge<QT, kFp8, D, RN>::kRuns;
     constexpr int kMT = D / 16, kG = RN == 8 ? 8 : 4;  // pieces a group
     const DecodeArgs &a = kp.a;
@@ -1178,14 +1182,128 @@ __global__ void __launch_bounds__(128) tile_merge_kernel(const __grid_constant__
     }
 }
 
+// The same for items in many pieces (kernels with sinks, few items): a CTA where that kernel has a warp, whose
+// 8 warps take every eighth piece each and then join their sums.
+template <typename QT, bool kFp8, int D, int RN>
+__global__ void __launch_bounds__(256) tile_merge_long_kernel(const __grid_constant__ KernelParams kp) {
+    constexpr int kNR = RN / 8, kRuns = TileMerge<QT, kFp8, D, RN>::kRuns, kWarps = 8;
+    constexpr int kMT = D / 16, kG = RN == 8 ? 8 : 4;  // pieces a group
+    static_assert(TileMerge<QT, kFp8, D, RN>::kMW == 1, "an m-tile a CTA");
+    __shared__ float part[kWarps][kNR][8][32];  // sums (4), maxima (2), weights (2)
+    const DecodeArgs &a = kp.a;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c4 = lane & 3;
+    const int ncw = kp.heads_per_cta * kp.warps_per_head;
+    const int run = blockIdx.x % kRuns, tw = blockIdx.x / kRuns;
+    const int item = tw / ncw, t = tw - item * ncw;
+    const int MW = kp.warps_per_head, h_loc = t / MW, rt = t - h_loc * MW;
+    const int B = a.num_seqs, g = a.num_q_heads / a.num_kv_heads, R = g * a.q_len;
+    const int seq = item % B, grp = item / B;
+    const TileRows tr{static_cast<int64_t>(seq) * a.q_len, (grp * kp.heads_per_cta + h_loc) * g, g, R, a.num_q_heads};
+    previous_kernel_done();  // the attention kernel's results
+    const int32_t p0 = a.ws_prefix[item], p1 = a.ws_prefix[item + 1];
+    const int c_lo = a.ws_pieces[2 * item], c_hi = a.ws_pieces[2 * item + 1];
+    float acc[1][kNR][4], mx[kNR][2], sum[kNR][2];
+#pragma unroll
+    for (int nt = 0; nt < kNR; ++nt) {
+        acc[0][nt][0] = acc[0][nt][1] = acc[0][nt][2] = acc[0][nt][3] = 0.f;
+        mx[nt][0] = mx[nt][1] = -INFINITY;
+        sum[nt][0] = sum[nt][1] = 0.f;
+    }
+    if (p1 > p0) {
+        if (c_lo == c_hi) return;  // one CTA covered it and wrote the output
+        for (int base = c_lo + warp; base <= c_hi; base += kG * kWarps) {
+            float4 v[kG][kNR];
+            float l[kG][kNR][2];
+#pragma unroll
+            for (int u = 0; u < kG; ++u) {
+                const int c = base + u * kWarps;
+                const bool in = c <= c_hi;
+                const float4 *tile = reinterpret_cast<const float4 *>(a.ws_o) +
+                                     (static_cast<int64_t>(item + c) * ncw + t) * (RN * D / 4);
+                const float *lse = a.ws_lse + static_cast<int64_t>(item + c) * kp.rows_per_item + h_loc * R;
+#pragma unroll
+                for (int nt = 0; nt < kNR; ++nt) {
+                    v[u][nt] = in ? __ldcg(tile + (nt * kMT + run) * 32 + lane) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int r = rt * RN + nt * 8 + 2 * c4 + e;
+                        l[u][nt][e] = in && r < R ? __ldcg(lse + r) : -INFINITY;
+                    }
+                }
+            }
+#pragma unroll
+            for (int nt = 0; nt < kNR; ++nt)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    float m = mx[nt][e];
+#pragma unroll
+                    for (int u = 0; u < kG; ++u) m = fmaxf(m, l[u][nt][e]);
+                    const float ref = m == -INFINITY ? 0.f : m, f = mx[nt][e] == -INFINITY ? 1.f : expf(mx[nt][e] - ref);
+                    mx[nt][e] = m;
+                    sum[nt][e] *= f;  // (all zero, or NaN, while there is no maximum)
+                    acc[0][nt][e] *= f, acc[0][nt][2 + e] *= f;
+#pragma unroll
+                    for (int u = 0; u < kG; ++u) {
+                        const float w = l[u][nt][e] == -INFINITY ? 0.f : expf(l[u][nt][e] - ref);
+                        if (!counts<true>(w)) continue;
+                        sum[nt][e] += w;
+                        acc[0][nt][e] += w * (e ? v[u][nt].y : v[u][nt].x);
+                        acc[0][nt][2 + e] += w * (e ? v[u][nt].w : v[u][nt].z);
+                    }
+                }
+        }
+    }
+#pragma unroll
+    for (int nt = 0; nt < kNR; ++nt) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) part[warp][nt][e][lane] = acc[0][nt][e];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) part[warp][nt][4 + e][lane] = mx[nt][e], part[warp][nt][6 + e][lane] = sum[nt][e];
+    }
+    __syncthreads();
+    if (warp) return;
+    float inv[kNR][2];
+#pragma unroll
+    for (int nt = 0; nt < kNR; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            float top = -INFINITY, total = 0.f, lo = 0.f, hi = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) top = fmaxf(top, part[i][nt][4 + e][lane]);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float m = part[i][nt][4 + e][lane], f = m == -INFINITY ? 1.f : expf(m - top);
+                const float s = part[i][nt][6 + e][lane];
+                if (s == 0.f) continue;
+                total += s * f;
+                lo += part[i][nt][e][lane] * f;
+                hi += part[i][nt][2 + e][lane] * f;
+            }
+            acc[0][nt][e] = lo, acc[0][nt][2 + e] = hi;
+            inv[nt][e] = counts<true>(total) ? 1.f / total : 0.f;
+            const int r = rt * RN + nt * 8 + 2 * c4 + e;
+            if (run == 0 && a.lse_out && (lane >> 2) == 0 && r < R)
+                a.lse_out[tr.row(r)] = counts<true>(total) ? (top == -INFINITY ? 0.f : top) + logf(total) : -INFINITY;
+        }
+    store_out_tile<QT, kFp8, D, RN, 1>(acc, inv, rt * RN, tr, static_cast<QT *>(a.out), lane, run);
+}
+
 template <typename QT, bool kFp8, int D, int RN, bool kNan>
 static cudaError_t tile_merge(const KernelParams &kp, int num_workers, cudaStream_t stream) {
     const int64_t warps = static_cast<int64_t>(kp.num_items) * kp.heads_per_cta * kp.warps_per_head *
                           TileMerge<QT, kFp8, D, RN>::kRuns;
     const int threads = 128;
     const int64_t blocks = (warps * 32 + threads - 1) / threads;
-    tile_merge_kernel<QT, kFp8, D, RN, kNan><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
-    return cudaGetLastError();
+    if constexpr (kNan) {  // kernels with sinks: as a programmatic dependent of theirs
+        if (static_cast<int64_t>(kp.num_items) * kLongMergeShare <= num_workers)
+            return launch_dependent(tile_merge_long_kernel<QT, kFp8, D, RN>, dim3(static_cast<unsigned>(warps)), dim3(256), 0,
+                                    stream, kp);
+        return launch_dependent(tile_merge_kernel<QT, kFp8, D, RN, true>, dim3(static_cast<unsigned>(blocks)), dim3(threads), 0,
+                                stream, kp, num_workers);
+    } else {
+        tile_merge_kernel<QT, kFp8, D, RN, false><<<static_cast<unsigned>(blocks), threads, 0, stream>>>(kp, num_workers);
+        return cudaGetLastError();
+    }
 }
 
 template <typename QT, typename CT, int D, int RN, bool kFused, int kBS, bool kLens, bool kSinks>
@@ -1212,8 +1330,12 @@ static cudaError_t launch_typed(const CUtensorMap &tk, const CUtensorMap &tv, co
     });
     if (attr_status[dev] != cudaSuccess) return attr_status[dev];
     {
-        kern<<<plan.num_ctas, plan.threads, plan.smem_bytes, stream>>>(tk, tv, kp);
-        e = cudaGetLastError();
+        if constexpr (kSinks) {
+            e = launch_dependent(kern, dim3(plan.num_ctas), dim3(plan.threads), plan.smem_bytes, stream, tk, tv, kp);
+        } else {
+            kern<<<plan.num_ctas, plan.threads, plan.smem_bytes, stream>>>(tk, tv, kp);
+            e = cudaGetLastError();
+        }
         if (e != cudaSuccess) return e;
         return kp.tile_ws ? tile_merge<QT, CacheTraits<CT>::kFp8, D, RN, kSinks>(kp, plan.num_ctas, stream)
                           : row_merge<QT, D, kSinks>(kp, plan.num_ctas, stream);

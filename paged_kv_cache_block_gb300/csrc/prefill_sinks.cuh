@@ -101,6 +101,12 @@ struct Seq {
     int pairs;          // of row tiles
 };
 
+// a / b for 0 <= a, 0 < b: most are small, and a 64-bit division takes some hundred cycles.
+__device__ __forceinline__ int64_t quotient(int64_t a, int64_t b) {
+    if (((a | b) >> 32) == 0) return static_cast<uint32_t>(a) / static_cast<uint32_t>(b);
+    return a / b;
+}
+
 struct Costs {
     int step;           // tokens of a pair
     int64_t extra;      // of a window: window - 1 + keys of the sinks' blocks (no window: far above any length)
@@ -116,7 +122,7 @@ struct Costs {
     // Of pairs 0 .. k - 1: whole pairs i < m lie below the window's bound ctx + (i + 1) step <= extra + step.
     __device__ __forceinline__ int64_t before(const Seq &s, int k) const {
         const int64_t whole = min(k, s.pairs - 1);
-        const int64_t m = min(whole, extra < s.ctx ? int64_t(0) : (extra - s.ctx) / step + 1);
+        const int64_t m = min(whole, extra < s.ctx ? int64_t(0) : quotient(extra - s.ctx, step) + 1);
         int64_t sum = m * s.ctx + step * (m * (m + 1) / 2) + (whole - m) * (extra + step) + whole * item;
         if (k == s.pairs) sum += of(s, s.pairs - 1);
         return sum;
@@ -187,22 +193,23 @@ __device__ __forceinline__ void share_of_cta(const SinkPrefillParams &p, int c, 
     // a tile's end, hence a tile: no share between two of an item is empty.
     const bool big = all_keys >= static_cast<int64_t>(kBigShare) * kBN * p.t.workers;
     item_cost = big ? kItemCost * kBN : 0;
+    // (With an item's cost, 8 tiles a worker are more than such a length anyway.)
     const int64_t total = all_keys + item_cost * all_items;
-    const int64_t most = total / (kBN + item_cost);
-    const int64_t shares = min(static_cast<int64_t>(p.t.workers), most > 0 ? most : (total > 0 ? 1 : 0));
+    const int64_t most = big ? p.t.workers : min(static_cast<int64_t>(p.t.workers), total / kBN);
+    const int64_t shares = most > 0 ? most : (total > 0 ? 1 : 0);
     x0 = x1 = 0;
     if (c >= shares) return;
-    x0 = total * c / shares;
-    x1 = total * (c + 1) / shares;
+    x0 = quotient(total * c, shares);
+    x1 = quotient(total * (c + 1), shares);
     const int64_t before = keys_before + item_cost * items_before;
     if (x0 < before || x0 >= before + keys + item_cost * items) return;
     const Costs costs(p, item_cost);
     int64_t at = before;  // one thread
     for (int b = b_lo; b < b_hi; ++b) {
-        if (!load_seq(p, b, s, &rejected)) continue;
+        if (per > 1 && !load_seq(p, b, s, &rejected)) continue;
         const int64_t head = costs.before(s, s.pairs);
         if (x0 < at + head * heads) {
-            const int64_t h = (x0 - at) / head;
+            const int64_t h = quotient(x0 - at, head);
             at += h * head;
             int lo = 0, hi = s.pairs - 1;  // the last pair that starts at or before x0
             while (lo < hi) {
@@ -260,7 +267,7 @@ struct Walk {
     }
     // The tile that a cost lies in, of a cost within the item (its end: tiles): a tile belongs to the share
     // that its end lies in.
-    __device__ __forceinline__ int tile_at(int64_t x) const { return static_cast<int>((x - at) * tiles / cost); }
+    __device__ __forceinline__ int tile_at(int64_t x) const { return static_cast<int>(quotient((x - at) * tiles, cost)); }
     __device__ __forceinline__ bool next(const SinkPrefillParams &p) {
         const Costs costs(p, item_cost);
         const TreeArgs &a = p.t.a;
