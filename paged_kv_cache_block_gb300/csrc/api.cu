@@ -1480,18 +1480,17 @@ static kv_status decode_sinks(const void *q, kv_dtype q_dtype, int32_t num_seqs,
     a.block_size = c.block_size;
     a.num_blocks = c.num_blocks;
     a.window = window;
-    a.num_sinks = window > 0 ? std::min(num_sinks, a.max_seq_len) : 0;
+    const pkv::SinkArgs sinks{c.v, window > 0 ? std::min(num_sinks, a.max_seq_len) : 0};
     a.scale_log2 = scale_log2;  // INT4: the MMAs see codes in units of 2^-24
     a.v_scale = fp8 ? c.v_scale : 1.0f;
-    a.v_cache = c.v;
     if (int4) {
         a.k_gscales = c.k_scales;
         a.v_gscales = c.v_scales;
         a.group_shift = log2_of(c.group_size);
         a.lse_offset_scale = 8.f * scale;
-        e = pkv::launch_paged_decode_sinks_int4(tk, tv, a, plan, q_dtype, s);
+        e = pkv::launch_paged_decode_sinks_int4(tk, tv, a, sinks, plan, q_dtype, s);
     } else {
-        e = pkv::launch_paged_decode_sinks(tk, tv, a, plan, q_dtype, c.dtype, s);
+        e = pkv::launch_paged_decode_sinks(tk, tv, a, sinks, plan, q_dtype, c.dtype, s);
     }
     if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
     return ok();

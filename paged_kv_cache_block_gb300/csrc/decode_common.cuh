@@ -29,6 +29,7 @@ struct KernelParams {
                            // by stages plus this per item); 0: equal stage counts
     int lens_smem;         // 16-bit / E4M3 kernel: the length table is in shared memory (it fits
                            // without costing the ring a stage); else lengths are read from seq_lens
+    SinkArgs sinks;        // kernels with sinks
 };
 
 // The CTA that owns flat stage s when S stages are split into G equal shares
@@ -107,12 +108,13 @@ struct SinkAxis {
     int hidden;  // blocks left out
     int len;     // length on the axis
 };
-__device__ __forceinline__ int sink_blocks(const DecodeArgs &a, int bs_shift) {
-    return (a.num_sinks + a.block_size - 1) >> bs_shift;
+__device__ __forceinline__ int sink_blocks(const KernelParams &kp, int bs_shift) {
+    return (kp.sinks.num_sinks + kp.a.block_size - 1) >> bs_shift;
 }
-__device__ __forceinline__ SinkAxis sink_axis(const DecodeArgs &a, int L, int bs_shift) {
+__device__ __forceinline__ SinkAxis sink_axis(const KernelParams &kp, int L, int bs_shift) {
+    const DecodeArgs &a = kp.a;
     const int first = a.window > 0 ? max(0, L - a.q_len - a.window + 1) >> bs_shift : 0;
-    const int hidden = max(0, first - sink_blocks(a, bs_shift));
+    const int hidden = max(0, first - sink_blocks(kp, bs_shift));
     return SinkAxis{hidden, L - (hidden << bs_shift)};
 }
 
@@ -122,8 +124,9 @@ __device__ __forceinline__ SinkAxis sink_axis(const DecodeArgs &a, int L, int bs
 //   (returns whether some length was rejected)
 //   P[i]   the number of stages of items 0 .. i-1 (an item is (head group, sequence), group-major;
 //          a stage is BPS consecutive cache blocks of the attended range), P[0] = 0.
+// (kp: kSinks)
 template <bool kLens = true, bool kSinks = false>
-__device__ __forceinline__ bool build_schedule(const DecodeArgs &a, int NI, int BPS, int32_t *Ls,
+__device__ __forceinline__ bool build_schedule(const KernelParams &kp, const DecodeArgs &a, int NI, int BPS, int32_t *Ls,
                                                int32_t *P, int32_t *warp_sums) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int B = a.num_seqs, q_len = a.q_len, bs = a.block_size;
@@ -148,7 +151,7 @@ __device__ __forceinline__ bool build_schedule(const DecodeArgs &a, int NI, int 
             else L = checked_len(a, seq);
             if (L < 0) return 0;
             if constexpr (kSinks) {
-                return (((sink_axis(a, L, bs_shift).len + bs - 1) >> bs_shift) + BPS - 1) >> bps_shift;
+                return (((sink_axis(kp, L, bs_shift).len + bs - 1) >> bs_shift) + BPS - 1) >> bps_shift;
             } else {
                 const int lo_key = a.window > 0 ? max(0, L - q_len - a.window + 1) : 0;
                 const int nb = ((L + bs - 1) >> bs_shift) - (lo_key >> bs_shift);

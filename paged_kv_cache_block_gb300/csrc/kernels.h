@@ -115,7 +115,10 @@ struct DecodeArgs {
     const float *k_gscales, *v_gscales;  // [num_kv_heads, head_dim >> group_shift]
     int32_t group_shift;                 // log2(group_size)
     float lse_offset_scale;              // 8 * softmax scale
-    // kernels with sinks only
+};
+
+// What the decode kernels with sinks take besides.
+struct SinkArgs {
     const void *v_cache;  // 16-bit and E4M3 caches
     int32_t num_sinks;    // a windowed row sees the keys below it too (0 without a window)
 };
@@ -126,8 +129,8 @@ cudaError_t launch_paged_decode(const CUtensorMap &tmap_k, const CUtensorMap &tm
 
 // The same with a window and sinks (paged_sinks.cu).
 cudaError_t launch_paged_decode_sinks(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
-                                      const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
-                                      int cache_dtype, cudaStream_t stream);
+                                      const DecodeArgs &a, const SinkArgs &sinks, const DecodePlan &plan,
+                                      int q_dtype, int cache_dtype, cudaStream_t stream);
 
 // Decode attention over INT4 caches (paged_decode_int4.cu): warps with private TMA rings,
 // int4_decode_warps(rows_per_warp) per CTA, then the merge kernel.
@@ -136,8 +139,8 @@ cudaError_t launch_paged_decode_int4(const CUtensorMap &tmap_k, const CUtensorMa
                                      const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
                                      cudaStream_t stream);
 cudaError_t launch_paged_decode_sinks_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
-                                           const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
-                                           cudaStream_t stream);
+                                           const DecodeArgs &a, const SinkArgs &sinks, const DecodePlan &plan,
+                                           int q_dtype, cudaStream_t stream);
 // The INT4 one-launch step: each worker writes (as INT4 codes) the new-token rows it reads.
 cudaError_t launch_decode_step_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
                                     const DecodeArgs &a, const StepArgs &f, const DecodePlan &plan,

@@ -131,7 +131,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
         fence_barrier_init();
     }
     if constexpr (kSinks) previous_kernel_done();  // launched as a programmatic dependent
-    (void)build_schedule<true, kSinks>(a, NI, BPS, Ls, P, warp_sums);
+    (void)build_schedule<true, kSinks>(kp, a, NI, BPS, Ls, P, warp_sums);
     if (blockIdx.x == 0)  // the merge kernel reads the same prefix
         for (int i = threadIdx.x; i <= NI; i += blockDim.x) a.ws_prefix[i] = P[i];
 
@@ -245,7 +245,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
         my_ok = false;
         my_id = a.num_blocks;  // one past the pool: a copy from there reads zeros
         if (lb < p_nblk) {
-            const int behind = kSinks && lb >= sink_blocks(a, bs_shift) ? p_hidden : 0;
+            const int behind = kSinks && lb >= sink_blocks(kp, bs_shift) ? p_hidden : 0;
             const int e = a.block_table[static_cast<int64_t>(p_row) * a.bt_stride + lb + behind];
             if (e >= 0 && e < a.num_blocks) {
                 my_id = e;
@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
             p_row = seq;
             p_head = grp * HG + h_loc;
             if constexpr (kSinks) {
-                const SinkAxis ax = sink_axis(a, L, bs_shift);
+                const SinkAxis ax = sink_axis(kp, L, bs_shift);
                 p_hidden = ax.hidden;
                 p_nblk = (ax.len + bs - 1) >> bs_shift;
                 p_lb = (ps - P[p_item]) * BPS;
@@ -399,8 +399,9 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                         const int tok = cr[j].c0 + l4 + (e >> 1) * 8;
                         const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
                         const int ph = pos_hi[nt][e & 1];
-                        const bool okk =
-                            blk_ok && tok <= ph && (W <= 0 || tok > ph - W || (kSinks && tok < a.num_sinks));
+                        bool okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
+                        if constexpr (kSinks)
+                            okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W || tok < kp.sinks.num_sinks);
                         v = okk ? v : -INFINITY;
                     }
                     sa[j][nt][e] = v;
@@ -503,7 +504,7 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
             grp = item / B;
             L = Ls[seq];
             n_item = item_end - item_begin;
-            if constexpr (kSinks) L = sink_axis(a, L, bs_shift).len;  // positions on the axis from here on
+            if constexpr (kSinks) L = sink_axis(kp, L, bs_shift).len;  // positions on the axis from here on
             const int key_lo = a.window > 0 ? max(0, L - q_len - a.window + 1) : 0;
             b0 = kSinks ? 0 : key_lo / bs;
             lo_last = a.window > 0 ? max(0, L - a.window) : 0;
@@ -580,10 +581,9 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
             }
         }
         const bool pair = two || n_chunks == 2;
-        auto below = [&](const Int4Chunk &c) { return c.c0 < lo_last && !(kSinks && c.c0 + 15 < a.num_sinks); };
-        bool need_mask = below(cr[0]) || (cr[0].c0 + 15 > hi_first) || (cr[0].mask != full_mask);
+        bool need_mask = (cr[0].c0 < lo_last) || (cr[0].c0 + 15 > hi_first) || (cr[0].mask != full_mask);
         if (pair)
-            need_mask = need_mask || below(cr[1]) || (cr[1].c0 + 15 > hi_first) ||
+            need_mask = need_mask || (cr[1].c0 < lo_last) || (cr[1].c0 + 15 > hi_first) ||
                         (cr[1].mask != full_mask);
         if (pair) {
             if (need_mask) unit(cr, std::integral_constant<int, 2>{}, std::true_type{});
@@ -624,12 +624,12 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                     l += __shfl_xor_sync(0xffffffffu, l, 16);
                     const int r = rt * RN + nt * 8 + 2 * c4 + e;
                     if (r >= R) continue;
-                    const bool some = kSinks ? l != 0.f : l > 0.f;  // kSinks: NaN stays NaN
-                    const float inv = some ? 1.f / l : 0.f;
-                    const float m = kSinks ? m_run[nt][e] - kShift : m_run[nt][e];
-                    const float lse = some ? (m + log2f(l)) * 0.69314718055994531f -
-                                                 a.lse_offset_scale * q_sum[nt][e]
-                                           : -INFINITY;
+                    // (kSinks: a sum that is NaN stays one)
+                    const float inv = (kSinks ? l != 0.f : l > 0.f) ? 1.f / l : 0.f;
+                    const float lse = (kSinks ? l != 0.f : l > 0.f)
+                                          ? (m_run[nt][e] - kShift + log2f(l)) * 0.69314718055994531f -
+                                                a.lse_offset_scale * q_sum[nt][e]
+                                          : -INFINITY;
                     const int64_t tokq = static_cast<int64_t>(seq) * q_len + r / g;
                     const int64_t rowid = tokq * a.num_q_heads + hkv * g + r % g;
                     const int64_t wrow = static_cast<int64_t>(item + vc) * kp.rows_per_item + h_loc * R + r;
@@ -641,7 +641,9 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                             const int d = (mt >> 1) * 32 + 4 * l4 + 2 * (mt & 1) + hf;
                             const float unit_scale = hf ? 1048576.f : 16777216.f;  // 2^20, 2^24
                             const float v =
-                                some ? vsc[d >> gshift] * fmaf(o[mt][nt][2 * hf + e] * unit_scale, inv, -8.f) : 0.f;
+                                (kSinks ? l != 0.f : l > 0.f)
+                                    ? vsc[d >> gshift] * fmaf(o[mt][nt][2 * hf + e] * unit_scale, inv, -8.f)
+                                    : 0.f;
                             if (whole) static_cast<QT *>(a.out)[rowid * kD + d] = from_float<QT>(v);
                             else a.ws_o[wrow * kD + d] = v;
                         }
@@ -713,7 +715,8 @@ int int4_decode_warps(int rows_per_warp) {
 
 template <bool kFused, bool kSinks = false>
 static cudaError_t launch_int4_any(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v, const DecodeArgs &a,
-                                   const StepArgs &f, const DecodePlan &plan, int q_dtype, cudaStream_t stream) {
+                                   const StepArgs &f, const DecodePlan &plan, int q_dtype, cudaStream_t stream,
+                                   const SinkArgs &sinks = SinkArgs{}) {
     if (a.num_seqs == 0) return cudaSuccess;
     KernelParams kp;
     kp.a = a;
@@ -731,6 +734,7 @@ static cudaError_t launch_int4_any(const CUtensorMap &tmap_k, const CUtensorMap 
     kp.tile_ws = 0;
     kp.item_cost = 0;
     kp.lens_smem = 1;
+    kp.sinks = sinks;
     const bool f16 = q_dtype == KV_F16;
     auto launch = [&](auto rows, auto block) {
         constexpr int RN = decltype(rows)::value, kBS = decltype(block)::value;
@@ -757,9 +761,9 @@ cudaError_t launch_paged_decode_int4(const CUtensorMap &tmap_k, const CUtensorMa
 }
 
 cudaError_t launch_paged_decode_sinks_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,
-                                           const DecodeArgs &a, const DecodePlan &plan, int q_dtype,
-                                           cudaStream_t stream) {
-    return launch_int4_any<false, true>(tmap_k, tmap_v, a, StepArgs{}, plan, q_dtype, stream);
+                                           const DecodeArgs &a, const SinkArgs &sinks, const DecodePlan &plan,
+                                           int q_dtype, cudaStream_t stream) {
+    return launch_int4_any<false, true>(tmap_k, tmap_v, a, StepArgs{}, plan, q_dtype, stream, sinks);
 }
 
 cudaError_t launch_decode_step_int4(const CUtensorMap &tmap_k, const CUtensorMap &tmap_v,

@@ -332,7 +332,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
     // beside this kernel's cost more than they saved, 16.1 us a call for one sequence instead of 14.1.)
     if constexpr (kSinks) previous_kernel_done();
     int32_t *Ls = kLens ? P + NI + 1 : nullptr;
-    const bool any_empty = build_schedule<kLens, kSinks>(a, NI, BPS, Ls, P, warp_sums);
+    const bool any_empty = build_schedule<kLens, kSinks>(kp, a, NI, BPS, Ls, P, warp_sums);
     // an item with stages has an accepted length
     auto len_of = [&](int seq) {
         if constexpr (kLens) return Ls[seq];
@@ -397,7 +397,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
             }
             int nblk, lb0, hidden = 0;
             if constexpr (kSinks) {
-                const SinkAxis ax = sink_axis(a, L, bs_shift);
+                const SinkAxis ax = sink_axis(kp, L, bs_shift);
                 hidden = ax.hidden;
                 nblk = (ax.len + bs - 1) >> bs_shift;
                 lb0 = k * BPS;
@@ -424,7 +424,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 my_ok = false;
                 my_id = a.num_blocks;  // one past the pool: a copy from there reads zeros
                 if (lb < nblk) {
-                    const int behind = kSinks && lb >= sink_blocks(a, bs_shift) ? hidden : 0;
+                    const int behind = kSinks && lb >= sink_blocks(kp, bs_shift) ? hidden : 0;
                     const int e = a.block_table[static_cast<int64_t>(seq) * a.bt_stride + lb + behind];
                     if (e >= 0 && e < a.num_blocks) {
                         my_id = e;
@@ -665,8 +665,9 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                         const int tok = cr[j].c0 + l4 + (e >> 1) * 8;
                         const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
                         const int ph = pos_hi[nt][e & 1];
-                        const bool okk =
-                            blk_ok && tok <= ph && (W <= 0 || tok > ph - W || (kSinks && tok < a.num_sinks));
+                        bool okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
+                        if constexpr (kSinks)
+                            okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W || tok < kp.sinks.num_sinks);
                         v = okk ? v : -INFINITY;
                     }
                     sa[j][nt][e] = v;
@@ -740,7 +741,8 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 for (int e = 0; e < 4; ++e) {
                     const int tok = cr[j].c0 + 2 * c4 + (e >> 1) * 8 + (e & 1);
                     const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
-                    keep[e] = (blk_ok && (tok >= key_lo || (kSinks && tok < a.num_sinks)) && tok < L) ? 0xffffu : 0u;
+                    keep[e] = (blk_ok && tok >= key_lo && tok < L) ? 0xffffu : 0u;
+                    if constexpr (kSinks) keep[e] |= (blk_ok && tok < kp.sinks.num_sinks && tok < L) ? 0xffffu : 0u;
                 }
                 keep_lo = keep[0] | (keep[1] << 16);
                 keep_hi = keep[2] | (keep[3] << 16);
@@ -754,7 +756,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int tok = cr[j].c0 + 2 * c4 + (e >> 1) * 8 + (e & 1);
-                    some[e] = tok > hi_first || (tok < lo_last && tok >= a.num_sinks) ? 0xffffu : 0u;
+                    some[e] = tok > hi_first || (tok < lo_last && tok >= kp.sinks.num_sinks) ? 0xffffu : 0u;
                 }
                 some_lo = some[0] | (some[1] << 16);
                 some_hi = some[2] | (some[3] << 16);
@@ -826,7 +828,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
             grp = item / B;
             L = len_of(seq);
             n_item = P[item + 1] - P[item];
-            if constexpr (kSinks) L = sink_axis(a, L, bs_shift).len;  // positions on the axis from here on
+            if constexpr (kSinks) L = sink_axis(kp, L, bs_shift).len;  // positions on the axis from here on
             nonfinite = 0;
             key_lo = a.window > 0 ? max(0, L - q_len - a.window + 1) : 0;
             b0 = kSinks ? 0 : key_lo / bs;
@@ -906,9 +908,14 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
             }
         }
         const bool pair = two || n_chunks == 2;
+        // (the conditions with sinks stand beside the others, not inside them: `|| (kSinks && ...)` alone made
+        // the compiler order the kernels without sinks otherwise, up to 1.7 % slower)
         auto chunk_masked = [&](const ChunkRef &c) {
-            return (c.c0 < lo_last && !(kSinks && c.c0 + 15 < a.num_sinks)) || (c.c0 + 15 > hi_first) ||
-                   (c.mask != full_mask);
+            if constexpr (kSinks)
+                return (c.c0 < lo_last && c.c0 + 15 >= kp.sinks.num_sinks) || (c.c0 + 15 > hi_first) ||
+                       (c.mask != full_mask);
+            else
+                return (c.c0 < lo_last) || (c.c0 + 15 > hi_first) || (c.mask != full_mask);
         };
         if constexpr (kNR == 1) {
             const bool need_mask = chunk_masked(cr[0]) || (pair && chunk_masked(cr[1]));
@@ -952,9 +959,9 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                     // the values set aside, added to the rows that see their keys: as the weight is above
                     // 0, the value itself will do.  The keys are the q_len - 1 at each edge of what the
                     // window and the rows' own tokens leave in full view.
-                    const int hidden = sink_axis(a, len_of(seq), bs_shift).hidden;
+                    const int hidden = sink_axis(kp, len_of(seq), bs_shift).hidden;
                     const int from = seg_k0 * ST, to = min(L, (k_last + 1) * ST);
-                    const int edge = max(key_lo, a.num_sinks), view = max(edge, lo_last);
+                    const int edge = max(key_lo, kp.sinks.num_sinks), view = max(edge, lo_last);
                     for (int t = edge; t < L; ++t) {
                         if (t >= view && t <= hi_first) {  // seen by every row
                             t = hi_first;
@@ -963,7 +970,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                         if (t < from || t >= to) continue;
                         const int lb = t >> bs_shift;
                         const int id = a.block_table[static_cast<int64_t>(seq) * a.bt_stride + lb +
-                                                     (lb >= sink_blocks(a, bs_shift) ? hidden : 0)];
+                                                     (lb >= sink_blocks(kp, bs_shift) ? hidden : 0)];
                         if (id < 0 || id >= a.num_blocks) continue;
                         const int64_t at =
                             ((static_cast<int64_t>(id) * bs + (t & (bs - 1))) * a.num_kv_heads + hkv) * D;
@@ -974,10 +981,10 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                                 float v;
                                 if constexpr (kFp8) {
                                     const __nv_fp8_storage_t c =
-                                        static_cast<const uint8_t *>(a.v_cache)[at + mt * 16 + 2 * l4 + hf];
+                                        static_cast<const uint8_t *>(kp.sinks.v_cache)[at + mt * 16 + 2 * l4 + hf];
                                     v = __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
                                 } else {
-                                    v = to_float<QT>(static_cast<const QT *>(a.v_cache)[at + mt * 16 + l4 + 8 * hf]);
+                                    v = to_float<QT>(static_cast<const QT *>(kp.sinks.v_cache)[at + mt * 16 + l4 + 8 * hf]);
                                 }
                                 if (isfinite(v)) continue;
 #pragma unroll
@@ -985,7 +992,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
 #pragma unroll
                                     for (int e = 0; e < 2; ++e) {
                                         const int ph = pos_hi[nt][e];
-                                        if (t <= ph && (W <= 0 || t > ph - W || t < a.num_sinks))
+                                        if (t <= ph && (W <= 0 || t > ph - W || t < kp.sinks.num_sinks))
                                             o[mt][nt][2 * hf + e] += v;
                                     }
                             }
@@ -1001,12 +1008,14 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                     l += __shfl_xor_sync(0xffffffffu, l, 4);
                     l += __shfl_xor_sync(0xffffffffu, l, 8);
                     l += __shfl_xor_sync(0xffffffffu, l, 16);
-                    const bool some = kSinks ? l != 0.f : l > 0.f;  // kSinks: NaN stays NaN
-                    inv[nt][e] = some ? a.v_scale / l : 0.f;
+                    // (kSinks: a sum that is NaN stays one)
+                    inv[nt][e] = (kSinks ? l != 0.f : l > 0.f) ? a.v_scale / l : 0.f;
                     const int r = rt * RN + nt * 8 + 2 * c4 + e;
                     if (l4 == 0 && r < R) {
-                        const float m = kSinks ? m_run[nt][e] - kWeightShift<MT> : m_run[nt][e];
-                        const float lse = some ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+                        const float shift = kSinks ? kWeightShift<MT> : 0.f;
+                        const float lse = (kSinks ? l != 0.f : l > 0.f)
+                                              ? (m_run[nt][e] - shift + log2f(l)) * 0.69314718055994531f
+                                              : -INFINITY;
                         if (whole) {
                             if (a.lse_out) a.lse_out[tr.row(r)] = lse;
                         } else {
@@ -1377,6 +1386,7 @@ inline KernelParams make_params(const DecodeArgs &a, const DecodePlan &plan) {
     kp.tile_ws = plan.tile_ws;
     kp.item_cost = plan.item_cost;
     kp.lens_smem = plan.lens_smem;
+    kp.sinks = SinkArgs{};
     return kp;
 }
 

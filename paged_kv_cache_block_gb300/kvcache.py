@@ -964,7 +964,6 @@ def paged_attention_tree(q: torch.Tensor, k_cache: torch.Tensor, v_cache: torch.
     return out
 
 
-
 # ---------------------------------------------------------------- windows with sinks (pagedkv_sinks.h)
 
 def _cache_code(k_cache, v_cache, D, dev, k_scales, v_scales):
