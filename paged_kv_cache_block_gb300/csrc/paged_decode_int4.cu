@@ -399,9 +399,11 @@ __global__ void __launch_bounds__(Int4Launch<RN>::kThreads, 1)
                         const int tok = cr[j].c0 + l4 + (e >> 1) * 8;
                         const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
                         const int ph = pos_hi[nt][e & 1];
-                        bool okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
+                        bool okk;
                         if constexpr (kSinks)
                             okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W || tok < kp.sinks.num_sinks);
+                        else
+                            okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
                         v = okk ? v : -INFINITY;
                     }
                     sa[j][nt][e] = v;

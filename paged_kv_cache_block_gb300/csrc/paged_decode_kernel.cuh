@@ -665,9 +665,11 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                         const int tok = cr[j].c0 + l4 + (e >> 1) * 8;
                         const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
                         const int ph = pos_hi[nt][e & 1];
-                        bool okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
+                        bool okk;
                         if constexpr (kSinks)
                             okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W || tok < kp.sinks.num_sinks);
+                        else
+                            okk = blk_ok && tok <= ph && (W <= 0 || tok > ph - W);
                         v = okk ? v : -INFINITY;
                     }
                     sa[j][nt][e] = v;
@@ -741,8 +743,10 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 for (int e = 0; e < 4; ++e) {
                     const int tok = cr[j].c0 + 2 * c4 + (e >> 1) * 8 + (e & 1);
                     const bool blk_ok = (cr[j].mask >> ((tok - cr[j].tok0) / bs)) & 1u;
-                    keep[e] = (blk_ok && tok >= key_lo && tok < L) ? 0xffffu : 0u;
-                    if constexpr (kSinks) keep[e] |= (blk_ok && tok < kp.sinks.num_sinks && tok < L) ? 0xffffu : 0u;
+                    if constexpr (kSinks)
+                        keep[e] = (blk_ok && (tok >= key_lo || tok < kp.sinks.num_sinks) && tok < L) ? 0xffffu : 0u;
+                    else
+                        keep[e] = (blk_ok && tok >= key_lo && tok < L) ? 0xffffu : 0u;
                 }
                 keep_lo = keep[0] | (keep[1] << 16);
                 keep_hi = keep[2] | (keep[3] << 16);
@@ -912,7 +916,7 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
         // the compiler order the kernels without sinks otherwise, up to 1.7 % slower)
         auto chunk_masked = [&](const ChunkRef &c) {
             if constexpr (kSinks)
-                return (c.c0 < lo_last && c.c0 + 15 >= kp.sinks.num_sinks) || (c.c0 + 15 > hi_first) ||
+                return (c.c0 < lo_last && !(c.c0 + 15 < kp.sinks.num_sinks)) || (c.c0 + 15 > hi_first) ||
                        (c.mask != full_mask);
             else
                 return (c.c0 < lo_last) || (c.c0 + 15 > hi_first) || (c.mask != full_mask);

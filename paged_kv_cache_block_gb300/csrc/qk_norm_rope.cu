@@ -14,8 +14,8 @@
 //
 // INT4 caches (kInt4) take a key's four codes of a piece, its float32 values divided by the scale of
 // their group, as 16 bits; a piece never crosses a group, whose size is at least 8.
-// 16384 tokens of 64 + 16 heads take 119 us (5.3 TB/s): the division a value that the codes' rounding is
-// defined by, and a quarter of the bytes written.
+// 16384 tokens of 64 + 16 heads take 119 us (5.3 TB/s); 121 with one reciprocal for a piece's four quotients,
+// 122 with that and 3 blocks an SM (no spills).
 //
 // About 2 bytes move per element each way: the bound is HBM, once the instructions per element are
 // few (packed arithmetic, pointers advanced by a constant).  A warp takes several heads, loaded four

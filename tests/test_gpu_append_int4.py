@@ -101,6 +101,33 @@ def test_without_norm_and_rotation_it_is_the_cache_write(kv):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("dt", [BF16, F16])
+@pytest.mark.parametrize("seed", [0, 1])
+def test_codes_of_any_scale_are_those_of_the_cache_write(kv, dt, seed):
+    """Without norm and rotation every code is that of the quotient's two roundings: scales of any size (0, the
+    smallest and largest numbers, infinity, NaN, negative ones), values at and next to the middle of two codes."""
+    rng = np.random.default_rng(seed)
+    T, H, D, bs = 400, 16, 128, 16
+    NB = T // bs
+    with np.errstate(over="ignore"):
+        scales = (rng.uniform(1, 2, (2, H, D // 8)) * 2.0 ** rng.integers(-149, 128, (2, H, D // 8))).astype(np.float32)
+    scales[:, 8:] = rng.uniform(0.01, 2.0, (2, H - 8, D // 8))
+    scales[:, 0, :8] = [0.0, -0.0, np.inf, np.nan, 1e-45, 3e38, -0.5, -1e-40]
+    wide = np.repeat(scales.astype(np.float64), 8, 2)[:, None]
+    with np.errstate(all="ignore"):
+        x = np.where(rng.random((2, T, H, D)) < 0.7, rng.integers(-10, 10, (2, T, H, D)) + 0.5, rng.uniform(-10, 10, (2, T, H, D))) * wide
+        x *= np.where(rng.random(x.shape) < 0.5, 1.0, 1 + rng.integers(-3, 4, x.shape) * 2.0 ** -8)
+    x[:, 0] = [np.inf, -np.inf, np.nan, 0.0, -0.0, 6e-8, 65504.0, -65504.0] * 16
+    k, v = (torch.from_numpy(y).to(dt).cuda() for y in x)
+    sc = [torch.from_numpy(y).cuda() for y in scales]
+    slots = torch.from_numpy(rng.permutation(T)).cuda()
+    caches = [torch.zeros((NB, bs, H, D // 2), dtype=torch.uint8, device="cuda") for _ in range(4)]
+    kv.reshape_and_cache_int4(k, v, slots, *caches[:2], *sc)
+    kv.qk_norm_rope_and_cache_int4(k, k, v, None, None, slots, *caches[2:], *sc)
+    for a, b in zip(caches[:2], caches[2:]):
+        assert torch.equal(a, b)
+
+
 def test_padding_bad_positions_and_slots(kv):
     s = inputs(4, 30, 8, 2, BF16, 16, 32, 128, True)
     pos, slots = s["pos"].copy(), s["slots"].copy()
