@@ -38,11 +38,11 @@
 // phase: about 4,700 clocks a tile of two row tiles, of which the products take 2 x 1,300 and a softmax 1,700.
 // Times of the call, one GB300 (32/8 heads of 128 dims and blocks of 16 where not said):
 //   16 chunks of 1024 tokens in the middle of 7168 + 1024, window 4096, 4 sinks     977 us, 957 TFLOP/s counted
-//   8 ragged prompts up to 2048, 64/8 heads, window 512, 128 sinks                  317 us, 464 (tiles on the
+//   8 ragged prompts up to 2048, 64/8 heads, window 512, 128 sinks                  321 us, 459 (tiles on the
 //     diagonal and at the window's edge are half masked)
 //   100 tokens after 20000, window 4096, 4 sinks    31 us: start 5, 2.4 a key tile, partial results and merge 10
-//   the 16 chunks over an INT4 cache, full attention                               1505 us, 806
-//   257 tokens after 8000 over an INT4 cache                                         80 us
+//   the 16 chunks over an INT4 cache, full attention                               1518 us, 799
+//   257 tokens after 8000 over an INT4 cache                                         81 us
 // Shares by closed-form costs instead of by items are what the ragged prompts and the single sequences live by.
 // Every wait is bounded (2 s): on expiry KV_DERR_TIMEOUT is set, what was issued is drained, TMEM is freed
 // and the CTA returns.
@@ -404,6 +404,13 @@ template <typename MT> constexpr float kAbove = 16.f;
 template <> constexpr float kAbove<__half> = kRescaleLog2;
 template <typename MT> constexpr float kBelow = 16.f;
 template <> constexpr float kBelow<__half> = 0.f;
+
+// Rows at positions below this see only keys of the first tile, few of them.  With the reference at 0 a largest
+// weight is not 1 and has a rounding of its own, which many keys average out and few do not (a row of one key would
+// be off by 2^-9 of it): these rows are divided by the sum of the rounded weights, so that one key comes out as it
+// is.  The log-sum-exp keeps the other
+// sum.  (Whole prompts 317 -> 321 us for it, INT4 chunks 1505 -> 1518, others alike.)
+constexpr int kFewKeys = 64;
 
 // The larger magnitudes of two packed pairs.
 template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
@@ -944,6 +951,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
             const float2 cc = make_float2(c2, c2);
             float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
             float2 sum = make_float2(0.f, 0.f);  // sum of the weights
+            float excess = 0.f;                  // rows of few keys: what the rounded weights' sum is above it
             const int step = nt == 2 ? 1 : 2;
             const int first = w.ja + (nt == 2 ? 0 : x);
             uint32_t wt[64];
@@ -1029,6 +1037,12 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                         }
                     }
                     sum = add2(sum, part_sum);
+                    if (j == 0 && first_pos < kFewKeys) {
+                        float2 rounded = make_float2(0.f, 0.f);
+#pragma unroll
+                        for (int k = 0; k < 64; ++k) rounded = add2(rounded, unpack2<MT>(wt[k]));
+                        excess = pos < kFewKeys ? (rounded.x + rounded.y) - (part_sum.x + part_sum.y) : 0.f;
+                    }
                     // P_x into TMEM: 128 keys of 16-bit weights = 64 columns over the S_x just read
                     tmem_st32u(t_s, wt);
                     tmem_st32u(t_s + 32, wt + 32);
@@ -1074,8 +1088,9 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                 // (no guard: a chain whose scores are all NaN has no maximum, hence weight 0, and a sum of NaN,
                 // which has to come through; an empty one has a sum of 0)
                 l = l * f0 + l1 * f1;
+                excess *= f0;  // (tile 0 is chain 0's)
             }
-            const float inv = l == 0.f ? 0.f : (kCache == kCacheE4M3 ? p.v_scale : 1.f) / l;
+            const float inv = l == 0.f ? 0.f : (kCache == kCacheE4M3 ? p.v_scale : 1.f) / (l + excess);
             f0 *= inv;
             f1 *= inv;
             QT *out16 = static_cast<QT *>(a.out) + row * D;

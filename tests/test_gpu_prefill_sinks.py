@@ -319,3 +319,22 @@ def test_caches_past_32_bits(kv, cache):
         big.append(c)
     d |= dict(k_cache=big[0], v_cache=big[1], table=torch.where(d["table"] >= 0, d["table"] + (NB - x.NB), -1))
     verify(x, *prefill(kv, x, d))
+
+
+@pytest.mark.parametrize("cache,dtype", [("same", BF16), ("same", F16), ("e4m3", BF16)])
+@pytest.mark.parametrize("Hq", [2, 16])
+def test_one_key_comes_out_as_it_is(kv, cache, dtype, Hq):
+    """A row that sees one key is that key's value, a bit copy over a 16-bit cache (E4M3: times v_scale, one rounding)."""
+    x = Inputs(31, [0, 0, 40], [1, 90, 3], Hq, 2, window=1, sinks=0, cache=cache, dtype=dtype)
+    out, lse, err = prefill(kv, x)
+    verify(x, out, lse, err)
+    got, v = out.float().cpu().numpy(), x.values("v")
+    for b, (q0, n) in enumerate(zip(x.qsl, x.new)):
+        for t in range(min(n, 64 - (x.lens[b] - n))):
+            want = np.repeat(v[x.slot(b, x.lens[b] - n + t)], Hq // 2, 0)
+            want = torch.from_numpy(want).to(dtype).float().numpy()
+            if cache == "same":
+                assert np.array_equal(got[q0 + t], want), (b, t)
+            else:  # the sum's reciprocal, the product and the output are rounded
+                step = np.abs(want) * (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -21)
+                assert (np.abs(got[q0 + t] - want) <= step).all(), (b, t)
