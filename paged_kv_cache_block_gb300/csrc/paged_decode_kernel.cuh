@@ -962,11 +962,12 @@ __global__ void __maxnreg__(DecodeLaunch<RN>::kMaxRegs)
                 if (__any_sync(0xffffffffu, nonfinite != 0)) {
                     // the values set aside, added to the rows that see their keys: as the weight is above
                     // 0, the value itself will do.  The keys are the q_len - 1 at each edge of what the
-                    // window and the rows' own tokens leave in full view.
+                    // window and the rows' own tokens leave in full view; the rows' own are among them where
+                    // the sinks reach past the first row, too.
                     const int hidden = sink_axis(kp, len_of(seq), bs_shift).hidden;
                     const int from = seg_k0 * ST, to = min(L, (k_last + 1) * ST);
                     const int edge = max(key_lo, kp.sinks.num_sinks), view = max(edge, lo_last);
-                    for (int t = edge; t < L; ++t) {
+                    for (int t = min(edge, hi_first + 1); t < L; ++t) {
                         if (t >= view && t <= hi_first) {  // seen by every row
                             t = hi_first;
                             continue;
