@@ -1,5 +1,7 @@
 // Prefill attention with a sliding window and sinks: the plan, the launch, and the instantiations over
 // 16-bit caches (those over E4M3 and INT4 caches: prefill_sinks_wide.cu).
+#include <algorithm>
+
 #include "prefill_sinks.cuh"
 
 namespace pkv {
@@ -34,8 +36,10 @@ cudaError_t launch_prefill_sinks(const CUtensorMap &tq, const CUtensorMap &tk, c
     p.t.key_shift = plan.key_shift;
     p.t.workers = plan.workers;
     p.t.rows_per_item = plan.rows_per_item;
-    const int row_tiles = (a.t.max_query_len + plan.tokens_per_tile - 1) / plan.tokens_per_tile;
-    p.t.items_per_seq = (row_tiles + 1) / 2 * a.t.num_kv_heads;
+    // max_query_len may be any bound: no accepted sequence has more rows than there are tokens
+    const int64_t most = std::min(a.t.max_query_len, a.t.num_tokens);
+    const int64_t row_tiles = (most + plan.tokens_per_tile - 1) / plan.tokens_per_tile;
+    p.t.items_per_seq = static_cast<int>((row_tiles + 1) / 2 * a.t.num_kv_heads);
     char *ws = static_cast<char *>(workspace);
     p.t.ws_first = reinterpret_cast<int4 *>(ws);
     p.t.ws_lse = reinterpret_cast<float *>(ws + plan.lse_off);

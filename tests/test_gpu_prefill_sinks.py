@@ -338,3 +338,17 @@ def test_one_key_comes_out_as_it_is(kv, cache, dtype, Hq):
             else:  # the sum's reciprocal, the product and the output are rounded
                 step = np.abs(want) * (2.0 ** -8 + 2.0 ** -8 + 2.0 ** -21)
                 assert (np.abs(got[q0 + t] - want) <= step).all(), (b, t)
+
+
+@pytest.mark.parametrize("cache", ["same", "int4"])
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (8, 8), (128, 1), (256, 2)])
+def test_a_loose_bound_of_the_rows(kv, cache, Hq, Hkv):
+    """Any max_query_len above the true one gives the tight one's bits: the items to merge are counted without it."""
+    x = Inputs(32, [700, 0, 30], [5, 40, 1], Hq, Hkv, window=400, sinks=4, cache=cache)
+    d = x.device()
+    want = prefill(kv, x, d)
+    verify(x, *want)
+    # (of a tile of one token, 2^29 .. 2^30 + 2 made a product of 2^31 and more)
+    for bound in (41, 4096, 2 ** 29, 2 ** 30 + 2, 2 ** 31 - 1):
+        out, lse, err = prefill(kv, x, d, max_query_len=bound)
+        assert err == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
