@@ -27,8 +27,9 @@
  *     infinities included).  A NaN score that it does see makes its result and log-sum-exp NaN; a NaN
  *     or an infinity in a value that it does see reaches that dim of its result.
  *   - Softmax sums are float32, of the weights before they are rounded to 16 bits for the second product
- *     (INT4 decode: of the rounded weights, whose codes' offset comes out exactly with them; prefill rows
- *     that see only a few keys are divided by the rounded weights' sum too).  fp16
+ *     (INT4 decode: of the rounded weights, whose codes' offset comes out exactly with them; prefill: the
+ *     result is divided by a sum that takes the largest weight of each 128 keys as it was rounded).  A row
+ *     whose weight lies with one key is that key's value, rounded once.  fp16
  *     weights are formed 2^14 (prefill: 2^7) higher than they are, so that the many small weights beside
  *     a sink that holds nearly all of them keep their digits.
  */

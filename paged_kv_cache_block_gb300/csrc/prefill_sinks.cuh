@@ -86,8 +86,8 @@ template <int D> struct Tile {
     static constexpr int kGroup = kHalves * 1024;       // 8 keys of a K or V tile: [64 dims of D][key][dim]
     static constexpr int kStages = D == 128 ? 4 : 8;    // ring entries (128 KB)
     static constexpr int kOffKV = 2 * kBytes;           // after Q_0, Q_1
-    static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // chain 1's maxima and sums: 2 x 128 floats
-    static constexpr int kOffScratch = kOffJoin + 2 * 128 * 4;   // of the schedule
+    static constexpr int kOffJoin = kOffKV + kStages * kBytes;   // chain 1's maxima, sums and excess: 3 x 128 floats
+    static constexpr int kOffScratch = kOffJoin + 3 * 128 * 4;   // of the schedule
     static constexpr int kScratchBytes = 512;
     static constexpr int kOffBar = kOffScratch + kScratchBytes;
     static constexpr int kNumBars = 14 + 2 * kStages;
@@ -405,12 +405,15 @@ template <> constexpr float kAbove<__half> = kRescaleLog2;
 template <typename MT> constexpr float kBelow = 16.f;
 template <> constexpr float kBelow<__half> = 0.f;
 
-// Rows at positions below this see only keys of the first tile, few of them.  With the reference at 0 a largest
-// weight is not 1 and has a rounding of its own, which many keys average out and few do not (a row of one key would
-// be off by 2^-9 of it): these rows are divided by the sum of the rounded weights, so that one key comes out as it
-// is.  The log-sum-exp keeps the other
-// sum.  (Whole prompts 317 -> 321 us for it, INT4 chunks 1505 -> 1518, others alike.)
-constexpr int kFewKeys = 64;
+// The sum is of the weights before their rounding.  With a reference that is not a row's maximum its largest weight is
+// not 1 and has a rounding of its own, up to 2^-9 of it in bf16, which stays in the result where that key holds most of
+// the row's weight: a sink, or the only key of a row.  So the result is divided by the sum and the `excess`, what the
+// rounding added to the largest weight of each tile: six instructions a row and tile.  Worked out in 64 bits, the
+// error over that of rounding the result alone, with the excess / with a sum of all rounded weights / without: 1.00 /
+// 1.00 / off by the weight's rounding for one key, 1.12 / 1.11 / 1.40 for two, 1.27 / 1.26 / 1.42 for 8, 1.38 / 1.37 /
+// 1.40 for 128, 1.02 / 1.02 / 1.41 for 128 with one 2^10 above the others.  The log-sum-exp is the plain sum's.
+__device__ __forceinline__ float rounding_of(float x, __half) { return __half2float(__float2half_rn(x)) - x; }
+__device__ __forceinline__ float rounding_of(float x, __nv_bfloat16) { return __bfloat162float(__float2bfloat16_rn(x)) - x; }
 
 // The larger magnitudes of two packed pairs.
 template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b) {
@@ -951,7 +954,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
             const float2 cc = make_float2(c2, c2);
             float m_used = -INFINITY;  // the reference maximum of O and the sums, in log2 units
             float2 sum = make_float2(0.f, 0.f);  // sum of the weights
-            float excess = 0.f;                  // rows of few keys: what the rounded weights' sum is above it
+            float excess = 0.f;                  // what the largest weights' rounding adds to it
             const int step = nt == 2 ? 1 : 2;
             const int first = w.ja + (nt == 2 ? 0 : x);
             uint32_t wt[64];
@@ -980,6 +983,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                         tmem_wait_st();
                     }
                     float2 part_sum;
+                    float part_excess;
                     // One pass over the tile's S: weights against the reference in use (0 at first), the tile
                     // maximum tracked alongside, 32 columns at a time with the next load in flight.  A second one
                     // when the reference has to move.
@@ -1007,6 +1011,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                                 part_sum = add2(part_sum, x2);
                             }
                         }
+                        part_excess = rounding_of(fast_exp2(fmaf(mraw, c2, nref)), MT());  // (as the pass formed it)
                         if (again) break;
                         // scale > 0, so the scaled maximum is the maximum of the scaled scores
                         const float mt = mraw == -INFINITY ? -INFINITY : mraw * c2;
@@ -1021,6 +1026,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                         if (moved) {
                             m_used = mt;
                             sum.x *= f, sum.y *= f;
+                            excess *= f;
                         }
                         if (__any_sync(0xffffffffu, rescale)) {
                             // the warp loads and stores O together; rows that keep their maximum scale by 1
@@ -1037,12 +1043,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                         }
                     }
                     sum = add2(sum, part_sum);
-                    if (j == 0 && first_pos < kFewKeys) {
-                        float2 rounded = make_float2(0.f, 0.f);
-#pragma unroll
-                        for (int k = 0; k < 64; ++k) rounded = add2(rounded, unpack2<MT>(wt[k]));
-                        excess = pos < kFewKeys ? (rounded.x + rounded.y) - (part_sum.x + part_sum.y) : 0.f;
-                    }
+                    excess += part_excess;
                     // P_x into TMEM: 128 keys of 16-bit weights = 64 columns over the S_x just read
                     tmem_st32u(t_s, wt);
                     tmem_st32u(t_s + 32, wt + 32);
@@ -1062,9 +1063,10 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
             bool use1 = false;
             if (nt == 1) {
                 if (x == 1) {
-                    // hand the maximum and sum to chain 0's thread of the same row, which joins the two
+                    // hand the maximum and sums to chain 0's thread of the same row, which joins the two
                     join[r] = m;
                     join[128 + r] = l;
+                    join[256 + r] = excess;
                     tc_fence_before();
                     mbar_arrive(bar(kBarJoin));
                     if (!wait_all(bar(kBarJoined), njoin++ & 1)) {
@@ -1088,7 +1090,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                 // (no guard: a chain whose scores are all NaN has no maximum, hence weight 0, and a sum of NaN,
                 // which has to come through; an empty one has a sum of 0)
                 l = l * f0 + l1 * f1;
-                excess *= f0;  // (tile 0 is chain 0's)
+                excess = excess * f0 + join[256 + r] * f1;
             }
             const float inv = l == 0.f ? 0.f : (kCache == kCacheE4M3 ? p.v_scale : 1.f) / (l + excess);
             f0 *= inv;

@@ -5,6 +5,7 @@ import pytest
 import torch
 
 from tests.sinks_reference import BF16, F16, Inputs, check
+from tests.step_reference import HALF, TINY
 
 pytestmark = pytest.mark.gpu
 
@@ -352,3 +353,59 @@ def test_a_loose_bound_of_the_rows(kv, cache, Hq, Hkv):
     for bound in (41, 4096, 2 ** 29, 2 ** 30 + 2, 2 ** 31 - 1):
         out, lse, err = prefill(kv, x, d, max_query_len=bound)
         assert err == 0 and torch.equal(out, want[0]) and torch.equal(lse, want[1])
+
+
+def one_rounding(x, out, want, acc=0.0):
+    """out within acc (and float32's 2^-21) of want, rounded once (to a subnormal: half its step, which also
+    keeps the quotient of the check defined where a value is 0)."""
+    acc = acc + 2.0 ** -21 * np.abs(want)
+    check(out, want, acc + HALF[x.dtype] * (np.abs(want) + acc) + TINY[x.dtype], "out")
+
+
+@pytest.mark.parametrize("cache,dtype", CACHES)
+@pytest.mark.parametrize("Hq,D", [(2, 128), (16, 128), (16, 64)])
+def test_one_key_at_any_position(kv, cache, dtype, Hq, D):
+    """A window of one key: each row is that key's value wherever it stands in the sequence."""
+    if D == 64 and cache != "same":
+        pytest.skip("128 dims alone")
+    x = Inputs(33, [0, 100, 1000, 63], [200, 3, 150, 2], Hq, 2, D, window=1, sinks=0, cache=cache, dtype=dtype)
+    out, lse, err = prefill(kv, x)
+    verify(x, out, lse, err)
+    v = x.values("v")
+    rows = [v[x.slot(b, L - n + t)] for b, (L, n) in enumerate(zip(x.lens, x.new)) for t in range(n)]
+    want = np.repeat(np.stack(rows), Hq // 2, 1)
+    one_rounding(x, out, want)
+    if cache == "same":
+        assert np.array_equal(out.double().cpu().numpy(), want)
+
+
+@pytest.mark.parametrize("cache,dtype", CACHES)
+@pytest.mark.parametrize("workers", [0, 1, 40])
+@pytest.mark.parametrize("new", [1, 5, 300])
+@pytest.mark.parametrize("at", [0, 480])
+def test_rows_of_one_heavy_key(kv, cache, dtype, workers, new, at):
+    """A key that holds nearly all of every row's weight, a sink or one in the window: its value and one rounding."""
+    x = Inputs(34, [500], [new], 8, 2, window=400, sinks=1, cache=cache, dtype=dtype)
+    rng = np.random.default_rng(35)
+    x.q = torch.from_numpy(1 + 0.25 * rng.standard_normal(x.q.shape)).to(dtype)
+    blk, off = x.slot(0, at)
+    # scores of about `heavy` and `others` in powers of 2, near the reference that the kernel begins with: a key far
+    # above it has a weight of 1, which has no rounding
+    heavy, others = (6.5, -25.0) if at == 0 else (14.5, -14.5)
+    unit = x.scale * 128 / np.log(2)
+    if cache == "int4":
+        code = 2 if at == 0 else 7
+        x.k_scales[:] = heavy / unit / code
+        x.k_cache[:] = 0x88 if at == 0 else 0x99   # -8, -7
+        x.k_cache[blk, off] = code * 0x11
+    else:
+        x.k_cache = torch.full(x.k_cache.shape, others / unit / x.k_scale).to(x.k_cache.dtype)
+        x.k_cache[blk, off] = torch.full(x.k_cache.shape[2:], heavy / unit / x.k_scale).to(x.k_cache.dtype)
+    r = x.reference()
+    out, lse, err = prefill(kv, x, num_workers=workers)
+    verify(x, out, lse, err)
+    # (32 products of 16 keys or fewer: each addition to the heavy key's, of next to nothing, is off by 2^-23 at most)
+    v = np.abs(x.values("v"))
+    one_rounding(x, out, r["out"], 2.0 ** -18 * float(v[np.isfinite(v)].max()))
+    value = np.repeat(x.values("v")[blk, off], 4, 0)
+    assert np.abs(r["out"] - value).max() < 2.0 ** -17 * v[np.isfinite(v)].max(), "the inputs are what they claim"
