@@ -399,11 +399,15 @@ __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
 // How far (log2) a row's maximum may exceed the reference in use, and how far below the first one, 0, it may
-// lie: bf16 has float's exponents; fp16 weights are formed 2^7 higher, the largest then at 2^7 .. 2^15.
+// lie: bf16 has float's exponents; fp16 weights are formed 2^7 higher (kFactor), the largest then at 2^7 .. 2^15.
 template <typename MT> constexpr float kAbove = 16.f;
 template <> constexpr float kAbove<__half> = kRescaleLog2;
 template <typename MT> constexpr float kBelow = 16.f;
 template <> constexpr float kBelow<__half> = 0.f;
+// log2 of a factor on all weights: bf16 weights are formed as much lower, at most 1, so that no value near bf16's
+// largest is multiplied beyond float's range (values above 2^111 were, by weights of up to 2^16).
+template <typename MT> constexpr float kFactor = -kAbove<MT>;
+template <> constexpr float kFactor<__half> = kWeightLog2<__half>;
 
 // The sum is of the weights before their rounding.  With a reference that is not a row's maximum its largest weight is
 // not 1 and has a rounding of its own, up to 2^-9 of it in bf16, which stays in the result where that key holds most of
@@ -990,7 +994,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
 #pragma unroll 1
                     for (bool again = false;; again = true) {
                         const bool none = m_used == -INFINITY;  // no key seen so far
-                        const float nref = kWeightLog2<MT> - (none ? 0.f : m_used);
+                        const float nref = kFactor<MT> - (none ? 0.f : m_used);
                         const float2 ref2 = make_float2(nref, nref);
                         float mraw = -INFINITY;
                         part_sum = make_float2(0.f, 0.f);
@@ -1146,7 +1150,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
             }
             __syncwarp();  // (a row is written by the lanes of its quad)
             if (valid) {
-                const float lse2 = l == 0.f ? -INFINITY : m + (log2f(l) - kWeightLog2<MT>);
+                const float lse2 = l == 0.f ? -INFINITY : m + (log2f(l) - kFactor<MT>);
                 if (!w.whole) *part_lse(p.t, slot, prow) = lse2;
                 else if (a.lse_out) a.lse_out[row] = lse2 * 0.69314718055994531f;
                 if constexpr (kCache != kCacheInt4) {

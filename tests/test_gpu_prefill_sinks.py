@@ -409,3 +409,21 @@ def test_rows_of_one_heavy_key(kv, cache, dtype, workers, new, at):
     one_rounding(x, out, r["out"], 2.0 ** -18 * float(v[np.isfinite(v)].max()))
     value = np.repeat(x.values("v")[blk, off], 4, 0)
     assert np.abs(r["out"] - value).max() < 2.0 ** -17 * v[np.isfinite(v)].max(), "the inputs are what they claim"
+
+
+@pytest.mark.parametrize("workers", [0, 1])
+@pytest.mark.parametrize("new,Hq,D", [(3, 8, 128), (200, 8, 128), (60, 4, 64)])
+def test_values_near_the_largest(kv, workers, new, Hq, D):
+    """Values of 2^120 under scores that rise by powers of two: a weighted mean never leaves their range."""
+    x = Inputs(36, [500], [new], Hq, 2, D, window=300, sinks=4)
+    x.v_cache = (x.v_cache.float() * 2.0 ** 120).to(BF16)
+    x.q = torch.ones_like(x.q)
+    k = torch.zeros(x.k_cache.shape)
+    unit = x.scale * D / np.log(2)
+    for p in range(500 + new):
+        if p < 4 or p > 200:  # from 2^-14 to 2^14
+            k[x.slot(0, p)] = (28 * p / (500 + new) - 14) / unit
+    x.k_cache = k.to(BF16)
+    r = x.reference()
+    assert np.isfinite(r["out"]).all() and np.abs(r["out"]).max() > 2.0 ** 116
+    verify(x, *prefill(kv, x, num_workers=workers))
