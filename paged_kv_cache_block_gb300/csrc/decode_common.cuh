@@ -191,9 +191,12 @@ __device__ __forceinline__ bool build_schedule(const KernelParams &kp, const Dec
     return any_rejected;  // (an item without stages is one of a rejected length)
 }
 
-// Whether a piece of weight w counts in a merge: one of weight 0 (no key seen) adds nothing.  kNan:
-// a piece whose weight is NaN (a score that its row sees was NaN) counts, so that the NaN stays.
+// Whether a sum of weights w counts: one of 0 (no key seen) gives nothing.  kNan: one that is NaN (a score that
+// its row sees was NaN) counts, so that the NaN stays.
 template <bool kNan> __device__ __forceinline__ bool counts(float w) { return kNan ? w != 0.f : w > 0.f; }
+// The same of a piece in a merge, with its lse.  kNan: every piece that saw a key counts, at a weight that has
+// underflowed to 0 too: a NaN or an infinity that it holds stays (as NaN), as it would in one piece with the others.
+template <bool kNan> __device__ __forceinline__ bool counts(float w, float lse) { return kNan ? lse != -INFINITY : w > 0.f; }
 
 // One warp per (item, row): combine the pieces of a sequence that several CTAs shared, and
 // write zeros (lse -inf) for sequences whose length was rejected.  P is the stage prefix.
@@ -259,9 +262,9 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
         for (int o = 16; o > 0; o >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, o);
 #pragma unroll
         for (int u = 0; u < kFewPieces; ++u) {
-            const float wu = __shfl_sync(0xffffffffu, wl, u);
+            const float wu = __shfl_sync(0xffffffffu, wl, u), lu = kNan ? __shfl_sync(0xffffffffu, lv, u) : 0.f;
 #pragma unroll
-            for (int e = 0; e < kPer; ++e) acc[e] += counts<kNan>(wu) ? wu * v[u][e] : 0.f;
+            for (int e = 0; e < kPer; ++e) acc[e] += counts<kNan>(wu, lu) ? wu * v[u][e] : 0.f;
         }
     } else {
         for (int c = c_lo + lane; c <= c_hi; c += 32)
@@ -274,9 +277,11 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
             // four pieces at a time, every load issued before the sums use them
             for (int base = c_lo; base <= c_hi; base += 32) {
                 const int c = base + lane;
-                float wl = 0.f;
-                if (c <= c_hi && !empty_share(c))
-                    wl = expf(__ldcg(a.ws_lse + static_cast<int64_t>(item + c) * kp.rows_per_item + rr) - ref);
+                float wl = 0.f, ll = -INFINITY;
+                if (c <= c_hi && !empty_share(c)) {
+                    ll = __ldcg(a.ws_lse + static_cast<int64_t>(item + c) * kp.rows_per_item + rr);
+                    wl = expf(ll - ref);
+                }
                 float wsb = wl;
 #pragma unroll
                 for (int o = 16; o > 0; o >>= 1) wsb += __shfl_xor_sync(0xffffffffu, wsb, o);
@@ -287,7 +292,8 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
 #pragma unroll
                     for (int u = 0; u < 4; ++u) {
                         w[u] = __shfl_sync(0xffffffffu, wl, (u0 + u) & 31);
-                        const bool ok = u0 + u < nb && counts<kNan>(w[u]);  // a piece of weight 0 adds nothing
+                        const float lu = kNan ? __shfl_sync(0xffffffffu, ll, (u0 + u) & 31) : 0.f;
+                        const bool ok = u0 + u < nb && counts<kNan>(w[u], lu);  // a piece without keys adds nothing
                         const float *src =
                             a.ws_o + (static_cast<int64_t>(item + base + u0 + u) * kp.rows_per_item + rr) * D + lane * kPer;
 #pragma unroll
@@ -359,8 +365,8 @@ __global__ void __launch_bounds__(256) lse_merge_long_kernel(const __grid_consta
             for (int e = 0; e < kPer; ++e) acc[e] *= f;
 #pragma unroll
             for (int u = 0; u < kG; ++u) {
-                const float w = l[u] == -INFINITY ? 0.f : expf(l[u] - ref);
-                if (!counts<true>(w)) continue;
+                const float w = expf(l[u] - ref);
+                if (!counts<true>(w, l[u])) continue;
                 wsum += w;
 #pragma unroll
                 for (int e = 0; e < kPer; ++e) acc[e] += w * v[u][e];

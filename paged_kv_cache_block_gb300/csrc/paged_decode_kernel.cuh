@@ -1168,13 +1168,14 @@ __global__ void __launch_bounds__(128) tile_merge_kernel(const __grid_constant__
                     }
                     wsum[nt][0] += w0;
                     wsum[nt][1] += w1;
-                    // pieces of weight 0 (empty rows) may hold anything: selected away, never multiplied
+                    // pieces without keys (empty rows) may hold anything: selected away, never multiplied
+                    const bool c0 = counts<kNan>(w0, wl[u][nt][0]), c1 = counts<kNan>(w1, wl[u][nt][1]);
 #pragma unroll
                     for (int m = 0; m < kMW; ++m) {
-                        acc[m][nt][0] += counts<kNan>(w0) ? w0 * v[u][nt][m].x : 0.f;
-                        acc[m][nt][1] += counts<kNan>(w1) ? w1 * v[u][nt][m].y : 0.f;
-                        acc[m][nt][2] += counts<kNan>(w0) ? w0 * v[u][nt][m].z : 0.f;
-                        acc[m][nt][3] += counts<kNan>(w1) ? w1 * v[u][nt][m].w : 0.f;
+                        acc[m][nt][0] += c0 ? w0 * v[u][nt][m].x : 0.f;
+                        acc[m][nt][1] += c1 ? w1 * v[u][nt][m].y : 0.f;
+                        acc[m][nt][2] += c0 ? w0 * v[u][nt][m].z : 0.f;
+                        acc[m][nt][3] += c1 ? w1 * v[u][nt][m].w : 0.f;
                     }
                 }
         }
@@ -1258,8 +1259,8 @@ __global__ void __launch_bounds__(256) tile_merge_long_kernel(const __grid_const
                     acc[0][nt][e] *= f, acc[0][nt][2 + e] *= f;
 #pragma unroll
                     for (int u = 0; u < kG; ++u) {
-                        const float w = l[u][nt][e] == -INFINITY ? 0.f : expf(l[u][nt][e] - ref);
-                        if (!counts<true>(w)) continue;
+                        const float w = expf(l[u][nt][e] - ref);
+                        if (!counts<true>(w, l[u][nt][e])) continue;
                         sum[nt][e] += w;
                         acc[0][nt][e] += w * (e ? v[u][nt].y : v[u][nt].x);
                         acc[0][nt][2 + e] += w * (e ? v[u][nt].w : v[u][nt].z);

@@ -1064,7 +1064,7 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
             tc_fence_after();
             float m = m_used, l = sum.x + sum.y;
             float f0 = 1.f, f1 = 0.f;  // weights of O_0 (O_x with two row tiles) and O_1 in the result
-            bool use1 = false;
+            bool seen0 = false, seen1 = false, use1 = false;
             if (nt == 1) {
                 if (x == 1) {
                     // hand the maximum and sums to chain 0's thread of the same row, which joins the two
@@ -1089,6 +1089,10 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                 const float mm = fmaxf(m, m1);
                 f0 = m == -INFINITY ? 0.f : fast_exp2(m - mm);
                 f1 = m1 == -INFINITY ? 0.f : fast_exp2(m1 - mm);
+                // a chain that saw keys counts at a weight that underflows to 0 too (a NaN or an infinity in its O
+                // stays, as NaN)
+                seen0 = m != -INFINITY;
+                seen1 = m1 != -INFINITY;
                 use1 = w.jb - w.ja > 1;
                 m = mm;
                 // (no guard: a chain whose scores are all NaN has no maximum, hence weight 0, and a sum of NaN,
@@ -1099,6 +1103,8 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
             const float inv = l == 0.f ? 0.f : (kCache == kCacheE4M3 ? p.v_scale : 1.f) / (l + excess);
             f0 *= inv;
             f1 *= inv;
+            seen0 |= f0 != 0.f;
+            seen1 |= f1 != 0.f;
             QT *out16 = static_cast<QT *>(a.out) + row * D;
             const int prow = (nt == 2 ? x * 128 : 0) + r;
             const int64_t slot = part_slot(c, w.ja == 0);
@@ -1111,15 +1117,15 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                     float o[32];
                     tmem_ld32(t_o + ch * 32, o);
                     tmem_wait_ld();
-                    // a row of weight 0 in a chain has nothing there, whatever O holds
+                    // a row that sees no key in a chain has nothing there, whatever O holds
 #pragma unroll
-                    for (int k = 0; k < 32; ++k) o[k] = f0 != 0.f ? o[k] * f0 : 0.f;
+                    for (int k = 0; k < 32; ++k) o[k] = seen0 ? o[k] * f0 : 0.f;
                     if (use1) {
                         float o1[32];
                         tmem_ld32(trow + kColO + 128 + ch * 32, o1);
                         tmem_wait_ld();
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) o[k] += f1 != 0.f ? o1[k] * f1 : 0.f;
+                        for (int k = 0; k < 32; ++k) o[k] += seen1 ? o1[k] * f1 : 0.f;
                     }
                     if constexpr (kCache == kCacheInt4) {
                         // times the V scales, the dims of each eight back in order
@@ -1205,7 +1211,7 @@ static __global__ void __launch_bounds__(256, 4) merge_items_kernel(const __grid
     const int4 sq = __ldcg(&p.ws_first[2 * first + 1]);
     if (Joined::row_of(p, sq, idx, rr) < 0) return;
     Joined x;
-    x.add_pieces<D>(p, first - 1, first - 1, 1, first - 1 + count, rr, q);
+    x.add_pieces<D, true>(p, first - 1, first - 1, 1, first - 1 + count, rr, q);
     x.store<T, D>(p, sq, idx, rr, q);
 }
 
@@ -1229,7 +1235,8 @@ static cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, co
     if (items <= p.t.workers)
         return launch_dependent(merge_items_kernel<QT, D>, dim3(static_cast<unsigned>(items), p.t.rows_per_item / 32 * (D / 8) / 8),
                                 dim3(256), 0, stream, p.t);
-    return launch_tree_merge<QT, D>(p.t, stream);
+    return launch_dependent(tree_merge_kernel<QT, D, true>, dim3(p.t.workers - 1, p.t.rows_per_item / 32 * (D / 8) / 8),
+                            dim3(256), 0, stream, p.t);
 }
 
 }  // namespace sinks

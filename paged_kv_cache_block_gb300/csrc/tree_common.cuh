@@ -368,8 +368,9 @@ struct Joined {
 #pragma unroll
         for (int e = 0; e < 8; ++e) acc[e] = 0.f;
     }
-    // Further pieces: their lse (-inf: nothing seen, or no piece) and 8 dims.
-    template <int N> __device__ __forceinline__ void add(const float (&l)[N], const float4 (&v)[N][2]) {
+    // Further pieces: their lse (-inf: nothing seen, or no piece) and 8 dims.  kKeep: a piece that saw keys counts at
+    // a weight that has underflowed to 0 too, so that a NaN or an infinity that it holds stays (as NaN).
+    template <bool kKeep, int N> __device__ __forceinline__ void add(const float (&l)[N], const float4 (&v)[N][2]) {
         float m = mx;
         bool nan = false;
 #pragma unroll
@@ -383,14 +384,14 @@ struct Joined {
 #pragma unroll
         for (int u = 0; u < N; ++u) {
             const float w = l[u] == -INFINITY ? 0.f : fast_exp2(l[u] - mx);
-            if (w == 0.f) continue;  // it adds nothing, whatever it holds
+            if (kKeep ? l[u] == -INFINITY : w == 0.f) continue;  // it adds nothing, whatever it holds
             wsum += w;
             acc[0] += w * v[u][0].x, acc[1] += w * v[u][0].y, acc[2] += w * v[u][0].z, acc[3] += w * v[u][0].w;
             acc[4] += w * v[u][1].x, acc[5] += w * v[u][1].y, acc[6] += w * v[u][1].z, acc[7] += w * v[u][1].w;
         }
     }
     // Pieces e0, e0 + step, .. up to `last` of the item that starts in share c: row rr, the dims of float4s q, q + 1.
-    template <int D>
+    template <int D, bool kKeep>
     __device__ __forceinline__ void add_pieces(const TreeParams &p, int c, int e0, int step, int last, int rr, int q) {
         for (; e0 <= last; e0 += kPieces * step) {
             float l[kPieces];
@@ -405,7 +406,7 @@ struct Joined {
                 v[u][0] = in ? __ldcg(src) : make_float4(0.f, 0.f, 0.f, 0.f);
                 v[u][1] = in ? __ldcg(src + p.rows_per_item) : make_float4(0.f, 0.f, 0.f, 0.f);
             }
-            add(l, v);
+            add<kKeep>(l, v);
         }
     }
     // The joined result of that row of item idx of a sequence (sq: its second record), if the row exists.
@@ -442,7 +443,7 @@ struct Joined {
 };
 
 // A CTA a share c (and 8 units of 8 dims of 32 rows): the item that starts in it and goes on into the next ones.
-template <typename T, int D>
+template <typename T, int D, bool kKeep = false>
 static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_constant__ TreeParams p) {
     const int c = blockIdx.x, lane = threadIdx.x & 31;
     const int unit = blockIdx.y * 8 + (threadIdx.x >> 5);
@@ -473,7 +474,7 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_kernel(const __grid_
     }
     if (Joined::row_of(p, sq, idx, rr) < 0) return;
     Joined x;
-    x.add_pieces<D>(p, c, c, 1, last, rr, q);
+    x.add_pieces<D, kKeep>(p, c, c, 1, last, rr, q);
     x.store<T, D>(p, sq, idx, rr, q);
 }
 
@@ -501,7 +502,7 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_long_kernel(const __
     const int4 sq = __ldcg(&p.ws_first[2 * first + 1]);
     const int c = first - 1, last = c + count;
     Joined x;  // (a row that does not exist is read as it is, and not stored)
-    x.add_pieces<D>(p, c, c + warp, 8, last, rr, q);
+    x.add_pieces<D, false>(p, c, c + warp, 8, last, rr, q);
     // each warp's result as one more piece
     lse[warp][lane] = x.wsum == 0.f ? -INFINITY : x.mx + log2f(x.wsum);
     const float inv = x.wsum == 0.f ? 0.f : 1.f / x.wsum;
@@ -516,7 +517,7 @@ static __global__ void __launch_bounds__(256, 4) tree_merge_long_kernel(const __
         float4 v[kPieces][2];
 #pragma unroll
         for (int u = 0; u < kPieces; ++u) l[u] = lse[w0 + u][lane], v[u][0] = part[w0 + u][0][lane], v[u][1] = part[w0 + u][1][lane];
-        y.add(l, v);
+        y.add<false>(l, v);
     }
     y.store<T, D>(p, sq, idx, rr, q);
 }
