@@ -1541,6 +1541,8 @@ static kv_status check_prefill_sinks_sizes(int32_t num_seqs, int32_t max_query_l
     if (num_q_heads / num_kv_heads > 128)
         return fail(KV_ERR_UNSUPPORTED, "prefill: num_q_heads / num_kv_heads must be at most 128");
     const bool wide = cache_dtype == KV_FP8_E4M3 || cache_dtype == KV_INT4;
+    if (!wide && cache_dtype != KV_F16 && cache_dtype != KV_BF16)
+        return fail(KV_ERR_UNSUPPORTED, "prefill: cache dtype %d", static_cast<int>(cache_dtype));
     if (head_dim != 128 && (head_dim != 64 || wide))
         return fail(KV_ERR_UNSUPPORTED, "prefill: head_dim %d (supported: 64, 128; E4M3 and INT4 caches: 128)", head_dim);
     if (num_workers > 32767) return fail(KV_ERR_UNSUPPORTED, "prefill: num_workers > 32767");

@@ -225,3 +225,11 @@ def test_manager_shares_sinks_after_the_window_has_moved(kc):  # noqa: F811
 def test_manager_refuses_negative_sinks(kc):  # noqa: F811
     with pytest.raises(kc.KVError):
         kc.BlockManager(64, 4, 3, 40, window=8, num_sinks=-1)
+
+
+@pytest.mark.parametrize("dtype", [-1, 4, 5, 17, 2 ** 31 - 1])
+@pytest.mark.parametrize("head_dim", [64, 128])
+def test_workspace_of_no_cache_type(kc, dtype, head_dim):  # noqa: F811
+    with pytest.raises(kc.KVError, match="cache dtype"):
+        kc.paged_attention_prefill_sinks_workspace_size(1, 4, 8, 2, head_dim, dtype, 100)
+    assert call(kc, "kv_paged_attention_prefill_sinks", PREFILL, cache_dtype=dtype, head_dim=head_dim) == UNSUPPORTED
