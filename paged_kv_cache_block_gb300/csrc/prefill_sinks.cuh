@@ -922,9 +922,9 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                     const float2 v = unpack2<QT>(max2<QT>(max2<QT>(raw[i].x, raw[i].y), max2<QT>(raw[i].z, raw[i].w)));
                     most = fmaxf(most, fmaxf(v.x, v.y) * ks[i]);
                 }
-                // 2^up with 2^7 <= most * 2^up < 2^8, as far as floats go
+                // 2^up with 2^7 <= most * 2^up < 2^8, as far as floats go (2^up and 2^-up are normal ones)
                 const int exponent = static_cast<int>(__float_as_uint(most) >> 23) - 127;  // (-127: 0 or subnormal)
-                const int up = most > 0.f && exponent < 128 ? min(max(7 - exponent, -100), 100) : 0;
+                const int up = most > 0.f && exponent < 128 ? min(7 - exponent, 126) : 0;  // (-120 at least)
                 const float factor = __uint_as_float(static_cast<uint32_t>(127 + up) << 23);
                 // (a scale that underflows, or of 0, as the least normal number: an unseen score of -inf times it
                 // has to stay -inf)

@@ -427,3 +427,18 @@ def test_values_near_the_largest(kv, workers, new, Hq, D):
     r = x.reference()
     assert np.isfinite(r["out"]).all() and np.abs(r["out"]).max() > 2.0 ** 116
     verify(x, *prefill(kv, x, num_workers=workers))
+
+
+@pytest.mark.parametrize("cache", ["int4", "e4m3"])
+@pytest.mark.parametrize("exponent", [-110, -60, 60, 118])
+def test_queries_times_a_power_of_two(kv, cache, exponent):
+    """Over E4M3 and INT4 caches each row brings its own power of two: queries larger or smaller by one under a scale that
+    takes it off give the same bits, over all of bf16's exponents."""
+    x = Inputs(37, [200, 30], [40, 20], window=100, sinks=4, cache=cache)
+    x.q[x.q.abs() < 2.0 ** -8] = 0  # (so that no query leaves the normal numbers)
+    want, lse, err = prefill(kv, x)
+    verify(x, want, lse, err)
+    x.q = (x.q.double() * 2.0 ** exponent).to(BF16)
+    x.scale *= 2.0 ** -exponent
+    out, lse2, err = prefill(kv, x)
+    assert err == 0 and torch.equal(out, want) and torch.equal(lse2, lse)
