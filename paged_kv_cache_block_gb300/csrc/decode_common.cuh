@@ -316,8 +316,13 @@ __device__ __forceinline__ void merge_row(const KernelParams &kp, const int32_t 
 
 // Items at most, as a share of the workers, for the merges below that take a CTA where the others take a warp:
 // with few items each is in many pieces, and a warp's round trips through L2, one for every 4 or 8 pieces, add
-// up.  (One sequence of 4104 keys over 64 workers, the
-// whole call: 31 us with the merge by warps, 14 by CTAs and as a programmatic dependent.)
+// up; with many the CTAs themselves do.  The whole call on 152 SMs, sequences of 4100 seen keys, in us by CTAs / by
+// warps (both as programmatic dependents):
+//   32/8 heads, 1 row, items 1, 4, 8, 12, 16, 32   14.2 / 26.1, 22.5 / 30.6, 32.1 / 36.5, 42.2 / 45.9, 52.8 / 55.0, 93.8 / 92.1
+//   the same, 4 rows, items 1, 4, 8, 16            21.5 / 36.7, 29.2 / 36.4, 43.3 / 41.7, 71.2 / 60.5
+//   12 heads of 64, items 1, 8, 16, 32             12.7 / 23.5, 25.7 / 29.4, 41.2 / 43.1, 71.0 / 70.9
+//   INT4, 32/8 heads, 8 or 16, 32 sequences        25.0 / 32.4, 29.9 / 32.8, 46.5 / 45.8
+// The two cross between 8 and 32 items of 152 workers, 9 with this share.
 constexpr int kLongMergeShare = 16;
 
 // The merge of one row's pieces by a CTA of 8 warps: each takes every eighth piece, then their sums are joined.

@@ -398,8 +398,11 @@ __device__ __forceinline__ void copy16_async(uint32_t dst, const void *src, bool
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 
+// The first tile's weights are formed before its maximum is known, and the reference in use kept while it will do.
 // How far (log2) a row's maximum may exceed the reference in use, and how far below the first one, 0, it may
 // lie: bf16 has float's exponents; fp16 weights are formed 2^7 higher (kFactor), the largest then at 2^7 .. 2^15.
+// (16 chunks / over INT4, us: 967 / 1468; with 8 in the place of 16 for bf16 986 / 1468, with each row's first maximum as
+// its first reference, hence a second pass over that tile, 987 / 1485.)
 template <typename MT> constexpr float kAbove = 16.f;
 template <> constexpr float kAbove<__half> = kRescaleLog2;
 template <typename MT> constexpr float kBelow = 16.f;
@@ -972,7 +975,8 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                 if (warp_valid) {  // (a warp without rows leaves its lanes of P as they are)
                     if (w.mixed(p, j, first_pos, last_pos)) {
                         // (scale > 0: an unseen score of -inf gets weight 0.  Apart from the pass below, whose
-                        // unrolled code the warps would fetch anew each time.)
+                        // unrolled code the warps would fetch anew each time.  32 keys that the warp's rows all see
+                        // are left as they are: 967 us and not 970 for the 16 chunks, 1468 and not 1494 over INT4.)
 #pragma unroll 1
                         for (int ch = 0; ch < 4; ++ch) {
                             const uint32_t seen = valid ? seen32(j * kBN + ch * 32, pos, klo, p.num_sinks) : 0u;
@@ -1188,9 +1192,15 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemCols) : "memory");
 }
 
-// The merge of tree_common.cuh with a row of CTAs an item instead of one a share, for fewer items than workers: most
-// of its CTAs would find that no item starts in their share, after a round trip.  (One sequence of 100 tokens,
-// 16 items: 33.5 us for the call with that merge, 31.5 with this one.)
+// The merge of tree_common.cuh with a row of CTAs an item instead of one a share: most of that one's CTAs find that no
+// item starts in their share, after a round trip, but this one's have to look for their item first.  With partial
+// results of 256 rows of 128 dims (16 CTAs a share or item) and 152 workers the whole call takes, in us with this /
+// that merge: 8 items 31.6 / 29.5, 16: 30.2 / 31.7 to 33.7, 24: 37.8 / 39.0, 32: 41.6 / 42.3, 48: 51.0 / 50.5, 64: 62.1 /
+// 59.1, 96: 84 / 77.  With half as many CTAs the other is faster everywhere: 128 rows 24.9 / 22.3 (8 items), 36.1 / 34.9
+// (32); 64 dims 26.5 / 26.1 (16 items), 46.3 / 45.0 (64).
+static bool merge_by_items(int64_t items, const TreeParams &p) {  // (128 dims)
+    return p.rows_per_item == 2 * kTreeRows && items * 4 <= p.workers && items * 16 > p.workers;
+}
 template <typename T, int D>
 static __global__ void __launch_bounds__(256, 4) merge_items_kernel(const __grid_constant__ TreeParams p) {
     const int lane = threadIdx.x & 31;
@@ -1232,11 +1242,12 @@ static cudaError_t launch_typed(const CUtensorMap &tq, const CUtensorMap &tk, co
     const cudaError_t e = launch_dependent(kernel, dim3(p.t.workers), dim3(kThreads<kCache>), kSmem, stream, tq, tk, tv, p);
     if (e != cudaSuccess || p.t.workers < 2) return e;
     const int64_t items = static_cast<int64_t>(p.t.items_per_seq) * p.t.a.num_seqs;
-    if (items <= p.t.workers)
-        return launch_dependent(merge_items_kernel<QT, D>, dim3(static_cast<unsigned>(items), p.t.rows_per_item / 32 * (D / 8) / 8),
-                                dim3(256), 0, stream, p.t);
-    return launch_dependent(tree_merge_kernel<QT, D, true>, dim3(p.t.workers - 1, p.t.rows_per_item / 32 * (D / 8) / 8),
-                            dim3(256), 0, stream, p.t);
+    const unsigned ctas = p.t.rows_per_item / 32 * (D / 8) / 8;  // a share or item
+    if constexpr (D == 128) {
+        if (merge_by_items(items, p.t))
+            return launch_dependent(merge_items_kernel<QT, D>, dim3(static_cast<unsigned>(items), ctas), dim3(256), 0, stream, p.t);
+    }
+    return launch_dependent(tree_merge_kernel<QT, D, true>, dim3(p.t.workers - 1, ctas), dim3(256), 0, stream, p.t);
 }
 
 }  // namespace sinks
