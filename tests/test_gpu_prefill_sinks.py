@@ -442,3 +442,13 @@ def test_queries_times_a_power_of_two(kv, cache, exponent):
     x.scale *= 2.0 ** -exponent
     out, lse2, err = prefill(kv, x)
     assert err == 0 and torch.equal(out, want) and torch.equal(lse2, lse)
+
+
+@pytest.mark.parametrize("cache,dtype", CACHES)
+@pytest.mark.parametrize("sinks", [2 ** 28 - 1, 2 ** 28 + 300, 2 ** 29, 2 ** 31 - 200, 2 ** 31 - 1])
+@pytest.mark.parametrize("window", [1, 40, 2 ** 31 - 1])
+def test_loose_bounds_and_sinks_past_any_length(kv, cache, dtype, sinks, window):
+    """max_seq_len bounds nothing, and no sequence is as long as the sinks: every earlier key is seen."""
+    x = Inputs(38, [118, 700, 0], [150, 1, 5], 8, 2, window=window, sinks=sinks, cache=cache, dtype=dtype)
+    for workers in (0, 1000):
+        verify(x, *prefill(kv, x, max_seq_len=2 ** 31 - 1, num_workers=workers))
