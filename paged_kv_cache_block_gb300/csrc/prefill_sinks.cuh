@@ -699,8 +699,9 @@ prefill_sinks_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_co
                     const int k0 = j * kBN;
                     bool odd = false;
                     auto clean = [&](int lo, int hi, bool zero) {
-                        lo = min(max(lo - k0, 0), kBN);  // (either may lie 2^31 from the tile: sinks past any length)
-                        hi = min(max(hi - k0, 0), kBN);
+                        lo = max(lo, k0) - k0;
+                        hi = min(hi, k0 + kBN) - k0;
+                        if (lo >= hi) return;  // (either may lie 2^31 from the tile: sinks past any length)
                         for (int i = lo * 8 + lane; i < hi * 8; i += 32)
                             for (int hf = 0; hf < TL::kHalves; ++hf)
                                 clean_chunk<MT>(tile + (i >> 6) * TL::kGroup + hf * 1024 + (i & 63) * 16, zero, odd);

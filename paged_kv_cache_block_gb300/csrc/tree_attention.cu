@@ -342,8 +342,9 @@ tree_attention_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_c
                 // keys no row sees: [block start, kv_lo) and [L, block end); keys some rows may not
                 // see: [kv_lo, ctx + n - window) of the context, the drafted [ctx, L)
                 auto clean = [&](int lo, int hi, bool zero) {
-                    lo = min(max(lo - k0, 0), kBN);  // (either may lie far from the tile)
-                    hi = min(max(hi - k0, 0), kBN);
+                    lo = max(lo, k0) - k0;
+                    hi = min(hi, k0 + kBN) - k0;
+                    if (lo >= hi) return;  // (either may lie far from the tile)
                     for (int i = lo * 8 + lane; i < hi * 8; i += 32)
                         for (int hf = 0; hf < TL::kHalves; ++hf)
                             clean_chunk<T>(tile + (i >> 6) * TL::kGroup + hf * 1024 + (i & 63) * 16, zero, odd);

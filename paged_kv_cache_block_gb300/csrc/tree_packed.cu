@@ -327,8 +327,9 @@ tree_packed_kernel(const __grid_constant__ CUtensorMap tmap_q, const __grid_cons
                 // keys no row sees: [block start, kv_lo) and [L, block end); keys some rows may not
                 // see: [kv_lo, ctx + n - window) of the context, the drafted [ctx, L)
                 auto clean = [&](int lo, int hi, bool zero) {
-                    lo = min(max(lo - k0, 0), kKeys);  // (either may lie far from the tile)
-                    hi = min(max(hi - k0, 0), kKeys);
+                    lo = max(lo, k0) - k0;
+                    hi = min(hi, k0 + kKeys) - k0;
+                    if (lo >= hi) return;  // (either may lie far from the tile)
                     // 16-byte chunks: 8 of a key's 64 dims, of every head and side
                     for (int i = lo * 8 + lane; i < hi * 8; i += 32) {
                         const int key = i >> 3;
