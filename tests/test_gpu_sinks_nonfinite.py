@@ -57,7 +57,7 @@ CASES = [("same", BF16, 128), ("same", F16, 128), ("same", F16, 64), ("e4m3", BF
 
 @pytest.mark.parametrize("cache,dtype,D", CASES)
 @pytest.mark.parametrize("workers", [0, 1, 3, 20, 300])
-@pytest.mark.parametrize("ctx,q_len", [([3000], 1), ([3000], 4), ([3000], 3), ([700] * 30, 2)])
+@pytest.mark.parametrize("ctx,q_len", [([3000], 1), ([3000], 4), ([3000], 3), ([700] * 12, 2)])
 def test_decode_keeps_what_weighs_nothing(kv, cache, dtype, D, workers, ctx, q_len):
     """A NaN in the value of a key whose weight underflows reaches its dim in however many pieces the keys are taken."""
     for heavy in (0, 690):
@@ -67,16 +67,17 @@ def test_decode_keeps_what_weighs_nothing(kv, cache, dtype, D, workers, ctx, q_l
             for i, pos in enumerate((1, 140, c // 2, c - 20)):
                 vc[(*x.slot(b, pos), i % 2, 7 * i + 1)] = np.nan
         x.v_cache = torch.from_numpy(vc).to(x.v_cache.dtype)
-        verify(x, *decode(kv, x, num_workers=workers))
+        out, lse, err = decode(kv, x, num_workers=workers)
+        verify(x, out, lse, err)
         if cache == "same":  # an infinity: not in the result as a number, whether it comes out as itself or as NaN
             x.v_cache[x.v_cache.isnan()] = np.inf
-            out = decode(kv, x, num_workers=workers)[0].double().cpu().numpy()
-            assert np.array_equal(np.isfinite(out), np.isfinite(x.reference()["out"]))
+            other = decode(kv, x, num_workers=workers)[0]
+            assert torch.equal(other.isfinite(), out.isfinite())
 
 
 @pytest.mark.parametrize("cache,dtype,D", CASES)
 @pytest.mark.parametrize("workers", [0, 1, 3, 20, 300])
-@pytest.mark.parametrize("ctx,new", [([3000], 1), ([3000], 40), ([3000], 90), ([700] * 30, 20)])
+@pytest.mark.parametrize("ctx,new", [([3000], 1), ([3000], 40), ([3000], 90), ([700] * 12, 20)])
 def test_prefill_keeps_what_weighs_nothing(kv, cache, dtype, D, workers, ctx, new):
     """The same, where the two chains of a row tile share its key tiles too."""
     for heavy in (0, 690):
@@ -86,8 +87,9 @@ def test_prefill_keeps_what_weighs_nothing(kv, cache, dtype, D, workers, ctx, ne
             for i, pos in enumerate((1, 140, c // 2, c - 20)):
                 vc[(*x.slot(b, pos), i % 2, 7 * i + 1)] = np.nan
         x.v_cache = torch.from_numpy(vc).to(x.v_cache.dtype)
-        verify_prefill(x, *prefill(kv, x, num_workers=workers))
+        out, lse, err = prefill(kv, x, num_workers=workers)
+        verify_prefill(x, out, lse, err)
         if cache == "same":
             x.v_cache[x.v_cache.isnan()] = np.inf
-            out = prefill(kv, x, num_workers=workers)[0].double().cpu().numpy()
-            assert np.array_equal(np.isfinite(out), np.isfinite(x.reference()["out"]))
+            other = prefill(kv, x, num_workers=workers)[0]
+            assert torch.equal(other.isfinite(), out.isfinite())
