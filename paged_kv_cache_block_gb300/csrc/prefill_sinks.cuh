@@ -37,12 +37,14 @@
 // where they are written (two row tiles of 128 dims leave TMEM no other columns), and both chains come to be in
 // phase: about 4,700 clocks a tile of two row tiles, of which the products take 2 x 1,300 and a softmax 1,700.
 // Times of the call, one GB300 (32/8 heads of 128 dims and blocks of 16 where not said):
-//   16 chunks of 1024 tokens in the middle of 7168 + 1024, window 4096, 4 sinks     977 us, 957 TFLOP/s counted
-//   8 ragged prompts up to 2048, 64/8 heads, window 512, 128 sinks                  321 us, 459 (tiles on the
+//   16 chunks of 1024 tokens in the middle of 7168 + 1024, window 4096, 4 sinks     969 us, 965 TFLOP/s counted
+//   8 ragged prompts up to 2048, 64/8 heads, window 512, 128 sinks                  319 us, 461 (tiles on the
 //     diagonal and at the window's edge are half masked)
 //   100 tokens after 20000, window 4096, 4 sinks    31 us: start 5, 2.4 a key tile, partial results and merge 10
-//   the 16 chunks over an INT4 cache, full attention                               1518 us, 799
-//   257 tokens after 8000 over an INT4 cache                                         81 us
+//   the 16 chunks over an E4M3 cache, the same window                              1368 us, 683
+//   the 16 chunks, 40/8 heads of 64 dims                                           1012 us, 577
+//   the 16 chunks over an INT4 cache, full attention                               1470 us, 825
+//   257 tokens after 8000 over an INT4 cache                                         79 us
 // Shares by closed-form costs instead of by items are what the ragged prompts and the single sequences live by.
 // Every wait is bounded (2 s): on expiry KV_DERR_TIMEOUT is set, what was issued is drained, TMEM is freed
 // and the CTA returns.

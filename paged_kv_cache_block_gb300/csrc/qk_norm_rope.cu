@@ -14,8 +14,9 @@
 //
 // INT4 caches (kInt4) take a key's four codes of a piece, its float32 values divided by the scale of
 // their group, as 16 bits; a piece never crosses a group, whose size is at least 8.
-// 16384 tokens of 64 + 16 heads take 119 us (5.3 TB/s); 121 with one reciprocal for a piece's four quotients,
-// 122 with that and 3 blocks an SM (no spills).
+// 16384 tokens of 64 + 16 heads take 119 us (5.3 TB/s): 107 at HBM's rate, which is what codes that are neither
+// divided nor clamped take (5.9 TB/s; the 16-bit form 6.1), and 12 of the codes' instructions.  121 with one reciprocal
+// for a piece's four quotients and two exact steps, 122 with that and 3 blocks an SM (no spills).
 //
 // About 2 bytes move per element each way: the bound is HBM, once the instructions per element are
 // few (packed arithmetic, pointers advanced by a constant).  A warp takes several heads, loaded four
