@@ -26,7 +26,7 @@
  *   - A key that a row does not see has no part in its result, whatever the cache holds there (NaN and
  *     infinities included).  A NaN score that it does see makes its result and log-sum-exp NaN; a NaN
  *     or an infinity in a value that it does see reaches that dim of its result (an infinity as NaN where its
- *     key's weight underflows to 0 in float32).
+ *     key's weight underflows to 0, in float32 or in the 16 bits of the second product).
  *   - Softmax sums are float32, of the weights before they are rounded to 16 bits for the second product
  *     (INT4 decode: of the rounded weights, whose codes' offset comes out exactly with them; prefill: the
  *     result is divided by a sum that takes the largest weight of each 128 keys as it was rounded).  A row
